@@ -12,6 +12,7 @@ import ctypes
 import math
 import os
 import threading
+from typing import NamedTuple
 
 import torch
 
@@ -27,6 +28,7 @@ DEVERR_SEQ_LEN = 1
 DEVERR_POS = 2
 DEVERR_TIMEOUT = 4
 DEVERR_BOUNDS = 8    # set only by the bounds-checked test build
+DEVERR_VALUE = 16    # a NaN or infinity among rows to quantise
 
 _DTYPES = {torch.float32: DA_FP32, torch.bfloat16: DA_BF16}
 # 8-bit caches are passed as torch.int8 / torch.float8_e4m3fn tensors of codes
@@ -62,6 +64,19 @@ SIGNATURES = {
     "decode_attn_partial": (_I, [_P, _P, _P, _P, _I, _I, _P, _P, _I, _I, _I, _I, _I, _I, _F, _I,
                                  _I, _P, _SZ, _P, _P]),
     "decode_attn_combine": (_I, [_P, _P, _I, _P, _P, _I, _I, _I, _I, _P]),
+    "decode_attn_mod_workspace_bytes": (_SZ, [_P, _I, _I, _I, _I, _I, _I, _I, _I,
+                                              ctypes.POINTER(_I)]),
+    "decode_attn_mod": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _I, _I, _P, _SZ,
+                             _P, _P]),
+    "decode_attn_mod_append": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F,
+                                    _I, _I, _P, _SZ, _P, _P]),
+    "decode_attn_q8b_workspace_bytes": (_SZ, [_P, _I, _I, _I, _I, _I, _I, _I, _I,
+                                              ctypes.POINTER(_I)]),
+    "decode_attn_q8b": (_I, [_P, _P, _P, _P, _P, _I, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _I, _I,
+                             _P, _SZ, _P, _P]),
+    "kv_append_q8b": (_I, [_P, _P, _P, _P, _I, _I, _P, _P, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I,
+                           _P, _P]),
+    "kv_read_q8b": (_I, [_P, _P, _P, _P, _I, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _P, _P]),
 }
 
 
@@ -504,3 +519,286 @@ def kv_append_q8(k_new, v_new, k_new_scale, v_new_scale, K, V, k_scale, v_scale,
 def launch_count() -> int:
     """Kernels launched by the library in this process so far."""
     return int(load().decode_attn_launch_count())
+
+
+# ----------------------------------------------------------------- score terms
+class ScoreMod(NamedTuple):
+    """What a model adds to the plain scores before the softmax, and which cached
+    rows the query (at row n - 1 of its n rows) sees; see ``da_score_mod``.
+
+    ``softcap`` c > 0: u = c tanh(t / c) of the scaled score t.  ``slopes`` (float32
+    CUDA tensor [h_q]): s_l = u_l - slopes[h] * (n - 1 - l).  Row l < n is seen when
+    l < ``prefix`` or l >= max(doc_begin[b], n - window): ``window`` last rows (0: all),
+    ``doc_begin`` (int32 CUDA tensor [B]) the first row of the query's document."""
+    softcap: float = 0.0
+    slopes: torch.Tensor | None = None
+    window: int = 0
+    prefix: int = 0
+    doc_begin: torch.Tensor | None = None
+
+
+class _CMod(ctypes.Structure):
+    _fields_ = [("softcap", ctypes.c_float), ("window", ctypes.c_int), ("prefix", ctypes.c_int),
+                ("slopes", ctypes.c_void_p), ("doc_begin", ctypes.c_void_p)]
+
+
+def _c_mod(mod: ScoreMod, B: int, h_q: int, device: torch.device) -> _CMod:
+    slopes, begin = mod.slopes, mod.doc_begin
+    if slopes is not None and (slopes.shape != (h_q,) or slopes.dtype != torch.float32
+                               or slopes.device != device or not slopes.is_contiguous()):
+        raise ValueError("slopes must be a contiguous float32 tensor [h_q] on the query's device")
+    if begin is not None and (begin.shape != (B,) or begin.dtype != torch.int32
+                              or begin.device != device or not begin.is_contiguous()):
+        raise ValueError("doc_begin must be a contiguous int32 tensor [B] on the query's device")
+    if not 0 <= mod.window < 1 << 31 or not 0 <= mod.prefix < 1 << 31:
+        raise ValueError("window and prefix must be non-negative ints")
+    return _CMod(mod.softcap, mod.window, mod.prefix,
+                 None if slopes is None else slopes.data_ptr(),
+                 None if begin is None else begin.data_ptr())
+
+
+def _same_device(device: torch.device, **tensors) -> None:
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} must be on the device of the other tensors ({device})")
+
+
+def _check_workspace(workspace: torch.Tensor, device: torch.device) -> None:
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the query's device")
+
+
+_mod_bytes_cache: dict = {}
+
+
+def _terms_workspace(entry: str, cmod, key, device: torch.device, stream,
+                     workspace: torch.Tensor | None) -> tuple[torch.Tensor | None, int]:
+    """Workspace and its size for a call with score terms or block scales (``key``: the sizes,
+    dtype code and split choice).  Without a given one: a tensor of the stream the call runs on,
+    kept for its next call; while that stream is captured, a tensor of the graph's own pool,
+    since two graphs that share scratch may be replayed at the same time."""
+    if workspace is not None:
+        _check_workspace(workspace, device)
+        return workspace, workspace.numel() * workspace.element_size()
+    seen = (cmod.window, cmod.prefix) if cmod is not None else None
+    full = (entry, device.index, seen, key)
+    need = _mod_bytes_cache.get(full)
+    if need is None:
+        st = ctypes.c_int(0)
+        need = int(getattr(load(), entry)(None if cmod is None else ctypes.byref(cmod), *key,
+                                          ctypes.byref(st)))
+        _check(st.value, entry)
+        if len(_mod_bytes_cache) > 4096:
+            _mod_bytes_cache.clear()
+        _mod_bytes_cache[full] = need
+    if need == 0:
+        return None, 0
+    s = stream if stream is not None else torch.cuda.current_stream(device)
+    at = (device.index, s.cuda_stream, "terms")
+    ws = _ws_cache.get(at)
+    with torch.cuda.stream(stream):  # (None: the current one) memory returns in that stream's order
+        if torch.cuda.is_current_stream_capturing():
+            return torch.empty(need, dtype=torch.uint8, device=device), need
+        if ws is None or ws.numel() < need:
+            ws = _ws_cache[at] = torch.empty(need, dtype=torch.uint8, device=device)
+    return ws, ws.numel()
+
+
+def decode_attn_mod(q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, seq_lens: torch.Tensor,
+                    mod: ScoreMod, out: torch.Tensor | None = None, scale: float | None = None,
+                    num_splits: int = 0, workspace: torch.Tensor | None = None,
+                    dev_error: torch.Tensor | None = None,
+                    stream: torch.cuda.Stream | None = None,
+                    out_dtype: torch.dtype | None = None) -> torch.Tensor:
+    """``decode_attn`` with score terms (calls ``decode_attn_mod``): capped scores, a distance
+    bias, a window, documents and an always-seen prefix, as ``mod`` says.  Returns ``out``."""
+    B, h_q, h_kv, d_k, d_v, n_max = _cache_dims(q, K, V, seq_lens)
+    _same_device(q.device, K=K, V=V, seq_lens=seq_lens, dev_error=dev_error)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d_k)
+    out, oflag = _out(out, out_dtype, B, h_q, d_v, q.device)
+    dt = _DTYPES[q.dtype] | oflag
+    cm = _c_mod(mod, B, h_q, q.device)
+    with _on_device(q):
+        ws, nbytes = _terms_workspace("decode_attn_mod_workspace_bytes", cm,
+                                      (B, h_q, h_kv, d_k, d_v, n_max, dt, int(num_splits)),
+                                      q.device, stream, workspace)
+        st = load().decode_attn_mod(_ptr(q), _ptr(K), _ptr(V), _ptr(seq_lens), ctypes.byref(cm),
+                                    _ptr(out), B, h_q, h_kv, d_k, d_v, n_max, float(scale), dt,
+                                    int(num_splits), _ptr(ws), nbytes, _ptr(dev_error),
+                                    _stream(q, stream))
+    _check(st, "decode_attn_mod")
+    return out
+
+
+def decode_attn_mod_append(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor,
+                           K: torch.Tensor, V: torch.Tensor, seq_lens: torch.Tensor, mod: ScoreMod,
+                           out: torch.Tensor | None = None,
+                           seq_lens_out: torch.Tensor | None = None, scale: float | None = None,
+                           num_splits: int = 0, workspace: torch.Tensor | None = None,
+                           dev_error: torch.Tensor | None = None,
+                           stream: torch.cuda.Stream | None = None,
+                           out_dtype: torch.dtype | None = None) -> torch.Tensor:
+    """``decode_attn_append`` with score terms (calls ``decode_attn_mod_append``): row
+    seq_lens[b] of every kv head is appended, and the query sees what ``mod`` says of the
+    seq_lens[b] + 1 rows.  Returns ``out``."""
+    B, h_q, h_kv, d_k, d_v, n_max = _cache_dims(q, K, V, seq_lens)
+    if k_new.shape != (B, h_kv, d_k) or v_new.shape != (B, h_kv, d_v):
+        raise ValueError("k_new/v_new must be [B, h_kv, d]")
+    for name, t in (("k_new", k_new), ("v_new", v_new)):
+        if not t.is_cuda or not t.is_contiguous() or t.dtype != K.dtype:
+            raise ValueError(f"{name} must be a contiguous CUDA tensor of the cache dtype")
+    if seq_lens_out is not None and (seq_lens_out.shape != (B,)
+                                     or seq_lens_out.dtype != torch.int32
+                                     or not seq_lens_out.is_contiguous()):
+        raise ValueError("seq_lens_out must be a contiguous int32 tensor of shape [B]")
+    _same_device(q.device, K=K, V=V, seq_lens=seq_lens, k_new=k_new, v_new=v_new,
+                 seq_lens_out=seq_lens_out, dev_error=dev_error)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d_k)
+    out, oflag = _out(out, out_dtype, B, h_q, d_v, q.device)
+    dt = _DTYPES[q.dtype] | oflag
+    cm = _c_mod(mod, B, h_q, q.device)
+    with _on_device(q):
+        ws, nbytes = _terms_workspace("decode_attn_mod_workspace_bytes", cm,
+                                      (B, h_q, h_kv, d_k, d_v, n_max, dt, int(num_splits)),
+                                      q.device, stream, workspace)
+        st = load().decode_attn_mod_append(
+            _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(K), _ptr(V), _ptr(seq_lens),
+            _ptr(seq_lens_out), ctypes.byref(cm), _ptr(out), B, h_q, h_kv, d_k, d_v, n_max,
+            float(scale), dt, int(num_splits), _ptr(ws), nbytes, _ptr(dev_error),
+            _stream(q, stream))
+    _check(st, "decode_attn_mod_append")
+    return out
+
+
+# ------------------------------------------------- 8-bit caches with a scale per block
+def _q8b_cache(K, V, k_scale, v_scale, block: int):
+    """Checks a block-scaled cache; returns B, h_kv, n_max, d."""
+    if K.dim() != 4 or V.shape != K.shape or K.dtype not in _Q8_DTYPES or V.dtype != K.dtype:
+        raise ValueError("K, V must be 8-bit code tensors [B, h_kv, n_max, d] of one dtype")
+    if block not in (16, 32, 64, 128):
+        raise ValueError("block must be 16, 32, 64 or 128")
+    B, h_kv, n_max, d = K.shape
+    scales = (B, h_kv, -(-n_max // block))
+    for name, t, shape, dt in (("K", K, K.shape, K.dtype), ("V", V, K.shape, K.dtype),
+                               ("k_scale", k_scale, scales, torch.float32),
+                               ("v_scale", v_scale, scales, torch.float32)):
+        if t.shape != shape or t.dtype != dt or not t.is_cuda or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous CUDA tensor {list(shape)} of {dt}")
+    _same_device(K.device, V=V, k_scale=k_scale, v_scale=v_scale)
+    return B, h_kv, n_max, d
+
+
+def _row_counts(name: str, t: torch.Tensor | None, B: int, device: torch.device) -> None:
+    if t is not None and (t.shape != (B,) or t.dtype != torch.int32 or t.device != device
+                          or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous int32 tensor [B] on the cache's device")
+
+
+def decode_attn_q8b(q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, k_scale: torch.Tensor,
+                    v_scale: torch.Tensor, seq_lens: torch.Tensor, block: int,
+                    mod: ScoreMod | None = None, out: torch.Tensor | None = None,
+                    scale: float | None = None, num_splits: int = 0,
+                    workspace: torch.Tensor | None = None, dev_error: torch.Tensor | None = None,
+                    stream: torch.cuda.Stream | None = None,
+                    out_dtype: torch.dtype | None = None) -> torch.Tensor:
+    """Decode over an 8-bit cache with a scale per block of tokens and head (calls
+    ``decode_attn_q8b``): K, V codes [B, h_kv, n_max, d] (torch.int8 or torch.float8_e4m3fn),
+    scales float32 [B, h_kv, ceil(n_max / block)], q bf16 [B, h_q, d]; ``mod`` adds score terms.
+    Returns ``out``."""
+    B, h_kv, n_max, d = _q8b_cache(K, V, k_scale, v_scale, block)
+    if q.dim() != 3 or q.shape[0] != B or q.shape[2] != d or q.dtype != torch.bfloat16 \
+            or not q.is_contiguous():
+        raise ValueError("q must be a contiguous bfloat16 tensor [B, h_q, d]")
+    _row_counts("seq_lens", seq_lens, B, K.device)
+    _same_device(K.device, q=q, dev_error=dev_error)
+    h_q = q.shape[1]
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    out, oflag = _out(out, out_dtype, B, h_q, d, q.device)
+    dt = _Q8_DTYPES[K.dtype] | oflag
+    cm = None if mod is None else _c_mod(mod, B, h_q, q.device)
+    with _on_device(q):
+        ws, nbytes = _terms_workspace("decode_attn_q8b_workspace_bytes", cm,
+                                      (B, h_q, h_kv, d, d, n_max, dt, int(num_splits)), q.device,
+                                      stream, workspace)
+        st = load().decode_attn_q8b(_ptr(q), _ptr(K), _ptr(V), _ptr(k_scale), _ptr(v_scale), block,
+                                    _ptr(seq_lens), None if cm is None else ctypes.byref(cm),
+                                    _ptr(out), B, h_q, h_kv, d, d, n_max, float(scale), dt,
+                                    int(num_splits), _ptr(ws), nbytes, _ptr(dev_error),
+                                    _stream(q, stream))
+    _check(st, "decode_attn_q8b")
+    return out
+
+
+def kv_append_q8b(k_new: torch.Tensor, v_new: torch.Tensor, K: torch.Tensor, V: torch.Tensor,
+                  k_scale: torch.Tensor, v_scale: torch.Tensor, pos: torch.Tensor, block: int,
+                  n_new: torch.Tensor | None = None, dev_error: torch.Tensor | None = None,
+                  stream: torch.cuda.Stream | None = None) -> None:
+    """Quantise rows as they are written into a block-scaled cache (calls ``kv_append_q8b``):
+    the rows k_new/v_new [B, h_kv, T, d] (float32 or bfloat16, any strides but a contiguous last
+    dimension; [B, h_kv, d] for one row) become rows pos[b] .. of sequence b, n_new[b] of them
+    where given.  A block's scale grows to what its new rows need, and the codes it holds are
+    then rewritten.  Lengths are the caller's to advance."""
+    B, h_kv, n_max, d = _q8b_cache(K, V, k_scale, v_scale, block)
+    if k_new.dim() == 3:
+        k_new = k_new.unsqueeze(2)
+    if v_new.dim() == 3:
+        v_new = v_new.unsqueeze(2)
+    T = k_new.shape[2] if k_new.dim() == 4 else -1
+    for name, t in (("k_new", k_new), ("v_new", v_new)):
+        if t.shape != (B, h_kv, T, d) or t.dtype not in _DTYPES or t.dtype != k_new.dtype:
+            raise ValueError(f"{name} must be a float32 or bfloat16 tensor [B, h_kv, T, d], "
+                             "k_new and v_new alike")
+        if t.stride(3) != 1:
+            raise ValueError(f"{name} must be contiguous in its last dimension")
+    _row_counts("pos", pos, B, K.device)
+    _row_counts("n_new", n_new, B, K.device)
+    _same_device(K.device, k_new=k_new, v_new=v_new, dev_error=dev_error)
+    # a dimension of one element has no step: its stride in the tensor may be anything
+    ks, vs = ((ctypes.c_longlong * 3)(*(t.stride(i) if t.shape[i] > 1 else 0 for i in range(3)))
+              for t in (k_new, v_new))
+    with _on_device(K):
+        st = load().kv_append_q8b(_ptr(k_new), _ptr(v_new), ks, vs, _DTYPES[k_new.dtype], T,
+                                  _ptr(n_new), _ptr(K), _ptr(V), _ptr(k_scale), _ptr(v_scale),
+                                  block, _ptr(pos), B, h_kv, d, n_max, _Q8_DTYPES[K.dtype],
+                                  _ptr(dev_error), _stream(K, stream))
+    _check(st, "kv_append_q8b")
+
+
+def kv_read_q8b(K: torch.Tensor, V: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
+                seq_lens: torch.Tensor, block: int, rows: int | None = None,
+                row_begin: torch.Tensor | None = None, k_out: torch.Tensor | None = None,
+                v_out: torch.Tensor | None = None, out_dtype: torch.dtype = torch.bfloat16,
+                dev_error: torch.Tensor | None = None, stream: torch.cuda.Stream | None = None):
+    """Read rows of a block-scaled cache back as values (calls ``kv_read_q8b``): row
+    row_begin[b] + i (row_begin None: i) of sequence b goes to row i of k_out/v_out
+    [B, h_kv, rows, d] (float32 or bfloat16) while it lies below seq_lens[b]; other rows of the
+    outputs are left as they are (zero in outputs allocated here, of ``out_dtype``, with ``rows``
+    rows, n_max by default).  Returns ``(k_out, v_out)``."""
+    B, h_kv, n_max, d = _q8b_cache(K, V, k_scale, v_scale, block)
+    if k_out is None or v_out is None:
+        if k_out is not None or v_out is not None:
+            raise ValueError("give both k_out and v_out, or neither")
+        with torch.cuda.stream(stream):  # (None: the current stream)
+            k_out, v_out = (torch.zeros((B, h_kv, n_max if rows is None else rows, d),
+                                        dtype=out_dtype, device=K.device) for _ in range(2))
+    T = k_out.shape[2] if k_out.dim() == 4 else -1
+    if rows is not None and rows != T:
+        raise ValueError("rows disagrees with the outputs")
+    for name, t in (("k_out", k_out), ("v_out", v_out)):
+        if t.shape != (B, h_kv, T, d) or t.dtype not in _DTYPES or t.dtype != k_out.dtype \
+                or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous float32 or bfloat16 tensor "
+                             "[B, h_kv, rows, d], k_out and v_out alike")
+    _row_counts("seq_lens", seq_lens, B, K.device)
+    _row_counts("row_begin", row_begin, B, K.device)
+    _same_device(K.device, k_out=k_out, v_out=v_out, dev_error=dev_error)
+    with _on_device(K):
+        st = load().kv_read_q8b(_ptr(K), _ptr(V), _ptr(k_scale), _ptr(v_scale), block,
+                                _ptr(seq_lens), _ptr(row_begin), _ptr(k_out), _ptr(v_out),
+                                _DTYPES[k_out.dtype], T, B, h_kv, d, n_max, _Q8_DTYPES[K.dtype],
+                                _ptr(dev_error), _stream(K, stream))
+    _check(st, "kv_read_q8b")
+    return k_out, v_out

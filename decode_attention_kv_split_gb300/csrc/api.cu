@@ -152,7 +152,9 @@ int encode_cache_map_uncached(CUtensorMap* map, const void* base, int dtype, int
                                                       : CU_TENSOR_MAP_DATA_TYPE_UINT8;
     r = fn(map, ty, 3, const_cast<void*>(base), dims, strides, box, estr,
            CU_TENSOR_MAP_INTERLEAVE_NONE,
-           ks.swizzle128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+           ks.swizzle128 == 1   ? CU_TENSOR_MAP_SWIZZLE_128B
+           : ks.swizzle128 == 2 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                : CU_TENSOR_MAP_SWIZZLE_NONE,
            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   }
   if (r != CUDA_SUCCESS) {
@@ -180,7 +182,9 @@ bool parse_dtype(int dtype, DtypeArg* a) {
          (a->kv == DA_FP32 || a->kv == DA_BF16 || a->kv == DA_INT8 || a->kv == DA_FP8_E4M3);
 }
 
-int check_sizes(int B, int h_q, int h_kv, int d_k, int d_v, int n_max, int dtype) {
+// block: an 8-bit cache with block scales (no row-scale tensor map).
+int check_sizes(int B, int h_q, int h_kv, int d_k, int d_v, int n_max, int dtype,
+                bool block = false) {
   DtypeArg dt;
   if (!parse_dtype(dtype, &dt)) return DA_ERR_DTYPE;
   if (B <= 0 || h_q <= 0 || h_kv <= 0 || n_max <= 0) return DA_ERR_SHAPE;
@@ -193,8 +197,43 @@ int check_sizes(int B, int h_q, int h_kv, int d_k, int d_v, int n_max, int dtype
   const bool common = (d_k == 64 || d_k == 128) && d_v == d_k;
   const bool wide = dt.kv == DA_BF16 && ((d_k == 256 && d_v == 256) || (d_k == 192 && d_v == 128));
   if (!common && !wide) return DA_ERR_UNSUPPORTED;
-  if (is_q8(dt.kv) && n_max % 4 != 0) return DA_ERR_SHAPE;  // row-scale tensor map stride
+  if (is_q8(dt.kv) && !block && n_max % 4 != 0) return DA_ERR_SHAPE;  // row-scale tensor map stride
   return DA_OK;
+}
+
+// Score terms: argument checks, the most rows a query can see, and the terms
+// as the kernels of one launch slice take them (no mod: plain scores).
+int check_mod(const da_score_mod* mod) {
+  if (!mod) return DA_ERR_NULL;
+  if (!(mod->softcap >= 0.f) || !isfinite(mod->softcap)) return DA_ERR_SHAPE;
+  // the kernels hold softcap * log2(e) and its inverse in float
+  if (mod->softcap > 0.f && (mod->softcap < 1e-30f || mod->softcap > 1e30f)) return DA_ERR_SHAPE;
+  if (mod->window < 0 || mod->prefix < 0) return DA_ERR_SHAPE;
+  if ((reinterpret_cast<uintptr_t>(mod->slopes) & 3u) != 0 ||
+      (reinterpret_cast<uintptr_t>(mod->doc_begin) & 3u) != 0)
+    return DA_ERR_ALIGN;
+  return DA_OK;
+}
+
+long long seen_rows(const da_score_mod* mod, int n_max) {
+  if (!mod) return -1;
+  return mod->window > 0 ? (long long)mod->window + mod->prefix : n_max;
+}
+
+da::ScoreTerms score_terms_of(const da_score_mod* mod, int tile_rows, int b0) {
+  da::ScoreTerms t{};
+  if (!mod) return t;
+  t.on = 1;
+  t.tile_rows = tile_rows;
+  t.window = mod->window;
+  t.prefix = mod->prefix;
+  t.doc_begin = mod->doc_begin ? mod->doc_begin + b0 : nullptr;
+  t.slopes = mod->slopes;
+  if (mod->softcap > 0.f) {
+    t.cap_log2 = float(double(mod->softcap) * 1.4426950408889634);
+    t.inv_cap_log2 = float(1.0 / (double(mod->softcap) * 1.4426950408889634));
+  }
+  return t;
 }
 
 struct Plan {
@@ -249,18 +288,26 @@ bool single_split_suffices(long long units, int n_max, int chunk_min, int tile, 
 // the library chooses, the device picks the length from the actual sequence
 // lengths; the host only bounds it from below so that the partial outputs of
 // at most about 4 x SMs work items per launch need workspace.
+// seen: with score terms, the most rows a query can see (a window and the
+// prefix; n_max without a window), else -1.  block: an 8-bit cache with block
+// scales.
 int make_plan(int B, int h_q, int h_kv, int d, int d_v, int n_max, int dtype_arg, int requested,
-              int sms, Plan* pl, bool balance_rule = true) {
+              int sms, Plan* pl, bool balance_rule = true, long long seen = -1,
+              bool block = false) {
   const int dtype = dtype_arg & 0xff;
   const int group = h_q / h_kv;
   pl->tc5 = dtype == DA_BF16 && d == 128 && d_v == 128 && group > 8;
   pl->ks = pl->tc5 ? da::tc5_shape(group)
+           : block        ? da::q8b_shape(d, group)
            : is_q8(dtype) ? da::q8_shape(d)
                           : (dtype == DA_BF16 ? da::bf16_shape(d, d_v, group)
                                               : da::f32_shape(d, group));
   pl->head_chunks = (group + pl->ks.heads_per_cta - 1) / pl->ks.heads_per_cta;
   pl->batch_per_launch = B < da::kMaxBatchPerLaunch ? B : da::kMaxBatchPerLaunch;
   const long long tile = pl->ks.tile_rows;
+  // A work list with score terms holds whole tiles of the rows that are seen:
+  // less than a tile more at the prefix's end and at the window's start.
+  if (seen >= 0 && seen + 2 * tile < n_max) n_max = int(seen + 2 * tile);
   const long long max_tiles = (n_max + tile - 1) / tile;
   pl->balanced = false;
   pl->units = int((long long)pl->batch_per_launch * h_kv * pl->head_chunks);
@@ -352,21 +399,29 @@ struct QuantArgs {
   const float* v_new_scale;
 };
 
+// A block-scaled 8-bit cache: one scale per 2^shift rows and head.
+struct BlockArgs {
+  const float* k_scale;
+  const float* v_scale;
+  int shift;
+};
+
 int run_decode(const void* q, const void* K, const void* V, const int32_t* seq_lens,
                       void* out, int B, int h_q, int h_kv, int d_k, int d_v, int n_max,
                       float scale, int dtype_arg, int num_splits, void* workspace,
                       size_t workspace_bytes, int32_t* dev_error, cudaStream_t stream,
                       const void* k_new, const void* v_new, int32_t* seq_lens_out,
                       const QuantArgs* qa, int row_off = 0, int row_lim = 0x7fffffff,
-                      float* lse_out = nullptr) {
+                      float* lse_out = nullptr, const da_score_mod* mod = nullptr,
+                      const BlockArgs* ba = nullptr) {
   if (!q || !K || !V || !seq_lens || !out) return DA_ERR_NULL;
-  int st = check_sizes(B, h_q, h_kv, d_k, d_v, n_max, dtype_arg);
+  int st = check_sizes(B, h_q, h_kv, d_k, d_v, n_max, dtype_arg, ba != nullptr);
   if (st != DA_OK) return st;
   DtypeArg dta;
   parse_dtype(dtype_arg, &dta);
   const int dtype = dta.kv;
   // 8-bit caches go through the entry points that carry their row scales
-  if (is_q8(dtype) != (qa != nullptr)) return DA_ERR_DTYPE;
+  if (is_q8(dtype) != (qa != nullptr || ba != nullptr)) return DA_ERR_DTYPE;
   if (qa && (!qa->k_scale || !qa->v_scale || (k_new && (!qa->k_new_scale || !qa->v_new_scale))))
     return DA_ERR_NULL;
   if (qa && (!aligned16(qa->k_scale) || !aligned16(qa->v_scale))) return DA_ERR_ALIGN;
@@ -380,7 +435,8 @@ int run_decode(const void* q, const void* K, const void* V, const int32_t* seq_l
   int dev, sms;
   if ((st = current_device(&dev, &sms)) != DA_OK) return st;
   Plan pl;
-  if ((st = make_plan(B, h_q, h_kv, d_k, d_v, n_max, dtype, num_splits, sms, &pl)) != DA_OK)
+  if ((st = make_plan(B, h_q, h_kv, d_k, d_v, n_max, dtype, num_splits, sms, &pl, true,
+                      seen_rows(mod, n_max), ba != nullptr)) != DA_OK)
     return st;
   const size_t out_es = dta.out_bf16 ? 2 : 4;
   const WorkspaceLayout wl = workspace_layout(pl, h_q, d_v);
@@ -397,7 +453,7 @@ int run_decode(const void* q, const void* K, const void* V, const int32_t* seq_l
   }
 
   const int es = elem_size(dtype);          // cached (and appended) elements
-  const int q_es = qa ? 2 : es;             // q is bf16 with an 8-bit cache
+  const int q_es = is_q8(dtype) ? 2 : es;   // q is bf16 with an 8-bit cache
   char* ws = static_cast<char*>(workspace);
   for (int b0 = 0; b0 < B; b0 += pl.batch_per_launch) {
     const int bn = (B - b0) < pl.batch_per_launch ? (B - b0) : pl.batch_per_launch;
@@ -407,6 +463,7 @@ int run_decode(const void* q, const void* K, const void* V, const int32_t* seq_l
     p.out = static_cast<char*>(out) + size_t(b0) * h_q * d_v * out_es;
     p.out_bf16 = dta.out_bf16 ? 1 : 0;
     p.row_off = row_off;
+    p.mod = score_terms_of(mod, pl.ks.tile_rows, b0);
     p.row_lim = row_lim;
     p.lse_out = lse_out ? lse_out + size_t(b0) * h_q : nullptr;
     p.o_part = wl.total ? reinterpret_cast<float*>(ws + wl.o_part) : nullptr;
@@ -429,6 +486,13 @@ int run_decode(const void* q, const void* K, const void* V, const int32_t* seq_l
     p.v_scale = qa ? qa->v_scale : nullptr;
     p.k_new_scale = qa && qa->k_new_scale ? qa->k_new_scale + size_t(b0) * h_kv : nullptr;
     p.v_new_scale = qa && qa->v_new_scale ? qa->v_new_scale + size_t(b0) * h_kv : nullptr;
+    if (ba) {
+      p.k_scale = const_cast<float*>(ba->k_scale);
+      p.v_scale = const_cast<float*>(ba->v_scale);
+    }
+    p.blk_shift = ba ? ba->shift : 0;
+    p.nblk = ba ? int(((long long)n_max + (1 << ba->shift) - 1) >> ba->shift) : 0;
+    p.scale_elems = (long long)B * h_kv * p.nblk;
     p.B = bn;
     p.h_q = h_q;
     p.h_kv = h_kv;
@@ -452,6 +516,7 @@ int run_decode(const void* q, const void* K, const void* V, const int32_t* seq_l
     const int grid = int(items < grid_cap ? items : grid_cap);
     cudaError_t err =
         pl.tc5 ? da::launch_split_tc5(p, tk, tv, grid, stream)
+        : ba   ? da::launch_split_q8b(p, tk, tv, d_k, dtype == DA_INT8 ? 1 : 2, grid, stream)
         : qa   ? da::launch_split_q8(p, tk, tv, tks, tvs, d_k, dtype == DA_INT8 ? 1 : 2, grid, stream)
         : dtype == DA_BF16 ? da::launch_split_bf16(p, tk, tv, d_k, d_v, grid, stream)
                            : da::launch_split_f32(p, tk, tv, d_k, grid, stream);
@@ -526,15 +591,63 @@ int decode_attn_resolve_splits(int B, int h_q, int h_kv, int d_k, int d_v, int n
   return pl.max_splits;
 }
 
-size_t decode_attn_workspace_bytes(int B, int h_q, int h_kv, int d_k, int d_v, int n_max, int dtype,
-                                   int num_splits, int* status) {
-  int st = check_sizes(B, h_q, h_kv, d_k, d_v, n_max, dtype);
+namespace {
+size_t plan_workspace(int B, int h_q, int h_kv, int d_k, int d_v, int n_max, int dtype,
+                      int num_splits, long long seen, bool block, int* status) {
+  int st = check_sizes(B, h_q, h_kv, d_k, d_v, n_max, dtype, block);
   int dev = 0, sms = 0;
   Plan pl;
   if (st == DA_OK) st = current_device(&dev, &sms);
-  if (st == DA_OK) st = make_plan(B, h_q, h_kv, d_k, d_v, n_max, dtype, num_splits, sms, &pl);
+  if (st == DA_OK)
+    st = make_plan(B, h_q, h_kv, d_k, d_v, n_max, dtype, num_splits, sms, &pl, true, seen,
+                   block);
   if (status) *status = st;
   return st == DA_OK ? workspace_layout(pl, h_q, d_v).total : 0;
+}
+}  // namespace
+
+size_t decode_attn_workspace_bytes(int B, int h_q, int h_kv, int d_k, int d_v, int n_max, int dtype,
+                                   int num_splits, int* status) {
+  return plan_workspace(B, h_q, h_kv, d_k, d_v, n_max, dtype, num_splits, -1, false, status);
+}
+
+size_t decode_attn_mod_workspace_bytes(const da_score_mod* mod, int B, int h_q, int h_kv, int d_k,
+                                       int d_v, int n_max, int dtype, int num_splits,
+                                       int* status) {
+  const int st = check_mod(mod);
+  if (st != DA_OK || is_q8(dtype & 0xff)) {
+    if (status) *status = st != DA_OK ? st : DA_ERR_DTYPE;
+    return 0;
+  }
+  return plan_workspace(B, h_q, h_kv, d_k, d_v, n_max, dtype, num_splits, seen_rows(mod, n_max),
+                        false, status);
+}
+
+int decode_attn_mod(const void* q, const void* K, const void* V, const int32_t* seq_lens,
+                    const da_score_mod* mod, void* out, int B, int h_q, int h_kv, int d_k, int d_v,
+                    int n_max, float scale, int dtype, int num_splits, void* workspace,
+                    size_t workspace_bytes, int32_t* dev_error, cudaStream_t stream) {
+  const int st = check_mod(mod);
+  if (st != DA_OK) return st;
+  return run_decode(q, K, V, seq_lens, out, B, h_q, h_kv, d_k, d_v, n_max, scale, dtype,
+                    num_splits, workspace, workspace_bytes, dev_error, stream, nullptr, nullptr,
+                    nullptr, nullptr, 0, 0x7fffffff, nullptr, mod);
+}
+
+int decode_attn_mod_append(const void* q, const void* k_new, const void* v_new, void* K, void* V,
+                           const int32_t* seq_lens, int32_t* seq_lens_out,
+                           const da_score_mod* mod, void* out, int B, int h_q, int h_kv, int d_k,
+                           int d_v, int n_max, float scale, int dtype, int num_splits,
+                           void* workspace, size_t workspace_bytes, int32_t* dev_error,
+                           cudaStream_t stream) {
+  const int st = check_mod(mod);
+  if (st != DA_OK) return st;
+  if (!k_new || !v_new) return DA_ERR_NULL;
+  if (!aligned16(k_new) || !aligned16(v_new)) return DA_ERR_ALIGN;
+  if (seq_lens_out && seq_lens_out == seq_lens) return DA_ERR_SHAPE;
+  return run_decode(q, K, V, seq_lens, out, B, h_q, h_kv, d_k, d_v, n_max, scale, dtype,
+                    num_splits, workspace, workspace_bytes, dev_error, stream, k_new, v_new,
+                    seq_lens_out, nullptr, 0, 0x7fffffff, nullptr, mod);
 }
 
 int decode_attn_ex(const void* q, const void* K, const void* V, const int32_t* seq_lens, void* out,
@@ -697,6 +810,122 @@ int decode_attn_q8_append(const void* q, const void* k_new, const void* v_new,
   return run_decode(q, K, V, seq_lens, out, B, h_q, h_kv, d_k, d_v, n_max, scale, dtype,
                     num_splits, workspace, workspace_bytes, dev_error, stream, k_new, v_new,
                     seq_lens_out, &qa);
+}
+
+namespace {
+// log2 of a block length with kernels (16, 32, 64, 128), or -1.
+int block_shift(int block) {
+  return block == 16 ? 4 : block == 32 ? 5 : block == 64 ? 6 : block == 128 ? 7 : -1;
+}
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Sizes and types shared by the write into and the read from a block-scaled cache.
+int check_blocks(int B, int h_kv, int T, int d, int n_max, int block, int dtype, int io_dtype) {
+  if (!is_q8(dtype) || (io_dtype != DA_FP32 && io_dtype != DA_BF16)) return DA_ERR_DTYPE;
+  if (B <= 0 || h_kv <= 0 || T < 0 || n_max <= 0 || n_max > (1 << 30)) return DA_ERR_SHAPE;
+  if (block_shift(block) < 0) return DA_ERR_SHAPE;
+  if ((long long)B * h_kv > 0x7fffffffLL || (long long)B * h_kv * (long long)n_max > 0x7fffffffLL)
+    return DA_ERR_SHAPE;
+  if (d != 64 && d != 128) return DA_ERR_UNSUPPORTED;
+  return DA_OK;
+}
+}  // namespace
+
+size_t decode_attn_q8b_workspace_bytes(const da_score_mod* mod, int B, int h_q, int h_kv, int d_k,
+                                       int d_v, int n_max, int dtype, int num_splits,
+                                       int* status) {
+  int st = mod ? check_mod(mod) : DA_OK;
+  if (st == DA_OK && !is_q8(dtype & 0xff)) st = DA_ERR_DTYPE;
+  if (st != DA_OK) {
+    if (status) *status = st;
+    return 0;
+  }
+  return plan_workspace(B, h_q, h_kv, d_k, d_v, n_max, dtype, num_splits, seen_rows(mod, n_max),
+                        true, status);
+}
+
+int decode_attn_q8b(const void* q, const void* K, const void* V, const float* k_scale,
+                    const float* v_scale, int block, const int32_t* seq_lens,
+                    const da_score_mod* mod, void* out, int B, int h_q, int h_kv, int d_k, int d_v,
+                    int n_max, float scale, int dtype, int num_splits, void* workspace,
+                    size_t workspace_bytes, int32_t* dev_error, cudaStream_t stream) {
+  if (!is_q8(dtype & 0xff)) return DA_ERR_DTYPE;
+  if (!k_scale || !v_scale) return DA_ERR_NULL;
+  if (block_shift(block) < 0) return DA_ERR_SHAPE;
+  if (!aligned4(k_scale) || !aligned4(v_scale)) return DA_ERR_ALIGN;
+  const int st = mod ? check_mod(mod) : DA_OK;
+  if (st != DA_OK) return st;
+  const BlockArgs ba{k_scale, v_scale, block_shift(block)};
+  return run_decode(q, K, V, seq_lens, out, B, h_q, h_kv, d_k, d_v, n_max, scale, dtype,
+                    num_splits, workspace, workspace_bytes, dev_error, stream, nullptr, nullptr,
+                    nullptr, nullptr, 0, 0x7fffffff, nullptr, mod, &ba);
+}
+
+int kv_append_q8b(const void* k_new, const void* v_new, const long long* k_strides,
+                  const long long* v_strides, int x_dtype, int T, const int32_t* n_new, void* K,
+                  void* V, float* k_scale, float* v_scale, int block, const int32_t* pos, int B,
+                  int h_kv, int d, int n_max, int dtype, int32_t* dev_error, cudaStream_t stream) {
+  if (!K || !V || !k_scale || !v_scale || !pos || !k_strides || !v_strides) return DA_ERR_NULL;
+  int st = check_blocks(B, h_kv, T, d, n_max, block, dtype, x_dtype);
+  if (st != DA_OK) return st;
+  if (T == 0) return DA_OK;
+  if (!k_new || !v_new) return DA_ERR_NULL;
+  if (!aligned16(k_new) || !aligned16(v_new) || !aligned16(K) || !aligned16(V) ||
+      !aligned4(k_scale) || !aligned4(v_scale) || !aligned4(pos) || !aligned4(n_new))
+    return DA_ERR_ALIGN;
+  da::BlockWriteArgs a{};
+  for (int i = 0; i < 3; ++i) {
+    // rows are read 16 bytes at a time; the bound keeps offsets inside 64 bits
+    const long long ks = k_strides[i], vs = v_strides[i], es = elem_size(x_dtype);
+    if (ks < 0 || vs < 0 || ks > (1LL << 31) * 256 || vs > (1LL << 31) * 256) return DA_ERR_SHAPE;
+    if (ks * es % 16 != 0 || vs * es % 16 != 0) return DA_ERR_ALIGN;
+    a.stride[0][i] = ks;
+    a.stride[1][i] = vs;
+  }
+  int dev, sms;
+  if ((st = current_device(&dev, &sms)) != DA_OK) return st;
+  a.x[0] = k_new, a.x[1] = v_new;
+  a.codes[0] = K, a.codes[1] = V;
+  a.scale[0] = k_scale, a.scale[1] = v_scale;
+  a.pos = pos, a.n_new = n_new, a.dev_error = dev_error;
+  a.B = B, a.h_kv = h_kv, a.T = T, a.d = d, a.n_max = n_max;
+  a.blk_shift = block_shift(block);
+  a.kind = dtype == DA_INT8 ? 1 : 2;
+  a.x_bf16 = x_dtype == DA_BF16;
+  cudaError_t e = da::launch_kv_append_q8b(a, stream);
+  if (e != cudaSuccess) return fail_cuda(e, "kv_append_q8b launch");
+  g_launches.fetch_add(1);
+  return DA_OK;
+}
+
+int kv_read_q8b(const void* K, const void* V, const float* k_scale, const float* v_scale,
+                int block, const int32_t* seq_lens, const int32_t* row_begin, void* k_out,
+                void* v_out, int out_dtype, int T, int B, int h_kv, int d, int n_max, int dtype,
+                int32_t* dev_error, cudaStream_t stream) {
+  if (!K || !V || !k_scale || !v_scale || !seq_lens) return DA_ERR_NULL;
+  int st = check_blocks(B, h_kv, T, d, n_max, block, dtype, out_dtype);
+  if (st != DA_OK) return st;
+  if (T == 0) return DA_OK;
+  if (!k_out || !v_out) return DA_ERR_NULL;
+  if (T > (1 << 30)) return DA_ERR_SHAPE;
+  if (!aligned16(k_out) || !aligned16(v_out) || !aligned16(K) || !aligned16(V) ||
+      !aligned4(k_scale) || !aligned4(v_scale) || !aligned4(seq_lens) || !aligned4(row_begin))
+    return DA_ERR_ALIGN;
+  int dev, sms;
+  if ((st = current_device(&dev, &sms)) != DA_OK) return st;
+  da::BlockReadArgs a{};
+  a.codes[0] = K, a.codes[1] = V;
+  a.scale[0] = k_scale, a.scale[1] = v_scale;
+  a.out[0] = k_out, a.out[1] = v_out;
+  a.seq_lens = seq_lens, a.row_begin = row_begin, a.dev_error = dev_error;
+  a.B = B, a.h_kv = h_kv, a.T = T, a.d = d, a.n_max = n_max;
+  a.blk_shift = block_shift(block);
+  a.kind = dtype == DA_INT8 ? 1 : 2;
+  a.out_bf16 = out_dtype == DA_BF16;
+  cudaError_t e = da::launch_kv_read_q8b(a, stream);
+  if (e != cudaSuccess) return fail_cuda(e, "kv_read_q8b launch");
+  g_launches.fetch_add(1);
+  return DA_OK;
 }
 
 int kv_quantize(const void* x, int x_dtype, void* codes, float* scales, long long rows, int d,

@@ -63,7 +63,12 @@ __device__ __forceinline__ int splits_of_head(const SplitParams& p, int bh, int 
   const bool appended = p.append && n >= 0 && n < p.n_max;
   n = n < 0 ? 0 : (n > p.n_max ? p.n_max : n);
   if (appended) ++n;
-  else n = max(0, min(n, p.row_lim) - p.row_off);
+  if (p.mod.on) {  // the rows of the work list
+    ItemRows r;
+    n = list_rows(p.mod, p.mod.tile_rows, b, n, appended, r);
+  } else if (!appended) {
+    n = max(0, min(n, p.row_lim) - p.row_off);
+  }
   const int chunk = *reinterpret_cast<const volatile int*>(p.chunk_out);
   int nv;
   if (chunk > 0) {  // chunked list: ceil(n / chunk) splits

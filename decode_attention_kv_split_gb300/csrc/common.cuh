@@ -23,6 +23,16 @@ namespace da {
 // lengths; the host cuts larger batches into several launches.
 constexpr int kMaxBatchPerLaunch = 512;
 
+// The score terms of decode_attn_mod (da_score_mod) as the kernels take them.
+struct ScoreTerms {
+  int on;                        // 0: plain scores, the other fields are unused
+  int tile_rows;                 // rows of a stage, for the combine (its grid knows no tile)
+  int window, prefix;            // window 0: unlimited
+  const int32_t* doc_begin;      // nullable: [B], this launch's slice
+  const float* slopes;           // nullable: [h_q]
+  float cap_log2, inv_cap_log2;  // softcap * log2 e and its inverse; 0: no cap
+};
+
 struct SplitParams {
   const void* q;                 // [B, h_q, d]  (this launch's slice of the batch)
   const int32_t* seq_lens;       // [B]
@@ -45,11 +55,17 @@ struct SplitParams {
   float* v_scale;
   const float* k_new_scale;
   const float* v_new_scale;
+  // Block-scaled 8-bit caches: k_scale and v_scale hold [B, h_kv, nblk] scales,
+  // one for 2^blk_shift consecutive rows.
+  int nblk, blk_shift;
+  long long scale_elems;         // elements of k_scale, for the checked build
   int append;
   int out_bf16;                  // out holds bf16 (rounded once from the fp32 result)
   // Rows decoded per sequence: [row_off, min(row_lim, seq_lens[b])) (row_off = 0
   // and row_lim >= n_max decode every cached row).  Never combined with append.
   int row_off, row_lim;
+  // Score terms (ScoreMod kernels only; see "Score terms" below).
+  ScoreTerms mod;
   float* lse_out;                // nullable: [B, h_q] natural-log log-sum-exp of the decoded rows
   int B, h_q, h_kv, group;       // group = h_q / h_kv
   int b_offset;                  // first sequence of this launch inside the tensor maps
@@ -290,7 +306,7 @@ struct KernelShape {
   int tile_rows;
   int heads_per_cta;
   int box_cols;     // inner box width in elements
-  int swizzle128;   // 1: 128-byte swizzle, 0: none
+  int swizzle128;   // 1: 128-byte swizzle, 2: 64-byte swizzle, 0: none
   float cta_speed;  // how fast one CTA streams relative to an even share of HBM (measured)
 };
 
@@ -298,6 +314,32 @@ KernelShape bf16_shape(int d_k, int d_v, int group);
 KernelShape f32_shape(int d, int group);
 KernelShape tc5_shape(int group);
 KernelShape q8_shape(int d);
+KernelShape q8b_shape(int d, int group);
+cudaError_t launch_split_q8b(const SplitParams& p, const CUtensorMap& tk, const CUtensorMap& tv,
+                             int d, int kind, int grid, cudaStream_t stream);
+
+// kv_append_q8b and kv_read_q8b (index 0: K, 1: V; kind 1: int8, 2: e4m3).
+struct BlockWriteArgs {
+  const void* x[2];
+  long long stride[2][3];  // elements: sequence, head, row
+  void* codes[2];
+  float* scale[2];
+  const int32_t* pos;
+  const int32_t* n_new;
+  int32_t* dev_error;
+  int B, h_kv, T, d, n_max, blk_shift, kind, x_bf16;
+};
+cudaError_t launch_kv_append_q8b(const BlockWriteArgs& a, cudaStream_t stream);
+struct BlockReadArgs {
+  const void* codes[2];
+  const float* scale[2];
+  void* out[2];
+  const int32_t* seq_lens;
+  const int32_t* row_begin;
+  int32_t* dev_error;
+  int B, h_kv, T, d, n_max, blk_shift, kind, out_bf16;
+};
+cudaError_t launch_kv_read_q8b(const BlockReadArgs& a, cudaStream_t stream);
 cudaError_t launch_split_q8(const SplitParams& p, const CUtensorMap& tk, const CUtensorMap& tv,
                             const CUtensorMap& tks, const CUtensorMap& tvs, int d, int kind,
                             int grid, cudaStream_t stream);
@@ -342,13 +384,19 @@ cudaError_t launch_kv_append(const void* k_new, const void* v_new, void* K, void
 // kMaxBatchPerLaunch sequences, reduction scratch for up to 16 warps, and the
 // decoded items 0 .. kItemCache-1 of the CTA (later items are decoded on the
 // fly).  Kernels reserve kSchedWords ints.
-constexpr int kItemCache = 64;
-constexpr int kItemWords = 8;
+// With score terms an item carries its row mapping too: half as many items in
+// the same words.
+template <bool MOD>
+constexpr int item_cache() { return MOD ? 32 : 64; }
+template <bool MOD>
+constexpr int item_words() { return MOD ? 16 : 8; }
 constexpr int kSchedRedWords = 16 * 32 + 64;
 constexpr int kSchedLens = kMaxBatchPerLaunch + 1;          // offset of lens[]
 constexpr int kSchedRed = kSchedLens + kMaxBatchPerLaunch;  // offset of the scratch
 constexpr int kSchedItems = (kSchedRed + kSchedRedWords + 3) & ~3;
-constexpr int kSchedWords = kSchedItems + kItemCache * kItemWords;
+constexpr int kSchedWords = kSchedItems + item_cache<false>() * item_words<false>();
+static_assert(item_cache<false>() * item_words<false>() == item_cache<true>() * item_words<true>(),
+              "one size of the work list for all kernels");
 
 struct Schedule {
   int* w;           // kSchedWords ints of shared memory:
@@ -379,6 +427,124 @@ struct Item {
   int tiles;
   int new_row;             // row appended by this call (-1: none); the unit's last row
 };
+
+// ---------------------------------------------------------------------------
+// Score terms.  The query of sequence b stands at row n - 1 and sees row l < n
+// when l < prefix or l >= first, first = max(doc_begin[b], n - window).  The
+// work list counts only tiles that hold a visible row: with tiles of TILE rows,
+// the list's rows are those of [0, pt) and of [pt + shift, n), pt = prefix
+// rounded up and pt + shift = first rounded down to a whole tile (one run when
+// they meet).  List row v is cache row v for v < pt and v + shift behind it; a
+// tile lies on one side of pt, so its cache rows are consecutive, and the rows
+// of a tile that the query does not see are masked one by one.
+// ---------------------------------------------------------------------------
+struct ItemRows {
+  int prefix, first;  // visible: l < prefix or l >= first (first = 0 when all are)
+  int pt, shift;      // list row v >= pt is cache row v + shift
+  int lo, hi;         // first and last visible row: where a distance bias is zero
+};
+
+template <bool MOD>
+struct ItemT : Item {};
+template <>
+struct ItemT<true> : Item {
+  ItemRows rows;
+};
+
+// The cache row of an item's list row v.
+__device__ __forceinline__ int cache_row(const ItemT<false>&, int v) { return v; }
+__device__ __forceinline__ int cache_row(const ItemT<true>& it, int v) {
+  return v < it.rows.pt ? v : v + it.rows.shift;
+}
+
+// The row mapping of sequence b at n cached rows (the appended one among them)
+// and the rows its work list holds.  An appended row is always in the list,
+// seen or not, so that it reaches the cache.
+__device__ __forceinline__ int list_rows(const ScoreTerms& m, int tile, int b, int n, bool app,
+                                         ItemRows& r) {
+  const int begin = m.doc_begin ? __ldcg(m.doc_begin + b) : 0;
+  int first = begin;
+  if (m.window > 0) first = max(first, n - m.window);
+  first = min(max(first, 0), n);
+  const int prefix = min(max(m.prefix, 0), n);
+  r.hi = first < n ? n - 1 : prefix - 1;
+  r.lo = prefix > 0 ? 0 : first;
+  r.prefix = prefix;
+  r.first = prefix >= first ? 0 : first;  // all rows: one comparison then decides
+  r.pt = 0x7fffffff;
+  r.shift = 0;
+  if (first >= n && !app) return prefix;  // nothing behind the prefix
+  const int from = (app ? min(first, n - 1) : first) / tile * tile;
+  const int pt = (prefix + tile - 1) / tile * tile;
+  if (from <= pt) return n;
+  r.pt = pt;
+  r.shift = from - pt;
+  return n - r.shift;
+}
+
+// The row mapping of an item's sequence, from its length as it reads now.
+template <int TILE>
+__device__ __forceinline__ ItemRows item_rows(const SplitParams& p, int b) {
+  int n = __ldcg(p.seq_lens + b);
+  const bool app = p.append && n >= 0 && n < p.n_max;
+  n = min(max(n, 0), p.n_max) + (app ? 1 : 0);
+  ItemRows r;
+  list_rows(p.mod, TILE, b, n, app, r);
+  return r;
+}
+
+// Which rows of a stage a query sees, and (MOD) the cache row of its row 0.
+template <bool MOD>
+struct TileMask;
+template <>
+struct TileMask<false> {
+  int valid;
+  __device__ __forceinline__ TileMask(const ItemT<false>&, int, int v) : valid(v) {}
+  __device__ __forceinline__ bool seen(int row) const { return row < valid; }
+  // rows [row, row + count) all seen
+  __device__ __forceinline__ bool all_seen(int row, int count) const { return row + count <= valid; }
+  // some row of [row, row + count) may be seen
+  __device__ __forceinline__ bool any_seen(int row, int) const { return row < valid; }
+};
+template <>
+struct TileMask<true> {
+  int valid, row0, prefix, first;
+  __device__ __forceinline__ TileMask(const ItemT<true>& it, int tile_row0, int v)
+      : valid(v), row0(cache_row(it, tile_row0)), prefix(it.rows.prefix - row0),
+        first(it.rows.first - row0) {}
+  __device__ __forceinline__ bool seen(int row) const {
+    return row < valid && (row < prefix || row >= first);
+  }
+  __device__ __forceinline__ bool all_seen(int row, int count) const {
+    return row + count <= valid && (row + count <= prefix || row >= first);
+  }
+  __device__ __forceinline__ bool any_seen(int row, int count) const {
+    return row < valid && (row < prefix || row + count > first);
+  }
+};
+
+// One query head's distance bias: slope * log2 e per row, and the row where it
+// is zero.  The largest biased row is taken as zero, not the query's own: a
+// softmax does not change when all scores move together, and the biases of the
+// rows that count stay small numbers.
+struct HeadBias {
+  float slope;
+  int zero;
+};
+__device__ __forceinline__ HeadBias head_bias(const SplitParams& p, const ItemT<true>& it, int head,
+                                              bool ok) {
+  HeadBias h;
+  h.slope = p.mod.slopes && ok ? __ldg(p.mod.slopes + head) * 1.4426950408889634f : 0.f;
+  h.zero = h.slope >= 0.f ? it.rows.hi : it.rows.lo;
+  return h;
+}
+
+// A score in the log2 domain with its terms: capped, then biased (row: its cache row).
+__device__ __forceinline__ float score_terms(const SplitParams& p, float x, int row,
+                                             const HeadBias& h) {
+  if (p.mod.cap_log2 > 0.f) x = p.mod.cap_log2 * tanhf(x * p.mod.inv_cap_log2);
+  return fmaf(h.slope, float(row - h.zero), x);
+}
 
 template <int TILE>
 __device__ __forceinline__ Item schedule_item(const SplitParams& p, const Schedule& s, int i) {
@@ -521,13 +687,18 @@ __device__ __noinline__ Item bal_item_far(const SplitParams& p, const Schedule& 
 
 // The k-th item of this CTA (k < s.mine), read back from shared memory when
 // build_schedule decoded it.
-template <int TILE>
-__device__ __forceinline__ Item cta_item(const SplitParams& p, const Schedule& s, int k) {
-  if (k >= kItemCache)
-    return s.balanced ? bal_item_far<TILE>(p, s, int(blockIdx.x), s.u0 + k)
-                      : schedule_item<TILE>(p, s, int(blockIdx.x) + k * int(gridDim.x));
-  const int* w = s.w + kSchedItems + k * kItemWords;
-  Item it;
+template <int TILE, bool MOD = false>
+__device__ __forceinline__ ItemT<MOD> cta_item(const SplitParams& p, const Schedule& s, int k) {
+  ItemT<MOD> it;
+  if (k >= item_cache<MOD>()) {
+    static_cast<Item&>(it) = s.balanced
+                                 ? bal_item_far<TILE>(p, s, int(blockIdx.x), s.u0 + k)
+                                 : schedule_item<TILE>(p, s, int(blockIdx.x) + k * int(gridDim.x));
+    if constexpr (MOD) it.rows = item_rows<TILE>(p, it.b);
+    return it;
+  }
+  const int* w = s.w + kSchedItems + k * item_words<MOD>();
+  if constexpr (MOD) it.rows = ItemRows{w[8], w[9], w[10], w[11], w[12], w[13]};
   it.b = w[0];
   it.kvh = w[1];
   it.hc = w[2];
@@ -682,8 +853,9 @@ __device__ __forceinline__ int choose_chunk_warp(const SplitParams& p, int n_lan
 // clamped into [0, n_max], plus the appended row when there is room for it
 // (kAppendFlag set), else cut to the decoded row range.  `n_out` receives the
 // length after the append (the seq_lens_out value).
-__device__ __forceinline__ int list_len(const SplitParams& p, int n, bool& bad, bool& bad_pos,
-                                        int& n_out) {
+template <int TILE, bool MOD>
+__device__ __forceinline__ int list_len(const SplitParams& p, int b, int n, bool& bad,
+                                        bool& bad_pos, int& n_out) {
   bool app = false;
   if (p.append) {
     app = n >= 0 && n < p.n_max;  // room for the new row
@@ -695,7 +867,10 @@ __device__ __forceinline__ int list_len(const SplitParams& p, int n, bool& bad, 
   }
   if (app) ++n;
   n_out = n;
-  if (!app) {  // rows of the decoded range (all of them unless a range was asked for)
+  if (MOD) {
+    ItemRows r;
+    n = list_rows(p.mod, TILE, b, n, app, r);
+  } else if (!app) {  // rows of the decoded range (all of them unless a range was asked for)
     n = min(n, p.row_lim) - p.row_off;
     n = n < 0 ? 0 : n;
   }
@@ -707,7 +882,7 @@ __device__ __forceinline__ int list_len(const SplitParams& p, int n, bool& bad, 
 // but shared memory, so it may run before the wait for the previous grid,
 // on lengths that grid may still be writing: commit_schedule checks them
 // afterwards and builds again if any changed.
-template <int TILE>
+template <int TILE, bool MOD = false>
 __device__ __forceinline__ Schedule build_schedule_core(const SplitParams& p, int* sched) {
   int* first = sched;
   int* lens = sched + kSchedLens;
@@ -721,7 +896,7 @@ __device__ __forceinline__ Schedule build_schedule_core(const SplitParams& p, in
   int my_n = 0;      // n of sequence tid (the one-warp path: B <= 32)
   for (int b = tid; b < p.B; b += blockDim.x) {
     int n_out;
-    const int lv = list_len(p, __ldcg(p.seq_lens + b), bad, bad_pos, n_out);  // through L2
+    const int lv = list_len<TILE, MOD>(p, b, __ldcg(p.seq_lens + b), bad, bad_pos, n_out);  // through L2
     const int n = len_of(lv);
     lens[b] = lv;
     rows += float(n);
@@ -779,10 +954,10 @@ __device__ __forceinline__ Schedule build_schedule_core(const SplitParams& p, in
       const int th = tags[blockIdx.x + 1];
       s.mine = (th >> 1) - (th & 1) - s.u0 + 1;
     }
-    for (int t = tid; t < s.mine && t < kItemCache; t += blockDim.x) {
+    for (int t = tid; t < s.mine && t < item_cache<MOD>(); t += blockDim.x) {
       const Item it = bal_item<TILE>(p, s, int(blockIdx.x), s.u0 + t);
       {
-        int* w = items + t * kItemWords;
+        int* w = items + t * item_words<MOD>();
         w[0] = it.b;
         w[1] = it.kvh;
         w[2] = it.hc;
@@ -874,9 +1049,9 @@ __device__ __forceinline__ Schedule build_schedule_core(const SplitParams& p, in
   // decode this CTA's first items, one per thread
   const int mine = s.total > int(blockIdx.x) ? (s.total - 1 - int(blockIdx.x)) / int(gridDim.x) + 1 : 0;
   s.mine = mine;
-  if (tid < mine && tid < kItemCache) {
+  if (tid < mine && tid < item_cache<MOD>()) {
     const Item it = schedule_item<TILE>(p, s, int(blockIdx.x) + tid * int(gridDim.x));
-    int* w = items + tid * kItemWords;
+    int* w = items + tid * item_words<MOD>();
     w[0] = it.b;
     w[1] = it.kvh;
     w[2] = it.hc;
@@ -895,7 +1070,7 @@ __device__ __forceinline__ Schedule build_schedule_core(const SplitParams& p, in
 // make the list's global writes: seq_lens_out and the error bits (CTA 0), the
 // split length or balanced marker for the combine (CTA 0) and, in balanced
 // mode, each unit's partial count (its first CTA).  Every thread must call it.
-template <int TILE>
+template <int TILE, bool MOD = false>
 __device__ __forceinline__ Schedule commit_schedule(const SplitParams& p, int* sched,
                                                     Schedule s) {
   const int* lens = sched + kSchedLens;
@@ -904,13 +1079,13 @@ __device__ __forceinline__ Schedule commit_schedule(const SplitParams& p, int* s
   int changed = 0;
   for (int b = tid; b < p.B; b += blockDim.x) {
     int n_out;
-    const int lv = list_len(p, __ldcg(p.seq_lens + b), bad, bad_pos, n_out);
+    const int lv = list_len<TILE, MOD>(p, b, __ldcg(p.seq_lens + b), bad, bad_pos, n_out);
     changed |= lv != lens[b];
     if (blockIdx.x == 0 && p.seq_lens_out && DA_IN(p, b, p.B)) p.seq_lens_out[b] = n_out;
   }
   if (bad && blockIdx.x == 0) flag_error(p.dev_error, DA_DEVERR_SEQ_LEN);
   if (bad_pos && blockIdx.x == 0) flag_error(p.dev_error, DA_DEVERR_POS);
-  if (__syncthreads_or(changed)) s = build_schedule_core<TILE>(p, sched);
+  if (__syncthreads_or(changed)) s = build_schedule_core<TILE, MOD>(p, sched);
   if (blockIdx.x == 0 && tid == 0 && p.chunk_out) *p.chunk_out = s.balanced ? -1 : s.chunk;
   if (s.balanced && p.unit_nv)
     for (int t = tid; t < s.mine; t += blockDim.x) {
@@ -918,6 +1093,19 @@ __device__ __forceinline__ Schedule commit_schedule(const SplitParams& p, int* s
       if (it.split == 0 && DA_IN(p, s.u0 + t, p.B * p.h_kv * p.head_chunks))
         p.unit_nv[s.u0 + t] = it.nv;  // the unit's first CTA
     }
+  if (MOD) {  // the items' row mappings, now that nothing changes under them
+    for (int t = tid; t < s.mine && t < item_cache<MOD>(); t += blockDim.x) {
+      int* w = sched + kSchedItems + t * item_words<MOD>();
+      const ItemRows r = item_rows<TILE>(p, w[0]);
+      w[8] = r.prefix;
+      w[9] = r.first;
+      w[10] = r.pt;
+      w[11] = r.shift;
+      w[12] = r.lo;
+      w[13] = r.hi;
+    }
+    __syncthreads();
+  }
   return s;
 }
 
@@ -1070,11 +1258,12 @@ __device__ __forceinline__ bool read_hint(const SplitParams& p, int4 h, int max_
 }
 
 // After the work list is built: record this CTA's first tiles for the next launch.
-template <int TILE>
-__device__ __forceinline__ void write_hint(const SplitParams& p, const Item& it, int max_tiles) {
+template <int TILE, bool MOD>
+__device__ __forceinline__ void write_hint(const SplitParams& p, const ItemT<MOD>& it,
+                                           int max_tiles) {
   if (!p.hints || blockIdx.x >= unsigned(kMaxHintCtas)) return;
   const int z = (p.b_offset + it.b) * p.h_kv + it.kvh;
-  const int y0 = it.row_begin;
+  const int y0 = cache_row(it, it.row_begin);
   const int tiles = it.tiles < max_tiles ? it.tiles : max_tiles;
   p.hints[blockIdx.x] = make_int4(z, y0, tiles, z ^ y0 ^ tiles ^ kHintSeal);
 }
@@ -1098,12 +1287,13 @@ __device__ __forceinline__ void prefetch_hinted(const SplitParams& p, int4 hint,
 // Fused append: copy the new K and V rows (shared-memory slot, the K row of
 // KROW bytes then the V row of VROW bytes) into row `it.new_row` of kv head
 // (b_offset + b, kvh) of the caches.  One warp; an exact copy of the bits.
-template <int KROW, int VROW>
-__device__ __forceinline__ void store_new_row(const SplitParams& p, const Item& it,
+template <int KROW, int VROW, bool MOD>
+__device__ __forceinline__ void store_new_row(const SplitParams& p, const ItemT<MOD>& it,
                                               const uint8_t* slot, int lane) {
   const size_t head = size_t(p.b_offset + it.b) * p.h_kv + it.kvh;
-  const size_t row = head * size_t(p.n_max) + size_t(it.new_row);
-  if (!DA_IN(p, row, p.cache_rows) || !DA_IN(p, it.new_row, p.n_max)) return;
+  const int l = cache_row(it, it.new_row);
+  const size_t row = head * size_t(p.n_max) + size_t(l);
+  if (!DA_IN(p, row, p.cache_rows) || !DA_IN(p, l, p.n_max)) return;
   const uint4* ks = reinterpret_cast<const uint4*>(slot);
   const uint4* vs = reinterpret_cast<const uint4*>(slot + KROW);
   uint4* kd = reinterpret_cast<uint4*>(static_cast<char*>(p.k_cache) + row * KROW);
@@ -1174,7 +1364,7 @@ cudaError_t launch_dependent(void (*kernel)(Params...), int grid, int threads, s
 // that holds the unit's last row, into that stage's new-row slot
 // (2 * ROW_BYTES: the K row, then the V row).
 template <int TILE, int STAGES, int STAGE_BYTES, int NBOX_K, int NBOX_V, int BOX_COLS,
-          int BOX_BYTES, int V_OFFSET, int HEADS, int QROW, int KROW, int VROW>
+          int BOX_BYTES, int V_OFFSET, int HEADS, int QROW, int KROW, int VROW, bool MOD = false>
 __device__ __forceinline__ void produce(const CUtensorMap* tmK, const CUtensorMap* tmV,
                                         const SplitParams& p, const Schedule& s, uint32_t ring,
                                         uint32_t qslots, uint32_t newslots, uint32_t full0,
@@ -1187,7 +1377,7 @@ __device__ __forceinline__ void produce(const CUtensorMap* tmK, const CUtensorMa
   uint32_t phase = 0, issued = 0, issued_parity = 0;
   bool aborted = false;
   for (int k = 0; k < s.mine && !aborted; ++k) {
-    const Item it = cta_item<TILE>(p, s, k);
+    const ItemT<MOD> it = cta_item<TILE, MOD>(p, s, k);
     const int z = (p.b_offset + it.b) * p.h_kv + it.kvh;
     for (int t = 0; t < it.tiles; ++t) {
       if (!mbar_wait_bounded(empty0 + 8 * stage, phase ^ 1u, abort_flag)) {
@@ -1228,7 +1418,7 @@ __device__ __forceinline__ void produce(const CUtensorMap* tmK, const CUtensorMa
                   static_cast<const char*>(p.v_new) + src * VROW, VROW, bar);
       }
       const uint32_t kdst = ring + stage * STAGE_BYTES;
-      const int y = it.row_begin + t * TILE;
+      const int y = cache_row(it, it.row_begin + t * TILE);
 #pragma unroll
       for (int h = 0; h < NBOX_K; ++h)
         tma_load_3d(kdst + h * BOX_BYTES, tmK, h * BOX_COLS, y, z, bar, policy);

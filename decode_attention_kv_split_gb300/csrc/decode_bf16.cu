@@ -72,7 +72,7 @@ __device__ __forceinline__ uint32_t swz(int row, int col) {
   return uint32_t(half * Cfg::kHalfBytes + row * 128 + ((chunk ^ (row & 7)) << 4));
 }
 
-template <class Cfg>
+template <class Cfg, bool MOD>
 __global__ void __launch_bounds__(Cfg::kThreads, 1)
     split_decode_bf16_kernel(const __grid_constant__ CUtensorMap tmK,
                              const __grid_constant__ CUtensorMap tmV, const SplitParams p) {
@@ -122,19 +122,20 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
   // checked and built again if they changed once the wait is over.  The hint
   // is loaded first and used after the build, so that its round trip does
   // not hold the build's first barrier.
-  Schedule sched = build_schedule_core<Cfg::kTile>(p, sched_words);
+  Schedule sched = build_schedule_core<Cfg::kTile, MOD>(p, sched_words);
   if (threadIdx.x == Cfg::kConsumerThreads)
     prefetch_hinted<Cfg::kTile, Cfg::kHalvesK, Cfg::kHalvesV, 64>(p, hint, &tmK, &tmV, STAGES);
   wait_for_prerequisite_grid();
-  sched = commit_schedule<Cfg::kTile>(p, sched_words, sched);
+  sched = commit_schedule<Cfg::kTile, MOD>(p, sched_words, sched);
   allow_dependent_launch();
-  if (threadIdx.x == 0 && sched.mine > 0) write_hint<Cfg::kTile>(p, cta_item<Cfg::kTile>(p, sched, 0), STAGES);
+  if (threadIdx.x == 0 && sched.mine > 0)
+    write_hint<Cfg::kTile, MOD>(p, cta_item<Cfg::kTile, MOD>(p, sched, 0), STAGES);
 
   // ------------------------------------------------------------------ producer
   if (warp == Cfg::kConsumerWarps) {
     if (lane == 0)
       produce<Cfg::kTile, STAGES, Cfg::kStageBytes, Cfg::kHalvesK, Cfg::kHalvesV, 64,
-              Cfg::kHalfBytes, Cfg::kTileBytesK, Cfg::kHeadsPerCta, DK * 2, DK * 2, DV * 2>(&tmK, &tmV, p, sched, ring, smem_u32(qslots),
+              Cfg::kHalfBytes, Cfg::kTileBytesK, Cfg::kHeadsPerCta, DK * 2, DK * 2, DV * 2, MOD>(&tmK, &tmV, p, sched, ring, smem_u32(qslots),
                                         smem_u32(newslots), full0, empty0, abort_flag);
     return;
   }
@@ -148,12 +149,23 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
   uint32_t phase = 0;
 
   for (int k = 0; k < sched.mine; ++k) {
-    const Item it = cta_item<Cfg::kTile>(p, sched, k);
+    const ItemT<MOD> it = cta_item<Cfg::kTile, MOD>(p, sched, k);
 
     // Query heads of this warp: group-local index hl = hc*HeadsPerCta + hg*kHPW + nb*8 + n.
     // Their bf16 rows arrive with the item's first stage (rows past the group are zero).
     const int head_base = it.hc * Cfg::kHeadsPerCta + hg * kHPW;
     uint32_t qf[NB][MBK][2];
+
+    [[maybe_unused]] HeadBias bias[NB][2];
+    if constexpr (MOD) {
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int hl = head_base + nb * 8 + 2 * c + j;
+          bias[nb][j] = head_bias(p, it, it.kvh * p.group + hl, hl < p.group);
+        }
+    }
 
     float m_run[NB][2], l_run[NB][2];
     float acc[MB][NB][4];
@@ -180,6 +192,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
       const uint32_t vbase = kbase + Cfg::kTileBytesK;
       const int tile_row0 = it.row_begin + t * Cfg::kTile;
       const int valid = min(Cfg::kTile, it.row_end - tile_row0);
+      const TileMask<MOD> mask(it, tile_row0, valid);
       const int key0 = kw * KBW * 16;  // first row of this warp inside the stage
       // A row appended by this call replaces the stale cache row the tile load
       // brought in.
@@ -203,7 +216,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
             *reinterpret_cast<uint4*>(vtile + swz<Cfg>(new_local, col)) =
                 *reinterpret_cast<const uint4*>(slot + DK * 2 + col * 2);
           }
-          if (it.hc == 0) store_new_row<DK * 2, DV * 2>(p, it, slot, lane);
+          if (it.hc == 0) store_new_row<DK * 2, DV * 2, MOD>(p, it, slot, lane);
           fence_proxy_async_smem();
         }
         named_bar_sync(2, Cfg::kConsumerThreads);
@@ -225,7 +238,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
 
       // warp-uniform (the MMAs and shuffles below need the whole warp)
       const bool live = __all_sync(0xffffffffu, !*abort_flag);
-      if (live && key0 < valid) {
+      if (live && mask.any_seen(key0, KBW * 16)) {
         // ---- Step I: scores for KBW blocks of 16 rows.
         float s[KBW][NB][4];
 #pragma unroll
@@ -258,8 +271,15 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
 #pragma unroll
             for (int kb = 0; kb < KBW; ++kb) {
               const int row_lo = key0 + kb * 16 + r;
-              s[kb][nb][j] = row_lo < valid ? s[kb][nb][j] * p.scale_log2 : -INFINITY;
-              s[kb][nb][j + 2] = row_lo + 8 < valid ? s[kb][nb][j + 2] * p.scale_log2 : -INFINITY;
+              s[kb][nb][j] *= p.scale_log2;
+              s[kb][nb][j + 2] *= p.scale_log2;
+              if constexpr (MOD) {
+                const int l = mask.row0 + row_lo;
+                s[kb][nb][j] = score_terms(p, s[kb][nb][j], l, bias[nb][j]);
+                s[kb][nb][j + 2] = score_terms(p, s[kb][nb][j + 2], l + 8, bias[nb][j]);
+              }
+              s[kb][nb][j] = mask.seen(row_lo) ? s[kb][nb][j] : -INFINITY;
+              s[kb][nb][j + 2] = mask.seen(row_lo + 8) ? s[kb][nb][j + 2] : -INFINITY;
               mx = fmaxf(mx, fmaxf(s[kb][nb][j], s[kb][nb][j + 2]));
             }
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
@@ -310,19 +330,19 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
             pl[nb][1] = movmatrix_trans(l1);
           }
           const int blk0 = key0 + kb * 16;
-          const bool partial = blk0 + 16 > valid;
+          const bool partial = !mask.all_seen(blk0, 16);
           // rows held by this lane's A registers: {2c, 2c+1} and {8+2c, 9+2c}
-          const uint32_t mlo = (blk0 + 2 * c < valid ? 0x0000ffffu : 0u) |
-                               (blk0 + 2 * c + 1 < valid ? 0xffff0000u : 0u);
-          const uint32_t mhi = (blk0 + 8 + 2 * c < valid ? 0x0000ffffu : 0u) |
-                               (blk0 + 9 + 2 * c < valid ? 0xffff0000u : 0u);
+          const uint32_t mlo = (mask.seen(blk0 + 2 * c) ? 0x0000ffffu : 0u) |
+                               (mask.seen(blk0 + 2 * c + 1) ? 0xffff0000u : 0u);
+          const uint32_t mhi = (mask.seen(blk0 + 8 + 2 * c) ? 0x0000ffffu : 0u) |
+                               (mask.seen(blk0 + 9 + 2 * c) ? 0xffff0000u : 0u);
 #pragma unroll
           for (int mb = 0; mb < MB; ++mb) {
             const int row = blk0 + (lane & 7) + ((lane >> 4) & 1) * 8;
             const int col = mb * 16 + ((lane >> 3) & 1) * 8;
             uint32_t a[4];
             ldmatrix_x4_trans(a, vbase + swz<Cfg>(row, col));
-            if (partial) {  // rows past the end may hold anything, even NaN
+            if (partial) {  // rows past the end or not seen may hold anything, even NaN
               a[0] &= mlo;
               a[1] &= mlo;
               a[2] &= mhi;
@@ -410,14 +430,22 @@ KernelShape bf16_shape(int d_k, int d_v, int group) {
   return shape_of<Bf16G32D64>();
 }
 
+template <class Cfg, bool MOD>
+static cudaError_t launch_cfg_mod(const SplitParams& p, const CUtensorMap& tk,
+                                  const CUtensorMap& tv, int grid, cudaStream_t stream) {
+  static std::atomic<unsigned long long> smem_set{0};
+  const cudaError_t e =
+      set_smem_limit_once(split_decode_bf16_kernel<Cfg, MOD>, Cfg::kSmemBytes, smem_set);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(split_decode_bf16_kernel<Cfg, MOD>, grid, Cfg::kThreads,
+                          Cfg::kSmemBytes, stream, tk, tv, p);
+}
+
 template <class Cfg>
 static cudaError_t launch_cfg(const SplitParams& p, const CUtensorMap& tk, const CUtensorMap& tv,
                               int grid, cudaStream_t stream) {
-  static std::atomic<unsigned long long> smem_set{0};
-  const cudaError_t e = set_smem_limit_once(split_decode_bf16_kernel<Cfg>, Cfg::kSmemBytes, smem_set);
-  if (e != cudaSuccess) return e;
-  return launch_dependent(split_decode_bf16_kernel<Cfg>, grid, Cfg::kThreads, Cfg::kSmemBytes, stream, tk, tv,
-                          p);
+  return p.mod.on ? launch_cfg_mod<Cfg, true>(p, tk, tv, grid, stream)
+                  : launch_cfg_mod<Cfg, false>(p, tk, tv, grid, stream);
 }
 
 cudaError_t launch_split_bf16(const SplitParams& p, const CUtensorMap& tk, const CUtensorMap& tv,

@@ -57,7 +57,7 @@ __device__ __forceinline__ void load_lane(float (&v)[N], const float* p) {
   }
 }
 
-template <class Cfg>
+template <class Cfg, bool MOD>
 __global__ void __launch_bounds__(Cfg::kThreads, 1)
     split_decode_f32_kernel(const __grid_constant__ CUtensorMap tmK,
                             const __grid_constant__ CUtensorMap tmV, const SplitParams p) {
@@ -104,19 +104,20 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
   // checked and built again if they changed once the wait is over.  The hint
   // is loaded first and used after the build, so that its round trip does
   // not hold the build's first barrier.
-  Schedule sched = build_schedule_core<Cfg::kTile>(p, sched_words);
+  Schedule sched = build_schedule_core<Cfg::kTile, MOD>(p, sched_words);
   if (threadIdx.x == Cfg::kConsumerThreads)
     prefetch_hinted<Cfg::kTile, 1, 1, 0>(p, hint, &tmK, &tmV, STAGES);
   wait_for_prerequisite_grid();
-  sched = commit_schedule<Cfg::kTile>(p, sched_words, sched);
+  sched = commit_schedule<Cfg::kTile, MOD>(p, sched_words, sched);
   allow_dependent_launch();
-  if (threadIdx.x == 0 && sched.mine > 0) write_hint<Cfg::kTile>(p, cta_item<Cfg::kTile>(p, sched, 0), STAGES);
+  if (threadIdx.x == 0 && sched.mine > 0)
+    write_hint<Cfg::kTile, MOD>(p, cta_item<Cfg::kTile, MOD>(p, sched, 0), STAGES);
 
   // ------------------------------------------------------------------ producer
   if (warp == W) {
     if (lane == 0)
       produce<Cfg::kTile, STAGES, Cfg::kStageBytes, 1, 1, 0, 0, Cfg::kTileBytes, G, D * 4, D * 4,
-              D * 4>(
+              D * 4, MOD>(
           &tmK, &tmV, p, sched, ring, smem_u32(qslots), smem_u32(newslots), full0, empty0,
           abort_flag);
     return;
@@ -127,12 +128,19 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
   uint32_t phase = 0;
 
   for (int k = 0; k < sched.mine; ++k) {
-    const Item it = cta_item<Cfg::kTile>(p, sched, k);
+    const ItemT<MOD> it = cta_item<Cfg::kTile, MOD>(p, sched, k);
 
     const int head_base = it.hc * G;  // group-local index of this item's first head
     // q (pre-multiplied by scale * log2(e) once loaded, so scores come out in
     // the log2 domain) arrives with the item's first stage.
     float qv[G][EPL];
+
+    [[maybe_unused]] HeadBias bias[G];
+    if constexpr (MOD) {
+#pragma unroll
+      for (int g = 0; g < G; ++g)
+        bias[g] = head_bias(p, it, it.kvh * p.group + head_base + g, head_base + g < p.group);
+    }
 
     float m_run[G], l_run[G], acc[G][EPL];
 #pragma unroll
@@ -165,8 +173,8 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
       }
       const int tile_row0 = it.row_begin + t * Cfg::kTile;
       const int valid = min(Cfg::kTile, it.row_end - tile_row0);
+      const TileMask<MOD> mask(it, tile_row0, valid);
       const int row0 = warp * RPW;
-      const int nrows = min(RPW, valid - row0);  // may be <= 0
       // A row appended by this call replaces the stale cache row the tile load
       // brought in.
       const int new_local = (it.new_row >= tile_row0 && it.new_row < tile_row0 + Cfg::kTile)
@@ -184,7 +192,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
             reinterpret_cast<uint4*>(vtile + size_t(new_local) * D * 4)[ch] =
                 reinterpret_cast<const uint4*>(slot + D * 4)[ch];
           }
-          if (it.hc == 0) store_new_row<D * 4, D * 4>(p, it, slot, lane);
+          if (it.hc == 0) store_new_row<D * 4, D * 4, MOD>(p, it, slot, lane);
           fence_proxy_async_smem();
         }
         named_bar_sync(2, Cfg::kConsumerThreads);
@@ -192,7 +200,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
 
       // warp-uniform (the shuffles below need the whole warp)
       const bool live = __all_sync(0xffffffffu, !*abort_flag);
-      if (live && nrows > 0) {
+      if (live && mask.any_seen(row0, RPW)) {
         // Step I: s[g][r] = (scale*log2e*q_g) . K_row, reduced across the warp.
         float s[G][RPW];
 #pragma unroll
@@ -217,7 +225,8 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
             x += __shfl_xor_sync(0xffffffffu, x, 4);
             x += __shfl_xor_sync(0xffffffffu, x, 2);
             x += __shfl_xor_sync(0xffffffffu, x, 1);
-            s[g][rr] = rr < nrows ? x : -INFINITY;
+            if constexpr (MOD) x = score_terms(p, x, mask.row0 + row0 + rr, bias[g]);
+            s[g][rr] = mask.seen(row0 + rr) ? x : -INFINITY;
           }
         // Step II: running max and sum (warp-uniform values).
         float alpha[G];
@@ -243,7 +252,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
         // Step III: acc += p * V_row over the valid rows of this warp.
 #pragma unroll
         for (int rr = 0; rr < RPW; ++rr) {
-          if (rr < nrows) {
+          if (mask.seen(row0 + rr)) {
             float vv[EPL];
             load_lane<EPL>(vv, vs + (row0 + rr) * D + lane * EPL);
 #pragma unroll
@@ -309,14 +318,22 @@ KernelShape f32_shape(int d, int group) {
   return d == 128 ? f32_shape_d<128>(group) : f32_shape_d<64>(group);
 }
 
+template <class Cfg, bool MOD>
+static cudaError_t launch_f32_mod(const SplitParams& p, const CUtensorMap& tk,
+                                  const CUtensorMap& tv, int grid, cudaStream_t stream) {
+  static std::atomic<unsigned long long> smem_set{0};
+  const cudaError_t e =
+      set_smem_limit_once(split_decode_f32_kernel<Cfg, MOD>, Cfg::kSmemBytes, smem_set);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(split_decode_f32_kernel<Cfg, MOD>, grid, Cfg::kThreads,
+                          Cfg::kSmemBytes, stream, tk, tv, p);
+}
+
 template <class Cfg>
 static cudaError_t launch_f32_cfg(const SplitParams& p, const CUtensorMap& tk, const CUtensorMap& tv,
                                   int grid, cudaStream_t stream) {
-  static std::atomic<unsigned long long> smem_set{0};
-  const cudaError_t e = set_smem_limit_once(split_decode_f32_kernel<Cfg>, Cfg::kSmemBytes, smem_set);
-  if (e != cudaSuccess) return e;
-  return launch_dependent(split_decode_f32_kernel<Cfg>, grid, Cfg::kThreads, Cfg::kSmemBytes, stream, tk, tv,
-                          p);
+  return p.mod.on ? launch_f32_mod<Cfg, true>(p, tk, tv, grid, stream)
+                  : launch_f32_mod<Cfg, false>(p, tk, tv, grid, stream);
 }
 
 template <int D>

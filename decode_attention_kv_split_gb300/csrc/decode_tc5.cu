@@ -181,7 +181,7 @@ struct Tc5Cfg {
 // items, in order, into slot (stage % NSLOT).  Each load completes on the
 // slot's full barrier; the slot is refilled after its empty barrier (an MMA
 // commit).  The appended row of a unit rides with the tile that holds it.
-template <int T, int NSLOT, int TILE_BYTES, int HALF_BYTES, int ROW_BYTES>
+template <int T, int NSLOT, int TILE_BYTES, int HALF_BYTES, int ROW_BYTES, bool MOD>
 __device__ __forceinline__ void produce_ring(const CUtensorMap* map, const void* new_rows,
                                              const SplitParams& p, const Schedule& s,
                                              uint32_t slots, uint32_t newslots, uint32_t full0,
@@ -193,7 +193,7 @@ __device__ __forceinline__ void produce_ring(const CUtensorMap* map, const void*
   uint32_t phase = 0, issued = 0, issued_parity = 0;
   bool aborted = false;
   for (int k = 0; k < s.mine && !aborted; ++k) {
-    const Item it = cta_item<T>(p, s, k);
+    const ItemT<MOD> it = cta_item<T, MOD>(p, s, k);
     const int z = (p.b_offset + it.b) * p.h_kv + it.kvh;
     for (int t = 0; t < it.tiles; ++t) {
       if (!mbar_wait_bounded(empty0 + 8 * slot, phase ^ 1u, abort_flag)) {
@@ -214,8 +214,9 @@ __device__ __forceinline__ void produce_ring(const CUtensorMap* map, const void*
       const bool with_new = it.new_row >= y0 && it.new_row < y0 + T;
       mbar_arrive_expect_tx(bar, TILE_BYTES + (with_new ? ROW_BYTES : 0));
       const uint32_t dst = slots + slot * TILE_BYTES;
-      tma_load_3d(dst, map, 0, y0, z, bar, policy);
-      tma_load_3d(dst + HALF_BYTES, map, 64, y0, z, bar, policy);
+      const int y = cache_row(it, y0);
+      tma_load_3d(dst, map, 0, y, z, bar, policy);
+      tma_load_3d(dst + HALF_BYTES, map, 64, y, z, bar, policy);
       if (with_new)  // (a checked build flags a row outside k_new / v_new and leaves the stage short)
         if (DA_IN(p, size_t(it.b) * p.h_kv + it.kvh, size_t(p.B) * p.h_kv))
           bulk_load(newslots + slot * ROW_BYTES,
@@ -236,7 +237,7 @@ __device__ __forceinline__ void produce_ring(const CUtensorMap* map, const void*
   }
 }
 
-template <class Cfg>
+template <class Cfg, bool MOD>
 __global__ void __launch_bounds__(Cfg::kThreads, 1)
     split_decode_tc5_kernel(const __grid_constant__ CUtensorMap tmK,
                             const __grid_constant__ CUtensorMap tmV, const SplitParams p) {
@@ -310,24 +311,25 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
   // is loaded first and used after the build, so that its round trip does
   // not hold the build's first barrier.
   tc5::fence_before();
-  Schedule sched = build_schedule_core<T>(p, sched_words);
+  Schedule sched = build_schedule_core<T, MOD>(p, sched_words);
   if (threadIdx.x == 8 * 32) prefetch_hinted<T, 2, 2, 64>(p, hint, &tmK, &tmV, KST);
   wait_for_prerequisite_grid();
-  sched = commit_schedule<T>(p, sched_words, sched);
+  sched = commit_schedule<T, MOD>(p, sched_words, sched);
   tc5::fence_after();
   allow_dependent_launch();
-  if (threadIdx.x == 0 && sched.mine > 0) write_hint<T>(p, cta_item<T>(p, sched, 0), KST);
+  if (threadIdx.x == 0 && sched.mine > 0)
+    write_hint<T, MOD>(p, cta_item<T, MOD>(p, sched, 0), KST);
   const uint32_t tmem = *tmem_slot;
   const uint32_t s_col0 = tmem, o_col = tmem + 2 * NH;  // chain c at o_col + c * 2 NH
 
   // ------------------------------------------------------------------ producers
   if (warp == 8) {
     if (lane == 0)
-      produce_ring<T, KST, Cfg::kTileBytes, Cfg::kHalfBytes, Cfg::kRowBytes>(
+      produce_ring<T, KST, Cfg::kTileBytes, Cfg::kHalfBytes, Cfg::kRowBytes, MOD>(
           &tmK, p.k_new, p, sched, smem_u32(kslots), smem_u32(knew), kfull0, kempty0, abort_flag,
           true);
     else if (lane == 1)
-      produce_ring<T, VST, Cfg::kTileBytes, Cfg::kHalfBytes, Cfg::kRowBytes>(
+      produce_ring<T, VST, Cfg::kTileBytes, Cfg::kHalfBytes, Cfg::kRowBytes, MOD>(
           &tmV, p.v_new, p, sched, smem_u32(vslots), smem_u32(vnew), vfull0, vempty0, abort_flag,
           false);
     return;
@@ -359,7 +361,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
       int kslot = 0;
       uint32_t kphase = 0;
       for (int k = 0; k < sched.mine && !aborted; ++k) {
-        const Item it = cta_item<T>(p, sched, k);
+        const ItemT<MOD> it = cta_item<T, MOD>(p, sched, k);
         if (it.tiles == 0) continue;
         // Q of the item's NH heads, swizzled K-major (rows past the group are
         // zero).  The score MMAs of the previous stage are complete once the
@@ -403,11 +405,11 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
               *reinterpret_cast<uint4*>(kt + tc5::sw128(new_local, ch * 8, T)) =
                   reinterpret_cast<const uint4*>(slot)[ch];
             if (it.hc == 0 &&  // and into the K cache
-                DA_IN(p, (size_t(p.b_offset + it.b) * p.h_kv + it.kvh) * size_t(p.n_max) + it.new_row,
+                DA_IN(p, (size_t(p.b_offset + it.b) * p.h_kv + it.kvh) * size_t(p.n_max) + cache_row(it, it.new_row),
                       p.cache_rows)) {
               const size_t head = size_t(p.b_offset + it.b) * p.h_kv + it.kvh;
               uint4* dst = reinterpret_cast<uint4*>(
-                  static_cast<char*>(p.k_cache) + (head * size_t(p.n_max) + size_t(it.new_row)) * (D * 2));
+                  static_cast<char*>(p.k_cache) + (head * size_t(p.n_max) + size_t(cache_row(it, it.new_row))) * (D * 2));
               for (int ch = lane; ch < D / 8; ch += 32) dst[ch] = reinterpret_cast<const uint4*>(slot)[ch];
             }
             fence_proxy_async_smem();
@@ -440,7 +442,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
       int vslot = 0;
       uint32_t vphase = 0;
       for (int k = 0; k < sched.mine && !aborted; ++k) {
-        const Item it = cta_item<T>(p, sched, k);
+        const ItemT<MOD> it = cta_item<T, MOD>(p, sched, k);
         for (int t = 0; t < it.tiles; ++t, ++j) {
           const uint32_t b = j & 1;
           if (!warp_wait(p_full0 + 8 * b, (j >> 1) & 1)) break;
@@ -448,7 +450,14 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
           uint8_t* vt = vslots + size_t(vslot) * Cfg::kTileBytes;
           const int row0 = it.row_begin + t * T;
           const int valid = min(T, it.row_end - row0);
-          if (valid < T) {  // rows past the end may hold anything, even NaN
+          if constexpr (MOD) {  // rows past the end or not seen may hold anything, even NaN
+            const TileMask<MOD> mask(it, row0, valid);
+            if (!mask.all_seen(0, T))
+              for (int r = 0; r < T; ++r)  // warp-uniform; a lane per 16-byte piece of the row
+                if (!mask.seen(r) && lane < D / 8)
+                  *reinterpret_cast<uint4*>(vt + tc5::sw128(r, lane * 8, T)) =
+                      make_uint4(0, 0, 0, 0);
+          } else if (valid < T) {  // rows past the end may hold anything, even NaN
             for (int ch = lane; ch < (T - valid) * (D / 8); ch += 32) {
               const int r = valid + ch / (D / 8), col = (ch % (D / 8)) * 8;
               *reinterpret_cast<uint4*>(vt + tc5::sw128(r, col, T)) = make_uint4(0, 0, 0, 0);
@@ -462,11 +471,11 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
               *reinterpret_cast<uint4*>(vt + tc5::sw128(new_local, ch * 8, T)) =
                   reinterpret_cast<const uint4*>(slot)[ch];
             if (it.hc == 0 &&  // and into the V cache
-                DA_IN(p, (size_t(p.b_offset + it.b) * p.h_kv + it.kvh) * size_t(p.n_max) + it.new_row,
+                DA_IN(p, (size_t(p.b_offset + it.b) * p.h_kv + it.kvh) * size_t(p.n_max) + cache_row(it, it.new_row),
                       p.cache_rows)) {
               const size_t head = size_t(p.b_offset + it.b) * p.h_kv + it.kvh;
               uint4* dst = reinterpret_cast<uint4*>(
-                  static_cast<char*>(p.v_cache) + (head * size_t(p.n_max) + size_t(it.new_row)) * (D * 2));
+                  static_cast<char*>(p.v_cache) + (head * size_t(p.n_max) + size_t(cache_row(it, it.new_row))) * (D * 2));
               for (int ch = lane; ch < D / 8; ch += 32) dst[ch] = reinterpret_cast<const uint4*>(slot)[ch];
             }
           }
@@ -539,10 +548,16 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
     tc5::fence_after();
   };
   for (int k = 0; k < sched.mine; ++k) {
-    const Item it = cta_item<T>(p, sched, k);
+    const ItemT<MOD> it = cta_item<T, MOD>(p, sched, k);
     const int head0 = it.hc * NH;
     const size_t bh0 = size_t(it.b) * p.h_q + size_t(it.kvh) * p.group + head0;
     const int nheads = min(NH, p.group - head0);
+    [[maybe_unused]] HeadBias bias[HT];
+    if constexpr (MOD) {
+#pragma unroll
+      for (int h = 0; h < HT; ++h)
+        bias[h] = head_bias(p, it, it.kvh * p.group + head0 + hb + h, hb + h < nheads);
+    }
     float m_run[HT], l_part[HT];
 #pragma unroll
     for (int h = 0; h < HT; ++h) {
@@ -560,14 +575,22 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
       // warp-uniform: the TMEM loads below are .sync.aligned
       const bool live = __all_sync(0xffffffffu, !*abort_flag);
       const int valid = min(T, it.row_end - (it.row_begin + t * T));
-      const bool row_ok = t_row < valid;
+      const TileMask<MOD> mask(it, it.row_begin + t * T, valid);
+      const bool row_ok = mask.seen(t_row);
       float s[HT];
       if (live) {
         tc5::ld16x(s_col0 + (j & 1) * NH + hb + lane_base, s, HT);
         tc5::wait_ld();
       }
 #pragma unroll
-      for (int h = 0; h < HT; ++h) s[h] = (live && row_ok) ? s[h] * p.scale_log2 : -INFINITY;
+      for (int h = 0; h < HT; ++h) {
+        if constexpr (MOD) {
+          const float x = score_terms(p, s[h] * p.scale_log2, mask.row0 + t_row, bias[h]);
+          s[h] = (live && row_ok) ? x : -INFINITY;
+        } else {
+          s[h] = (live && row_ok) ? s[h] * p.scale_log2 : -INFINITY;
+        }
+      }
 
       // Running max: exact on an item's first stage, else only when some score
       // exceeds it by more than 2^8 (a vote; the exponentials stay <= 2^8).
@@ -742,14 +765,22 @@ KernelShape tc5_shape(int group) {
   return KernelShape{Tc5G32::kTile, 32, 64, 1, 0.7f};
 }
 
+template <class Cfg, bool MOD>
+static cudaError_t launch_tc5_mod(const SplitParams& p, const CUtensorMap& tk,
+                                  const CUtensorMap& tv, int grid, cudaStream_t stream) {
+  static std::atomic<unsigned long long> smem_set{0};
+  const cudaError_t e =
+      set_smem_limit_once(split_decode_tc5_kernel<Cfg, MOD>, Cfg::kSmemBytes, smem_set);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(split_decode_tc5_kernel<Cfg, MOD>, grid, Cfg::kThreads,
+                          Cfg::kSmemBytes, stream, tk, tv, p);
+}
+
 template <class Cfg>
 static cudaError_t launch_tc5_cfg(const SplitParams& p, const CUtensorMap& tk,
                                   const CUtensorMap& tv, int grid, cudaStream_t stream) {
-  static std::atomic<unsigned long long> smem_set{0};
-  const cudaError_t e = set_smem_limit_once(split_decode_tc5_kernel<Cfg>, Cfg::kSmemBytes, smem_set);
-  if (e != cudaSuccess) return e;
-  return launch_dependent(split_decode_tc5_kernel<Cfg>, grid, Cfg::kThreads, Cfg::kSmemBytes, stream, tk, tv,
-                          p);
+  return p.mod.on ? launch_tc5_mod<Cfg, true>(p, tk, tv, grid, stream)
+                  : launch_tc5_mod<Cfg, false>(p, tk, tv, grid, stream);
 }
 
 cudaError_t launch_split_tc5(const SplitParams& p, const CUtensorMap& tk, const CUtensorMap& tv,

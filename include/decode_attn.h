@@ -82,6 +82,7 @@ typedef enum {
 #define DA_DEVERR_SEQ_LEN 1 /* some seq_lens[b] outside [0, n_max]: clamped into range */
 #define DA_DEVERR_POS 2     /* some kv_append pos[b] outside [0, n_max): that row not written */
 #define DA_DEVERR_TIMEOUT 4 /* a pipeline wait exceeded its time limit: outputs invalid */
+#define DA_DEVERR_VALUE 16  /* a NaN or infinity among rows to quantise: written as 0 */
 #define DA_DEVERR_BOUNDS 8  /* bounds-checked test builds only: an index fell outside its
                                buffer and that access was skipped; outputs invalid */
 
@@ -345,6 +346,132 @@ DA_API int kv_append_q8(const void* k_new, const void* v_new, const float* k_new
  * when s = 0.  x must be finite; d a multiple of 32, at most 256. */
 DA_API int kv_quantize(const void* x, int x_dtype, void* codes, float* scales, long long rows,
                        int d, int code_dtype, cudaStream_t stream);
+
+/*
+ * Score terms: what a model adds to the plain scores of Step I before the
+ * softmax, and which cached rows its query sees.  The query of sequence b
+ * stands at row n - 1, n = seq_lens[b] (with a fused append: the length after
+ * it).  With t_l = scale * q.K[l]:
+ *   softcap > 0   u_l = softcap * tanh(t_l / softcap)     (else u_l = t_l)
+ *   slopes        s_l = u_l - slopes[h] * (n - 1 - l)     (else s_l = u_l)
+ *   row l < n is seen when
+ *     l < prefix, or l >= max(doc_begin[b], n - window)
+ * The softmax runs over the seen rows; none seen gives out = 0.  Rows that are
+ * not seen are not read into results (they may hold anything, including NaN),
+ * and whole stages of them are not loaded.
+ *   softcap   : 0 for none, else in [1e-30, 1e30]
+ *   window    : the last `window` rows are seen; 0 for all
+ *   prefix    : the first `prefix` rows are seen whatever the window and the
+ *               document (a shared prompt, or the rows a window keeps)
+ *   slopes    : nullable device float32 [h_q], finite, of either sign
+ *   doc_begin : nullable device int32 [B], the first row of the document the
+ *               query belongs to; values outside [0, n] act as the nearer end
+ * The struct is read during the call; the arrays it names by the kernels.
+ */
+typedef struct {
+  float softcap;
+  int window;
+  int prefix;
+  const float* slopes;
+  const int32_t* doc_begin;
+} da_score_mod;
+
+/* Bytes of device workspace the two calls below need (as
+ * decode_attn_workspace_bytes; a window makes it smaller).  It depends on mod's
+ * window and prefix, not on its arrays. */
+DA_API size_t decode_attn_mod_workspace_bytes(const da_score_mod* mod, int B, int h_q, int h_kv,
+                                              int d_k, int d_v, int n_max, int dtype,
+                                              int num_splits, int* status);
+
+/* decode_attn_ex with score terms: fp32 and bf16 caches, every head dimension
+ * and output type of decode_attn_ex.  num_splits > 0 cuts the rows a query can
+ * see (window + prefix, or n_max without a window). */
+DA_API int decode_attn_mod(const void* q, const void* K, const void* V, const int32_t* seq_lens,
+                           const da_score_mod* mod, void* out, int B, int h_q, int h_kv, int d_k,
+                           int d_v, int n_max, float scale, int dtype, int num_splits,
+                           void* workspace, size_t workspace_bytes, int32_t* dev_error,
+                           cudaStream_t stream);
+
+/* decode_attn_append with score terms: the row is appended whether the query
+ * sees it or not, and n counts it. */
+DA_API int decode_attn_mod_append(const void* q, const void* k_new, const void* v_new, void* K,
+                                  void* V, const int32_t* seq_lens, int32_t* seq_lens_out,
+                                  const da_score_mod* mod, void* out, int B, int h_q, int h_kv,
+                                  int d_k, int d_v, int n_max, float scale, int dtype,
+                                  int num_splits, void* workspace, size_t workspace_bytes,
+                                  int32_t* dev_error, cudaStream_t stream);
+
+/*
+ * 8-bit caches with a scale per block of tokens and head: as the 8-bit caches
+ * above, but rows [i * block, (i + 1) * block) of a head share one float32
+ * scale.  Layouts (row-major, device):
+ *   K, V             [B, h_kv, n_max, d]  codes (1 byte each), 16-byte aligned
+ *   k_scale, v_scale [B, h_kv, ceil(n_max / block)]  float32
+ *   block            16, 32, 64 or 128;  d_k == d_v in {64, 128};  any n_max
+ * dtype is DA_INT8 or DA_FP8_E4M3.
+ */
+
+/* Decode over a block-scaled cache; mod is nullable (plain scores); other
+ * arguments, workspace and errors as decode_attn_q8_ex and decode_attn_mod.
+ * Scales of blocks that hold a seen row must be finite; they may be of any
+ * size, zero or not a power of two.  q is multiplied as fp16: exact for
+ * |q| in [2^-14, 65504]. */
+DA_API size_t decode_attn_q8b_workspace_bytes(const da_score_mod* mod, int B, int h_q, int h_kv,
+                                              int d_k, int d_v, int n_max, int dtype,
+                                              int num_splits, int* status);
+DA_API int decode_attn_q8b(const void* q, const void* K, const void* V, const float* k_scale,
+                           const float* v_scale, int block, const int32_t* seq_lens,
+                           const da_score_mod* mod, void* out, int B, int h_q, int h_kv, int d_k,
+                           int d_v, int n_max, float scale, int dtype, int num_splits,
+                           void* workspace, size_t workspace_bytes, int32_t* dev_error,
+                           cudaStream_t stream);
+
+/*
+ * Quantise rows as they are written into a block-scaled cache: the m new rows
+ * of sequence b (m = n_new[b], or T where n_new is NULL) become its rows
+ * [pos[b], pos[b] + m), for a prompt, a chunk of one or a single token.  For
+ * every block that receives rows, with a = max |x| over those rows and Q the
+ * largest code value (127, or 448 for e4m3):
+ *   need = the smallest power of two >= 2^-126 with a <= Q * need; 0 if a = 0
+ *   s'   = max(s, need), s the block's scale, or 0 when it holds no row before
+ *          pos[b]
+ *   new rows: code = round-to-nearest-even(x / s'), clamped to [-Q, Q]; 0 for s' = 0
+ *   rows the block already holds, when s' > s: code = round(code * (s / s'))
+ * Rows at or past pos[b] + m and the scales of untouched blocks are left as
+ * they are.
+ *   k_new, v_new : device rows [B, h_kv, T, d] of x_dtype (DA_FP32 or DA_BF16),
+ *                  element (b, h, i, j) at b * strides[0] + h * strides[1] +
+ *                  i * strides[2] + j (strides in elements, host arrays,
+ *                  multiples of 16 bytes, >= 0); 16-byte aligned.  Rows at or
+ *                  past m are not read.
+ *   pos          : device int32 [B], the rows each sequence holds.  Rows that
+ *                  would reach past n_max are not written, a pos outside
+ *                  [0, n_max] writes nothing, an n_new outside [0, T] is
+ *                  clamped; each sets DA_DEVERR_POS.
+ *   NaN and infinite elements are written as 0 and set DA_DEVERR_VALUE.
+ * Does not change lengths: the caller advances them.  T = 0 does nothing.
+ */
+DA_API int kv_append_q8b(const void* k_new, const void* v_new, const long long* k_strides,
+                         const long long* v_strides, int x_dtype, int T, const int32_t* n_new,
+                         void* K, void* V, float* k_scale, float* v_scale, int block,
+                         const int32_t* pos, int B, int h_kv, int d, int n_max, int dtype,
+                         int32_t* dev_error, cudaStream_t stream);
+
+/*
+ * Read rows of a block-scaled cache back as values: for every b, h and i < T
+ * with row_begin[b] + i < seq_lens[b] (row_begin NULL: 0)
+ *   k_out[b, h, i, :] = k_scale[b, h, block of the row] * value(code), v_out alike,
+ * rounded once to out_dtype (DA_FP32 or DA_BF16).  Other rows of the outputs
+ * are left as they are.
+ *   k_out, v_out : device [B, h_kv, T, d], 16-byte aligned
+ *   seq_lens     : device int32 [B]; outside [0, n_max]: clamped, DA_DEVERR_SEQ_LEN
+ *   row_begin    : nullable device int32 [B]; negative: nothing is read for that
+ *                  sequence, DA_DEVERR_SEQ_LEN
+ */
+DA_API int kv_read_q8b(const void* K, const void* V, const float* k_scale, const float* v_scale,
+                       int block, const int32_t* seq_lens, const int32_t* row_begin, void* k_out,
+                       void* v_out, int out_dtype, int T, int B, int h_kv, int d, int n_max,
+                       int dtype, int32_t* dev_error, cudaStream_t stream);
 
 /* Static, human-readable name of a da_status. */
 DA_API const char* decode_attn_status_string(int status);
