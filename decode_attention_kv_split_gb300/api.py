@@ -8,6 +8,7 @@ if the shared library is missing the first call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -542,66 +543,116 @@ class _CMod(ctypes.Structure):
                 ("slopes", ctypes.c_void_p), ("doc_begin", ctypes.c_void_p)]
 
 
-def _c_mod(mod: ScoreMod, B: int, h_q: int, device: torch.device) -> _CMod:
-    slopes, begin = mod.slopes, mod.doc_begin
+def _c_mod(mod: ScoreMod, B: int, h_q: int, device: int) -> _CMod:
+    """The C struct of ``mod`` for tensors on CUDA device ``device``."""
+    softcap, slopes, window, prefix, begin = mod
     if slopes is not None and (slopes.shape != (h_q,) or slopes.dtype != torch.float32
-                               or slopes.device != device or not slopes.is_contiguous()):
+                               or slopes.get_device() != device or not slopes.is_contiguous()):
         raise ValueError("slopes must be a contiguous float32 tensor [h_q] on the query's device")
-    if begin is not None and (begin.shape != (B,) or begin.dtype != torch.int32
-                              or begin.device != device or not begin.is_contiguous()):
-        raise ValueError("doc_begin must be a contiguous int32 tensor [B] on the query's device")
-    if not 0 <= mod.window < 1 << 31 or not 0 <= mod.prefix < 1 << 31:
+    if begin is not None:
+        _row_counts("doc_begin", begin, B, device)
+    if not 0 <= window < 1 << 31 or not 0 <= prefix < 1 << 31:
         raise ValueError("window and prefix must be non-negative ints")
-    return _CMod(mod.softcap, mod.window, mod.prefix,
-                 None if slopes is None else slopes.data_ptr(),
+    return _CMod(softcap, window, prefix, None if slopes is None else slopes.data_ptr(),
                  None if begin is None else begin.data_ptr())
 
 
-def _same_device(device: torch.device, **tensors) -> None:
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} must be on the device of the other tensors ({device})")
+def _row_counts(name: str, t: torch.Tensor | None, B: int, device: int) -> None:
+    if t is not None and (t.shape != (B,) or t.dtype != torch.int32 or t.get_device() != device
+                          or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous int32 tensor [B] on the device of the others")
 
 
-def _check_workspace(workspace: torch.Tensor, device: torch.device) -> None:
-    if workspace.device != device or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous tensor on the query's device")
+def _addr(t: torch.Tensor | None):
+    return None if t is None else t.data_ptr()
+
+
+def _error_word(t: torch.Tensor | None, device: int):
+    if t is None:
+        return None
+    if t.get_device() != device or t.dtype != torch.int32 or t.numel() < 1:
+        raise ValueError("dev_error must be an int32 tensor on the device of the others")
+    return t.data_ptr()
+
+
+def _cache_args(q, K, V, seq_lens, out, out_dtype):
+    """Checks of a decode over an fp32 or bf16 cache: its sizes, the output, the dtype code."""
+    device = q.get_device()
+    dtype = q.dtype
+    if q.dim() != 3 or K.dim() != 4 or V.dim() != 4:
+        raise ValueError("expected q [B, h_q, d_k], K [B, h_kv, n_max, d_k], V [B, h_kv, n_max, d_v]")
+    B, h_q, d_k = q.shape
+    Bk, h_kv, n_max, d = K.shape
+    d_v = V.shape[3]
+    if Bk != B or d != d_k or V.shape != (B, h_kv, n_max, d_v):
+        raise ValueError("q, K and V shapes disagree")
+    if dtype not in _DTYPES or K.dtype != dtype or V.dtype != dtype:
+        raise ValueError("q, K, V must share dtype float32 or bfloat16")
+    for name, t in (("q", q), ("K", K), ("V", V)):
+        if device < 0 or t.get_device() != device or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous CUDA tensor, all on one device")
+    _row_counts("seq_lens", seq_lens, B, device)
+    out, oflag = _out(out, out_dtype, B, h_q, d_v, q.device)
+    return device, out, (B, h_q, h_kv, d_k, d_v, n_max), _DTYPES[dtype] | oflag
+
+
+class _CallOn:
+    """Runs a call on tensors of CUDA device ``device``: makes it current where it is not, and
+    gives the raw stream (that of ``stream``, else the device's current one)."""
+    __slots__ = ("device", "stream", "prev", "raw")
+
+    def __init__(self, device: int, stream):
+        self.device, self.stream, self.prev = device, stream, -1
+
+    def __enter__(self):
+        cur = torch.cuda.current_device()
+        if cur != self.device:
+            self.prev = cur
+            torch.cuda.set_device(self.device)
+        s = self.stream
+        self.raw = (s.cuda_stream if s is not None
+                    else torch._C._cuda_getCurrentRawStream(self.device))
+        return self
+
+    def __exit__(self, *exc):
+        if self.prev >= 0:
+            torch.cuda.set_device(self.prev)
 
 
 _mod_bytes_cache: dict = {}
 
 
-def _terms_workspace(entry: str, cmod, key, device: torch.device, stream,
-                     workspace: torch.Tensor | None) -> tuple[torch.Tensor | None, int]:
-    """Workspace and its size for a call with score terms or block scales (``key``: the sizes,
-    dtype code and split choice).  Without a given one: a tensor of the stream the call runs on,
-    kept for its next call; while that stream is captured, a tensor of the graph's own pool,
-    since two graphs that share scratch may be replayed at the same time."""
+def _terms_workspace(entry: str, cmod, sizes, on: _CallOn, workspace: torch.Tensor | None):
+    """Address and bytes of the workspace of a call with score terms or block scales (``sizes``:
+    the sizes, dtype code and split choice).  Without a given one: a tensor of the stream the
+    call runs on, kept for its next call; while that stream is captured, a tensor of the graph's
+    own pool, since two graphs that share scratch may be replayed at the same time.  (The third
+    value keeps a graph's tensor alive through the call.)"""
     if workspace is not None:
-        _check_workspace(workspace, device)
-        return workspace, workspace.numel() * workspace.element_size()
-    seen = (cmod.window, cmod.prefix) if cmod is not None else None
-    full = (entry, device.index, seen, key)
-    need = _mod_bytes_cache.get(full)
+        if workspace.get_device() != on.device or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on the query's device")
+        return workspace.data_ptr(), workspace.numel() * workspace.element_size(), None
+    key = (entry, on.device, sizes, None if cmod is None else (cmod.window, cmod.prefix))
+    need = _mod_bytes_cache.get(key)
     if need is None:
         st = ctypes.c_int(0)
-        need = int(getattr(load(), entry)(None if cmod is None else ctypes.byref(cmod), *key,
+        need = int(getattr(load(), entry)(None if cmod is None else ctypes.byref(cmod), *sizes,
                                           ctypes.byref(st)))
         _check(st.value, entry)
         if len(_mod_bytes_cache) > 4096:
             _mod_bytes_cache.clear()
-        _mod_bytes_cache[full] = need
+        _mod_bytes_cache[key] = need
     if need == 0:
-        return None, 0
-    s = stream if stream is not None else torch.cuda.current_stream(device)
-    at = (device.index, s.cuda_stream, "terms")
-    ws = _ws_cache.get(at)
-    with torch.cuda.stream(stream):  # (None: the current one) memory returns in that stream's order
+        return None, 0, None
+    at = (on.device, on.raw, "terms")
+    with torch.cuda.stream(on.stream) if on.stream is not None else contextlib.nullcontext():
         if torch.cuda.is_current_stream_capturing():
-            return torch.empty(need, dtype=torch.uint8, device=device), need
+            ws = torch.empty(need, dtype=torch.uint8, device=on.device)
+            return ws.data_ptr(), need, ws
+        ws = _ws_cache.get(at)
         if ws is None or ws.numel() < need:
-            ws = _ws_cache[at] = torch.empty(need, dtype=torch.uint8, device=device)
-    return ws, ws.numel()
+            ws = _ws_cache[at] = torch.empty(need, dtype=torch.uint8, device=on.device)
+    return ws.data_ptr(), ws.numel(), None
 
 
 def decode_attn_mod(q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, seq_lens: torch.Tensor,
@@ -612,21 +663,17 @@ def decode_attn_mod(q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, seq_lens:
                     out_dtype: torch.dtype | None = None) -> torch.Tensor:
     """``decode_attn`` with score terms (calls ``decode_attn_mod``): capped scores, a distance
     bias, a window, documents and an always-seen prefix, as ``mod`` says.  Returns ``out``."""
-    B, h_q, h_kv, d_k, d_v, n_max = _cache_dims(q, K, V, seq_lens)
-    _same_device(q.device, K=K, V=V, seq_lens=seq_lens, dev_error=dev_error)
+    device, out, dims, dt = _cache_args(q, K, V, seq_lens, out, out_dtype)
+    cm = _c_mod(mod, dims[0], dims[1], device)
+    err = _error_word(dev_error, device)
     if scale is None:
-        scale = 1.0 / math.sqrt(d_k)
-    out, oflag = _out(out, out_dtype, B, h_q, d_v, q.device)
-    dt = _DTYPES[q.dtype] | oflag
-    cm = _c_mod(mod, B, h_q, q.device)
-    with _on_device(q):
-        ws, nbytes = _terms_workspace("decode_attn_mod_workspace_bytes", cm,
-                                      (B, h_q, h_kv, d_k, d_v, n_max, dt, int(num_splits)),
-                                      q.device, stream, workspace)
-        st = load().decode_attn_mod(_ptr(q), _ptr(K), _ptr(V), _ptr(seq_lens), ctypes.byref(cm),
-                                    _ptr(out), B, h_q, h_kv, d_k, d_v, n_max, float(scale), dt,
-                                    int(num_splits), _ptr(ws), nbytes, _ptr(dev_error),
-                                    _stream(q, stream))
+        scale = 1.0 / math.sqrt(dims[3])
+    with _CallOn(device, stream) as on:
+        ws, nbytes, _keep = _terms_workspace("decode_attn_mod_workspace_bytes", cm,
+                                             (*dims, dt, num_splits), on, workspace)
+        st = (_lib or load()).decode_attn_mod(
+            q.data_ptr(), K.data_ptr(), V.data_ptr(), seq_lens.data_ptr(), ctypes.byref(cm),
+            out.data_ptr(), *dims, scale, dt, num_splits, ws, nbytes, err, on.raw)
     _check(st, "decode_attn_mod")
     return out
 
@@ -642,58 +689,47 @@ def decode_attn_mod_append(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Te
     """``decode_attn_append`` with score terms (calls ``decode_attn_mod_append``): row
     seq_lens[b] of every kv head is appended, and the query sees what ``mod`` says of the
     seq_lens[b] + 1 rows.  Returns ``out``."""
-    B, h_q, h_kv, d_k, d_v, n_max = _cache_dims(q, K, V, seq_lens)
+    device, out, dims, dt = _cache_args(q, K, V, seq_lens, out, out_dtype)
+    B, h_q, h_kv, d_k, d_v, _ = dims
     if k_new.shape != (B, h_kv, d_k) or v_new.shape != (B, h_kv, d_v):
         raise ValueError("k_new/v_new must be [B, h_kv, d]")
     for name, t in (("k_new", k_new), ("v_new", v_new)):
-        if not t.is_cuda or not t.is_contiguous() or t.dtype != K.dtype:
+        if t.get_device() != device or not t.is_contiguous() or t.dtype != K.dtype:
             raise ValueError(f"{name} must be a contiguous CUDA tensor of the cache dtype")
-    if seq_lens_out is not None and (seq_lens_out.shape != (B,)
-                                     or seq_lens_out.dtype != torch.int32
-                                     or not seq_lens_out.is_contiguous()):
-        raise ValueError("seq_lens_out must be a contiguous int32 tensor of shape [B]")
-    _same_device(q.device, K=K, V=V, seq_lens=seq_lens, k_new=k_new, v_new=v_new,
-                 seq_lens_out=seq_lens_out, dev_error=dev_error)
+    _row_counts("seq_lens_out", seq_lens_out, B, device)
+    cm = _c_mod(mod, B, h_q, device)
+    err = _error_word(dev_error, device)
     if scale is None:
         scale = 1.0 / math.sqrt(d_k)
-    out, oflag = _out(out, out_dtype, B, h_q, d_v, q.device)
-    dt = _DTYPES[q.dtype] | oflag
-    cm = _c_mod(mod, B, h_q, q.device)
-    with _on_device(q):
-        ws, nbytes = _terms_workspace("decode_attn_mod_workspace_bytes", cm,
-                                      (B, h_q, h_kv, d_k, d_v, n_max, dt, int(num_splits)),
-                                      q.device, stream, workspace)
-        st = load().decode_attn_mod_append(
-            _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(K), _ptr(V), _ptr(seq_lens),
-            _ptr(seq_lens_out), ctypes.byref(cm), _ptr(out), B, h_q, h_kv, d_k, d_v, n_max,
-            float(scale), dt, int(num_splits), _ptr(ws), nbytes, _ptr(dev_error),
-            _stream(q, stream))
+    with _CallOn(device, stream) as on:
+        ws, nbytes, _keep = _terms_workspace("decode_attn_mod_workspace_bytes", cm,
+                                             (*dims, dt, num_splits), on, workspace)
+        st = (_lib or load()).decode_attn_mod_append(
+            q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), K.data_ptr(), V.data_ptr(),
+            seq_lens.data_ptr(), _addr(seq_lens_out), ctypes.byref(cm), out.data_ptr(), *dims,
+            scale, dt, num_splits, ws, nbytes, err, on.raw)
     _check(st, "decode_attn_mod_append")
     return out
 
 
 # ------------------------------------------------- 8-bit caches with a scale per block
 def _q8b_cache(K, V, k_scale, v_scale, block: int):
-    """Checks a block-scaled cache; returns B, h_kv, n_max, d."""
-    if K.dim() != 4 or V.shape != K.shape or K.dtype not in _Q8_DTYPES or V.dtype != K.dtype:
+    """Checks a block-scaled cache; returns its device, B, h_kv, n_max, d."""
+    dtype, device, shape = K.dtype, K.get_device(), K.shape
+    if len(shape) != 4 or V.shape != shape or dtype not in _Q8_DTYPES or V.dtype != dtype:
         raise ValueError("K, V must be 8-bit code tensors [B, h_kv, n_max, d] of one dtype")
     if block not in (16, 32, 64, 128):
         raise ValueError("block must be 16, 32, 64 or 128")
-    B, h_kv, n_max, d = K.shape
+    B, h_kv, n_max, d = shape
     scales = (B, h_kv, -(-n_max // block))
-    for name, t, shape, dt in (("K", K, K.shape, K.dtype), ("V", V, K.shape, K.dtype),
-                               ("k_scale", k_scale, scales, torch.float32),
-                               ("v_scale", v_scale, scales, torch.float32)):
-        if t.shape != shape or t.dtype != dt or not t.is_cuda or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous CUDA tensor {list(shape)} of {dt}")
-    _same_device(K.device, V=V, k_scale=k_scale, v_scale=v_scale)
-    return B, h_kv, n_max, d
-
-
-def _row_counts(name: str, t: torch.Tensor | None, B: int, device: torch.device) -> None:
-    if t is not None and (t.shape != (B,) or t.dtype != torch.int32 or t.device != device
-                          or not t.is_contiguous()):
-        raise ValueError(f"{name} must be a contiguous int32 tensor [B] on the cache's device")
+    for name, t, shp, dt in (("K", K, shape, dtype), ("V", V, shape, dtype),
+                             ("k_scale", k_scale, scales, torch.float32),
+                             ("v_scale", v_scale, scales, torch.float32)):
+        if t.shape != shp or t.dtype != dt or device < 0 or t.get_device() != device \
+                or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous CUDA tensor {list(shp)} of {dt}, all on "
+                             "one device")
+    return device, B, h_kv, n_max, d
 
 
 def decode_attn_q8b(q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, k_scale: torch.Tensor,
@@ -707,29 +743,31 @@ def decode_attn_q8b(q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, k_scale: 
     ``decode_attn_q8b``): K, V codes [B, h_kv, n_max, d] (torch.int8 or torch.float8_e4m3fn),
     scales float32 [B, h_kv, ceil(n_max / block)], q bf16 [B, h_q, d]; ``mod`` adds score terms.
     Returns ``out``."""
-    B, h_kv, n_max, d = _q8b_cache(K, V, k_scale, v_scale, block)
+    device, B, h_kv, n_max, d = _q8b_cache(K, V, k_scale, v_scale, block)
     if q.dim() != 3 or q.shape[0] != B or q.shape[2] != d or q.dtype != torch.bfloat16 \
-            or not q.is_contiguous():
-        raise ValueError("q must be a contiguous bfloat16 tensor [B, h_q, d]")
-    _row_counts("seq_lens", seq_lens, B, K.device)
-    _same_device(K.device, q=q, dev_error=dev_error)
+            or q.get_device() != device or not q.is_contiguous():
+        raise ValueError("q must be a contiguous bfloat16 tensor [B, h_q, d] on the cache's device")
+    _row_counts("seq_lens", seq_lens, B, device)
     h_q = q.shape[1]
-    if scale is None:
-        scale = 1.0 / math.sqrt(d)
     out, oflag = _out(out, out_dtype, B, h_q, d, q.device)
     dt = _Q8_DTYPES[K.dtype] | oflag
-    cm = None if mod is None else _c_mod(mod, B, h_q, q.device)
-    with _on_device(q):
-        ws, nbytes = _terms_workspace("decode_attn_q8b_workspace_bytes", cm,
-                                      (B, h_q, h_kv, d, d, n_max, dt, int(num_splits)), q.device,
-                                      stream, workspace)
-        st = load().decode_attn_q8b(_ptr(q), _ptr(K), _ptr(V), _ptr(k_scale), _ptr(v_scale), block,
-                                    _ptr(seq_lens), None if cm is None else ctypes.byref(cm),
-                                    _ptr(out), B, h_q, h_kv, d, d, n_max, float(scale), dt,
-                                    int(num_splits), _ptr(ws), nbytes, _ptr(dev_error),
-                                    _stream(q, stream))
+    cm = None if mod is None else _c_mod(mod, B, h_q, device)
+    err = _error_word(dev_error, device)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    with _CallOn(device, stream) as on:
+        ws, nbytes, _keep = _terms_workspace("decode_attn_q8b_workspace_bytes", cm,
+                                             (B, h_q, h_kv, d, d, n_max, dt, num_splits), on,
+                                             workspace)
+        st = (_lib or load()).decode_attn_q8b(
+            q.data_ptr(), K.data_ptr(), V.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), block,
+            seq_lens.data_ptr(), None if cm is None else ctypes.byref(cm), out.data_ptr(), B, h_q,
+            h_kv, d, d, n_max, scale, dt, num_splits, ws, nbytes, err, on.raw)
     _check(st, "decode_attn_q8b")
     return out
+
+
+_Strides = ctypes.c_longlong * 3
 
 
 def kv_append_q8b(k_new: torch.Tensor, v_new: torch.Tensor, K: torch.Tensor, V: torch.Tensor,
@@ -741,29 +779,32 @@ def kv_append_q8b(k_new: torch.Tensor, v_new: torch.Tensor, K: torch.Tensor, V: 
     dimension; [B, h_kv, d] for one row) become rows pos[b] .. of sequence b, n_new[b] of them
     where given.  A block's scale grows to what its new rows need, and the codes it holds are
     then rewritten.  Lengths are the caller's to advance."""
-    B, h_kv, n_max, d = _q8b_cache(K, V, k_scale, v_scale, block)
+    device, B, h_kv, n_max, d = _q8b_cache(K, V, k_scale, v_scale, block)
     if k_new.dim() == 3:
         k_new = k_new.unsqueeze(2)
     if v_new.dim() == 3:
         v_new = v_new.unsqueeze(2)
     T = k_new.shape[2] if k_new.dim() == 4 else -1
+    x_dtype = k_new.dtype
+    strides = []
     for name, t in (("k_new", k_new), ("v_new", v_new)):
-        if t.shape != (B, h_kv, T, d) or t.dtype not in _DTYPES or t.dtype != k_new.dtype:
-            raise ValueError(f"{name} must be a float32 or bfloat16 tensor [B, h_kv, T, d], "
-                             "k_new and v_new alike")
-        if t.stride(3) != 1:
+        if t.shape != (B, h_kv, T, d) or t.dtype not in _DTYPES or t.dtype != x_dtype \
+                or t.get_device() != device:
+            raise ValueError(f"{name} must be a float32 or bfloat16 tensor [B, h_kv, T, d] on the "
+                             "cache's device, k_new and v_new alike")
+        sb, sh, st, sd = t.stride()
+        if sd != 1:
             raise ValueError(f"{name} must be contiguous in its last dimension")
-    _row_counts("pos", pos, B, K.device)
-    _row_counts("n_new", n_new, B, K.device)
-    _same_device(K.device, k_new=k_new, v_new=v_new, dev_error=dev_error)
-    # a dimension of one element has no step: its stride in the tensor may be anything
-    ks, vs = ((ctypes.c_longlong * 3)(*(t.stride(i) if t.shape[i] > 1 else 0 for i in range(3)))
-              for t in (k_new, v_new))
-    with _on_device(K):
-        st = load().kv_append_q8b(_ptr(k_new), _ptr(v_new), ks, vs, _DTYPES[k_new.dtype], T,
-                                  _ptr(n_new), _ptr(K), _ptr(V), _ptr(k_scale), _ptr(v_scale),
-                                  block, _ptr(pos), B, h_kv, d, n_max, _Q8_DTYPES[K.dtype],
-                                  _ptr(dev_error), _stream(K, stream))
+        # a dimension of one element has no step: its stride in the tensor may be anything
+        strides.append(_Strides(sb if B > 1 else 0, sh if h_kv > 1 else 0, st if T > 1 else 0))
+    _row_counts("pos", pos, B, device)
+    _row_counts("n_new", n_new, B, device)
+    err = _error_word(dev_error, device)
+    with _CallOn(device, stream) as on:
+        st = (_lib or load()).kv_append_q8b(
+            k_new.data_ptr(), v_new.data_ptr(), strides[0], strides[1], _DTYPES[x_dtype], T,
+            _addr(n_new), K.data_ptr(), V.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), block,
+            pos.data_ptr(), B, h_kv, d, n_max, _Q8_DTYPES[K.dtype], err, on.raw)
     _check(st, "kv_append_q8b")
 
 
@@ -777,7 +818,7 @@ def kv_read_q8b(K: torch.Tensor, V: torch.Tensor, k_scale: torch.Tensor, v_scale
     [B, h_kv, rows, d] (float32 or bfloat16) while it lies below seq_lens[b]; other rows of the
     outputs are left as they are (zero in outputs allocated here, of ``out_dtype``, with ``rows``
     rows, n_max by default).  Returns ``(k_out, v_out)``."""
-    B, h_kv, n_max, d = _q8b_cache(K, V, k_scale, v_scale, block)
+    device, B, h_kv, n_max, d = _q8b_cache(K, V, k_scale, v_scale, block)
     if k_out is None or v_out is None:
         if k_out is not None or v_out is not None:
             raise ValueError("give both k_out and v_out, or neither")
@@ -789,16 +830,16 @@ def kv_read_q8b(K: torch.Tensor, V: torch.Tensor, k_scale: torch.Tensor, v_scale
         raise ValueError("rows disagrees with the outputs")
     for name, t in (("k_out", k_out), ("v_out", v_out)):
         if t.shape != (B, h_kv, T, d) or t.dtype not in _DTYPES or t.dtype != k_out.dtype \
-                or not t.is_contiguous():
+                or t.get_device() != device or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous float32 or bfloat16 tensor "
-                             "[B, h_kv, rows, d], k_out and v_out alike")
-    _row_counts("seq_lens", seq_lens, B, K.device)
-    _row_counts("row_begin", row_begin, B, K.device)
-    _same_device(K.device, k_out=k_out, v_out=v_out, dev_error=dev_error)
-    with _on_device(K):
-        st = load().kv_read_q8b(_ptr(K), _ptr(V), _ptr(k_scale), _ptr(v_scale), block,
-                                _ptr(seq_lens), _ptr(row_begin), _ptr(k_out), _ptr(v_out),
-                                _DTYPES[k_out.dtype], T, B, h_kv, d, n_max, _Q8_DTYPES[K.dtype],
-                                _ptr(dev_error), _stream(K, stream))
+                             "[B, h_kv, rows, d] on the cache's device, k_out and v_out alike")
+    _row_counts("seq_lens", seq_lens, B, device)
+    _row_counts("row_begin", row_begin, B, device)
+    err = _error_word(dev_error, device)
+    with _CallOn(device, stream) as on:
+        st = (_lib or load()).kv_read_q8b(
+            K.data_ptr(), V.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), block,
+            seq_lens.data_ptr(), _addr(row_begin), k_out.data_ptr(), v_out.data_ptr(),
+            _DTYPES[k_out.dtype], T, B, h_kv, d, n_max, _Q8_DTYPES[K.dtype], err, on.raw)
     _check(st, "kv_read_q8b")
     return k_out, v_out

@@ -206,7 +206,7 @@ int check_sizes(int B, int h_q, int h_kv, int d_k, int d_v, int n_max, int dtype
 int check_mod(const da_score_mod* mod) {
   if (!mod) return DA_ERR_NULL;
   if (!(mod->softcap >= 0.f) || !isfinite(mod->softcap)) return DA_ERR_SHAPE;
-  // the kernels hold softcap * log2(e) and its inverse in float
+  // the kernels hold softcap * log2(e) and scale / softcap in float
   if (mod->softcap > 0.f && (mod->softcap < 1e-30f || mod->softcap > 1e30f)) return DA_ERR_SHAPE;
   if (mod->window < 0 || mod->prefix < 0) return DA_ERR_SHAPE;
   if ((reinterpret_cast<uintptr_t>(mod->slopes) & 3u) != 0 ||
@@ -229,10 +229,7 @@ da::ScoreTerms score_terms_of(const da_score_mod* mod, int tile_rows, int b0) {
   t.prefix = mod->prefix;
   t.doc_begin = mod->doc_begin ? mod->doc_begin + b0 : nullptr;
   t.slopes = mod->slopes;
-  if (mod->softcap > 0.f) {
-    t.cap_log2 = float(double(mod->softcap) * 1.4426950408889634);
-    t.inv_cap_log2 = float(1.0 / (double(mod->softcap) * 1.4426950408889634));
-  }
+  t.cap_log2 = float(double(mod->softcap) * 1.4426950408889634);
   return t;
 }
 
@@ -504,7 +501,9 @@ int run_decode(const void* q, const void* K, const void* V, const int32_t* seq_l
     p.chunk_min = pl.chunk_min;
     p.max_splits = pl.max_splits;
     p.cta_speed = pl.ks.cta_speed;
-    p.scale_log2 = float(double(scale) * 1.4426950408889634);  // log2(e) = 1 / ln 2
+    p.scale_log2 = mod && mod->softcap > 0.f
+                       ? float(double(scale) / double(mod->softcap))
+                       : float(double(scale) * 1.4426950408889634);  // log2(e) = 1 / ln 2
 #ifdef DA_TEST_HOOKS
     p.withhold_cta = b0 == 0 ? g_test_withhold_cta.load() : -1;
 #endif

@@ -30,7 +30,7 @@ struct ScoreTerms {
   int window, prefix;            // window 0: unlimited
   const int32_t* doc_begin;      // nullable: [B], this launch's slice
   const float* slopes;           // nullable: [h_q]
-  float cap_log2, inv_cap_log2;  // softcap * log2 e and its inverse; 0: no cap
+  float cap_log2;                // softcap * log2 e (scale_log2 is then scale / softcap); 0: none
 };
 
 struct SplitParams {
@@ -82,7 +82,7 @@ struct SplitParams {
   int chunk_min;                 // else: smallest rows per split the device may choose
   int max_splits;                // partial slots per query head (ceil(n_max / chunk))
   float cta_speed;               // one CTA's streaming rate / its even share (split-length model)
-  float scale_log2;              // scale * log2(e)
+  float scale_log2;              // scale * log2(e); with capped scores scale / softcap
 #ifdef DA_TEST_HOOKS
   int withhold_cta;              // test builds: this CTA's producer never fills the last stage
                                  // of its first item (-1: none), so a wait must run out
@@ -523,27 +523,54 @@ struct TileMask<true> {
   }
 };
 
-// One query head's distance bias: slope * log2 e per row, and the row where it
-// is zero.  The largest biased row is taken as zero, not the query's own: a
-// softmax does not change when all scores move together, and the biases of the
-// rows that count stay small numbers.
-struct HeadBias {
-  float slope;
-  int zero;
-};
-__device__ __forceinline__ HeadBias head_bias(const SplitParams& p, const ItemT<true>& it, int head,
-                                              bool ok) {
-  HeadBias h;
-  h.slope = p.mod.slopes && ok ? __ldg(p.mod.slopes + head) * 1.4426950408889634f : 0.f;
-  h.zero = h.slope >= 0.f ? it.rows.hi : it.rows.lo;
-  return h;
+// A query head's distance bias per row in the log2 domain (0: none).
+__device__ __forceinline__ float head_slope(const SplitParams& p, int head, bool ok) {
+  return p.mod.slopes && ok ? __ldg(p.mod.slopes + head) * 1.4426950408889634f : 0.f;
 }
 
-// A score in the log2 domain with its terms: capped, then biased (row: its cache row).
-__device__ __forceinline__ float score_terms(const SplitParams& p, float x, int row,
-                                             const HeadBias& h) {
-  if (p.mod.cap_log2 > 0.f) x = p.mod.cap_log2 * tanhf(x * p.mod.inv_cap_log2);
-  return fmaf(h.slope, float(row - h.zero), x);
+// The distances of a cache row that the biases multiply.  A bias is zero at the
+// seen row where it is largest (the last one for a slope >= 0, else the first)
+// and negative elsewhere, not zero at the query's own row: a softmax does not
+// change when all scores of a head move together, and the biases of the rows
+// that count stay small numbers.
+struct RowDistance {
+  float to_last, to_first;
+  __device__ __forceinline__ RowDistance(const ItemT<true>& it, int row)
+      : to_last(float(row - it.rows.hi)), to_first(float(row - it.rows.lo)) {}
+};
+
+// tanh to about 3 * 2^-23 of its value.  Below 1/2 the odd polynomial
+// x + x u (c0 + u (c1 + u (c2 + u c3))), u = x^2, with the c fitted here for
+// the smallest largest relative error (1.5e-8); from 1/2 on
+// (1 - e) / (1 + e) with e = exp(-2 |x|) <= 0.37, where 1 - e loses no digits.
+// Both sides are computed and one selected: 14 instructions, two of them on
+// the special-function unit, and no branch for a warp's rows to differ on (the
+// library's tanhf branches: with 16 capped scores per thread the 32-head
+// kernel took 57.5 us a step at 8 x 32768 rows).
+__device__ __forceinline__ float tanh_fast(float x) {
+  const float u = x * x;
+  float c = fmaf(u, 0.01724149100482464f, -0.05304549261927605f);
+  c = fmaf(u, c, 0.13325878977775574f);
+  c = fmaf(u, c, -0.333331435918808f);
+  const float small = fmaf(x * u, c, x);
+  const float e = ex2(-2.f * 1.4426950408889634f * fabsf(x));
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+  const float large = copysignf((1.f - e) * r, x);
+  return fabsf(x) < 0.5f ? small : large;
+}
+
+// A log2-domain score with its distance bias.
+__device__ __forceinline__ float biased(float x, const RowDistance& d, float slope) {
+  return fmaf(slope, slope >= 0.f ? d.to_last : d.to_first, x);
+}
+
+// A raw score (times scale_log2) with its terms, in the log2 domain.
+__device__ __forceinline__ float score_terms(const SplitParams& p, float x, const RowDistance& d,
+                                             float slope) {
+  if (p.mod.cap_log2 > 0.f) x = p.mod.cap_log2 * tanh_fast(x);
+  if (p.mod.slopes) x = biased(x, d, slope);
+  return x;
 }
 
 template <int TILE>

@@ -156,14 +156,14 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
     const int head_base = it.hc * Cfg::kHeadsPerCta + hg * kHPW;
     uint32_t qf[NB][MBK][2];
 
-    [[maybe_unused]] HeadBias bias[NB][2];
+    [[maybe_unused]] float slope[NB][2];
     if constexpr (MOD) {
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const int hl = head_base + nb * 8 + 2 * c + j;
-          bias[nb][j] = head_bias(p, it, it.kvh * p.group + hl, hl < p.group);
+          slope[nb][j] = head_slope(p, it.kvh * p.group + hl, hl < p.group);
         }
     }
 
@@ -274,9 +274,9 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
               s[kb][nb][j] *= p.scale_log2;
               s[kb][nb][j + 2] *= p.scale_log2;
               if constexpr (MOD) {
-                const int l = mask.row0 + row_lo;
-                s[kb][nb][j] = score_terms(p, s[kb][nb][j], l, bias[nb][j]);
-                s[kb][nb][j + 2] = score_terms(p, s[kb][nb][j + 2], l + 8, bias[nb][j]);
+                const RowDistance lo(it, mask.row0 + row_lo), hi(it, mask.row0 + row_lo + 8);
+                s[kb][nb][j] = score_terms(p, s[kb][nb][j], lo, slope[nb][j]);
+                s[kb][nb][j + 2] = score_terms(p, s[kb][nb][j + 2], hi, slope[nb][j]);
               }
               s[kb][nb][j] = mask.seen(row_lo) ? s[kb][nb][j] : -INFINITY;
               s[kb][nb][j + 2] = mask.seen(row_lo + 8) ? s[kb][nb][j + 2] : -INFINITY;

@@ -135,11 +135,11 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
     // the log2 domain) arrives with the item's first stage.
     float qv[G][EPL];
 
-    [[maybe_unused]] HeadBias bias[G];
+    [[maybe_unused]] float slope[G];
     if constexpr (MOD) {
 #pragma unroll
       for (int g = 0; g < G; ++g)
-        bias[g] = head_bias(p, it, it.kvh * p.group + head_base + g, head_base + g < p.group);
+        slope[g] = head_slope(p, it.kvh * p.group + head_base + g, head_base + g < p.group);
     }
 
     float m_run[G], l_run[G], acc[G][EPL];
@@ -225,7 +225,8 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
             x += __shfl_xor_sync(0xffffffffu, x, 4);
             x += __shfl_xor_sync(0xffffffffu, x, 2);
             x += __shfl_xor_sync(0xffffffffu, x, 1);
-            if constexpr (MOD) x = score_terms(p, x, mask.row0 + row0 + rr, bias[g]);
+            if constexpr (MOD)
+              x = score_terms(p, x, RowDistance(it, mask.row0 + row0 + rr), slope[g]);
             s[g][rr] = mask.seen(row0 + rr) ? x : -INFINITY;
           }
         // Step II: running max and sum (warp-uniform values).

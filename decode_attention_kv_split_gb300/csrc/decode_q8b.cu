@@ -223,14 +223,14 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
     load_scales(0, sk_next, sv_next);
     sk_now = sk_next, sv_now = sv_next;
 
-    [[maybe_unused]] HeadBias bias[NB][2];
+    [[maybe_unused]] float slope[NB][2];
     if constexpr (MOD) {
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const int hl = head_base + nb * 8 + 2 * t + j;
-          bias[nb][j] = head_bias(p, it, it.kvh * p.group + hl, hl < p.group);
+          slope[nb][j] = head_slope(p, it.kvh * p.group + hl, hl < p.group);
         }
     }
     uint32_t qf[MB][NB][2];  // B fragments of q, in the permuted column order
@@ -349,8 +349,8 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
           for (int j = 0; j < 2; ++j) {
             float xA = s[nb][j] * ks, xB = s[nb][j + 2] * ks;
             if constexpr (MOD) {
-              xA = score_terms(p, xA, mask.row0 + rA, bias[nb][j]);
-              xB = score_terms(p, xB, mask.row0 + rB, bias[nb][j]);
+              xA = score_terms(p, xA, RowDistance(it, mask.row0 + rA), slope[nb][j]);
+              xB = score_terms(p, xB, RowDistance(it, mask.row0 + rB), slope[nb][j]);
             }
             xA = seenA ? xA : -INFINITY;
             xB = seenB ? xB : -INFINITY;

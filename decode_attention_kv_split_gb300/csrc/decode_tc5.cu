@@ -167,11 +167,13 @@ struct Tc5Cfg {
   static constexpr int kSchedWords = da::kSchedWords;  // work list (common.cuh)
   static constexpr int kRedGroup = 4 * (NH / 2) + 4;   // [4 quarters][NH/2] partials + 4 flags
   static constexpr int kRedFloats = 2 * 2 * kRedGroup; // two groups, double-buffered
+  static constexpr int kSlopeFloats = NH;              // distance biases of the item's heads
   // kfull, kempty, vfull, vempty, s_full[2], p_full[2], pv_done[2], fin
   static constexpr int kBars = 2 * KST + 2 * VST + 2 + 2 + 2 + 1;
   static constexpr size_t kSmemBytes = 1024 + size_t(KST + VST) * (kTileBytes + kRowBytes) +
                                        kQBytes + 2 * kPBytes +
-                                       size_t(kSchedWords + kRedFloats) * 4 + kBars * 8 + 32;
+                                       size_t(kSchedWords + kRedFloats + kSlopeFloats) * 4 +
+                                       kBars * 8 + 32;
   static_assert(NH == 16 || NH == 32, "heads per item");
   static_assert(kSmemBytes <= 227 * 1024, "shared memory");
   static_assert(kRedFloats % 2 == 0, "alignment");
@@ -258,7 +260,8 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
   uint8_t* vnew = knew + size_t(KST) * Cfg::kRowBytes;           // [VST] appended V rows
   int* sched_words = reinterpret_cast<int*>(vnew + size_t(VST) * Cfg::kRowBytes);
   float* red = reinterpret_cast<float*>(sched_words + Cfg::kSchedWords);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(red + Cfg::kRedFloats);
+  float* slopes = red + Cfg::kRedFloats;                         // 16-byte aligned
+  uint64_t* bars = reinterpret_cast<uint64_t*>(slopes + Cfg::kSlopeFloats);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + Cfg::kBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -552,11 +555,15 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
     const int head0 = it.hc * NH;
     const size_t bh0 = size_t(it.b) * p.h_q + size_t(it.kvh) * p.group + head0;
     const int nheads = min(NH, p.group - head0);
-    [[maybe_unused]] HeadBias bias[HT];
     if constexpr (MOD) {
-#pragma unroll
-      for (int h = 0; h < HT; ++h)
-        bias[h] = head_bias(p, it, it.kvh * p.group + head0 + hb + h, hb + h < nheads);
+      // the biases of this group's heads, read back by every thread of it (16
+      // more registers a thread would spill)
+      if (p.mod.slopes) {
+        if (t_row < HT)
+          slopes[hb + t_row] =
+              head_slope(p, it.kvh * p.group + head0 + hb + t_row, hb + t_row < nheads);
+        named_bar_sync(bar_id, 128);
+      }
     }
     float m_run[HT], l_part[HT];
 #pragma unroll
@@ -582,14 +589,31 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
         tc5::ld16x(s_col0 + (j & 1) * NH + hb + lane_base, s, HT);
         tc5::wait_ld();
       }
+      if constexpr (MOD) {
+        if (p.mod.cap_log2 > 0.f) {
 #pragma unroll
-      for (int h = 0; h < HT; ++h) {
-        if constexpr (MOD) {
-          const float x = score_terms(p, s[h] * p.scale_log2, mask.row0 + t_row, bias[h]);
-          s[h] = (live && row_ok) ? x : -INFINITY;
+          for (int h = 0; h < HT; ++h)
+            s[h] = p.mod.cap_log2 * tanh_fast(s[h] * p.scale_log2);
         } else {
-          s[h] = (live && row_ok) ? s[h] * p.scale_log2 : -INFINITY;
+#pragma unroll
+          for (int h = 0; h < HT; ++h) s[h] *= p.scale_log2;
         }
+        if (p.mod.slopes) {
+          const RowDistance dist(it, mask.row0 + t_row);
+#pragma unroll
+          for (int h = 0; h < HT; h += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(slopes + hb + h);
+            s[h] = biased(s[h], dist, f.x);
+            s[h + 1] = biased(s[h + 1], dist, f.y);
+            s[h + 2] = biased(s[h + 2], dist, f.z);
+            s[h + 3] = biased(s[h + 3], dist, f.w);
+          }
+        }
+#pragma unroll
+        for (int h = 0; h < HT; ++h) s[h] = (live && row_ok) ? s[h] : -INFINITY;
+      } else {
+#pragma unroll
+        for (int h = 0; h < HT; ++h) s[h] = (live && row_ok) ? s[h] * p.scale_log2 : -INFINITY;
       }
 
       // Running max: exact on an item's first stage, else only when some score

@@ -138,10 +138,10 @@ def test_binding_checks_tensors(lib):
     with pytest.raises(ValueError):
         api.decode_attn_q8b(q, codes, codes, scale, scale, lens, block=16)
     with pytest.raises(ValueError, match="slopes"):
-        api._c_mod(api.ScoreMod(slopes=torch.zeros(3)), 1, 2, torch.device("cpu"))
+        api._c_mod(api.ScoreMod(slopes=torch.zeros(3)), 1, 2, 0)
     with pytest.raises(ValueError, match="doc_begin"):
-        api._c_mod(api.ScoreMod(doc_begin=torch.zeros(1)), 1, 2, torch.device("cpu"))
+        api._c_mod(api.ScoreMod(doc_begin=torch.zeros(1)), 1, 2, 0)
     with pytest.raises(ValueError, match="window"):
-        api._c_mod(api.ScoreMod(window=-1), 1, 2, torch.device("cpu"))
+        api._c_mod(api.ScoreMod(window=-1), 1, 2, -1)
     with pytest.raises(ValueError, match="window"):
-        api._c_mod(api.ScoreMod(prefix=1 << 31), 1, 2, torch.device("cpu"))
+        api._c_mod(api.ScoreMod(prefix=1 << 31), 1, 2, -1)
