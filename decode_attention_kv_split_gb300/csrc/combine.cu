@@ -65,7 +65,7 @@ __device__ __forceinline__ int splits_of_head(const SplitParams& p, int bh, int 
   if (appended) ++n;
   if (p.mod.on) {  // the rows of the work list
     ItemRows r;
-    n = list_rows(p.mod, p.mod.tile_rows, b, n, appended, r);
+    n = list_rows(p.mod, p.mod.tile_rows, doc_begin(p.mod, b), n, appended, r);
   } else if (!appended) {
     n = max(0, min(n, p.row_lim) - p.row_off);
   }

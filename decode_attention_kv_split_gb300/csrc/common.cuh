@@ -418,6 +418,11 @@ struct Schedule {
   __device__ __forceinline__ int lens(int b) const { return w[kSchedLens + b]; }
 };
 
+// With score terms and at most kSeqCache sequences, the unused upper halves of
+// first[] and lens[] hold each sequence's cached rows and document begin, from
+// which the items' row mappings are taken without another trip to memory.
+constexpr int kSeqCache = kMaxBatchPerLaunch / 2;
+
 constexpr int kAppendFlag = int(0x80000000u);
 __device__ __forceinline__ int len_of(int v) { return v & 0x7fffffff; }
 
@@ -457,12 +462,15 @@ __device__ __forceinline__ int cache_row(const ItemT<true>& it, int v) {
   return v < it.rows.pt ? v : v + it.rows.shift;
 }
 
-// The row mapping of sequence b at n cached rows (the appended one among them)
-// and the rows its work list holds.  An appended row is always in the list,
-// seen or not, so that it reaches the cache.
-__device__ __forceinline__ int list_rows(const ScoreTerms& m, int tile, int b, int n, bool app,
+__device__ __forceinline__ int doc_begin(const ScoreTerms& m, int b) {
+  return m.doc_begin ? __ldcg(m.doc_begin + b) : 0;
+}
+
+// The row mapping of a sequence with n cached rows (the appended one among
+// them) whose document begins at `begin`, and the rows its work list holds.  An
+// appended row is always in the list, seen or not, so that it reaches the cache.
+__device__ __forceinline__ int list_rows(const ScoreTerms& m, int tile, int begin, int n, bool app,
                                          ItemRows& r) {
-  const int begin = m.doc_begin ? __ldcg(m.doc_begin + b) : 0;
   int first = begin;
   if (m.window > 0) first = max(first, n - m.window);
   first = min(max(first, 0), n);
@@ -489,7 +497,7 @@ __device__ __forceinline__ ItemRows item_rows(const SplitParams& p, int b) {
   const bool app = p.append && n >= 0 && n < p.n_max;
   n = min(max(n, 0), p.n_max) + (app ? 1 : 0);
   ItemRows r;
-  list_rows(p.mod, TILE, b, n, app, r);
+  list_rows(p.mod, TILE, doc_begin(p.mod, b), n, app, r);
   return r;
 }
 
@@ -537,6 +545,10 @@ struct RowDistance {
   float to_last, to_first;
   __device__ __forceinline__ RowDistance(const ItemT<true>& it, int row)
       : to_last(float(row - it.rows.hi)), to_first(float(row - it.rows.lo)) {}
+  // k rows on (integer conversions run at a quarter of the rate of an addition;
+  // exact up to 2^24 rows, and one float rounding of a far row's bias behind that)
+  __device__ __forceinline__ RowDistance(const RowDistance& d, int k)
+      : to_last(d.to_last + float(k)), to_first(d.to_first + float(k)) {}
 };
 
 // tanh to about 3 * 2^-23 of its value.  Below 1/2 the odd polynomial
@@ -563,14 +575,6 @@ __device__ __forceinline__ float tanh_fast(float x) {
 // A log2-domain score with its distance bias.
 __device__ __forceinline__ float biased(float x, const RowDistance& d, float slope) {
   return fmaf(slope, slope >= 0.f ? d.to_last : d.to_first, x);
-}
-
-// A raw score (times scale_log2) with its terms, in the log2 domain.
-__device__ __forceinline__ float score_terms(const SplitParams& p, float x, const RowDistance& d,
-                                             float slope) {
-  if (p.mod.cap_log2 > 0.f) x = p.mod.cap_log2 * tanh_fast(x);
-  if (p.mod.slopes) x = biased(x, d, slope);
-  return x;
 }
 
 template <int TILE>
@@ -879,9 +883,10 @@ __device__ __forceinline__ int choose_chunk_warp(const SplitParams& p, int n_lan
 // The rows a sequence contributes to the work list, from its seq_lens value:
 // clamped into [0, n_max], plus the appended row when there is room for it
 // (kAppendFlag set), else cut to the decoded row range.  `n_out` receives the
-// length after the append (the seq_lens_out value).
+// length after the append (the seq_lens_out value).  With score terms: the rows
+// its work list holds, for a document that begins at `begin`.
 template <int TILE, bool MOD>
-__device__ __forceinline__ int list_len(const SplitParams& p, int b, int n, bool& bad,
+__device__ __forceinline__ int list_len(const SplitParams& p, int begin, int n, bool& bad,
                                         bool& bad_pos, int& n_out) {
   bool app = false;
   if (p.append) {
@@ -896,12 +901,27 @@ __device__ __forceinline__ int list_len(const SplitParams& p, int b, int n, bool
   n_out = n;
   if (MOD) {
     ItemRows r;
-    n = list_rows(p.mod, TILE, b, n, app, r);
+    n = list_rows(p.mod, TILE, begin, n, app, r);
   } else if (!app) {  // rows of the decoded range (all of them unless a range was asked for)
     n = min(n, p.row_lim) - p.row_off;
     n = n < 0 ? 0 : n;
   }
   return app ? (n | kAppendFlag) : n;
+}
+
+// The row mapping of the item at w, from the sequences' values the list was built on.
+template <int TILE>
+__device__ __forceinline__ void put_item_rows(const SplitParams& p, const int* sched, int* w) {
+  const int b = w[0];
+  ItemRows r;
+  list_rows(p.mod, TILE, sched[kSchedLens + kSeqCache + b], sched[kSeqCache + 1 + b],
+            (sched[kSchedLens + b] & kAppendFlag) != 0, r);
+  w[8] = r.prefix;
+  w[9] = r.first;
+  w[10] = r.pt;
+  w[11] = r.shift;
+  w[12] = r.lo;
+  w[13] = r.hi;
 }
 
 // Builds the work list in shared memory; every thread of the CTA must call it.
@@ -923,9 +943,15 @@ __device__ __forceinline__ Schedule build_schedule_core(const SplitParams& p, in
   int my_n = 0;      // n of sequence tid (the one-warp path: B <= 32)
   for (int b = tid; b < p.B; b += blockDim.x) {
     int n_out;
-    const int lv = list_len<TILE, MOD>(p, b, __ldcg(p.seq_lens + b), bad, bad_pos, n_out);  // through L2
+    const int begin = MOD ? doc_begin(p.mod, b) : 0;
+    const int lv = list_len<TILE, MOD>(p, begin, __ldcg(p.seq_lens + b), bad, bad_pos,
+                                       n_out);  // through L2
     const int n = len_of(lv);
     lens[b] = lv;
+    if (MOD && p.B <= kSeqCache) {
+      first[kSeqCache + 1 + b] = n_out;
+      lens[kSeqCache + b] = begin;
+    }
     rows += float(n);
     nmax = n > nmax ? n : nmax;
     my_n = n;
@@ -993,6 +1019,7 @@ __device__ __forceinline__ Schedule build_schedule_core(const SplitParams& p, in
         w[5] = it.row_begin;
         w[6] = it.row_end;
         w[7] = it.new_row;
+        if (MOD && p.B <= kSeqCache) put_item_rows<TILE>(p, sched, w);
       }
     }
     __syncthreads();
@@ -1087,6 +1114,7 @@ __device__ __forceinline__ Schedule build_schedule_core(const SplitParams& p, in
     w[5] = it.row_begin;
     w[6] = it.row_end;
     w[7] = it.new_row;
+    if (MOD && p.B <= kSeqCache) put_item_rows<TILE>(p, sched, w);
   }
   __syncthreads();
   return s;
@@ -1106,8 +1134,11 @@ __device__ __forceinline__ Schedule commit_schedule(const SplitParams& p, int* s
   int changed = 0;
   for (int b = tid; b < p.B; b += blockDim.x) {
     int n_out;
-    const int lv = list_len<TILE, MOD>(p, b, __ldcg(p.seq_lens + b), bad, bad_pos, n_out);
+    const int begin = MOD ? doc_begin(p.mod, b) : 0;
+    const int lv = list_len<TILE, MOD>(p, begin, __ldcg(p.seq_lens + b), bad, bad_pos, n_out);
     changed |= lv != lens[b];
+    if (MOD && p.B <= kSeqCache)
+      changed |= n_out != sched[kSeqCache + 1 + b] || begin != lens[kSeqCache + b];
     if (blockIdx.x == 0 && p.seq_lens_out && DA_IN(p, b, p.B)) p.seq_lens_out[b] = n_out;
   }
   if (bad && blockIdx.x == 0) flag_error(p.dev_error, DA_DEVERR_SEQ_LEN);
@@ -1120,7 +1151,7 @@ __device__ __forceinline__ Schedule commit_schedule(const SplitParams& p, int* s
       if (it.split == 0 && DA_IN(p, s.u0 + t, p.B * p.h_kv * p.head_chunks))
         p.unit_nv[s.u0 + t] = it.nv;  // the unit's first CTA
     }
-  if (MOD) {  // the items' row mappings, now that nothing changes under them
+  if (MOD && p.B > kSeqCache) {  // the items' row mappings, now that nothing changes under them
     for (int t = tid; t < s.mine && t < item_cache<MOD>(); t += blockDim.x) {
       int* w = sched + kSchedItems + t * item_words<MOD>();
       const ItemRows r = item_rows<TILE>(p, w[0]);
@@ -1285,12 +1316,14 @@ __device__ __forceinline__ bool read_hint(const SplitParams& p, int4 h, int max_
 }
 
 // After the work list is built: record this CTA's first tiles for the next launch.
+// (last_first: the item's tiles are taken from the last one down.)
 template <int TILE, bool MOD>
 __device__ __forceinline__ void write_hint(const SplitParams& p, const ItemT<MOD>& it,
-                                           int max_tiles) {
+                                           int max_tiles, bool last_first = false) {
   if (!p.hints || blockIdx.x >= unsigned(kMaxHintCtas)) return;
   const int z = (p.b_offset + it.b) * p.h_kv + it.kvh;
-  const int y0 = cache_row(it, it.row_begin);
+  const int skip = last_first && it.tiles > max_tiles ? it.tiles - max_tiles : 0;
+  const int y0 = cache_row(it, it.row_begin + skip * TILE);
   const int tiles = it.tiles < max_tiles ? it.tiles : max_tiles;
   p.hints[blockIdx.x] = make_int4(z, y0, tiles, z ^ y0 ^ tiles ^ kHintSeal);
 }

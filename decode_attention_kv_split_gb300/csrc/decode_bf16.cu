@@ -261,6 +261,42 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
         }
 
         // ---- Step II: mask rows past the end, scale, running max and sum.
+        bool seen[KBW][2];  // this lane's rows of each block
+        const bool all = mask.all_seen(0, Cfg::kTile);
+#pragma unroll
+        for (int kb = 0; kb < KBW; ++kb) {
+          seen[kb][0] = all || mask.seen(key0 + kb * 16 + r);
+          seen[kb][1] = all || mask.seen(key0 + kb * 16 + r + 8);
+        }
+        if constexpr (MOD) {  // score terms (one branch for all of a lane's scores)
+          if (p.mod.cap_log2 > 0.f) {
+#pragma unroll
+            for (int kb = 0; kb < KBW; ++kb)
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  s[kb][nb][e] = p.mod.cap_log2 * tanh_fast(s[kb][nb][e] * p.scale_log2);
+          } else {
+#pragma unroll
+            for (int kb = 0; kb < KBW; ++kb)
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[kb][nb][e] *= p.scale_log2;
+          }
+          if (p.mod.slopes) {
+            const RowDistance dist(it, mask.row0 + key0 + r);
+#pragma unroll
+            for (int kb = 0; kb < KBW; ++kb)
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  s[kb][nb][e] = biased(s[kb][nb][e], RowDistance(dist, kb * 16 + (e >> 1) * 8),
+                                        slope[nb][e & 1]);
+          }
+        }
         float alpha[NB][2];
         bool changed = false;
 #pragma unroll
@@ -270,16 +306,12 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
             float mx = -INFINITY;
 #pragma unroll
             for (int kb = 0; kb < KBW; ++kb) {
-              const int row_lo = key0 + kb * 16 + r;
-              s[kb][nb][j] *= p.scale_log2;
-              s[kb][nb][j + 2] *= p.scale_log2;
-              if constexpr (MOD) {
-                const RowDistance lo(it, mask.row0 + row_lo), hi(it, mask.row0 + row_lo + 8);
-                s[kb][nb][j] = score_terms(p, s[kb][nb][j], lo, slope[nb][j]);
-                s[kb][nb][j + 2] = score_terms(p, s[kb][nb][j + 2], hi, slope[nb][j]);
+              if constexpr (!MOD) {
+                s[kb][nb][j] *= p.scale_log2;
+                s[kb][nb][j + 2] *= p.scale_log2;
               }
-              s[kb][nb][j] = mask.seen(row_lo) ? s[kb][nb][j] : -INFINITY;
-              s[kb][nb][j + 2] = mask.seen(row_lo + 8) ? s[kb][nb][j + 2] : -INFINITY;
+              s[kb][nb][j] = seen[kb][0] ? s[kb][nb][j] : -INFINITY;
+              s[kb][nb][j + 2] = seen[kb][1] ? s[kb][nb][j + 2] : -INFINITY;
               mx = fmaxf(mx, fmaxf(s[kb][nb][j], s[kb][nb][j + 2]));
             }
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
@@ -330,7 +362,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
             pl[nb][1] = movmatrix_trans(l1);
           }
           const int blk0 = key0 + kb * 16;
-          const bool partial = !mask.all_seen(blk0, 16);
+          const bool partial = !all && !mask.all_seen(blk0, 16);
           // rows held by this lane's A registers: {2c, 2c+1} and {8+2c, 9+2c}
           const uint32_t mlo = (mask.seen(blk0 + 2 * c) ? 0x0000ffffu : 0u) |
                                (mask.seen(blk0 + 2 * c + 1) ? 0xffff0000u : 0u);

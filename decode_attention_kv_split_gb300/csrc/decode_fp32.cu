@@ -200,7 +200,14 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
 
       // warp-uniform (the shuffles below need the whole warp)
       const bool live = __all_sync(0xffffffffu, !*abort_flag);
-      if (live && mask.any_seen(row0, RPW)) {
+      // which of this warp's rows are seen (one bit each; a whole tile usually is)
+      uint32_t seen = (1u << RPW) - 1u;
+      if (!mask.all_seen(0, Cfg::kTile)) {
+        seen = 0;
+#pragma unroll
+        for (int rr = 0; rr < RPW; ++rr) seen |= uint32_t(mask.seen(row0 + rr)) << rr;
+      }
+      if (live && seen) {
         // Step I: s[g][r] = (scale*log2e*q_g) . K_row, reduced across the warp.
         float s[G][RPW];
 #pragma unroll
@@ -225,10 +232,30 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
             x += __shfl_xor_sync(0xffffffffu, x, 4);
             x += __shfl_xor_sync(0xffffffffu, x, 2);
             x += __shfl_xor_sync(0xffffffffu, x, 1);
-            if constexpr (MOD)
-              x = score_terms(p, x, RowDistance(it, mask.row0 + row0 + rr), slope[g]);
-            s[g][rr] = mask.seen(row0 + rr) ? x : -INFINITY;
+            s[g][rr] = MOD || (seen >> rr & 1u) ? x : -INFINITY;
           }
+        if constexpr (MOD) {  // score terms (one branch for all of them), then the mask
+          if (p.mod.cap_log2 > 0.f) {
+#pragma unroll
+            for (int g = 0; g < G; ++g)
+#pragma unroll
+              for (int rr = 0; rr < RPW; ++rr)
+                s[g][rr] = p.mod.cap_log2 * tanh_fast(s[g][rr]);
+          }
+          if (p.mod.slopes) {
+            const RowDistance dist(it, mask.row0 + row0);
+#pragma unroll
+            for (int g = 0; g < G; ++g)
+#pragma unroll
+              for (int rr = 0; rr < RPW; ++rr)
+                s[g][rr] = biased(s[g][rr], RowDistance(dist, rr), slope[g]);
+          }
+#pragma unroll
+          for (int g = 0; g < G; ++g)
+#pragma unroll
+            for (int rr = 0; rr < RPW; ++rr)
+              s[g][rr] = (seen >> rr & 1u) ? s[g][rr] : -INFINITY;
+        }
         // Step II: running max and sum (warp-uniform values).
         float alpha[G];
 #pragma unroll
@@ -253,7 +280,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
         // Step III: acc += p * V_row over the valid rows of this warp.
 #pragma unroll
         for (int rr = 0; rr < RPW; ++rr) {
-          if (mask.seen(row0 + rr)) {
+          if (seen >> rr & 1u) {
             float vv[EPL];
             load_lane<EPL>(vv, vs + (row0 + rr) * D + lane * EPL);
 #pragma unroll

@@ -340,6 +340,26 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
           for (int e = 0; e < 4; ++e) s[0][e] += s2[e];
         }
         // ---- Step II: scale, terms, mask, running max and sum
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[nb][e] *= ks;
+        if constexpr (MOD) {  // one branch for all of a lane's scores
+          if (p.mod.cap_log2 > 0.f) {
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) s[nb][e] = p.mod.cap_log2 * tanh_fast(s[nb][e]);
+          }
+          if (p.mod.slopes) {
+            const RowDistance dist(it, mask.row0 + rA);
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                s[nb][e] = biased(s[nb][e], RowDistance(dist, (e >> 1) * 8), slope[nb][e & 1]);
+          }
+        }
         const bool seenA = mask.seen(rA), seenB = mask.seen(rB);
         float alpha[NB][2];
         bool changed = false;
@@ -347,13 +367,8 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            float xA = s[nb][j] * ks, xB = s[nb][j + 2] * ks;
-            if constexpr (MOD) {
-              xA = score_terms(p, xA, RowDistance(it, mask.row0 + rA), slope[nb][j]);
-              xB = score_terms(p, xB, RowDistance(it, mask.row0 + rB), slope[nb][j]);
-            }
-            xA = seenA ? xA : -INFINITY;
-            xB = seenB ? xB : -INFINITY;
+            const float xA = seenA ? s[nb][j] : -INFINITY;
+            const float xB = seenB ? s[nb][j + 2] : -INFINITY;
             float mx = fmaxf(xA, xB);
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
