@@ -220,7 +220,7 @@ long long seen_rows(const da_score_mod* mod, int n_max) {
   return mod->window > 0 ? (long long)mod->window + mod->prefix : n_max;
 }
 
-da::ScoreTerms score_terms_of(const da_score_mod* mod, int tile_rows, int b0) {
+da::ScoreTerms score_terms_of(const da_score_mod* mod, int tile_rows, int b0, bool out_bf16) {
   da::ScoreTerms t{};
   if (!mod) return t;
   t.on = 1;
@@ -229,6 +229,7 @@ da::ScoreTerms score_terms_of(const da_score_mod* mod, int tile_rows, int b0) {
   t.prefix = mod->prefix;
   t.doc_begin = mod->doc_begin ? mod->doc_begin + b0 : nullptr;
   t.slopes = mod->slopes;
+  t.short_tanh = out_bf16 && mod->softcap <= da::kShortTanhCap;
   t.cap_log2 = float(double(mod->softcap) * 1.4426950408889634);
   return t;
 }
@@ -280,6 +281,15 @@ bool single_split_suffices(long long units, int n_max, int chunk_min, int tile, 
   return best_c >= n_max;
 }
 
+// Block-scaled caches (see make_plan).  Rounds 2, 3, 4 and 6 of the grid: 37.3,
+// 34.7, 35.5 and 38.5 us on 16 ragged int8 sequences with 8 kv heads, 92.8, 88.7,
+// 87.9 and 88.4 us on 2 x 131072 rows of fp8.  One round of longer chunks where
+// a partial has 16 heads: 33.5 us on 8 x 30000 rows for 32 heads (compute-bound,
+// so a second, short round costs a whole one: 48.8 us in chunks of 1024 rows).
+constexpr long long kBlockRounds = 3;
+constexpr long long kBlockRowsPerHead = 96;
+constexpr long long kBlockMinRows = 128;
+
 // Splits per sequence requested by the caller -> a split length that is a
 // whole number of pipeline stages, as close as possible to n_max / S.  When
 // the library chooses, the device picks the length from the actual sequence
@@ -300,7 +310,8 @@ int make_plan(int B, int h_q, int h_kv, int d, int d_v, int n_max, int dtype_arg
                           : (dtype == DA_BF16 ? da::bf16_shape(d, d_v, group)
                                               : da::f32_shape(d, group));
   pl->head_chunks = (group + pl->ks.heads_per_cta - 1) / pl->ks.heads_per_cta;
-  pl->batch_per_launch = B < da::kMaxBatchPerLaunch ? B : da::kMaxBatchPerLaunch;
+  // (no work list, no limit on the batch of a launch, for block-scaled caches)
+  pl->batch_per_launch = block || B < da::kMaxBatchPerLaunch ? B : da::kMaxBatchPerLaunch;
   const long long tile = pl->ks.tile_rows;
   // A work list with score terms holds whole tiles of the rows that are seen:
   // less than a tile more at the prefix's end and at the window's start.
@@ -309,6 +320,32 @@ int make_plan(int B, int h_q, int h_kv, int d, int d_v, int n_max, int dtype_arg
   pl->balanced = false;
   pl->units = int((long long)pl->batch_per_launch * h_kv * pl->head_chunks);
   if (requested < -1) return DA_ERR_SHAPE;
+  if (block) {
+    // One CTA per chunk (decode_q8b.cu): the grid, not a work list, balances
+    // the SMs.  The library aims at kBlockRounds CTAs for every place on the GPU
+    // with all sequences at full length, but keeps chunks at kBlockRowsPerHead
+    // rows for each head of a partial (which costs 4 D bytes a head to write and
+    // merge against 2 D bytes a row read), unless they then leave places empty.
+    const long long places = (long long)sms * (long long)pl->ks.cta_speed;
+    const int heads = group < pl->ks.heads_per_cta ? group : pl->ks.heads_per_cta;
+    long long chunk;
+    if (requested > 0) {
+      chunk = (n_max + requested - 1) / requested;
+    } else {
+      chunk = (long long)pl->units * n_max / (kBlockRounds * places);
+      const long long per_unit = places / pl->units > 0 ? places / pl->units : 1;
+      const long long one_round = (n_max + per_unit - 1) / per_unit;
+      const long long by_heads = kBlockRowsPerHead * heads;
+      if (chunk < by_heads) chunk = by_heads < one_round ? by_heads : one_round;
+      if (chunk < kBlockMinRows) chunk = kBlockMinRows;
+      if (n_max <= 2 * kBlockMinRows) chunk = n_max;
+    }
+    chunk = (chunk + tile - 1) / tile * tile;
+    pl->chunk_fixed = pl->chunk_min = int(chunk);
+    pl->max_splits = int((n_max + chunk - 1) / chunk);
+    if ((long long)pl->units * pl->max_splits > 0x7fffffffLL) return DA_ERR_SHAPE;
+    return DA_OK;
+  }
   // Balanced pieces when the row stream fits an int and the partials of up
   // to one per SM per query head stay within 256 MiB.
   auto take_balanced = [&]() {
@@ -460,7 +497,7 @@ int run_decode(const void* q, const void* K, const void* V, const int32_t* seq_l
     p.out = static_cast<char*>(out) + size_t(b0) * h_q * d_v * out_es;
     p.out_bf16 = dta.out_bf16 ? 1 : 0;
     p.row_off = row_off;
-    p.mod = score_terms_of(mod, pl.ks.tile_rows, b0);
+    p.mod = score_terms_of(mod, pl.ks.tile_rows, b0, dta.out_bf16);
     p.row_lim = row_lim;
     p.lse_out = lse_out ? lse_out + size_t(b0) * h_q : nullptr;
     p.o_part = wl.total ? reinterpret_cast<float*>(ws + wl.o_part) : nullptr;
@@ -512,7 +549,8 @@ int run_decode(const void* q, const void* K, const void* V, const int32_t* seq_l
     // tag per CTA in the two halves of the work list's reduction scratch)
     const long long max_grid = da::kSchedRedWords / 2 - 1;
     const long long grid_cap = sms < max_grid ? sms : max_grid;
-    const int grid = int(items < grid_cap ? items : grid_cap);
+    // (a block-scaled cache: one CTA per item, not persistent)
+    const int grid = int(ba || items < grid_cap ? items : grid_cap);
     cudaError_t err =
         pl.tc5 ? da::launch_split_tc5(p, tk, tv, grid, stream)
         : ba   ? da::launch_split_q8b(p, tk, tv, d_k, dtype == DA_INT8 ? 1 : 2, grid, stream)

@@ -69,7 +69,8 @@ __device__ __forceinline__ int splits_of_head(const SplitParams& p, int bh, int 
   } else if (!appended) {
     n = max(0, min(n, p.row_lim) - p.row_off);
   }
-  const int chunk = *reinterpret_cast<const volatile int*>(p.chunk_out);
+  const int chunk = p.chunk_fixed > 0 ? p.chunk_fixed  // no need to ask the split grid
+                                      : *reinterpret_cast<const volatile int*>(p.chunk_out);
   int nv;
   if (chunk > 0) {  // chunked list: ceil(n / chunk) splits
     nv = n <= 0 ? 1 : (n + chunk - 1) / chunk;

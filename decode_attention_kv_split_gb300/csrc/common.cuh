@@ -30,6 +30,7 @@ struct ScoreTerms {
   int window, prefix;            // window 0: unlimited
   const int32_t* doc_begin;      // nullable: [B], this launch's slice
   const float* slopes;           // nullable: [h_q]
+  int short_tanh;                // tanh_short is exact enough for this call's output
   float cap_log2;                // softcap * log2 e (scale_log2 is then scale / softcap); 0: none
 };
 
@@ -307,7 +308,8 @@ struct KernelShape {
   int heads_per_cta;
   int box_cols;     // inner box width in elements
   int swizzle128;   // 1: 128-byte swizzle, 2: 64-byte swizzle, 0: none
-  float cta_speed;  // how fast one CTA streams relative to an even share of HBM (measured)
+  float cta_speed;  // how fast one CTA streams relative to an even share of HBM (measured);
+                    // q8b_shape: the CTAs that share an SM
 };
 
 KernelShape bf16_shape(int d_k, int d_v, int group);
@@ -570,6 +572,18 @@ __device__ __forceinline__ float tanh_fast(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
   const float large = copysignf((1.f - e) * r, x);
   return fabsf(x) < 0.5f ? small : large;
+}
+
+// tanh with an absolute error of about 2^-22: 1 - 2 / (1 + e^2x), 5 instructions.
+// A score capped at c is off by up to c 2^-22, its weight by that factor: for a
+// bf16 output and c <= kShortTanhCap that is at most 2^-15, far below the
+// output's own half step of 2^-9.
+constexpr float kShortTanhCap = 128.f;
+__device__ __forceinline__ float tanh_short(float x) {
+  const float e = ex2(2.f * 1.4426950408889634f * x);
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+  return fmaf(-2.f, r, 1.f);
 }
 
 // A log2-domain score with its distance bias.

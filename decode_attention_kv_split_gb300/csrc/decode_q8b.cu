@@ -13,27 +13,43 @@
 // query head, so a group of 8 stays at 16 flops per byte, far below the fp16
 // MMA rate per byte of HBM.
 //
-// Layout.  The code tiles arrive by TMA (128 rows, a row's D bytes contiguous
-// with the 128- or 64-byte swizzle) and MMA A fragments are built from them in
-// registers; no fp16 copy of a stage is written.  Eight consumer warps own 16
-// rows of a stage each; as S is a multiple of 16, a warp's rows of a stage
-// have ONE K scale and ONE V scale.  So scales are not staged: a warp loads
-// those of its next 32 stages with one load per tensor (a lane per stage), a
-// group ahead, and takes each by a shuffle.  With lane = 4 g + t:
+// Work.  A CTA of four warps takes one chunk of a (sequence, kv head, head
+// chunk)'s rows: its place in the grid names all three, so there is no work list
+// to build, and two to four CTAs share an SM, so that one's start and end
+// (loads of q, the merge of its warps) pass under the others' streams.  The
+// persistent form of this kernel (one CTA of eight warps a SM, every CTA
+// building the list) took 40.8 us on 16 ragged int8 sequences with 8 kv heads.
+// Within a CTA warp w takes the 32-row steps w, w + 4, ... of the chunk and
+// feeds itself: its lane 0 keeps a ring of steps (K and V codes, 2 TMA boxes of
+// 32 rows) in flight on the warp's own barriers, and no warp waits for another
+// before the chunk's end.  A step holds two 16-row MMA blocks, so that the
+// barrier, the maximum's shuffles and the rescaling come once for both and two
+// independent chains fill each other's latencies (with one block a step the
+// kernel issued 375 instructions a block and took 4 % longer on long fp8 caches).
+//
+// Layout.  The boxes have a row's D bytes contiguous with the 128- or 64-byte
+// swizzle; MMA A fragments are built from them in registers, no fp16 copy is
+// written.  As S is a multiple of 16, a block of rows has ONE K scale and ONE V
+// scale: a warp loads those of its next 32 blocks (16 steps) with one load per
+// tensor (a lane per block), a group ahead, and takes each by a shuffle.
+// With lane = 4 g + t:
 //   Step I  (S^T = K . Q^T, rows of K as M): lane (g, t) reads bytes
-//           [t D/4, (t + 1) D/4) of rows g and g + 8 of the warp's block; k-block
-//           kb takes the 4 codes at t D/4 + 4 kb as the A elements at logical
+//           [t D/4, (t + 1) D/4) of rows g and g + 8 of the block; k-block kb
+//           takes the 4 codes at t D/4 + 4 kb as the A elements at logical
 //           columns 2t, 2t+1, 2t+8, 2t+9.  That relabels the columns of d one to
 //           one, and the q fragments are taken in the same order.
 //   Step III (O^T += V^T . P^T, d as M): lane (g, t) reads bytes
 //           [g D/8, (g + 1) D/8) of rows 2t, 2t+1, 2t+8, 2t+9; a byte permute
 //           pairs a column's codes of two rows; m-block mb takes columns
 //           g D/8 + 2 mb and + 1.
-// The V scale multiplies P before P becomes fp16 (head + remainder, ~22 bits).
+// The V scale multiplies P before P becomes fp16.  For a float32 output P is an
+// fp16 head and an fp16 remainder (~22 bits, two MMAs).  For a bf16 output it is
+// the head alone: 2^-12 of each weight, an eighth of the half step (2^-9) by which
+// the output's own rounding moves it, and a third of the MMAs less.
 // Scales may be of any size (2^-126 for tiny rows), and fp16 has few exponents,
 // so a warp keeps its accumulator in units of the largest V scale it has seen:
 // P is multiplied by vs / unit <= 1, the accumulator is rescaled when the unit
-// grows (as by a running maximum), and the unit returns at the item's end.
+// grows (as by a running maximum), and the unit returns at the chunk's end.
 #include <math.h>
 
 #include "common.cuh"
@@ -41,34 +57,34 @@
 
 namespace da {
 
-template <int D_, int NB_, int STAGES_, int KIND_>
+template <int D_, int NB_, int STAGES_, int CTAS_, int KIND_>
 struct Q8BCfg {
   static constexpr int D = D_;
-  static constexpr int NB = NB_;           // 8-head MMA blocks per item
-  static constexpr int KW = 8;             // consumer warps, one 16-row block each
-  static constexpr int STAGES = STAGES_;
+  static constexpr int NB = NB_;           // 8-head MMA blocks per CTA
+  static constexpr int KW = 4;             // warps
+  static constexpr int STAGES = STAGES_;   // steps in flight per warp
+  static constexpr int ROWS = 32;          // rows of a step: two MMA blocks
+  static constexpr int CTAS = CTAS_;       // CTAs per SM
   static constexpr int KIND = KIND_;       // 1: int8 codes, 2: fp8 e4m3 codes
   static constexpr int kHPW = 8 * NB;
-  static constexpr int kTile = 16 * KW;
-  static constexpr int kConsumerThreads = 32 * KW;
-  static constexpr int kThreads = kConsumerThreads + 32;
-  static constexpr int kCodeBytes = kTile * D;
-  static constexpr int kStageBytes = 2 * kCodeBytes;
-  static constexpr int kQBytes = kHPW * D * 2;
+  static constexpr int kThreads = 32 * KW;
+  static constexpr int kCodeBytes = ROWS * D;           // a step's codes of one tensor
+  static constexpr int kStepBytes = 2 * kCodeBytes;
+  static constexpr int kRingBytes = KW * STAGES * kStepBytes;
   static constexpr int kSlotStride = D + 4;
   static constexpr int kEpiAccFloats = KW * kHPW * kSlotStride;
   static constexpr int kEpiMLFloats = 2 * KW * kHPW;
-  static constexpr int kSchedWords = da::kSchedWords;
-  static constexpr size_t kSmemBytes = 1024 + size_t(STAGES) * (kStageBytes + kQBytes) +
-                                       size_t(kEpiAccFloats + kEpiMLFloats + kSchedWords) * 4 +
-                                       2 * STAGES * 8 + 16;
+  // the merge of the warps reuses the ring
+  static constexpr int kEpiBytes = (kEpiAccFloats + kEpiMLFloats) * 4;
+  static constexpr int kDataBytes = kRingBytes > kEpiBytes ? kRingBytes : kEpiBytes;
+  static constexpr size_t kSmemBytes = 1024 + kDataBytes + KW * STAGES * 8 + 16;
   static_assert(D == 64 || D == 128, "head dim");
   static_assert(KIND == 1 || KIND == 2, "code type");
-  static_assert(kSmemBytes <= 227 * 1024, "shared memory");
-  static_assert((kEpiAccFloats + kEpiMLFloats) % 2 == 0, "mbarrier alignment");
+  static_assert(CTAS * (kSmemBytes + 1024) <= 228 * 1024, "shared memory");
+  static_assert(kDataBytes % 8 == 0, "mbarrier alignment");
 };
 
-// Byte offset of 16-byte piece `piece` of row `row` of a code tile: the 128-byte
+// Byte offset of 16-byte piece `piece` of row `row` of a box: the 128-byte
 // swizzle for 128-byte rows, the 64-byte swizzle for 64-byte rows.
 template <int D>
 __device__ __forceinline__ int code_at(int row, int piece) {
@@ -76,347 +92,362 @@ __device__ __forceinline__ int code_at(int row, int piece) {
                   : row * 64 + ((piece ^ ((row >> 1) & 3)) << 4);
 }
 
-// Producer: one thread streams the K and V code tiles of every stage of the
-// CTA's items, and each item's bf16 q rows with its first stage.
 template <class Cfg, bool MOD>
-__device__ __forceinline__ void produce_q8b(const CUtensorMap* tmK, const CUtensorMap* tmV,
-                                            const SplitParams& p, const Schedule& s, uint32_t ring,
-                                            uint32_t qslots, uint32_t full0, uint32_t empty0,
-                                            volatile int* abort_flag) {
-  constexpr int T = Cfg::kTile, STAGES = Cfg::STAGES, D = Cfg::D;
-  const uint64_t policy = l2_policy_evict_first();
-  int stage = 0;
-  uint32_t phase = 0, issued = 0, issued_parity = 0;
-  bool aborted = false;
-  for (int k = 0; k < s.mine && !aborted; ++k) {
-    const ItemT<MOD> it = cta_item<T, MOD>(p, s, k);
-    const int z = (p.b_offset + it.b) * p.h_kv + it.kvh;
-    for (int t = 0; t < it.tiles; ++t) {
-      if (!mbar_wait_bounded(empty0 + 8 * stage, phase ^ 1u, abort_flag)) {
-        *abort_flag = 1;
-        flag_error(p.dev_error, DA_DEVERR_TIMEOUT);
-        aborted = true;
-        break;
-      }
-      if (test_withhold(p, k, t, it.tiles)) {  // test builds only: never filled
-        if (++stage == STAGES) {
-          stage = 0;
-          phase ^= 1u;
-        }
-        continue;
-      }
-      const uint32_t bar = full0 + 8 * stage;
-      const int h0 = it.hc * Cfg::kHPW;
-      const int nh = min(Cfg::kHPW, p.group - h0);
-      const size_t bhq = size_t(it.b) * p.h_q + size_t(it.kvh) * p.group + h0;
-      const bool load_q = t == 0 && DA_IN(p, bhq + nh - 1, size_t(p.B) * p.h_q);
-      mbar_arrive_expect_tx(bar, Cfg::kStageBytes + (load_q ? uint32_t(nh) * (D * 2) : 0u));
-      if (load_q)
-        bulk_load(qslots + stage * Cfg::kQBytes, static_cast<const char*>(p.q) + bhq * (D * 2),
-                  uint32_t(nh) * (D * 2), bar);
-      const uint32_t dst = ring + stage * Cfg::kStageBytes;
-      const int y = cache_row(it, it.row_begin + t * T);
-      tma_load_3d(dst, tmK, 0, y, z, bar, policy);
-      tma_load_3d(dst + Cfg::kCodeBytes, tmV, 0, y, z, bar, policy);
-      issued |= 1u << stage;
-      issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
-      if (++stage == STAGES) {
-        stage = 0;
-        phase ^= 1u;
-      }
-    }
-  }
-  if (aborted) {  // every copy this thread started lands before the CTA can exit
-    volatile int never = 0;
-    for (int st = 0; st < STAGES; ++st)
-      if (issued & (1u << st)) mbar_wait_bounded(full0 + 8 * st, (issued_parity >> st) & 1u, &never);
-  }
-}
-
-template <class Cfg, bool MOD>
-__global__ void __launch_bounds__(Cfg::kThreads, 1)
+__global__ void __launch_bounds__(Cfg::kThreads, Cfg::CTAS)
     split_decode_q8b_kernel(const __grid_constant__ CUtensorMap tmK,
                             const __grid_constant__ CUtensorMap tmV, const SplitParams p) {
-  constexpr int D = Cfg::D, NB = Cfg::NB, KW = Cfg::KW, STAGES = Cfg::STAGES, T = Cfg::kTile;
+  constexpr int D = Cfg::D, NB = Cfg::NB, KW = Cfg::KW, STAGES = Cfg::STAGES, ROWS = Cfg::ROWS;
   constexpr int kHPW = Cfg::kHPW;
   constexpr int MB = D / 16;        // 16-wide blocks of d (Step III m-blocks; Step I k-blocks)
   constexpr int KV4 = D / 16 / 4;   // 16-byte pieces a lane reads of a K row
   constexpr int VW = D / 32;        // 4-byte words a lane reads of a V row
   constexpr int KIND = Cfg::KIND;
+  constexpr float kLazy = 8.f;      // log2 of how far a weight may exceed 1
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
-  uint8_t* qslots = smem + size_t(STAGES) * Cfg::kStageBytes;
-  float* epi_acc = reinterpret_cast<float*>(qslots + size_t(STAGES) * Cfg::kQBytes);
+  float* epi_acc = reinterpret_cast<float*>(smem);
   float* epi_m = epi_acc + Cfg::kEpiAccFloats;
   float* epi_l = epi_m + KW * kHPW;
-  int* sched_words = reinterpret_cast<int*>(epi_l + KW * kHPW);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sched_words + Cfg::kSchedWords);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 2 * STAGES);
-  const uint32_t ring = smem_u32(smem);
-  const uint32_t full0 = smem_u32(bars);
-  const uint32_t empty0 = full0 + 8 * STAGES;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Cfg::kDataBytes);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + KW * STAGES);
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
+  const uint32_t full0 = smem_u32(bars) + 8 * STAGES * warp;
+  const uint8_t* ring = smem + warp * (STAGES * Cfg::kStepBytes);
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < STAGES; ++s) {
-      mbar_init(full0 + 8 * s, 1);
-      mbar_init(empty0 + 8 * s, KW);
-    }
+    for (int s = 0; s < KW * STAGES; ++s) mbar_init(smem_u32(bars) + 8 * s, 1);
     *abort_flag = 0;
     fence_mbar_init();
-  }
-  if (threadIdx.x == 32) {  // the tensor maps do not depend on the preceding grid
     prefetch_tmap(&tmK);
     prefetch_tmap(&tmV);
   }
-  if (threadIdx.x == Cfg::kConsumerThreads)  // producer lane: L2 prefetch of the hinted tiles
-    prefetch_hinted<T, 1, 1, D>(p, load_hint(p), &tmK, &tmV, STAGES);
-  // Launched as a programmatic dependent: before the wait only the hinted L2
-  // prefetch and the work list touch what the previous grid may write (the
-  // list is checked, and built again if a length changed, after the wait).
-  Schedule sched = build_schedule_core<T, MOD>(p, sched_words);
-  wait_for_prerequisite_grid();
-  sched = commit_schedule<T, MOD>(p, sched_words, sched);
-  allow_dependent_launch();
-  if (threadIdx.x == 0 && sched.mine > 0)
-    write_hint<T, MOD>(p, cta_item<T, MOD>(p, sched, 0), STAGES);
-
-  // ------------------------------------------------------------------ producer
-  if (warp == KW) {
-    if (lane == 0)
-      produce_q8b<Cfg, MOD>(&tmK, &tmV, p, sched, ring, smem_u32(qslots), full0, empty0,
-                            abort_flag);
-    return;
+  // the CTA's place: head chunk, split, kv head, sequence (fastest first)
+  Item where;
+  {
+    unsigned i = blockIdx.x;
+    const unsigned hcs = unsigned(p.head_chunks), sp = unsigned(p.max_splits);
+    where.hc = int(i % hcs);
+    i /= hcs;
+    where.split = int(i % sp);
+    i /= sp;
+    where.kvh = int(i % unsigned(p.h_kv));
+    where.b = int(i / unsigned(p.h_kv));
   }
+  wait_for_prerequisite_grid();
+  allow_dependent_launch();
+  ItemT<MOD> it;
+  static_cast<Item&>(it) = where;
+  bool bad = false, bad_pos = false;
+  int n_out;
+  const int begin = MOD ? doc_begin(p.mod, it.b) : 0;
+  const int n_in = __ldcg(p.seq_lens + it.b);
+  const int n = list_len<ROWS, MOD>(p, begin, n_in, bad, bad_pos, n_out);
+  if constexpr (MOD) list_rows(p.mod, ROWS, begin, n_out, false, it.rows);
+  if (bad && it.split == 0 && it.kvh == 0 && it.hc == 0 && threadIdx.x == 0)
+    flag_error(p.dev_error, DA_DEVERR_SEQ_LEN);
+  it.nv = n <= 0 ? 1 : (n - 1) / p.chunk_fixed + 1;
+  if (it.split >= it.nv) return;
+  it.row_begin = it.split * p.chunk_fixed;
+  it.row_end = min(n, it.row_begin + p.chunk_fixed);
+  it.new_row = -1;
+  const int steps = (it.row_end - it.row_begin + ROWS - 1) / ROWS;
+  it.tiles = steps > warp ? (steps - warp + KW - 1) / KW : 0;  // this warp's
+  __syncthreads();  // barriers initialised
 
-  // ------------------------------------------------------------------ consumers
+  // First list row of this warp's i-th step.
+  auto step_row = [&](int i) { return it.row_begin + (i * KW + warp) * ROWS; };
+  const int z = (p.b_offset + it.b) * p.h_kv + it.kvh;
+  // Lane 0: load step i into a slot.
+  const uint64_t policy = l2_policy_evict_first();
+  auto load_step = [&](int i, int slot) {
+    if (test_withhold(p, 0, i, it.tiles)) return;  // test builds only: never filled
+    const uint32_t bar = full0 + 8 * slot, dst = smem_u32(ring) + slot * Cfg::kStepBytes;
+    const int y = cache_row(it, step_row(i));
+    mbar_arrive_expect_tx(bar, Cfg::kStepBytes);
+    tma_load_3d(dst, &tmK, 0, y, z, bar, policy);
+    tma_load_3d(dst + Cfg::kCodeBytes, &tmV, 0, y, z, bar, policy);
+  };
+  if (lane == 0)
+    for (int i = 0; i < STAGES && i < it.tiles; ++i) load_step(i, i);
+
   const int g = lane >> 2;   // MMA fragment row group
   const int t = lane & 3;    // MMA fragment column pair
-  const int key0 = warp * 16;  // first row of this warp's block inside a stage
-  const int rA = key0 + g, rB = rA + 8;             // Step I rows (and P rows)
-  const int r0 = key0 + 2 * t, r1 = r0 + 1, r2 = r0 + 8, r3 = r0 + 9;  // Step III rows
-  int stage = 0;
+  const int head_base = it.hc * kHPW;
+  // This warp's K and V scales of the two blocks of steps first .. first + 15
+  // (lane 2 k + u: block u of step first + k), loaded a group ahead.
+  auto load_scales = [&](int first, float& sk, float& sv) {
+    const int v = step_row(first + (lane >> 1)) + (lane & 1) * 16;
+    sk = sv = 0.f;
+    if (v < it.row_end) {
+      const int blk = cache_row(it, v) >> p.blk_shift;
+      const size_t at = size_t(z) * size_t(p.nblk) + size_t(blk);
+      if (DA_IN(p, blk, p.nblk) && DA_IN(p, at, p.scale_elems)) {
+        sk = __ldcg(p.k_scale + at);
+        sv = __ldcg(p.v_scale + at);
+      }
+    }
+  };
+  float sk_now = 0.f, sv_now = 0.f, sk_next, sv_next;
+  load_scales(0, sk_next, sv_next);
+
+  // q as B fragments in the permuted column order (heads past the group are
+  // zero): lane (g, t) takes columns [t D/4, (t + 1) D/4) of head 8 nb + g.
+  uint32_t qf[MB][NB][2];
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb) {
+    const int hl = head_base + nb * 8 + g;
+    const size_t bhq = size_t(it.b) * p.h_q + size_t(it.kvh) * p.group + hl;
+    const bool ok = hl < p.group && DA_IN(p, bhq, size_t(p.B) * p.h_q);
+    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const char*>(p.q) +
+                                                      bhq * (D * 2) + t * (D / 2));
+#pragma unroll
+    for (int u = 0; u < MB / 2; ++u) {
+      const uint4 w = ok ? __ldg(src + u) : make_uint4(0, 0, 0, 0);
+      qf[2 * u][nb][0] = q8::pack_f16x2(bf16_lo_to_f32(w.x), bf16_hi_to_f32(w.x));
+      qf[2 * u][nb][1] = q8::pack_f16x2(bf16_lo_to_f32(w.y), bf16_hi_to_f32(w.y));
+      qf[2 * u + 1][nb][0] = q8::pack_f16x2(bf16_lo_to_f32(w.z), bf16_hi_to_f32(w.z));
+      qf[2 * u + 1][nb][1] = q8::pack_f16x2(bf16_lo_to_f32(w.w), bf16_hi_to_f32(w.w));
+    }
+  }
+  [[maybe_unused]] float slope[NB][2];
+  if constexpr (MOD) {
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int hl = head_base + nb * 8 + 2 * t + j;
+        slope[nb][j] = head_slope(p, it.kvh * p.group + hl, hl < p.group);
+      }
+  }
+
+  float m_run[NB][2], l_run[NB][2];
+  float acc[MB][NB][4];
+  float unit = 0.f;        // the accumulator's unit: the largest |V scale| so far
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb) {
+    m_run[nb][0] = m_run[nb][1] = -INFINITY;
+    l_run[nb][0] = l_run[nb][1] = 0.f;
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[mb][nb][e] = 0.f;
+  }
+
+  const bool exact_p = p.out_bf16 == 0;  // P's fp16 remainder too
+  int slot = 0;
   uint32_t phase = 0;
-
-  for (int k = 0; k < sched.mine; ++k) {
-    const ItemT<MOD> it = cta_item<T, MOD>(p, sched, k);
-    const int head_base = it.hc * kHPW;
-    const size_t kvhead = size_t(p.b_offset + it.b) * p.h_kv + it.kvh;
-    // This warp's K and V scales of stages 32 i + lane, loaded a group ahead.
-    auto load_scales = [&](int first, float& sk, float& sv) {
-      const int v = it.row_begin + (first + lane) * T + key0;
-      sk = sv = 0.f;
-      if (v < it.row_end) {
-        const int blk = cache_row(it, v) >> p.blk_shift;
-        const size_t at = kvhead * size_t(p.nblk) + size_t(blk);
-        if (DA_IN(p, blk, p.nblk) && DA_IN(p, at, p.scale_elems)) {
-          sk = __ldcg(p.k_scale + at);
-          sv = __ldcg(p.v_scale + at);
-        }
-      }
-    };
-    float sk_now, sv_now, sk_next, sv_next;
-    load_scales(0, sk_next, sv_next);
-    sk_now = sk_next, sv_now = sv_next;
-
-    [[maybe_unused]] float slope[NB][2];
-    if constexpr (MOD) {
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int hl = head_base + nb * 8 + 2 * t + j;
-          slope[nb][j] = head_slope(p, it.kvh * p.group + hl, hl < p.group);
-        }
+  for (int i = 0; i < it.tiles; ++i) {
+    if ((i & 15) == 0) {
+      sk_now = sk_next, sv_now = sv_next;
+      load_scales(i + 16, sk_next, sv_next);
     }
-    uint32_t qf[MB][NB][2];  // B fragments of q, in the permuted column order
-    float m_run[NB][2], l_run[NB][2];
-    float acc[MB][NB][4];
-    float unit = 0.f;        // the accumulator's unit: the largest |V scale| so far
-#pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-      m_run[nb][0] = m_run[nb][1] = -INFINITY;
-      l_run[nb][0] = l_run[nb][1] = 0.f;
-#pragma unroll
-      for (int mb = 0; mb < MB; ++mb)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[mb][nb][e] = 0.f;
+    // warp-uniform (the MMAs and shuffles below need the whole warp)
+    const bool ok = mbar_wait_bounded(full0 + 8 * slot, phase, abort_flag);
+    if (!__all_sync(0xffffffffu, ok)) {
+      if (lane == 0 && !*abort_flag) flag_error(p.dev_error, DA_DEVERR_TIMEOUT);
+      *abort_flag = 1;
+      // this warp's copies in flight (steps i .. i + STAGES - 1) land before the CTA can exit
+      volatile int never = 0;
+      for (int k = i; k < i + STAGES && k < it.tiles; ++k)
+        if (!test_withhold(p, 0, k, it.tiles))
+          mbar_wait_bounded(full0 + 8 * (k % STAGES), (k / STAGES) & 1, &never);
+      break;
     }
+    const uint8_t* ktile = ring + slot * Cfg::kStepBytes;
+    const uint8_t* vtile = ktile + Cfg::kCodeBytes;
+    const int v0 = step_row(i);
+    const TileMask<MOD> mask(it, v0, min(ROWS, it.row_end - v0));
+    const bool all = mask.all_seen(0, ROWS);
 
-    for (int tt = 0; tt < it.tiles; ++tt) {
-      if ((tt & 31) == 0) {
-        sk_now = sk_next, sv_now = sv_next;
-        load_scales(tt + 32, sk_next, sv_next);
-      }
-      if (!mbar_wait_bounded(full0 + 8 * stage, phase, abort_flag)) {
-        if (!*abort_flag) {
-          *abort_flag = 1;
-          flag_error(p.dev_error, DA_DEVERR_TIMEOUT);
-        }
-      }
-      const uint8_t* ktile = smem + size_t(stage) * Cfg::kStageBytes;
-      const uint8_t* vtile = ktile + Cfg::kCodeBytes;
-      const int tile_row0 = it.row_begin + tt * T;
-      const int valid = min(T, it.row_end - tile_row0);
-      const TileMask<MOD> mask(it, tile_row0, valid);
-
-      // ---- this lane's codes, into registers
-      uint4 kA[KV4], kB[KV4];
-      uint32_t v[4][VW];
+    if (all || mask.any_seen(0, ROWS)) {
+      float ks[2], vs[2];
 #pragma unroll
-      for (int u = 0; u < KV4; ++u) {
-        kA[u] = *reinterpret_cast<const uint4*>(ktile + code_at<D>(rA, t * KV4 + u));
-        kB[u] = *reinterpret_cast<const uint4*>(ktile + code_at<D>(rB, t * KV4 + u));
+      for (int u = 0; u < 2; ++u) {
+        ks[u] = __shfl_sync(0xffffffffu, sk_now, 2 * (i & 15) + u) * p.scale_log2;
+        vs[u] = __shfl_sync(0xffffffffu, sv_now, 2 * (i & 15) + u);
+        // (a block without a seen row may have any scale)
+        if (!all && !mask.any_seen(u * 16, 16)) ks[u] = vs[u] = 0.f;
       }
-      const int vr[4] = {r0, r1, r2, r3};
+      // ---- Step I
+      float s[2][NB][4];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        if constexpr (D == 128) {
-          const uint4 w = *reinterpret_cast<const uint4*>(vtile + code_at<D>(vr[u], g));
-          v[u][0] = w.x, v[u][1] = w.y, v[u][2] = w.z, v[u][3] = w.w;
-        } else {
-          const uint2 w =
-              *reinterpret_cast<const uint2*>(vtile + code_at<D>(vr[u], g >> 1) + (g & 1) * 8);
-          v[u][0] = w.x, v[u][1] = w.y;
-        }
-        // rows past the end or not seen may hold anything: their values must not reach O
-        if (!mask.seen(vr[u])) {
-#pragma unroll
-          for (int w = 0; w < VW; ++w) v[u][w] = 0;
-        }
-      }
-      if (tt == 0) {  // q of head 8 nb + g (rows past the group are zero), bf16 -> fp16
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-          const bool ok = head_base + nb * 8 + g < p.group;
-          const uint8_t* qs = qslots + size_t(stage) * Cfg::kQBytes + (nb * 8 + g) * (D * 2) +
-                              t * (D / 2);
-#pragma unroll
-          for (int kb = 0; kb < MB; ++kb) {
-            uint2 w = *reinterpret_cast<const uint2*>(qs + kb * 8);
-            if (!ok) w = make_uint2(0, 0);
-            qf[kb][nb][0] = q8::pack_f16x2(bf16_lo_to_f32(w.x), bf16_hi_to_f32(w.x));
-            qf[kb][nb][1] = q8::pack_f16x2(bf16_lo_to_f32(w.y), bf16_hi_to_f32(w.y));
-          }
-        }
-      }
-      const float ks = __shfl_sync(0xffffffffu, sk_now, tt & 31) * p.scale_log2;
-      const float vs = __shfl_sync(0xffffffffu, sv_now, tt & 31);
-      __syncwarp();
-      // every byte this warp needs from the stage is in registers now
-      if (lane == 0) mbar_arrive(empty0 + 8 * stage);
-      if (++stage == STAGES) {
-        stage = 0;
-        phase ^= 1u;
-      }
-
-      // warp-uniform (the MMAs and shuffles below need the whole warp)
-      const bool live = __all_sync(0xffffffffu, !*abort_flag);
-      if (live && mask.any_seen(key0, 16)) {
-        // ---- Step I
-        float s[NB][4];
+      for (int u = 0; u < 2; ++u) {
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[nb][e] = 0.f;
-        float s2[4] = {0.f, 0.f, 0.f, 0.f};  // one head block: two independent chains
+          for (int e = 0; e < 4; ++e) s[u][nb][e] = 0.f;
+        uint4 kA[KV4], kB[KV4];
+#pragma unroll
+        for (int w = 0; w < KV4; ++w) {
+          kA[w] = *reinterpret_cast<const uint4*>(ktile + code_at<D>(u * 16 + g, t * KV4 + w));
+          kB[w] = *reinterpret_cast<const uint4*>(ktile + code_at<D>(u * 16 + g + 8, t * KV4 + w));
+        }
 #pragma unroll
         for (int kb = 0; kb < MB; ++kb) {
           uint32_t a[4];
           q8::codes_to_f16<KIND>(word_of(kA[kb >> 2], kb & 3), a[0], a[2]);
           q8::codes_to_f16<KIND>(word_of(kB[kb >> 2], kb & 3), a[1], a[3]);
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb) {
-            if (NB == 1 && (kb & 1)) q8::mma_f16_16816(s2, a, qf[kb][nb][0], qf[kb][nb][1]);
-            else q8::mma_f16_16816(s[nb], a, qf[kb][nb][0], qf[kb][nb][1]);
-          }
+          for (int nb = 0; nb < NB; ++nb)
+            q8::mma_f16_16816(s[u][nb], a, qf[kb][nb][0], qf[kb][nb][1]);
         }
-        if (NB == 1) {
+      }
+      // ---- Step II: scale, terms, mask, running max and sum
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[0][e] += s2[e];
-        }
-        // ---- Step II: scale, terms, mask, running max and sum
+      for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[nb][e] *= ks;
-        if constexpr (MOD) {  // one branch for all of a lane's scores
-          if (p.mod.cap_log2 > 0.f) {
+          for (int e = 0; e < 4; ++e) s[u][nb][e] *= ks[u];
+      if constexpr (MOD) {  // one branch for all of a lane's scores
+        if (p.mod.cap_log2 > 0.f) {
+          if (p.mod.short_tanh) {
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
+            for (int u = 0; u < 2; ++u)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) s[nb][e] = p.mod.cap_log2 * tanh_fast(s[nb][e]);
+              for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  s[u][nb][e] = p.mod.cap_log2 * tanh_short(s[u][nb][e]);
+          } else {
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  s[u][nb][e] = p.mod.cap_log2 * tanh_fast(s[u][nb][e]);
           }
-          if (p.mod.slopes) {
-            const RowDistance dist(it, mask.row0 + rA);
+        }
+        if (p.mod.slopes) {
+          const RowDistance dist(it, mask.row0 + g);
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
               for (int e = 0; e < 4; ++e)
-                s[nb][e] = biased(s[nb][e], RowDistance(dist, (e >> 1) * 8), slope[nb][e & 1]);
-          }
+                s[u][nb][e] = biased(s[u][nb][e], RowDistance(dist, u * 16 + (e >> 1) * 8),
+                                     slope[nb][e & 1]);
         }
-        const bool seenA = mask.seen(rA), seenB = mask.seen(rB);
-        float alpha[NB][2];
-        bool changed = false;
+      }
+      if (!all) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const bool seenA = mask.seen(u * 16 + g), seenB = mask.seen(u * 16 + g + 8);
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              s[u][nb][e] = (e < 2 ? seenA : seenB) ? s[u][nb][e] : -INFINITY;
+        }
+      }
+      // The maximum is kept lazily: only where some score is more than 2^kLazy
+      // above it does a vote bring the exact one (three shuffles a head) and the
+      // rescaling.  Every weight and sum is taken against the maximum as it
+      // stands; weights reach 2^kLazy, well inside fp16.
+      bool over = false;
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float mx =
+              fmaxf(fmaxf(s[0][nb][j], s[0][nb][j + 2]), fmaxf(s[1][nb][j], s[1][nb][j + 2]));
+          over |= mx > m_run[nb][j] + kLazy;
+        }
+      // the V scales in units of the accumulator (the same on every lane)
+      const float avs = fmaxf(fabsf(vs[0]), fabsf(vs[1]));
+      if (__any_sync(0xffffffffu, over || avs > unit)) {
+        float f = 1.f;
+        if (avs > unit) {
+          f = __fdiv_rn(unit, avs);
+          unit = avs;
+        }
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const float xA = seenA ? s[nb][j] : -INFINITY;
-            const float xB = seenB ? s[nb][j + 2] : -INFINITY;
-            float mx = fmaxf(xA, xB);
+            float mx =
+                fmaxf(fmaxf(s[0][nb][j], s[0][nb][j + 2]), fmaxf(s[1][nb][j], s[1][nb][j + 2]));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
             const float m_new = fmaxf(m_run[nb][j], mx);
-            const float m_use = (m_new == -INFINITY) ? 0.f : m_new;
-            alpha[nb][j] = ex2(m_run[nb][j] - m_use);
-            changed |= (m_new != m_run[nb][j]);
+            const float alpha = ex2(m_run[nb][j] - (m_new == -INFINITY ? 0.f : m_new));
             m_run[nb][j] = m_new;
-            s[nb][j] = ex2(xA - m_use);
-            s[nb][j + 2] = ex2(xB - m_use);
-            l_run[nb][j] = l_run[nb][j] * alpha[nb][j] + (s[nb][j] + s[nb][j + 2]);
-          }
-        // the V scale in units of the accumulator (the same on every lane)
-        float w = 1.f;
-        const float avs = fabsf(vs);
-        if (avs > unit) {
-          const float f = __fdiv_rn(unit, avs);
-          unit = avs;
-          changed = true;
+            l_run[nb][j] *= alpha;
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb) alpha[nb][0] *= f, alpha[nb][1] *= f;
-        }
-        if (vs != unit) w = unit > 0.f ? __fdiv_rn(vs, unit) : 0.f;
-        if (__any_sync(0xffffffffu, changed)) {
-#pragma unroll
-          for (int mb = 0; mb < MB; ++mb)
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb) {
-              acc[mb][nb][0] *= alpha[nb][0];
-              acc[mb][nb][1] *= alpha[nb][1];
-              acc[mb][nb][2] *= alpha[nb][0];
-              acc[mb][nb][3] *= alpha[nb][1];
+            for (int mb = 0; mb < MB; ++mb) {
+              acc[mb][nb][j] *= alpha * f;
+              acc[mb][nb][j + 2] *= alpha * f;
             }
+          }
+      }
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float m_use = m_run[nb][j] == -INFINITY ? 0.f : m_run[nb][j];
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            s[u][nb][j] = ex2(s[u][nb][j] - m_use);
+            s[u][nb][j + 2] = ex2(s[u][nb][j + 2] - m_use);
+            l_run[nb][j] += s[u][nb][j] + s[u][nb][j + 2];
+          }
         }
-        // ---- Step III: O^T += V^T . (P * w)^T, P as fp16 head + fp16 remainder
+      if (vs[0] != unit || vs[1] != unit) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const float w = unit > 0.f ? __fdiv_rn(vs[u], unit) : 0.f;
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[u][nb][e] *= w;
+        }
+      }
+      // ---- Step III: O^T += V^T . P^T
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
         uint32_t ph[NB][2], pl[NB][2];
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
-          const float p0 = s[nb][0] * w, p1 = s[nb][1] * w, p2 = s[nb][2] * w, p3 = s[nb][3] * w;
-          const uint32_t h0 = q8::pack_f16x2(p0, p1);  // row g
-          const uint32_t h1 = q8::pack_f16x2(p2, p3);  // row g + 8
-          const uint32_t l0 = q8::pack_f16x2(p0 - q8::f16_lo(h0), p1 - q8::f16_hi(h0));
-          const uint32_t l1 = q8::pack_f16x2(p2 - q8::f16_lo(h1), p3 - q8::f16_hi(h1));
+          const float* x = s[u][nb];
+          const uint32_t h0 = q8::pack_f16x2(x[0], x[1]);  // row g
+          const uint32_t h1 = q8::pack_f16x2(x[2], x[3]);  // row g + 8
           ph[nb][0] = movmatrix_trans(h0);
           ph[nb][1] = movmatrix_trans(h1);
-          pl[nb][0] = movmatrix_trans(l0);
-          pl[nb][1] = movmatrix_trans(l1);
+          if (exact_p) {
+            pl[nb][0] = movmatrix_trans(
+                q8::pack_f16x2(x[0] - q8::f16_lo(h0), x[1] - q8::f16_hi(h0)));
+            pl[nb][1] = movmatrix_trans(
+                q8::pack_f16x2(x[2] - q8::f16_lo(h1), x[3] - q8::f16_hi(h1)));
+          }
+        }
+        uint32_t v[4][VW];
+        const int vr[4] = {u * 16 + 2 * t, u * 16 + 2 * t + 1, u * 16 + 2 * t + 8,
+                           u * 16 + 2 * t + 9};
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          if constexpr (D == 128) {
+            const uint4 w = *reinterpret_cast<const uint4*>(vtile + code_at<D>(vr[r], g));
+            v[r][0] = w.x, v[r][1] = w.y, v[r][2] = w.z, v[r][3] = w.w;
+          } else {
+            const uint2 w =
+                *reinterpret_cast<const uint2*>(vtile + code_at<D>(vr[r], g >> 1) + (g & 1) * 8);
+            v[r][0] = w.x, v[r][1] = w.y;
+          }
+        }
+        if (!all) {  // rows past the end or not seen may hold anything: nothing of them reaches O
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (!mask.seen(vr[r])) {
+#pragma unroll
+              for (int w = 0; w < VW; ++w) v[r][w] = 0;
+            }
         }
 #pragma unroll
         for (int mb = 0; mb < MB; ++mb) {
@@ -429,68 +460,76 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb) {
             q8::mma_f16_16816(acc[mb][nb], a, ph[nb][0], ph[nb][1]);
-            q8::mma_f16_16816(acc[mb][nb], a, pl[nb][0], pl[nb][1]);
+            if (exact_p) q8::mma_f16_16816(acc[mb][nb], a, pl[nb][0], pl[nb][1]);
           }
         }
       }
     }
+    // every lane's reads of the slot have been used: it may be refilled
+    __syncwarp();
+    if (lane == 0 && i + STAGES < it.tiles) load_step(i + STAGES, slot);
+    if (++slot == STAGES) {
+      slot = 0;
+      phase ^= 1u;
+    }
+  }
 
-    // ---- Epilogue: per-warp state to shared slots, then the shared finish.
+  // ---- the warps' states to shared slots (over the rings), then the shared finish
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      float x = l_run[nb][j];
+      x += __shfl_xor_sync(0xffffffffu, x, 4);
+      x += __shfl_xor_sync(0xffffffffu, x, 8);
+      x += __shfl_xor_sync(0xffffffffu, x, 16);
+      l_run[nb][j] = x;
+    }
+  __syncthreads();
+  float* slots = epi_acc + warp * kHPW * Cfg::kSlotStride;
+  if (lane < 4) {
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        float x = l_run[nb][j];
-        x += __shfl_xor_sync(0xffffffffu, x, 4);
-        x += __shfl_xor_sync(0xffffffffu, x, 8);
-        x += __shfl_xor_sync(0xffffffffu, x, 16);
-        l_run[nb][j] = x;
+        epi_m[warp * kHPW + nb * 8 + 2 * lane + j] = m_run[nb][j];
+        epi_l[warp * kHPW + nb * 8 + 2 * lane + j] = l_run[nb][j];
       }
-    named_bar_sync(1, Cfg::kConsumerThreads);  // earlier readers of the slots are done
-    float* slot = epi_acc + warp * kHPW * Cfg::kSlotStride;
-    if (lane < 4) {
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          epi_m[warp * kHPW + nb * 8 + 2 * lane + j] = m_run[nb][j];
-          epi_l[warp * kHPW + nb * 8 + 2 * lane + j] = l_run[nb][j];
-        }
-    }
-#pragma unroll
-    for (int mb = 0; mb < MB; ++mb)
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb) {
-        const int d0 = (D / 8) * g + 2 * mb;  // acc[0..1]: column d0; acc[2..3]: d0 + 1
-        const int h0 = nb * 8 + 2 * t;
-        slot[h0 * Cfg::kSlotStride + d0] = acc[mb][nb][0] * unit;
-        slot[(h0 + 1) * Cfg::kSlotStride + d0] = acc[mb][nb][1] * unit;
-        slot[h0 * Cfg::kSlotStride + d0 + 1] = acc[mb][nb][2] * unit;
-        slot[(h0 + 1) * Cfg::kSlotStride + d0 + 1] = acc[mb][nb][3] * unit;
-      }
-    named_bar_sync(1, Cfg::kConsumerThreads);
-    finish_item<D, 1, KW, kHPW, Cfg::kSlotStride>(p, it, epi_acc, epi_m, epi_l, threadIdx.x,
-                                                  Cfg::kConsumerThreads, abort_flag);
   }
+#pragma unroll
+  for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      const int d0 = (D / 8) * g + 2 * mb;  // acc[0..1]: column d0; acc[2..3]: d0 + 1
+      const int h0 = nb * 8 + 2 * t;
+      slots[h0 * Cfg::kSlotStride + d0] = acc[mb][nb][0] * unit;
+      slots[(h0 + 1) * Cfg::kSlotStride + d0] = acc[mb][nb][1] * unit;
+      slots[h0 * Cfg::kSlotStride + d0 + 1] = acc[mb][nb][2] * unit;
+      slots[(h0 + 1) * Cfg::kSlotStride + d0 + 1] = acc[mb][nb][3] * unit;
+    }
+  __syncthreads();
+  finish_item<D, 1, KW, kHPW, Cfg::kSlotStride>(p, it, epi_acc, epi_m, epi_l, threadIdx.x,
+                                                Cfg::kThreads, abort_flag);
 }
 
 // ---------------------------------------------------------------------------
 // Variants and launcher.  Groups of up to 8 query heads take one MMA block of
-// heads, larger ones two (16 heads an item), so that a group of 32 reads the
-// cache twice, not four times.
+// heads, larger ones two (16 heads a CTA); the head chunks of one cache chunk
+// are neighbours in the grid, so all but the first find its codes in L2.
 // ---------------------------------------------------------------------------
 template <int KIND>
-using Q8BD128N1 = Q8BCfg<128, 1, 5, KIND>;
+using Q8BD128N1 = Q8BCfg<128, 1, 2, 3, KIND>;
 template <int KIND>
-using Q8BD128N2 = Q8BCfg<128, 2, 4, KIND>;
+using Q8BD128N2 = Q8BCfg<128, 2, 2, 3, KIND>;
 template <int KIND>
-using Q8BD64N1 = Q8BCfg<64, 1, 9, KIND>;
+using Q8BD64N1 = Q8BCfg<64, 1, 3, 4, KIND>;
 template <int KIND>
-using Q8BD64N2 = Q8BCfg<64, 2, 8, KIND>;
+using Q8BD64N2 = Q8BCfg<64, 2, 4, 3, KIND>;
 
 KernelShape q8b_shape(int d, int group) {
-  const int heads = group <= 8 ? 8 : 16;
-  return KernelShape{128, heads, d, d == 128 ? 1 : 2, 1.0f};
+  const bool one = group <= 8;
+  const int ctas = d == 64 && one ? 4 : 3;
+  return KernelShape{32, one ? 8 : 16, d, d == 128 ? 1 : 2, float(ctas)};
 }
 
 template <class Cfg, bool MOD>

@@ -607,7 +607,11 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
         tc5::wait_ld();
       }
       if constexpr (MOD) {
-        if (p.mod.cap_log2 > 0.f) {
+        if (p.mod.short_tanh && p.mod.cap_log2 > 0.f) {
+#pragma unroll
+          for (int h = 0; h < HT; ++h)
+            s[h] = p.mod.cap_log2 * tanh_short(s[h] * p.scale_log2);
+        } else if (p.mod.cap_log2 > 0.f) {
 #pragma unroll
           for (int h = 0; h < HT; ++h)
             s[h] = p.mod.cap_log2 * tanh_fast(s[h] * p.scale_log2);
