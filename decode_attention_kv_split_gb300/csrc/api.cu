@@ -906,6 +906,10 @@ int kv_append_q8b(const void* k_new, const void* v_new, const long long* k_strid
   int st = check_blocks(B, h_kv, T, d, n_max, block, dtype, x_dtype);
   if (st != DA_OK) return st;
   if (T == 0) return DA_OK;
+  if (T > (1 << 30)) return DA_ERR_SHAPE;
+  // the kernels count blocks (and below, parts of 32 rows or more) in 32 bits
+  if (2LL * B * h_kv * (((T < n_max ? T : n_max) + block - 1) / block + 1) > 0x3fffffffLL)
+    return DA_ERR_SHAPE;
   if (!k_new || !v_new) return DA_ERR_NULL;
   if (!aligned16(k_new) || !aligned16(v_new) || !aligned16(K) || !aligned16(V) ||
       !aligned4(k_scale) || !aligned4(v_scale) || !aligned4(pos) || !aligned4(n_new))
@@ -929,6 +933,7 @@ int kv_append_q8b(const void* k_new, const void* v_new, const long long* k_strid
   a.blk_shift = block_shift(block);
   a.kind = dtype == DA_INT8 ? 1 : 2;
   a.x_bf16 = x_dtype == DA_BF16;
+  a.sms = sms;
   cudaError_t e = da::launch_kv_append_q8b(a, stream);
   if (e != cudaSuccess) return fail_cuda(e, "kv_append_q8b launch");
   g_launches.fetch_add(1);
@@ -944,7 +949,7 @@ int kv_read_q8b(const void* K, const void* V, const float* k_scale, const float*
   if (st != DA_OK) return st;
   if (T == 0) return DA_OK;
   if (!k_out || !v_out) return DA_ERR_NULL;
-  if (T > (1 << 30)) return DA_ERR_SHAPE;
+  if (T > (1 << 30) || 2LL * B * h_kv * ((T + 31LL) / 32) > 0x3fffffffLL) return DA_ERR_SHAPE;
   if (!aligned16(k_out) || !aligned16(v_out) || !aligned16(K) || !aligned16(V) ||
       !aligned4(k_scale) || !aligned4(v_scale) || !aligned4(seq_lens) || !aligned4(row_begin))
     return DA_ERR_ALIGN;
@@ -959,6 +964,7 @@ int kv_read_q8b(const void* K, const void* V, const float* k_scale, const float*
   a.blk_shift = block_shift(block);
   a.kind = dtype == DA_INT8 ? 1 : 2;
   a.out_bf16 = out_dtype == DA_BF16;
+  a.sms = sms;
   cudaError_t e = da::launch_kv_read_q8b(a, stream);
   if (e != cudaSuccess) return fail_cuda(e, "kv_read_q8b launch");
   g_launches.fetch_add(1);

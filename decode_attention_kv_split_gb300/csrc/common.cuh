@@ -329,7 +329,7 @@ struct BlockWriteArgs {
   const int32_t* pos;
   const int32_t* n_new;
   int32_t* dev_error;
-  int B, h_kv, T, d, n_max, blk_shift, kind, x_bf16;
+  int B, h_kv, T, d, n_max, blk_shift, kind, x_bf16, sms;
 };
 cudaError_t launch_kv_append_q8b(const BlockWriteArgs& a, cudaStream_t stream);
 struct BlockReadArgs {
@@ -339,7 +339,7 @@ struct BlockReadArgs {
   const int32_t* seq_lens;
   const int32_t* row_begin;
   int32_t* dev_error;
-  int B, h_kv, T, d, n_max, blk_shift, kind, out_bf16;
+  int B, h_kv, T, d, n_max, blk_shift, kind, out_bf16, sms;
 };
 cudaError_t launch_kv_read_q8b(const BlockReadArgs& a, cudaStream_t stream);
 cudaError_t launch_split_q8(const SplitParams& p, const CUtensorMap& tk, const CUtensorMap& tv,

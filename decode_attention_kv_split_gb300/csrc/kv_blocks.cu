@@ -14,10 +14,14 @@
 // subnormals.  It costs int8 half a bit on average against max|x| / Q.
 //
 // Bound: HBM for prompts (x once in, codes once out; a block's rows wait in
-// registers for its maximum), latency for single tokens: lengths, then x, the
-// scale and the held codes at once, then the stores.  A warp owns 16 rows of a
-// block, S / 16 warps a block, 128 / S blocks a CTA; a lane owns 16 elements
-// of a row, so that it stores 16 codes at once.
+// registers for its maximum), latency for single tokens: positions, then x and
+// the scale at once, then the stores.  For prompts the CTAs are persistent and
+// read the next block's position while they work on this one: with a CTA per
+// block every one began with that trip to memory, and the kernel ran at 3.8 TB/s.  A warp owns 16 rows of a
+// block, S / 16 warps a block, 128 / S blocks a CTA; a lane takes 16 bytes of x
+// at a time, so that a warp's loads and its stores of codes are both whole runs
+// of consecutive bytes (with 16 elements a lane, strided loads, prompts of fp32
+// rows were written at half the rate).
 #include <math.h>
 
 #include "common.cuh"
@@ -37,15 +41,16 @@ __device__ __forceinline__ float block_scale(float a) {
   return __uint_as_float(uint32_t(max(e, 1)) << 23);
 }
 
-// Four values, already divided by the scale, as codes.
+// Four values times `by` (exact) as codes; the products lie in [-Q, Q].
 template <int KIND>
-__device__ __forceinline__ uint32_t to_codes(float a, float b, float c, float d) {
-  constexpr float Q = KIND == 1 ? 127.f : 448.f;
-  a = fminf(fmaxf(a, -Q), Q), b = fminf(fmaxf(b, -Q), Q);
-  c = fminf(fmaxf(c, -Q), Q), d = fminf(fmaxf(d, -Q), Q);
+__device__ __forceinline__ uint32_t to_codes(float a, float b, float c, float d, float by) {
   if constexpr (KIND == 1) {
-    const uint32_t ab = __byte_perm(__float2int_rn(a), __float2int_rn(b), 0x0040);
-    const uint32_t cd = __byte_perm(__float2int_rn(c), __float2int_rn(d), 0x0040);
+    // rounded to an integer by an addition at 1.5 * 2^23: its low byte is the code
+    constexpr float kMagic = 12582912.f;
+    const uint32_t ab = __byte_perm(__float_as_uint(fmaf(a, by, kMagic)),
+                                    __float_as_uint(fmaf(b, by, kMagic)), 0x0040);
+    const uint32_t cd = __byte_perm(__float_as_uint(fmaf(c, by, kMagic)),
+                                    __float_as_uint(fmaf(d, by, kMagic)), 0x0040);
     return __byte_perm(ab, cd, 0x5410);
   } else {
     uint32_t r;
@@ -54,9 +59,15 @@ __device__ __forceinline__ uint32_t to_codes(float a, float b, float c, float d)
         "cvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n\t"
         "mov.b32 %0, {l, h};\n\t}"
         : "=r"(r)
-        : "f"(a), "f"(b), "f"(c), "f"(d));
+        : "f"(a * by), "f"(b * by), "f"(c * by), "f"(d * by));
     return r;
   }
+}
+
+template <int KIND>
+__device__ __forceinline__ float clamp_code(float x) {
+  constexpr float Q = KIND == 1 ? 127.f : 448.f;
+  return fminf(fmaxf(x, -Q), Q);
 }
 
 // Four codes as values.
@@ -77,152 +88,216 @@ struct BlockWrite {
   const int32_t* n_new;      // nullable: [B], rows of the call that sequence b takes (else T)
   int32_t* dev_error;
   int B, h_kv, T, n_max, nblk, blk_shift, touched;
-  long long units;           // 2 * B * h_kv * touched
+  unsigned units;            // 2 * B * h_kv * touched
   long long cache_rows, scale_elems;  // extents, for the checked build
 };
 
 constexpr int kWriteThreads = 256;
+// CTAs an SM, by the registers that a warp's 16 rows take.
+template <int D, bool XBF16>
+constexpr int write_ctas() { return D == 128 && !XBF16 ? 2 : D == 64 && XBF16 ? 5 : 3; }
+
+// Element e of the 16 bytes of x that a lane holds.
+template <bool XBF16>
+__device__ __forceinline__ float x_elem(const uint4& w, int e) {
+  if constexpr (XBF16) {
+    const uint32_t v = word_of(w, e >> 1);
+    return (e & 1) ? bf16_hi_to_f32(v) : bf16_lo_to_f32(v);
+  } else {
+    return __uint_as_float(word_of(w, e));
+  }
+}
 
 template <int D, bool XBF16, int KIND>
-__global__ void __launch_bounds__(kWriteThreads)
+__global__ void __launch_bounds__(kWriteThreads, write_ctas<D, XBF16>())
     kv_append_q8b_kernel(const BlockWrite p) {
-  constexpr int LPR = D / 16;        // lanes per row
-  constexpr int RPP = 32 / LPR;      // rows a warp covers at once
-  constexpr int PASS = 16 / RPP;     // passes over its 16 rows
-  __shared__ float red[kWriteThreads / 32];
+  constexpr int EPL = XBF16 ? 8 : 4;  // elements of 16 bytes
+  constexpr int LPR = D / EPL;        // lanes per row
+  constexpr int RPP = 32 / LPR;       // rows a warp covers at once
+  constexpr int PASS = 16 / RPP;      // passes over its 16 rows
+  constexpr int kWarps = kWriteThreads / 32;
+  __shared__ float red[2][kWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int S = 1 << p.blk_shift, W = S >> 4;  // rows of a block, warps of a block
-  const int per_cta = (kWriteThreads / 32) / W;
-  const long long unit = (long long)blockIdx.x * per_cta + warp / W;
+  const unsigned per_cta = unsigned(kWarps / W);
   const int sub = warp % W;
+  const int rl = lane / LPR, c = lane % LPR;
   allow_dependent_launch();
   wait_for_prerequisite_grid();
 
-  // unit -> (head, touched block, tensor); a unit past the end only takes part in the barrier
-  const bool live_unit = unit < p.units;
-  const int tensor = int(unit & 1);
-  const long long u2 = unit >> 1;
-  const int j = live_unit ? int(u2 % p.touched) : 0;
-  const int head = live_unit ? int(u2 / p.touched) : 0;  // b * h_kv + h
-  const int b = head / p.h_kv, h = head - b * p.h_kv;
-  const int pos = __ldcg(p.pos + b);
-  int m = p.T;
-  bool bad = false;
-  if (p.n_new) {
-    m = __ldcg(p.n_new + b);
-    bad = m < 0 || m > p.T;
+  // The raw position and count of a unit's sequence.
+  auto load_counts = [&](unsigned unit, int& pos, int& m) {
+    pos = 0, m = 0;
+    if (unit >= p.units) return;
+    const int b = int((unit >> 1) / unsigned(p.touched)) / p.h_kv;
+    pos = __ldcg(p.pos + b);
+    m = p.n_new ? __ldcg(p.n_new + b) : p.T;
+  };
+  int pos_next, m_next;
+  load_counts(blockIdx.x * per_cta + warp / W, pos_next, m_next);
+  int turn = 0;
+  for (unsigned base = blockIdx.x * per_cta; base < p.units; base += gridDim.x * per_cta) {
+    // unit -> (head, touched block, tensor); a unit past the end only takes part in the barrier
+    const unsigned unit = base + unsigned(warp / W);
+    const bool live_unit = unit < p.units;
+    const int tensor = int(unit & 1u);
+    const int j = live_unit ? int((unit >> 1) % unsigned(p.touched)) : 0;
+    const int head = live_unit ? int((unit >> 1) / unsigned(p.touched)) : 0;  // b * h_kv + h
+    const int b = head / p.h_kv, h = head - b * p.h_kv;
+    const int pos = pos_next;
+    int m = m_next;
+    load_counts(unit + gridDim.x * per_cta, pos_next, m_next);
+    bool bad = m < 0 || m > p.T;
     m = min(max(m, 0), p.T);
-  }
-  if (pos < 0 || pos > p.n_max) {
-    bad |= m > 0;
-    m = 0;
-  } else if (m > p.n_max - pos) {
-    bad = true;
-    m = p.n_max - pos;
-  }
-  if (bad && live_unit && j == 0 && tensor == 0 && h == 0 && sub == 0 && lane == 0)
-    flag_error(p.dev_error, DA_DEVERR_POS);
-  const int blk = (pos >> p.blk_shift) + j;
-  const int row0 = (blk << p.blk_shift) + sub * 16;  // this warp's first cache row
-  const bool work = live_unit && m > 0 && (blk << p.blk_shift) < pos + m;
-  const bool held = work && (blk << p.blk_shift) < pos;  // the block holds earlier rows
-  const int rl = lane / LPR, c = lane % LPR;
+    if (pos < 0 || pos > p.n_max) {
+      bad |= m > 0;
+      m = 0;
+    } else if (m > p.n_max - pos) {
+      bad = true;
+      m = p.n_max - pos;
+    }
+    if (bad && live_unit && j == 0 && tensor == 0 && h == 0 && sub == 0 && lane == 0)
+      flag_error(p.dev_error, DA_DEVERR_POS);
+    const int blk = (pos >> p.blk_shift) + j;
+    const int row0 = int((unsigned(blk) << p.blk_shift) + unsigned(sub) * 16u);  // this warp's first cache row
+    const unsigned start = unsigned(blk) << p.blk_shift;  // (past 2^31 for the last block of 2^30 rows)
+    const bool work = live_unit && m > 0 && start < unsigned(pos + m);
+    const bool held = work && start < unsigned(pos);  // the block holds earlier rows
 
-  // ---- loads: new rows, the block's scale, the codes it already holds
-  const size_t scale_at = size_t(head) * p.nblk + blk;
-  float s_old = 0.f;
-  const bool scale_in = !work || DA_IN(p, scale_at, p.scale_elems);
-  if (held && scale_in) s_old = __ldcg(p.scale[tensor] + scale_at);
-  float x[PASS][16];
-  uint4 old[PASS];
-  bool finite = true;
-  float a = 0.f;
-  if (work) {
-    const char* base = static_cast<const char*>(p.x[tensor]);
-    const long long off = (long long)b * p.sb[tensor] + (long long)h * p.sh[tensor] + c * 16;
-    uint4 raw[PASS][XBF16 ? 2 : 4];
+    // ---- loads: new rows and the block's scale
+    const size_t scale_at = size_t(head) * p.nblk + blk;
+    uint4 x[PASS];
+    const char* xs = static_cast<const char*>(tensor ? p.x[1] : p.x[0]);
+    uint8_t* codes = tensor ? p.codes[1] : p.codes[0];
+    float* scale = tensor ? p.scale[1] : p.scale[0];
+    const long long sb = tensor ? p.sb[1] : p.sb[0], sh = tensor ? p.sh[1] : p.sh[0],
+                    st = tensor ? p.st[1] : p.st[0];
+    const bool scale_in = !work || DA_IN(p, scale_at, p.scale_elems);
+    float s_old = 0.f;
+    if (held && scale_in) s_old = __ldcg(scale + scale_at);
+    float a = 0.f;
+    if (work) {
+      xs += ((long long)b * sb + (long long)h * sh + c * EPL) * (16 / EPL);
 #pragma unroll
-    for (int u = 0; u < PASS; ++u) {
-      const int row = row0 + u * RPP + rl;
-      const int i = row - pos;
-      if (i >= 0 && i < m) {
-        const uint4* src = reinterpret_cast<const uint4*>(
-            base + (off + (long long)i * p.st[tensor]) * (XBF16 ? 2 : 4));
+      for (int u = 0; u < PASS; ++u) {
+        const int i = row0 + u * RPP + rl - pos;
+        x[u] = i >= 0 && i < m
+                   ? __ldcs(reinterpret_cast<const uint4*>(xs + (long long)i * st * (16 / EPL)))
+                   : make_uint4(0, 0, 0, 0);
+      }
+      // the largest magnitude, as bits without their sign
+      uint32_t top = 0;
 #pragma unroll
-        for (int e = 0; e < (XBF16 ? 2 : 4); ++e) raw[u][e] = __ldcs(src + e);
-      } else {
+      for (int u = 0; u < PASS; ++u)
 #pragma unroll
-        for (int e = 0; e < (XBF16 ? 2 : 4); ++e) raw[u][e] = make_uint4(0, 0, 0, 0);
-        if (i < 0 && DA_IN(p, size_t(head) * p.n_max + row, p.cache_rows))
-          old[u] = *reinterpret_cast<const uint4*>(p.codes[tensor] +
-                                                   (size_t(head) * p.n_max + row) * D + c * 16);
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t w = word_of(x[u], e);
+          top = XBF16 ? __vmaxu2(top, w & 0x7fff7fffu) : max(top, w & 0x7fffffffu);
+        }
+      if (XBF16) top = max(top & 0xffff0000u, top << 16);
+      if (top >= 0x7f800000u) {  // NaN or infinity among them: they count as 0
+        flag_error(p.dev_error, DA_DEVERR_VALUE);
+        top = 0;
+#pragma unroll
+        for (int u = 0; u < PASS; ++u) {
+          uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if (XBF16) {
+              if ((w[e] & 0x7f80u) == 0x7f80u) w[e] &= 0xffff0000u;
+              if ((w[e] & 0x7f800000u) == 0x7f800000u) w[e] &= 0xffffu;
+              top = max(top, max(w[e] & 0x7fff0000u, (w[e] << 16) & 0x7fffffffu));
+            } else {
+              if ((w[e] & 0x7f800000u) == 0x7f800000u) w[e] = 0;
+              top = max(top, w[e] & 0x7fffffffu);
+            }
+          }
+          x[u] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+      a = __uint_as_float(top);
+    }
+
+    // ---- the block's maximum and scale
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+    if (W > 1) {
+      // (two scratch rows: a warp reaches this one's next use only past the
+      // barrier of the turn between)
+      if (lane == 0) red[turn][warp] = a;
+      __syncthreads();
+      const int w0 = warp - sub;
+      for (int w = 0; w < W; ++w) a = fmaxf(a, red[turn][w0 + w]);
+      turn ^= 1;
+    }
+    if (!work) continue;
+    const float s_new = fmaxf(s_old, block_scale<KIND>(a));
+    if (sub == 0 && lane == 0 && scale_in) scale[scale_at] = s_new;
+
+    // ---- codes
+    // a power of two divides exactly by its inverse (2^-126 .. 2^125 have a normal one)
+    const uint32_t sbits = __float_as_uint(s_new);
+    const bool pow2 = (sbits & 0x807fffffu) == 0 && sbits != 0 && (sbits >> 23) < 253;
+    const float inv = pow2 ? __uint_as_float((254u << 23) - sbits) : 0.f;
+    uint8_t* dst0 = codes + (size_t(head) * p.n_max + row0 + rl) * D + c * EPL;
+    auto put = [&](int u, const float (&f)[EPL], float by) {
+      uint8_t* dst = dst0 + u * (RPP * D);
+      const uint32_t w0 = to_codes<KIND>(f[0], f[1], f[2], f[3], by);
+      if constexpr (XBF16)
+        *reinterpret_cast<uint2*>(dst) =
+            make_uint2(w0, to_codes<KIND>(f[4], f[5], f[6], f[7], by));
+      else
+        *reinterpret_cast<uint32_t*>(dst) = w0;
+    };
+    // (a block written in whole has no row to test)
+    const bool whole = row0 >= pos && row0 + 16 <= pos + m;
+    if (pow2 || s_new == 0.f) {  // (0: every element is 0)
+#pragma unroll
+      for (int u = 0; u < PASS; ++u) {
+        const int row = row0 + u * RPP + rl;
+        if (!whole && (row < pos || row >= pos + m)) continue;
+        if (!DA_IN(p, size_t(head) * p.n_max + row, p.cache_rows)) continue;
+        float f[EPL];
+#pragma unroll
+        for (int e = 0; e < EPL; ++e) f[e] = x_elem<XBF16>(x[u], e);
+        put(u, f, inv);
+      }
+    } else {  // a scale from elsewhere: a rounded division and a clamp
+#pragma unroll 1
+      for (int u = 0; u < PASS; ++u) {
+        const int row = row0 + u * RPP + rl;
+        uint4 xu = x[0];
+#pragma unroll
+        for (int k = 1; k < PASS; ++k)
+          if (k == u) xu = x[k];
+        if (row < pos || row >= pos + m ||
+            !DA_IN(p, size_t(head) * p.n_max + row, p.cache_rows))
+          continue;
+        float f[EPL];
+#pragma unroll
+        for (int e = 0; e < EPL; ++e)
+          f[e] = clamp_code<KIND>(__fdiv_rn(x_elem<XBF16>(xu, e), s_new));
+        put(u, f, 1.f);
       }
     }
+    // ---- a scale that grew: the codes of the rows the block already holds, 16 a lane
+    if (held && s_new > s_old) {
+      const float ratio = __fdiv_rn(s_old, s_new);
+      for (int k = lane; k < 16 * (D / 16); k += 32) {
+        const int row = row0 + k / (D / 16);
+        if (row >= pos || !DA_IN(p, size_t(head) * p.n_max + row, p.cache_rows)) continue;
+        uint4* at = reinterpret_cast<uint4*>(codes + (size_t(head) * p.n_max + row) * D) + k % (D / 16);
+        const uint4 old = *at;
+        uint32_t w[4];
 #pragma unroll
-    for (int u = 0; u < PASS; ++u)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        float f;
-        if constexpr (XBF16) {
-          const uint32_t w = word_of(raw[u][e >> 3], (e >> 1) & 3);
-          f = (e & 1) ? bf16_hi_to_f32(w) : bf16_lo_to_f32(w);
-        } else {
-          f = __uint_as_float(word_of(raw[u][e >> 2], e & 3));
+        for (int e = 0; e < 4; ++e) {
+          float f[4];
+          from_codes<KIND>(word_of(old, e), f);
+          w[e] = to_codes<KIND>(clamp_code<KIND>(f[0] * ratio), clamp_code<KIND>(f[1] * ratio),
+                                clamp_code<KIND>(f[2] * ratio), clamp_code<KIND>(f[3] * ratio), 1.f);
         }
-        if (!isfinite(f)) {
-          finite = false;
-          f = 0.f;
-        }
-        x[u][e] = f;
-        a = fmaxf(a, fabsf(f));
+        *at = make_uint4(w[0], w[1], w[2], w[3]);
       }
-  }
-  if (!finite) flag_error(p.dev_error, DA_DEVERR_VALUE);
-
-  // ---- the block's maximum and scale
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-  if (lane == 0) red[warp] = a;
-  __syncthreads();
-  if (!work) return;
-  const int w0 = warp - sub;
-  for (int w = 0; w < W; ++w) a = fmaxf(a, red[w0 + w]);
-  const float s_new = fmaxf(s_old, block_scale<KIND>(a));
-  if (sub == 0 && lane == 0 && scale_in) p.scale[tensor][scale_at] = s_new;
-
-  // ---- codes
-  const bool grown = held && s_new > s_old;
-  const float ratio = grown ? __fdiv_rn(s_old, s_new) : 1.f;
-  // a power of two divides exactly by its inverse (2^-126 .. 2^121 have one)
-  const uint32_t sbits = __float_as_uint(s_new);
-  const bool pow2 = (sbits & 0x807fffffu) == 0 && sbits != 0 && (sbits >> 23) < 253;
-  const float inv = pow2 ? __uint_as_float((254u << 23) - sbits) : 0.f;
-#pragma unroll
-  for (int u = 0; u < PASS; ++u) {
-    const int row = row0 + u * RPP + rl;
-    const int i = row - pos;
-    uint4* dst = reinterpret_cast<uint4*>(p.codes[tensor] + (size_t(head) * p.n_max + row) * D +
-                                          c * 16);
-    if (i >= m || !DA_IN(p, size_t(head) * p.n_max + row, p.cache_rows)) continue;
-    uint32_t w[4];
-    if (i >= 0) {
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        if (pow2) x[u][e] *= inv;
-        else x[u][e] = s_new != 0.f ? __fdiv_rn(x[u][e], s_new) : 0.f;
-      }
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        w[e] = to_codes<KIND>(x[u][4 * e], x[u][4 * e + 1], x[u][4 * e + 2], x[u][4 * e + 3]);
-      *dst = make_uint4(w[0], w[1], w[2], w[3]);
-    } else if (grown) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        float f[4];
-        from_codes<KIND>(word_of(old[u], e), f);
-        w[e] = to_codes<KIND>(f[0] * ratio, f[1] * ratio, f[2] * ratio, f[3] * ratio);
-      }
-      *dst = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
 }
@@ -245,12 +320,16 @@ cudaError_t launch_kv_append_q8b(const BlockWriteArgs& a, cudaStream_t stream) {
   // blocks that T rows at any position can touch (never more than there are)
   const long long touched = ((long long)a.T + 2 * S - 2) / S;
   p.touched = int(touched < p.nblk ? touched : p.nblk);
-  p.units = 2LL * a.B * a.h_kv * p.touched;
+  const long long units = 2LL * a.B * a.h_kv * p.touched;
+  if (units > 0x7fffffffLL) return cudaErrorInvalidValue;  // (checked by the caller)
+  p.units = unsigned(units);
   p.cache_rows = (long long)a.B * a.h_kv * a.n_max;
   p.scale_elems = (long long)a.B * a.h_kv * p.nblk;
   const int per_cta = (kWriteThreads / 32) / (S / 16);
-  const long long grid = (p.units + per_cta - 1) / per_cta;
-  if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
+  const long long ctas = (units + per_cta - 1) / per_cta;
+  const long long places = (long long)a.sms * (a.d == 128 ? (a.x_bf16 ? write_ctas<128, true>() : write_ctas<128, false>())
+                                                     : (a.x_bf16 ? write_ctas<64, true>() : write_ctas<64, false>()));
+  const long long grid = ctas < places ? ctas : places;
   auto go = [&](auto kernel) {
     return launch_dependent(kernel, int(grid), kWriteThreads, 0, stream, p);
   };
@@ -265,8 +344,10 @@ cudaError_t launch_kv_append_q8b(const BlockWriteArgs& a, cudaStream_t stream) {
 // ---------------------------------------------------------------------------
 // Read: out[b, h, i, :] = s[block] * value(code) of row row_begin[b] + i, for
 // the rows below the sequence's length; other rows of out are left alone.
-// Bound: HBM (1 byte in, 2 or 4 out per element).  A lane takes 16 codes and
-// four rows' worth of loads are in flight per lane.
+// Bound: HBM (1 byte in, 2 or 4 out per element).  A lane writes 16 bytes at a
+// time, so that a warp's loads and stores are whole runs of bytes.  CTAs are
+// persistent and hold two parts of kReadUnroll rows for every run of lanes: one
+// is loaded while the other is converted and stored.
 // ---------------------------------------------------------------------------
 struct BlockRead {
   const uint8_t* codes[2];
@@ -275,76 +356,103 @@ struct BlockRead {
   const int32_t* seq_lens;   // [B]
   const int32_t* row_begin;  // nullable: [B] (else 0)
   int32_t* dev_error;
-  int B, h_kv, T, n_max, nblk, blk_shift, per_head;  // per_head: CTAs of one head of one tensor
+  int B, h_kv, T, n_max, nblk, blk_shift;
+  unsigned per_head, parts;  // parts of one head of one tensor, and of all
   long long cache_rows, scale_elems, out_rows;       // extents, for the checked build
 };
 
 constexpr int kReadThreads = 256;
-constexpr int kReadUnroll = 4;
+constexpr int kReadUnroll = 8;
+constexpr int kReadCtas = 4;  // CTAs an SM
 
 template <int D, bool OBF16, int KIND>
-__global__ void __launch_bounds__(kReadThreads) kv_read_q8b_kernel(const BlockRead p) {
-  constexpr int LPR = D / 16;
-  constexpr int ROWS = kReadThreads / LPR;  // rows of one step of the CTA
+__global__ void __launch_bounds__(kReadThreads, kReadCtas)
+    kv_read_q8b_kernel(const BlockRead p) {
+  constexpr int EPL = OBF16 ? 8 : 4;        // elements of 16 output bytes
+  constexpr int LPR = D / EPL;              // lanes per row
+  constexpr int SETS = kReadThreads / LPR;  // row sets of a part: one for each LPR lanes
   allow_dependent_launch();
   wait_for_prerequisite_grid();
-  const int part = int(blockIdx.x % unsigned(p.per_head));
-  const unsigned u = blockIdx.x / unsigned(p.per_head);
-  const int tensor = int(u & 1u);
-  const int head = int(u >> 1);
-  const int b = head / p.h_kv;
-  int n = __ldcg(p.seq_lens + b);
-  const int begin = p.row_begin ? __ldcg(p.row_begin + b) : 0;
-  const bool bad = n < 0 || n > p.n_max || begin < 0;
-  n = min(max(n, 0), p.n_max);
-  if (bad && part == 0 && tensor == 0 && head == b * p.h_kv && threadIdx.x == 0)
-    flag_error(p.dev_error, DA_DEVERR_SEQ_LEN);
-  if (begin < 0) return;
-  const int rows = min(p.T, n - begin);  // may be <= 0
+
+  // One part: kReadUnroll consecutive rows for every LPR lanes.  Its codes and
+  // scales are loaded while the part before it is converted and stored.
+  struct Part {
+    uint2 w[kReadUnroll];
+    float s[2];          // the scales of the first row's block and of the next
+    int tensor, head, i0, rows, first_next;  // rows of i0 .. below `rows`; from i0 + first_next
+                                             // on the second scale
+  };
   const int c = threadIdx.x % LPR;
-  const int i0 = part * (ROWS * kReadUnroll) + threadIdx.x / LPR;
-  const size_t in0 = size_t(head) * p.n_max + begin;
-  const uint8_t* codes = tensor ? p.codes[1] : p.codes[0];
-  const float* scales = tensor ? p.scale[1] : p.scale[0];
-  void* out = tensor ? p.out[1] : p.out[0];
-  uint4 w[kReadUnroll];
-  float s[kReadUnroll];
+  auto load = [&](unsigned part, Part& q, int n, int begin) {
+    q.rows = 0;
+    if (part >= p.parts) return;
+    const unsigned u = part / p.per_head;
+    q.tensor = int(u & 1u);
+    q.head = int(u >> 1);
+    const bool bad = n < 0 || n > p.n_max || begin < 0;
+    if (bad && part % p.per_head == 0 && q.tensor == 0 && q.head % p.h_kv == 0 && threadIdx.x == 0)
+      flag_error(p.dev_error, DA_DEVERR_SEQ_LEN);
+    if (begin < 0) return;
+    n = min(max(n, 0), p.n_max);
+    q.rows = min(p.T, n - begin);  // may be <= 0
+    q.i0 = int(part % p.per_head) * (SETS * kReadUnroll) + int(threadIdx.x / LPR) * kReadUnroll;
+    if (q.i0 >= q.rows) return;
+    const int blk = (begin + q.i0) >> p.blk_shift;
+    q.first_next = ((blk + 1) << p.blk_shift) - (begin + q.i0);
+    const float* scales = (q.tensor ? p.scale[1] : p.scale[0]) + size_t(q.head) * p.nblk;
+    q.s[0] = q.s[1] = 0.f;
+    if (DA_IN(p, blk, p.nblk)) q.s[0] = __ldcg(scales + blk);
+    if (q.first_next < kReadUnroll && q.i0 + q.first_next < q.rows && DA_IN(p, blk + 1, p.nblk))
+      q.s[1] = __ldcg(scales + blk + 1);
+    const size_t in = size_t(q.head) * p.n_max + begin + q.i0;
+    const uint8_t* src = (q.tensor ? p.codes[1] : p.codes[0]) + in * D + c * EPL;
 #pragma unroll
-  for (int k = 0; k < kReadUnroll; ++k) {
-    const int i = i0 + k * ROWS;
-    if (i < rows && DA_IN(p, in0 + i, p.cache_rows) &&
-        DA_IN(p, size_t(head) * p.nblk + ((begin + i) >> p.blk_shift), p.scale_elems)) {
-      w[k] = __ldcs(reinterpret_cast<const uint4*>(codes + (in0 + i) * D + c * 16));
-      s[k] = __ldcg(scales + size_t(head) * p.nblk + ((begin + i) >> p.blk_shift));
+    for (int k = 0; k < kReadUnroll; ++k)
+      if (q.i0 + k < q.rows && DA_IN(p, in + k, p.cache_rows)) {
+        if constexpr (OBF16) q.w[k] = __ldcs(reinterpret_cast<const uint2*>(src + k * D));
+        else q.w[k].x = __ldcs(reinterpret_cast<const unsigned*>(src + k * D));
+      }
+  };
+  auto store = [&](const Part& q) {
+    const size_t row0 = size_t(q.head) * p.T + q.i0;
+    void* out = q.tensor ? p.out[1] : p.out[0];
+#pragma unroll
+    for (int k = 0; k < kReadUnroll; ++k) {
+      if (q.i0 + k >= q.rows || !DA_IN(p, row0 + k, p.out_rows)) continue;
+      const float s = k < q.first_next ? q.s[0] : q.s[1];
+      const size_t at = (row0 + k) * D + c * EPL;
+      float f[4];
+      from_codes<KIND>(q.w[k].x, f);
+      if constexpr (OBF16) {
+        float g[4];
+        from_codes<KIND>(q.w[k].y, g);
+        __stcs(reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(out) + at),
+               make_uint4(pack_bf16x2(f[0] * s, f[1] * s), pack_bf16x2(f[2] * s, f[3] * s),
+                          pack_bf16x2(g[0] * s, g[1] * s), pack_bf16x2(g[2] * s, g[3] * s)));
+      } else {
+        __stcs(reinterpret_cast<float4*>(static_cast<float*>(out) + at),
+               make_float4(f[0] * s, f[1] * s, f[2] * s, f[3] * s));
+      }
     }
-  }
-#pragma unroll
-  for (int k = 0; k < kReadUnroll; ++k) {
-    const int i = i0 + k * ROWS;
-    if (i >= rows || !DA_IN(p, size_t(head) * p.T + i, p.out_rows)) continue;
-    float f[16];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      float q[4];
-      from_codes<KIND>(word_of(w[k], e), q);
-#pragma unroll
-      for (int z = 0; z < 4; ++z) f[4 * e + z] = q[z] * s[k];
-    }
-    const size_t at = (size_t(head) * p.T + i) * D + c * 16;
-    if constexpr (OBF16) {
-      uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(out) + at);
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-        __stcs(dst + e, make_uint4(pack_bf16x2(f[8 * e], f[8 * e + 1]),
-                                   pack_bf16x2(f[8 * e + 2], f[8 * e + 3]),
-                                   pack_bf16x2(f[8 * e + 4], f[8 * e + 5]),
-                                   pack_bf16x2(f[8 * e + 6], f[8 * e + 7])));
-    } else {
-      float4* dst = reinterpret_cast<float4*>(static_cast<float*>(out) + at);
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        __stcs(dst + e, make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]));
-    }
+  };
+  auto counts = [&](unsigned part, int& n, int& begin) {
+    n = begin = 0;
+    if (part >= p.parts) return;
+    const int b = int(part / p.per_head >> 1) / p.h_kv;
+    n = __ldcg(p.seq_lens + b);
+    if (p.row_begin) begin = __ldcg(p.row_begin + b);
+  };
+  Part now, next;
+  int n, begin;
+  unsigned part = blockIdx.x;
+  counts(part, n, begin);
+  load(part, now, n, begin);
+  counts(part + gridDim.x, n, begin);
+  for (; part < p.parts; part += gridDim.x) {
+    load(part + gridDim.x, next, n, begin);
+    counts(part + 2 * gridDim.x, n, begin);
+    if (now.rows > 0) store(now);
+    now = next;
   }
 }
 
@@ -361,13 +469,17 @@ cudaError_t launch_kv_read_q8b(const BlockReadArgs& a, cudaStream_t stream) {
   p.B = a.B, p.h_kv = a.h_kv, p.T = a.T, p.n_max = a.n_max, p.blk_shift = a.blk_shift;
   const int S = 1 << a.blk_shift;
   p.nblk = (a.n_max + S - 1) / S;
-  const int rows = kReadThreads / (a.d / 16) * kReadUnroll;
-  p.per_head = (a.T + rows - 1) / rows;
+  const int rows = kReadThreads / (a.d / (a.out_bf16 ? 8 : 4)) * kReadUnroll;
+  const long long per_head = (a.T + rows - 1LL) / rows;
   p.cache_rows = (long long)a.B * a.h_kv * a.n_max;
   p.scale_elems = (long long)a.B * a.h_kv * p.nblk;
   p.out_rows = (long long)a.B * a.h_kv * a.T;
-  const long long grid = 2LL * a.B * a.h_kv * p.per_head;
-  if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
+  const long long parts = 2LL * a.B * a.h_kv * per_head;
+  if (parts > 0x3fffffffLL) return cudaErrorInvalidValue;  // (checked by the caller)
+  p.per_head = unsigned(per_head);
+  p.parts = unsigned(parts);
+  const long long places = (long long)a.sms * kReadCtas;
+  const long long grid = parts < places ? parts : places;
   auto go = [&](auto kernel) {
     return launch_dependent(kernel, int(grid), kReadThreads, 0, stream, p);
   };
