@@ -220,7 +220,8 @@ long long seen_rows(const da_score_mod* mod, int n_max) {
   return mod->window > 0 ? (long long)mod->window + mod->prefix : n_max;
 }
 
-da::ScoreTerms score_terms_of(const da_score_mod* mod, int tile_rows, int b0, bool out_bf16) {
+da::ScoreTerms score_terms_of(const da_score_mod* mod, int tile_rows, int b0, float scale,
+                               bool out_bf16) {
   da::ScoreTerms t{};
   if (!mod) return t;
   t.on = 1;
@@ -229,7 +230,8 @@ da::ScoreTerms score_terms_of(const da_score_mod* mod, int tile_rows, int b0, bo
   t.prefix = mod->prefix;
   t.doc_begin = mod->doc_begin ? mod->doc_begin + b0 : nullptr;
   t.slopes = mod->slopes;
-  t.short_tanh = out_bf16 && mod->softcap <= da::kShortTanhCap;
+  if (mod->softcap > 0.f && mod->softcap <= da::kShortTanhCap && out_bf16)
+    t.short_scale = float(2.0 * 1.4426950408889634 * double(scale) / double(mod->softcap));
   t.cap_log2 = float(double(mod->softcap) * 1.4426950408889634);
   return t;
 }
@@ -497,7 +499,7 @@ int run_decode(const void* q, const void* K, const void* V, const int32_t* seq_l
     p.out = static_cast<char*>(out) + size_t(b0) * h_q * d_v * out_es;
     p.out_bf16 = dta.out_bf16 ? 1 : 0;
     p.row_off = row_off;
-    p.mod = score_terms_of(mod, pl.ks.tile_rows, b0, dta.out_bf16);
+    p.mod = score_terms_of(mod, pl.ks.tile_rows, b0, scale, dta.out_bf16);
     p.row_lim = row_lim;
     p.lse_out = lse_out ? lse_out + size_t(b0) * h_q : nullptr;
     p.o_part = wl.total ? reinterpret_cast<float*>(ws + wl.o_part) : nullptr;

@@ -30,7 +30,8 @@ struct ScoreTerms {
   int window, prefix;            // window 0: unlimited
   const int32_t* doc_begin;      // nullable: [B], this launch's slice
   const float* slopes;           // nullable: [h_q]
-  int short_tanh;                // tanh_short is exact enough for this call's output
+  float short_scale;             // 2 log2 e scale / softcap where capped_short is exact enough
+                                 // for this call's output, else 0
   float cap_log2;                // softcap * log2 e (scale_log2 is then scale / softcap); 0: none
 };
 
@@ -574,21 +575,21 @@ __device__ __forceinline__ float tanh_fast(float x) {
   return fabsf(x) < 0.5f ? small : large;
 }
 
-// tanh with an absolute error of about 2^-22: 1 - 2 / (1 + e^2x), 5 instructions.
-// A score capped at c is off by up to c 2^-22, its weight by that factor: for a
-// bf16 output and c <= kShortTanhCap that is at most 2^-15, far below the
-// output's own half step of 2^-9.
+// A capped score c tanh(t / c) in the log2 domain from x = 2 log2 e t / c, as
+// c - 2 c / (1 + e^(2 t / c)): 4 instructions, off by about c 2^-22 whatever the
+// score's size, and its weight by that factor.  For a bf16 output and
+// c <= kShortTanhCap that is at most 2^-15, far below the output's own half step
+// of 2^-9; other calls take tanh_fast.
 constexpr float kShortTanhCap = 128.f;
-__device__ __forceinline__ float tanh_short(float x) {
-  const float e = ex2(2.f * 1.4426950408889634f * x);
+__device__ __forceinline__ float capped_short(const ScoreTerms& m, float x) {
   float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
-  return fmaf(-2.f, r, 1.f);
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2(x)));
+  return fmaf(-2.f * m.cap_log2, r, m.cap_log2);
 }
 
-// A log2-domain score with its distance bias.
-__device__ __forceinline__ float biased(float x, const RowDistance& d, float slope) {
-  return fmaf(slope, slope >= 0.f ? d.to_last : d.to_first, x);
+// A log2-domain score with its distance bias (up: every slope in hand is >= 0).
+__device__ __forceinline__ float biased(float x, const RowDistance& d, float slope, bool up) {
+  return fmaf(slope, up || slope >= 0.f ? d.to_last : d.to_first, x);
 }
 
 template <int TILE>

@@ -269,14 +269,14 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
           seen[kb][1] = all || mask.seen(key0 + kb * 16 + r + 8);
         }
         if constexpr (MOD) {  // score terms (one branch for all of a lane's scores)
-          if (p.mod.short_tanh && p.mod.cap_log2 > 0.f) {
+          if (p.mod.short_scale != 0.f) {
 #pragma unroll
             for (int kb = 0; kb < KBW; ++kb)
 #pragma unroll
               for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                  s[kb][nb][e] = p.mod.cap_log2 * tanh_short(s[kb][nb][e] * p.scale_log2);
+                  s[kb][nb][e] = capped_short(p.mod, s[kb][nb][e] * p.mod.short_scale);
           } else if (p.mod.cap_log2 > 0.f) {
 #pragma unroll
             for (int kb = 0; kb < KBW; ++kb)
@@ -302,7 +302,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                   s[kb][nb][e] = biased(s[kb][nb][e], RowDistance(dist, kb * 16 + (e >> 1) * 8),
-                                        slope[nb][e & 1]);
+                                        slope[nb][e & 1], false);
           }
         }
         float alpha[NB][2];

@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
             for (int g = 0; g < G; ++g)
 #pragma unroll
               for (int rr = 0; rr < RPW; ++rr)
-                s[g][rr] = biased(s[g][rr], RowDistance(dist, rr), slope[g]);
+                s[g][rr] = biased(s[g][rr], RowDistance(dist, rr), slope[g], false);
           }
 #pragma unroll
           for (int g = 0; g < G; ++g)

@@ -238,6 +238,13 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::CTAS)
   }
 
   const bool exact_p = p.out_bf16 == 0;  // P's fp16 remainder too
+  const float score_scale = MOD && p.mod.short_scale != 0.f ? p.mod.short_scale : p.scale_log2;
+  [[maybe_unused]] bool slopes_up = true;
+  if constexpr (MOD) {
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) slopes_up &= slope[nb][0] >= 0.f && slope[nb][1] >= 0.f;
+    slopes_up = __all_sync(0xffffffffu, slopes_up);
+  }
   int slot = 0;
   uint32_t phase = 0;
   for (int i = 0; i < it.tiles; ++i) {
@@ -267,7 +274,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::CTAS)
       float ks[2], vs[2];
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        ks[u] = __shfl_sync(0xffffffffu, sk_now, 2 * (i & 15) + u) * p.scale_log2;
+        ks[u] = __shfl_sync(0xffffffffu, sk_now, 2 * (i & 15) + u) * score_scale;
         vs[u] = __shfl_sync(0xffffffffu, sv_now, 2 * (i & 15) + u);
         // (a block without a seen row may have any scale)
         if (!all && !mask.any_seen(u * 16, 16)) ks[u] = vs[u] = 0.f;
@@ -305,14 +312,14 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::CTAS)
           for (int e = 0; e < 4; ++e) s[u][nb][e] *= ks[u];
       if constexpr (MOD) {  // one branch for all of a lane's scores
         if (p.mod.cap_log2 > 0.f) {
-          if (p.mod.short_tanh) {
+          if (p.mod.short_scale != 0.f) {
 #pragma unroll
             for (int u = 0; u < 2; ++u)
 #pragma unroll
               for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                  s[u][nb][e] = p.mod.cap_log2 * tanh_short(s[u][nb][e]);
+                  s[u][nb][e] = capped_short(p.mod, s[u][nb][e]);
           } else {
 #pragma unroll
             for (int u = 0; u < 2; ++u)
@@ -325,14 +332,25 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::CTAS)
         }
         if (p.mod.slopes) {
           const RowDistance dist(it, mask.row0 + g);
+          if (slopes_up) {
 #pragma unroll
-          for (int u = 0; u < 2; ++u)
+            for (int u = 0; u < 2; ++u)
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
+              for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                s[u][nb][e] = biased(s[u][nb][e], RowDistance(dist, u * 16 + (e >> 1) * 8),
-                                     slope[nb][e & 1]);
+                for (int e = 0; e < 4; ++e)
+                  s[u][nb][e] = biased(s[u][nb][e], RowDistance(dist, u * 16 + (e >> 1) * 8),
+                                       slope[nb][e & 1], true);
+          } else {
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  s[u][nb][e] = biased(s[u][nb][e], RowDistance(dist, u * 16 + (e >> 1) * 8),
+                                       slope[nb][e & 1], false);
+          }
         }
       }
       if (!all) {

@@ -571,6 +571,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
     const int head0 = it.hc * NH;
     const size_t bh0 = size_t(it.b) * p.h_q + size_t(it.kvh) * p.group + head0;
     const int nheads = min(NH, p.group - head0);
+    [[maybe_unused]] bool slopes_up = false;
     if constexpr (MOD) {
       // the biases of this group's heads, read back by every thread of it (16
       // more registers a thread would spill)
@@ -579,6 +580,8 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
           slopes[hb + t_row] =
               head_slope(p, it.kvh * p.group + head0 + hb + t_row, hb + t_row < nheads);
         named_bar_sync(bar_id, 128);
+        const bool up = lane >= HT || slopes[hb + lane % HT] >= 0.f;
+        slopes_up = __all_sync(0xffffffffu, up);
       }
     }
     float m_run[HT], l_part[HT];
@@ -607,10 +610,9 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
         tc5::wait_ld();
       }
       if constexpr (MOD) {
-        if (p.mod.short_tanh && p.mod.cap_log2 > 0.f) {
+        if (p.mod.short_scale != 0.f) {
 #pragma unroll
-          for (int h = 0; h < HT; ++h)
-            s[h] = p.mod.cap_log2 * tanh_short(s[h] * p.scale_log2);
+          for (int h = 0; h < HT; ++h) s[h] = capped_short(p.mod, s[h] * p.mod.short_scale);
         } else if (p.mod.cap_log2 > 0.f) {
 #pragma unroll
           for (int h = 0; h < HT; ++h)
@@ -621,13 +623,24 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
         }
         if (p.mod.slopes) {
           const RowDistance dist(it, mask.row0 + t_row);
+          if (slopes_up) {
 #pragma unroll
-          for (int h = 0; h < HT; h += 4) {
-            const float4 f = *reinterpret_cast<const float4*>(slopes + hb + h);
-            s[h] = biased(s[h], dist, f.x);
-            s[h + 1] = biased(s[h + 1], dist, f.y);
-            s[h + 2] = biased(s[h + 2], dist, f.z);
-            s[h + 3] = biased(s[h + 3], dist, f.w);
+            for (int h = 0; h < HT; h += 4) {
+              const float4 f = *reinterpret_cast<const float4*>(slopes + hb + h);
+              s[h] = biased(s[h], dist, f.x, true);
+              s[h + 1] = biased(s[h + 1], dist, f.y, true);
+              s[h + 2] = biased(s[h + 2], dist, f.z, true);
+              s[h + 3] = biased(s[h + 3], dist, f.w, true);
+            }
+          } else {
+#pragma unroll
+            for (int h = 0; h < HT; h += 4) {
+              const float4 f = *reinterpret_cast<const float4*>(slopes + hb + h);
+              s[h] = biased(s[h], dist, f.x, false);
+              s[h + 1] = biased(s[h + 1], dist, f.y, false);
+              s[h + 2] = biased(s[h + 2], dist, f.z, false);
+              s[h + 3] = biased(s[h + 3], dist, f.w, false);
+            }
           }
         }
 #pragma unroll
