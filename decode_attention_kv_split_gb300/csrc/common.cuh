@@ -446,6 +446,16 @@ struct Item {
 // tile lies on one side of pt, so its cache rows are consecutive, and the rows
 // of a tile that the query does not see are masked one by one.
 // ---------------------------------------------------------------------------
+// Kernels are compiled for sets of terms (bits): a masked-only call then pays
+// for no test of the others (the 32-head kernel lost 0.1 us a stage to them).
+constexpr int kTermsMask = 1;    // the row mapping and the mask: with any term
+constexpr int kTermsCap = 2;
+constexpr int kTermsSlopes = 4;
+// Host: the set of a call's terms.
+inline int terms_of(const ScoreTerms& m) {
+  return m.on ? kTermsMask | (m.cap_log2 > 0.f ? kTermsCap : 0) | (m.slopes ? kTermsSlopes : 0) : 0;
+}
+
 struct ItemRows {
   int prefix, first;  // visible: l < prefix or l >= first (first = 0 when all are)
   int pt, shift;      // list row v >= pt is cache row v + shift

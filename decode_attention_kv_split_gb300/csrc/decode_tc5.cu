@@ -185,13 +185,9 @@ namespace tc5 {
 // its largest scores first, where upwards every stage would exceed the lazy
 // running maximum and rescale O (MQA, 8 x 32768 rows: 47.8 us a step upwards,
 // against 34.4 without biases).
-template <int T>
-__device__ __forceinline__ int stage_row(const SplitParams&, const ItemT<false>& it, int t) {
-  return it.row_begin + t * T;
-}
-template <int T>
-__device__ __forceinline__ int stage_row(const SplitParams& p, const ItemT<true>& it, int t) {
-  return it.row_begin + (p.mod.slopes ? it.tiles - 1 - t : t) * T;
+template <int T, bool LAST_FIRST>
+__device__ __forceinline__ int stage_row(const Item& it, int t) {
+  return it.row_begin + (LAST_FIRST ? it.tiles - 1 - t : t) * T;
 }
 }  // namespace tc5
 
@@ -199,7 +195,7 @@ __device__ __forceinline__ int stage_row(const SplitParams& p, const ItemT<true>
 // items, in order, into slot (stage % NSLOT).  Each load completes on the
 // slot's full barrier; the slot is refilled after its empty barrier (an MMA
 // commit).  The appended row of a unit rides with the tile that holds it.
-template <int T, int NSLOT, int TILE_BYTES, int HALF_BYTES, int ROW_BYTES, bool MOD>
+template <int T, int NSLOT, int TILE_BYTES, int HALF_BYTES, int ROW_BYTES, bool MOD, bool SLOPES>
 __device__ __forceinline__ void produce_ring(const CUtensorMap* map, const void* new_rows,
                                              const SplitParams& p, const Schedule& s,
                                              uint32_t slots, uint32_t newslots, uint32_t full0,
@@ -228,7 +224,7 @@ __device__ __forceinline__ void produce_ring(const CUtensorMap* map, const void*
         continue;
       }
       const uint32_t bar = full0 + 8 * slot;
-      const int y0 = tc5::stage_row<T>(p, it, t);
+      const int y0 = tc5::stage_row<T, SLOPES>(it, t);
       const bool with_new = it.new_row >= y0 && it.new_row < y0 + T;
       mbar_arrive_expect_tx(bar, TILE_BYTES + (with_new ? ROW_BYTES : 0));
       const uint32_t dst = slots + slot * TILE_BYTES;
@@ -255,10 +251,12 @@ __device__ __forceinline__ void produce_ring(const CUtensorMap* map, const void*
   }
 }
 
-template <class Cfg, bool MOD>
+template <class Cfg, int TERMS>
 __global__ void __launch_bounds__(Cfg::kThreads, 1)
     split_decode_tc5_kernel(const __grid_constant__ CUtensorMap tmK,
                             const __grid_constant__ CUtensorMap tmV, const SplitParams p) {
+  constexpr bool MOD = TERMS != 0, CAP = (TERMS & kTermsCap) != 0,
+                 SLOPES = (TERMS & kTermsSlopes) != 0;
   constexpr int NH = Cfg::NH, KST = Cfg::KST, VST = Cfg::VST, D = Cfg::D, T = Cfg::kTile;
   // TMEM: S[2] (NH columns each), then O^T as two accumulation chains (even
   // and odd 16-row blocks of a stage), each 2 NH columns (head | remainder).
@@ -337,18 +335,20 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
   tc5::fence_after();
   allow_dependent_launch();
   if (threadIdx.x == 0 && sched.mine > 0)
-    write_hint<T, MOD>(p, cta_item<T, MOD>(p, sched, 0), KST, MOD && p.mod.slopes);
+    write_hint<T, MOD>(p, cta_item<T, MOD>(p, sched, 0), KST, SLOPES);
   const uint32_t tmem = *tmem_slot;
   const uint32_t s_col0 = tmem, o_col = tmem + 2 * NH;  // chain c at o_col + c * 2 NH
 
   // ------------------------------------------------------------------ producers
   if (warp == 8) {
     if (lane == 0)
-      produce_ring<T, KST, Cfg::kTileBytes, Cfg::kHalfBytes, Cfg::kRowBytes, MOD>(
+      produce_ring<T, KST, Cfg::kTileBytes, Cfg::kHalfBytes, Cfg::kRowBytes, MOD,
+                   SLOPES>(
           &tmK, p.k_new, p, sched, smem_u32(kslots), smem_u32(knew), kfull0, kempty0, abort_flag,
           true);
     else if (lane == 1)
-      produce_ring<T, VST, Cfg::kTileBytes, Cfg::kHalfBytes, Cfg::kRowBytes, MOD>(
+      produce_ring<T, VST, Cfg::kTileBytes, Cfg::kHalfBytes, Cfg::kRowBytes, MOD,
+                   SLOPES>(
           &tmV, p.v_new, p, sched, smem_u32(vslots), smem_u32(vnew), vfull0, vempty0, abort_flag,
           false);
     return;
@@ -414,7 +414,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
           // S buffer j % 2 is free once the softmax warps have read stage j - 2
           if (j >= 2 && !warp_wait(p_full0 + 8 * (j & 1), ((j - 2) >> 1) & 1)) break;
           if (!warp_wait(kfull0 + 8 * kslot, kphase)) break;
-          const int row0 = tc5::stage_row<T>(p, it, t);
+          const int row0 = tc5::stage_row<T, SLOPES>(it, t);
           const int new_local =
               (it.new_row >= row0 && it.new_row < row0 + T) ? it.new_row - row0 : -1;
           uint8_t* kt = kslots + size_t(kslot) * Cfg::kTileBytes;
@@ -467,7 +467,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
           if (!warp_wait(p_full0 + 8 * b, (j >> 1) & 1)) break;
           if (!warp_wait(vfull0 + 8 * vslot, vphase)) break;
           uint8_t* vt = vslots + size_t(vslot) * Cfg::kTileBytes;
-          const int row0 = tc5::stage_row<T>(p, it, t);
+          const int row0 = tc5::stage_row<T, SLOPES>(it, t);
           const int valid = min(T, it.row_end - row0);
           if constexpr (MOD) {  // rows past the end or not seen may hold anything, even NaN
             const TileMask<MOD> mask(it, row0, valid);
@@ -566,23 +566,34 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
     }
     tc5::fence_after();
   };
+  // Rescale this thread's row of O^T (column d = t_row): 2 chains x 2 halves.
+  auto rescale_o = [&](const float (&alpha)[HT]) {
+#pragma unroll
+    for (int part = 0; part < 4; ++part) {
+      float o[HT];
+      tc5::ld16x(o_col + part * NH + hb + lane_base, o, HT);
+      tc5::wait_ld();
+#pragma unroll
+      for (int u = 0; u < HT; ++u) o[u] *= alpha[u];
+      tc5::st16x(o_col + part * NH + hb + lane_base, o, HT);
+    }
+    tc5::wait_st();
+  };
   for (int k = 0; k < sched.mine; ++k) {
     const ItemT<MOD> it = cta_item<T, MOD>(p, sched, k);
     const int head0 = it.hc * NH;
     const size_t bh0 = size_t(it.b) * p.h_q + size_t(it.kvh) * p.group + head0;
     const int nheads = min(NH, p.group - head0);
     [[maybe_unused]] bool slopes_up = false;
-    if constexpr (MOD) {
+    if constexpr (SLOPES) {
       // the biases of this group's heads, read back by every thread of it (16
       // more registers a thread would spill)
-      if (p.mod.slopes) {
-        if (t_row < HT)
-          slopes[hb + t_row] =
-              head_slope(p, it.kvh * p.group + head0 + hb + t_row, hb + t_row < nheads);
-        named_bar_sync(bar_id, 128);
-        const bool up = lane >= HT || slopes[hb + lane % HT] >= 0.f;
-        slopes_up = __all_sync(0xffffffffu, up);
-      }
+      if (t_row < HT)
+        slopes[hb + t_row] =
+            head_slope(p, it.kvh * p.group + head0 + hb + t_row, hb + t_row < nheads);
+      named_bar_sync(bar_id, 128);
+      const bool up = lane >= HT || slopes[hb + lane % HT] >= 0.f;
+      slopes_up = __all_sync(0xffffffffu, up);
     }
     float m_run[HT], l_part[HT];
 #pragma unroll
@@ -600,7 +611,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
       tc5::fence_after();
       // warp-uniform: the TMEM loads below are .sync.aligned
       const bool live = __all_sync(0xffffffffu, !*abort_flag);
-      const int row0 = tc5::stage_row<T>(p, it, t);
+      const int row0 = tc5::stage_row<T, SLOPES>(it, t);
       const int valid = min(T, it.row_end - row0);
       const TileMask<MOD> mask(it, row0, valid);
       const bool row_ok = mask.seen(t_row);
@@ -609,46 +620,40 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
         tc5::ld16x(s_col0 + (j & 1) * NH + hb + lane_base, s, HT);
         tc5::wait_ld();
       }
-      if constexpr (MOD) {
+      if constexpr (CAP) {
         if (p.mod.short_scale != 0.f) {
 #pragma unroll
           for (int h = 0; h < HT; ++h) s[h] = capped_short(p.mod, s[h] * p.mod.short_scale);
-        } else if (p.mod.cap_log2 > 0.f) {
-#pragma unroll
-          for (int h = 0; h < HT; ++h)
-            s[h] = p.mod.cap_log2 * tanh_fast(s[h] * p.scale_log2);
         } else {
 #pragma unroll
-          for (int h = 0; h < HT; ++h) s[h] *= p.scale_log2;
+          for (int h = 0; h < HT; ++h) s[h] = p.mod.cap_log2 * tanh_fast(s[h] * p.scale_log2);
         }
-        if (p.mod.slopes) {
-          const RowDistance dist(it, mask.row0 + t_row);
-          if (slopes_up) {
+      }
+      if constexpr (SLOPES) {
+        const RowDistance dist(it, mask.row0 + t_row);
+        if (slopes_up) {
 #pragma unroll
-            for (int h = 0; h < HT; h += 4) {
-              const float4 f = *reinterpret_cast<const float4*>(slopes + hb + h);
-              s[h] = biased(s[h], dist, f.x, true);
-              s[h + 1] = biased(s[h + 1], dist, f.y, true);
-              s[h + 2] = biased(s[h + 2], dist, f.z, true);
-              s[h + 3] = biased(s[h + 3], dist, f.w, true);
-            }
-          } else {
+          for (int h = 0; h < HT; h += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(slopes + hb + h);
+            s[h] = biased(CAP ? s[h] : s[h] * p.scale_log2, dist, f.x, true);
+            s[h + 1] = biased(CAP ? s[h + 1] : s[h + 1] * p.scale_log2, dist, f.y, true);
+            s[h + 2] = biased(CAP ? s[h + 2] : s[h + 2] * p.scale_log2, dist, f.z, true);
+            s[h + 3] = biased(CAP ? s[h + 3] : s[h + 3] * p.scale_log2, dist, f.w, true);
+          }
+        } else {
 #pragma unroll
-            for (int h = 0; h < HT; h += 4) {
-              const float4 f = *reinterpret_cast<const float4*>(slopes + hb + h);
-              s[h] = biased(s[h], dist, f.x, false);
-              s[h + 1] = biased(s[h + 1], dist, f.y, false);
-              s[h + 2] = biased(s[h + 2], dist, f.z, false);
-              s[h + 3] = biased(s[h + 3], dist, f.w, false);
-            }
+          for (int h = 0; h < HT; h += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(slopes + hb + h);
+            s[h] = biased(CAP ? s[h] : s[h] * p.scale_log2, dist, f.x, false);
+            s[h + 1] = biased(CAP ? s[h + 1] : s[h + 1] * p.scale_log2, dist, f.y, false);
+            s[h + 2] = biased(CAP ? s[h + 2] : s[h + 2] * p.scale_log2, dist, f.z, false);
+            s[h + 3] = biased(CAP ? s[h + 3] : s[h + 3] * p.scale_log2, dist, f.w, false);
           }
         }
-#pragma unroll
-        for (int h = 0; h < HT; ++h) s[h] = (live && row_ok) ? s[h] : -INFINITY;
-      } else {
-#pragma unroll
-        for (int h = 0; h < HT; ++h) s[h] = (live && row_ok) ? s[h] * p.scale_log2 : -INFINITY;
       }
+#pragma unroll
+      for (int h = 0; h < HT; ++h)
+        s[h] = (live && row_ok) ? (CAP || SLOPES ? s[h] : s[h] * p.scale_log2) : -INFINITY;
 
       // Running max: exact on an item's first stage, else only when some score
       // exceeds it by more than 2^8 (a vote; the exponentials stay <= 2^8).
@@ -688,31 +693,28 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
           alpha[h] = (m_run[h] == -INFINITY) ? 0.f : ex2(m_run[h] - m_new);
           m_run[h] = m_new;
         }
+        if (MOD) {  // rescale here: 16 registers less through the rest of the stage
+#pragma unroll
+          for (int h = 0; h < HT; ++h) l_part[h] *= alpha[h];
+          if (t > 0) {
+            wait_pv(j - 1);
+            if (live) rescale_o(alpha);
+          }
+        }
       }
 #pragma unroll
       for (int h = 0; h < HT; ++h) {
         const float m_use = m_run[h] == -INFINITY ? 0.f : m_run[h];
         s[h] = ex2(s[h] - m_use);  // 0 for masked rows
-        l_part[h] = l_part[h] * alpha[h] + s[h];
+        l_part[h] = MOD ? l_part[h] + s[h] : l_part[h] * alpha[h] + s[h];
       }
       // P buffer j % 2 is free once the P.V of stage j - 2 has completed; O may
       // be rescaled once the P.V of stage j - 1 has.  (Each pv_done barrier
       // completes once per use of its buffer, so neither wait can be lapped.)
       if (j >= 2) wait_pv(j - 2);
-      if (exact && t > 0) {
+      if (!MOD && exact && t > 0) {
         wait_pv(j - 1);
-        if (live) {  // rescale this thread's row of O^T (column d = t_row): 2 chains x 2 halves
-#pragma unroll
-          for (int part = 0; part < 4; ++part) {
-            float o[HT];
-            tc5::ld16x(o_col + part * NH + hb + lane_base, o, HT);
-            tc5::wait_ld();
-#pragma unroll
-            for (int u = 0; u < HT; ++u) o[u] *= alpha[u];
-            tc5::st16x(o_col + part * NH + hb + lane_base, o, HT);
-          }
-          tc5::wait_st();
-        }
+        if (live) rescale_o(alpha);
       }
       // P^T (heads x stage rows), K-major over the rows: bf16 head + remainder
       uint8_t* pb = p_buf + (j & 1) * Cfg::kPBytes;
@@ -823,22 +825,27 @@ KernelShape tc5_shape(int group) {
   return KernelShape{Tc5G32::kTile, 32, 64, 1, 0.7f};
 }
 
-template <class Cfg, bool MOD>
-static cudaError_t launch_tc5_mod(const SplitParams& p, const CUtensorMap& tk,
-                                  const CUtensorMap& tv, int grid, cudaStream_t stream) {
+template <class Cfg, int TERMS>
+static cudaError_t launch_tc5_terms(const SplitParams& p, const CUtensorMap& tk,
+                                    const CUtensorMap& tv, int grid, cudaStream_t stream) {
   static std::atomic<unsigned long long> smem_set{0};
   const cudaError_t e =
-      set_smem_limit_once(split_decode_tc5_kernel<Cfg, MOD>, Cfg::kSmemBytes, smem_set);
+      set_smem_limit_once(split_decode_tc5_kernel<Cfg, TERMS>, Cfg::kSmemBytes, smem_set);
   if (e != cudaSuccess) return e;
-  return launch_dependent(split_decode_tc5_kernel<Cfg, MOD>, grid, Cfg::kThreads,
+  return launch_dependent(split_decode_tc5_kernel<Cfg, TERMS>, grid, Cfg::kThreads,
                           Cfg::kSmemBytes, stream, tk, tv, p);
 }
 
 template <class Cfg>
 static cudaError_t launch_tc5_cfg(const SplitParams& p, const CUtensorMap& tk,
                                   const CUtensorMap& tv, int grid, cudaStream_t stream) {
-  return p.mod.on ? launch_tc5_mod<Cfg, true>(p, tk, tv, grid, stream)
-                  : launch_tc5_mod<Cfg, false>(p, tk, tv, grid, stream);
+  switch (terms_of(p.mod)) {
+    case 0: return launch_tc5_terms<Cfg, 0>(p, tk, tv, grid, stream);
+    case 1: return launch_tc5_terms<Cfg, 1>(p, tk, tv, grid, stream);
+    case 3: return launch_tc5_terms<Cfg, 3>(p, tk, tv, grid, stream);
+    case 5: return launch_tc5_terms<Cfg, 5>(p, tk, tv, grid, stream);
+    default: return launch_tc5_terms<Cfg, 7>(p, tk, tv, grid, stream);
+  }
 }
 
 cudaError_t launch_split_tc5(const SplitParams& p, const CUtensorMap& tk, const CUtensorMap& tv,
