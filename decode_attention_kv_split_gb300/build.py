@@ -1,6 +1,7 @@
 """Build libdecode_attn.so in-tree with nvcc (sm_103a only).
 
 Each .cu file under csrc/ is compiled in parallel into csrc/../_build/*.o
+(those of TERM_SOURCES once for each set of score terms, -DDA_TERMS=set)
 and linked into decode_attention_kv_split_gb300/libdecode_attn.so.  Objects
 are rebuilt when their source or any header is newer.  Run as
 ``python -m decode_attention_kv_split_gb300.build``.
@@ -25,6 +26,11 @@ INCLUDE = os.path.join(ROOT, "include")
 # and reported as DA_DEVERR_BOUNDS).  Only the tests load it.
 BUILD_TEST = os.path.join(PKG, "_build_test")
 LIB_TEST = os.path.join(PKG, "libdecode_attn_test.so")
+
+# Sources of split kernels with score terms, and the sets of terms (bits: 1 the
+# mask, with any term; 2 capped scores; 4 distance biases).
+TERM_SOURCES = {"decode_bf16.cu", "decode_fp32.cu", "decode_tc5.cu", "decode_q8b.cu"}
+TERM_SETS = (0, 1, 3, 5, 7)
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -57,12 +63,15 @@ def build(verbose: bool = False, ptxas_info: bool = False, test_hooks: bool = Fa
     nvcc = _nvcc()
     jobs = []
     objects = []
-    for src in sources:
-        obj = os.path.join(build_dir, os.path.basename(src)[:-3] + ".o")
+    units = [(src, terms) for src in sources
+             for terms in (TERM_SETS if os.path.basename(src) in TERM_SOURCES else (None,))]
+    for src, terms in units:
+        name = os.path.basename(src)[:-3] + ("" if terms is None else f".terms{terms}")
+        obj = os.path.join(build_dir, name + ".o")
         objects.append(obj)
         if ptxas_info or _stale(obj, [src, *headers]):
-            cmd = [nvcc, *ARCH, *NVCC_FLAGS, *(["-DDA_TEST_HOOKS", "-DDA_BOUNDS_CHECK"] if test_hooks else []), "-c",
-                   src, "-o", obj]
+            cmd = [nvcc, *ARCH, *NVCC_FLAGS, *(["-DDA_TEST_HOOKS", "-DDA_BOUNDS_CHECK"] if test_hooks else []),
+                   *([] if terms is None else [f"-DDA_TERMS={terms}"]), "-c", src, "-o", obj]
             if ptxas_info:
                 cmd.insert(1, "-Xptxas=-v")
             jobs.append(cmd)

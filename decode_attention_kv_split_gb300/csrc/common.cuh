@@ -446,21 +446,46 @@ struct Item {
 // tile lies on one side of pt, so its cache rows are consecutive, and the rows
 // of a tile that the query does not see are masked one by one.
 // ---------------------------------------------------------------------------
-// Kernels are compiled for sets of terms (bits): a masked-only call then pays
-// for no test of the others (the 32-head kernel lost 0.1 us a stage to them).
-constexpr int kTermsMask = 1;    // the row mapping and the mask: with any term
-constexpr int kTermsCap = 2;
-constexpr int kTermsSlopes = 4;
-// Host: the set of a call's terms.
-inline int terms_of(const ScoreTerms& m) {
-  return m.on ? kTermsMask | (m.cap_log2 > 0.f ? kTermsCap : 0) | (m.slopes ? kTermsSlopes : 0) : 0;
-}
-
 struct ItemRows {
   int prefix, first;  // visible: l < prefix or l >= first (first = 0 when all are)
   int pt, shift;      // list row v >= pt is cache row v + shift
   int lo, hi;         // first and last visible row: where a distance bias is zero
 };
+
+// Kernels are compiled for sets of terms (bits), each split-kernel source once
+// per set (DA_TERMS, see build.py): tests of the terms inside a stage keep the
+// compiler from moving loads and MMAs across them, which cost the 4-head bf16
+// kernel 0.38 of 0.63 us a stage.
+constexpr int kTermsMask = 1;    // the row mapping and the mask: with any term
+constexpr int kTermsCap = 2;
+constexpr int kTermsSlopes = 4;
+#ifndef DA_TERMS
+#define DA_TERMS 0
+#endif
+// Host: the set of a call's terms.
+inline int terms_of(const ScoreTerms& m) {
+  return m.on ? kTermsMask | (m.cap_log2 > 0.f ? kTermsCap : 0) | (m.slopes ? kTermsSlopes : 0) : 0;
+}
+
+// Host: the launchers of all sets (each object defines its own), and the call of
+// the one for a call's set.
+#define DA_DECLARE_SETS(launch_T, params) \
+  template <>                             \
+  cudaError_t launch_T<0> params;         \
+  template <>                             \
+  cudaError_t launch_T<1> params;         \
+  template <>                             \
+  cudaError_t launch_T<3> params;         \
+  template <>                             \
+  cudaError_t launch_T<5> params;         \
+  template <>                             \
+  cudaError_t launch_T<7> params;
+#define DA_LAUNCH_TERMS(launch_T, terms, ...)                          \
+  ((terms) == 0   ? launch_T<0>(__VA_ARGS__)                           \
+   : (terms) == 1 ? launch_T<1>(__VA_ARGS__)                           \
+   : (terms) == 3 ? launch_T<3>(__VA_ARGS__)                           \
+   : (terms) == 5 ? launch_T<5>(__VA_ARGS__)                           \
+                  : launch_T<7>(__VA_ARGS__))
 
 template <bool MOD>
 struct ItemT : Item {};

@@ -72,10 +72,12 @@ __device__ __forceinline__ uint32_t swz(int row, int col) {
   return uint32_t(half * Cfg::kHalfBytes + row * 128 + ((chunk ^ (row & 7)) << 4));
 }
 
-template <class Cfg, bool MOD>
+template <class Cfg, int TERMS>
 __global__ void __launch_bounds__(Cfg::kThreads, 1)
     split_decode_bf16_kernel(const __grid_constant__ CUtensorMap tmK,
                              const __grid_constant__ CUtensorMap tmV, const SplitParams p) {
+  constexpr bool MOD = TERMS != 0, CAP = (TERMS & kTermsCap) != 0,
+                 SLOPES = (TERMS & kTermsSlopes) != 0;
   constexpr int DK = Cfg::DK, DV = Cfg::DV, NB = Cfg::NB, KW = Cfg::KW, KBW = Cfg::KBW,
                 STAGES = Cfg::STAGES;
   constexpr int kHPW = Cfg::kHPW;
@@ -157,7 +159,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
     uint32_t qf[NB][MBK][2];
 
     [[maybe_unused]] float slope[NB][2];
-    if constexpr (MOD) {
+    if constexpr (SLOPES) {
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -268,7 +270,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
           seen[kb][0] = all || mask.seen(key0 + kb * 16 + r);
           seen[kb][1] = all || mask.seen(key0 + kb * 16 + r + 8);
         }
-        if constexpr (MOD) {  // score terms (one branch for all of a lane's scores)
+        if constexpr (CAP) {
           if (p.mod.short_scale != 0.f) {
 #pragma unroll
             for (int kb = 0; kb < KBW; ++kb)
@@ -277,7 +279,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                   s[kb][nb][e] = capped_short(p.mod, s[kb][nb][e] * p.mod.short_scale);
-          } else if (p.mod.cap_log2 > 0.f) {
+          } else {
 #pragma unroll
             for (int kb = 0; kb < KBW; ++kb)
 #pragma unroll
@@ -285,25 +287,19 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                   s[kb][nb][e] = p.mod.cap_log2 * tanh_fast(s[kb][nb][e] * p.scale_log2);
-          } else {
-#pragma unroll
-            for (int kb = 0; kb < KBW; ++kb)
-#pragma unroll
-              for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) s[kb][nb][e] *= p.scale_log2;
           }
-          if (p.mod.slopes) {
-            const RowDistance dist(it, mask.row0 + key0 + r);
+        }
+        if constexpr (SLOPES) {
+          const RowDistance dist(it, mask.row0 + key0 + r);
 #pragma unroll
-            for (int kb = 0; kb < KBW; ++kb)
+          for (int kb = 0; kb < KBW; ++kb)
 #pragma unroll
-              for (int nb = 0; nb < NB; ++nb)
+            for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  s[kb][nb][e] = biased(s[kb][nb][e], RowDistance(dist, kb * 16 + (e >> 1) * 8),
-                                        slope[nb][e & 1], false);
-          }
+              for (int e = 0; e < 4; ++e)
+                s[kb][nb][e] = biased(CAP ? s[kb][nb][e] : s[kb][nb][e] * p.scale_log2,
+                                      RowDistance(dist, kb * 16 + (e >> 1) * 8),
+                                      slope[nb][e & 1], false);
         }
         float alpha[NB][2];
         bool changed = false;
@@ -314,7 +310,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
             float mx = -INFINITY;
 #pragma unroll
             for (int kb = 0; kb < KBW; ++kb) {
-              if constexpr (!MOD) {
+              if constexpr (!CAP && !SLOPES) {
                 s[kb][nb][j] *= p.scale_log2;
                 s[kb][nb][j + 2] *= p.scale_log2;
               }
@@ -455,6 +451,35 @@ using Bf16G8D256 = Bf16Cfg<256, 256, 1, 1, 4, 1, 2>;   // 64-row stages of 64 KB
 using Bf16G8D192V128 = Bf16Cfg<192, 128, 1, 1, 4, 1, 3>;
 
 template <class Cfg>
+static cudaError_t launch_cfg(const SplitParams& p, const CUtensorMap& tk, const CUtensorMap& tv,
+                              int grid, cudaStream_t stream) {
+  static std::atomic<unsigned long long> smem_set{0};
+  const cudaError_t e =
+      set_smem_limit_once(split_decode_bf16_kernel<Cfg, DA_TERMS>, Cfg::kSmemBytes, smem_set);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(split_decode_bf16_kernel<Cfg, DA_TERMS>, grid, Cfg::kThreads,
+                          Cfg::kSmemBytes, stream, tk, tv, p);
+}
+
+// This object's set of terms (DA_TERMS); the dispatch is in the object of set 0.
+template <int TERMS>
+cudaError_t launch_bf16_set(const SplitParams& p, const CUtensorMap& tk, const CUtensorMap& tv,
+                            int d_k, int d_v, int grid, cudaStream_t stream);
+DA_DECLARE_SETS(launch_bf16_set, (const SplitParams&, const CUtensorMap&, const CUtensorMap&, int, int, int, cudaStream_t))
+template <>
+cudaError_t launch_bf16_set<DA_TERMS>(const SplitParams& p, const CUtensorMap& tk,
+                                      const CUtensorMap& tv, int d_k, int d_v, int grid,
+                                      cudaStream_t stream) {
+  if (d_k == 256) return launch_cfg<Bf16G8D256>(p, tk, tv, grid, stream);
+  if (d_k == 192) return launch_cfg<Bf16G8D192V128>(p, tk, tv, grid, stream);
+  if (d_k == 128) return launch_cfg<Bf16G8D128>(p, tk, tv, grid, stream);
+  if (p.group <= 8) return launch_cfg<Bf16G8D64>(p, tk, tv, grid, stream);
+  if (p.group <= 16) return launch_cfg<Bf16G16D64>(p, tk, tv, grid, stream);
+  return launch_cfg<Bf16G32D64>(p, tk, tv, grid, stream);
+}
+
+#if DA_TERMS == 0
+template <class Cfg>
 static KernelShape shape_of() {
   return KernelShape{Cfg::kTile, Cfg::kHeadsPerCta, 64, 1, 1.5f};
 }
@@ -470,32 +495,10 @@ KernelShape bf16_shape(int d_k, int d_v, int group) {
   return shape_of<Bf16G32D64>();
 }
 
-template <class Cfg, bool MOD>
-static cudaError_t launch_cfg_mod(const SplitParams& p, const CUtensorMap& tk,
-                                  const CUtensorMap& tv, int grid, cudaStream_t stream) {
-  static std::atomic<unsigned long long> smem_set{0};
-  const cudaError_t e =
-      set_smem_limit_once(split_decode_bf16_kernel<Cfg, MOD>, Cfg::kSmemBytes, smem_set);
-  if (e != cudaSuccess) return e;
-  return launch_dependent(split_decode_bf16_kernel<Cfg, MOD>, grid, Cfg::kThreads,
-                          Cfg::kSmemBytes, stream, tk, tv, p);
-}
-
-template <class Cfg>
-static cudaError_t launch_cfg(const SplitParams& p, const CUtensorMap& tk, const CUtensorMap& tv,
-                              int grid, cudaStream_t stream) {
-  return p.mod.on ? launch_cfg_mod<Cfg, true>(p, tk, tv, grid, stream)
-                  : launch_cfg_mod<Cfg, false>(p, tk, tv, grid, stream);
-}
-
 cudaError_t launch_split_bf16(const SplitParams& p, const CUtensorMap& tk, const CUtensorMap& tv,
                               int d_k, int d_v, int grid, cudaStream_t stream) {
-  if (d_k == 256) return launch_cfg<Bf16G8D256>(p, tk, tv, grid, stream);
-  if (d_k == 192) return launch_cfg<Bf16G8D192V128>(p, tk, tv, grid, stream);
-  if (d_k == 128) return launch_cfg<Bf16G8D128>(p, tk, tv, grid, stream);
-  if (p.group <= 8) return launch_cfg<Bf16G8D64>(p, tk, tv, grid, stream);
-  if (p.group <= 16) return launch_cfg<Bf16G16D64>(p, tk, tv, grid, stream);
-  return launch_cfg<Bf16G32D64>(p, tk, tv, grid, stream);
+  return DA_LAUNCH_TERMS(launch_bf16_set, terms_of(p.mod), p, tk, tv, d_k, d_v, grid, stream);
 }
+#endif
 
 }  // namespace da

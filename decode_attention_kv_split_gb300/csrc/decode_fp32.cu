@@ -57,12 +57,14 @@ __device__ __forceinline__ void load_lane(float (&v)[N], const float* p) {
   }
 }
 
-template <class Cfg, bool MOD>
+template <class Cfg, int TERMS>
 __global__ void __launch_bounds__(Cfg::kThreads, 1)
     split_decode_f32_kernel(const __grid_constant__ CUtensorMap tmK,
                             const __grid_constant__ CUtensorMap tmV, const SplitParams p) {
   constexpr int D = Cfg::D, G = Cfg::G, W = Cfg::W, STAGES = Cfg::STAGES, EPL = Cfg::kEPL;
   constexpr int RPW = Cfg::kRowsPerWarp;
+  constexpr bool MOD = TERMS != 0, CAP = (TERMS & kTermsCap) != 0,
+                 SLOPES = (TERMS & kTermsSlopes) != 0;
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -136,7 +138,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
     float qv[G][EPL];
 
     [[maybe_unused]] float slope[G];
-    if constexpr (MOD) {
+    if constexpr (SLOPES) {
 #pragma unroll
       for (int g = 0; g < G; ++g)
         slope[g] = head_slope(p, it.kvh * p.group + head_base + g, head_base + g < p.group);
@@ -222,6 +224,10 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
             s[g][rr] = x;
           }
         }
+        [[maybe_unused]] const auto dist = [&] {
+          if constexpr (SLOPES) return RowDistance(it, mask.row0 + row0);
+          else return 0;
+        }();
 #pragma unroll
         for (int g = 0; g < G; ++g)
 #pragma unroll
@@ -232,30 +238,10 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
             x += __shfl_xor_sync(0xffffffffu, x, 4);
             x += __shfl_xor_sync(0xffffffffu, x, 2);
             x += __shfl_xor_sync(0xffffffffu, x, 1);
-            s[g][rr] = MOD || (seen >> rr & 1u) ? x : -INFINITY;
+            if constexpr (CAP) x = p.mod.cap_log2 * tanh_fast(x);
+            if constexpr (SLOPES) x = biased(x, RowDistance(dist, rr), slope[g], false);
+            s[g][rr] = (seen >> rr & 1u) ? x : -INFINITY;
           }
-        if constexpr (MOD) {  // score terms (one branch for all of them), then the mask
-          if (p.mod.cap_log2 > 0.f) {
-#pragma unroll
-            for (int g = 0; g < G; ++g)
-#pragma unroll
-              for (int rr = 0; rr < RPW; ++rr)
-                s[g][rr] = p.mod.cap_log2 * tanh_fast(s[g][rr]);
-          }
-          if (p.mod.slopes) {
-            const RowDistance dist(it, mask.row0 + row0);
-#pragma unroll
-            for (int g = 0; g < G; ++g)
-#pragma unroll
-              for (int rr = 0; rr < RPW; ++rr)
-                s[g][rr] = biased(s[g][rr], RowDistance(dist, rr), slope[g], false);
-          }
-#pragma unroll
-          for (int g = 0; g < G; ++g)
-#pragma unroll
-            for (int rr = 0; rr < RPW; ++rr)
-              s[g][rr] = (seen >> rr & 1u) ? s[g][rr] : -INFINITY;
-        }
         // Step II: running max and sum (warp-uniform values).
         float alpha[G];
 #pragma unroll
@@ -330,6 +316,39 @@ template <int D>
 using F32G8 = F32Cfg<D, 8, 8, (D == 128 ? 32 : 64), 5>;
 
 template <class Cfg>
+static cudaError_t launch_f32_cfg(const SplitParams& p, const CUtensorMap& tk,
+                                  const CUtensorMap& tv, int grid, cudaStream_t stream) {
+  static std::atomic<unsigned long long> smem_set{0};
+  const cudaError_t e =
+      set_smem_limit_once(split_decode_f32_kernel<Cfg, DA_TERMS>, Cfg::kSmemBytes, smem_set);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(split_decode_f32_kernel<Cfg, DA_TERMS>, grid, Cfg::kThreads,
+                          Cfg::kSmemBytes, stream, tk, tv, p);
+}
+
+template <int D>
+static cudaError_t launch_f32_d(const SplitParams& p, const CUtensorMap& tk, const CUtensorMap& tv,
+                                int grid, cudaStream_t stream) {
+  if (p.group <= 1) return launch_f32_cfg<F32G1<D>>(p, tk, tv, grid, stream);
+  if (p.group <= 2) return launch_f32_cfg<F32G2<D>>(p, tk, tv, grid, stream);
+  if (p.group <= 4) return launch_f32_cfg<F32G4<D>>(p, tk, tv, grid, stream);
+  return launch_f32_cfg<F32G8<D>>(p, tk, tv, grid, stream);
+}
+
+// This object's set of terms (DA_TERMS); the dispatch is in the object of set 0.
+template <int TERMS>
+cudaError_t launch_f32_set(const SplitParams& p, const CUtensorMap& tk, const CUtensorMap& tv,
+                           int d, int grid, cudaStream_t stream);
+DA_DECLARE_SETS(launch_f32_set, (const SplitParams&, const CUtensorMap&, const CUtensorMap&, int, int, cudaStream_t))
+template <>
+cudaError_t launch_f32_set<DA_TERMS>(const SplitParams& p, const CUtensorMap& tk,
+                                     const CUtensorMap& tv, int d, int grid, cudaStream_t stream) {
+  return d == 128 ? launch_f32_d<128>(p, tk, tv, grid, stream)
+                  : launch_f32_d<64>(p, tk, tv, grid, stream);
+}
+
+#if DA_TERMS == 0
+template <class Cfg>
 static KernelShape f32_shape_of() {
   return KernelShape{Cfg::kTile, Cfg::G, Cfg::D, 0, 1.5f};
 }
@@ -346,37 +365,10 @@ KernelShape f32_shape(int d, int group) {
   return d == 128 ? f32_shape_d<128>(group) : f32_shape_d<64>(group);
 }
 
-template <class Cfg, bool MOD>
-static cudaError_t launch_f32_mod(const SplitParams& p, const CUtensorMap& tk,
-                                  const CUtensorMap& tv, int grid, cudaStream_t stream) {
-  static std::atomic<unsigned long long> smem_set{0};
-  const cudaError_t e =
-      set_smem_limit_once(split_decode_f32_kernel<Cfg, MOD>, Cfg::kSmemBytes, smem_set);
-  if (e != cudaSuccess) return e;
-  return launch_dependent(split_decode_f32_kernel<Cfg, MOD>, grid, Cfg::kThreads,
-                          Cfg::kSmemBytes, stream, tk, tv, p);
-}
-
-template <class Cfg>
-static cudaError_t launch_f32_cfg(const SplitParams& p, const CUtensorMap& tk, const CUtensorMap& tv,
-                                  int grid, cudaStream_t stream) {
-  return p.mod.on ? launch_f32_mod<Cfg, true>(p, tk, tv, grid, stream)
-                  : launch_f32_mod<Cfg, false>(p, tk, tv, grid, stream);
-}
-
-template <int D>
-static cudaError_t launch_f32_d(const SplitParams& p, const CUtensorMap& tk, const CUtensorMap& tv,
-                                int grid, cudaStream_t stream) {
-  if (p.group <= 1) return launch_f32_cfg<F32G1<D>>(p, tk, tv, grid, stream);
-  if (p.group <= 2) return launch_f32_cfg<F32G2<D>>(p, tk, tv, grid, stream);
-  if (p.group <= 4) return launch_f32_cfg<F32G4<D>>(p, tk, tv, grid, stream);
-  return launch_f32_cfg<F32G8<D>>(p, tk, tv, grid, stream);
-}
-
 cudaError_t launch_split_f32(const SplitParams& p, const CUtensorMap& tk, const CUtensorMap& tv,
                              int d, int grid, cudaStream_t stream) {
-  return d == 128 ? launch_f32_d<128>(p, tk, tv, grid, stream)
-                  : launch_f32_d<64>(p, tk, tv, grid, stream);
+  return DA_LAUNCH_TERMS(launch_f32_set, terms_of(p.mod), p, tk, tv, d, grid, stream);
 }
+#endif
 
 }  // namespace da

@@ -92,7 +92,7 @@ __device__ __forceinline__ int code_at(int row, int piece) {
                   : row * 64 + ((piece ^ ((row >> 1) & 3)) << 4);
 }
 
-template <class Cfg, bool MOD>
+template <class Cfg, int TERMS>
 __global__ void __launch_bounds__(Cfg::kThreads, Cfg::CTAS)
     split_decode_q8b_kernel(const __grid_constant__ CUtensorMap tmK,
                             const __grid_constant__ CUtensorMap tmV, const SplitParams p) {
@@ -102,6 +102,8 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::CTAS)
   constexpr int KV4 = D / 16 / 4;   // 16-byte pieces a lane reads of a K row
   constexpr int VW = D / 32;        // 4-byte words a lane reads of a V row
   constexpr int KIND = Cfg::KIND;
+  constexpr bool MOD = TERMS != 0, CAP = (TERMS & kTermsCap) != 0,
+                 SLOPES = (TERMS & kTermsSlopes) != 0;
   constexpr float kLazy = 8.f;      // log2 of how far a weight may exceed 1
 
   extern __shared__ uint8_t smem_raw[];
@@ -214,7 +216,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::CTAS)
     }
   }
   [[maybe_unused]] float slope[NB][2];
-  if constexpr (MOD) {
+  if constexpr (SLOPES) {
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -238,9 +240,9 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::CTAS)
   }
 
   const bool exact_p = p.out_bf16 == 0;  // P's fp16 remainder too
-  const float score_scale = MOD && p.mod.short_scale != 0.f ? p.mod.short_scale : p.scale_log2;
+  const float score_scale = CAP && p.mod.short_scale != 0.f ? p.mod.short_scale : p.scale_log2;
   [[maybe_unused]] bool slopes_up = true;
-  if constexpr (MOD) {
+  if constexpr (SLOPES) {
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) slopes_up &= slope[nb][0] >= 0.f && slope[nb][1] >= 0.f;
     slopes_up = __all_sync(0xffffffffu, slopes_up);
@@ -310,47 +312,44 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::CTAS)
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
           for (int e = 0; e < 4; ++e) s[u][nb][e] *= ks[u];
-      if constexpr (MOD) {  // one branch for all of a lane's scores
-        if (p.mod.cap_log2 > 0.f) {
-          if (p.mod.short_scale != 0.f) {
+      if constexpr (CAP) {
+        if (p.mod.short_scale != 0.f) {
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
+          for (int u = 0; u < 2; ++u)
 #pragma unroll
-              for (int nb = 0; nb < NB; ++nb)
+            for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  s[u][nb][e] = capped_short(p.mod, s[u][nb][e]);
-          } else {
+              for (int e = 0; e < 4; ++e) s[u][nb][e] = capped_short(p.mod, s[u][nb][e]);
+        } else {
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
+          for (int u = 0; u < 2; ++u)
 #pragma unroll
-              for (int nb = 0; nb < NB; ++nb)
+            for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  s[u][nb][e] = p.mod.cap_log2 * tanh_fast(s[u][nb][e]);
-          }
+              for (int e = 0; e < 4; ++e)
+                s[u][nb][e] = p.mod.cap_log2 * tanh_fast(s[u][nb][e]);
         }
-        if (p.mod.slopes) {
-          const RowDistance dist(it, mask.row0 + g);
-          if (slopes_up) {
+      }
+      if constexpr (SLOPES) {
+        const RowDistance dist(it, mask.row0 + g);
+        if (slopes_up) {
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
+          for (int u = 0; u < 2; ++u)
 #pragma unroll
-              for (int nb = 0; nb < NB; ++nb)
+            for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  s[u][nb][e] = biased(s[u][nb][e], RowDistance(dist, u * 16 + (e >> 1) * 8),
-                                       slope[nb][e & 1], true);
-          } else {
+              for (int e = 0; e < 4; ++e)
+                s[u][nb][e] = biased(s[u][nb][e], RowDistance(dist, u * 16 + (e >> 1) * 8),
+                                     slope[nb][e & 1], true);
+        } else {
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
+          for (int u = 0; u < 2; ++u)
 #pragma unroll
-              for (int nb = 0; nb < NB; ++nb)
+            for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  s[u][nb][e] = biased(s[u][nb][e], RowDistance(dist, u * 16 + (e >> 1) * 8),
-                                       slope[nb][e & 1], false);
-          }
+              for (int e = 0; e < 4; ++e)
+                s[u][nb][e] = biased(s[u][nb][e], RowDistance(dist, u * 16 + (e >> 1) * 8),
+                                     slope[nb][e & 1], false);
         }
       }
       if (!all) {
@@ -544,28 +543,15 @@ using Q8BD64N1 = Q8BCfg<64, 1, 3, 4, KIND>;
 template <int KIND>
 using Q8BD64N2 = Q8BCfg<64, 2, 4, 3, KIND>;
 
-KernelShape q8b_shape(int d, int group) {
-  const bool one = group <= 8;
-  const int ctas = d == 64 && one ? 4 : 3;
-  return KernelShape{32, one ? 8 : 16, d, d == 128 ? 1 : 2, float(ctas)};
-}
-
-template <class Cfg, bool MOD>
-static cudaError_t launch_q8b_mod(const SplitParams& p, const CUtensorMap& tk,
-                                  const CUtensorMap& tv, int grid, cudaStream_t stream) {
-  static std::atomic<unsigned long long> smem_set{0};
-  const cudaError_t e =
-      set_smem_limit_once(split_decode_q8b_kernel<Cfg, MOD>, Cfg::kSmemBytes, smem_set);
-  if (e != cudaSuccess) return e;
-  return launch_dependent(split_decode_q8b_kernel<Cfg, MOD>, grid, Cfg::kThreads,
-                          Cfg::kSmemBytes, stream, tk, tv, p);
-}
-
 template <class Cfg>
 static cudaError_t launch_q8b_cfg(const SplitParams& p, const CUtensorMap& tk,
                                   const CUtensorMap& tv, int grid, cudaStream_t stream) {
-  return p.mod.on ? launch_q8b_mod<Cfg, true>(p, tk, tv, grid, stream)
-                  : launch_q8b_mod<Cfg, false>(p, tk, tv, grid, stream);
+  static std::atomic<unsigned long long> smem_set{0};
+  const cudaError_t e =
+      set_smem_limit_once(split_decode_q8b_kernel<Cfg, DA_TERMS>, Cfg::kSmemBytes, smem_set);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(split_decode_q8b_kernel<Cfg, DA_TERMS>, grid, Cfg::kThreads,
+                          Cfg::kSmemBytes, stream, tk, tv, p);
 }
 
 template <int KIND>
@@ -578,10 +564,30 @@ static cudaError_t launch_q8b_kind(const SplitParams& p, const CUtensorMap& tk,
                       : launch_q8b_cfg<Q8BD64N2<KIND>>(p, tk, tv, grid, stream);
 }
 
-cudaError_t launch_split_q8b(const SplitParams& p, const CUtensorMap& tk, const CUtensorMap& tv,
-                             int d, int kind, int grid, cudaStream_t stream) {
+// This object's set of terms (DA_TERMS); the dispatch is in the object of set 0.
+template <int TERMS>
+cudaError_t launch_q8b_set(const SplitParams& p, const CUtensorMap& tk, const CUtensorMap& tv,
+                           int d, int kind, int grid, cudaStream_t stream);
+DA_DECLARE_SETS(launch_q8b_set, (const SplitParams&, const CUtensorMap&, const CUtensorMap&, int, int, int, cudaStream_t))
+template <>
+cudaError_t launch_q8b_set<DA_TERMS>(const SplitParams& p, const CUtensorMap& tk,
+                                     const CUtensorMap& tv, int d, int kind, int grid,
+                                     cudaStream_t stream) {
   return kind == 1 ? launch_q8b_kind<1>(p, tk, tv, d, grid, stream)
                    : launch_q8b_kind<2>(p, tk, tv, d, grid, stream);
 }
+
+#if DA_TERMS == 0
+KernelShape q8b_shape(int d, int group) {
+  const bool one = group <= 8;
+  const int ctas = d == 64 && one ? 4 : 3;
+  return KernelShape{32, one ? 8 : 16, d, d == 128 ? 1 : 2, float(ctas)};
+}
+
+cudaError_t launch_split_q8b(const SplitParams& p, const CUtensorMap& tk, const CUtensorMap& tv,
+                             int d, int kind, int grid, cudaStream_t stream) {
+  return DA_LAUNCH_TERMS(launch_q8b_set, terms_of(p.mod), p, tk, tv, d, kind, grid, stream);
+}
+#endif
 
 }  // namespace da

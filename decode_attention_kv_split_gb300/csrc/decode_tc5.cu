@@ -820,11 +820,6 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
 using Tc5G16 = Tc5Cfg<16, 3, 3>;
 using Tc5G32 = Tc5Cfg<32, 3, 2>;
 
-KernelShape tc5_shape(int group) {
-  if (group <= 16) return KernelShape{Tc5G16::kTile, 16, 64, 1, 0.7f};
-  return KernelShape{Tc5G32::kTile, 32, 64, 1, 0.7f};
-}
-
 template <class Cfg, int TERMS>
 static cudaError_t launch_tc5_terms(const SplitParams& p, const CUtensorMap& tk,
                                     const CUtensorMap& tv, int grid, cudaStream_t stream) {
@@ -836,22 +831,28 @@ static cudaError_t launch_tc5_terms(const SplitParams& p, const CUtensorMap& tk,
                           Cfg::kSmemBytes, stream, tk, tv, p);
 }
 
-template <class Cfg>
-static cudaError_t launch_tc5_cfg(const SplitParams& p, const CUtensorMap& tk,
-                                  const CUtensorMap& tv, int grid, cudaStream_t stream) {
-  switch (terms_of(p.mod)) {
-    case 0: return launch_tc5_terms<Cfg, 0>(p, tk, tv, grid, stream);
-    case 1: return launch_tc5_terms<Cfg, 1>(p, tk, tv, grid, stream);
-    case 3: return launch_tc5_terms<Cfg, 3>(p, tk, tv, grid, stream);
-    case 5: return launch_tc5_terms<Cfg, 5>(p, tk, tv, grid, stream);
-    default: return launch_tc5_terms<Cfg, 7>(p, tk, tv, grid, stream);
-  }
+// This object's set of terms (DA_TERMS); the dispatch is in the object of set 0.
+template <int TERMS>
+cudaError_t launch_tc5_set(const SplitParams& p, const CUtensorMap& tk, const CUtensorMap& tv,
+                           int grid, cudaStream_t stream);
+DA_DECLARE_SETS(launch_tc5_set, (const SplitParams&, const CUtensorMap&, const CUtensorMap&, int, cudaStream_t))
+template <>
+cudaError_t launch_tc5_set<DA_TERMS>(const SplitParams& p, const CUtensorMap& tk,
+                                     const CUtensorMap& tv, int grid, cudaStream_t stream) {
+  if (p.group <= 16) return launch_tc5_terms<Tc5G16, DA_TERMS>(p, tk, tv, grid, stream);
+  return launch_tc5_terms<Tc5G32, DA_TERMS>(p, tk, tv, grid, stream);
+}
+
+#if DA_TERMS == 0
+KernelShape tc5_shape(int group) {
+  if (group <= 16) return KernelShape{Tc5G16::kTile, 16, 64, 1, 0.7f};
+  return KernelShape{Tc5G32::kTile, 32, 64, 1, 0.7f};
 }
 
 cudaError_t launch_split_tc5(const SplitParams& p, const CUtensorMap& tk, const CUtensorMap& tv,
                              int grid, cudaStream_t stream) {
-  if (p.group <= 16) return launch_tc5_cfg<Tc5G16>(p, tk, tv, grid, stream);
-  return launch_tc5_cfg<Tc5G32>(p, tk, tv, grid, stream);
+  return DA_LAUNCH_TERMS(launch_tc5_set, terms_of(p.mod), p, tk, tv, grid, stream);
 }
+#endif
 
 }  // namespace da
