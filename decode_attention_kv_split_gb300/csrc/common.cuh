@@ -552,20 +552,23 @@ struct TileMask<false> {
   // some row of [row, row + count) may be seen
   __device__ __forceinline__ bool any_seen(int row, int) const { return row < valid; }
 };
+// (The rows between prefix and first are a gap: one unsigned comparison, and no
+// branch that would keep loads and MMAs from moving across it.)
 template <>
 struct TileMask<true> {
-  int valid, row0, prefix, first;
+  int valid, row0, gap;
+  unsigned hidden;  // rows of the gap, from row `gap` of the tile on
   __device__ __forceinline__ TileMask(const ItemT<true>& it, int tile_row0, int v)
-      : valid(v), row0(cache_row(it, tile_row0)), prefix(it.rows.prefix - row0),
-        first(it.rows.first - row0) {}
+      : valid(v), row0(cache_row(it, tile_row0)), gap(it.rows.prefix - row0),
+        hidden(unsigned(max(it.rows.first - it.rows.prefix, 0))) {}
   __device__ __forceinline__ bool seen(int row) const {
-    return row < valid && (row < prefix || row >= first);
+    return (row < valid) & (unsigned(row - gap) >= hidden);
   }
   __device__ __forceinline__ bool all_seen(int row, int count) const {
-    return row + count <= valid && (row + count <= prefix || row >= first);
+    return (row + count <= valid) & ((row + count <= gap) | (row >= gap + int(hidden)));
   }
   __device__ __forceinline__ bool any_seen(int row, int count) const {
-    return row < valid && (row < prefix || row + count > first);
+    return (row < valid) & ((row < gap) | (row + count > gap + int(hidden)));
   }
 };
 

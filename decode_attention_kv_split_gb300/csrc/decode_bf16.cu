@@ -263,13 +263,6 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
         }
 
         // ---- Step II: mask rows past the end, scale, running max and sum.
-        bool seen[KBW][2];  // this lane's rows of each block
-        const bool all = mask.all_seen(0, Cfg::kTile);
-#pragma unroll
-        for (int kb = 0; kb < KBW; ++kb) {
-          seen[kb][0] = all || mask.seen(key0 + kb * 16 + r);
-          seen[kb][1] = all || mask.seen(key0 + kb * 16 + r + 8);
-        }
         if constexpr (CAP) {
           if (p.mod.short_scale != 0.f) {
 #pragma unroll
@@ -314,8 +307,9 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
                 s[kb][nb][j] *= p.scale_log2;
                 s[kb][nb][j + 2] *= p.scale_log2;
               }
-              s[kb][nb][j] = seen[kb][0] ? s[kb][nb][j] : -INFINITY;
-              s[kb][nb][j + 2] = seen[kb][1] ? s[kb][nb][j + 2] : -INFINITY;
+              const int row_lo = key0 + kb * 16 + r;
+              s[kb][nb][j] = mask.seen(row_lo) ? s[kb][nb][j] : -INFINITY;
+              s[kb][nb][j + 2] = mask.seen(row_lo + 8) ? s[kb][nb][j + 2] : -INFINITY;
               mx = fmaxf(mx, fmaxf(s[kb][nb][j], s[kb][nb][j + 2]));
             }
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
@@ -366,7 +360,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
             pl[nb][1] = movmatrix_trans(l1);
           }
           const int blk0 = key0 + kb * 16;
-          const bool partial = !all && !mask.all_seen(blk0, 16);
+          const bool partial = !mask.all_seen(blk0, 16);
           // rows held by this lane's A registers: {2c, 2c+1} and {8+2c, 9+2c}
           const uint32_t mlo = (mask.seen(blk0 + 2 * c) ? 0x0000ffffu : 0u) |
                                (mask.seen(blk0 + 2 * c + 1) ? 0xffff0000u : 0u);
