@@ -462,6 +462,11 @@ constexpr int kTermsSlopes = 4;
 #ifndef DA_TERMS
 #define DA_TERMS 0
 #endif
+// Host: whether the kernels' short forms serve a call: a bf16 output, and scores
+// not capped or capped where capped_short is exact enough.
+inline bool short_forms(bool out_bf16, const ScoreTerms& m) {
+  return out_bf16 && !(m.on && m.cap_log2 > 0.f && m.short_scale == 0.f);
+}
 // Host: the set of a call's terms.
 inline int terms_of(const ScoreTerms& m) {
   return m.on ? kTermsMask | (m.cap_log2 > 0.f ? kTermsCap : 0) | (m.slopes ? kTermsSlopes : 0) : 0;

@@ -92,7 +92,8 @@ __device__ __forceinline__ int code_at(int row, int piece) {
                   : row * 64 + ((piece ^ ((row >> 1) & 3)) << 4);
 }
 
-template <class Cfg, int TERMS>
+// SHORT: P without its remainder and capped_short (short_forms, for bf16 outputs).
+template <class Cfg, int TERMS, bool SHORT>
 __global__ void __launch_bounds__(Cfg::kThreads, Cfg::CTAS)
     split_decode_q8b_kernel(const __grid_constant__ CUtensorMap tmK,
                             const __grid_constant__ CUtensorMap tmV, const SplitParams p) {
@@ -228,7 +229,10 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::CTAS)
 
   float m_run[NB][2], l_run[NB][2];
   float acc[MB][NB][4];
-  float unit = 0.f;        // the accumulator's unit: the largest |V scale| so far
+  // The accumulator's unit, the largest |V scale| so far: a scale is
+  // (scale * unit_by) * unit_inv units (unit_by brings tiny ones to where the
+  // inverse exists).
+  float unit = 0.f, unit_by = 1.f, unit_inv = 0.f;
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb) {
     m_run[nb][0] = m_run[nb][1] = -INFINITY;
@@ -239,8 +243,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::CTAS)
       for (int e = 0; e < 4; ++e) acc[mb][nb][e] = 0.f;
   }
 
-  const bool exact_p = p.out_bf16 == 0;  // P's fp16 remainder too
-  const float score_scale = CAP && p.mod.short_scale != 0.f ? p.mod.short_scale : p.scale_log2;
+  const float score_scale = CAP && SHORT ? p.mod.short_scale : p.scale_log2;
   [[maybe_unused]] bool slopes_up = true;
   if constexpr (SLOPES) {
 #pragma unroll
@@ -270,17 +273,18 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::CTAS)
     const uint8_t* vtile = ktile + Cfg::kCodeBytes;
     const int v0 = step_row(i);
     const TileMask<MOD> mask(it, v0, min(ROWS, it.row_end - v0));
-    const bool all = mask.all_seen(0, ROWS);
-
-    if (all || mask.any_seen(0, ROWS)) {
-      float ks[2], vs[2];
+    // Every step holds a seen row (the list has only such tiles); its second
+    // block may hold none, and then any scale.
+    float ks[2], vs[2];
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        ks[u] = __shfl_sync(0xffffffffu, sk_now, 2 * (i & 15) + u) * score_scale;
-        vs[u] = __shfl_sync(0xffffffffu, sv_now, 2 * (i & 15) + u);
-        // (a block without a seen row may have any scale)
-        if (!all && !mask.any_seen(u * 16, 16)) ks[u] = vs[u] = 0.f;
-      }
+    for (int u = 0; u < 2; ++u) {
+      ks[u] = __shfl_sync(0xffffffffu, sk_now, 2 * (i & 15) + u) * score_scale;
+      vs[u] = __shfl_sync(0xffffffffu, sv_now, 2 * (i & 15) + u);
+      const bool any = !MOD || mask.any_seen(u * 16, 16);
+      ks[u] = any ? ks[u] : 0.f;
+      vs[u] = any ? vs[u] : 0.f;
+    }
+    {
       // ---- Step I
       float s[2][NB][4];
 #pragma unroll
@@ -313,22 +317,14 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::CTAS)
 #pragma unroll
           for (int e = 0; e < 4; ++e) s[u][nb][e] *= ks[u];
       if constexpr (CAP) {
-        if (p.mod.short_scale != 0.f) {
 #pragma unroll
-          for (int u = 0; u < 2; ++u)
+        for (int u = 0; u < 2; ++u)
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
+          for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) s[u][nb][e] = capped_short(p.mod, s[u][nb][e]);
-        } else {
-#pragma unroll
-          for (int u = 0; u < 2; ++u)
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                s[u][nb][e] = p.mod.cap_log2 * tanh_fast(s[u][nb][e]);
-        }
+            for (int e = 0; e < 4; ++e)
+              s[u][nb][e] = SHORT ? capped_short(p.mod, s[u][nb][e])
+                                  : p.mod.cap_log2 * tanh_fast(s[u][nb][e]);
       }
       if constexpr (SLOPES) {
         const RowDistance dist(it, mask.row0 + g);
@@ -352,16 +348,14 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::CTAS)
                                      slope[nb][e & 1], false);
         }
       }
-      if (!all) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const bool seenA = mask.seen(u * 16 + g), seenB = mask.seen(u * 16 + g + 8);
+      for (int u = 0; u < 2; ++u) {
+        const bool seenA = mask.seen(u * 16 + g), seenB = mask.seen(u * 16 + g + 8);
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb)
+        for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              s[u][nb][e] = (e < 2 ? seenA : seenB) ? s[u][nb][e] : -INFINITY;
-        }
+          for (int e = 0; e < 4; ++e)
+            s[u][nb][e] = (e < 2 ? seenA : seenB) ? s[u][nb][e] : -INFINITY;
       }
       // The maximum is kept lazily: only where some score is more than 2^kLazy
       // above it does a vote bring the exact one (three shuffles a head) and the
@@ -383,6 +377,8 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::CTAS)
         if (avs > unit) {
           f = __fdiv_rn(unit, avs);
           unit = avs;
+          unit_by = unit < 1.f ? 18446744073709551616.f : 1.f;  // 2^64
+          unit_inv = __fdiv_rn(1.f, unit * unit_by);
         }
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
@@ -416,20 +412,19 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::CTAS)
             l_run[nb][j] += s[u][nb][j] + s[u][nb][j + 2];
           }
         }
-      if (vs[0] != unit || vs[1] != unit) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const float w = unit > 0.f ? __fdiv_rn(vs[u], unit) : 0.f;
+      for (int u = 0; u < 2; ++u) {
+        const float w = (vs[u] * unit_by) * unit_inv;
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb)
+        for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[u][nb][e] *= w;
-        }
+          for (int e = 0; e < 4; ++e) s[u][nb][e] *= w;
       }
       // ---- Step III: O^T += V^T . P^T
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        uint32_t ph[NB][2], pl[NB][2];
+        uint32_t ph[NB][2];
+        [[maybe_unused]] uint32_t pl[NB][2];
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
           const float* x = s[u][nb];
@@ -437,7 +432,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::CTAS)
           const uint32_t h1 = q8::pack_f16x2(x[2], x[3]);  // row g + 8
           ph[nb][0] = movmatrix_trans(h0);
           ph[nb][1] = movmatrix_trans(h1);
-          if (exact_p) {
+          if constexpr (!SHORT) {
             pl[nb][0] = movmatrix_trans(
                 q8::pack_f16x2(x[0] - q8::f16_lo(h0), x[1] - q8::f16_hi(h0)));
             pl[nb][1] = movmatrix_trans(
@@ -458,13 +453,12 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::CTAS)
             v[r][0] = w.x, v[r][1] = w.y;
           }
         }
-        if (!all) {  // rows past the end or not seen may hold anything: nothing of them reaches O
+        // rows past the end or not seen may hold anything: nothing of them reaches O
 #pragma unroll
-          for (int r = 0; r < 4; ++r)
-            if (!mask.seen(vr[r])) {
+        for (int r = 0; r < 4; ++r) {
+          const bool seen = mask.seen(vr[r]);
 #pragma unroll
-              for (int w = 0; w < VW; ++w) v[r][w] = 0;
-            }
+          for (int w = 0; w < VW; ++w) v[r][w] = seen ? v[r][w] : 0u;
         }
 #pragma unroll
         for (int mb = 0; mb < MB; ++mb) {
@@ -477,7 +471,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::CTAS)
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb) {
             q8::mma_f16_16816(acc[mb][nb], a, ph[nb][0], ph[nb][1]);
-            if (exact_p) q8::mma_f16_16816(acc[mb][nb], a, pl[nb][0], pl[nb][1]);
+            if constexpr (!SHORT) q8::mma_f16_16816(acc[mb][nb], a, pl[nb][0], pl[nb][1]);
           }
         }
       }
@@ -543,15 +537,22 @@ using Q8BD64N1 = Q8BCfg<64, 1, 3, 4, KIND>;
 template <int KIND>
 using Q8BD64N2 = Q8BCfg<64, 2, 4, 3, KIND>;
 
+template <class Cfg, bool SHORT>
+static cudaError_t launch_q8b_form(const SplitParams& p, const CUtensorMap& tk,
+                                   const CUtensorMap& tv, int grid, cudaStream_t stream) {
+  static std::atomic<unsigned long long> smem_set{0};
+  const cudaError_t e = set_smem_limit_once(split_decode_q8b_kernel<Cfg, DA_TERMS, SHORT>,
+                                            Cfg::kSmemBytes, smem_set);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(split_decode_q8b_kernel<Cfg, DA_TERMS, SHORT>, grid, Cfg::kThreads,
+                          Cfg::kSmemBytes, stream, tk, tv, p);
+}
+
 template <class Cfg>
 static cudaError_t launch_q8b_cfg(const SplitParams& p, const CUtensorMap& tk,
                                   const CUtensorMap& tv, int grid, cudaStream_t stream) {
-  static std::atomic<unsigned long long> smem_set{0};
-  const cudaError_t e =
-      set_smem_limit_once(split_decode_q8b_kernel<Cfg, DA_TERMS>, Cfg::kSmemBytes, smem_set);
-  if (e != cudaSuccess) return e;
-  return launch_dependent(split_decode_q8b_kernel<Cfg, DA_TERMS>, grid, Cfg::kThreads,
-                          Cfg::kSmemBytes, stream, tk, tv, p);
+  return short_forms(p.out_bf16 != 0, p.mod) ? launch_q8b_form<Cfg, true>(p, tk, tv, grid, stream)
+                                             : launch_q8b_form<Cfg, false>(p, tk, tv, grid, stream);
 }
 
 template <int KIND>
