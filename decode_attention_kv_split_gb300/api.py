@@ -575,25 +575,47 @@ def _error_word(t: torch.Tensor | None, device: int):
     return t.data_ptr()
 
 
+def _bad_seq_lens(t: torch.Tensor, B: int, device: int) -> bool:
+    return (t.dtype is not torch.int32 or t.shape != (B,) or t.get_device() != device
+            or not t.is_contiguous())
+
+
+def _out_on(out: torch.Tensor | None, out_dtype: torch.dtype | None, B: int, h_q: int, d_v: int,
+            q: torch.Tensor, device: int):
+    """The output tensor (allocated when None) and its dtype flag."""
+    if out is None:
+        out = torch.empty((B, h_q, d_v), dtype=out_dtype or torch.float32, device=q.device)
+    dtype = out.dtype
+    if out.shape != (B, h_q, d_v) or out.get_device() != device or not out.is_contiguous() \
+            or (dtype is not torch.bfloat16 and dtype is not torch.float32) \
+            or (out_dtype is not None and dtype is not out_dtype):
+        raise ValueError("out must be a contiguous float32 or bfloat16 tensor [B, h_q, d_v] "
+                         "on the query's device")
+    return out, (DA_OUT_BF16 if dtype is torch.bfloat16 else 0)
+
+
 def _cache_args(q, K, V, seq_lens, out, out_dtype):
-    """Checks of a decode over an fp32 or bf16 cache: its sizes, the output, the dtype code."""
+    """Checks of a decode over an fp32 or bf16 cache: its sizes, the output, the dtype code.
+    (A step's host time is mostly these checks and the launches: 2 us of about 11.)"""
     device = q.get_device()
     dtype = q.dtype
     if q.dim() != 3 or K.dim() != 4 or V.dim() != 4:
         raise ValueError("expected q [B, h_q, d_k], K [B, h_kv, n_max, d_k], V [B, h_kv, n_max, d_v]")
     B, h_q, d_k = q.shape
     Bk, h_kv, n_max, d = K.shape
-    d_v = V.shape[3]
-    if Bk != B or d != d_k or V.shape != (B, h_kv, n_max, d_v):
+    Bv, h_kv2, n_max2, d_v = V.shape
+    if Bk != B or Bv != B or h_kv2 != h_kv or n_max2 != n_max or d != d_k:
         raise ValueError("q, K and V shapes disagree")
-    if dtype not in _DTYPES or K.dtype != dtype or V.dtype != dtype:
+    code = _DTYPES.get(dtype)
+    if code is None or K.dtype is not dtype or V.dtype is not dtype:
         raise ValueError("q, K, V must share dtype float32 or bfloat16")
-    for name, t in (("q", q), ("K", K), ("V", V)):
-        if device < 0 or t.get_device() != device or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous CUDA tensor, all on one device")
-    _row_counts("seq_lens", seq_lens, B, device)
-    out, oflag = _out(out, out_dtype, B, h_q, d_v, q.device)
-    return device, out, (B, h_q, h_kv, d_k, d_v, n_max), _DTYPES[dtype] | oflag
+    if device < 0 or K.get_device() != device or V.get_device() != device \
+            or not (q.is_contiguous() and K.is_contiguous() and V.is_contiguous()):
+        raise ValueError("q, K and V must be contiguous CUDA tensors on one device")
+    if _bad_seq_lens(seq_lens, B, device):
+        raise ValueError("seq_lens must be a contiguous int32 tensor [B] on the device of the others")
+    out, oflag = _out_on(out, out_dtype, B, h_q, d_v, q, device)
+    return device, out, (B, h_q, h_kv, d_k, d_v, n_max), code | oflag
 
 
 class _CallOn:
@@ -716,19 +738,19 @@ def decode_attn_mod_append(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Te
 def _q8b_cache(K, V, k_scale, v_scale, block: int):
     """Checks a block-scaled cache; returns its device, B, h_kv, n_max, d."""
     dtype, device, shape = K.dtype, K.get_device(), K.shape
-    if len(shape) != 4 or V.shape != shape or dtype not in _Q8_DTYPES or V.dtype != dtype:
+    if len(shape) != 4 or dtype not in _Q8_DTYPES or V.dtype is not dtype or V.shape != shape:
         raise ValueError("K, V must be 8-bit code tensors [B, h_kv, n_max, d] of one dtype")
     if block not in (16, 32, 64, 128):
         raise ValueError("block must be 16, 32, 64 or 128")
     B, h_kv, n_max, d = shape
+    if device < 0 or V.get_device() != device or not (K.is_contiguous() and V.is_contiguous()):
+        raise ValueError("K and V must be contiguous CUDA tensors on one device")
     scales = (B, h_kv, -(-n_max // block))
-    for name, t, shp, dt in (("K", K, shape, dtype), ("V", V, shape, dtype),
-                             ("k_scale", k_scale, scales, torch.float32),
-                             ("v_scale", v_scale, scales, torch.float32)):
-        if t.shape != shp or t.dtype != dt or device < 0 or t.get_device() != device \
+    for t in (k_scale, v_scale):
+        if t.dtype is not torch.float32 or t.shape != scales or t.get_device() != device \
                 or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous CUDA tensor {list(shp)} of {dt}, all on "
-                             "one device")
+            raise ValueError("k_scale and v_scale must be contiguous float32 tensors "
+                             f"{list(scales)} on the cache's device")
     return device, B, h_kv, n_max, d
 
 
@@ -744,12 +766,13 @@ def decode_attn_q8b(q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, k_scale: 
     scales float32 [B, h_kv, ceil(n_max / block)], q bf16 [B, h_q, d]; ``mod`` adds score terms.
     Returns ``out``."""
     device, B, h_kv, n_max, d = _q8b_cache(K, V, k_scale, v_scale, block)
-    if q.dim() != 3 or q.shape[0] != B or q.shape[2] != d or q.dtype != torch.bfloat16 \
-            or q.get_device() != device or not q.is_contiguous():
+    h_q = q.shape[1] if q.dim() == 3 else 0
+    if q.shape != (B, h_q, d) or q.dtype is not torch.bfloat16 or q.get_device() != device \
+            or not q.is_contiguous():
         raise ValueError("q must be a contiguous bfloat16 tensor [B, h_q, d] on the cache's device")
-    _row_counts("seq_lens", seq_lens, B, device)
-    h_q = q.shape[1]
-    out, oflag = _out(out, out_dtype, B, h_q, d, q.device)
+    if _bad_seq_lens(seq_lens, B, device):
+        raise ValueError("seq_lens must be a contiguous int32 tensor [B] on the cache's device")
+    out, oflag = _out_on(out, out_dtype, B, h_q, d, q, device)
     dt = _Q8_DTYPES[K.dtype] | oflag
     cm = None if mod is None else _c_mod(mod, B, h_q, device)
     err = _error_word(dev_error, device)
@@ -786,15 +809,17 @@ def kv_append_q8b(k_new: torch.Tensor, v_new: torch.Tensor, K: torch.Tensor, V: 
         v_new = v_new.unsqueeze(2)
     T = k_new.shape[2] if k_new.dim() == 4 else -1
     x_dtype = k_new.dtype
+    code = _DTYPES.get(x_dtype)
+    if code is None or v_new.dtype is not x_dtype or k_new.shape != (B, h_kv, T, d) \
+            or v_new.shape != k_new.shape or k_new.get_device() != device \
+            or v_new.get_device() != device:
+        raise ValueError("k_new and v_new must be float32 or bfloat16 tensors [B, h_kv, T, d] of "
+                         "one type on the cache's device")
     strides = []
-    for name, t in (("k_new", k_new), ("v_new", v_new)):
-        if t.shape != (B, h_kv, T, d) or t.dtype not in _DTYPES or t.dtype != x_dtype \
-                or t.get_device() != device:
-            raise ValueError(f"{name} must be a float32 or bfloat16 tensor [B, h_kv, T, d] on the "
-                             "cache's device, k_new and v_new alike")
+    for t in (k_new, v_new):
         sb, sh, st, sd = t.stride()
         if sd != 1:
-            raise ValueError(f"{name} must be contiguous in its last dimension")
+            raise ValueError("k_new and v_new must be contiguous in their last dimension")
         # a dimension of one element has no step: its stride in the tensor may be anything
         strides.append(_Strides(sb if B > 1 else 0, sh if h_kv > 1 else 0, st if T > 1 else 0))
     _row_counts("pos", pos, B, device)
@@ -802,7 +827,7 @@ def kv_append_q8b(k_new: torch.Tensor, v_new: torch.Tensor, K: torch.Tensor, V: 
     err = _error_word(dev_error, device)
     with _CallOn(device, stream) as on:
         st = (_lib or load()).kv_append_q8b(
-            k_new.data_ptr(), v_new.data_ptr(), strides[0], strides[1], _DTYPES[x_dtype], T,
+            k_new.data_ptr(), v_new.data_ptr(), strides[0], strides[1], code, T,
             _addr(n_new), K.data_ptr(), V.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), block,
             pos.data_ptr(), B, h_kv, d, n_max, _Q8_DTYPES[K.dtype], err, on.raw)
     _check(st, "kv_append_q8b")
@@ -828,11 +853,11 @@ def kv_read_q8b(K: torch.Tensor, V: torch.Tensor, k_scale: torch.Tensor, v_scale
     T = k_out.shape[2] if k_out.dim() == 4 else -1
     if rows is not None and rows != T:
         raise ValueError("rows disagrees with the outputs")
-    for name, t in (("k_out", k_out), ("v_out", v_out)):
-        if t.shape != (B, h_kv, T, d) or t.dtype not in _DTYPES or t.dtype != k_out.dtype \
+    for t in (k_out, v_out):
+        if t.dtype not in _DTYPES or t.dtype is not k_out.dtype or t.shape != (B, h_kv, T, d) \
                 or t.get_device() != device or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous float32 or bfloat16 tensor "
-                             "[B, h_kv, rows, d] on the cache's device, k_out and v_out alike")
+            raise ValueError("k_out and v_out must be contiguous float32 or bfloat16 tensors "
+                             "[B, h_kv, rows, d] of one type on the cache's device")
     _row_counts("seq_lens", seq_lens, B, device)
     _row_counts("row_begin", row_begin, B, device)
     err = _error_word(dev_error, device)
