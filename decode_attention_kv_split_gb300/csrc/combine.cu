@@ -54,7 +54,7 @@ __device__ __forceinline__ void ldcg_vec(float (&v)[EPL], const float* src) {
 // balanced pieces, the count the unit's first CTA recorded).  Returns 1 when
 // the split kernel wrote the output itself and 0 when a checked build finds
 // the partial rows or the output row outside their buffers.
-template <int D>
+template <int D, bool TERMS>
 __device__ __forceinline__ int splits_of_head(const SplitParams& p, int bh, int seq_len,
                                               int heads_per_cta) {
   const int h_q = p.h_q;
@@ -63,7 +63,7 @@ __device__ __forceinline__ int splits_of_head(const SplitParams& p, int bh, int 
   const bool appended = p.append && n >= 0 && n < p.n_max;
   n = n < 0 ? 0 : (n > p.n_max ? p.n_max : n);
   if (appended) ++n;
-  if (p.mod.on) {  // the rows of the work list
+  if (TERMS) {  // the rows of the work list
     ItemRows r;
     n = list_rows(p.mod, p.mod.tile_rows, doc_begin(p.mod, b), n, appended, r);
   } else if (!appended) {
@@ -163,7 +163,7 @@ __device__ __forceinline__ void merge_head(const SplitParams& p, int bh, int nv,
   }
 }
 
-template <int D, int W>
+template <int D, int W, bool TERMS>
 __global__ void __launch_bounds__(W * 32, 32 / W)
     lse_combine_kernel(const SplitParams p, int heads_per_cta) {
   constexpr int EPL = D / 32;
@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(W * 32, 32 / W)
   allow_dependent_launch();
   wait_for_prerequisite_grid();
 
-  const int nv = splits_of_head<D>(p, bh, seq_len, heads_per_cta);
+  const int nv = splits_of_head<D, TERMS>(p, bh, seq_len, heads_per_cta);
   if (nv <= 1) return;  // written by the split kernel, or out of range (CTA-uniform)
   // NB splits per warp in flight at once: one pass covers NB * kWarps
   // splits, 272 for d <= 128 (256 splits and the one that rows appended past
@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(W * 32, 32 / W)
 // merge_head, within one warp.
 constexpr int kWarpCombineWarps = 8;
 
-template <int D, int NB>
+template <int D, int NB, bool TERMS>
 __global__ void __launch_bounds__(kWarpCombineWarps * 32, 4)
     lse_combine_warp_kernel(const SplitParams p, int heads_per_cta) {
   constexpr int EPL = D / 32;
@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(kWarpCombineWarps * 32, 4)
       ldcg_vec<EPL>(v[u], op + size_t(u) * D);
     }
   }
-  const int nv = splits_of_head<D>(p, bh, seq_len, heads_per_cta);
+  const int nv = splits_of_head<D, TERMS>(p, bh, seq_len, heads_per_cta);
   if (nv <= 1) return;  // written by the split kernel, or out of range
   float m = -INFINITY, wsum = 0.f, acc[EPL];
 #pragma unroll
@@ -274,19 +274,19 @@ __global__ void __launch_bounds__(kWarpCombineWarps * 32, 4)
   if (lane == 0 && p.lse_out) p.lse_out[bh] = wsum > 0.f ? (m + log2f(wsum)) * kLn2 : -INFINITY;
 }
 
-template <int D, int W>
+template <int D, int W, bool TERMS>
 static cudaError_t launch_combine_dw(const SplitParams& p, int heads_per_cta,
                                      cudaStream_t stream) {
   constexpr int kSmem = combine_smem_bytes<W>();
   static_assert(W * (D + 2) * 4 <= kSmem, "combine scratch");
   static std::atomic<unsigned long long> smem_set{0};
-  const cudaError_t e = set_smem_limit_once(lse_combine_kernel<D, W>, kSmem, smem_set);
+  const cudaError_t e = set_smem_limit_once(lse_combine_kernel<D, W, TERMS>, kSmem, smem_set);
   if (e != cudaSuccess) return e;
-  return launch_dependent(lse_combine_kernel<D, W>, p.B * p.h_q, W * 32, size_t(kSmem), stream,
+  return launch_dependent(lse_combine_kernel<D, W, TERMS>, p.B * p.h_q, W * 32, size_t(kSmem), stream,
                           p, heads_per_cta);
 }
 
-template <int D>
+template <int D, bool TERMS>
 static cudaError_t launch_combine_d(const SplitParams& p, int heads_per_cta, int split_grid,
                                     cudaStream_t stream) {
   // One warp per head when a head's splits are expected to fit one pass of
@@ -300,22 +300,29 @@ static cudaError_t launch_combine_d(const SplitParams& p, int heads_per_cta, int
   if (expected <= NB) {
     const long long heads = (long long)p.B * p.h_q;
     const int grid = int((heads + kWarpCombineWarps - 1) / kWarpCombineWarps);
-    return launch_dependent(lse_combine_warp_kernel<D, NB>, grid, kWarpCombineWarps * 32, 0,
+    return launch_dependent(lse_combine_warp_kernel<D, NB, TERMS>, grid, kWarpCombineWarps * 32, 0,
                             stream, p, heads_per_cta);
   }
   constexpr int NB8 = D == 128 ? 17 : (D == 64 ? 16 : 8);  // splits in flight per warp
   // balanced pieces: max_splits is one slot per CTA, but a unit rarely spans
   // more than a few pieces (8 warps take any count, in more than one pass)
   if (p.max_splits > 8 * NB8 && !p.balanced)
-    return launch_combine_dw<D, 16>(p, heads_per_cta, stream);
-  return launch_combine_dw<D, 8>(p, heads_per_cta, stream);
+    return launch_combine_dw<D, 16, TERMS>(p, heads_per_cta, stream);
+  return launch_combine_dw<D, 8, TERMS>(p, heads_per_cta, stream);
+}
+
+template <bool TERMS>
+static cudaError_t launch_combine_terms(const SplitParams& p, int d, int heads_per_cta,
+                                        int split_grid, cudaStream_t stream) {
+  if (d == 256) return launch_combine_d<256, TERMS>(p, heads_per_cta, split_grid, stream);
+  if (d == 128) return launch_combine_d<128, TERMS>(p, heads_per_cta, split_grid, stream);
+  return launch_combine_d<64, TERMS>(p, heads_per_cta, split_grid, stream);
 }
 
 cudaError_t launch_combine(const SplitParams& p, int d, int heads_per_cta, int split_grid,
                            cudaStream_t stream) {
-  if (d == 256) return launch_combine_d<256>(p, heads_per_cta, split_grid, stream);
-  if (d == 128) return launch_combine_d<128>(p, heads_per_cta, split_grid, stream);
-  return launch_combine_d<64>(p, heads_per_cta, split_grid, stream);
+  return p.mod.on ? launch_combine_terms<true>(p, d, heads_per_cta, split_grid, stream)
+                  : launch_combine_terms<false>(p, d, heads_per_cta, split_grid, stream);
 }
 
 // ---------------------------------------------------------------------------

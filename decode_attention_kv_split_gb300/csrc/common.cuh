@@ -66,8 +66,6 @@ struct SplitParams {
   // Rows decoded per sequence: [row_off, min(row_lim, seq_lens[b])) (row_off = 0
   // and row_lim >= n_max decode every cached row).  Never combined with append.
   int row_off, row_lim;
-  // Score terms (ScoreMod kernels only; see "Score terms" below).
-  ScoreTerms mod;
   float* lse_out;                // nullable: [B, h_q] natural-log log-sum-exp of the decoded rows
   int B, h_q, h_kv, group;       // group = h_q / h_kv
   int b_offset;                  // first sequence of this launch inside the tensor maps
@@ -85,6 +83,7 @@ struct SplitParams {
   int max_splits;                // partial slots per query head (ceil(n_max / chunk))
   float cta_speed;               // one CTA's streaming rate / its even share (split-length model)
   float scale_log2;              // scale * log2(e); with capped scores scale / softcap
+  ScoreTerms mod;                // score terms (kernels compiled for them; see "Score terms")
 #ifdef DA_TEST_HOOKS
   int withhold_cta;              // test builds: this CTA's producer never fills the last stage
                                  // of its first item (-1: none), so a wait must run out

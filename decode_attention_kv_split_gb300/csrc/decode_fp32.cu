@@ -204,10 +204,14 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
       const bool live = __all_sync(0xffffffffu, !*abort_flag);
       // which of this warp's rows are seen (one bit each; a whole tile usually is)
       uint32_t seen = (1u << RPW) - 1u;
-      if (!mask.all_seen(0, Cfg::kTile)) {
-        seen = 0;
+      if constexpr (MOD) {
+        if (!mask.all_seen(0, Cfg::kTile)) {
+          seen = 0;
 #pragma unroll
-        for (int rr = 0; rr < RPW; ++rr) seen |= uint32_t(mask.seen(row0 + rr)) << rr;
+          for (int rr = 0; rr < RPW; ++rr) seen |= uint32_t(mask.seen(row0 + rr)) << rr;
+        }
+      } else {
+        seen >>= RPW - min(max(valid - row0, 0), RPW);
       }
       if (live && seen) {
         // Step I: s[g][r] = (scale*log2e*q_g) . K_row, reduced across the warp.
