@@ -246,6 +246,8 @@ struct Plan {
   int batch_per_launch;
   bool balanced;       // num_splits = -1: one equal piece of all rows per CTA
   int units;           // (sequence, kv head, head chunk) units of one launch slice
+  int places, rounds;  // block-scaled caches: see SplitParams
+  long long grid;      // block-scaled caches: CTAs of a full launch slice
 };
 
 // The device-side cost model (choose_chunk) evaluated with every sequence at
@@ -283,14 +285,8 @@ bool single_split_suffices(long long units, int n_max, int chunk_min, int tile, 
   return best_c >= n_max;
 }
 
-// Block-scaled caches (see make_plan).  Rounds 2, 3, 4 and 6 of the grid: 37.3,
-// 34.7, 35.5 and 38.5 us on 16 ragged int8 sequences with 8 kv heads, 92.8, 88.7,
-// 87.9 and 88.4 us on 2 x 131072 rows of fp8.  One round of longer chunks where
-// a partial has 16 heads: 33.5 us on 8 x 30000 rows for 32 heads (compute-bound,
-// so a second, short round costs a whole one: 48.8 us in chunks of 1024 rows).
-constexpr long long kBlockRounds = 3;
-constexpr long long kBlockRowsPerHead = 96;
-constexpr long long kBlockMinRows = 128;
+// Block-scaled caches (see make_plan): the most bytes of partials.
+constexpr long long kBlockPartialBytes = 64LL << 20;
 
 // Splits per sequence requested by the caller -> a split length that is a
 // whole number of pipeline stages, as close as possible to n_max / S.  When
@@ -312,40 +308,51 @@ int make_plan(int B, int h_q, int h_kv, int d, int d_v, int n_max, int dtype_arg
                           : (dtype == DA_BF16 ? da::bf16_shape(d, d_v, group)
                                               : da::f32_shape(d, group));
   pl->head_chunks = (group + pl->ks.heads_per_cta - 1) / pl->ks.heads_per_cta;
-  // (no work list, no limit on the batch of a launch, for block-scaled caches)
-  pl->batch_per_launch = block || B < da::kMaxBatchPerLaunch ? B : da::kMaxBatchPerLaunch;
+  pl->batch_per_launch = B < da::kMaxBatchPerLaunch ? B : da::kMaxBatchPerLaunch;
   const long long tile = pl->ks.tile_rows;
   // A work list with score terms holds whole tiles of the rows that are seen:
   // less than a tile more at the prefix's end and at the window's start.
   if (seen >= 0 && seen + 2 * tile < n_max) n_max = int(seen + 2 * tile);
   const long long max_tiles = (n_max + tile - 1) / tile;
   pl->balanced = false;
+  pl->places = pl->rounds = 0;
+  pl->grid = 0;
   pl->units = int((long long)pl->batch_per_launch * h_kv * pl->head_chunks);
   if (requested < -1) return DA_ERR_SHAPE;
   if (block) {
-    // One CTA per chunk (decode_q8b.cu): the grid, not a work list, balances
-    // the SMs.  The library aims at kBlockRounds CTAs for every place on the GPU
-    // with all sequences at full length, but keeps chunks at kBlockRowsPerHead
-    // rows for each head of a partial (which costs 4 D bytes a head to write and
-    // merge against 2 D bytes a row read), unless they then leave places empty.
+    // One CTA per chunk, whose length the kernel picks from the actual lengths
+    // (candidate_chunk in decode_q8b.cu); the host sizes the grid for every sequence at
+    // full length and bounds the splits, by the chunks there can be and by the
+    // partials' bytes.
     const long long places = (long long)sms * (long long)pl->ks.cta_speed;
-    const int heads = group < pl->ks.heads_per_cta ? group : pl->ks.heads_per_cta;
-    long long chunk;
+    const long long per_seq = (long long)h_kv * pl->head_chunks, units = pl->units;
+    pl->places = int(places);
+    pl->rounds = 1;
     if (requested > 0) {
-      chunk = (n_max + requested - 1) / requested;
+      const long long chunk = ((n_max + requested - 1LL) / requested + tile - 1) / tile * tile;
+      pl->chunk_fixed = pl->chunk_min = int(chunk);
+      pl->grid = units * ((n_max + chunk - 1) / chunk);
     } else {
-      chunk = (long long)pl->units * n_max / (kBlockRounds * places);
-      const long long per_unit = places / pl->units > 0 ? places / pl->units : 1;
-      const long long one_round = (n_max + per_unit - 1) / per_unit;
-      const long long by_heads = kBlockRowsPerHead * heads;
-      if (chunk < by_heads) chunk = by_heads < one_round ? by_heads : one_round;
-      if (chunk < kBlockMinRows) chunk = kBlockMinRows;
-      if (n_max <= 2 * kBlockMinRows) chunk = n_max;
+      const long long rounds = (units * n_max + places * da::kBlockRoundRows - 1) /
+                               (places * da::kBlockRoundRows);
+      pl->rounds = int(rounds < 1 ? 1 : (rounds < da::kBlockRounds ? rounds : da::kBlockRounds));
+      pl->grid = units <= places ? pl->rounds * places : units + pl->rounds * places;
+      long long most = pl->grid / per_seq + 1;  // chunks one sequence's unit can get
+      const long long by_rows = (n_max + da::kBlockMinRows - 1) / da::kBlockMinRows;
+      const long long by_bytes = kBlockPartialBytes /
+                                 ((long long)pl->batch_per_launch * h_q * (d_v + 1) * 4);
+      if (most > by_rows) most = by_rows;
+      if (most > by_bytes) most = by_bytes;
+      if (n_max <= 2 * da::kBlockMinRows || most < 2) most = 1;
+      pl->chunk_fixed = 0;
+      pl->chunk_min = int(((n_max + most - 1) / most + tile - 1) / tile * tile);
+      if (most == 1) {  // no partials, no combine
+        pl->chunk_fixed = pl->chunk_min;
+        pl->grid = units;
+      }
     }
-    chunk = (chunk + tile - 1) / tile * tile;
-    pl->chunk_fixed = pl->chunk_min = int(chunk);
-    pl->max_splits = int((n_max + chunk - 1) / chunk);
-    if ((long long)pl->units * pl->max_splits > 0x7fffffffLL) return DA_ERR_SHAPE;
+    pl->max_splits = int((n_max + pl->chunk_min - 1) / pl->chunk_min);
+    if (pl->grid > 0x7fffffffLL) return DA_ERR_SHAPE;
     return DA_OK;
   }
   // Balanced pieces when the row stream fits an int and the partials of up
@@ -529,6 +536,8 @@ int run_decode(const void* q, const void* K, const void* V, const int32_t* seq_l
     p.blk_shift = ba ? ba->shift : 0;
     p.nblk = ba ? int(((long long)n_max + (1 << ba->shift) - 1) >> ba->shift) : 0;
     p.scale_elems = (long long)B * h_kv * p.nblk;
+    p.places = pl.places;
+    p.rounds = pl.rounds;
     p.B = bn;
     p.h_q = h_q;
     p.h_kv = h_kv;
@@ -551,8 +560,8 @@ int run_decode(const void* q, const void* K, const void* V, const int32_t* seq_l
     // tag per CTA in the two halves of the work list's reduction scratch)
     const long long max_grid = da::kSchedRedWords / 2 - 1;
     const long long grid_cap = sms < max_grid ? sms : max_grid;
-    // (a block-scaled cache: one CTA per item, not persistent)
-    const int grid = int(ba || items < grid_cap ? items : grid_cap);
+    // (a block-scaled cache: one CTA per chunk, not persistent)
+    const int grid = int(ba ? pl.grid : (items < grid_cap ? items : grid_cap));
     cudaError_t err =
         pl.tc5 ? da::launch_split_tc5(p, tk, tv, grid, stream)
         : ba   ? da::launch_split_q8b(p, tk, tv, d_k, dtype == DA_INT8 ? 1 : 2, grid, stream)

@@ -296,7 +296,10 @@ static cudaError_t launch_combine_d(const SplitParams& p, int heads_per_cta, int
   // splits 2 % slower in one warp.)
   constexpr int NB = D == 256 ? 4 : (D == 128 ? 8 : 12);
   const long long units = (long long)p.B * p.h_kv * p.head_chunks;
-  const long long expected = p.balanced ? (split_grid + units - 1) / units + 1 : p.max_splits;
+  // (balanced pieces and a block-scaled cache's chunks: one slot for the most a
+  // unit could get, but about a grid's worth over all units)
+  const bool spread = p.balanced || (p.places > 0 && p.chunk_fixed <= 0);
+  const long long expected = spread ? (split_grid + units - 1) / units + 1 : p.max_splits;
   if (expected <= NB) {
     const long long heads = (long long)p.B * p.h_q;
     const int grid = int((heads + kWarpCombineWarps - 1) / kWarpCombineWarps);
@@ -306,7 +309,7 @@ static cudaError_t launch_combine_d(const SplitParams& p, int heads_per_cta, int
   constexpr int NB8 = D == 128 ? 17 : (D == 64 ? 16 : 8);  // splits in flight per warp
   // balanced pieces: max_splits is one slot per CTA, but a unit rarely spans
   // more than a few pieces (8 warps take any count, in more than one pass)
-  if (p.max_splits > 8 * NB8 && !p.balanced)
+  if ((p.places > 0 ? expected : p.max_splits) > 8 * NB8 && !p.balanced)
     return launch_combine_dw<D, 16, TERMS>(p, heads_per_cta, stream);
   return launch_combine_dw<D, 8, TERMS>(p, heads_per_cta, stream);
 }

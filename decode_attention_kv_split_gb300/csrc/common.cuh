@@ -60,6 +60,7 @@ struct SplitParams {
   // Block-scaled 8-bit caches: k_scale and v_scale hold [B, h_kv, nblk] scales,
   // one for 2^blk_shift consecutive rows.
   int nblk, blk_shift;
+  int places, rounds;            // CTAs the GPU holds at once; most rounds of them in the grid
   long long scale_elems;         // elements of k_scale, for the checked build
   int append;
   int out_bf16;                  // out holds bf16 (rounded once from the fp32 result)
@@ -317,6 +318,11 @@ KernelShape f32_shape(int d, int group);
 KernelShape tc5_shape(int group);
 KernelShape q8_shape(int d);
 KernelShape q8b_shape(int d, int group);
+// Block-scaled decode: rows per place on the GPU that ask for another round of
+// chunks (up to kBlockRounds), and the fewest rows of a chunk.
+constexpr int kBlockRoundRows = 2200;
+constexpr int kBlockRounds = 3;
+constexpr int kBlockMinRows = 128;
 cudaError_t launch_split_q8b(const SplitParams& p, const CUtensorMap& tk, const CUtensorMap& tv,
                              int d, int kind, int grid, cudaStream_t stream);
 

@@ -14,11 +14,15 @@
 // MMA rate per byte of HBM.
 //
 // Work.  A CTA of four warps takes one chunk of a (sequence, kv head, head
-// chunk)'s rows: its place in the grid names all three, so there is no work list
-// to build, and two to four CTAs share an SM, so that one's start and end
-// (loads of q, the merge of its warps) pass under the others' streams.  The
-// persistent form of this kernel (one CTA of eight warps a SM, every CTA
-// building the list) took 40.8 us on 16 ragged int8 sequences with 8 kv heads.
+// chunk)'s rows, and three or four CTAs share an SM, so that one's start and end
+// (loads of q, the merge of its warps) pass under the others' streams (one CTA of
+// eight warps a SM: 40.8 us on 16 ragged int8 sequences with 8 kv heads).  Every
+// CTA finds its chunk from the lengths (find_item_few, _many): the chunk length is the
+// shortest whose chunks all fit on the GPU at once, so that there is one round
+// of equal CTAs, whatever n_max is (33.1 us with a length fixed by n_max).  Long
+// caches take two or three shorter rounds: HBM does not serve all SMs alike, and
+// the CTAs of a later round go where an early one ended (one round of 4600 rows a
+// CTA took 107 us, three of them 88).
 // Within a CTA warp w takes the 32-row steps w, w + 4, ... of the chunk and
 // feeds itself: its lane 0 keeps a ring of steps (K and V codes, 2 TMA boxes of
 // 32 rows) in flight on the warp's own barriers, and no warp waits for another
@@ -57,6 +61,10 @@
 
 namespace da {
 
+// Shared memory of find_item: the lengths of a launch slice's sequences, and
+// scratch for four warps.
+constexpr int kFindWords = kMaxBatchPerLaunch + 4 * 32 + 16;
+
 template <int D_, int NB_, int STAGES_, int CTAS_, int KIND_>
 struct Q8BCfg {
   static constexpr int D = D_;
@@ -77,12 +85,182 @@ struct Q8BCfg {
   // the merge of the warps reuses the ring
   static constexpr int kEpiBytes = (kEpiAccFloats + kEpiMLFloats) * 4;
   static constexpr int kDataBytes = kRingBytes > kEpiBytes ? kRingBytes : kEpiBytes;
-  static constexpr size_t kSmemBytes = 1024 + kDataBytes + KW * STAGES * 8 + 16;
+  static constexpr size_t kSmemBytes =
+      1024 + kDataBytes + KW * STAGES * 8 + 16 + kFindWords * 4;
   static_assert(D == 64 || D == 128, "head dim");
   static_assert(KIND == 1 || KIND == 2, "code type");
   static_assert(CTAS * (kSmemBytes + 1024) <= 228 * 1024, "shared memory");
   static_assert(kDataBytes % 8 == 0, "mbarrier alignment");
 };
+
+// Quotients by one divisor: floor(x / d) for x < 2^31, by a multiplication that
+// is at most one too high and a correction.
+struct Divisor {
+  unsigned d, by;
+  __device__ __forceinline__ explicit Divisor(unsigned d_) : d(d_), by(0xffffffffu / d_ + 1) {}
+  __device__ __forceinline__ int up(int x) const {  // ceil(x / d)
+    const unsigned y = unsigned(x) + d - 1;
+    const unsigned q = d > 1 ? __umulhi(y, by) : y;
+    return int(q - (q * d > y));
+  }
+};
+
+// The candidate chunk length of a lane.  With `rows` rows over all units, the
+// launch may have `most` chunks: a round or more of the GPU's places; with more
+// units than places, one for each unit and a round for the long ones' further
+// chunks.  Lane k tries the k-th of 32 lengths between rows / most (no shorter one
+// can do) and rows / (most - units) (which does).
+template <int ROWS>
+__device__ __forceinline__ int candidate_chunk(const SplitParams& p, unsigned long long rows,
+                                               int longest, long long& most) {
+  const int lane = threadIdx.x & 31;
+  const long long units = (long long)p.B * p.h_kv * p.head_chunks;
+  const unsigned long long round = (unsigned long long)p.places * kBlockRoundRows;
+  const int rounds = rows <= round ? 1 : min(p.rounds, int((rows + round - 1) / round));
+  most = (units <= p.places ? 0 : units) + (long long)rounds * p.places;
+  // (in float: candidates may be off by a row, whether one does is counted exactly)
+  const float least = float(rows) / float(most);
+  const float enough = most > units ? float(rows) / float(most - units) : float(longest);
+  float c = ceilf(least + (enough - least) * (float(lane) * (1.f / 31.f)));
+  c = fminf(fmaxf(c, float(kBlockMinRows)), 2147483000.f);
+  int chunk = lane == 31 ? longest : min(int(c), longest);  // (one chunk a unit: always enough)
+  chunk = max(chunk, p.chunk_min);
+  return (chunk + ROWS - 1) / ROWS * ROWS;
+}
+
+// The blockIdx.x-th chunk of the launch slice, in `it`, and the chunk length;
+// false when there are fewer.  Sequence b has max(1, ceil(n_b / chunk)) chunks for
+// each kv head and head chunk; head chunks are neighbours, so that all but the
+// first of them find the codes in L2.
+
+// For at most 8 sequences: each warp by itself, lane b on sequence b, with its
+// rows in n.
+constexpr int kFewSequences = 8;
+
+template <int ROWS>
+__device__ __forceinline__ bool find_item_few(const SplitParams& p, int n, Item& it, int& chunk) {
+  const int lane = threadIdx.x & 31;
+  const int per_seq = p.h_kv * p.head_chunks;
+  chunk = p.chunk_fixed;
+  if (p.chunk_fixed <= 0) {
+    unsigned long long rows = unsigned(n);
+    int longest = n;
+#pragma unroll
+    for (int o = kFewSequences / 2; o > 0; o >>= 1) {
+      rows += __shfl_xor_sync(0xffffffffu, rows, o);
+      longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, o));
+    }
+    rows = __shfl_sync(0xffffffffu, rows, 0) * unsigned(per_seq);
+    longest = __shfl_sync(0xffffffffu, longest, 0);
+    long long most;
+    const int c = candidate_chunk<ROWS>(p, rows, longest, most);
+    const Divisor by{unsigned(c)};
+    int count = 0;
+    for (int b = 0; b < p.B; ++b) count += by.up(__shfl_sync(0xffffffffu, n, b));
+    const unsigned fits =
+        __ballot_sync(0xffffffffu, (long long)count * per_seq <= most) | 0x80000000u;
+    chunk = __shfl_sync(0xffffffffu, c, __ffs(int(fits)) - 1);
+  }
+  const int nv = lane < p.B ? Divisor{unsigned(chunk)}.up(n) : 0;
+  const int mine = per_seq * nv;  // (the grid holds all chunks: an int)
+  int upto = mine;
+#pragma unroll
+  for (int o = 1; o < kFewSequences; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += y;
+  }
+  const int i = int(blockIdx.x);
+  const unsigned here =
+      __ballot_sync(0xffffffffu, lane < p.B && i >= upto - mine && i < upto);
+  if (here == 0) return false;
+  const int b = __ffs(int(here)) - 1;
+  int at = __shfl_sync(0xffffffffu, i - (upto - mine), b);
+  it.b = b;
+  it.nv = __shfl_sync(0xffffffffu, nv, b);
+  it.hc = at % p.head_chunks;
+  at /= p.head_chunks;
+  it.split = at % it.nv;
+  it.kvh = at / it.nv;
+  return true;
+}
+
+// For any number: all 128 threads, lengths in sm[0 .. B) (filled by the caller,
+// not yet synchronised).
+template <int ROWS>
+__device__ __forceinline__ bool find_item_many(const SplitParams& p, int* sm, Item& it,
+                                               int& chunk) {
+  const int* lens = sm;
+  int* scratch = sm + kMaxBatchPerLaunch;  // [4][32]
+  int* found = scratch + 4 * 32;           // [16]
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per_seq = p.h_kv * p.head_chunks;
+  __syncthreads();  // lens
+  chunk = p.chunk_fixed;
+  if (p.chunk_fixed <= 0) {
+    unsigned long long rows = 0;
+    int longest = 1;
+    for (int b = lane; b < p.B; b += 32) {  // every warp all of them: no barrier
+      rows += unsigned(lens[b]);
+      longest = max(longest, lens[b]);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      rows += __shfl_xor_sync(0xffffffffu, rows, o);
+      longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, o));
+    }
+    long long most;
+    const int c = candidate_chunk<ROWS>(p, rows * unsigned(per_seq), longest, most);
+    const Divisor by{unsigned(c)};
+    int count = 0;
+    for (int b = warp; b < p.B; b += 4) count += by.up(lens[b]);
+    scratch[warp * 32 + lane] = count;
+    __syncthreads();
+    count = scratch[lane] + scratch[32 + lane] + scratch[64 + lane] + scratch[96 + lane];
+    const unsigned fits =
+        __ballot_sync(0xffffffffu, (long long)count * per_seq <= most) | 0x80000000u;
+    chunk = __shfl_sync(0xffffffffu, c, __ffs(int(fits)) - 1);
+  }
+  // The sequence that holds chunk blockIdx.x: a scan of the counts, in runs of
+  // consecutive sequences per thread.
+  const Divisor by{unsigned(chunk)};
+  const int run = (p.B + 127) / 128;
+  const int b0 = tid * run, b1 = min(p.B, b0 + run);
+  int mine = 0;
+  for (int b = b0; b < b1; ++b) mine += per_seq * by.up(lens[b]);
+  int upto = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += y;
+  }
+  if (lane == 31) found[warp] = upto;
+  if (tid == 0) found[8] = -1;
+  __syncthreads();
+  for (int w = 0; w < warp; ++w) upto += found[w];
+  const int i = int(blockIdx.x);
+  if (i >= upto - mine && i < upto) {
+    int at = i - (upto - mine), b = b0, nv;
+    for (;; ++b) {
+      nv = by.up(lens[b]);
+      if (at < per_seq * nv) break;
+      at -= per_seq * nv;
+    }
+    found[9] = b;
+    found[10] = at;
+    found[11] = nv;
+    found[8] = 0;
+  }
+  __syncthreads();
+  if (found[8] < 0) return false;
+  int at = found[10];
+  it.b = found[9];
+  it.nv = found[11];
+  it.hc = at % p.head_chunks;
+  at /= p.head_chunks;
+  it.split = at % it.nv;
+  it.kvh = at / it.nv;
+  return true;
+}
 
 // Byte offset of 16-byte piece `piece` of row `row` of a box: the 128-byte
 // swizzle for 128-byte rows, the 64-byte swizzle for 64-byte rows.
@@ -128,39 +306,59 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::CTAS)
     prefetch_tmap(&tmK);
     prefetch_tmap(&tmV);
   }
-  // the CTA's place: head chunk, split, kv head, sequence (fastest first)
-  Item where;
-  {
-    unsigned i = blockIdx.x;
-    const unsigned hcs = unsigned(p.head_chunks), sp = unsigned(p.max_splits);
-    where.hc = int(i % hcs);
-    i /= hcs;
-    where.split = int(i % sp);
-    i /= sp;
-    where.kvh = int(i % unsigned(p.h_kv));
-    where.b = int(i / unsigned(p.h_kv));
-  }
-  wait_for_prerequisite_grid();
-  allow_dependent_launch();
+  // Launched as a programmatic dependent.  The CTAs of the first round, which may
+  // start while the previous grid runs, find their chunk on the lengths as they
+  // read before the wait (that grid may be writing them), and again if one has
+  // changed after it; later ones have nothing to wait for.
+  int* find = reinterpret_cast<int*>(bars + KW * STAGES) + 4;
   ItemT<MOD> it;
-  static_cast<Item&>(it) = where;
+  int chunk = 0;
+  bool any = false;
+  const bool early = int(blockIdx.x) < p.places, few = p.B <= kFewSequences;
   bool bad = false, bad_pos = false;
   int n_out;
+  auto rows_of = [&](int b) {  // (an empty sequence has one chunk, for its zeros)
+    return max(1, list_len<ROWS, MOD>(p, MOD ? doc_begin(p.mod, b) : 0, __ldcg(p.seq_lens + b), bad,
+                                      bad_pos, n_out));
+  };
+  int seen_n = 0;
+  if (early) {
+    if (few) {
+      seen_n = lane < p.B ? rows_of(lane) : 0;
+      any = find_item_few<ROWS>(p, seen_n, it, chunk);
+    } else {
+      for (int b = threadIdx.x; b < p.B; b += Cfg::kThreads) find[b] = rows_of(b);
+      any = find_item_many<ROWS>(p, find, it, chunk);
+    }
+  }
+  bad = false;
+  wait_for_prerequisite_grid();
+  allow_dependent_launch();
+  if (few) {
+    const int n = lane < p.B ? rows_of(lane) : 0;
+    if (!early || __any_sync(0xffffffffu, n != seen_n))
+      any = find_item_few<ROWS>(p, n, it, chunk);
+  } else {
+    int changed = early ? 0 : 1;
+    for (int b = threadIdx.x; b < p.B; b += Cfg::kThreads) {
+      const int n = rows_of(b);
+      changed |= n != find[b];
+      find[b] = n;
+    }
+    if (__syncthreads_or(changed)) any = find_item_many<ROWS>(p, find, it, chunk);
+  }
+  if (bad && blockIdx.x == 0) flag_error(p.dev_error, DA_DEVERR_SEQ_LEN);
+  if (blockIdx.x == 0 && threadIdx.x == 0 && p.chunk_out) *p.chunk_out = chunk;
+  if (!any) return;
   const int begin = MOD ? doc_begin(p.mod, it.b) : 0;
-  const int n_in = __ldcg(p.seq_lens + it.b);
-  const int n = list_len<ROWS, MOD>(p, begin, n_in, bad, bad_pos, n_out);
+  const int n = list_len<ROWS, MOD>(p, begin, __ldcg(p.seq_lens + it.b), bad, bad_pos, n_out);
   if constexpr (MOD) list_rows(p.mod, ROWS, begin, n_out, false, it.rows);
-  if (bad && it.split == 0 && it.kvh == 0 && it.hc == 0 && threadIdx.x == 0)
-    flag_error(p.dev_error, DA_DEVERR_SEQ_LEN);
-  it.nv = n <= 0 ? 1 : (n - 1) / p.chunk_fixed + 1;
-  if (it.split >= it.nv) return;
-  it.row_begin = it.split * p.chunk_fixed;
-  it.row_end = min(n, it.row_begin + p.chunk_fixed);
+  it.row_begin = it.split * chunk;
+  it.row_end = min(n, it.row_begin + chunk);
   it.new_row = -1;
+  if (few) __syncthreads();  // barriers initialised
   const int steps = (it.row_end - it.row_begin + ROWS - 1) / ROWS;
   it.tiles = steps > warp ? (steps - warp + KW - 1) / KW : 0;  // this warp's
-  __syncthreads();  // barriers initialised
-
   // First list row of this warp's i-th step.
   auto step_row = [&](int i) { return it.row_begin + (i * KW + warp) * ROWS; };
   const int z = (p.b_offset + it.b) * p.h_kv + it.kvh;
@@ -525,8 +723,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::CTAS)
 
 // ---------------------------------------------------------------------------
 // Variants and launcher.  Groups of up to 8 query heads take one MMA block of
-// heads, larger ones two (16 heads a CTA); the head chunks of one cache chunk
-// are neighbours in the grid, so all but the first find its codes in L2.
+// heads, larger ones two (16 heads a CTA).
 // ---------------------------------------------------------------------------
 template <int KIND>
 using Q8BD128N1 = Q8BCfg<128, 1, 2, 3, KIND>;
