@@ -324,7 +324,10 @@ int make_plan(int B, int h_q, int h_kv, int d, int d_v, int n_max, int dtype_arg
     // (candidate_chunk in decode_q8b.cu); the host sizes the grid for every sequence at
     // full length and bounds the splits, by the chunks there can be and by the
     // partials' bytes.
-    const long long places = (long long)sms * (long long)pl->ks.cta_speed;
+    // (a sixteenth of the places is left over: the previous grid's last CTAs hold
+    // some, and chunks that miss a round cost another one; on 2 x 131072 rows of
+    // fp8, 80 chunks a unit in 2.8 rounds take 86.3 us, 84 in 2.95 rounds 88.8 us)
+    const long long places = (long long)sms * (long long)pl->ks.cta_speed * 15 / 16;
     const long long per_seq = (long long)h_kv * pl->head_chunks, units = pl->units;
     pl->places = int(places);
     pl->rounds = 1;

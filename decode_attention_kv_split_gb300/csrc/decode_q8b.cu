@@ -105,26 +105,27 @@ struct Divisor {
   }
 };
 
-// The candidate chunk length of a lane.  With `rows` rows over all units, the
-// launch may have `most` chunks: a round or more of the GPU's places; with more
-// units than places, one for each unit and a round for the long ones' further
-// chunks.  Lane k tries the k-th of 32 lengths between rows / most (no shorter one
-// can do) and rows / (most - units) (which does).
+// The candidate chunk length of a lane.  With `rows` rows over the sequences
+// (below 2^31: the cache's rows are), the launch may have `most` chunks: a round
+// or more of the GPU's places; with more units than places, one for each unit and
+// a round for the long ones' further chunks.  Lane k tries the k-th of 32 lengths
+// between (all units' rows) / most, below which none can do, and rows / (most -
+// units), which does.  In float: a candidate may be off by a row, but whether it
+// does is counted exactly, and lane 31's, one chunk a unit, always does.
 template <int ROWS>
-__device__ __forceinline__ int candidate_chunk(const SplitParams& p, unsigned long long rows,
-                                               int longest, long long& most) {
+__device__ __forceinline__ int candidate_chunk(const SplitParams& p, unsigned rows, int longest,
+                                               int& most) {
   const int lane = threadIdx.x & 31;
-  const long long units = (long long)p.B * p.h_kv * p.head_chunks;
-  const unsigned long long round = (unsigned long long)p.places * kBlockRoundRows;
-  const int rounds = rows <= round ? 1 : min(p.rounds, int((rows + round - 1) / round));
-  most = (units <= p.places ? 0 : units) + (long long)rounds * p.places;
-  // (in float: candidates may be off by a row, whether one does is counted exactly)
-  const float least = float(rows) / float(most);
-  const float enough = most > units ? float(rows) / float(most - units) : float(longest);
-  float c = ceilf(least + (enough - least) * (float(lane) * (1.f / 31.f)));
-  c = fminf(fmaxf(c, float(kBlockMinRows)), 2147483000.f);
-  int chunk = lane == 31 ? longest : min(int(c), longest);  // (one chunk a unit: always enough)
-  chunk = max(chunk, p.chunk_min);
+  const int units = p.B * p.h_kv * p.head_chunks;
+  const float all = float(rows) * float(p.h_kv * p.head_chunks);
+  const int rounds =
+      max(1, min(p.rounds, int(ceilf(all * __fdividef(1.f, float(p.places) * kBlockRoundRows)))));
+  most = (units <= p.places ? 0 : units) + rounds * p.places;
+  const float least = __fdividef(all, float(most));
+  const float enough = most > units ? __fdividef(all, float(most - units)) : float(longest);
+  float c = ceilf(fmaf(enough - least, float(lane) * (1.f / 31.f), least));
+  c = fminf(fmaxf(c, float(kBlockMinRows)), float(longest));
+  const int chunk = max(lane == 31 ? longest : int(c), p.chunk_min);
   return (chunk + ROWS - 1) / ROWS * ROWS;
 }
 
@@ -143,16 +144,16 @@ __device__ __forceinline__ bool find_item_few(const SplitParams& p, int n, Item&
   const int per_seq = p.h_kv * p.head_chunks;
   chunk = p.chunk_fixed;
   if (p.chunk_fixed <= 0) {
-    unsigned long long rows = unsigned(n);
+    unsigned rows = unsigned(n);
     int longest = n;
 #pragma unroll
     for (int o = kFewSequences / 2; o > 0; o >>= 1) {
       rows += __shfl_xor_sync(0xffffffffu, rows, o);
       longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, o));
     }
-    rows = __shfl_sync(0xffffffffu, rows, 0) * unsigned(per_seq);
+    rows = __shfl_sync(0xffffffffu, rows, 0);
     longest = __shfl_sync(0xffffffffu, longest, 0);
-    long long most;
+    int most;
     const int c = candidate_chunk<ROWS>(p, rows, longest, most);
     const Divisor by{unsigned(c)};
     int count = 0;
@@ -197,7 +198,7 @@ __device__ __forceinline__ bool find_item_many(const SplitParams& p, int* sm, It
   __syncthreads();  // lens
   chunk = p.chunk_fixed;
   if (p.chunk_fixed <= 0) {
-    unsigned long long rows = 0;
+    unsigned rows = 0;
     int longest = 1;
     for (int b = lane; b < p.B; b += 32) {  // every warp all of them: no barrier
       rows += unsigned(lens[b]);
@@ -208,8 +209,8 @@ __device__ __forceinline__ bool find_item_many(const SplitParams& p, int* sm, It
       rows += __shfl_xor_sync(0xffffffffu, rows, o);
       longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, o));
     }
-    long long most;
-    const int c = candidate_chunk<ROWS>(p, rows * unsigned(per_seq), longest, most);
+    int most;
+    const int c = candidate_chunk<ROWS>(p, rows, longest, most);
     const Divisor by{unsigned(c)};
     int count = 0;
     for (int b = warp; b < p.B; b += 4) count += by.up(lens[b]);
