@@ -347,7 +347,10 @@ cudaError_t launch_kv_append_q8b(const BlockWriteArgs& a, cudaStream_t stream) {
 // Bound: HBM (1 byte in, 2 or 4 out per element).  A lane writes 16 bytes at a
 // time, so that a warp's loads and stores are whole runs of bytes.  CTAs are
 // persistent and hold two parts of kReadUnroll rows for every run of lanes: one
-// is loaded while the other is converted and stored.
+// is loaded while the other is converted and stored.  The parts that hold rows
+// are counted from the lengths and dealt round (dealt over all T rows of every
+// sequence, a ragged batch of 4 took 21 us instead of 17; in one run per CTA,
+// neighbouring addresses came apart in time and long reads took 3 to 15 % more).
 // ---------------------------------------------------------------------------
 struct BlockRead {
   const uint8_t* codes[2];
@@ -357,13 +360,14 @@ struct BlockRead {
   const int32_t* row_begin;  // nullable: [B] (else 0)
   int32_t* dev_error;
   int B, h_kv, T, n_max, nblk, blk_shift;
-  unsigned per_head, parts;  // parts of one head of one tensor, and of all
+  int part_rows;             // rows of a part
   long long cache_rows, scale_elems, out_rows;       // extents, for the checked build
 };
 
 constexpr int kReadThreads = 256;
 constexpr int kReadUnroll = 8;
 constexpr int kReadCtas = 4;  // CTAs an SM
+constexpr int kReadBatch = 512;  // sequences whose rows are counted at a time
 
 template <int D, bool OBF16, int KIND>
 __global__ void __launch_bounds__(kReadThreads, kReadCtas)
@@ -374,6 +378,10 @@ __global__ void __launch_bounds__(kReadThreads, kReadCtas)
   allow_dependent_launch();
   wait_for_prerequisite_grid();
 
+  // Rows and first part of every sequence (a slice of the batch at a time).
+  __shared__ int rows_of[kReadBatch], begin_of[kReadBatch], first_of[kReadBatch + 1];
+  __shared__ int warp_sum[kReadThreads / 32];
+
   // One part: kReadUnroll consecutive rows for every LPR lanes.  Its codes and
   // scales are loaded while the part before it is converted and stored.
   struct Part {
@@ -383,19 +391,11 @@ __global__ void __launch_bounds__(kReadThreads, kReadCtas)
                                              // on the second scale
   };
   const int c = threadIdx.x % LPR;
-  auto load = [&](unsigned part, Part& q, int n, int begin) {
-    q.rows = 0;
-    if (part >= p.parts) return;
-    const unsigned u = part / p.per_head;
-    q.tensor = int(u & 1u);
-    q.head = int(u >> 1);
-    const bool bad = n < 0 || n > p.n_max || begin < 0;
-    if (bad && part % p.per_head == 0 && q.tensor == 0 && q.head % p.h_kv == 0 && threadIdx.x == 0)
-      flag_error(p.dev_error, DA_DEVERR_SEQ_LEN);
-    if (begin < 0) return;
-    n = min(max(n, 0), p.n_max);
-    q.rows = min(p.T, n - begin);  // may be <= 0
-    q.i0 = int(part % p.per_head) * (SETS * kReadUnroll) + int(threadIdx.x / LPR) * kReadUnroll;
+  auto load = [&](int b, int unit, int part, int rows, int begin, Part& q) {
+    q.tensor = unit & 1;
+    q.head = b * p.h_kv + (unit >> 1);
+    q.rows = rows;
+    q.i0 = part * p.part_rows + int(threadIdx.x / LPR) * kReadUnroll;
     if (q.i0 >= q.rows) return;
     const int blk = (begin + q.i0) >> p.blk_shift;
     q.first_next = ((blk + 1) << p.blk_shift) - (begin + q.i0);
@@ -435,24 +435,84 @@ __global__ void __launch_bounds__(kReadThreads, kReadCtas)
       }
     }
   };
-  auto counts = [&](unsigned part, int& n, int& begin) {
-    n = begin = 0;
-    if (part >= p.parts) return;
-    const int b = int(part / p.per_head >> 1) / p.h_kv;
-    n = __ldcg(p.seq_lens + b);
-    if (p.row_begin) begin = __ldcg(p.row_begin + b);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int units = 2 * p.h_kv;  // heads of K and V of a sequence
+  // A sequence's rows (T at most), and its first one.
+  auto rows_from = [&](int b, int& begin) {
+    const int n = __ldcg(p.seq_lens + b);
+    begin = p.row_begin ? __ldcg(p.row_begin + b) : 0;
+    if ((n < 0 || n > p.n_max || begin < 0) && blockIdx.x == 0)
+      flag_error(p.dev_error, DA_DEVERR_SEQ_LEN);
+    return begin < 0 ? 0 : max(0, min(p.T, min(max(n, 0), p.n_max) - begin));
   };
-  Part now, next;
-  int n, begin;
-  unsigned part = blockIdx.x;
-  counts(part, n, begin);
-  load(part, now, n, begin);
-  counts(part + gridDim.x, n, begin);
-  for (; part < p.parts; part += gridDim.x) {
-    load(part + gridDim.x, next, n, begin);
-    counts(part + 2 * gridDim.x, n, begin);
-    if (now.rows > 0) store(now);
-    now = next;
+  if (p.T <= p.part_rows) {  // one part a head: no need to count them (0.6 us of 3.8)
+    for (int b = blockIdx.x == 0 ? tid : p.B; b < p.B; b += kReadThreads) {
+      int begin;
+      rows_from(b, begin);  // (CTA 0: every sequence's flags)
+    }
+    for (unsigned q = blockIdx.x; q < unsigned(p.B) * unsigned(units); q += gridDim.x) {
+      const int b = int(q / unsigned(units));
+      int begin;
+      const int rows = rows_from(b, begin);
+      Part now;
+      load(b, int(q - unsigned(b) * unsigned(units)), 0, rows, begin, now);
+      store(now);
+    }
+    return;
+  }
+  for (int b0 = 0; b0 < p.B; b0 += kReadBatch) {
+    const int nb = min(kReadBatch, p.B - b0);
+    // the rows of each sequence, and a scan of the parts they make
+    const int run = (nb + kReadThreads - 1) / kReadThreads;
+    const int from = min(nb, tid * run), to = min(nb, from + run);
+    int mine = 0;
+    for (int b = from; b < to; ++b) {
+      int begin;
+      const int rows = rows_from(b0 + b, begin);
+      rows_of[b] = rows;
+      begin_of[b] = begin;
+      mine += units * ((rows + p.part_rows - 1) / p.part_rows);
+    }
+    int upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += y;
+    }
+    if (lane == 31) warp_sum[warp] = upto;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) upto += warp_sum[w];
+    int at = upto - mine;
+    for (int b = from; b < to; ++b) {
+      first_of[b] = at;
+      at += units * ((rows_of[b] + p.part_rows - 1) / p.part_rows);
+    }
+    if (tid == kReadThreads - 1) first_of[nb] = upto;
+    __syncthreads();
+    const int total = first_of[nb];
+    int part = int(blockIdx.x), b = 0;
+    if (part < total) {
+      auto load_part = [&](int q, Part& to_part) {
+        if (q >= first_of[b + 1]) {  // (parts come in order): the last b with first_of[b] <= q
+          int hi = nb - 1;
+          for (++b; b < hi;) {
+            const int mid = (b + hi + 1) >> 1;
+            if (first_of[mid] <= q) b = mid; else hi = mid - 1;
+          }
+        }
+        const int per = (rows_of[b] + p.part_rows - 1) / p.part_rows;
+        const int r = q - first_of[b], unit = r / per;
+        load(b0 + b, unit, r - unit * per, rows_of[b], begin_of[b], to_part);
+      };
+      Part now, next;
+      load_part(part, now);
+      for (; part < total; part += int(gridDim.x)) {
+        if (part + int(gridDim.x) < total) load_part(part + int(gridDim.x), next);
+        store(now);
+        now = next;
+      }
+    }
+    __syncthreads();  // the arrays are read
   }
 }
 
@@ -469,15 +529,13 @@ cudaError_t launch_kv_read_q8b(const BlockReadArgs& a, cudaStream_t stream) {
   p.B = a.B, p.h_kv = a.h_kv, p.T = a.T, p.n_max = a.n_max, p.blk_shift = a.blk_shift;
   const int S = 1 << a.blk_shift;
   p.nblk = (a.n_max + S - 1) / S;
-  const int rows = kReadThreads / (a.d / (a.out_bf16 ? 8 : 4)) * kReadUnroll;
-  const long long per_head = (a.T + rows - 1LL) / rows;
+  p.part_rows = kReadThreads / (a.d / (a.out_bf16 ? 8 : 4)) * kReadUnroll;
+  const long long per_head = (a.T + p.part_rows - 1LL) / p.part_rows;
   p.cache_rows = (long long)a.B * a.h_kv * a.n_max;
   p.scale_elems = (long long)a.B * a.h_kv * p.nblk;
   p.out_rows = (long long)a.B * a.h_kv * a.T;
   const long long parts = 2LL * a.B * a.h_kv * per_head;
   if (parts > 0x3fffffffLL) return cudaErrorInvalidValue;  // (checked by the caller)
-  p.per_head = unsigned(per_head);
-  p.parts = unsigned(parts);
   const long long places = (long long)a.sms * kReadCtas;
   const long long grid = parts < places ? parts : places;
   auto go = [&](auto kernel) {

@@ -214,6 +214,35 @@ def test_read(dtype, out_dtype, d):
     assert k.shape == (B, h, n_max, d) and k.dtype == out_dtype
 
 
+def test_read_of_many_sequences():
+    """More sequences than are counted at a time, most of them without rows to read."""
+    B, h, n_max, d, block = 1100, 1, 70, 64, 16
+    K, V, ks, vs = random_cache(B, h, n_max, d, block, torch.int8, 5)
+    g = torch.Generator().manual_seed(1)
+    lens = torch.randint(0, n_max + 1, (B,), generator=g).tolist()
+    begin = [n if b % 3 else max(0, n - 9) for b, n in enumerate(lens)]
+    for rows in (5, 200):
+        k, v = (torch.full((B, h, rows, d), 77.0, device="cuda") for _ in range(2))
+        api.kv_read_q8b(K.cuda(), V.cuda(), ks.cuda(), vs.cuda(), i32(lens), block, row_begin=i32(begin), k_out=k,
+                        v_out=v)
+        for codes, sc, got in ((K, ks, k), (V, vs, v)):
+            all_rows = codes.float() * sc.repeat_interleave(block, 2)[:, :, :n_max, None]
+            want = torch.full((B, h, rows, d), 77.0)
+            for b in range(B):
+                n = max(0, min(rows, lens[b] - begin[b]))
+                want[b, :, :n] = all_rows[b, :, begin[b]:begin[b] + n]
+            assert torch.equal(got.cpu(), want)
+
+
+def test_decode_of_very_unequal_lengths():
+    """One long sequence among many short ones: its unit is cut further than the others'."""
+    for B, h_q, h_kv, d in ((60, 4, 2, 128), (300, 8, 2, 64), (9, 16, 1, 128), (5, 4, 1, 64)):
+        lens = [(b * 7) % 90 for b in range(B)]
+        lens[B // 2] = 2500
+        decode_case(B, h_q, h_kv, d, 2500, lens, torch.int8, 32)
+    decode_case(20, 8, 4, 128, 6000, [(b * 11) % 150 for b in range(20)], torch.float8_e4m3fn, 16)
+
+
 def test_read_out_of_range():
     K, V, ks, vs = (c.cuda() for c in random_cache(3, 1, 50, 64, 16, torch.int8, 1))
     for lens, begin in (([60, 50, 50], [0, 0, 0]), ([50, -2, 50], [0, 0, 0]), ([50, 50, 50], [0, -1, 0])):
