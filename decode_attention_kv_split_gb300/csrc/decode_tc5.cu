@@ -486,9 +486,11 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
               (it.new_row >= row0 && it.new_row < row0 + T) ? it.new_row - row0 : -1;
           if (new_local >= 0) {
             const uint8_t* slot = vnew + size_t(vslot) * Cfg::kRowBytes;
-            for (int ch = lane; ch < D / 8; ch += 32)
-              *reinterpret_cast<uint4*>(vt + tc5::sw128(new_local, ch * 8, T)) =
-                  reinterpret_cast<const uint4*>(slot)[ch];
+            // (with terms, a row that the query does not see stays out of O)
+            if (!MOD || TileMask<MOD>(it, row0, valid).seen(new_local))
+              for (int ch = lane; ch < D / 8; ch += 32)
+                *reinterpret_cast<uint4*>(vt + tc5::sw128(new_local, ch * 8, T)) =
+                    reinterpret_cast<const uint4*>(slot)[ch];
             if (it.hc == 0 &&  // and into the V cache
                 DA_IN(p, (size_t(p.b_offset + it.b) * p.h_kv + it.kvh) * size_t(p.n_max) + cache_row(it, it.new_row),
                       p.cache_rows)) {

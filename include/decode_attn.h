@@ -359,7 +359,8 @@ DA_API int kv_quantize(const void* x, int x_dtype, void* codes, float* scales, l
  * The softmax runs over the seen rows; none seen gives out = 0.  Rows that are
  * not seen are not read into results (they may hold anything, including NaN),
  * and whole stages of them are not loaded.
- *   softcap   : 0 for none, else in [1e-30, 1e30]
+ *   softcap   : 0 for none, else in [1e-30, 1e30], with scale / softcap finite
+ *               in float
  *   window    : the last `window` rows are seen; 0 for all
  *   prefix    : the first `prefix` rows are seen whatever the window and the
  *               document (a shared prompt, or the rows a window keeps)

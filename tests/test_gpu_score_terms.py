@@ -42,6 +42,10 @@ def make(B, h_q, h_kv, d_k, d_v, n_max, lens, dtype, seed, terms, append=False):
     return q, K, V, kn, vn
 
 
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
 def c_terms(terms):
     sl, bg = terms.get("slopes"), terms.get("begin")
     return ScoreMod(softcap=terms.get("softcap", 0.0),
@@ -178,6 +182,19 @@ def test_rows_that_nothing_sees(heads, append):
     for prefix in (0, 3, 200):
         for begin in (299, 300, 301, 302, 5000, 2 ** 31 - 1, -5, -2 ** 31):
             run(*heads, 400, [300] * B, dtype, {"begin": [begin] * B, "prefix": prefix}, append=append)
+
+
+def test_appended_rows_that_nothing_sees_may_hold_anything():
+    """A new row before its own document (a slot written ahead): NaN in it stays out of the output."""
+    for heads in EDGE:
+        B, h_q, h_kv, d, _ = heads
+        dtype = torch.float32 if d == 64 else torch.bfloat16
+        for prefix in (0, 100):
+            q, K, V, *_ = make(*heads, 400, [300] * B, dtype, 3, {"begin": [10 ** 6] * B, "prefix": prefix}, True)
+            bad = torch.full((B, h_kv, d), float("nan"), dtype=dtype, device="cuda")
+            out = api.decode_attn_mod_append(q.cuda(), bad, bad, K.cuda(), V.cuda(), i32([300] * B),
+                                             ScoreMod(prefix=prefix, doc_begin=i32([10 ** 6] * B)))
+            check(out, q, K, V, [301] * B, {"begin": [10 ** 6] * B, "prefix": prefix}, dtype, 1 / math.sqrt(d))
 
 
 def test_empty_sequences():

@@ -45,6 +45,7 @@ def test_score_terms(lib):
     assert _mod(lib, _cmod(), h_q=3, h_kv=2) == -2
     assert _mod(lib, _cmod(), n_max=0) == -2
     assert _mod(lib, _cmod(), scale=nan) == -2
+    assert _mod(lib, _cmod(softcap=1e-30), scale=1e10) == -2   # scale / softcap overflows
     m = ctypes.byref(_cmod())
 
     def app(k_new=OK, lens_out=None, mod=m):
