@@ -135,12 +135,14 @@ __device__ __forceinline__ int candidate_chunk(const SplitParams& p, unsigned ro
 // first of them find the codes in L2.
 
 // For at most 8 sequences: each warp by itself, lane b on sequence b, with its
-// rows in n.
+// rows in n_b.
 constexpr int kFewSequences = 8;
 
 template <int ROWS>
-__device__ __forceinline__ bool find_item_few(const SplitParams& p, int n, Item& it, int& chunk) {
+__device__ __forceinline__ bool find_item_few(const SplitParams& p, int n_b, Item& it,
+                                              int& chunk) {
   const int lane = threadIdx.x & 31;
+  const int n = lane < p.B ? max(n_b, 1) : 0;  // (an empty sequence has one chunk, for its zeros)
   const int per_seq = p.h_kv * p.head_chunks;
   chunk = p.chunk_fixed;
   if (p.chunk_fixed <= 0) {
@@ -201,7 +203,7 @@ __device__ __forceinline__ bool find_item_many(const SplitParams& p, int* sm, It
     unsigned rows = 0;
     int longest = 1;
     for (int b = lane; b < p.B; b += 32) {  // every warp all of them: no barrier
-      rows += unsigned(lens[b]);
+      rows += unsigned(max(lens[b], 1));
       longest = max(longest, lens[b]);
     }
 #pragma unroll
@@ -213,7 +215,7 @@ __device__ __forceinline__ bool find_item_many(const SplitParams& p, int* sm, It
     const int c = candidate_chunk<ROWS>(p, rows, longest, most);
     const Divisor by{unsigned(c)};
     int count = 0;
-    for (int b = warp; b < p.B; b += 4) count += by.up(lens[b]);
+    for (int b = warp; b < p.B; b += 4) count += by.up(max(lens[b], 1));
     scratch[warp * 32 + lane] = count;
     __syncthreads();
     count = scratch[lane] + scratch[32 + lane] + scratch[64 + lane] + scratch[96 + lane];
@@ -227,7 +229,7 @@ __device__ __forceinline__ bool find_item_many(const SplitParams& p, int* sm, It
   const int run = (p.B + 127) / 128;
   const int b0 = tid * run, b1 = min(p.B, b0 + run);
   int mine = 0;
-  for (int b = b0; b < b1; ++b) mine += per_seq * by.up(lens[b]);
+  for (int b = b0; b < b1; ++b) mine += per_seq * by.up(max(lens[b], 1));
   int upto = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -242,7 +244,7 @@ __device__ __forceinline__ bool find_item_many(const SplitParams& p, int* sm, It
   if (i >= upto - mine && i < upto) {
     int at = i - (upto - mine), b = b0, nv;
     for (;; ++b) {
-      nv = by.up(lens[b]);
+      nv = by.up(max(lens[b], 1));
       if (at < per_seq * nv) break;
       at -= per_seq * nv;
     }
@@ -318,15 +320,16 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::CTAS)
   const bool early = int(blockIdx.x) < p.places, few = p.B <= kFewSequences;
   bool bad = false, bad_pos = false;
   int n_out;
-  auto rows_of = [&](int b) {  // (an empty sequence has one chunk, for its zeros)
-    return max(1, list_len<ROWS, MOD>(p, MOD ? doc_begin(p.mod, b) : 0, __ldcg(p.seq_lens + b), bad,
-                                      bad_pos, n_out));
+  int begin = 0;
+  auto rows_of = [&](int b) {
+    begin = MOD ? doc_begin(p.mod, b) : 0;
+    return list_len<ROWS, MOD>(p, begin, __ldcg(p.seq_lens + b), bad, bad_pos, n_out);
   };
-  int seen_n = 0;
+  int n_b = 0;
   if (early) {
     if (few) {
-      seen_n = lane < p.B ? rows_of(lane) : 0;
-      any = find_item_few<ROWS>(p, seen_n, it, chunk);
+      if (lane < p.B) n_b = rows_of(lane);
+      any = find_item_few<ROWS>(p, n_b, it, chunk);
     } else {
       for (int b = threadIdx.x; b < p.B; b += Cfg::kThreads) find[b] = rows_of(b);
       any = find_item_many<ROWS>(p, find, it, chunk);
@@ -335,24 +338,29 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::CTAS)
   bad = false;
   wait_for_prerequisite_grid();
   allow_dependent_launch();
+  int n = 0;  // rows of the chunk's sequence
+  n_out = 0;
   if (few) {
-    const int n = lane < p.B ? rows_of(lane) : 0;
-    if (!early || __any_sync(0xffffffffu, n != seen_n))
-      any = find_item_few<ROWS>(p, n, it, chunk);
+    const int before = n_b;
+    if (lane < p.B) n_b = rows_of(lane);
+    if (!early || __any_sync(0xffffffffu, n_b != before))
+      any = find_item_few<ROWS>(p, n_b, it, chunk);
+    n = __shfl_sync(0xffffffffu, n_b, any ? it.b : 0);
+    n_out = __shfl_sync(0xffffffffu, n_out, any ? it.b : 0);
+    begin = __shfl_sync(0xffffffffu, begin, any ? it.b : 0);
   } else {
     int changed = early ? 0 : 1;
     for (int b = threadIdx.x; b < p.B; b += Cfg::kThreads) {
-      const int n = rows_of(b);
-      changed |= n != find[b];
-      find[b] = n;
+      const int now = rows_of(b);
+      changed |= now != find[b];
+      find[b] = now;
     }
     if (__syncthreads_or(changed)) any = find_item_many<ROWS>(p, find, it, chunk);
+    if (any) n = MOD ? rows_of(it.b) : find[it.b];
   }
   if (bad && blockIdx.x == 0) flag_error(p.dev_error, DA_DEVERR_SEQ_LEN);
   if (blockIdx.x == 0 && threadIdx.x == 0 && p.chunk_out) *p.chunk_out = chunk;
   if (!any) return;
-  const int begin = MOD ? doc_begin(p.mod, it.b) : 0;
-  const int n = list_len<ROWS, MOD>(p, begin, __ldcg(p.seq_lens + it.b), bad, bad_pos, n_out);
   if constexpr (MOD) list_rows(p.mod, ROWS, begin, n_out, false, it.rows);
   it.row_begin = it.split * chunk;
   it.row_end = min(n, it.row_begin + chunk);
