@@ -334,6 +334,32 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::CTAS)
       for (int b = threadIdx.x; b < p.B; b += Cfg::kThreads) find[b] = rows_of(b);
       any = find_item_many<ROWS>(p, find, it, chunk);
     }
+    // The chunk's first steps into L2 meanwhile: only a hint, so that it may go by
+    // lengths that change yet, and by a cache that the previous grid still writes.
+    // (GQA int8 32.2 -> 31.2 us, long fp8 86.9 -> 84.4; twice as many steps cost the
+    // previous grid's last CTAs more than they bring: 33.0 and 83.7 us.)
+    if (any) {
+      int n = 0;
+      if (few) {
+        n = __shfl_sync(0xffffffffu, n_b, it.b);
+        n_out = __shfl_sync(0xffffffffu, n_out, it.b);
+        begin = __shfl_sync(0xffffffffu, begin, it.b);
+      } else {
+        n = MOD ? rows_of(it.b) : find[it.b];
+      }
+      if constexpr (MOD) list_rows(p.mod, ROWS, begin, n_out, false, it.rows);
+      if (lane == 0) {
+        const int head = (p.b_offset + it.b) * p.h_kv + it.kvh;
+        const int end = min(n, it.split * chunk + chunk);
+        for (int i = 0; i < STAGES; ++i) {
+          const int v = it.split * chunk + (i * KW + warp) * ROWS;
+          if (v >= end) break;
+          const int y = cache_row(it, v);
+          tma_prefetch_3d(&tmK, 0, y, head);
+          tma_prefetch_3d(&tmV, 0, y, head);
+        }
+      }
+    }
   }
   bad = false;
   wait_for_prerequisite_grid();
