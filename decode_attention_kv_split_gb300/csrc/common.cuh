@@ -320,7 +320,7 @@ KernelShape q8_shape(int d);
 KernelShape q8b_shape(int d, int group);
 // Block-scaled decode: rows per place on the GPU that ask for another round of
 // chunks (up to kBlockRounds), and the fewest rows of a chunk.
-constexpr int kBlockRoundRows = 2200;
+constexpr int kBlockRoundRows = 2800;
 constexpr int kBlockRounds = 3;
 constexpr int kBlockMinRows = 128;
 cudaError_t launch_split_q8b(const SplitParams& p, const CUtensorMap& tk, const CUtensorMap& tv,

@@ -19,17 +19,20 @@
 // eight warps a SM: 40.8 us on 16 ragged int8 sequences with 8 kv heads).  Every
 // CTA finds its chunk from the lengths (find_item_few, _many): the chunk length is the
 // shortest whose chunks all fit on the GPU at once, so that there is one round
-// of equal CTAs, whatever n_max is (33.1 us with a length fixed by n_max).  Long
-// caches take two or three shorter rounds: HBM does not serve all SMs alike, and
-// the CTAs of a later round go where an early one ended (one round of 4600 rows a
-// CTA took 107 us, three of them 88).
+// of equal CTAs, whatever n_max is (31.0 us; 33.1 with a length fixed by n_max).
+// Beyond kBlockRoundRows rows a CTA there are two or three shorter rounds: HBM does
+// not serve all SMs alike, and the CTAs of a later round go where an early one
+// ended (2 x 131072 rows of fp8 with 64 query heads: 85.6 us in one round, 83.7 in
+// two, 6.4 TB/s; ncu on it: DRAM 77 % busy, 1.4 instructions a cycle of 4, the MMA
+// pipe 17 %).  With 32 heads on one kv head the MMAs and the instructions around
+// them, not HBM, are the bound: 31.4 us for 8 x 30000 rows, 9.2 us of HBM time.
 // Within a CTA warp w takes the 32-row steps w, w + 4, ... of the chunk and
 // feeds itself: its lane 0 keeps a ring of steps (K and V codes, 2 TMA boxes of
 // 32 rows) in flight on the warp's own barriers, and no warp waits for another
 // before the chunk's end.  A step holds two 16-row MMA blocks, so that the
 // barrier, the maximum's shuffles and the rescaling come once for both and two
-// independent chains fill each other's latencies (with one block a step the
-// kernel issued 375 instructions a block and took 4 % longer on long fp8 caches).
+// independent chains fill each other's latencies (375 instructions a block with
+// one block a step, 260 with two).
 //
 // Layout.  The boxes have a row's D bytes contiguous with the 128- or 64-byte
 // swizzle; MMA A fragments are built from them in registers, no fp16 copy is
