@@ -618,43 +618,35 @@ def _cache_args(q, K, V, seq_lens, out, out_dtype):
     return device, out, (B, h_q, h_kv, d_k, d_v, n_max), code | oflag
 
 
-class _CallOn:
-    """Runs a call on tensors of CUDA device ``device``: makes it current where it is not, and
-    gives the raw stream (that of ``stream``, else the device's current one)."""
-    __slots__ = ("device", "stream", "prev", "raw")
+def _enter(device: int) -> int:
+    """Makes ``device`` current; returns the device to go back to, or -1."""
+    cur = torch._C._cuda_getDevice()
+    if cur == device:
+        return -1
+    torch.cuda.set_device(device)
+    return cur
 
-    def __init__(self, device: int, stream):
-        self.device, self.stream, self.prev = device, stream, -1
 
-    def __enter__(self):
-        cur = torch.cuda.current_device()
-        if cur != self.device:
-            self.prev = cur
-            torch.cuda.set_device(self.device)
-        s = self.stream
-        self.raw = (s.cuda_stream if s is not None
-                    else torch._C._cuda_getCurrentRawStream(self.device))
-        return self
-
-    def __exit__(self, *exc):
-        if self.prev >= 0:
-            torch.cuda.set_device(self.prev)
+def _raw(stream, device: int) -> int:
+    """The raw stream of a call: that of ``stream``, else the device's current one."""
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
 
 
 _mod_bytes_cache: dict = {}
 
 
-def _terms_workspace(entry: str, cmod, sizes, on: _CallOn, workspace: torch.Tensor | None):
-    """Address and bytes of the workspace of a call with score terms or block scales (``sizes``:
-    the sizes, dtype code and split choice).  Without a given one: a tensor of the stream the
-    call runs on, kept for its next call; while that stream is captured, a tensor of the graph's
-    own pool, since two graphs that share scratch may be replayed at the same time.  (The third
-    value keeps a graph's tensor alive through the call.)"""
+def _terms_workspace(entry: str, cmod, sizes, device: int, stream, raw: int,
+                     workspace: torch.Tensor | None):
+    """The workspace of a call with score terms or block scales and its bytes (``sizes``: the
+    sizes, dtype code and split choice).  Without a given one: a tensor of the stream the call
+    runs on, kept for its next call; while that stream is captured, a tensor of the graph's own
+    pool, since two graphs that share scratch may be replayed at the same time."""
     if workspace is not None:
-        if workspace.get_device() != on.device or not workspace.is_contiguous():
+        if workspace.get_device() != device or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous tensor on the query's device")
-        return workspace.data_ptr(), workspace.numel() * workspace.element_size(), None
-    key = (entry, on.device, sizes, None if cmod is None else (cmod.window, cmod.prefix))
+        return workspace, workspace.numel() * workspace.element_size()
+    key = (entry, device, sizes, 0, 0) if cmod is None else (entry, device, sizes, cmod.window,
+                                                             cmod.prefix)
     need = _mod_bytes_cache.get(key)
     if need is None:
         st = ctypes.c_int(0)
@@ -665,16 +657,23 @@ def _terms_workspace(entry: str, cmod, sizes, on: _CallOn, workspace: torch.Tens
             _mod_bytes_cache.clear()
         _mod_bytes_cache[key] = need
     if need == 0:
-        return None, 0, None
-    at = (on.device, on.raw, "terms")
-    with torch.cuda.stream(on.stream) if on.stream is not None else contextlib.nullcontext():
-        if torch.cuda.is_current_stream_capturing():
-            ws = torch.empty(need, dtype=torch.uint8, device=on.device)
-            return ws.data_ptr(), need, ws
-        ws = _ws_cache.get(at)
+        return None, 0
+    with _on_stream(stream):
+        if torch._C._cuda_isCurrentStreamCapturing():
+            return torch.empty(need, dtype=torch.uint8, device=device), need
+        ws = _ws_cache.get((device, raw, "terms"))
         if ws is None or ws.numel() < need:
-            ws = _ws_cache[at] = torch.empty(need, dtype=torch.uint8, device=on.device)
-    return ws.data_ptr(), ws.numel(), None
+            ws = _ws_cache[device, raw, "terms"] = torch.empty(need, dtype=torch.uint8,
+                                                               device=device)
+    return ws, need
+
+
+_no_stream = contextlib.nullcontext()
+
+
+def _on_stream(stream):
+    """Allocations in the order of ``stream`` (None: the current one)."""
+    return _no_stream if stream is None else torch.cuda.stream(stream)
 
 
 def decode_attn_mod(q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, seq_lens: torch.Tensor,
@@ -687,15 +686,20 @@ def decode_attn_mod(q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, seq_lens:
     bias, a window, documents and an always-seen prefix, as ``mod`` says.  Returns ``out``."""
     device, out, dims, dt = _cache_args(q, K, V, seq_lens, out, out_dtype)
     cm = _c_mod(mod, dims[0], dims[1], device)
-    err = _error_word(dev_error, device)
+    err = None if dev_error is None else _error_word(dev_error, device)
     if scale is None:
         scale = 1.0 / math.sqrt(dims[3])
-    with _CallOn(device, stream) as on:
-        ws, nbytes, _keep = _terms_workspace("decode_attn_mod_workspace_bytes", cm,
-                                             (*dims, dt, num_splits), on, workspace)
+    prev = _enter(device)
+    try:
+        raw = _raw(stream, device)
+        ws, nbytes = _terms_workspace("decode_attn_mod_workspace_bytes", cm,
+                                      (*dims, dt, num_splits), device, stream, raw, workspace)
         st = (_lib or load()).decode_attn_mod(
             q.data_ptr(), K.data_ptr(), V.data_ptr(), seq_lens.data_ptr(), ctypes.byref(cm),
-            out.data_ptr(), *dims, scale, dt, num_splits, ws, nbytes, err, on.raw)
+            out.data_ptr(), *dims, scale, dt, num_splits, _addr(ws), nbytes, err, raw)
+    finally:
+        if prev >= 0:
+            torch.cuda.set_device(prev)
     _check(st, "decode_attn_mod")
     return out
 
@@ -720,16 +724,21 @@ def decode_attn_mod_append(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Te
             raise ValueError(f"{name} must be a contiguous CUDA tensor of the cache dtype")
     _row_counts("seq_lens_out", seq_lens_out, B, device)
     cm = _c_mod(mod, B, h_q, device)
-    err = _error_word(dev_error, device)
+    err = None if dev_error is None else _error_word(dev_error, device)
     if scale is None:
         scale = 1.0 / math.sqrt(d_k)
-    with _CallOn(device, stream) as on:
-        ws, nbytes, _keep = _terms_workspace("decode_attn_mod_workspace_bytes", cm,
-                                             (*dims, dt, num_splits), on, workspace)
+    prev = _enter(device)
+    try:
+        raw = _raw(stream, device)
+        ws, nbytes = _terms_workspace("decode_attn_mod_workspace_bytes", cm,
+                                      (*dims, dt, num_splits), device, stream, raw, workspace)
         st = (_lib or load()).decode_attn_mod_append(
             q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), K.data_ptr(), V.data_ptr(),
             seq_lens.data_ptr(), _addr(seq_lens_out), ctypes.byref(cm), out.data_ptr(), *dims,
-            scale, dt, num_splits, ws, nbytes, err, on.raw)
+            scale, dt, num_splits, _addr(ws), nbytes, err, raw)
+    finally:
+        if prev >= 0:
+            torch.cuda.set_device(prev)
     _check(st, "decode_attn_mod_append")
     return out
 
@@ -775,17 +784,22 @@ def decode_attn_q8b(q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, k_scale: 
     out, oflag = _out_on(out, out_dtype, B, h_q, d, q, device)
     dt = _Q8_DTYPES[K.dtype] | oflag
     cm = None if mod is None else _c_mod(mod, B, h_q, device)
-    err = _error_word(dev_error, device)
+    err = None if dev_error is None else _error_word(dev_error, device)
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    with _CallOn(device, stream) as on:
-        ws, nbytes, _keep = _terms_workspace("decode_attn_q8b_workspace_bytes", cm,
-                                             (B, h_q, h_kv, d, d, n_max, dt, num_splits), on,
-                                             workspace)
+    prev = _enter(device)
+    try:
+        raw = _raw(stream, device)
+        ws, nbytes = _terms_workspace("decode_attn_q8b_workspace_bytes", cm,
+                                      (B, h_q, h_kv, d, d, n_max, dt, num_splits), device, stream,
+                                      raw, workspace)
         st = (_lib or load()).decode_attn_q8b(
             q.data_ptr(), K.data_ptr(), V.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), block,
             seq_lens.data_ptr(), None if cm is None else ctypes.byref(cm), out.data_ptr(), B, h_q,
-            h_kv, d, d, n_max, scale, dt, num_splits, ws, nbytes, err, on.raw)
+            h_kv, d, d, n_max, scale, dt, num_splits, _addr(ws), nbytes, err, raw)
+    finally:
+        if prev >= 0:
+            torch.cuda.set_device(prev)
     _check(st, "decode_attn_q8b")
     return out
 
@@ -822,14 +836,20 @@ def kv_append_q8b(k_new: torch.Tensor, v_new: torch.Tensor, K: torch.Tensor, V: 
             raise ValueError("k_new and v_new must be contiguous in their last dimension")
         # a dimension of one element has no step: its stride in the tensor may be anything
         strides.append(_Strides(sb if B > 1 else 0, sh if h_kv > 1 else 0, st if T > 1 else 0))
-    _row_counts("pos", pos, B, device)
-    _row_counts("n_new", n_new, B, device)
-    err = _error_word(dev_error, device)
-    with _CallOn(device, stream) as on:
+    if _bad_seq_lens(pos, B, device):
+        raise ValueError("pos must be a contiguous int32 tensor [B] on the cache's device")
+    if n_new is not None:
+        _row_counts("n_new", n_new, B, device)
+    err = None if dev_error is None else _error_word(dev_error, device)
+    prev = _enter(device)
+    try:
         st = (_lib or load()).kv_append_q8b(
             k_new.data_ptr(), v_new.data_ptr(), strides[0], strides[1], code, T,
             _addr(n_new), K.data_ptr(), V.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), block,
-            pos.data_ptr(), B, h_kv, d, n_max, _Q8_DTYPES[K.dtype], err, on.raw)
+            pos.data_ptr(), B, h_kv, d, n_max, _Q8_DTYPES[K.dtype], err, _raw(stream, device))
+    finally:
+        if prev >= 0:
+            torch.cuda.set_device(prev)
     _check(st, "kv_append_q8b")
 
 
@@ -847,24 +867,31 @@ def kv_read_q8b(K: torch.Tensor, V: torch.Tensor, k_scale: torch.Tensor, v_scale
     if k_out is None or v_out is None:
         if k_out is not None or v_out is not None:
             raise ValueError("give both k_out and v_out, or neither")
-        with torch.cuda.stream(stream):  # (None: the current stream)
+        with _on_stream(stream):
             k_out, v_out = (torch.zeros((B, h_kv, n_max if rows is None else rows, d),
                                         dtype=out_dtype, device=K.device) for _ in range(2))
     T = k_out.shape[2] if k_out.dim() == 4 else -1
     if rows is not None and rows != T:
         raise ValueError("rows disagrees with the outputs")
+    code = _DTYPES.get(k_out.dtype)
     for t in (k_out, v_out):
-        if t.dtype not in _DTYPES or t.dtype is not k_out.dtype or t.shape != (B, h_kv, T, d) \
+        if code is None or t.dtype is not k_out.dtype or t.shape != (B, h_kv, T, d) \
                 or t.get_device() != device or not t.is_contiguous():
             raise ValueError("k_out and v_out must be contiguous float32 or bfloat16 tensors "
                              "[B, h_kv, rows, d] of one type on the cache's device")
-    _row_counts("seq_lens", seq_lens, B, device)
-    _row_counts("row_begin", row_begin, B, device)
-    err = _error_word(dev_error, device)
-    with _CallOn(device, stream) as on:
+    if _bad_seq_lens(seq_lens, B, device) or row_begin is not None \
+            and _bad_seq_lens(row_begin, B, device):
+        raise ValueError("seq_lens and row_begin must be contiguous int32 tensors [B] on the "
+                         "cache's device")
+    err = None if dev_error is None else _error_word(dev_error, device)
+    prev = _enter(device)
+    try:
         st = (_lib or load()).kv_read_q8b(
             K.data_ptr(), V.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), block,
             seq_lens.data_ptr(), _addr(row_begin), k_out.data_ptr(), v_out.data_ptr(),
-            _DTYPES[k_out.dtype], T, B, h_kv, d, n_max, _Q8_DTYPES[K.dtype], err, on.raw)
+            code, T, B, h_kv, d, n_max, _Q8_DTYPES[K.dtype], err, _raw(stream, device))
+    finally:
+        if prev >= 0:
+            torch.cuda.set_device(prev)
     _check(st, "kv_read_q8b")
     return k_out, v_out
