@@ -57,6 +57,56 @@ __device__ __forceinline__ void load_lane(float (&v)[N], const float* p) {
   }
 }
 
+// A warp's scores with score terms.  Each lane has its columns' part of the G x RPW
+// dot products (index g RPW + r); halving exchanges (lane bit 4 keeps the upper half
+// of the indexes, bit 3 the upper half of those, ...) leave lane i with the whole
+// sums of indexes i S / 32 on, VPL of them, or the same one on DUP lanes: 31 shuffles
+// for 32 scores instead of 160, and a term, an exponential and a mask for one score a
+// lane instead of all 32 on every lane.  4 sequences of 16384 rows, 4 kv heads of 8
+// query heads, capped: 65.6 us, against 248.7 us with whole sums on every lane.
+//
+// The running maximum follows a larger score only when some head's grew by more than
+// kLazyMax (a weight is at most 2^4 then, exact in the ratio of the two sums), so that
+// most stages do without the exchange of the maximum and the rescaling.
+constexpr float kLazyMax = 4.f;
+template <int G, int RPW>
+struct LaneScores {
+  static constexpr int S = G * RPW;
+  static constexpr int VPL = S > 32 ? S / 32 : 1;
+  static constexpr int DUP = S < 32 ? 32 / S : 1;
+  static constexpr int kHeadLanes = RPW * DUP / VPL;  // lanes of one head's scores
+  static __device__ __forceinline__ int index(int lane, int j) { return lane / DUP * VPL + j; }
+  static __device__ __forceinline__ void reduce(float (&v)[S], int lane) {
+    int n = S;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      if (n > VPL) {
+        n >>= 1;
+        const bool up = lane & o;
+#pragma unroll
+        for (int i = 0; i < S / 2; ++i)
+          if (i < n) {
+            const float send = up ? v[i] : v[i + n], keep = up ? v[i + n] : v[i];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+          }
+      } else {
+        v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+      }
+    }
+  }
+  // The largest, or the sum, of a value over a head's lanes.
+  static __device__ __forceinline__ float head_max(float x) {
+#pragma unroll
+    for (int o = DUP; o < kHeadLanes; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+    return x;
+  }
+  static __device__ __forceinline__ float head_sum(float x) {
+#pragma unroll
+    for (int o = DUP; o < kHeadLanes; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+  }
+};
+
 template <class Cfg, int TERMS>
 __global__ void __launch_bounds__(Cfg::kThreads, 1)
     split_decode_f32_kernel(const __grid_constant__ CUtensorMap tmK,
@@ -137,11 +187,12 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
     // the log2 domain) arrives with the item's first stage.
     float qv[G][EPL];
 
-    [[maybe_unused]] float slope[G];
+    using LS = LaneScores<G, RPW>;
+    // with terms: this lane's head's bias, running maximum and sum
+    [[maybe_unused]] float slope = 0.f, m_lane = -INFINITY, l_lane = 0.f;
     if constexpr (SLOPES) {
-#pragma unroll
-      for (int g = 0; g < G; ++g)
-        slope[g] = head_slope(p, it.kvh * p.group + head_base + g, head_base + g < p.group);
+      const int hl = head_base + LS::index(lane, 0) / RPW;
+      slope = head_slope(p, it.kvh * p.group + hl, hl < p.group);
     }
 
     float m_run[G], l_run[G], acc[G][EPL];
@@ -213,7 +264,69 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
       } else {
         seen >>= RPW - min(max(valid - row0, 0), RPW);
       }
-      if (live && seen) {
+      if (MOD && live && seen) {
+        if constexpr (MOD) {
+          float v[LS::S];
+#pragma unroll
+          for (int rr = 0; rr < RPW; ++rr) {
+            float kv[EPL];
+            load_lane<EPL>(kv, ks + (row0 + rr) * D + lane * EPL);
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+              float x = 0.f;
+#pragma unroll
+              for (int e = 0; e < EPL; ++e) x = fmaf(qv[g][e], kv[e], x);
+              v[g * RPW + rr] = x;
+            }
+          }
+          LS::reduce(v, lane);
+          float mx = -INFINITY;
+#pragma unroll
+          for (int j = 0; j < LS::VPL; ++j) {
+            const int rr = LS::index(lane, j) % RPW;
+            if constexpr (CAP) v[j] = p.mod.cap_log2 * tanh_fast(v[j]);
+            if constexpr (SLOPES)
+              v[j] = biased(v[j], RowDistance(it, mask.row0 + row0 + rr), slope, false);
+            v[j] = (seen >> rr & 1u) ? v[j] : -INFINITY;
+            mx = fmaxf(mx, v[j]);
+          }
+          if (__any_sync(0xffffffffu, mx > m_lane + kLazyMax)) {
+            const float m_new = fmaxf(m_lane, LS::head_max(mx));
+            const float alpha = ex2(m_lane - (m_new == -INFINITY ? 0.f : m_new));
+            m_lane = m_new;
+            l_lane *= alpha;
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+              const float f = __shfl_sync(0xffffffffu, alpha, g * LS::kHeadLanes);
+#pragma unroll
+              for (int e = 0; e < EPL; ++e) acc[g][e] *= f;
+            }
+          }
+          const float m_use = m_lane == -INFINITY ? 0.f : m_lane;
+#pragma unroll
+          for (int j = 0; j < LS::VPL; ++j) {
+            v[j] = ex2(v[j] - m_use);
+            l_lane += v[j];
+          }
+#pragma unroll
+          for (int rr = 0; rr < RPW; ++rr) {
+            float w[G];
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+              const int at = g * RPW + rr;
+              w[g] = __shfl_sync(0xffffffffu, v[at % LS::VPL], at / LS::VPL * LS::DUP);
+            }
+            if (seen >> rr & 1u) {
+              float vv[EPL];
+              load_lane<EPL>(vv, vs + (row0 + rr) * D + lane * EPL);
+#pragma unroll
+              for (int g = 0; g < G; ++g)
+#pragma unroll
+                for (int e = 0; e < EPL; ++e) acc[g][e] = fmaf(w[g], vv[e], acc[g][e]);
+            }
+          }
+        }
+      } else if (!MOD && live && seen) {
         // Step I: s[g][r] = (scale*log2e*q_g) . K_row, reduced across the warp.
         float s[G][RPW];
 #pragma unroll
@@ -228,10 +341,6 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
             s[g][rr] = x;
           }
         }
-        [[maybe_unused]] const auto dist = [&] {
-          if constexpr (SLOPES) return RowDistance(it, mask.row0 + row0);
-          else return 0;
-        }();
 #pragma unroll
         for (int g = 0; g < G; ++g)
 #pragma unroll
@@ -242,8 +351,6 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
             x += __shfl_xor_sync(0xffffffffu, x, 4);
             x += __shfl_xor_sync(0xffffffffu, x, 2);
             x += __shfl_xor_sync(0xffffffffu, x, 1);
-            if constexpr (CAP) x = p.mod.cap_log2 * tanh_fast(x);
-            if constexpr (SLOPES) x = biased(x, RowDistance(dist, rr), slope[g], false);
             s[g][rr] = (seen >> rr & 1u) ? x : -INFINITY;
           }
         // Step II: running max and sum (warp-uniform values).
@@ -290,7 +397,13 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
 
     // Epilogue: merge the W warps, normalise, store.
     named_bar_sync(1, Cfg::kConsumerThreads);
-    if (lane == 0) {
+    if constexpr (MOD) {
+      l_lane = LS::head_sum(l_lane);
+      if (lane % LS::kHeadLanes == 0) {
+        epi_m[warp * G + lane / LS::kHeadLanes] = m_lane;
+        epi_l[warp * G + lane / LS::kHeadLanes] = l_lane;
+      }
+    } else if (lane == 0) {
 #pragma unroll
       for (int g = 0; g < G; ++g) {
         epi_m[warp * G + g] = m_run[g];
