@@ -581,10 +581,11 @@ def _bad_seq_lens(t: torch.Tensor, B: int, device: int) -> bool:
 
 
 def _out_on(out: torch.Tensor | None, out_dtype: torch.dtype | None, B: int, h_q: int, d_v: int,
-            q: torch.Tensor, device: int):
-    """The output tensor (allocated when None) and its dtype flag."""
+            q: torch.Tensor, device: int, stream):
+    """The output tensor (allocated when None, in the call's stream) and its dtype flag."""
     if out is None:
-        out = torch.empty((B, h_q, d_v), dtype=out_dtype or torch.float32, device=q.device)
+        with _on_stream(stream):
+            out = torch.empty((B, h_q, d_v), dtype=out_dtype or torch.float32, device=q.device)
     dtype = out.dtype
     if out.shape != (B, h_q, d_v) or out.get_device() != device or not out.is_contiguous() \
             or (dtype is not torch.bfloat16 and dtype is not torch.float32) \
@@ -594,7 +595,7 @@ def _out_on(out: torch.Tensor | None, out_dtype: torch.dtype | None, B: int, h_q
     return out, (DA_OUT_BF16 if dtype is torch.bfloat16 else 0)
 
 
-def _cache_args(q, K, V, seq_lens, out, out_dtype):
+def _cache_args(q, K, V, seq_lens, out, out_dtype, stream):
     """Checks of a decode over an fp32 or bf16 cache: its sizes, the output, the dtype code.
     (A step's host time is mostly these checks and the launches: 2 us of about 11.)"""
     device = q.get_device()
@@ -614,7 +615,7 @@ def _cache_args(q, K, V, seq_lens, out, out_dtype):
         raise ValueError("q, K and V must be contiguous CUDA tensors on one device")
     if _bad_seq_lens(seq_lens, B, device):
         raise ValueError("seq_lens must be a contiguous int32 tensor [B] on the device of the others")
-    out, oflag = _out_on(out, out_dtype, B, h_q, d_v, q, device)
+    out, oflag = _out_on(out, out_dtype, B, h_q, d_v, q, device, stream)
     return device, out, (B, h_q, h_kv, d_k, d_v, n_max), code | oflag
 
 
@@ -684,7 +685,7 @@ def decode_attn_mod(q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, seq_lens:
                     out_dtype: torch.dtype | None = None) -> torch.Tensor:
     """``decode_attn`` with score terms (calls ``decode_attn_mod``): capped scores, a distance
     bias, a window, documents and an always-seen prefix, as ``mod`` says.  Returns ``out``."""
-    device, out, dims, dt = _cache_args(q, K, V, seq_lens, out, out_dtype)
+    device, out, dims, dt = _cache_args(q, K, V, seq_lens, out, out_dtype, stream)
     cm = _c_mod(mod, dims[0], dims[1], device)
     err = None if dev_error is None else _error_word(dev_error, device)
     if scale is None:
@@ -715,7 +716,7 @@ def decode_attn_mod_append(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Te
     """``decode_attn_append`` with score terms (calls ``decode_attn_mod_append``): row
     seq_lens[b] of every kv head is appended, and the query sees what ``mod`` says of the
     seq_lens[b] + 1 rows.  Returns ``out``."""
-    device, out, dims, dt = _cache_args(q, K, V, seq_lens, out, out_dtype)
+    device, out, dims, dt = _cache_args(q, K, V, seq_lens, out, out_dtype, stream)
     B, h_q, h_kv, d_k, d_v, _ = dims
     if k_new.shape != (B, h_kv, d_k) or v_new.shape != (B, h_kv, d_v):
         raise ValueError("k_new/v_new must be [B, h_kv, d]")
@@ -781,7 +782,7 @@ def decode_attn_q8b(q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, k_scale: 
         raise ValueError("q must be a contiguous bfloat16 tensor [B, h_q, d] on the cache's device")
     if _bad_seq_lens(seq_lens, B, device):
         raise ValueError("seq_lens must be a contiguous int32 tensor [B] on the cache's device")
-    out, oflag = _out_on(out, out_dtype, B, h_q, d, q, device)
+    out, oflag = _out_on(out, out_dtype, B, h_q, d, q, device, stream)
     dt = _Q8_DTYPES[K.dtype] | oflag
     cm = None if mod is None else _c_mod(mod, B, h_q, device)
     err = None if dev_error is None else _error_word(dev_error, device)

@@ -475,7 +475,8 @@ int run_decode(const void* q, const void* K, const void* V, const int32_t* seq_l
   if (qa && row_off != 0) return DA_ERR_UNSUPPORTED;
   if (k_new && (row_off != 0 || row_lim < n_max)) return DA_ERR_SHAPE;
   if (!isfinite(scale)) return DA_ERR_SHAPE;
-  if (mod && mod->softcap > 0.f && !isfinite(float(double(scale) / double(mod->softcap))))
+  // (the kernels hold 2 log2(e) scale / softcap in float)
+  if (mod && mod->softcap > 0.f && !isfinite(float(4.0 * double(scale) / double(mod->softcap))))
     return DA_ERR_SHAPE;
   if (!aligned16(q) || !aligned16(K) || !aligned16(V) || !aligned16(out) ||
       (workspace && !aligned16(workspace)))

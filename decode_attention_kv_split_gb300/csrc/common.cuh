@@ -582,9 +582,12 @@ struct TileMask<true> {
   }
 };
 
-// A query head's distance bias per row in the log2 domain (0: none).
+// A query head's distance bias per row in the log2 domain (0: none), kept finite: times
+// a distance of zero it has to give zero.
 __device__ __forceinline__ float head_slope(const SplitParams& p, int head, bool ok) {
-  return p.mod.slopes && ok ? __ldg(p.mod.slopes + head) * 1.4426950408889634f : 0.f;
+  if (!p.mod.slopes || !ok) return 0.f;
+  const float s = __ldg(p.mod.slopes + head) * 1.4426950408889634f;
+  return fminf(fmaxf(s, -3e38f), 3e38f);
 }
 
 // The distances of a cache row that the biases multiply.  A bias is zero at the

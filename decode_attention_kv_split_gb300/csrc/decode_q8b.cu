@@ -289,7 +289,11 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::CTAS)
   constexpr int KIND = Cfg::KIND;
   constexpr bool MOD = TERMS != 0, CAP = (TERMS & kTermsCap) != 0,
                  SLOPES = (TERMS & kTermsSlopes) != 0;
-  constexpr float kLazy = 8.f;      // log2 of how far a weight may exceed 1
+  // Weights are taken against 2^-kHead of the maximum, so that those far below it, and
+  // those of a block whose V scale is far below another's, keep their digits in fp16:
+  // its subnormals begin 2^21 below the largest, 2^14 without.
+  constexpr float kHead = 7.f;
+  constexpr float kLazy = 8.f;      // log2 of how far a weight may exceed 2^kHead
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -596,7 +600,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::CTAS)
       // The maximum is kept lazily: only where some score is more than 2^kLazy
       // above it does a vote bring the exact one (three shuffles a head) and the
       // rescaling.  Every weight and sum is taken against the maximum as it
-      // stands; weights reach 2^kLazy, well inside fp16.
+      // stands (m_run: kHead below it); weights reach 2^15, inside fp16's 65504.
       bool over = false;
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
@@ -604,7 +608,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::CTAS)
         for (int j = 0; j < 2; ++j) {
           const float mx =
               fmaxf(fmaxf(s[0][nb][j], s[0][nb][j + 2]), fmaxf(s[1][nb][j], s[1][nb][j + 2]));
-          over |= mx > m_run[nb][j] + kLazy;
+          over |= mx > m_run[nb][j] + (kHead + kLazy);
         }
       // the V scales in units of the accumulator (the same on every lane)
       const float avs = fmaxf(fabsf(vs[0]), fabsf(vs[1]));
@@ -625,7 +629,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::CTAS)
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-            const float m_new = fmaxf(m_run[nb][j], mx);
+            const float m_new = fmaxf(m_run[nb][j], mx - kHead);
             const float alpha = ex2(m_run[nb][j] - (m_new == -INFINITY ? 0.f : m_new));
             m_run[nb][j] = m_new;
             l_run[nb][j] *= alpha;

@@ -294,8 +294,9 @@ __global__ void __launch_bounds__(kWriteThreads, write_ctas<D, XBF16>())
         for (int e = 0; e < 4; ++e) {
           float f[4];
           from_codes<KIND>(word_of(old, e), f);
-          w[e] = to_codes<KIND>(clamp_code<KIND>(f[0] * ratio), clamp_code<KIND>(f[1] * ratio),
-                                clamp_code<KIND>(f[2] * ratio), clamp_code<KIND>(f[3] * ratio), 1.f);
+          if constexpr (KIND == 1)  // (int8's -128)
+            for (float& x : f) x = clamp_code<KIND>(x * ratio);
+          w[e] = to_codes<KIND>(f[0], f[1], f[2], f[3], KIND == 1 ? 1.f : ratio);
         }
         *at = make_uint4(w[0], w[1], w[2], w[3]);
       }

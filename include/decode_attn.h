@@ -359,8 +359,8 @@ DA_API int kv_quantize(const void* x, int x_dtype, void* codes, float* scales, l
  * The softmax runs over the seen rows; none seen gives out = 0.  Rows that are
  * not seen are not read into results (they may hold anything, including NaN),
  * and whole stages of them are not loaded.
- *   softcap   : 0 for none, else in [1e-30, 1e30], with scale / softcap finite
- *               in float
+ *   softcap   : 0 for none, else in [1e-30, 1e30], with 4 * scale / softcap
+ *               finite in float
  *   window    : the last `window` rows are seen; 0 for all
  *   prefix    : the first `prefix` rows are seen whatever the window and the
  *               document (a shared prompt, or the rows a window keeps)
@@ -415,8 +415,12 @@ DA_API int decode_attn_mod_append(const void* q, const void* k_new, const void* 
 /* Decode over a block-scaled cache; mod is nullable (plain scores); other
  * arguments, workspace and errors as decode_attn_q8_ex and decode_attn_mod.
  * Scales of blocks that hold a seen row must be finite; they may be of any
- * size, zero or not a power of two.  q is multiplied as fp16: exact for
- * |q| in [2^-14, 65504]. */
+ * size, zero or not a power of two.  Weights are multiplied as fp16 (two terms
+ * for a float32 out): a row's weight times its V scale keeps 2^-12 (2^-22) of
+ * itself down to about 2^-21 (2^-10) of the largest weight times the largest V
+ * scale that the query's head sees, and 2^-32 of that below.  q is multiplied as
+ * fp16: exact for |q| in [2^-14, 65504].  num_splits = -1 acts as 0: one CTA
+ * takes each chunk, and the kernel picks the chunks from the lengths. */
 DA_API size_t decode_attn_q8b_workspace_bytes(const da_score_mod* mod, int B, int h_q, int h_kv,
                                               int d_k, int d_v, int n_max, int dtype,
                                               int num_splits, int* status);
@@ -437,7 +441,8 @@ DA_API int decode_attn_q8b(const void* q, const void* K, const void* V, const fl
  *   s'   = max(s, need), s the block's scale, or 0 when it holds no row before
  *          pos[b]
  *   new rows: code = round-to-nearest-even(x / s'), clamped to [-Q, Q]; 0 for s' = 0
- *   rows the block already holds, when s' > s: code = round(code * (s / s'))
+ *   rows the block already holds, when s' > s: code = round(code * (s / s'));
+ *          a NaN of e4m3 stays one (s: finite, >= 0)
  * Rows at or past pos[b] + m and the scales of untouched blocks are left as
  * they are.
  *   k_new, v_new : device rows [B, h_kv, T, d] of x_dtype (DA_FP32 or DA_BF16),
@@ -448,7 +453,8 @@ DA_API int decode_attn_q8b(const void* q, const void* K, const void* V, const fl
  *   pos          : device int32 [B], the rows each sequence holds.  Rows that
  *                  would reach past n_max are not written, a pos outside
  *                  [0, n_max] writes nothing, an n_new outside [0, T] is
- *                  clamped; each sets DA_DEVERR_POS.
+ *                  clamped; each sets DA_DEVERR_POS.  The pos of a sequence
+ *                  with m = 0 is not looked at.
  *   NaN and infinite elements are written as 0 and set DA_DEVERR_VALUE.
  * Does not change lengths: the caller advances them.  T = 0 does nothing.
  */

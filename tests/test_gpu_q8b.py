@@ -170,6 +170,21 @@ def test_write_of_values_that_are_none(dtype):
         assert torch.equal(a, b)
 
 
+def test_held_nan_codes_stay():
+    """A block from elsewhere that holds NaN codes: its scale grows, the NaN rows still read as NaN."""
+    K, V, ks, vs = random_cache(1, 1, 64, 64, 32, torch.float8_e4m3fn, 3)
+    K.view(torch.uint8)[0, 0, 3, 7] = 0x7f
+    K.view(torch.uint8)[0, 0, 40, 0] = 0xff
+    nan = torch.isnan(K.float())
+    Kd, Vd, ksd, vsd = K.cuda(), V.cuda(), ks.cuda(), vs.cuda()
+    x = torch.full((1, 1, 2, 64), 1e6, device="cuda")
+    for pos in (20, 50):
+        api.kv_append_q8b(x, x, Kd, Vd, ksd, vsd, i32([pos]), 32)
+        nan[0, 0, pos:pos + 2] = False
+    assert bool((ksd.cpu() > ks).all())
+    assert torch.equal(torch.isnan(Kd.cpu().float()), nan)
+
+
 def test_write_of_broadcast_and_single_rows():
     """Strides of zero, and [B, h_kv, d] rows."""
     x = torch.randn(1, 1, 1, 64, device="cuda").expand(3, 2, 5, 64)
@@ -368,6 +383,42 @@ def test_decode_scales_of_any_size(dtype):
         vs[:, :, 1] *= -1
         return ks, vs
     decode_case(*shape, dtype, 16, scales=some_zero)
+
+
+@pytest.mark.parametrize("out_dtype", [torch.float32, torch.bfloat16], ids=["fp32", "bf16"])
+@pytest.mark.parametrize("far", [0, 8])
+@pytest.mark.parametrize("dtype", KINDS, ids=KID)
+def test_decode_behind_a_much_larger_scale(dtype, far, out_dtype):
+    """The weight lies on block 1 alone, and block `far`, seen by the same warp with no weight, has
+    a V scale 2^k times as large: the output keeps its digits.
+
+    Bound, relative to block 1's largest value: the 16 rows' scores are equal, so their weights
+    are off by fp16 alone, 2^-22 in two parts and 2^-12 in one, or by half a step of fp16's
+    subnormals, 2^-25, against the 2^(7 - k) that a row's weight counts in units of the large
+    scale; 16 products and the merge, under 64 float roundings of 2^-24; the output's own
+    rounding."""
+    d, n, block = 64, 200, 16
+    for k in (0, 8, 12, 16, 20):
+        K, V, ks, vs = random_cache(1, 1, n, d, block, dtype, k + 1)
+        K = torch.zeros(1, 1, n, d)
+        K[..., 0] = -100.0
+        K[0, 0, 16:32, 0] = 100.0
+        K = K.to(dtype)
+        kv = float(K[0, 0, 16, 0].float())
+        ks = torch.full_like(ks, 0.1)
+        vs = torch.full_like(vs, 2.0 ** -9)
+        vs[0, 0, far] = 2.0 ** (k - 9)
+        q = torch.zeros(1, 2, d, dtype=torch.bfloat16)
+        q[..., 0] = 8.0 * 100.0 / kv
+        out = api.decode_attn_q8b(q.cuda(), K.cuda(), V.cuda(), ks.cuda(), vs.cuda(), i32([n]), block, scale=1.0,
+                                  out_dtype=out_dtype).cpu().double()
+        rows = V[0, 0, 16:32].double() * 2.0 ** -9
+        want = rows.mean(0).expand(2, d)
+        # (the other rows: weights of e^-160, times 2^20, are nothing)
+        part = 2.0 ** -22 if out_dtype == torch.float32 else 2.0 ** -12 + torch.finfo(out_dtype).eps / 2
+        tol = float(rows.abs().max()) * (part + 2.0 ** (k - 32) + 64 * 2.0 ** -24)
+        err = float((out[0] - want).abs().max())
+        assert err <= tol, (k, err, tol)
 
 
 def test_decode_batch_above_one_launch_and_many_items():

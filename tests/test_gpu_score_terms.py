@@ -230,6 +230,27 @@ def test_bias_where_far_rows_win():
                  "window": 3000}, splits=3)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["fp32", "bf16"])
+@pytest.mark.parametrize("heads", EDGE, ids=["g4", "g32", "mha"])
+@pytest.mark.parametrize("slope", [3.4e38, -3.4e38])
+def test_largest_slopes(heads, dtype, slope):
+    """One row is all that counts: the last one, or the first that is seen."""
+    lens, h_q = [300, 77][:heads[0]], heads[1]
+    run(*heads, 300, lens, dtype, {"slopes": [slope] * h_q})
+    run(*heads, 300, lens, dtype, {"slopes": [slope] * h_q, "window": 40, "softcap": 9.0})
+
+
+def test_output_allocated_for_a_stream():
+    q, K, V, *_ = make(2, 8, 2, 128, 128, 300, [300, 9], torch.bfloat16, 3, {}, False)
+    q, K, V, l = q.cuda(), K.cuda(), V.cuda(), torch.tensor([300, 9], dtype=torch.int32, device="cuda")
+    want = api.decode_attn_mod(q, K, V, l, ScoreMod(window=90))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = api.decode_attn_mod(q, K, V, l, ScoreMod(window=90), stream=side)
+    side.synchronize()
+    assert torch.equal(got, want)
+
+
 def test_bf16_output_and_scales():
     for shape in (SHAPES[8], SHAPES[11]):
         run(*shape, {"softcap": 10.0, "window": 300}, out_dtype=torch.bfloat16)

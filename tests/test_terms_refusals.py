@@ -46,6 +46,7 @@ def test_score_terms(lib):
     assert _mod(lib, _cmod(), n_max=0) == -2
     assert _mod(lib, _cmod(), scale=nan) == -2
     assert _mod(lib, _cmod(softcap=1e-30), scale=1e10) == -2   # scale / softcap overflows
+    assert _mod(lib, _cmod(softcap=1e-30), scale=2e8) == -2    # 2 log2(e) of it does
     m = ctypes.byref(_cmod())
 
     def app(k_new=OK, lens_out=None, mod=m):
