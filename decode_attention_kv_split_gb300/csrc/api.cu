@@ -288,6 +288,24 @@ bool single_split_suffices(long long units, int n_max, int chunk_min, int tile, 
 // Block-scaled caches (see make_plan): the most bytes of partials.
 constexpr long long kBlockPartialBytes = 64LL << 20;
 
+// With score terms or block scales: the most rows that one CTA per unit takes where
+// there are no more units than SMs.  A second launch costs a step 4 us of host time,
+// and 1.5 to 2 us of the GPU's in a graph; one CTA streams these rows in about 3 us.
+// Measured at 1 and 8 sequences, one split against the cost model's choice: a call by
+// itself 2 to 5 us faster up to here, a step of a graph between 1.6 us faster and 0.6
+// slower; at twice the rows a graph's step 2 to 5 us slower.
+//   8-bit blocks: 5 to 8 ns a row, 10 for more than 8 heads a KV head
+//   bf16: 5 ns a row, 9 in the tcgen05 kernel, 12 for d = 256 or 32 heads of 64
+//   fp32: 8 ns a row for one head of 64, 10 for two or one of 128, 20 to 30 for more
+int single_split_rows(const KernelShape& ks, bool tc5, int dtype, int d, int d_v, int group,
+                      bool block) {
+  if (block) return group <= 8 ? 512 : 384;
+  if (dtype == DA_BF16)
+    return tc5 ? 512 : d + d_v > 256 || ks.heads_per_cta > 16 ? 256 : ks.heads_per_cta > 8 ? 384 : 512;
+  const int products = ks.heads_per_cta * d;
+  return products <= 64 ? 384 : products <= 128 ? 192 : 128;
+}
+
 // Splits per sequence requested by the caller -> a split length that is a
 // whole number of pipeline stages, as close as possible to n_max / S.  When
 // the library chooses, the device picks the length from the actual sequence
@@ -346,7 +364,9 @@ int make_plan(int B, int h_q, int h_kv, int d, int d_v, int n_max, int dtype_arg
                                  ((long long)pl->batch_per_launch * h_q * (d_v + 1) * 4);
       if (most > by_rows) most = by_rows;
       if (most > by_bytes) most = by_bytes;
-      if (n_max <= 2 * da::kBlockMinRows || most < 2) most = 1;
+      if (most < 2 || n_max <= 2 * da::kBlockMinRows ||
+          (units <= sms && n_max <= single_split_rows(pl->ks, pl->tc5, dtype, d, d_v, group, true)))
+        most = 1;
       pl->chunk_fixed = 0;
       pl->chunk_min = int(((n_max + most - 1) / most + tile - 1) / tile * tile);
       if (most == 1) {  // no partials, no combine
@@ -387,7 +407,11 @@ int make_plan(int B, int h_q, int h_kv, int d, int d_v, int n_max, int dtype_arg
     const long long per = (n_max + cap - 1) / cap;
     pl->chunk_fixed = 0;
     pl->chunk_min = int((per + tile - 1) / tile * tile);
-    if (single_split_suffices(units, n_max, pl->chunk_min, int(tile), sms, pl->ks.cta_speed)) {
+    if (seen >= 0 && units <= sms &&
+        n_max <= single_split_rows(pl->ks, pl->tc5, dtype, d, d_v, group, false)) {
+      pl->chunk_fixed = pl->chunk_min = int(max_tiles * tile);
+    } else if (single_split_suffices(units, n_max, pl->chunk_min, int(tile), sms,
+                                     pl->ks.cta_speed)) {
       // One split per unit needs no partials and no combine, but when the
       // units fill the grid's rounds unevenly (fewer units than CTAs, or a
       // ragged last round) the CTAs without a unit idle while the longest
