@@ -246,7 +246,7 @@ struct Plan {
   int batch_per_launch;
   bool balanced;       // num_splits = -1: one equal piece of all rows per CTA
   int units;           // (sequence, kv head, head chunk) units of one launch slice
-  int places, rounds;  // block-scaled caches: see SplitParams
+  int places, rounds, cluster;  // block-scaled caches: see SplitParams
   long long grid;      // block-scaled caches: CTAs of a full launch slice
 };
 
@@ -288,8 +288,9 @@ bool single_split_suffices(long long units, int n_max, int chunk_min, int tile, 
 // Block-scaled caches (see make_plan): the most bytes of partials.
 constexpr long long kBlockPartialBytes = 64LL << 20;
 
-// With score terms or block scales: the most rows that one CTA per unit takes where
-// there are no more units than SMs.  A second launch costs a step 4 us of host time,
+// With score terms or block scales: the most rows that one CTA takes by itself where
+// there are no more units than SMs (of 8-bit blocks: each CTA of a unit's cluster).  A
+// second launch costs a step 4 us of host time,
 // and 1.5 to 2 us of the GPU's in a graph; one CTA streams these rows in about 3 us.
 // Measured at 1 and 8 sequences, one split against the cost model's choice: a call by
 // itself 2 to 5 us faster up to here, a step of a graph between 1.6 us faster and 0.6
@@ -333,7 +334,7 @@ int make_plan(int B, int h_q, int h_kv, int d, int d_v, int n_max, int dtype_arg
   if (seen >= 0 && seen + 2 * tile < n_max) n_max = int(seen + 2 * tile);
   const long long max_tiles = (n_max + tile - 1) / tile;
   pl->balanced = false;
-  pl->places = pl->rounds = 0;
+  pl->places = pl->rounds = pl->cluster = 0;
   pl->grid = 0;
   pl->units = int((long long)pl->batch_per_launch * h_kv * pl->head_chunks);
   if (requested < -1) return DA_ERR_SHAPE;
@@ -364,9 +365,25 @@ int make_plan(int B, int h_q, int h_kv, int d, int d_v, int n_max, int dtype_arg
                                  ((long long)pl->batch_per_launch * h_q * (d_v + 1) * 4);
       if (most > by_rows) most = by_rows;
       if (most > by_bytes) most = by_bytes;
-      if (most < 2 || n_max <= 2 * da::kBlockMinRows ||
-          (units <= sms && n_max <= single_split_rows(pl->ks, pl->tc5, dtype, d, d_v, group, true)))
-        most = 1;
+      if (most < 2 || n_max <= 2 * da::kBlockMinRows) most = 1;
+      // Short caches: a cluster of CTAs for each unit, which join its chunks themselves:
+      // one launch, no work list and no partials (one sequence of 1024 rows, 8 kv heads
+      // of 128: a graph's step 6.4 -> 4.6 us, a call by itself 25.3 -> 21.2; 16 of 512
+      // rows, 2 kv heads of 64 with 32 query heads: 9.2 -> 4.7 us).  Two CTAs on an SM
+      // cost more than they share (4 of 1024 rows, 8 kv heads: 8 a unit 6.5 us, 4 5.8).
+      const int alone = single_split_rows(pl->ks, pl->tc5, dtype, d, d_v, group, true);
+      long long c = (n_max + da::kBlockMinRows - 1) / da::kBlockMinRows;  // as many as have rows
+      if (c * units > sms) c = sms / units;             // while each has an SM,
+      const long long least = (n_max + alone - 1) / alone;
+      if (c < least) c = least;                         // and more where the rows ask for it
+      if (c > 8) c = 8;
+      if (n_max <= c * alone && c * units <= (c == 1 ? sms : places)) pl->cluster = int(c);
+      if (pl->cluster > 0) {
+        pl->chunk_fixed = pl->chunk_min = int((n_max + tile - 1) / tile * tile);
+        pl->grid = units * pl->cluster;
+        pl->max_splits = 1;
+        return DA_OK;
+      }
       pl->chunk_fixed = 0;
       pl->chunk_min = int(((n_max + most - 1) / most + tile - 1) / tile * tile);
       if (most == 1) {  // no partials, no combine
@@ -568,6 +585,7 @@ int run_decode(const void* q, const void* K, const void* V, const int32_t* seq_l
     p.scale_elems = (long long)B * h_kv * p.nblk;
     p.places = pl.places;
     p.rounds = pl.rounds;
+    p.cluster = pl.cluster;
     p.B = bn;
     p.h_q = h_q;
     p.h_kv = h_kv;

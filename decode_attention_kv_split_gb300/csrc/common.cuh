@@ -61,6 +61,7 @@ struct SplitParams {
   // one for 2^blk_shift consecutive rows.
   int nblk, blk_shift;
   int places, rounds;            // CTAs the GPU holds at once; most rounds of them in the grid
+  int cluster;                   // > 0: a cluster of this many CTAs for each unit (short caches)
   long long scale_elems;         // elements of k_scale, for the checked build
   int append;
   int out_bf16;                  // out holds bf16 (rounded once from the fp32 result)
@@ -1461,20 +1462,31 @@ cudaError_t set_smem_limit_once(void (*kernel)(Params...), size_t smem,
 // run griddepcontrol.launch_dependents, or exited) and must execute
 // griddepcontrol.wait before it reads anything that grid wrote or writes
 // anything it reads.
+// cluster > 1: in clusters of that many CTAs.
 template <class... Params, class... Args>
-cudaError_t launch_dependent(void (*kernel)(Params...), int grid, int threads, size_t smem,
-                             cudaStream_t stream, Args&&... args) {
+cudaError_t launch_dependent_clusters(void (*kernel)(Params...), int grid, int cluster, int threads,
+                                      size_t smem, cudaStream_t stream, Args&&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(grid));
   cfg.blockDim = dim3(unsigned(threads));
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = unsigned(cluster);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<Args&&>(args)...);
+}
+
+template <class... Params, class... Args>
+cudaError_t launch_dependent(void (*kernel)(Params...), int grid, int threads, size_t smem,
+                             cudaStream_t stream, Args&&... args) {
+  return launch_dependent_clusters(kernel, grid, 1, threads, smem, stream,
+                                   static_cast<Args&&>(args)...);
 }
 
 // ---------------------------------------------------------------------------

@@ -26,6 +26,9 @@
 // two, 6.4 TB/s; ncu on it: DRAM 77 % busy, 1.4 instructions a cycle of 4, the MMA
 // pipe 17 %).  With 32 heads on one kv head the MMAs and the instructions around
 // them, not HBM, are the bound: 31.4 us for 8 x 30000 rows, 9.2 us of HBM time.
+// Caches of up to 4096 rows with few enough units (make_plan) need no list: a cluster
+// of up to eight CTAs takes a unit's rows in equal shares and joins them through
+// distributed shared memory (finish_cluster), without a second kernel.
 // Within a CTA warp w takes the 32-row steps w, w + 4, ... of the chunk and
 // feeds itself: its lane 0 keeps a ring of steps (K and V codes, 2 TMA boxes of
 // 32 rows) in flight on the warp's own barriers, and no warp waits for another
@@ -268,6 +271,127 @@ __device__ __forceinline__ bool find_item_many(const SplitParams& p, int* sm, It
   return true;
 }
 
+// For a cluster per unit: this CTA's item, one share of its sequence's n list rows for
+// each CTA of the cluster, in whole 32-row steps and kBlockMinRows at least.
+template <int ROWS, bool MOD>
+__device__ __forceinline__ void cluster_chunk(const SplitParams& p, int n, ItemT<MOD>& it,
+                                              int& chunk) {
+  chunk = max(kBlockMinRows, (n + p.cluster - 1) / p.cluster);
+  chunk = (chunk + ROWS - 1) / ROWS * ROWS;
+  it.nv = max(1, (n + chunk - 1) / chunk);
+}
+
+// A barrier of all threads of a cluster, after which they see each other's shared memory.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+// Floats of CTA `rank`'s shared memory, at the address they have in this CTA's.
+__device__ __forceinline__ uint32_t cluster_addr(const float* at, int rank) {
+  uint32_t a;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(at)), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ float cluster_ld(const float* at, int rank) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];"
+               : "=f"(v)
+               : "r"(cluster_addr(at, rank))
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 cluster_ld4(const float* at, int rank) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(cluster_addr(at, rank))
+               : "memory");
+  return v;
+}
+
+// The merge of a unit's it.nv chunks, held by the CTAs of a cluster: each brings its
+// warps' states to one accumulator, relative to its own maximum, and then joins the
+// chunks' for its share of the unit's outputs, through distributed shared memory.  Every
+// CTA of the cluster takes part, those without rows too.
+template <int D, int KW, int HPW, int SLOT_STRIDE>
+__device__ __forceinline__ void finish_cluster(const SplitParams& p, const Item& it, float* epi_acc,
+                                               float* epi_m, float* epi_l, int tid, int nthreads,
+                                               volatile int* abort_flag) {
+  static_assert(KW >= 2, "a head's sum and maximum lie in two l slots");
+  const int head0 = it.hc * HPW;
+  const int nh = min(HPW, p.group - head0);
+  if (tid < HPW) {
+    float m[KW], M = -INFINITY, L = 0.f;
+#pragma unroll
+    for (int k = 0; k < KW; ++k) {
+      m[k] = epi_m[k * HPW + tid];
+      M = fmaxf(M, m[k]);
+    }
+    const float M_use = M == -INFINITY ? 0.f : M;
+#pragma unroll
+    for (int k = 0; k < KW; ++k) {
+      const float f = ex2(m[k] - M_use);
+      L += f * epi_l[k * HPW + tid];
+      epi_m[k * HPW + tid] = f;
+    }
+    epi_l[tid] = L;
+    epi_l[HPW + tid] = M;
+  }
+  __syncthreads();
+  // four columns a thread
+  static_assert(SLOT_STRIDE % 4 == 0, "16-byte aligned columns");
+  for (int idx = 4 * tid; idx < nh * D; idx += 4 * nthreads) {
+    const int h = idx / D, d = idx - h * D;
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < KW; ++k) {
+      const float f = epi_m[k * HPW + h];
+      const float4 x =
+          *reinterpret_cast<const float4*>(epi_acc + (k * HPW + h) * SLOT_STRIDE + d);
+      sum.x += f * x.x, sum.y += f * x.y, sum.z += f * x.z, sum.w += f * x.w;
+    }
+    // (this thread's own columns of the first slot)
+    *reinterpret_cast<float4*>(epi_acc + h * SLOT_STRIDE + d) = sum;
+  }
+  cluster_sync();
+  const size_t bh0 = size_t(it.b) * p.h_q + size_t(it.kvh) * p.group + head0;
+  // (consecutive threads of the cluster take consecutive CTAs' shares of a run)
+  for (int idx = 4 * (it.split + p.cluster * tid); idx < nh * D; idx += 4 * p.cluster * nthreads) {
+    const int h = idx / D, d = idx - h * D;
+    float m[8], l[8], M = -INFINITY;  // (a cluster is 8 CTAs at most)
+    float4 a[8];
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      m[r] = -INFINITY, l[r] = 0.f;
+      a[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (r < it.nv) {
+        m[r] = cluster_ld(epi_l + HPW + h, r);
+        l[r] = cluster_ld(epi_l + h, r);
+        a[r] = cluster_ld4(epi_acc + h * SLOT_STRIDE + d, r);
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < 8; ++r) M = fmaxf(M, m[r]);
+    const float M_use = M == -INFINITY ? 0.f : M;
+    float L = 0.f;
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      const float f = ex2(m[r] - M_use);
+      L += f * l[r];
+      sum.x += f * a[r].x, sum.y += f * a[r].y, sum.z += f * a[r].z, sum.w += f * a[r].w;
+    }
+    const float inv = L > 0.f ? __fdividef(1.f, L) : 0.f;
+    if (!*abort_flag) {
+      const size_t at = bh0 * D + idx;
+      store_out(p, at, sum.x * inv);
+      store_out(p, at + 1, sum.y * inv);
+      store_out(p, at + 2, sum.z * inv);
+      store_out(p, at + 3, sum.w * inv);
+    }
+  }
+  cluster_sync();  // no CTA's shared memory goes while another reads it
+}
+
 // Byte offset of 16-byte piece `piece` of row `row` of a box: the 128-byte
 // swizzle for 128-byte rows, the 64-byte swizzle for 64-byte rows.
 template <int D>
@@ -277,7 +401,9 @@ __device__ __forceinline__ int code_at(int row, int piece) {
 }
 
 // SHORT: P without its remainder and capped_short (short_forms, for bf16 outputs).
-template <class Cfg, int TERMS, bool SHORT>
+// CLUSTER: a cluster for each unit (p.cluster > 0; its code in the other kernel cost
+// that one 0.8 %).
+template <class Cfg, int TERMS, bool SHORT, bool CLUSTER>
 __global__ void __launch_bounds__(Cfg::kThreads, Cfg::CTAS)
     split_decode_q8b_kernel(const __grid_constant__ CUtensorMap tmK,
                             const __grid_constant__ CUtensorMap tmV, const SplitParams p) {
@@ -324,7 +450,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::CTAS)
   ItemT<MOD> it;
   int chunk = 0;
   bool any = false;
-  const bool early = int(blockIdx.x) < p.places, few = p.B <= kFewSequences;
+  const bool early = int(blockIdx.x) < p.places, few = !CLUSTER && p.B <= kFewSequences;
   bool bad = false, bad_pos = false;
   int n_out;
   int begin = 0;
@@ -333,8 +459,19 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::CTAS)
     return list_len<ROWS, MOD>(p, begin, __ldcg(p.seq_lens + b), bad, bad_pos, n_out);
   };
   int n_b = 0;
-  if (early) {
-    if (few) {
+  if constexpr (CLUSTER) {  // the units and their CTAs in order
+    const int unit = int(blockIdx.x) / p.cluster;
+    it.split = int(blockIdx.x) - unit * p.cluster;
+    it.hc = unit % p.head_chunks;
+    it.kvh = unit / p.head_chunks % p.h_kv;
+    it.b = unit / p.head_chunks / p.h_kv;
+    any = it.b < p.B;
+  }
+  if (CLUSTER ? any : early) {
+    if constexpr (CLUSTER) {
+      n_b = rows_of(it.b);
+      cluster_chunk<ROWS>(p, n_b, it, chunk);
+    } else if (few) {
       if (lane < p.B) n_b = rows_of(lane);
       any = find_item_few<ROWS>(p, n_b, it, chunk);
     } else {
@@ -346,8 +483,9 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::CTAS)
     // (GQA int8 32.2 -> 31.2 us, long fp8 86.9 -> 84.4; twice as many steps cost the
     // previous grid's last CTAs more than they bring: 33.0 and 83.7 us.)
     if (any) {
-      int n = 0;
-      if (few) {
+      int n = n_b;
+      if constexpr (CLUSTER) {
+      } else if (few) {
         n = __shfl_sync(0xffffffffu, n_b, it.b);
         n_out = __shfl_sync(0xffffffffu, n_out, it.b);
         begin = __shfl_sync(0xffffffffu, begin, it.b);
@@ -373,7 +511,11 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::CTAS)
   allow_dependent_launch();
   int n = 0;  // rows of the chunk's sequence
   n_out = 0;
-  if (few) {
+  if constexpr (CLUSTER) {
+    if (!any) return;
+    n = rows_of(it.b);
+    cluster_chunk<ROWS>(p, n, it, chunk);
+  } else if (few) {
     const int before = n_b;
     if (lane < p.B) n_b = rows_of(lane);
     if (!early || __any_sync(0xffffffffu, n_b != before))
@@ -391,15 +533,16 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::CTAS)
     if (__syncthreads_or(changed)) any = find_item_many<ROWS>(p, find, it, chunk);
     if (any) n = MOD ? rows_of(it.b) : find[it.b];
   }
-  if (bad && blockIdx.x == 0) flag_error(p.dev_error, DA_DEVERR_SEQ_LEN);
+  if (bad && (CLUSTER || blockIdx.x == 0)) flag_error(p.dev_error, DA_DEVERR_SEQ_LEN);
   if (blockIdx.x == 0 && threadIdx.x == 0 && p.chunk_out) *p.chunk_out = chunk;
   if (!any) return;
   if constexpr (MOD) list_rows(p.mod, ROWS, begin, n_out, false, it.rows);
   it.row_begin = it.split * chunk;
   it.row_end = min(n, it.row_begin + chunk);
   it.new_row = -1;
-  if (few) __syncthreads();  // barriers initialised
-  const int steps = (it.row_end - it.row_begin + ROWS - 1) / ROWS;
+  if (few || CLUSTER) __syncthreads();  // barriers initialised
+  int steps = (it.row_end - it.row_begin + ROWS - 1) / ROWS;
+  if (CLUSTER) steps = max(steps, 0);  // (its last CTAs may be past the rows)
   it.tiles = steps > warp ? (steps - warp + KW - 1) / KW : 0;  // this warp's
   // First list row of this warp's i-th step.
   auto step_row = [&](int i) { return it.row_begin + (i * KW + warp) * ROWS; };
@@ -759,8 +902,12 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::CTAS)
       slots[(h0 + 1) * Cfg::kSlotStride + d0 + 1] = acc[mb][nb][3] * unit;
     }
   __syncthreads();
-  finish_item<D, 1, KW, kHPW, Cfg::kSlotStride>(p, it, epi_acc, epi_m, epi_l, threadIdx.x,
-                                                Cfg::kThreads, abort_flag);
+  if (CLUSTER && p.cluster > 1)
+    finish_cluster<D, KW, kHPW, Cfg::kSlotStride>(p, it, epi_acc, epi_m, epi_l, threadIdx.x,
+                                                  Cfg::kThreads, abort_flag);
+  else
+    finish_item<D, 1, KW, kHPW, Cfg::kSlotStride>(p, it, epi_acc, epi_m, epi_l, threadIdx.x,
+                                                  Cfg::kThreads, abort_flag);
 }
 
 // ---------------------------------------------------------------------------
@@ -776,22 +923,26 @@ using Q8BD64N1 = Q8BCfg<64, 1, 3, 4, KIND>;
 template <int KIND>
 using Q8BD64N2 = Q8BCfg<64, 2, 4, 3, KIND>;
 
-template <class Cfg, bool SHORT>
+template <class Cfg, bool SHORT, bool CLUSTER>
 static cudaError_t launch_q8b_form(const SplitParams& p, const CUtensorMap& tk,
                                    const CUtensorMap& tv, int grid, cudaStream_t stream) {
   static std::atomic<unsigned long long> smem_set{0};
-  const cudaError_t e = set_smem_limit_once(split_decode_q8b_kernel<Cfg, DA_TERMS, SHORT>,
-                                            Cfg::kSmemBytes, smem_set);
+  const auto kernel = split_decode_q8b_kernel<Cfg, DA_TERMS, SHORT, CLUSTER>;
+  const cudaError_t e = set_smem_limit_once(kernel, Cfg::kSmemBytes, smem_set);
   if (e != cudaSuccess) return e;
-  return launch_dependent(split_decode_q8b_kernel<Cfg, DA_TERMS, SHORT>, grid, Cfg::kThreads,
-                          Cfg::kSmemBytes, stream, tk, tv, p);
+  return launch_dependent_clusters(kernel, grid, p.cluster, Cfg::kThreads, Cfg::kSmemBytes, stream,
+                                   tk, tv, p);
 }
 
 template <class Cfg>
 static cudaError_t launch_q8b_cfg(const SplitParams& p, const CUtensorMap& tk,
                                   const CUtensorMap& tv, int grid, cudaStream_t stream) {
-  return short_forms(p.out_bf16 != 0, p.mod) ? launch_q8b_form<Cfg, true>(p, tk, tv, grid, stream)
-                                             : launch_q8b_form<Cfg, false>(p, tk, tv, grid, stream);
+  const bool brief = short_forms(p.out_bf16 != 0, p.mod);
+  if (p.cluster > 0)
+    return brief ? launch_q8b_form<Cfg, true, true>(p, tk, tv, grid, stream)
+                 : launch_q8b_form<Cfg, false, true>(p, tk, tv, grid, stream);
+  return brief ? launch_q8b_form<Cfg, true, false>(p, tk, tv, grid, stream)
+               : launch_q8b_form<Cfg, false, false>(p, tk, tv, grid, stream);
 }
 
 template <int KIND>

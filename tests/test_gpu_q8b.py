@@ -385,6 +385,28 @@ def test_decode_scales_of_any_size(dtype):
     decode_case(*shape, dtype, 16, scales=some_zero)
 
 
+@pytest.mark.parametrize("dtype", KINDS, ids=KID)
+def test_decode_chunks_by_length(dtype):
+    """Few sequences of more rows than a cluster takes: chunks from the actual lengths."""
+    decode_case(3, 8, 2, 128, 9000, [9000, 0, 4100], dtype, 16)
+    decode_case(2, 32, 1, 128, 5003, [1, 5003], dtype, 32, {"softcap": 8.0, "window": 4999, "prefix": 130})
+
+
+@pytest.mark.parametrize("dtype", KINDS, ids=KID)
+def test_decode_clusters(dtype):
+    """One to eight CTAs a unit: shares that end with the rows, inside a step and empty ones."""
+    for n in (129, 256, 257, 385, 640, 769, 1024, 1025, 2047, 4096):
+        decode_case(2, 4, 2, 64, n, [n, n // 3], dtype, 16, seed=n)
+    for n in (129, 500, 1024, 3070):
+        decode_case(2, 40, 2, 128, n, [0, n], dtype, 64, seed=n, out_dtype=torch.bfloat16)
+    # an SM or less to each: clusters of three and two, and one CTA each
+    for B in (24, 38, 100):
+        decode_case(B, 4, 2, 64, 400, [(b * 61) % 401 for b in range(B)], dtype, 32, seed=B)
+    # windows: the rows that are seen are shared
+    decode_case(2, 8, 2, 128, 9000, [9000, 700], dtype, 16, {"window": 900, "prefix": 40})
+    decode_case(2, 8, 2, 128, 9000, [9000, 700], dtype, 128, {"window": 1, "prefix": 3000})
+
+
 @pytest.mark.parametrize("out_dtype", [torch.float32, torch.bfloat16], ids=["fp32", "bf16"])
 @pytest.mark.parametrize("far", [0, 8])
 @pytest.mark.parametrize("dtype", KINDS, ids=KID)
