@@ -302,9 +302,39 @@ int single_split_rows(const KernelShape& ks, bool tc5, int dtype, int d, int d_v
                       bool block) {
   if (block) return group <= 8 ? 512 : 384;
   if (dtype == DA_BF16)
-    return tc5 ? 512 : d + d_v > 256 || ks.heads_per_cta > 16 ? 256 : ks.heads_per_cta > 8 ? 384 : 512;
+    return tc5 ? 512 : ks.heads_per_cta > 16 ? 192 : d + d_v > 256 ? 256 : ks.heads_per_cta > 8 ? 384 : 512;
   const int products = ks.heads_per_cta * d;
-  return products <= 64 ? 384 : products <= 128 ? 192 : 128;
+  return products <= 64 ? 384 : products <= 128 ? 192 : products <= 512 ? 128 : 96;
+}
+
+// How many clusters of c CTAs that take an SM each the (current) device runs at once: a
+// cluster lies within one of its groups of SMs, so 152 SMs hold fewer than 19 of 8 (18
+// clusters of 7 or 8 took two rounds, 8.6 us for 4.5).  Asked once per device and c.
+__global__ void whole_sm_kernel() {}
+
+int clusters_at_once(int c, int dev) {
+  static std::atomic<int> known[kMaxDevices][9];
+  int n = known[dev][c].load(std::memory_order_relaxed);
+  if (n > 0) return n;
+  constexpr int kSmem = 200 * 1024;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = unsigned(c);
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(c));
+  cfg.blockDim = dim3(288);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (cudaFuncSetAttribute(whole_sm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) !=
+          cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&n, whole_sm_kernel, &cfg) != cudaSuccess || n < 1) {
+    cudaGetLastError();
+    n = 1;
+  }
+  known[dev][c].store(n, std::memory_order_relaxed);
+  return n;
 }
 
 // Splits per sequence requested by the caller -> a split length that is a
@@ -424,10 +454,23 @@ int make_plan(int B, int h_q, int h_kv, int d, int d_v, int n_max, int dtype_arg
     const long long per = (n_max + cap - 1) / cap;
     pl->chunk_fixed = 0;
     pl->chunk_min = int((per + tile - 1) / tile * tile);
-    if (seen >= 0 && units <= sms &&
-        n_max <= single_split_rows(pl->ks, pl->tc5, dtype, d, d_v, group, false)) {
-      pl->chunk_fixed = pl->chunk_min = int(max_tiles * tile);
-    } else if (single_split_suffices(units, n_max, pl->chunk_min, int(tile), sms,
+    const int alone = single_split_rows(pl->ks, pl->tc5, dtype, d, d_v, group, false);
+    int dev = 0;
+    if (seen >= 0 && units <= sms && n_max <= 8LL * alone && cudaGetDevice(&dev) == cudaSuccess) {
+      // as for block scales; a CTA has an SM to itself.  (The tcgen05 kernel has no such form.)
+      const long long share = alone / 4 > tile ? alone / 4 : tile;
+      long long c = pl->tc5 ? 1 : (n_max + share - 1) / share;
+      if (c > 8) c = 8;
+      while (c > 1 && units > clusters_at_once(int(c), dev)) --c;
+      if (n_max <= c * alone) {
+        pl->cluster = pl->tc5 ? 0 : int(c);
+        pl->chunk_fixed = pl->chunk_min = int(max_tiles * tile);
+        pl->grid = units * c;
+        pl->max_splits = 1;
+        return DA_OK;
+      }
+    }
+    if (single_split_suffices(units, n_max, pl->chunk_min, int(tile), sms,
                                      pl->ks.cta_speed)) {
       // One split per unit needs no partials and no combine, but when the
       // units fill the grid's rounds unevenly (fewer units than CTAs, or a
@@ -609,7 +652,7 @@ int run_decode(const void* q, const void* K, const void* V, const int32_t* seq_l
     const long long max_grid = da::kSchedRedWords / 2 - 1;
     const long long grid_cap = sms < max_grid ? sms : max_grid;
     // (a block-scaled cache: one CTA per chunk, not persistent)
-    const int grid = int(ba ? pl.grid : (items < grid_cap ? items : grid_cap));
+    const int grid = int(ba || pl.cluster > 0 ? pl.grid : (items < grid_cap ? items : grid_cap));
     cudaError_t err =
         pl.tc5 ? da::launch_split_tc5(p, tk, tv, grid, stream)
         : ba   ? da::launch_split_q8b(p, tk, tv, d_k, dtype == DA_INT8 ? 1 : 2, grid, stream)

@@ -1234,6 +1234,68 @@ __device__ __forceinline__ Schedule commit_schedule(const SplitParams& p, int* s
   return s;
 }
 
+// With score terms and p.cluster > 0: CTA blockIdx.x % cluster of a unit's cluster takes
+// an equal share of its sequence's list rows, in whole tiles, instead of a work list.
+// The item of this CTA as the lengths read now (a thread by itself).
+template <int TILE>
+__device__ __forceinline__ ItemT<true> cluster_item(const SplitParams& p, bool& bad, bool& bad_pos,
+                                                    int& n_out) {
+  ItemT<true> it;
+  const int unit = int(blockIdx.x) / p.cluster;
+  it.split = int(blockIdx.x) - unit * p.cluster;
+  it.hc = unit % p.head_chunks;
+  it.kvh = unit / p.head_chunks % p.h_kv;
+  it.b = unit / p.head_chunks / p.h_kv;
+  const int begin = doc_begin(p.mod, it.b);
+  const int lv = list_len<TILE, true>(p, begin, __ldcg(p.seq_lens + it.b), bad, bad_pos, n_out);
+  const bool app = (lv & kAppendFlag) != 0;
+  const int n = lv & ~kAppendFlag;
+  list_rows(p.mod, TILE, begin, n_out, app, it.rows);
+  const int chunk = max(TILE, ((n + p.cluster - 1) / p.cluster + TILE - 1) / TILE * TILE);
+  it.nv = max(1, (n + chunk - 1) / chunk);
+  it.row_begin = min(n, it.split * chunk);
+  it.row_end = min(n, it.row_begin + chunk);
+  it.new_row = app ? n - 1 : -1;
+  it.tiles = (it.row_end - it.row_begin + TILE - 1) / TILE;
+  return it;
+}
+
+// After the wait for the previous grid: this CTA's item as a list of one, and the call's
+// seq_lens_out and error bits.  Every thread must call it.
+template <int TILE>
+__device__ __forceinline__ Schedule cluster_schedule(const SplitParams& p, int* sched) {
+  Schedule s{};
+  s.w = sched;
+  s.mine = 1;
+  if (threadIdx.x == 0) {
+    bool bad = false, bad_pos = false;
+    int n_out;
+    const ItemT<true> it = cluster_item<TILE>(p, bad, bad_pos, n_out);
+    int* w = sched + kSchedItems;
+    w[0] = it.b;
+    w[1] = it.kvh;
+    w[2] = it.hc;
+    w[3] = it.split;
+    w[4] = it.nv;
+    w[5] = it.row_begin;
+    w[6] = it.row_end;
+    w[7] = it.new_row;
+    w[8] = it.rows.prefix;
+    w[9] = it.rows.first;
+    w[10] = it.rows.pt;
+    w[11] = it.rows.shift;
+    w[12] = it.rows.lo;
+    w[13] = it.rows.hi;
+    if (it.split == 0 && it.hc == 0 && it.kvh == 0) {  // the sequence's first CTA
+      if (p.seq_lens_out) p.seq_lens_out[it.b] = n_out;
+      if (bad) flag_error(p.dev_error, DA_DEVERR_SEQ_LEN);
+      if (bad_pos) flag_error(p.dev_error, DA_DEVERR_POS);
+    }
+  }
+  __syncthreads();
+  return s;
+}
+
 // The whole work list when nothing can change under it (a single call).
 template <int TILE>
 __device__ __forceinline__ Schedule build_schedule(const SplitParams& p, int* sched) {
@@ -1324,6 +1386,121 @@ __device__ __forceinline__ void finish_item(const SplitParams& p, const Item& it
   }
 }
 
+// A barrier of all threads of a cluster, after which they see each other's shared memory.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+// Floats of CTA `rank`'s shared memory, at the address they have in this CTA's.
+__device__ __forceinline__ uint32_t cluster_addr(const float* at, int rank) {
+  uint32_t a;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(at)), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ float cluster_ld(const float* at, int rank) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];"
+               : "=f"(v)
+               : "r"(cluster_addr(at, rank))
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 cluster_ld4(const float* at, int rank) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(cluster_addr(at, rank))
+               : "memory");
+  return v;
+}
+
+// The merge of a unit's it.nv chunks, held by the CTAs of a cluster: each brings its
+// warps' states to one accumulator, relative to its own maximum, and then joins the
+// chunks' for its share of the unit's outputs, through distributed shared memory.  Every
+// CTA of the cluster takes part, those without rows too.
+template <int D, int HG, int KW, int HPW, int SLOT_STRIDE>
+__device__ __forceinline__ void finish_cluster(const SplitParams& p, const Item& it, float* epi_acc,
+                                               float* epi_m, float* epi_l, int tid, int nthreads,
+                                               volatile int* abort_flag) {
+  static_assert(KW >= 2, "a head's sum and maximum lie in two l slots");
+  constexpr int GC = HG * HPW;
+  const int head0 = it.hc * GC;
+  const int nh = min(GC, p.group - head0);
+  // the first slot of a head's KW warps, and the head in it
+  auto slot = [](int h) { return h / HPW * KW * HPW + h % HPW; };
+  if (tid < GC) {
+    const int s0 = slot(tid);
+    float m[KW], M = -INFINITY, L = 0.f;
+#pragma unroll
+    for (int k = 0; k < KW; ++k) {
+      m[k] = epi_m[s0 + k * HPW];
+      M = fmaxf(M, m[k]);
+    }
+    const float M_use = M == -INFINITY ? 0.f : M;
+#pragma unroll
+    for (int k = 0; k < KW; ++k) {
+      const float f = ex2(m[k] - M_use);
+      L += f * epi_l[s0 + k * HPW];
+      epi_m[s0 + k * HPW] = f;
+    }
+    epi_l[s0] = L;
+    epi_l[s0 + HPW] = M;
+  }
+  named_bar_sync(1, nthreads);
+  // four columns a thread
+  static_assert(SLOT_STRIDE % 4 == 0, "16-byte aligned columns");
+  for (int idx = 4 * tid; idx < nh * D; idx += 4 * nthreads) {
+    const int h = idx / D, d = idx - h * D, s0 = slot(h);
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < KW; ++k) {
+      const float f = epi_m[s0 + k * HPW];
+      const float4 x =
+          *reinterpret_cast<const float4*>(epi_acc + (s0 + k * HPW) * SLOT_STRIDE + d);
+      sum.x += f * x.x, sum.y += f * x.y, sum.z += f * x.z, sum.w += f * x.w;
+    }
+    // (this thread's own columns of the first slot)
+    *reinterpret_cast<float4*>(epi_acc + s0 * SLOT_STRIDE + d) = sum;
+  }
+  cluster_sync();
+  const size_t bh0 = size_t(it.b) * p.h_q + size_t(it.kvh) * p.group + head0;
+  // (consecutive threads of the cluster take consecutive CTAs' shares of a run)
+  for (int idx = 4 * (it.split + p.cluster * tid); idx < nh * D; idx += 4 * p.cluster * nthreads) {
+    const int h = idx / D, d = idx - h * D, s0 = slot(h);
+    float m[8], l[8], M = -INFINITY;  // (a cluster is 8 CTAs at most)
+    float4 a[8];
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      m[r] = -INFINITY, l[r] = 0.f;
+      a[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (r < it.nv) {
+        m[r] = cluster_ld(epi_l + s0 + HPW, r);
+        l[r] = cluster_ld(epi_l + s0, r);
+        a[r] = cluster_ld4(epi_acc + s0 * SLOT_STRIDE + d, r);
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < 8; ++r) M = fmaxf(M, m[r]);
+    const float M_use = M == -INFINITY ? 0.f : M;
+    float L = 0.f;
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      const float f = ex2(m[r] - M_use);
+      L += f * l[r];
+      sum.x += f * a[r].x, sum.y += f * a[r].y, sum.z += f * a[r].z, sum.w += f * a[r].w;
+    }
+    const float inv = L > 0.f ? __fdividef(1.f, L) : 0.f;
+    if (!*abort_flag) {
+      const size_t at = bh0 * D + idx;
+      store_out(p, at, sum.x * inv);
+      store_out(p, at + 1, sum.y * inv);
+      store_out(p, at + 2, sum.z * inv);
+      store_out(p, at + 3, sum.w * inv);
+    }
+  }
+  cluster_sync();  // no CTA's shared memory goes while another reads it
+}
+
 // ---------------------------------------------------------------------------
 // First-tile hints.  A decode call usually follows one of the same shape on
 // the same workspace (the previous decode step), and a CTA's first tiles are
@@ -1408,6 +1585,23 @@ __device__ __forceinline__ void prefetch_hinted(const SplitParams& p, int4 hint,
     for (int h = 0; h < NBOX_K; ++h) tma_prefetch_3d(tmK, h * BOX_COLS, y0 + t * TILE, z);
 #pragma unroll
     for (int h = 0; h < NBOX_V; ++h) tma_prefetch_3d(tmV, h * BOX_COLS, y0 + t * TILE, z);
+  }
+}
+
+// The same for a cluster's CTA: its first tiles as the lengths read now (a hint).
+template <int TILE, int NBOX_K, int NBOX_V, int BOX_COLS>
+__device__ __forceinline__ void prefetch_cluster(const SplitParams& p, const CUtensorMap* tmK,
+                                                 const CUtensorMap* tmV, int max_tiles) {
+  bool bad, bad_pos;
+  int n_out;
+  const ItemT<true> it = cluster_item<TILE>(p, bad, bad_pos, n_out);
+  const int z = (p.b_offset + it.b) * p.h_kv + it.kvh;
+  for (int t = 0; t < it.tiles && t < max_tiles; ++t) {
+    const int y = cache_row(it, it.row_begin + t * TILE);
+#pragma unroll
+    for (int h = 0; h < NBOX_K; ++h) tma_prefetch_3d(tmK, h * BOX_COLS, y, z);
+#pragma unroll
+    for (int h = 0; h < NBOX_V; ++h) tma_prefetch_3d(tmV, h * BOX_COLS, y, z);
   }
 }
 

@@ -72,7 +72,8 @@ __device__ __forceinline__ uint32_t swz(int row, int col) {
   return uint32_t(half * Cfg::kHalfBytes + row * 128 + ((chunk ^ (row & 7)) << 4));
 }
 
-template <class Cfg, int TERMS>
+// CLUSTER: a cluster for each unit of a short cache (p.cluster > 0).
+template <class Cfg, int TERMS, bool CLUSTER>
 __global__ void __launch_bounds__(Cfg::kThreads, 1)
     split_decode_bf16_kernel(const __grid_constant__ CUtensorMap tmK,
                              const __grid_constant__ CUtensorMap tmV, const SplitParams p) {
@@ -115,7 +116,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
     prefetch_tmap(&tmV);
   }
   int4 hint = make_int4(0, 0, 0, 0);
-  if (threadIdx.x == Cfg::kConsumerThreads) hint = load_hint(p);  // producer lane
+  if (!CLUSTER && threadIdx.x == Cfg::kConsumerThreads) hint = load_hint(p);  // producer lane
   // Launched as a programmatic dependent: the set-up here overlaps the tail
   // of the previous grid on the stream, which may have produced seq_lens, q,
   // the caches or the new rows.  Before the wait below, only the hinted L2
@@ -124,14 +125,23 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
   // checked and built again if they changed once the wait is over.  The hint
   // is loaded first and used after the build, so that its round trip does
   // not hold the build's first barrier.
-  Schedule sched = build_schedule_core<Cfg::kTile, MOD>(p, sched_words);
-  if (threadIdx.x == Cfg::kConsumerThreads)
-    prefetch_hinted<Cfg::kTile, Cfg::kHalvesK, Cfg::kHalvesV, 64>(p, hint, &tmK, &tmV, STAGES);
-  wait_for_prerequisite_grid();
-  sched = commit_schedule<Cfg::kTile, MOD>(p, sched_words, sched);
-  allow_dependent_launch();
-  if (threadIdx.x == 0 && sched.mine > 0)
-    write_hint<Cfg::kTile, MOD>(p, cta_item<Cfg::kTile, MOD>(p, sched, 0), STAGES);
+  Schedule sched;
+  if constexpr (CLUSTER) {
+    if (threadIdx.x == Cfg::kConsumerThreads)
+      prefetch_cluster<Cfg::kTile, Cfg::kHalvesK, Cfg::kHalvesV, 64>(p, &tmK, &tmV, STAGES);
+    wait_for_prerequisite_grid();
+    sched = cluster_schedule<Cfg::kTile>(p, sched_words);
+    allow_dependent_launch();
+  } else {
+    sched = build_schedule_core<Cfg::kTile, MOD>(p, sched_words);
+    if (threadIdx.x == Cfg::kConsumerThreads)
+      prefetch_hinted<Cfg::kTile, Cfg::kHalvesK, Cfg::kHalvesV, 64>(p, hint, &tmK, &tmV, STAGES);
+    wait_for_prerequisite_grid();
+    sched = commit_schedule<Cfg::kTile, MOD>(p, sched_words, sched);
+    allow_dependent_launch();
+    if (threadIdx.x == 0 && sched.mine > 0)
+      write_hint<Cfg::kTile, MOD>(p, cta_item<Cfg::kTile, MOD>(p, sched, 0), STAGES);
+  }
 
   // ------------------------------------------------------------------ producer
   if (warp == Cfg::kConsumerWarps) {
@@ -429,8 +439,12 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
         slot[(h0 + 1) * Cfg::kSlotStride + d0 + 8] = acc[mb][nb][3];
       }
     named_bar_sync(1, Cfg::kConsumerThreads);
-    finish_item<DV, Cfg::HG, KW, kHPW, Cfg::kSlotStride>(p, it, epi_acc, epi_m, epi_l, threadIdx.x,
-                                                        Cfg::kConsumerThreads, abort_flag);
+    if (CLUSTER && p.cluster > 1)
+      finish_cluster<DV, Cfg::HG, KW, kHPW, Cfg::kSlotStride>(p, it, epi_acc, epi_m, epi_l, threadIdx.x, Cfg::kConsumerThreads,
+                     abort_flag);
+    else
+      finish_item<DV, Cfg::HG, KW, kHPW, Cfg::kSlotStride>(p, it, epi_acc, epi_m, epi_l, threadIdx.x, Cfg::kConsumerThreads,
+                  abort_flag);
   }
 }
 
@@ -444,15 +458,23 @@ using Bf16G32D64 = Bf16Cfg<64, 64, 2, 2, 4, 1, 8>;
 using Bf16G8D256 = Bf16Cfg<256, 256, 1, 1, 4, 1, 2>;   // 64-row stages of 64 KB
 using Bf16G8D192V128 = Bf16Cfg<192, 128, 1, 1, 4, 1, 3>;
 
-template <class Cfg>
-static cudaError_t launch_cfg(const SplitParams& p, const CUtensorMap& tk, const CUtensorMap& tv,
-                              int grid, cudaStream_t stream) {
+template <class Cfg, bool CLUSTER>
+static cudaError_t launch_cfg_form(const SplitParams& p, const CUtensorMap& tk, const CUtensorMap& tv,
+                           int grid, cudaStream_t stream) {
   static std::atomic<unsigned long long> smem_set{0};
-  const cudaError_t e =
-      set_smem_limit_once(split_decode_bf16_kernel<Cfg, DA_TERMS>, Cfg::kSmemBytes, smem_set);
+  const auto kernel = split_decode_bf16_kernel<Cfg, DA_TERMS, CLUSTER>;
+  const cudaError_t e = set_smem_limit_once(kernel, Cfg::kSmemBytes, smem_set);
   if (e != cudaSuccess) return e;
-  return launch_dependent(split_decode_bf16_kernel<Cfg, DA_TERMS>, grid, Cfg::kThreads,
-                          Cfg::kSmemBytes, stream, tk, tv, p);
+  return launch_dependent_clusters(kernel, grid, p.cluster, Cfg::kThreads, Cfg::kSmemBytes, stream,
+                                   tk, tv, p);
+}
+
+template <class Cfg>
+static cudaError_t launch_cfg(const SplitParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int grid,
+                      cudaStream_t stream) {
+  if constexpr (DA_TERMS != 0)
+    if (p.cluster > 0) return launch_cfg_form<Cfg, true>(p, tk, tv, grid, stream);
+  return launch_cfg_form<Cfg, false>(p, tk, tv, grid, stream);
 }
 
 // This object's set of terms (DA_TERMS); the dispatch is in the object of set 0.

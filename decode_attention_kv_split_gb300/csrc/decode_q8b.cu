@@ -281,117 +281,6 @@ __device__ __forceinline__ void cluster_chunk(const SplitParams& p, int n, ItemT
   it.nv = max(1, (n + chunk - 1) / chunk);
 }
 
-// A barrier of all threads of a cluster, after which they see each other's shared memory.
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
-}
-// Floats of CTA `rank`'s shared memory, at the address they have in this CTA's.
-__device__ __forceinline__ uint32_t cluster_addr(const float* at, int rank) {
-  uint32_t a;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(at)), "r"(rank));
-  return a;
-}
-__device__ __forceinline__ float cluster_ld(const float* at, int rank) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];"
-               : "=f"(v)
-               : "r"(cluster_addr(at, rank))
-               : "memory");
-  return v;
-}
-__device__ __forceinline__ float4 cluster_ld4(const float* at, int rank) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(cluster_addr(at, rank))
-               : "memory");
-  return v;
-}
-
-// The merge of a unit's it.nv chunks, held by the CTAs of a cluster: each brings its
-// warps' states to one accumulator, relative to its own maximum, and then joins the
-// chunks' for its share of the unit's outputs, through distributed shared memory.  Every
-// CTA of the cluster takes part, those without rows too.
-template <int D, int KW, int HPW, int SLOT_STRIDE>
-__device__ __forceinline__ void finish_cluster(const SplitParams& p, const Item& it, float* epi_acc,
-                                               float* epi_m, float* epi_l, int tid, int nthreads,
-                                               volatile int* abort_flag) {
-  static_assert(KW >= 2, "a head's sum and maximum lie in two l slots");
-  const int head0 = it.hc * HPW;
-  const int nh = min(HPW, p.group - head0);
-  if (tid < HPW) {
-    float m[KW], M = -INFINITY, L = 0.f;
-#pragma unroll
-    for (int k = 0; k < KW; ++k) {
-      m[k] = epi_m[k * HPW + tid];
-      M = fmaxf(M, m[k]);
-    }
-    const float M_use = M == -INFINITY ? 0.f : M;
-#pragma unroll
-    for (int k = 0; k < KW; ++k) {
-      const float f = ex2(m[k] - M_use);
-      L += f * epi_l[k * HPW + tid];
-      epi_m[k * HPW + tid] = f;
-    }
-    epi_l[tid] = L;
-    epi_l[HPW + tid] = M;
-  }
-  __syncthreads();
-  // four columns a thread
-  static_assert(SLOT_STRIDE % 4 == 0, "16-byte aligned columns");
-  for (int idx = 4 * tid; idx < nh * D; idx += 4 * nthreads) {
-    const int h = idx / D, d = idx - h * D;
-    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int k = 0; k < KW; ++k) {
-      const float f = epi_m[k * HPW + h];
-      const float4 x =
-          *reinterpret_cast<const float4*>(epi_acc + (k * HPW + h) * SLOT_STRIDE + d);
-      sum.x += f * x.x, sum.y += f * x.y, sum.z += f * x.z, sum.w += f * x.w;
-    }
-    // (this thread's own columns of the first slot)
-    *reinterpret_cast<float4*>(epi_acc + h * SLOT_STRIDE + d) = sum;
-  }
-  cluster_sync();
-  const size_t bh0 = size_t(it.b) * p.h_q + size_t(it.kvh) * p.group + head0;
-  // (consecutive threads of the cluster take consecutive CTAs' shares of a run)
-  for (int idx = 4 * (it.split + p.cluster * tid); idx < nh * D; idx += 4 * p.cluster * nthreads) {
-    const int h = idx / D, d = idx - h * D;
-    float m[8], l[8], M = -INFINITY;  // (a cluster is 8 CTAs at most)
-    float4 a[8];
-#pragma unroll
-    for (int r = 0; r < 8; ++r) {
-      m[r] = -INFINITY, l[r] = 0.f;
-      a[r] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (r < it.nv) {
-        m[r] = cluster_ld(epi_l + HPW + h, r);
-        l[r] = cluster_ld(epi_l + h, r);
-        a[r] = cluster_ld4(epi_acc + h * SLOT_STRIDE + d, r);
-      }
-    }
-#pragma unroll
-    for (int r = 0; r < 8; ++r) M = fmaxf(M, m[r]);
-    const float M_use = M == -INFINITY ? 0.f : M;
-    float L = 0.f;
-    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int r = 0; r < 8; ++r) {
-      const float f = ex2(m[r] - M_use);
-      L += f * l[r];
-      sum.x += f * a[r].x, sum.y += f * a[r].y, sum.z += f * a[r].z, sum.w += f * a[r].w;
-    }
-    const float inv = L > 0.f ? __fdividef(1.f, L) : 0.f;
-    if (!*abort_flag) {
-      const size_t at = bh0 * D + idx;
-      store_out(p, at, sum.x * inv);
-      store_out(p, at + 1, sum.y * inv);
-      store_out(p, at + 2, sum.z * inv);
-      store_out(p, at + 3, sum.w * inv);
-    }
-  }
-  cluster_sync();  // no CTA's shared memory goes while another reads it
-}
-
 // Byte offset of 16-byte piece `piece` of row `row` of a box: the 128-byte
 // swizzle for 128-byte rows, the 64-byte swizzle for 64-byte rows.
 template <int D>
@@ -903,7 +792,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::CTAS)
     }
   __syncthreads();
   if (CLUSTER && p.cluster > 1)
-    finish_cluster<D, KW, kHPW, Cfg::kSlotStride>(p, it, epi_acc, epi_m, epi_l, threadIdx.x,
+    finish_cluster<D, 1, KW, kHPW, Cfg::kSlotStride>(p, it, epi_acc, epi_m, epi_l, threadIdx.x,
                                                   Cfg::kThreads, abort_flag);
   else
     finish_item<D, 1, KW, kHPW, Cfg::kSlotStride>(p, it, epi_acc, epi_m, epi_l, threadIdx.x,

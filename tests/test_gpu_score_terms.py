@@ -240,6 +240,30 @@ def test_largest_slopes(heads, dtype, slope):
     run(*heads, 300, lens, dtype, {"slopes": [slope] * h_q, "window": 40, "softcap": 9.0})
 
 
+CLUSTERS = [  # heads, d_k, d_v, type, the most rows one CTA of a unit's cluster takes
+    (2, 2, 64, 64, torch.float32, 384), (6, 1, 128, 128, torch.float32, 96), (8, 2, 128, 128, torch.bfloat16, 512),
+    (40, 1, 64, 64, torch.bfloat16, 192), (4, 1, 256, 256, torch.bfloat16, 256), (6, 2, 192, 128, torch.bfloat16, 256),
+]
+
+
+@pytest.mark.parametrize("append", [False, True])
+@pytest.mark.parametrize("heads", CLUSTERS, ids=[f"{str(c[4])[6:]}-d{c[2]}h{c[0]}kv{c[1]}" for c in CLUSTERS])
+def test_short_caches(heads, append):
+    """Caches that one to eight CTAs a unit share: shares that end inside a tile, on one, empty ones."""
+    h_q, h_kv, d_k, d_v, dtype, most = heads
+    terms = {"softcap": 9.0, "slopes": slopes_of(h_q), "window": 0, "prefix": 2}
+    for n in (1, 2, most // 3, most - 1, most + 1, 2 * most, 5 * most + 7, 8 * most, 8 * most + 1):
+        run(2, h_q, h_kv, d_k, d_v, n, [n - append, n // 3], dtype, terms, seed=n, append=append)
+        run(3, h_q, h_kv, d_k, d_v, n, [0, n, n // 2], dtype, {"window": max(1, n // 3), "prefix": 5}, seed=n,
+            append=append)
+    # a window of a long cache: its rows are what the CTAs share
+    run(2, h_q, h_kv, d_k, d_v, 6000, [5999, 801], dtype, {"window": 2 * most, "prefix": 3}, append=append)
+    # more sequences: fewer CTAs for each, down to one
+    for B in (9, 17, 40, 70):
+        run(B, h_q, h_kv, d_k, d_v, 300, [(b * 47) % 300 for b in range(B)], dtype, {"prefix": 1, "window": 250},
+            seed=B, append=append)
+
+
 def test_output_allocated_for_a_stream():
     q, K, V, *_ = make(2, 8, 2, 128, 128, 300, [300, 9], torch.bfloat16, 3, {}, False)
     q, K, V, l = q.cuda(), K.cuda(), V.cuda(), torch.tensor([300, 9], dtype=torch.int32, device="cuda")
