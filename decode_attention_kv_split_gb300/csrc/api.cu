@@ -288,21 +288,19 @@ bool single_split_suffices(long long units, int n_max, int chunk_min, int tile, 
 // Block-scaled caches (see make_plan): the most bytes of partials.
 constexpr long long kBlockPartialBytes = 64LL << 20;
 
-// With score terms or block scales: the most rows that one CTA takes by itself where
-// there are no more units than SMs (of 8-bit blocks: each CTA of a unit's cluster).  A
-// second launch costs a step 4 us of host time,
-// and 1.5 to 2 us of the GPU's in a graph; one CTA streams these rows in about 3 us.
-// Measured at 1 and 8 sequences, one split against the cost model's choice: a call by
-// itself 2 to 5 us faster up to here, a step of a graph between 1.6 us faster and 0.6
-// slower; at twice the rows a graph's step 2 to 5 us slower.
+// With score terms or block scales: the most rows that a CTA of a unit's cluster takes,
+// by itself or with up to seven others, where there are no more units than SMs.  A second
+// launch costs a step 4 us of host time, and 1.5 to 2 us of the GPU's in a graph; one CTA
+// streams these rows in about 3 us.  Measured with one CTA a unit at 1 and 8 sequences
+// against the cost model's choice: a call by itself 2 to 5 us faster up to here, a step of
+// a graph between 1.6 us faster and 0.6 slower; at twice the rows 2 to 5 us slower.
 //   8-bit blocks: 5 to 8 ns a row, 10 for more than 8 heads a KV head
-//   bf16: 5 ns a row, 9 in the tcgen05 kernel, 12 for d = 256 or 32 heads of 64
+//   bf16: 5 ns a row, 12 for d = 256 or 32 heads of 64
 //   fp32: 8 ns a row for one head of 64, 10 for two or one of 128, 20 to 30 for more
-int single_split_rows(const KernelShape& ks, bool tc5, int dtype, int d, int d_v, int group,
-                      bool block) {
+int single_split_rows(const KernelShape& ks, int dtype, int d, int d_v, int group, bool block) {
   if (block) return group <= 8 ? 512 : 384;
   if (dtype == DA_BF16)
-    return tc5 ? 512 : ks.heads_per_cta > 16 ? 192 : d + d_v > 256 ? 256 : ks.heads_per_cta > 8 ? 384 : 512;
+    return ks.heads_per_cta > 16 ? 192 : d + d_v > 256 ? 256 : ks.heads_per_cta > 8 ? 384 : 512;
   const int products = ks.heads_per_cta * d;
   return products <= 64 ? 384 : products <= 128 ? 192 : products <= 512 ? 128 : 96;
 }
@@ -401,7 +399,7 @@ int make_plan(int B, int h_q, int h_kv, int d, int d_v, int n_max, int dtype_arg
       // of 128: a graph's step 6.4 -> 4.6 us, a call by itself 25.3 -> 21.2; 16 of 512
       // rows, 2 kv heads of 64 with 32 query heads: 9.2 -> 4.7 us).  Two CTAs on an SM
       // cost more than they share (4 of 1024 rows, 8 kv heads: 8 a unit 6.5 us, 4 5.8).
-      const int alone = single_split_rows(pl->ks, pl->tc5, dtype, d, d_v, group, true);
+      const int alone = single_split_rows(pl->ks, dtype, d, d_v, group, true);
       long long c = (n_max + da::kBlockMinRows - 1) / da::kBlockMinRows;  // as many as have rows
       if (c * units > sms) c = sms / units;             // while each has an SM,
       const long long least = (n_max + alone - 1) / alone;
@@ -454,23 +452,36 @@ int make_plan(int B, int h_q, int h_kv, int d, int d_v, int n_max, int dtype_arg
     const long long per = (n_max + cap - 1) / cap;
     pl->chunk_fixed = 0;
     pl->chunk_min = int((per + tile - 1) / tile * tile);
-    const int alone = single_split_rows(pl->ks, pl->tc5, dtype, d, d_v, group, false);
+    // With score terms, as for block scales; a CTA has an SM to itself.  More than 8 heads
+    // of 128 a KV head go to the mma.sync kernel then, 8 a CTA (the tcgen05 kernel has no
+    // such form, and its set-up alone takes longer: one sequence of 512 rows and 32 heads
+    // on one KV head 13.6 us, this way 5.2), and that with twice the rows a CTA.
+    const int chunks = pl->tc5 ? (group + 7) / 8 : pl->head_chunks;
+    const KernelShape ks = pl->tc5 ? da::bf16_shape(d, d_v, 8) : pl->ks;
+    const int alone = single_split_rows(ks, dtype, d, d_v, group, false) * (pl->tc5 ? 2 : 1);
+    const long long parts = (long long)pl->batch_per_launch * h_kv * chunks;
     int dev = 0;
-    if (seen >= 0 && units <= sms && n_max <= 8LL * alone && cudaGetDevice(&dev) == cudaSuccess) {
-      // as for block scales; a CTA has an SM to itself.  (The tcgen05 kernel has no such form.)
-      const long long share = alone / 4 > tile ? alone / 4 : tile;
-      long long c = pl->tc5 ? 1 : (n_max + share - 1) / share;
+    if (seen >= 0 && parts <= sms && n_max <= 8LL * alone && cudaGetDevice(&dev) == cudaSuccess) {
+      long long share = single_split_rows(ks, dtype, d, d_v, group, false) / 4;
+      if (share < ks.tile_rows) share = ks.tile_rows;
+      long long c = (n_max + share - 1) / share;
       if (c > 8) c = 8;
-      while (c > 1 && units > clusters_at_once(int(c), dev)) --c;
+      while (c > 1 && parts > clusters_at_once(int(c), dev)) --c;
       if (n_max <= c * alone) {
-        pl->cluster = pl->tc5 ? 0 : int(c);
-        pl->chunk_fixed = pl->chunk_min = int(max_tiles * tile);
-        pl->grid = units * c;
+        pl->tc5 = false;
+        pl->ks = ks;
+        pl->head_chunks = chunks;
+        pl->units = int(parts);
+        pl->cluster = int(c);
+        pl->chunk_fixed = pl->chunk_min = (n_max + ks.tile_rows - 1) / ks.tile_rows * ks.tile_rows;
+        pl->grid = parts * c;
         pl->max_splits = 1;
         return DA_OK;
       }
     }
-    if (single_split_suffices(units, n_max, pl->chunk_min, int(tile), sms,
+    if (seen >= 0 && pl->tc5 && units <= sms && n_max <= 512) {
+      pl->chunk_fixed = pl->chunk_min = int(max_tiles * tile);
+    } else if (single_split_suffices(units, n_max, pl->chunk_min, int(tile), sms,
                                      pl->ks.cta_speed)) {
       // One split per unit needs no partials and no combine, but when the
       // units fill the grid's rounds unevenly (fewer units than CTAs, or a

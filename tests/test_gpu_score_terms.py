@@ -5,6 +5,9 @@ the length, hold NaN and infinities; outputs start as NaN.  Tolerances are
 terms_reference.tolerance: bf16 weights are two bf16 parts (2^-17 of a weight),
 fp32 weights one float (2^-24)."""
 import math
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -243,6 +246,7 @@ def test_largest_slopes(heads, dtype, slope):
 CLUSTERS = [  # heads, d_k, d_v, type, the most rows one CTA of a unit's cluster takes
     (2, 2, 64, 64, torch.float32, 384), (6, 1, 128, 128, torch.float32, 96), (8, 2, 128, 128, torch.bfloat16, 512),
     (40, 1, 64, 64, torch.bfloat16, 192), (4, 1, 256, 256, torch.bfloat16, 256), (6, 2, 192, 128, torch.bfloat16, 256),
+    (20, 1, 128, 128, torch.bfloat16, 1024),
 ]
 
 
@@ -262,6 +266,27 @@ def test_short_caches(heads, append):
     for B in (9, 17, 40, 70):
         run(B, h_q, h_kv, d_k, d_v, 300, [(b * 47) % 300 for b in range(B)], dtype, {"prefix": 1, "window": 250},
             seed=B, append=append)
+
+
+FIRST = """
+import torch
+from decode_attention_kv_split_gb300 import api
+q, K = torch.randn(2, 8, 128, device="cuda"), torch.randn(2, 2, 600, 128, device="cuda")
+l = torch.tensor([600, 9], dtype=torch.int32, device="cuda")
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    out = api.decode_attn_mod(q, K, K, l, api.ScoreMod(softcap=5.0))
+g.replay()
+again = api.decode_attn_mod(q, K, K, l, api.ScoreMod(softcap=5.0))
+torch.cuda.synchronize()
+assert torch.equal(out, again)
+"""
+
+
+def test_first_call_of_a_process_in_a_capture():
+    """What the library asks the driver once, it asks then."""
+    subprocess.run([sys.executable, "-c", FIRST], check=True, timeout=300,
+                   cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 
 
 def test_output_allocated_for_a_stream():
