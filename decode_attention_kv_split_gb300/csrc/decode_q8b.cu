@@ -19,13 +19,13 @@
 // eight warps a SM: 40.8 us on 16 ragged int8 sequences with 8 kv heads).  Every
 // CTA finds its chunk from the lengths (find_item_few, _many): the chunk length is the
 // shortest whose chunks all fit on the GPU at once, so that there is one round
-// of equal CTAs, whatever n_max is (31.0 us; 33.1 with a length fixed by n_max).
+// of equal CTAs, whatever n_max is (31.7 us; 2.1 more with a length fixed by n_max).
 // Beyond kBlockRoundRows rows a CTA there are two or three shorter rounds: HBM does
 // not serve all SMs alike, and the CTAs of a later round go where an early one
 // ended (2 x 131072 rows of fp8 with 64 query heads: 85.6 us in one round, 83.7 in
-// two, 6.4 TB/s; ncu on it: DRAM 77 % busy, 1.4 instructions a cycle of 4, the MMA
+// two, 6.4 TB/s, with an earlier form of the steps, 82.5 with this one; ncu on the former: DRAM 77 % busy, 1.4 instructions a cycle of 4, the MMA
 // pipe 17 %).  With 32 heads on one kv head the MMAs and the instructions around
-// them, not HBM, are the bound: 31.4 us for 8 x 30000 rows, 9.2 us of HBM time.
+// them, not HBM, are the bound: 32.8 us for 8 x 30000 rows, 9.2 us of HBM time.
 // Caches of up to 4096 rows with few enough units (make_plan) need no list: a cluster
 // of up to eight CTAs takes a unit's rows in equal shares and joins them through
 // distributed shared memory (finish_cluster), without a second kernel.
@@ -54,12 +54,18 @@
 //           g D/8 + 2 mb and + 1.
 // The V scale multiplies P before P becomes fp16.  For a float32 output P is an
 // fp16 head and an fp16 remainder (~22 bits, two MMAs).  For a bf16 output it is
-// the head alone: 2^-12 of each weight, an eighth of the half step (2^-9) by which
-// the output's own rounding moves it, and a third of the MMAs less.
+// the head alone: 2^-11 of each weight, an eighth of the half step (2^-8) by which
+// the output's own rounding moves it, and a third of the MMAs less (with the remainder
+// the cases below take 33.8, 84.4 and 39.0 us, not 31.7, 82.5 and 32.8, for errors
+// against 64 bits of 0.99 of these).
 // Scales may be of any size (2^-126 for tiny rows), and fp16 has few exponents,
-// so a warp keeps its accumulator in units of the largest V scale it has seen:
-// P is multiplied by vs / unit <= 1, the accumulator is rescaled when the unit
-// grows (as by a running maximum), and the unit returns at the chunk's end.
+// so a warp keeps each head's accumulator in a unit that follows the largest
+// weight times V scale that the head has seen, a second running maximum beside
+// the softmax's: P is a weight times its V scale in that unit, and the unit
+// returns at the chunk's end.  It differs from the softmax's reference by a power
+// of two, so that P is rounded once.  (A unit for all heads that follows the V
+// scales alone takes a head's digits where a block it gives no weight, or that only
+// its neighbours weigh on, has a far larger scale; it takes 31.2, 84.1 and 31.5 us.)
 #include <math.h>
 
 #include "common.cuh"
@@ -281,6 +287,20 @@ __device__ __forceinline__ void cluster_chunk(const SplitParams& p, int n, ItemT
   it.nv = max(1, (n + chunk - 1) / chunk);
 }
 
+// log2 x on the special-function unit, off by 2^-22 (0: -infinity).  Subnormals, which it
+// takes for 0, are scaled first.
+__device__ __forceinline__ float log2_of(float x) {
+  const bool tiny = x < 1.17549435e-38f;
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(tiny ? x * 16777216.f : x));
+  return tiny ? y - 24.f : y;
+}
+
+// 2^k for an integral k in [-126, 127].
+__device__ __forceinline__ float pow2(float k) {
+  return __uint_as_float(__float_as_uint(k + (12582912.f + 127.f)) << 23);
+}
+
 // Byte offset of 16-byte piece `piece` of row `row` of a box: the 128-byte
 // swizzle for 128-byte rows, the 64-byte swizzle for 64-byte rows.
 template <int D>
@@ -304,11 +324,11 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::CTAS)
   constexpr int KIND = Cfg::KIND;
   constexpr bool MOD = TERMS != 0, CAP = (TERMS & kTermsCap) != 0,
                  SLOPES = (TERMS & kTermsSlopes) != 0;
-  // Weights are taken against 2^-kHead of the maximum, so that those far below it, and
-  // those of a block whose V scale is far below another's, keep their digits in fp16:
-  // its subnormals begin 2^21 below the largest, 2^14 without.
+  // Weights, and their products with the V scales, are taken against 2^-kHead of their
+  // maximum, so that those far below it keep their digits in fp16: its subnormals begin
+  // 2^20 below the largest product, 2^14 without.
   constexpr float kHead = 7.f;
-  constexpr float kLazy = 8.f;      // log2 of how far a weight may exceed 2^kHead
+  constexpr float kLazy = 8.f;      // log2 of how far either may exceed 2^kHead
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -501,14 +521,15 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::CTAS)
 
   float m_run[NB][2], l_run[NB][2];
   float acc[MB][NB][4];
-  // The accumulator's unit, the largest |V scale| so far: a scale is
-  // (scale * unit_by) * unit_inv units (unit_by brings tiny ones to where the
-  // inverse exists).
-  float unit = 0.f, unit_by = 1.f, unit_inv = 0.f;
+  // A head's accumulator counts in units of 2^-k_run beside the weights', which count
+  // in 2^m_run: the largest product of a weight and a V scale so far is 2^kHead or
+  // half of it (k_run is integral, and in [-126, 126]).
+  float k_run[NB][2], k_top = 0.f;  // k_top: the largest of them
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb) {
     m_run[nb][0] = m_run[nb][1] = -INFINITY;
     l_run[nb][0] = l_run[nb][1] = 0.f;
+    k_run[nb][0] = k_run[nb][1] = 0.f;
 #pragma unroll
     for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
@@ -629,46 +650,58 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::CTAS)
           for (int e = 0; e < 4; ++e)
             s[u][nb][e] = (e < 2 ? seenA : seenB) ? s[u][nb][e] : -INFINITY;
       }
-      // The maximum is kept lazily: only where some score is more than 2^kLazy
-      // above it does a vote bring the exact one (three shuffles a head) and the
-      // rescaling.  Every weight and sum is taken against the maximum as it
-      // stands (m_run: kHead below it); weights reach 2^15, inside fp16's 65504.
-      bool over = false;
+      // Both maxima are kept lazily: only where some score, by itself or with the step's
+      // larger V scale, is more than 2^kLazy above its own does a vote bring the exact
+      // ones (six shuffles a head) and the rescaling.  Every weight and sum is taken
+      // against the maximum as it stands (m_run: kHead below it); products reach 2^15,
+      // inside fp16's 65504.
+      float lv[2];  // log2 of the blocks' V scales (the same on every lane)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) lv[u] = log2_of(fabsf(vs[u]));
+      const float lv_top = fmaxf(lv[0], lv[1]);
+      // (a V scale that leaves float's range in units of the accumulator)
+      bool over = lv_top + k_top > 126.f;
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const float mx =
               fmaxf(fmaxf(s[0][nb][j], s[0][nb][j + 2]), fmaxf(s[1][nb][j], s[1][nb][j + 2]));
-          over |= mx > m_run[nb][j] + (kHead + kLazy);
+          over |= mx + fmaxf(k_run[nb][j] + lv_top, 0.f) > m_run[nb][j] + (kHead + kLazy);
         }
-      // the V scales in units of the accumulator (the same on every lane)
-      const float avs = fmaxf(fabsf(vs[0]), fabsf(vs[1]));
-      if (__any_sync(0xffffffffu, over || avs > unit)) {
-        float f = 1.f;
-        if (avs > unit) {
-          f = __fdiv_rn(unit, avs);
-          unit = avs;
-          unit_by = unit < 1.f ? 18446744073709551616.f : 1.f;  // 2^64
-          unit_inv = __fdiv_rn(1.f, unit * unit_by);
-        }
+      const bool update = __any_sync(0xffffffffu, over);
+      if (update) {
+        k_top = -126.f;
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            float mx =
-                fmaxf(fmaxf(s[0][nb][j], s[0][nb][j + 2]), fmaxf(s[1][nb][j], s[1][nb][j + 2]));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-            const float m_new = fmaxf(m_run[nb][j], mx - kHead);
-            const float alpha = ex2(m_run[nb][j] - (m_new == -INFINITY ? 0.f : m_new));
+            float mx[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              mx[u] = fmaxf(s[u][nb][j], s[u][nb][j + 2]);
+              mx[u] = fmaxf(mx[u], __shfl_xor_sync(0xffffffffu, mx[u], 4));
+              mx[u] = fmaxf(mx[u], __shfl_xor_sync(0xffffffffu, mx[u], 8));
+              mx[u] = fmaxf(mx[u], __shfl_xor_sync(0xffffffffu, mx[u], 16));
+            }
+            const float m_old = m_run[nb][j], k_old = k_run[nb][j];
+            const float m_new = fmaxf(m_old, fmaxf(mx[0], mx[1]) - kHead);
+            // the accumulator's reference, 2^(m - k), only grows
+            const float a =
+                fmaxf(m_old - k_old, fmaxf(mx[0] + lv[0], mx[1] + lv[1]) - kHead);
+            // (nothing seen yet: any)
+            const float k_new =
+                m_new == -INFINITY ? 0.f : fminf(fmaxf(floorf(m_new - a), -126.f), 126.f);
+            const float alpha = ex2(m_old - (m_new == -INFINITY ? 0.f : m_new));
+            const float f = alpha * pow2(fminf(fmaxf(k_new - k_old, -126.f), 127.f));
             m_run[nb][j] = m_new;
+            k_run[nb][j] = k_new;
+            k_top = fmaxf(k_top, k_new);
             l_run[nb][j] *= alpha;
 #pragma unroll
             for (int mb = 0; mb < MB; ++mb) {
-              acc[mb][nb][j] *= alpha * f;
-              acc[mb][nb][j + 2] *= alpha * f;
+              acc[mb][nb][j] *= f;
+              acc[mb][nb][j + 2] *= f;
             }
           }
       }
@@ -684,13 +717,24 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::CTAS)
             l_run[nb][j] += s[u][nb][j] + s[u][nb][j + 2];
           }
         }
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const float w = (vs[u] * unit_by) * unit_inv;
+      // times the V scale in units of the accumulator (a power of two times it: exact)
+      if (update) {  // (in two parts: a scale may leave float's range where its weights are 0)
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[u][nb][e] *= w;
+          for (int e = 0; e < 4; ++e)
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+              s[u][nb][e] = s[u][nb][e] * 0x1p16f *
+                            fminf(fmaxf(vs[u] * 0x1p-16f * pow2(k_run[nb][e & 1]), -0x1p127f),
+                                  0x1p127f);
+      } else {
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) s[u][nb][e] *= vs[u] * pow2(k_run[nb][e & 1]);
       }
       // ---- Step III: O^T += V^T . P^T
 #pragma unroll
@@ -779,16 +823,21 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::CTAS)
         epi_l[warp * kHPW + nb * 8 + 2 * lane + j] = l_run[nb][j];
       }
   }
+  float unit[NB][2];
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) unit[nb][j] = pow2(-k_run[nb][j]);
 #pragma unroll
   for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
       const int d0 = (D / 8) * g + 2 * mb;  // acc[0..1]: column d0; acc[2..3]: d0 + 1
       const int h0 = nb * 8 + 2 * t;
-      slots[h0 * Cfg::kSlotStride + d0] = acc[mb][nb][0] * unit;
-      slots[(h0 + 1) * Cfg::kSlotStride + d0] = acc[mb][nb][1] * unit;
-      slots[h0 * Cfg::kSlotStride + d0 + 1] = acc[mb][nb][2] * unit;
-      slots[(h0 + 1) * Cfg::kSlotStride + d0 + 1] = acc[mb][nb][3] * unit;
+      slots[h0 * Cfg::kSlotStride + d0] = acc[mb][nb][0] * unit[nb][0];
+      slots[(h0 + 1) * Cfg::kSlotStride + d0] = acc[mb][nb][1] * unit[nb][1];
+      slots[h0 * Cfg::kSlotStride + d0 + 1] = acc[mb][nb][2] * unit[nb][0];
+      slots[(h0 + 1) * Cfg::kSlotStride + d0 + 1] = acc[mb][nb][3] * unit[nb][1];
     }
   __syncthreads();
   if (CLUSTER && p.cluster > 1)

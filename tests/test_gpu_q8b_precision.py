@@ -1,0 +1,67 @@
+"""What the block-scaled decode keeps of its inputs' digits (needs a GB300)."""
+import pytest
+import torch
+
+import decode_bounds as D
+import terms_reference as R
+from decode_attention_kv_split_gb300 import api
+
+pytestmark = pytest.mark.gpu
+KINDS = [torch.int8, torch.float8_e4m3fn]
+KID = ["int8", "fp8"]
+OUTS = [torch.float32, torch.bfloat16]
+OID = ["fp32", "bf16"]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    api.load()
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def codes(shape, dtype, seed):
+    g = torch.Generator().manual_seed(seed)
+    v = torch.randn(shape, generator=g) * R.Q[dtype] / 4
+    return R.as_codes(R.round_codes(v.double().numpy(), dtype), dtype)
+
+
+@pytest.mark.parametrize("out_dtype", OUTS, ids=OID)
+@pytest.mark.parametrize("dtype", KINDS, ids=KID)
+@pytest.mark.parametrize("d,heads", [(64, 2), (128, 2), (64, 20), (128, 20)])
+@pytest.mark.parametrize("far", [0, 2, 8])
+def test_blocks_of_no_weight_take_no_digits(far, d, heads, dtype, out_dtype):
+    """The even heads' weight lies on block 1 alone, the odd heads' on block `far`, whose V scale is
+    2^k times as large (or as small) and which the same warp sees: each head's output is the mean of
+    its own block's rows, with all its digits.
+
+    The 16 rows' scores are equal, so that their weights are equal but for their rounding with
+    the V scale, part; 16 products and the merge are under 64 float roundings of 2^-24, in the
+    numerator and the denominator.  The other rows weigh e^-160 = 2^-230, times 2^k nothing."""
+    n, block = 200, 16
+    part = D.weight_rounding("q8b") if out_dtype == torch.float32 else 2.0 ** -11
+    for k in (0, 12, 20, 40, 100, -20, -100):
+        V = codes((1, 1, n, d), dtype, 7)
+        K = torch.zeros(1, 1, n, d)
+        K[..., :2] = -100.0
+        K[0, 0, 16:32, 0] = 100.0
+        K[0, 0, far * 16:far * 16 + 16, 1] = 100.0
+        K = K.to(dtype)
+        ks = torch.full((1, 1, 13), 0.1)
+        vs = torch.full((1, 1, 13), 2.0 ** -9)
+        vs[0, 0, far] = 2.0 ** (k - 9)
+        q = torch.zeros(1, heads, d, dtype=torch.bfloat16)
+        q[0, 0::2, 0] = q[0, 1::2, 1] = 8.0 * 100.0 / float(K[0, 0, 16, 0].float())
+        out = api.decode_attn_q8b(q.cuda(), K.cuda(), V.cuda(), ks.cuda(), vs.cuda(), i32([n]), block, scale=1.0,
+                                  out_dtype=out_dtype).cpu().double()
+        for h, at, s in ((0, 16, 2.0 ** -9), (1, far * 16, 2.0 ** (k - 9))):
+            rows = V[0, 0, at:at + 16].double() * s
+            want, size = rows.mean(0), rows.abs().mean(0)
+            tol = size * (part + 128 * 2.0 ** -24)
+            tol = tol + (want.abs() + tol) * (torch.finfo(out_dtype).eps / 2)
+            err = (out[0, h::2] - want).abs()
+            assert bool((err <= tol).all()), (k, h, float((err / tol).max()))
