@@ -502,12 +502,40 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::CTAS)
 #pragma unroll
     for (int u = 0; u < MB / 2; ++u) {
       const uint4 w = ok ? __ldg(src + u) : make_uint4(0, 0, 0, 0);
-      qf[2 * u][nb][0] = q8::pack_f16x2(bf16_lo_to_f32(w.x), bf16_hi_to_f32(w.x));
-      qf[2 * u][nb][1] = q8::pack_f16x2(bf16_lo_to_f32(w.y), bf16_hi_to_f32(w.y));
-      qf[2 * u + 1][nb][0] = q8::pack_f16x2(bf16_lo_to_f32(w.z), bf16_hi_to_f32(w.z));
-      qf[2 * u + 1][nb][1] = q8::pack_f16x2(bf16_lo_to_f32(w.w), bf16_hi_to_f32(w.w));
+      qf[2 * u][nb][0] = w.x;
+      qf[2 * u][nb][1] = w.y;
+      qf[2 * u + 1][nb][0] = w.z;
+      qf[2 * u + 1][nb][1] = w.w;
     }
   }
+  // As fp16 times the power of two that brings the largest finite |q| of the CTA's heads
+  // into [2^14, 2^15): exact down to 2^-31 of it, and no bf16 number is too large.
+  auto q_most = [&](auto part) {  // the bits of the largest part(word), two halves a word
+    uint32_t top = 0;
+#pragma unroll
+    for (int kb = 0; kb < MB; ++kb)
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+        top = __vmaxu2(top, __vmaxu2(part(qf[kb][nb][0] & 0x7fff7fffu),
+                                     part(qf[kb][nb][1] & 0x7fff7fffu)));
+    return __reduce_max_sync(0xffffffffu, max(top >> 16, top & 0xffffu));
+  };
+  uint32_t q_top = q_most([](uint32_t w) { return w; });
+  if (q_top >= 0x7f80u)  // some are infinite or NaN, and stay so
+    q_top = q_most([](uint32_t w) { return w & __vcmpltu2(w, 0x7f807f80u); });
+  const float q_up = q_top == 0 ? 0.f : fminf(float(141 - int(q_top >> 7)), 126.f);
+  const __nv_bfloat162 q_by = __float2bfloat162_rn(pow2(q_up));
+#pragma unroll
+  for (int kb = 0; kb < MB; ++kb)
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const __nv_bfloat162 x =
+            __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&qf[kb][nb][j]), q_by);
+        const uint32_t w = *reinterpret_cast<const uint32_t*>(&x);
+        qf[kb][nb][j] = q8::pack_f16x2(bf16_lo_to_f32(w), bf16_hi_to_f32(w));
+      }
   [[maybe_unused]] float slope[NB][2];
   if constexpr (SLOPES) {
 #pragma unroll
@@ -536,7 +564,10 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::CTAS)
       for (int e = 0; e < 4; ++e) acc[mb][nb][e] = 0.f;
   }
 
-  const float score_scale = CAP && SHORT ? p.mod.short_scale : p.scale_log2;
+  // (used once in 16 steps: kept in shared memory, not in a register of them all)
+  volatile float* q_down = reinterpret_cast<volatile float*>(find + kFindWords - KW + warp);
+  if (lane == 0) *q_down = pow2(-q_up);
+  __syncwarp();
   [[maybe_unused]] bool slopes_up = true;
   if constexpr (SLOPES) {
 #pragma unroll
@@ -547,7 +578,9 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::CTAS)
   uint32_t phase = 0;
   for (int i = 0; i < it.tiles; ++i) {
     if ((i & 15) == 0) {
-      sk_now = sk_next, sv_now = sv_next;
+      // (a score's whole factor)
+      sk_now = sk_next * *q_down * (CAP && SHORT ? p.mod.short_scale : p.scale_log2);
+      sv_now = sv_next;
       load_scales(i + 16, sk_next, sv_next);
     }
     // warp-uniform (the MMAs and shuffles below need the whole warp)
@@ -571,7 +604,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::CTAS)
     float ks[2], vs[2];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      ks[u] = __shfl_sync(0xffffffffu, sk_now, 2 * (i & 15) + u) * score_scale;
+      ks[u] = __shfl_sync(0xffffffffu, sk_now, 2 * (i & 15) + u);
       vs[u] = __shfl_sync(0xffffffffu, sv_now, 2 * (i & 15) + u);
       const bool any = !MOD || mask.any_seen(u * 16, 16);
       ks[u] = any ? ks[u] : 0.f;

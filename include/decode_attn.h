@@ -418,9 +418,10 @@ DA_API int decode_attn_mod_append(const void* q, const void* k_new, const void* 
  * size, zero or not a power of two.  Weights are multiplied as fp16 (two terms
  * for a float32 out): a row's weight times its V scale is rounded by at most 2^-11
  * (2^-22) of itself down to 2^-20 (2^-9) of the largest such product of the query's
- * head, and by 2^-31 of that below.  q is multiplied as
- * fp16: exact for |q| in [2^-14, 65504].  num_splits = -1 acts as 0: one CTA
- * takes each chunk, and the kernel picks the chunks from the lengths. */
+ * head, and by 2^-31 of that below.  q is multiplied as fp16 times a power of two
+ * for each run of 8 or 16 heads of a KV head: exact down to 2^-31 of their largest
+ * finite |q|.  num_splits = -1 acts as 0: one CTA takes each chunk, and the kernel
+ * picks the chunks from the lengths. */
 DA_API size_t decode_attn_q8b_workspace_bytes(const da_score_mod* mod, int B, int h_q, int h_kv,
                                               int d_k, int d_v, int n_max, int dtype,
                                               int num_splits, int* status);

@@ -65,3 +65,41 @@ def test_blocks_of_no_weight_take_no_digits(far, d, heads, dtype, out_dtype):
             tol = tol + (want.abs() + tol) * (torch.finfo(out_dtype).eps / 2)
             err = (out[0, h::2] - want).abs()
             assert bool((err <= tol).all()), (k, h, float((err / tol).max()))
+
+
+@pytest.mark.parametrize("dtype", KINDS, ids=KID)
+@pytest.mark.parametrize("d,h_q,h_kv", [(64, 6, 2), (128, 8, 1), (64, 40, 2), (128, 20, 1)])
+def test_queries_of_any_size(d, h_q, h_kv, dtype):
+    """q far above what fp16 holds, and below its normal numbers, over K scales that bring the scores back."""
+    B, n, block = 2, 700, 32
+    g = torch.Generator().manual_seed(3)
+    K, V = codes((B, h_kv, n, d), dtype, 4), codes((B, h_kv, n, d), dtype, 5)
+    vs = torch.exp2(torch.randint(-8, -4, (B, h_kv, 22), generator=g).float())
+    base = torch.randn(B, h_q, d, generator=g)
+    for f in (1.0, 2.0 ** 17, 2.0 ** 60, 2.0 ** 120, 2.0 ** -12, 2.0 ** -20, 2.0 ** -60, 2.0 ** -110):
+        q = (base * f).to(torch.bfloat16)
+        ks = torch.full((B, h_kv, 22), 2.0 ** -5 / f)
+        out = api.decode_attn_q8b(q.cuda(), K.cuda(), V.cuda(), ks.cuda(), vs.cuda(), i32([n, 333]), block)
+        at = torch.arange(n) // block
+        Kv, Vv = K.double() * ks[:, :, at, None].double(), V.double() * vs[:, :, at, None].double()
+        want, tol = D.attend(q.cuda(), Kv.cuda(), Vv.cuda(), [n, 333], d ** -0.5, D.weight_rounding("q8b"),
+                             floor=2.0 ** -31)
+        D.check(out, want, tol, f"q times {f}")
+
+
+def test_a_query_that_is_not_finite_stays_in_its_head():
+    B, n, block, d, h_q = 1, 300, 16, 64, 8
+    for dtype in KINDS:
+        K, V = codes((B, 1, n, d), dtype, 4), codes((B, 1, n, d), dtype, 5)
+        s = torch.full((B, 1, 19), 2.0 ** -5)
+        q = torch.randn(B, h_q, d, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16)
+        args = (K.cuda(), V.cuda(), s.cuda(), s.cuda(), i32([n]), block)
+        want, tol = D.attend(q.cuda(), K.cuda().double() * 2.0 ** -5, V.cuda().double() * 2.0 ** -5, [n], d ** -0.5,
+                             D.weight_rounding("q8b"), floor=2.0 ** -31)
+        for bad in (float("inf"), float("-inf"), float("nan")):
+            q2 = q.clone()
+            q2[0, 3, 7] = bad
+            out = api.decode_attn_q8b(q2.cuda(), *args)
+            keep = [h for h in range(h_q) if h != 3]
+            D.check(out[:, keep], want[:, keep], tol[:, keep])
+            assert not torch.isfinite(out[:, 3]).any()
