@@ -501,7 +501,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::CTAS)
                                                       bhq * (D * 2) + t * (D / 2));
 #pragma unroll
     for (int u = 0; u < MB / 2; ++u) {
-      const uint4 w = ok ? __ldg(src + u) : make_uint4(0, 0, 0, 0);
+      const uint4 w = ok ? __ldcg(src + u) : make_uint4(0, 0, 0, 0);
       qf[2 * u][nb][0] = w.x;
       qf[2 * u][nb][1] = w.y;
       qf[2 * u + 1][nb][0] = w.z;
