@@ -1417,7 +1417,8 @@ __device__ __forceinline__ float4 cluster_ld4(const float* at, int rank) {
 // The merge of a unit's it.nv chunks, held by the CTAs of a cluster: each brings its
 // warps' states to one accumulator, relative to its own maximum, and then joins the
 // chunks' for its share of the unit's outputs, through distributed shared memory.  Every
-// CTA of the cluster takes part, those without rows too.
+// CTA of the cluster takes part, those without rows too.  A CTA whose wait ran out says so
+// by a negative sum, and the whole unit's outputs are then left as they were.
 template <int D, int HG, int KW, int HPW, int SLOT_STRIDE>
 __device__ __forceinline__ void finish_cluster(const SplitParams& p, const Item& it, float* epi_acc,
                                                float* epi_m, float* epi_l, int tid, int nthreads,
@@ -1443,7 +1444,7 @@ __device__ __forceinline__ void finish_cluster(const SplitParams& p, const Item&
       L += f * epi_l[s0 + k * HPW];
       epi_m[s0 + k * HPW] = f;
     }
-    epi_l[s0] = L;
+    epi_l[s0] = *abort_flag ? -1.f : L;
     epi_l[s0 + HPW] = M;
   }
   named_bar_sync(1, nthreads);
@@ -1483,15 +1484,17 @@ __device__ __forceinline__ void finish_cluster(const SplitParams& p, const Item&
     for (int r = 0; r < 8; ++r) M = fmaxf(M, m[r]);
     const float M_use = M == -INFINITY ? 0.f : M;
     float L = 0.f;
+    bool aborted = false;
     float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int r = 0; r < 8; ++r) {
       const float f = ex2(m[r] - M_use);
+      aborted |= l[r] < 0.f;
       L += f * l[r];
       sum.x += f * a[r].x, sum.y += f * a[r].y, sum.z += f * a[r].z, sum.w += f * a[r].w;
     }
     const float inv = L > 0.f ? __fdividef(1.f, L) : 0.f;
-    if (!*abort_flag) {
+    if (!aborted) {
       const size_t at = bh0 * D + idx;
       store_out(p, at, sum.x * inv);
       store_out(p, at + 1, sum.y * inv);
