@@ -1288,7 +1288,7 @@ __device__ __forceinline__ Schedule cluster_schedule(const SplitParams& p, int* 
     w[12] = it.rows.lo;
     w[13] = it.rows.hi;
     if (it.split == 0 && it.hc == 0 && it.kvh == 0) {  // the sequence's first CTA
-      if (p.seq_lens_out) p.seq_lens_out[it.b] = n_out;
+      if (p.seq_lens_out && DA_IN(p, it.b, p.B)) p.seq_lens_out[it.b] = n_out;
       if (bad) flag_error(p.dev_error, DA_DEVERR_SEQ_LEN);
       if (bad_pos) flag_error(p.dev_error, DA_DEVERR_POS);
     }
