@@ -1596,7 +1596,7 @@ __device__ __forceinline__ void prefetch_hinted(const SplitParams& p, int4 hint,
 template <int TILE, int NBOX_K, int NBOX_V, int BOX_COLS>
 __device__ __forceinline__ void prefetch_cluster(const SplitParams& p, const CUtensorMap* tmK,
                                                  const CUtensorMap* tmV, int max_tiles) {
-  bool bad, bad_pos;
+  bool bad = false, bad_pos = false;  // (flagged after the wait)
   int n_out;
   const ItemT<true> it = cluster_item<TILE>(p, bad, bad_pos, n_out);
   const int z = (p.b_offset + it.b) * p.h_kv + it.kvh;
