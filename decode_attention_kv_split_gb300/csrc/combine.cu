@@ -156,7 +156,7 @@ __device__ __forceinline__ void merge_head(const SplitParams& p, int bh, int nv,
       W += f * red_w[w];
       a += f * red_acc[w * D + d];
     }
-    const float v = W > 0.f ? a / W : 0.f;
+    const float v = W > 0.f ? a / W : a * 0.f;  // (no rows: a is 0; all splits NaN: a is)
     if (p.out_bf16) static_cast<__nv_bfloat16*>(p.out)[size_t(bh) * D + d] = __float2bfloat16_rn(v);
     else static_cast<float*>(p.out)[size_t(bh) * D + d] = v;
     if (d == 0 && p.lse_out) p.lse_out[bh] = W > 0.f ? (M_use + log2f(W)) * kLn2 : -INFINITY;

@@ -583,13 +583,14 @@ struct TileMask<true> {
   }
 };
 
-// A query head's distance bias per row in the log2 domain (0: none), kept finite: times
-// a distance of zero it has to give zero.  (Like q, not through the read-only path: the
+// A query head's distance bias per row in the log2 domain (0: none), infinities and what
+// overflows kept finite: times a distance of zero they have to give zero.  A NaN stays
+// one, and so does the head's output.  (Like q, not through the read-only path: the
 // previous grid may still write it when this one starts.)
 __device__ __forceinline__ float head_slope(const SplitParams& p, int head, bool ok) {
   if (!p.mod.slopes || !ok) return 0.f;
   const float s = __ldcg(p.mod.slopes + head) * 1.4426950408889634f;
-  return fminf(fmaxf(s, -3e38f), 3e38f);
+  return s > 3e38f ? 3e38f : s < -3e38f ? -3e38f : s;
 }
 
 // The distances of a cache row that the biases multiply.  A bias is zero at the

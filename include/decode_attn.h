@@ -364,7 +364,8 @@ DA_API int kv_quantize(const void* x, int x_dtype, void* codes, float* scales, l
  *   window    : the last `window` rows are seen; 0 for all
  *   prefix    : the first `prefix` rows are seen whatever the window and the
  *               document (a shared prompt, or the rows a window keeps)
- *   slopes    : nullable device float32 [h_q], finite, of either sign
+ *   slopes    : nullable device float32 [h_q], of either sign; infinite ones act as
+ *               the largest finite ones, a NaN makes its head's output NaN
  *   doc_begin : nullable device int32 [B], the first row of the document the
  *               query belongs to; values outside [0, n] act as the nearer end
  * The struct is read during the call; the arrays it names by the kernels.
