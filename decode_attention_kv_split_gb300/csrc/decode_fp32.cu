@@ -194,7 +194,8 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
 
     const int head_base = it.hc * G;  // group-local index of this item's first head
     // q (pre-multiplied by scale * log2(e) once loaded, so scores come out in
-    // the log2 domain) arrives with the item's first stage.
+    // the log2 domain; with capped scores as it is, since scale / softcap may be
+    // far above what the products can bear) arrives with the item's first stage.
     float qv[G][EPL];
 
     using LS = LaneScores<G, RPW>;
@@ -231,7 +232,8 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
           load_lane<EPL>(tmp, qs + g * D + lane * EPL);
           const bool ok = head_base + g < p.group;
 #pragma unroll
-          for (int e = 0; e < EPL; ++e) qv[g][e] = ok ? tmp[e] * p.scale_log2 : 0.f;
+          for (int e = 0; e < EPL; ++e)
+            qv[g][e] = ok ? (CAP ? tmp[e] : tmp[e] * p.scale_log2) : 0.f;
         }
       }
       const int tile_row0 = it.row_begin + t * Cfg::kTile;
@@ -294,7 +296,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
 #pragma unroll
           for (int j = 0; j < LS::VPL; ++j) {
             const int rr = LS::index(lane, j) % RPW;
-            if constexpr (CAP) v[j] = p.mod.cap_log2 * tanh_fast(v[j]);
+            if constexpr (CAP) v[j] = p.mod.cap_log2 * tanh_fast(v[j] * p.scale_log2);
             if constexpr (SLOPES)
               v[j] = biased(v[j], RowDistance(it, mask.row0 + row0 + rr), slope, false);
             v[j] = (seen >> rr & 1u) ? v[j] : -INFINITY;
