@@ -578,8 +578,9 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::CTAS)
   uint32_t phase = 0;
   for (int i = 0; i < it.tiles; ++i) {
     if ((i & 15) == 0) {
-      // (a score's whole factor)
+      // (a score's whole factor, finite, so that a product of zero stays zero)
       sk_now = sk_next * *q_down * (CAP && SHORT ? p.mod.short_scale : p.scale_log2);
+      if (fabsf(sk_now) > 3e38f) sk_now = copysignf(3e38f, sk_now);
       sv_now = sv_next;
       load_scales(i + 16, sk_next, sv_next);
     }
