@@ -186,6 +186,14 @@ def workspace_bytes(B, h_q, h_kv, d_k, d_v, n_max, dtype: torch.dtype, num_split
 
 
 _ws_cache: dict = {}
+_ws_locks: dict = {}
+
+
+def _ws_lock(key):
+    """The lock of a kept workspace.  A call with splits is two launches that pass partials
+    through it, and the library call drops the GIL: without the lock a call that another host
+    thread makes on the same stream could come between them."""
+    return _ws_locks.get(key) or _ws_locks.setdefault(key, threading.Lock())
 
 
 def _out(out: torch.Tensor | None, out_dtype: torch.dtype | None, B: int, h_q: int, d_v: int,
@@ -201,15 +209,20 @@ def _out(out: torch.Tensor | None, out_dtype: torch.dtype | None, B: int, h_q: i
     return out, (DA_OUT_BF16 if out.dtype == torch.bfloat16 else 0)
 
 
-def _workspace(device: torch.device, nbytes: int) -> torch.Tensor | None:
-    if nbytes == 0:
-        return None
+def _workspace(device: torch.device, nbytes: int, given: torch.Tensor | None):
+    """A call's workspace (the given one, or the stream's own), its bytes, and the lock to
+    hold while the library is called."""
+    if given is not None or nbytes == 0:
+        return given, 0 if given is None else given.numel() * given.element_size(), _unlocked
     key = (device.index, torch.cuda.current_stream(device).cuda_stream)
     ws = _ws_cache.get(key)
     if ws is None or ws.numel() < nbytes:
         ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
         _ws_cache[key] = ws
-    return ws
+    return ws, ws.numel(), _ws_lock(key)
+
+
+_unlocked = contextlib.nullcontext()
 
 
 def decode_attn(q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, seq_lens: torch.Tensor,
@@ -232,12 +245,11 @@ def decode_attn(q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, seq_lens: tor
     lib = load()
     with _on_device(q):
         need = workspace_bytes(B, h_q, h_kv, d_k, d_v, n_max, q.dtype, num_splits)
-        if workspace is None:
-            workspace = _workspace(q.device, need)
-        nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-        st = lib.decode_attn_ex(_ptr(q), _ptr(K), _ptr(V), _ptr(seq_lens), _ptr(out), B, h_q, h_kv,
-                                d_k, d_v, n_max, float(scale), dt, int(num_splits), _ptr(workspace),
-                                nbytes, _ptr(dev_error), _stream(q, stream))
+        workspace, nbytes, lock = _workspace(q.device, need, workspace)
+        with lock:
+            st = lib.decode_attn_ex(_ptr(q), _ptr(K), _ptr(V), _ptr(seq_lens), _ptr(out), B, h_q,
+                                    h_kv, d_k, d_v, n_max, float(scale), dt, int(num_splits),
+                                    _ptr(workspace), nbytes, _ptr(dev_error), _stream(q, stream))
     _check(st, "decode_attn_ex")
     return out
 
@@ -265,14 +277,13 @@ def decode_attn_append(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor
     lib = load()
     with _on_device(q):
         need = workspace_bytes(B, h_q, h_kv, d_k, d_v, n_max, q.dtype, num_splits)
-        if workspace is None:
-            workspace = _workspace(q.device, need)
-        nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-        st = lib.decode_attn_append(_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(K), _ptr(V),
-                                    _ptr(seq_lens), _ptr(seq_lens_out), _ptr(out), B, h_q, h_kv,
-                                    d_k, d_v, n_max, float(scale), _DTYPES[q.dtype] | oflag,
-                                    int(num_splits), _ptr(workspace), nbytes, _ptr(dev_error),
-                                    _stream(q, stream))
+        workspace, nbytes, lock = _workspace(q.device, need, workspace)
+        with lock:
+            st = lib.decode_attn_append(_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(K), _ptr(V),
+                                        _ptr(seq_lens), _ptr(seq_lens_out), _ptr(out), B, h_q, h_kv,
+                                        d_k, d_v, n_max, float(scale), _DTYPES[q.dtype] | oflag,
+                                        int(num_splits), _ptr(workspace), nbytes, _ptr(dev_error),
+                                        _stream(q, stream))
     _check(st, "decode_attn_append")
     return out
 
@@ -337,13 +348,13 @@ def decode_attn_partial(q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, seq_l
     lib = load()
     with _on_device(q):
         need = workspace_bytes(B, h_q, h_kv, d_k, d_v, n_max, q.dtype, num_splits)
-        if workspace is None:
-            workspace = _workspace(q.device, need)
-        nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-        st = lib.decode_attn_partial(_ptr(q), _ptr(K), _ptr(V), _ptr(seq_lens), int(row_begin),
-                                     int(row_end), _ptr(o), _ptr(lse), B, h_q, h_kv, d_k, d_v,
-                                     n_max, float(scale), _DTYPES[q.dtype], int(num_splits),
-                                     _ptr(workspace), nbytes, _ptr(dev_error), _stream(q, stream))
+        workspace, nbytes, lock = _workspace(q.device, need, workspace)
+        with lock:
+            st = lib.decode_attn_partial(_ptr(q), _ptr(K), _ptr(V), _ptr(seq_lens), int(row_begin),
+                                         int(row_end), _ptr(o), _ptr(lse), B, h_q, h_kv, d_k, d_v,
+                                         n_max, float(scale), _DTYPES[q.dtype], int(num_splits),
+                                         _ptr(workspace), nbytes, _ptr(dev_error),
+                                         _stream(q, stream))
     _check(st, "decode_attn_partial")
     return o, lse
 
@@ -449,13 +460,12 @@ def decode_attn_q8(q, K, V, k_scale, v_scale, seq_lens, out=None, scale=None, nu
     lib = load()
     with _on_device(q):
         need = workspace_bytes(B, h_q, h_kv, d_k, d_v, n_max, K.dtype, num_splits)
-        if workspace is None:
-            workspace = _workspace(q.device, need)
-        nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-        st = lib.decode_attn_q8_ex(_ptr(q), _ptr(K), _ptr(V), _ptr(k_scale), _ptr(v_scale),
-                                   _ptr(seq_lens), _ptr(out), B, h_q, h_kv, d_k, d_v, n_max,
-                                   float(scale), _Q8_DTYPES[K.dtype] | oflag, int(num_splits),
-                                   _ptr(workspace), nbytes, _ptr(dev_error), _stream(q, stream))
+        workspace, nbytes, lock = _workspace(q.device, need, workspace)
+        with lock:
+            st = lib.decode_attn_q8_ex(_ptr(q), _ptr(K), _ptr(V), _ptr(k_scale), _ptr(v_scale),
+                                       _ptr(seq_lens), _ptr(out), B, h_q, h_kv, d_k, d_v, n_max,
+                                       float(scale), _Q8_DTYPES[K.dtype] | oflag, int(num_splits),
+                                       _ptr(workspace), nbytes, _ptr(dev_error), _stream(q, stream))
     _check(st, "decode_attn_q8_ex")
     return out
 
@@ -481,15 +491,15 @@ def decode_attn_q8_append(q, k_new, v_new, k_new_scale, v_new_scale, K, V, k_sca
     lib = load()
     with _on_device(q):
         need = workspace_bytes(B, h_q, h_kv, d_k, d_v, n_max, K.dtype, num_splits)
-        if workspace is None:
-            workspace = _workspace(q.device, need)
-        nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-        st = lib.decode_attn_q8_append(_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_new_scale),
-                                       _ptr(v_new_scale), _ptr(K), _ptr(V), _ptr(k_scale),
-                                       _ptr(v_scale), _ptr(seq_lens), _ptr(seq_lens_out), _ptr(out),
-                                       B, h_q, h_kv, d_k, d_v, n_max, float(scale),
-                                       _Q8_DTYPES[K.dtype] | oflag, int(num_splits),
-                                       _ptr(workspace), nbytes, _ptr(dev_error), _stream(q, stream))
+        workspace, nbytes, lock = _workspace(q.device, need, workspace)
+        with lock:
+            st = lib.decode_attn_q8_append(_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_new_scale),
+                                           _ptr(v_new_scale), _ptr(K), _ptr(V), _ptr(k_scale),
+                                           _ptr(v_scale), _ptr(seq_lens), _ptr(seq_lens_out),
+                                           _ptr(out), B, h_q, h_kv, d_k, d_v, n_max, float(scale),
+                                           _Q8_DTYPES[K.dtype] | oflag, int(num_splits),
+                                           _ptr(workspace), nbytes, _ptr(dev_error),
+                                           _stream(q, stream))
     _check(st, "decode_attn_q8_append")
     return out
 
@@ -638,14 +648,15 @@ _mod_bytes_cache: dict = {}
 
 def _terms_workspace(entry: str, cmod, sizes, device: int, stream, raw: int,
                      workspace: torch.Tensor | None):
-    """The workspace of a call with score terms or block scales and its bytes (``sizes``: the
-    sizes, dtype code and split choice).  Without a given one: a tensor of the stream the call
-    runs on, kept for its next call; while that stream is captured, a tensor of the graph's own
-    pool, since two graphs that share scratch may be replayed at the same time."""
+    """The workspace of a call with score terms or block scales, its bytes and the lock to hold
+    while the library is called (``sizes``: the sizes, dtype code and split choice).  Without a
+    given one: a tensor of the stream the call runs on, kept for its next call; while that
+    stream is captured, a tensor of the graph's own pool, since two graphs that share scratch
+    may be replayed at the same time."""
     if workspace is not None:
         if workspace.get_device() != device or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous tensor on the query's device")
-        return workspace, workspace.numel() * workspace.element_size()
+        return workspace, workspace.numel() * workspace.element_size(), _unlocked
     key = (entry, device, sizes, 0, 0) if cmod is None else (entry, device, sizes, cmod.window,
                                                              cmod.prefix)
     need = _mod_bytes_cache.get(key)
@@ -658,15 +669,15 @@ def _terms_workspace(entry: str, cmod, sizes, device: int, stream, raw: int,
             _mod_bytes_cache.clear()
         _mod_bytes_cache[key] = need
     if need == 0:
-        return None, 0
+        return None, 0, _unlocked
+    key = (device, raw, "terms")
     with _on_stream(stream):
         if torch._C._cuda_isCurrentStreamCapturing():
-            return torch.empty(need, dtype=torch.uint8, device=device), need
-        ws = _ws_cache.get((device, raw, "terms"))
+            return torch.empty(need, dtype=torch.uint8, device=device), need, _unlocked
+        ws = _ws_cache.get(key)
         if ws is None or ws.numel() < need:
-            ws = _ws_cache[device, raw, "terms"] = torch.empty(need, dtype=torch.uint8,
-                                                               device=device)
-    return ws, need
+            ws = _ws_cache[key] = torch.empty(need, dtype=torch.uint8, device=device)
+    return ws, need, _ws_lock(key)
 
 
 _no_stream = contextlib.nullcontext()
@@ -693,11 +704,12 @@ def decode_attn_mod(q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, seq_lens:
     prev = _enter(device)
     try:
         raw = _raw(stream, device)
-        ws, nbytes = _terms_workspace("decode_attn_mod_workspace_bytes", cm,
-                                      (*dims, dt, num_splits), device, stream, raw, workspace)
-        st = (_lib or load()).decode_attn_mod(
-            q.data_ptr(), K.data_ptr(), V.data_ptr(), seq_lens.data_ptr(), ctypes.byref(cm),
-            out.data_ptr(), *dims, scale, dt, num_splits, _addr(ws), nbytes, err, raw)
+        ws, nbytes, lock = _terms_workspace("decode_attn_mod_workspace_bytes", cm,
+                                            (*dims, dt, num_splits), device, stream, raw, workspace)
+        with lock:
+            st = (_lib or load()).decode_attn_mod(
+                q.data_ptr(), K.data_ptr(), V.data_ptr(), seq_lens.data_ptr(), ctypes.byref(cm),
+                out.data_ptr(), *dims, scale, dt, num_splits, _addr(ws), nbytes, err, raw)
     finally:
         if prev >= 0:
             torch.cuda.set_device(prev)
@@ -731,12 +743,13 @@ def decode_attn_mod_append(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Te
     prev = _enter(device)
     try:
         raw = _raw(stream, device)
-        ws, nbytes = _terms_workspace("decode_attn_mod_workspace_bytes", cm,
-                                      (*dims, dt, num_splits), device, stream, raw, workspace)
-        st = (_lib or load()).decode_attn_mod_append(
-            q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), K.data_ptr(), V.data_ptr(),
-            seq_lens.data_ptr(), _addr(seq_lens_out), ctypes.byref(cm), out.data_ptr(), *dims,
-            scale, dt, num_splits, _addr(ws), nbytes, err, raw)
+        ws, nbytes, lock = _terms_workspace("decode_attn_mod_workspace_bytes", cm,
+                                            (*dims, dt, num_splits), device, stream, raw, workspace)
+        with lock:
+            st = (_lib or load()).decode_attn_mod_append(
+                q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), K.data_ptr(), V.data_ptr(),
+                seq_lens.data_ptr(), _addr(seq_lens_out), ctypes.byref(cm), out.data_ptr(), *dims,
+                scale, dt, num_splits, _addr(ws), nbytes, err, raw)
     finally:
         if prev >= 0:
             torch.cuda.set_device(prev)
@@ -791,13 +804,15 @@ def decode_attn_q8b(q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, k_scale: 
     prev = _enter(device)
     try:
         raw = _raw(stream, device)
-        ws, nbytes = _terms_workspace("decode_attn_q8b_workspace_bytes", cm,
-                                      (B, h_q, h_kv, d, d, n_max, dt, num_splits), device, stream,
-                                      raw, workspace)
-        st = (_lib or load()).decode_attn_q8b(
-            q.data_ptr(), K.data_ptr(), V.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), block,
-            seq_lens.data_ptr(), None if cm is None else ctypes.byref(cm), out.data_ptr(), B, h_q,
-            h_kv, d, d, n_max, scale, dt, num_splits, _addr(ws), nbytes, err, raw)
+        ws, nbytes, lock = _terms_workspace("decode_attn_q8b_workspace_bytes", cm,
+                                            (B, h_q, h_kv, d, d, n_max, dt, num_splits), device,
+                                            stream, raw, workspace)
+        with lock:
+            st = (_lib or load()).decode_attn_q8b(
+                q.data_ptr(), K.data_ptr(), V.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                block, seq_lens.data_ptr(), None if cm is None else ctypes.byref(cm),
+                out.data_ptr(), B, h_q, h_kv, d, d, n_max, scale, dt, num_splits, _addr(ws), nbytes,
+                err, raw)
     finally:
         if prev >= 0:
             torch.cuda.set_device(prev)

@@ -141,7 +141,9 @@ DA_API size_t decode_attn_workspace_bytes(int B, int h_q, int h_kv, int d_k, int
  *                  may be NULL when that is 0.  Its contents need no
  *                  initialisation and are scratch after the call.  Calls
  *                  whose kernels may overlap on the GPU need separate
- *                  workspaces.
+ *                  workspaces, and so do calls that host threads make at
+ *                  the same time, on one stream too (a call is several
+ *                  launches).
  *   dev_error    : nullable device int32; kernels OR DA_DEVERR_* bits into it
  *                  (it is never cleared by the library).
  *   stream       : CUDA stream for every launch.
