@@ -185,6 +185,14 @@ def workspace_bytes(B, h_q, h_kv, d_k, d_v, n_max, dtype: torch.dtype, num_split
     return int(n)
 
 
+_no_stream = contextlib.nullcontext()
+
+
+def _on_stream(stream):
+    """Allocations in the order of ``stream`` (None: the current one)."""
+    return _no_stream if stream is None else torch.cuda.stream(stream)
+
+
 _ws_cache: dict = {}
 _ws_locks: dict = {}
 
@@ -197,10 +205,11 @@ def _ws_lock(key):
 
 
 def _out(out: torch.Tensor | None, out_dtype: torch.dtype | None, B: int, h_q: int, d_v: int,
-         device: torch.device) -> tuple[torch.Tensor, int]:
-    """The output tensor (allocated when None) and its dtype flag."""
+         device: torch.device, stream) -> tuple[torch.Tensor, int]:
+    """The output tensor (allocated when None, in the call's stream) and its dtype flag."""
     if out is None:
-        out = torch.empty((B, h_q, d_v), dtype=out_dtype or torch.float32, device=device)
+        with _on_stream(stream):
+            out = torch.empty((B, h_q, d_v), dtype=out_dtype or torch.float32, device=device)
     if (out.shape != (B, h_q, d_v) or out.dtype not in (torch.float32, torch.bfloat16)
             or not out.is_contiguous() or out.device != device
             or (out_dtype is not None and out.dtype != out_dtype)):
@@ -209,16 +218,25 @@ def _out(out: torch.Tensor | None, out_dtype: torch.dtype | None, B: int, h_q: i
     return out, (DA_OUT_BF16 if out.dtype == torch.bfloat16 else 0)
 
 
-def _workspace(device: torch.device, nbytes: int, given: torch.Tensor | None):
-    """A call's workspace (the given one, or the stream's own), its bytes, and the lock to
+def _workspace(device: torch.device, nbytes: int, given: torch.Tensor | None, stream):
+    """A call's workspace (the given one, or one of its stream), its bytes, and the lock to
     hold while the library is called."""
     if given is not None or nbytes == 0:
         return given, 0 if given is None else given.numel() * given.element_size(), _unlocked
-    key = (device.index, torch.cuda.current_stream(device).cuda_stream)
-    ws = _ws_cache.get(key)
-    if ws is None or ws.numel() < nbytes:
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
-        _ws_cache[key] = ws
+    return _kept_workspace((device.index, _raw(stream, device.index)), nbytes, stream)
+
+
+def _kept_workspace(key, need: int, stream):
+    """A workspace of ``need`` bytes, its bytes and its lock: a tensor of the stream the call
+    runs on, kept under ``key`` (the device first) for its next call; while that stream is
+    captured, a tensor of the graph's own pool, since two graphs that share scratch may be
+    replayed at the same time."""
+    with _on_stream(stream):
+        if torch._C._cuda_isCurrentStreamCapturing():
+            return torch.empty(need, dtype=torch.uint8, device=key[0]), need, _unlocked
+        ws = _ws_cache.get(key)
+        if ws is None or ws.numel() < need:
+            ws = _ws_cache[key] = torch.empty(need, dtype=torch.uint8, device=key[0])
     return ws, ws.numel(), _ws_lock(key)
 
 
@@ -240,12 +258,12 @@ def decode_attn(q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, seq_lens: tor
     B, h_q, h_kv, d_k, d_v, n_max = _cache_dims(q, K, V, seq_lens)
     if scale is None:
         scale = 1.0 / math.sqrt(d_k)
-    out, oflag = _out(out, out_dtype, B, h_q, d_v, q.device)
+    out, oflag = _out(out, out_dtype, B, h_q, d_v, q.device, stream)
     dt = _DTYPES[q.dtype] | oflag
     lib = load()
     with _on_device(q):
         need = workspace_bytes(B, h_q, h_kv, d_k, d_v, n_max, q.dtype, num_splits)
-        workspace, nbytes, lock = _workspace(q.device, need, workspace)
+        workspace, nbytes, lock = _workspace(q.device, need, workspace, stream)
         with lock:
             st = lib.decode_attn_ex(_ptr(q), _ptr(K), _ptr(V), _ptr(seq_lens), _ptr(out), B, h_q,
                                     h_kv, d_k, d_v, n_max, float(scale), dt, int(num_splits),
@@ -273,11 +291,11 @@ def decode_attn_append(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor
         raise ValueError("seq_lens_out must be an int32 tensor of shape [B]")
     if scale is None:
         scale = 1.0 / math.sqrt(d_k)
-    out, oflag = _out(out, out_dtype, B, h_q, d_v, q.device)
+    out, oflag = _out(out, out_dtype, B, h_q, d_v, q.device, stream)
     lib = load()
     with _on_device(q):
         need = workspace_bytes(B, h_q, h_kv, d_k, d_v, n_max, q.dtype, num_splits)
-        workspace, nbytes, lock = _workspace(q.device, need, workspace)
+        workspace, nbytes, lock = _workspace(q.device, need, workspace, stream)
         with lock:
             st = lib.decode_attn_append(_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(K), _ptr(V),
                                         _ptr(seq_lens), _ptr(seq_lens_out), _ptr(out), B, h_q, h_kv,
@@ -294,7 +312,7 @@ def decode_attn_owned(q, K, V, seq_lens, out=None, scale=None, stream=None,
     B, h_q, h_kv, d_k, d_v, n_max = _cache_dims(q, K, V, seq_lens)
     if scale is None:
         scale = 1.0 / math.sqrt(d_k)
-    out, oflag = _out(out, out_dtype, B, h_q, d_v, q.device)
+    out, oflag = _out(out, out_dtype, B, h_q, d_v, q.device, stream)
     with _on_device(q):
         st = load().decode_attn(_ptr(q), _ptr(K), _ptr(V), _ptr(seq_lens), _ptr(out), B, h_q, h_kv,
                                 d_k, d_v, n_max, float(scale), _DTYPES[q.dtype] | oflag,
@@ -312,7 +330,7 @@ def decode_attn_noalloc(q, K, V, seq_lens, out=None, scale=None, num_splits: int
     B, h_q, h_kv, d_k, d_v, n_max = _cache_dims(q, K, V, seq_lens)
     if scale is None:
         scale = 1.0 / math.sqrt(d_k)
-    out, oflag = _out(out, out_dtype, B, h_q, d_v, q.device)
+    out, oflag = _out(out, out_dtype, B, h_q, d_v, q.device, stream)
     with _on_device(q):
         st = load().decode_attn_noalloc(_ptr(q), _ptr(K), _ptr(V), _ptr(seq_lens), _ptr(out), B, h_q,
                                         h_kv, d_k, d_v, n_max, float(scale),
@@ -339,16 +357,17 @@ def decode_attn_partial(q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, seq_l
         row_end = n_max
     if scale is None:
         scale = 1.0 / math.sqrt(d_k)
-    o, _ = _out(o, torch.float32, B, h_q, d_v, q.device)
+    o, _ = _out(o, torch.float32, B, h_q, d_v, q.device, stream)
     if lse is None:
-        lse = torch.empty((B, h_q), dtype=torch.float32, device=q.device)
+        with _on_stream(stream):
+            lse = torch.empty((B, h_q), dtype=torch.float32, device=q.device)
     if lse.shape != (B, h_q) or lse.dtype != torch.float32 or not lse.is_contiguous() \
             or lse.device != q.device:
         raise ValueError("lse must be a contiguous float32 tensor [B, h_q] on the query's device")
     lib = load()
     with _on_device(q):
         need = workspace_bytes(B, h_q, h_kv, d_k, d_v, n_max, q.dtype, num_splits)
-        workspace, nbytes, lock = _workspace(q.device, need, workspace)
+        workspace, nbytes, lock = _workspace(q.device, need, workspace, stream)
         with lock:
             st = lib.decode_attn_partial(_ptr(q), _ptr(K), _ptr(V), _ptr(seq_lens), int(row_begin),
                                          int(row_end), _ptr(o), _ptr(lse), B, h_q, h_kv, d_k, d_v,
@@ -372,9 +391,10 @@ def decode_attn_combine(o_parts: torch.Tensor, lse_parts: torch.Tensor,
         if not t.is_cuda or not t.is_contiguous() or t.dtype != torch.float32:
             raise ValueError(f"{name} must be a contiguous float32 CUDA tensor")
     S, B, h_q, d_v = o_parts.shape
-    out, oflag = _out(out, out_dtype, B, h_q, d_v, o_parts.device)
+    out, oflag = _out(out, out_dtype, B, h_q, d_v, o_parts.device, stream)
     if lse_out is None:
-        lse_out = torch.empty((B, h_q), dtype=torch.float32, device=o_parts.device)
+        with _on_stream(stream):
+            lse_out = torch.empty((B, h_q), dtype=torch.float32, device=o_parts.device)
     if lse_out.shape != (B, h_q) or lse_out.dtype != torch.float32 or not lse_out.is_contiguous():
         raise ValueError("lse_out must be a contiguous float32 tensor [B, h_q]")
     with _on_device(o_parts):
@@ -438,8 +458,9 @@ def kv_quantize(x: torch.Tensor, code_dtype: torch.dtype, stream=None):
     if x.dtype not in _DTYPES or not x.is_cuda or not x.is_contiguous():
         raise ValueError("x must be a contiguous float32 or bfloat16 CUDA tensor")
     d = x.shape[-1]
-    codes = torch.empty(x.shape, dtype=code_dtype, device=x.device)
-    scales = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    with _on_stream(stream):
+        codes = torch.empty(x.shape, dtype=code_dtype, device=x.device)
+        scales = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
     with _on_device(x):
         st = load().kv_quantize(_ptr(x), _DTYPES[x.dtype], _ptr(codes), _ptr(scales),
                                 x.numel() // d if d else 0, d, _Q8_DTYPES[code_dtype],
@@ -456,11 +477,11 @@ def decode_attn_q8(q, K, V, k_scale, v_scale, seq_lens, out=None, scale=None, nu
     B, h_q, h_kv, d_k, d_v, n_max = _q8_dims(q, K, V, k_scale, v_scale, seq_lens)
     if scale is None:
         scale = 1.0 / math.sqrt(d_k)
-    out, oflag = _out(out, out_dtype, B, h_q, d_v, q.device)
+    out, oflag = _out(out, out_dtype, B, h_q, d_v, q.device, stream)
     lib = load()
     with _on_device(q):
         need = workspace_bytes(B, h_q, h_kv, d_k, d_v, n_max, K.dtype, num_splits)
-        workspace, nbytes, lock = _workspace(q.device, need, workspace)
+        workspace, nbytes, lock = _workspace(q.device, need, workspace, stream)
         with lock:
             st = lib.decode_attn_q8_ex(_ptr(q), _ptr(K), _ptr(V), _ptr(k_scale), _ptr(v_scale),
                                        _ptr(seq_lens), _ptr(out), B, h_q, h_kv, d_k, d_v, n_max,
@@ -487,11 +508,11 @@ def decode_attn_q8_append(q, k_new, v_new, k_new_scale, v_new_scale, K, V, k_sca
         raise ValueError("seq_lens_out must be an int32 tensor of shape [B]")
     if scale is None:
         scale = 1.0 / math.sqrt(d_k)
-    out, oflag = _out(out, out_dtype, B, h_q, d_v, q.device)
+    out, oflag = _out(out, out_dtype, B, h_q, d_v, q.device, stream)
     lib = load()
     with _on_device(q):
         need = workspace_bytes(B, h_q, h_kv, d_k, d_v, n_max, K.dtype, num_splits)
-        workspace, nbytes, lock = _workspace(q.device, need, workspace)
+        workspace, nbytes, lock = _workspace(q.device, need, workspace, stream)
         with lock:
             st = lib.decode_attn_q8_append(_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_new_scale),
                                            _ptr(v_new_scale), _ptr(K), _ptr(V), _ptr(k_scale),
@@ -649,10 +670,7 @@ _mod_bytes_cache: dict = {}
 def _terms_workspace(entry: str, cmod, sizes, device: int, stream, raw: int,
                      workspace: torch.Tensor | None):
     """The workspace of a call with score terms or block scales, its bytes and the lock to hold
-    while the library is called (``sizes``: the sizes, dtype code and split choice).  Without a
-    given one: a tensor of the stream the call runs on, kept for its next call; while that
-    stream is captured, a tensor of the graph's own pool, since two graphs that share scratch
-    may be replayed at the same time."""
+    while the library is called (``sizes``: the sizes, dtype code and split choice)."""
     if workspace is not None:
         if workspace.get_device() != device or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous tensor on the query's device")
@@ -670,22 +688,7 @@ def _terms_workspace(entry: str, cmod, sizes, device: int, stream, raw: int,
         _mod_bytes_cache[key] = need
     if need == 0:
         return None, 0, _unlocked
-    key = (device, raw, "terms")
-    with _on_stream(stream):
-        if torch._C._cuda_isCurrentStreamCapturing():
-            return torch.empty(need, dtype=torch.uint8, device=device), need, _unlocked
-        ws = _ws_cache.get(key)
-        if ws is None or ws.numel() < need:
-            ws = _ws_cache[key] = torch.empty(need, dtype=torch.uint8, device=device)
-    return ws, need, _ws_lock(key)
-
-
-_no_stream = contextlib.nullcontext()
-
-
-def _on_stream(stream):
-    """Allocations in the order of ``stream`` (None: the current one)."""
-    return _no_stream if stream is None else torch.cuda.stream(stream)
+    return _kept_workspace((device, raw, "terms"), need, stream)
 
 
 def decode_attn_mod(q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, seq_lens: torch.Tensor,

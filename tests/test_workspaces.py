@@ -176,3 +176,59 @@ def test_a_call_that_fails_leaves_the_workspace_free(monkeypatch, name):
     lib = use(monkeypatch, Library())
     calls()[name](Stream(1))
     assert len(lib.calls) == 1
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_the_workspace_goes_by_the_stream_of_the_call(monkeypatch, name):
+    """Not by the current one: calls on two given streams may run at the same time."""
+    lib = use(monkeypatch, Library())
+    for raw in (7, 8, 7, 8):
+        calls()[name](Stream(raw))
+    by = {raw: {ws for ws, r in lib.calls if r == raw} for raw in (7, 8)}
+    assert len(by[7]) == len(by[8]) == 1 and by[7] != by[8]
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_captured_calls_have_workspaces_of_their_graph(monkeypatch, capturing, name):
+    lib = use(monkeypatch, Library())
+    run = calls()[name]
+    run(Stream(7))
+    capturing.append(1)
+    run(Stream(7))
+    run(Stream(7))
+    capturing.clear()
+    run(Stream(7))
+    ws = [w for w, _ in lib.calls]
+    assert ws[0] == ws[3] and len(set(ws)) == 3
+
+
+def test_outputs_are_allocated_in_the_stream_of_the_call(monkeypatch):
+    on = []
+
+    @contextlib.contextmanager
+    def stream_of(s):
+        on.append(s)
+        yield
+        on.pop()
+    empty, where = torch.empty, []
+    monkeypatch.setattr(api, "_on_stream", stream_of)
+    monkeypatch.setattr(torch, "empty", lambda *a, **k: where.append(on[-1] if on else None) or empty(*a, **k))
+    use(monkeypatch, Library())
+    f, h, i, c = torch.float32, torch.bfloat16, torch.int32, torch.int8
+    q, K, one, lens = Tensor((2, 4, 64), f), Tensor((2, 2, 99, 64), f), Tensor((2, 2, 64), f), Tensor((2,), i)
+    q8, K8, new8 = Tensor((2, 4, 64), h), Tensor((2, 2, 99, 64), c), Tensor((2, 2, 64), c)
+    rows, row, parts, lses = Tensor((2, 2, 99), f), Tensor((2, 2), f), Tensor((3, 2, 4, 64), f), Tensor((3, 2, 4), f)
+    for run in (lambda s: api.decode_attn(q, K, K, lens, stream=s),
+                lambda s: api.decode_attn_append(q, one, one, K, K, lens, stream=s),
+                lambda s: api.decode_attn_owned(q, K, K, lens, stream=s),
+                lambda s: api.decode_attn_noalloc(q, K, K, lens, stream=s),
+                lambda s: api.decode_attn_partial(q, K, K, lens, stream=s),
+                lambda s: api.decode_attn_combine(parts, lses, stream=s),
+                lambda s: api.decode_attn_q8(q8, K8, K8, rows, rows, lens, stream=s),
+                lambda s: api.decode_attn_q8_append(q8, new8, new8, row, row, K8, K8, rows, rows, lens, stream=s),
+                lambda s: api.decode_attn_mod(q, K, K, lens, ScoreMod(), stream=s),
+                lambda s: api.kv_quantize(q, c, stream=s)):
+        where.clear()
+        side = Stream(9)
+        run(side)
+        assert where and all(s is side for s in where)
