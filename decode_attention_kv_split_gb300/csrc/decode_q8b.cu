@@ -701,7 +701,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::CTAS)
         for (int j = 0; j < 2; ++j) {
           const float mx =
               fmaxf(fmaxf(s[0][nb][j], s[0][nb][j + 2]), fmaxf(s[1][nb][j], s[1][nb][j + 2]));
-          over |= mx + fmaxf(k_run[nb][j] + lv_top, 0.f) > m_run[nb][j] + (kHead + kLazy);
+          over |= (mx - m_run[nb][j]) + fmaxf(k_run[nb][j] + lv_top, 0.f) > kHead + kLazy;
         }
       const bool update = __any_sync(0xffffffffu, over);
       if (update) {
@@ -720,13 +720,15 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::CTAS)
             }
             const float m_old = m_run[nb][j], k_old = k_run[nb][j];
             const float m_new = fmaxf(m_old, fmaxf(mx[0], mx[1]) - kHead);
-            // the accumulator's reference, 2^(m - k), only grows
+            const float m_use = m_new == -INFINITY ? 0.f : m_new;  // (nothing seen yet)
+            // The accumulator's reference, 2^(m - k), only grows.  (Differences from m: a
+            // large score's own float would swallow a scale's logarithm.)
             const float a =
-                fmaxf(m_old - k_old, fmaxf(mx[0] + lv[0], mx[1] + lv[1]) - kHead);
-            // (nothing seen yet: any)
+                fmaxf(m_old - m_use - k_old,
+                      fmaxf(mx[0] - m_use + lv[0], mx[1] - m_use + lv[1]) - kHead);
             const float k_new =
-                m_new == -INFINITY ? 0.f : fminf(fmaxf(floorf(m_new - a), -126.f), 126.f);
-            const float alpha = ex2(m_old - (m_new == -INFINITY ? 0.f : m_new));
+                m_new == -INFINITY ? 0.f : fminf(fmaxf(floorf(-a), -126.f), 126.f);
+            const float alpha = ex2(m_old - m_use);
             const float f = alpha * pow2(fminf(fmaxf(k_new - k_old, -126.f), 127.f));
             m_run[nb][j] = m_new;
             k_run[nb][j] = k_new;

@@ -103,3 +103,26 @@ def test_a_query_that_is_not_finite_stays_in_its_head():
             keep = [h for h in range(h_q) if h != 3]
             D.check(out[:, keep], want[:, keep], tol[:, keep])
             assert not torch.isfinite(out[:, 3]).any()
+
+
+@pytest.mark.parametrize("out_dtype", OUTS, ids=OID)
+@pytest.mark.parametrize("splits", [0, 1])
+@pytest.mark.parametrize("d,h_q", [(64, 2), (128, 8), (128, 20)])
+def test_scores_beyond_the_steps_of_float(d, h_q, splits, out_dtype):
+    """Scores so large that a float of their size has no room for a scale's logarithm: one row is all
+    that counts, and its value comes out, off by its weight's rounding, the merge's and the output's."""
+    n = 700
+    V = codes((1, 1, n, d), torch.int8, 3)
+    q = torch.zeros(1, h_q, d, dtype=torch.bfloat16)
+    q[..., 0] = 1.0
+    ks = torch.full((1, 1, 44), 2.0 ** 30)
+    vs = torch.exp2(torch.randint(-20, 21, (1, 1, 44), generator=torch.Generator().manual_seed(1)).float())
+    part = D.weight_rounding("q8b", out_dtype) + 64 * D.U
+    for at in (0, 15, 16, 37, 300, 699):
+        K = torch.randint(-100, 101, (1, 1, n, d), dtype=torch.int8)
+        K[0, 0, at, 0] = 127
+        out = api.decode_attn_q8b(q.cuda(), K.cuda(), V.cuda(), ks.cuda(), vs.cuda(), i32([n]), 16, scale=1.0,
+                                  num_splits=splits, out_dtype=out_dtype).cpu().double()
+        want = (V[0, 0, at].double() * float(vs[0, 0, at // 16])).expand(1, h_q, d)
+        tol = want.abs() * part
+        D.check(out, want, tol + (want.abs() + tol) * (torch.finfo(out_dtype).eps / 2))
