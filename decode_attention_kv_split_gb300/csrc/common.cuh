@@ -589,7 +589,7 @@ struct TileMask<true> {
 // previous grid may still write it when this one starts.)
 __device__ __forceinline__ float head_slope(const SplitParams& p, int head, bool ok) {
   if (!p.mod.slopes || !ok) return 0.f;
-  const float s = __ldcg(p.mod.slopes + head) * 1.4426950408889634f;
+  const float s = p.mod.slopes[head] * 1.4426950408889634f;
   return s > 3e38f ? 3e38f : s < -3e38f ? -3e38f : s;
 }
 

@@ -398,7 +398,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
             const int h = ch / (D / 8), c = (ch % (D / 8)) * 8;
             const size_t bhq = size_t(it.b) * p.h_q + size_t(it.kvh) * p.group + h0 + h;
             v[u] = h0 + h < p.group && DA_IN(p, bhq, size_t(p.B) * p.h_q)
-                       ? __ldcg(reinterpret_cast<const uint4*>(qbase + h * (D * 2) + c * 2))
+                       ? *reinterpret_cast<const uint4*>(qbase + h * (D * 2) + c * 2)
                        : make_uint4(0, 0, 0, 0);
           }
 #pragma unroll

@@ -11,12 +11,18 @@ U = 2.0 ** -24  # half a step of float, relative to the value
 
 def weight_rounding(kind, out_dtype=torch.float32):
     """The relative rounding of a weight as a kernel family multiplies it: a float; a bf16 head and
-    a bf16 remainder (2^-8 of 2^-8); an fp16 head and an fp16 remainder (2^-11 of 2^-11)."""
+    a bf16 remainder (2^-8 of 2^-8); an fp16 head and an fp16 remainder (2^-11 of 2^-11), for a
+    bf16 output the head alone."""
+    if kind == "q8b" and out_dtype == torch.bfloat16:
+        return 2.0 ** -11
     return {"fp32": U, "bf16": 2.0 ** -16, "q8b": 2.0 ** -22}[kind]
 
 
+SHORT_CAP = 128.0  # up to here the cap of a bf16 output may take the form that is off by c 2^-22
+
+
 def attend(q, K, V, lens, scale, part, out_dtype=torch.float32, softcap=0.0, slopes=None, window=0, prefix=0,
-           begin=None, short_cap=True, floor=0.0):
+           begin=None, floor=0.0):
     """q [B, h_q, d_k], K/V [B, h_kv, n_max, d] -> (want, tol), float64 [B, h_q, d_v] both.
 
     With u = 2^-24, p_l a row's weight of the softmax and v_l its value, a computed output is
@@ -55,8 +61,9 @@ def attend(q, K, V, lens, scale, part, out_dtype=torch.float32, softcap=0.0, slo
             top = s.abs().amax(1, keepdim=True)
             e = d * U * size + 2.0 ** -22 * (top + 2.0)
             if softcap > 0:
-                # (a cap far above the scores is off by parts of them, not of itself)
-                e = e + 2.0 ** -22 * (softcap if short_cap and out_dtype == torch.bfloat16 else min(softcap, float(size.max())))
+                # (the long form of a cap far above the scores is off by parts of them, not of itself)
+                short = out_dtype == torch.bfloat16 and softcap <= SHORT_CAP
+                e = e + 2.0 ** -22 * (softcap if short else min(softcap, float(size.max())))
             if slopes is not None:
                 sl = torch.as_tensor(slopes, dtype=torch.float32).double().to(dev)[k * g:k * g + g, None]
                 s = s - sl * (n - 1 - rows).double()
