@@ -215,6 +215,12 @@ int check_mod(const da_score_mod* mod) {
   return DA_OK;
 }
 
+// Whether two arrays of n words share one.
+bool words_overlap(const void* a, const void* b, long long n) {
+  const long long apart = (long long)(reinterpret_cast<uintptr_t>(a) - reinterpret_cast<uintptr_t>(b));
+  return a && b && apart < 4 * n && apart > -4 * n;
+}
+
 long long seen_rows(const da_score_mod* mod, int n_max) {
   if (!mod) return -1;
   return mod->window > 0 ? (long long)mod->window + mod->prefix : n_max;
@@ -794,7 +800,9 @@ int decode_attn_mod_append(const void* q, const void* k_new, const void* v_new, 
   if (st != DA_OK) return st;
   if (!k_new || !v_new) return DA_ERR_NULL;
   if (!aligned16(k_new) || !aligned16(v_new)) return DA_ERR_ALIGN;
-  if (seq_lens_out && seq_lens_out == seq_lens) return DA_ERR_SHAPE;
+  // (one CTA writes the new lengths while others still read the old ones and the begins)
+  if (words_overlap(seq_lens_out, seq_lens, B) || words_overlap(seq_lens_out, mod->doc_begin, B))
+    return DA_ERR_SHAPE;
   return run_decode(q, K, V, seq_lens, out, B, h_q, h_kv, d_k, d_v, n_max, scale, dtype,
                     num_splits, workspace, workspace_bytes, dev_error, stream, k_new, v_new,
                     seq_lens_out, nullptr, 0, 0x7fffffff, nullptr, mod);
@@ -1036,6 +1044,8 @@ int kv_append_q8b(const void* k_new, const void* v_new, const long long* k_strid
     a.stride[0][i] = ks;
     a.stride[1][i] = vs;
   }
+  // (K and V are written at the same time, held codes scaled in place)
+  if (K == V || k_scale == v_scale) return DA_ERR_SHAPE;
   int dev, sms;
   if ((st = current_device(&dev, &sms)) != DA_OK) return st;
   a.x[0] = k_new, a.x[1] = v_new;
@@ -1066,6 +1076,7 @@ int kv_read_q8b(const void* K, const void* V, const float* k_scale, const float*
   if (!aligned16(k_out) || !aligned16(v_out) || !aligned16(K) || !aligned16(V) ||
       !aligned4(k_scale) || !aligned4(v_scale) || !aligned4(seq_lens) || !aligned4(row_begin))
     return DA_ERR_ALIGN;
+  if (k_out == v_out) return DA_ERR_SHAPE;
   int dev, sms;
   if ((st = current_device(&dev, &sms)) != DA_OK) return st;
   da::BlockReadArgs a{};

@@ -397,7 +397,8 @@ DA_API int decode_attn_mod(const void* q, const void* K, const void* V, const in
                            cudaStream_t stream);
 
 /* decode_attn_append with score terms: the row is appended whether the query
- * sees it or not, and n counts it. */
+ * sees it or not, and n counts it.  seq_lens_out may share no element with
+ * seq_lens or doc_begin. */
 DA_API int decode_attn_mod_append(const void* q, const void* k_new, const void* v_new, void* K,
                                   void* V, const int32_t* seq_lens, int32_t* seq_lens_out,
                                   const da_score_mod* mod, void* out, int B, int h_q, int h_kv,
@@ -459,6 +460,7 @@ DA_API int decode_attn_q8b(const void* q, const void* K, const void* V, const fl
  *                  [0, n_max] writes nothing, an n_new outside [0, T] is
  *                  clamped; each sets DA_DEVERR_POS.  The pos of a sequence
  *                  with m = 0 is not looked at.
+ *   K, V, k_scale, v_scale : four different arrays
  *   NaN and infinite elements are written as 0 and set DA_DEVERR_VALUE.
  * Does not change lengths: the caller advances them.  T = 0 does nothing.
  */
@@ -472,9 +474,9 @@ DA_API int kv_append_q8b(const void* k_new, const void* v_new, const long long* 
  * Read rows of a block-scaled cache back as values: for every b, h and i < T
  * with row_begin[b] + i < seq_lens[b] (row_begin NULL: 0)
  *   k_out[b, h, i, :] = k_scale[b, h, block of the row] * value(code), v_out alike,
- * rounded once to out_dtype (DA_FP32 or DA_BF16).  Other rows of the outputs
- * are left as they are.
- *   k_out, v_out : device [B, h_kv, T, d], 16-byte aligned
+ * rounded to float (exact for a scale that is a power of two) and from that to
+ * out_dtype (DA_FP32 or DA_BF16).  Other rows of the outputs are left as they are.
+ *   k_out, v_out : device [B, h_kv, T, d], 16-byte aligned, two different arrays
  *   seq_lens     : device int32 [B]; outside [0, n_max]: clamped, DA_DEVERR_SEQ_LEN
  *   row_begin    : nullable device int32 [B]; negative: nothing is read for that
  *                  sequence, DA_DEVERR_SEQ_LEN
