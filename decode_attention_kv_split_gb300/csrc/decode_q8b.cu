@@ -765,7 +765,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::CTAS)
 #pragma unroll
             for (int u = 0; u < 2; ++u)
               s[u][nb][e] = s[u][nb][e] * 0x1p16f *
-                            fminf(fmaxf(vs[u] * 0x1p-16f * pow2(k_run[nb][e & 1]), -0x1p127f),
+                            fminf(fmaxf(vs[u] * (pow2(k_run[nb][e & 1]) * 0x1p-16f), -0x1p127f),
                                   0x1p127f);
       } else {
 #pragma unroll

@@ -126,3 +126,26 @@ def test_scores_beyond_the_steps_of_float(d, h_q, splits, out_dtype):
         want = (V[0, 0, at].double() * float(vs[0, 0, at // 16])).expand(1, h_q, d)
         tol = want.abs() * part
         D.check(out, want, tol + (want.abs() + tol) * (torch.finfo(out_dtype).eps / 2))
+
+
+@pytest.mark.parametrize("out_dtype", OUTS, ids=OID)
+@pytest.mark.parametrize("d,h_q", [(64, 4), (128, 8), (128, 20)])
+def test_v_scales_at_the_ends_of_float(d, h_q, out_dtype):
+    """V scales of every mantissa, down to float's subnormals and up to its largest powers."""
+    B, n, block = 2, 300, 16
+    g = torch.Generator().manual_seed(2)
+    K, V = codes((B, 1, n, d), torch.int8, 4), codes((B, 1, n, d), torch.int8, 5)
+    ks = torch.full((B, 1, 19), 2.0 ** -6)
+    q = torch.randn(B, h_q, d, generator=g).to(torch.bfloat16)
+    at = torch.arange(n) // block
+    for low, high in ((-130.0, -124.0), (-127.0, -100.0), (-3.0, 3.0), (90.0, 110.0)):
+        vs = torch.exp2(torch.empty(B, 1, 19, dtype=torch.float64).uniform_(low, high, generator=g)).float()
+        Kv, Vv = K.double() * 2.0 ** -6, V.double() * vs[:, :, at, None].double()
+        for splits in (0, 1, 2):
+            out = api.decode_attn_q8b(q.cuda(), K.cuda(), V.cuda(), ks.cuda(), vs.cuda(), i32([n, 77]), block, num_splits=splits,
+                                      out_dtype=out_dtype)
+            want, tol = D.attend(q.cuda(), Kv.cuda(), Vv.cuda(), [n, 77], d ** -0.5, D.weight_rounding("q8b", out_dtype),
+                                 out_dtype, floor=2.0 ** -31)
+            # (sums and outputs among the subnormals: half a step of theirs for each of 64 roundings)
+            D.check(out, want, tol + (64 * 2.0 ** -150 if out_dtype == torch.float32 else 2.0 ** -134 + 64 * 2.0 ** -150),
+                    f"scales from 2^{low} to 2^{high}")
