@@ -461,7 +461,8 @@ struct ItemRows {
 // Kernels are compiled for sets of terms (bits), each split-kernel source once
 // per set (DA_TERMS, see build.py): tests of the terms inside a stage keep the
 // compiler from moving loads and MMAs across them, which cost the 4-head bf16
-// kernel 0.38 of 0.63 us a stage.
+// kernel 0.38 of 0.63 us a stage.  (Two tests are left inside: the bf16 and tcgen05
+// kernels choose between the forms of a cap, the latter by the slopes' signs too.)
 constexpr int kTermsMask = 1;    // the row mapping and the mask: with any term
 constexpr int kTermsCap = 2;
 constexpr int kTermsSlopes = 4;
@@ -633,7 +634,7 @@ __device__ __forceinline__ float tanh_fast(float x) {
 // c - 2 c / (1 + e^(2 t / c)): 4 instructions, off by about c 2^-22 whatever the
 // score's size, and its weight by that factor.  For a bf16 output and
 // c <= kShortTanhCap that is at most 2^-15, far below the output's own half step
-// of 2^-9; other calls take tanh_fast.
+// of 2^-8; other calls take tanh_fast.
 constexpr float kShortTanhCap = 128.f;
 __device__ __forceinline__ float capped_short(const ScoreTerms& m, float x) {
   float r;

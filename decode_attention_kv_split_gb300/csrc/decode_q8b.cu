@@ -19,13 +19,12 @@
 // eight warps a SM: 40.8 us on 16 ragged int8 sequences with 8 kv heads).  Every
 // CTA finds its chunk from the lengths (find_item_few, _many): the chunk length is the
 // shortest whose chunks all fit on the GPU at once, so that there is one round
-// of equal CTAs, whatever n_max is (31.7 us; 2.1 more with a length fixed by n_max).
+// of equal CTAs, whatever n_max is (31.9 us; 2.1 more with a length fixed by n_max).
 // Beyond kBlockRoundRows rows a CTA there are two or three shorter rounds: HBM does
 // not serve all SMs alike, and the CTAs of a later round go where an early one
-// ended (2 x 131072 rows of fp8 with 64 query heads: 85.6 us in one round, 83.7 in
-// two, 6.4 TB/s, with an earlier form of the steps, 82.5 with this one; ncu on the former: DRAM 77 % busy, 1.4 instructions a cycle of 4, the MMA
-// pipe 17 %).  With 32 heads on one kv head the MMAs and the instructions around
-// them, not HBM, are the bound: 32.8 us for 8 x 30000 rows, 9.2 us of HBM time.
+// ended (2 x 131072 rows of fp8 with 64 query heads: 82.9 us, 6.5 TB/s; one round took
+// 1.9 us more than two).  With 32 heads on one kv head the MMAs and the instructions
+// around them, not HBM, are the bound: 33.3 us for 8 x 30000 rows, 9.2 us of HBM time.
 // Caches of up to 4096 rows with few enough units (make_plan) need no list: a cluster
 // of up to eight CTAs takes a unit's rows in equal shares and joins them through
 // distributed shared memory (finish_cluster), without a second kernel.
@@ -56,8 +55,8 @@
 // fp16 head and an fp16 remainder (~22 bits, two MMAs).  For a bf16 output it is
 // the head alone: 2^-11 of each weight, an eighth of the half step (2^-8) by which
 // the output's own rounding moves it, and a third of the MMAs less (with the remainder
-// the cases below take 33.8, 84.4 and 39.0 us, not 31.7, 82.5 and 32.8, for errors
-// against 64 bits of 0.99 of these).
+// the three steps named here take 2.1, 1.9 and 6.2 us more, for errors against 64 bits
+// of 0.99 of these; a caller who wants the digits asks for a float32 output).
 // Scales may be of any size (2^-126 for tiny rows), and fp16 has few exponents,
 // so a warp keeps each head's accumulator in a unit that follows the largest
 // weight times V scale that the head has seen, a second running maximum beside
@@ -65,7 +64,8 @@
 // returns at the chunk's end.  It differs from the softmax's reference by a power
 // of two, so that P is rounded once.  (A unit for all heads that follows the V
 // scales alone takes a head's digits where a block it gives no weight, or that only
-// its neighbours weigh on, has a far larger scale; it takes 31.2, 84.1 and 31.5 us.)
+// its neighbours weigh on, has a far larger scale; with that the same three steps take
+// 31.2, 84.1 and 31.5 us, with this one 31.9, 82.9 and 33.3.)
 #include <math.h>
 
 #include "common.cuh"
@@ -493,7 +493,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, Cfg::CTAS)
   // zero): lane (g, t) takes columns [t D/4, (t + 1) D/4) of head 8 nb + g.
   // (Ordinary loads: not through the read-only path, as the previous grid may still
   // write q when this one starts, but through L1, as all four warps want them; from L2
-  // the long fp8 step takes 86.4 us, this way 83.3.)
+  // the long fp8 step takes 3 us more.)
   uint32_t qf[MB][NB][2];
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb) {
