@@ -137,3 +137,43 @@ def test_long_caches(dtype, out_dtype):
         run(shape, 40000, [40000, 31111], 64, dtype, out_dtype)
         run(shape, 40000, [40000, 123], 128, dtype, out_dtype, softcap=30.0, window=30000, prefix=4)
         run(shape, 40000, [39999, 40000], 16, dtype, out_dtype, slopes=falling(shape[0]), begin=[5, 39000])
+
+
+@pytest.mark.parametrize("splits", [0, 1, 3])
+@pytest.mark.parametrize("dtype", KINDS, ids=KID)
+@pytest.mark.parametrize("shape", SHAPES, ids=SID)
+def test_largest_slopes(shape, dtype, splits):
+    """One row is all that counts, the last one or the first that is seen: its value, off by its
+    weight's rounding and a merge's."""
+    h_q, h_kv, d = shape
+    K, V = (torch.randn((2, h_kv, 700, d), device="cuda").mul(20).clamp(-100, 100) for _ in range(2))
+    K, V = (t.round().to(torch.int8) if dtype == torch.int8 else t.to(dtype) for t in (K, V))
+    s = torch.exp2(torch.randint(-9, -3, (2, h_kv, 22), device="cuda").float())
+    q = torch.randn((2, h_q, d), device="cuda").to(torch.bfloat16)
+    lens = [700, 277]
+    for slope in (3.4e38, -3.4e38, float("inf"), float("-inf")):
+        for terms in ({}, {"window": 40, "softcap": 9.0}):
+            mod = ScoreMod(slopes=torch.full((h_q,), slope, device="cuda"), **terms)
+            out = api.decode_attn_q8b(q, K, V, s, s, i32(lens), 32, mod=mod, num_splits=splits).double()
+            for b, n in enumerate(lens):
+                at = n - 1 if slope > 0 else max(0, n - 40) if terms else 0
+                want = (V[b, :, at].double() * s[b, :, at // 32, None].double()).repeat_interleave(h_q // h_kv, 0)
+                assert bool(((out[b] - want).abs() <= want.abs() * (D.weight_rounding("q8b") + 64 * D.U)).all())
+
+
+def test_results_repeat():
+    """The same call gives the same bits, whatever ran before it on the same workspace."""
+    g = torch.Generator(device="cuda").manual_seed(1)
+    K, V = (torch.randint(-127, 128, (3, 2, 9000, 128), dtype=torch.int8, device="cuda", generator=g) for _ in range(2))
+    s = torch.exp2(torch.randn((3, 2, 282), device="cuda", generator=g) - 6)
+    q = torch.randn((3, 32, 128), device="cuda", generator=g).to(torch.bfloat16)
+    Kb, Vb = (t.to(torch.bfloat16) / 64 for t in (K, V))
+    for lens in ([9000, 100, 4097], [1, 0, 8999]):
+        runs = [lambda c=c, n=n, o=o: api.decode_attn_q8b(q, K, V, s, s, i32(lens), 32, mod=ScoreMod(softcap=c) if c else None,
+                                                          num_splits=n, out_dtype=o)
+                for c in (0.0, 20.0) for n in (0, 7) for o in OUTS]
+        runs += [lambda c=c, n=n: api.decode_attn_mod(q, Kb, Vb, i32(lens), ScoreMod(softcap=c, window=5000), num_splits=n)
+                 for c in (0.0, 20.0) for n in (0, 7, -1)]
+        first = [run().clone() for run in runs]
+        for run, want in list(zip(runs, first))[::-1]:
+            assert torch.equal(run(), want)
