@@ -9,6 +9,7 @@ from . import workloads  # noqa: F401  (seeded inputs; no attention arithmetic)
 from .api import (  # noqa: F401
     DecodeAttnError,
     ScoreMod,
+    chunk_attn,
     decode_attn,
     decode_attn_append,
     decode_attn_mod,
@@ -16,8 +17,10 @@ from .api import (  # noqa: F401
     decode_attn_noalloc,
     decode_attn_owned,
     decode_attn_q8b,
+    decode_attn_shared,
     kv_append,
     kv_append_q8b,
+    kv_append_rope,
     kv_read_q8b,
     launch_count,
     resolve_splits,

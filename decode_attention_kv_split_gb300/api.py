@@ -77,6 +77,14 @@ SIGNATURES = {
                              _P, _SZ, _P, _P]),
     "kv_append_q8b": (_I, [_P, _P, _P, _P, _I, _I, _P, _P, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I,
                            _P, _P]),
+    "kv_append_rope": (_I, [_P, _P, _P, _P, _P, _P, _I, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I,
+                            _P, _P, _P, _F, _I, _I, _I, _I, _I, _I, _I, _P, _P]),
+    "chunk_attn_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I, _I, _I, ctypes.POINTER(_I)]),
+    "chunk_attn": (_I, [_P, _P, _I, _P, _P, _P, _P, _I, _I, _P, _P, _I, _I, _I, _I, _I, _F, _I, _P,
+                        _SZ, _P, _P]),
+    "decode_attn_shared_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I, _I, _I, ctypes.POINTER(_I)]),
+    "decode_attn_shared": (_I, [_P, _P, _P, _I, _I, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _I, _P,
+                                _SZ, _P, _P]),
     "kv_read_q8b": (_I, [_P, _P, _P, _P, _I, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _P, _P]),
 }
 
@@ -914,3 +922,221 @@ def kv_read_q8b(K: torch.Tensor, V: torch.Tensor, k_scale: torch.Tensor, v_scale
             torch.cuda.set_device(prev)
     _check(st, "kv_read_q8b")
     return k_out, v_out
+
+
+# ----------------------------------- from projections to the cache, chunks, shared prefixes
+def _row_strides(name: str, t: torch.Tensor, shape, dtype, device: int, write: bool = False):
+    """The strides (b, head, token) of rows t, which has to be of ``shape`` [B, h, T, d]."""
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != device:
+        raise ValueError(f"{name} must be a {dtype} tensor {list(shape)} on the cache's device")
+    sb, sh, st, sd = t.stride()
+    if sd != 1:
+        raise ValueError(f"{name} must be contiguous in its last dimension")
+    B, h, T, d = shape
+    # a dimension of one element has no step: its stride in the tensor may be anything
+    steps = (sb if B > 1 else 0, sh if h > 1 else 0, st if T > 1 else 0)
+    if write and not t.is_contiguous():
+        # rows that are written may not share an element: each step passes what the smaller ones reach
+        reach = d
+        for step, n in sorted(zip(steps, (B, h, T))):
+            if n > 1:
+                if step < reach:
+                    raise ValueError(f"{name} must not overlap itself")
+                reach = step * (n - 1) + reach
+    return _Strides(*steps)
+
+
+def _new_out(out, dtype, B: int, h: int, T: int, d: int, device, stream):
+    """Rows [B, h, T, d] of an output; allocated token after token where not given."""
+    if out is None:
+        with _on_stream(stream):
+            out = torch.empty((B, T, h, d), dtype=dtype, device=device).transpose(1, 2)
+    return out
+
+
+def kv_append_rope(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor, K: torch.Tensor,
+                   V: torch.Tensor, pos: torch.Tensor, cos: torch.Tensor, sin: torch.Tensor,
+                   q_weight: torch.Tensor | None = None, k_weight: torch.Tensor | None = None,
+                   eps: float = 1e-6, n_new: torch.Tensor | None = None,
+                   angle_pos: torch.Tensor | None = None, interleaved: bool = False,
+                   q_out: torch.Tensor | None = None, dev_error: torch.Tensor | None = None,
+                   stream: torch.cuda.Stream | None = None) -> torch.Tensor:
+    """Norm each head of q and k, rotate them by position, and write k and v into the cache (calls
+    ``kv_append_rope``): tokens q [B, h_q, T, d_k], k_new [B, h_kv, T, d_k], v_new [B, h_kv, T, d_v]
+    (any strides but a contiguous last dimension; [B, h, d] for one token) become rows pos[b] ..
+    of the caches K [B, h_kv, n_max, d_k], V [B, h_kv, n_max, d_v], n_new[b] of them where given.
+    ``cos`` and ``sin`` are float32 [n_angles, rot / 2]; angle row angle_pos[b] + i (pos[b] + i where
+    not given) turns token i.  Weights None: no norm.  Returns ``q_out``, shaped as q (allocated as
+    [B, T, h_q, d_k] in memory when None; q itself is allowed).  Lengths are the caller's to advance."""
+    single = q.dim() == 3
+    if single:
+        q, k_new, v_new = q.unsqueeze(2), k_new.unsqueeze(2), v_new.unsqueeze(2)
+        if q_out is not None:
+            q_out = q_out.unsqueeze(2)
+    device, dtype = K.get_device(), K.dtype
+    code = _DTYPES.get(dtype)
+    if q.dim() != 4 or K.dim() != 4 or V.dim() != 4 or code is None or V.dtype is not dtype:
+        raise ValueError("expected q [B, h_q, T, d_k] and float32 or bfloat16 caches K [B, h_kv, n_max, d_k], "
+                         "V [B, h_kv, n_max, d_v]")
+    B, h_kv, n_max, d_k = K.shape
+    h_q, T, d_v = q.shape[1], q.shape[2], V.shape[3]
+    if V.shape != (B, h_kv, n_max, d_v) or device < 0 or V.get_device() != device \
+            or not (K.is_contiguous() and V.is_contiguous()):
+        raise ValueError("K and V must be contiguous CUDA tensors of one batch, on one device")
+    q_shape = (B, h_q, T, d_k)
+    strides = (_row_strides("q", q, q_shape, dtype, device),
+               _row_strides("k_new", k_new, (B, h_kv, T, d_k), dtype, device),
+               _row_strides("v_new", v_new, (B, h_kv, T, d_v), dtype, device))
+    q_out = _new_out(q_out, dtype, B, h_q, T, d_k, K.device, stream)
+    out_strides = _row_strides("q_out", q_out, q_shape, dtype, device, write=True)
+    angles = cos.shape
+    for t in (cos, sin):
+        if t.dim() != 2 or t.shape != angles or t.dtype is not torch.float32 \
+                or t.get_device() != device or not t.is_contiguous():
+            raise ValueError("cos and sin must be contiguous float32 tensors [n_angles, rot / 2] on "
+                             "the cache's device")
+    for t in (q_weight, k_weight):
+        if t is not None and (t.shape != (d_k,) or t.dtype is not dtype or t.get_device() != device
+                              or not t.is_contiguous()):
+            raise ValueError("q_weight and k_weight must be contiguous tensors [d_k] of the cache's "
+                             "type and device")
+    if _bad_seq_lens(pos, B, device):
+        raise ValueError("pos must be a contiguous int32 tensor [B] on the cache's device")
+    _row_counts("n_new", n_new, B, device)
+    _row_counts("angle_pos", angle_pos, B, device)
+    err = None if dev_error is None else _error_word(dev_error, device)
+    prev = _enter(device)
+    try:
+        st = (_lib or load()).kv_append_rope(
+            q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), *strides, T, _addr(n_new),
+            q_out.data_ptr(), out_strides, K.data_ptr(), V.data_ptr(), pos.data_ptr(),
+            cos.data_ptr(), sin.data_ptr(), angles[0], 2 * angles[1], 1 if interleaved else 0,
+            _addr(angle_pos), _addr(q_weight), _addr(k_weight), eps, B, h_q, h_kv, d_k, d_v, n_max,
+            code, err, _raw(stream, device))
+    finally:
+        if prev >= 0:
+            torch.cuda.set_device(prev)
+    _check(st, "kv_append_rope")
+    return q_out.squeeze(2) if single else q_out
+
+
+def _attend_workspace(entry: str, sizes, device: int, stream, raw: int,
+                      workspace: torch.Tensor | None):
+    """The workspace of a chunk or shared-prefix call, its bytes and the lock to hold while the
+    library is called."""
+    if workspace is not None:
+        if workspace.get_device() != device or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on the query's device")
+        return workspace, workspace.numel() * workspace.element_size(), _unlocked
+    key = (entry, device, sizes)
+    need = _mod_bytes_cache.get(key)
+    if need is None:
+        st = ctypes.c_int(0)
+        need = int(getattr(load(), entry)(*sizes, ctypes.byref(st)))
+        _check(st.value, entry)
+        if len(_mod_bytes_cache) > 4096:
+            _mod_bytes_cache.clear()
+        _mod_bytes_cache[key] = need
+    if need == 0:
+        return None, 0, _unlocked
+    return _kept_workspace((device, raw, "attend"), need, stream)
+
+
+def chunk_attn(q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, seq_lens: torch.Tensor,
+               n_new: torch.Tensor | None = None, window: int = 0, prefix: int = 0,
+               out: torch.Tensor | None = None, scale: float | None = None,
+               workspace: torch.Tensor | None = None, dev_error: torch.Tensor | None = None,
+               stream: torch.cuda.Stream | None = None,
+               out_dtype: torch.dtype | None = None) -> torch.Tensor:
+    """Attention of a chunk of tokens over the cache that holds them (calls ``chunk_attn``): q
+    [B, h_q, T, d] bf16 (any strides but a contiguous last dimension), K, V [B, h_kv, n_max, d];
+    the last n_new[b] of sequence b's seq_lens[b] rows (T where not given) are the chunk's.  Token i
+    at row p sees row l <= p when l > p - window (0: all) or l < prefix.  Returns ``out`` [B, h_q,
+    T, d], float32 or bfloat16 (any strides; allocated as [B, T, h_q, d] in memory when None);
+    tokens at or past n_new[b] are left as they are."""
+    device = q.get_device()
+    if q.dim() != 4 or K.dim() != 4 or V.shape != K.shape:
+        raise ValueError("expected q [B, h_q, T, d], K and V [B, h_kv, n_max, d]")
+    B, h_kv, n_max, d = K.shape
+    h_q, T = q.shape[1], q.shape[2]
+    if K.dtype is not torch.bfloat16 or V.dtype is not torch.bfloat16 or device < 0 \
+            or K.get_device() != device or V.get_device() != device \
+            or not (K.is_contiguous() and V.is_contiguous()):
+        raise ValueError("K and V must be contiguous bfloat16 CUDA tensors on the query's device")
+    shape = (B, h_q, T, d)
+    q_strides = _row_strides("q", q, shape, torch.bfloat16, device)
+    out = _new_out(out, out_dtype or torch.float32, B, h_q, T, d, q.device, stream)
+    dtype = out.dtype
+    if (dtype is not torch.bfloat16 and dtype is not torch.float32) \
+            or (out_dtype is not None and dtype is not out_dtype):
+        raise ValueError("out must be float32 or bfloat16 (and of out_dtype where that is given)")
+    out_strides = _row_strides("out", out, shape, dtype, device, write=True)
+    if _bad_seq_lens(seq_lens, B, device):
+        raise ValueError("seq_lens must be a contiguous int32 tensor [B] on the device of the others")
+    _row_counts("n_new", n_new, B, device)
+    if not 0 <= window < 1 << 31 or not 0 <= prefix < 1 << 31:
+        raise ValueError("window and prefix must be non-negative ints")
+    err = None if dev_error is None else _error_word(dev_error, device)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    code = DA_BF16 | (DA_OUT_BF16 if dtype is torch.bfloat16 else 0)
+    prev = _enter(device)
+    try:
+        raw = _raw(stream, device)
+        ws, nbytes, lock = _attend_workspace("chunk_attn_workspace_bytes",
+                                             (B, T, h_q, h_kv, d, n_max, code), device, stream, raw,
+                                             workspace)
+        with lock:
+            st = (_lib or load()).chunk_attn(
+                q.data_ptr(), q_strides, T, _addr(n_new), K.data_ptr(), V.data_ptr(),
+                seq_lens.data_ptr(), window, prefix, out.data_ptr(), out_strides, B, h_q, h_kv, d,
+                n_max, scale, code, _addr(ws), nbytes, err, raw)
+    finally:
+        if prev >= 0:
+            torch.cuda.set_device(prev)
+    _check(st, "chunk_attn")
+    return out
+
+
+def decode_attn_shared(q: torch.Tensor, K_prefix: torch.Tensor, V_prefix: torch.Tensor,
+                       K: torch.Tensor, V: torch.Tensor, seq_lens: torch.Tensor,
+                       out: torch.Tensor | None = None, prefix_len: int | None = None,
+                       scale: float | None = None, workspace: torch.Tensor | None = None,
+                       dev_error: torch.Tensor | None = None,
+                       stream: torch.cuda.Stream | None = None,
+                       out_dtype: torch.dtype | None = None) -> torch.Tensor:
+    """Decode attention of a batch that shares a prefix (calls ``decode_attn_shared``): each query q
+    [B, h_q, d] sees the first prefix_len rows (all by default) of K_prefix, V_prefix [h_kv,
+    prefix_max, d], then the seq_lens[b] rows of its own K, V [B, h_kv, n_max, d] (bf16).  The
+    prefix is read once for the whole batch.  Returns ``out`` [B, h_q, d]."""
+    device, out, dims, dt = _cache_args(q, K, V, seq_lens, out, out_dtype, stream)
+    B, h_q, h_kv, d, d_v, n_max = dims
+    if K_prefix.dim() != 3 or K_prefix.shape[0] != h_kv or K_prefix.shape[2] != d or d_v != d \
+            or V_prefix.shape != K_prefix.shape or K_prefix.dtype is not K.dtype \
+            or V_prefix.dtype is not K.dtype or K_prefix.get_device() != device \
+            or V_prefix.get_device() != device \
+            or not (K_prefix.is_contiguous() and V_prefix.is_contiguous()):
+        raise ValueError("K_prefix and V_prefix must be contiguous tensors [h_kv, prefix_max, d] of "
+                         "the cache's type and device")
+    prefix_max = K_prefix.shape[1]
+    if prefix_len is None:
+        prefix_len = prefix_max
+    err = None if dev_error is None else _error_word(dev_error, device)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    prev = _enter(device)
+    try:
+        raw = _raw(stream, device)
+        ws, nbytes, lock = _attend_workspace("decode_attn_shared_workspace_bytes",
+                                             (B, h_q, h_kv, d, n_max, prefix_len, dt), device,
+                                             stream, raw, workspace)
+        with lock:
+            st = (_lib or load()).decode_attn_shared(
+                q.data_ptr(), K_prefix.data_ptr(), V_prefix.data_ptr(), prefix_len, prefix_max,
+                K.data_ptr(), V.data_ptr(), seq_lens.data_ptr(), out.data_ptr(), B, h_q, h_kv, d,
+                n_max, scale, dt, _addr(ws), nbytes, err, raw)
+    finally:
+        if prev >= 0:
+            torch.cuda.set_device(prev)
+    _check(st, "decode_attn_shared")
+    return out

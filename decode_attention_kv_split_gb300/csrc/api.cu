@@ -977,6 +977,12 @@ int block_shift(int block) {
 }
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
+// A stride of rows that are moved 16 bytes at a time (the bound keeps offsets inside 64 bits).
+int check_stride(long long stride, int es) {
+  if (stride < 0 || stride > (1LL << 31) * 256) return DA_ERR_SHAPE;
+  return stride * es % 16 != 0 ? DA_ERR_ALIGN : DA_OK;
+}
+
 // Sizes and types shared by the write into and the read from a block-scaled cache.
 int check_blocks(int B, int h_kv, int T, int d, int n_max, int block, int dtype, int io_dtype) {
   if (!is_q8(dtype) || (io_dtype != DA_FP32 && io_dtype != DA_BF16)) return DA_ERR_DTYPE;
@@ -1093,6 +1099,274 @@ int kv_read_q8b(const void* K, const void* V, const float* k_scale, const float*
   if (e != cudaSuccess) return fail_cuda(e, "kv_read_q8b launch");
   g_launches.fetch_add(1);
   return DA_OK;
+}
+
+int kv_append_rope(const void* q, const void* k_new, const void* v_new, const long long* q_strides,
+                   const long long* k_strides, const long long* v_strides, int T,
+                   const int32_t* n_new, void* q_out, const long long* out_strides, void* K, void* V,
+                   const int32_t* pos, const float* cos, const float* sin, int n_angles, int rot,
+                   int interleaved, const int32_t* angle_pos, const void* q_weight,
+                   const void* k_weight, float eps, int B, int h_q, int h_kv, int d_k, int d_v,
+                   int n_max, int dtype, int32_t* dev_error, cudaStream_t stream) {
+  if (!K || !V || !pos || !cos || !sin || !q_strides || !k_strides || !v_strides || !out_strides)
+    return DA_ERR_NULL;
+  if (dtype != DA_FP32 && dtype != DA_BF16) return DA_ERR_DTYPE;
+  if (B <= 0 || h_q <= 0 || h_kv <= 0 || T < 0 || n_max <= 0 || n_max > (1 << 30))
+    return DA_ERR_SHAPE;
+  if (n_angles <= 0 || rot <= 0 || rot > d_k || rot % 16 != 0) return DA_ERR_SHAPE;
+  if (!isfinite(eps) || eps < 0.f) return DA_ERR_SHAPE;
+  if ((long long)B * h_kv * (long long)n_max > 0x7fffffffLL) return DA_ERR_SHAPE;
+  const bool sizes = (d_k == d_v && (d_k == 64 || d_k == 128 || d_k == 256)) ||
+                     (d_k == 192 && d_v == 128);
+  if (!sizes) return DA_ERR_UNSUPPORTED;
+  if (T == 0) return DA_OK;
+  // lanes of the launch (one to four heads for every 4 to 32 of them) in 32 bits
+  if (T > (1 << 30) || (double)B * T * (h_q + 2.0 * h_kv) * 32.0 > 2147483647.0 * 256.0)
+    return DA_ERR_SHAPE;
+  if (!q || !k_new || !v_new || !q_out) return DA_ERR_NULL;
+  if (!aligned16(q) || !aligned16(k_new) || !aligned16(v_new) || !aligned16(q_out) ||
+      !aligned16(K) || !aligned16(V) || !aligned16(cos) || !aligned16(sin) ||
+      !aligned16(q_weight) || !aligned16(k_weight) || !aligned4(pos) || !aligned4(n_new) ||
+      !aligned4(angle_pos))
+    return DA_ERR_ALIGN;
+  if (K == V || cos == sin) return DA_ERR_SHAPE;
+  da::RopeAppendArgs a{};
+  const long long* strides[4] = {q_strides, k_strides, v_strides, out_strides};
+  const int heads[4] = {h_q, h_kv, h_kv, h_q}, widths[4] = {d_k, d_k, d_v, d_k};
+  for (int x = 0; x < 4; ++x) {
+    const long long shape[3] = {B, heads[x], T};
+    long long last = widths[x];
+    for (int i = 0; i < 3; ++i) {
+      const int st = check_stride(strides[x][i], elem_size(dtype));
+      if (st != DA_OK) return st;
+      (x < 3 ? a.x_stride[x] : a.out_stride)[i] = strides[x][i];
+      last += (shape[i] - 1) * strides[x][i];
+    }
+    (x < 3 ? a.x_elems[x] : a.out_elems) = last;
+  }
+  int dev, sms;
+  const int st = current_device(&dev, &sms);
+  if (st != DA_OK) return st;
+  a.x[0] = q, a.x[1] = k_new, a.x[2] = v_new;
+  a.q_out = q_out;
+  a.cache[0] = K, a.cache[1] = V;
+  a.pos = pos, a.n_new = n_new, a.angle_pos = angle_pos, a.cos = cos, a.sin = sin;
+  a.weight[0] = q_weight, a.weight[1] = k_weight;
+  a.dev_error = dev_error;
+  a.B = B, a.T = T, a.h_q = h_q, a.h_kv = h_kv, a.d_k = d_k, a.d_v = d_v, a.n_max = n_max;
+  a.rot = rot, a.n_angles = n_angles, a.interleaved = interleaved != 0;
+  a.bf16 = dtype == DA_BF16, a.sms = sms;
+  a.eps = eps, a.inv_d = 1.f / float(d_k);
+  const cudaError_t e = da::launch_kv_append_rope(a, stream);
+  if (e != cudaSuccess) return fail_cuda(e, "kv_append_rope launch");
+  g_launches.fetch_add(1);
+  return DA_OK;
+}
+
+namespace {
+// The launches of chunk_attn and decode_attn_shared.
+struct AttendPlan {
+  int slice;                 // sequences per launch
+  int q_tiles, prefix_tiles, entries, pitch, list;
+  long long units, max_items;
+  size_t table_bytes, part_rows;
+  size_t bytes(int d) const {
+    return list ? table_bytes + part_rows * (size_t(d) + 1) * 4 : 0;
+  }
+};
+
+// Sizes and types of both; P < 0: no shared prefix.
+int plan_attend(int B, int T, int h_q, int h_kv, int d, int n_max, int dtype, int P, int sms,
+                AttendPlan* plan) {
+  DtypeArg dt;
+  if (!parse_dtype(dtype, &dt)) return DA_ERR_DTYPE;
+  if (dt.kv != DA_FP32 && dt.kv != DA_BF16) return DA_ERR_DTYPE;
+  const int st = check_sizes(B, h_q, h_kv, d, d, n_max, dtype);
+  if (st != DA_OK) return st;
+  if (dt.kv != DA_BF16 || (d != 64 && d != 128)) return DA_ERR_UNSUPPORTED;
+  if (T < 0 || T > (1 << 30)) return DA_ERR_SHAPE;
+  if (T == 0) return *plan = AttendPlan{}, DA_OK;
+  const long long g = h_q / h_kv, rows = T * g;
+  // (query rows of a sequence, and of a batch behind a prefix, are counted in 32 bits)
+  if (rows > (1LL << 30) || (P >= 0 && B * g > (1LL << 30))) return DA_ERR_SHAPE;
+  AttendPlan a{};
+  a.q_tiles = int((rows + da::kAttendRows - 1) / da::kAttendRows);
+  a.slice = B;
+  if (P >= 0) {
+    const int most = (da::kAttendEntries - 1) / a.q_tiles;  // sequences whose entries fit a list
+    if (most < 1) return DA_ERR_UNSUPPORTED;
+    const int launches = (B + most - 1) / most;
+    a.slice = (B + launches - 1) / launches;
+    a.prefix_tiles = int((a.slice * g + da::kAttendRows - 1) / da::kAttendRows);
+  }
+  a.units = ((long long)a.slice * a.q_tiles + a.prefix_tiles) * h_kv;
+  if (a.units > 0x7fffffffLL - 2 * sms) return DA_ERR_SHAPE;
+  const long long entries = (long long)a.slice * a.q_tiles + (P >= 0 ? 1 : 0);
+  // Cut and merged behind a prefix (its units and a sequence's own are merged anyway), and in a
+  // chunk when there are few units of more than a few tiles.
+  a.list = P >= 0 || (a.units < 4LL * sms && n_max > 2 * 128 && entries <= da::kAttendEntries);
+  a.entries = a.list ? int(entries) : 0;
+  const long long tallest = P >= 0 ? a.slice * g : rows;
+  a.pitch = int(tallest < da::kAttendRows ? tallest : da::kAttendRows);
+  a.max_items = a.list ? a.units + 2 * sms : a.units;
+  a.table_bytes = (size_t(a.entries) * 8 + 255) & ~size_t(255);
+  a.part_rows = size_t(a.max_items) * a.pitch;
+  *plan = a;
+  return DA_OK;
+}
+
+size_t attend_workspace(int B, int T, int h_q, int h_kv, int d, int n_max, int dtype, int P,
+                        int* status) {
+  int dev, sms;
+  AttendPlan plan{};
+  // sizes first, so that a wrong call is told without a GPU
+  int st = plan_attend(B, T, h_q, h_kv, d, n_max, dtype, P, 1, &plan);
+  if (st == DA_OK) st = current_device(&dev, &sms);
+  if (st == DA_OK) st = plan_attend(B, T, h_q, h_kv, d, n_max, dtype, P, sms, &plan);
+  if (status) *status = st;
+  return st == DA_OK ? plan.bytes(d) : 0;
+}
+
+struct AttendCall {
+  const void *q, *K, *V, *K_prefix, *V_prefix;
+  void* out;
+  const long long *q_strides, *out_strides;
+  const int32_t *seq_lens, *n_new;
+  int B, T, h_q, h_kv, d, n_max, window, prefix, P, prefix_max, dtype;
+  float scale;
+};
+
+int run_attend(const AttendCall& c, void* workspace, size_t workspace_bytes, int32_t* dev_error,
+               cudaStream_t stream) {
+  const bool shared = c.P >= 0;
+  if (!c.K || !c.V || !c.seq_lens || !c.q_strides || !c.out_strides) return DA_ERR_NULL;
+  if (shared && (!c.K_prefix || !c.V_prefix)) return DA_ERR_NULL;
+  AttendPlan plan{};
+  int st = plan_attend(c.B, c.T, c.h_q, c.h_kv, c.d, c.n_max, c.dtype, c.P, 1, &plan);
+  if (st != DA_OK) return st;
+  if (c.window < 0 || c.prefix < 0) return DA_ERR_SHAPE;
+  const double scale_log2 = fabs(double(c.scale)) * 1.4426950408889634;
+  if (!isfinite(c.scale) || scale_log2 > 3e38) return DA_ERR_SHAPE;
+  if (shared && (c.prefix_max < 1 || c.P > c.prefix_max || c.prefix_max > (1 << 30) ||
+                 (long long)c.h_kv * c.prefix_max > 0x7fffffffLL))
+    return DA_ERR_SHAPE;
+  if (c.T == 0) return DA_OK;
+  if (!c.q || !c.out) return DA_ERR_NULL;
+  if (!aligned16(c.q) || !aligned16(c.K) || !aligned16(c.V) || !aligned16(c.out) ||
+      !aligned16(c.K_prefix) || !aligned16(c.V_prefix) || !aligned4(c.seq_lens) ||
+      !aligned4(c.n_new))
+    return DA_ERR_ALIGN;
+  da::AttendParams p{};
+  p.out_bf16 = (c.dtype & DA_OUT_BF16) != 0;
+  const long long shape[3] = {c.B, c.h_q, c.T};
+  p.q_elems = p.out_elems = c.d;
+  for (int i = 0; i < 3; ++i) {
+    if ((st = check_stride(c.q_strides[i], 2)) != DA_OK) return st;
+    if ((st = check_stride(c.out_strides[i], p.out_bf16 ? 2 : 4)) != DA_OK) return st;
+    p.q_stride[i] = c.q_strides[i];
+    p.out_stride[i] = c.out_strides[i];
+    p.q_elems += (shape[i] - 1) * c.q_strides[i];
+    p.out_elems += (shape[i] - 1) * c.out_strides[i];
+  }
+  int dev, sms;
+  if ((st = current_device(&dev, &sms)) != DA_OK) return st;
+  plan_attend(c.B, c.T, c.h_q, c.h_kv, c.d, c.n_max, c.dtype, c.P, sms, &plan);
+  if (plan.list && (!workspace || workspace_bytes < plan.bytes(c.d))) return DA_ERR_WORKSPACE;
+  if (plan.list && !aligned16(workspace)) return DA_ERR_ALIGN;
+  da::AttendMaps maps;
+  const KernelShape ks{128, 128, 64, 1, 1.f};
+  if ((st = encode_cache_map(&maps.k, c.K, DA_BF16, c.d, c.n_max, c.B * c.h_kv, ks)) != DA_OK ||
+      (st = encode_cache_map(&maps.v, c.V, DA_BF16, c.d, c.n_max, c.B * c.h_kv, ks)) != DA_OK)
+    return st;
+  maps.k_prefix = maps.k, maps.v_prefix = maps.v;
+  if (shared &&
+      ((st = encode_cache_map(&maps.k_prefix, c.K_prefix, DA_BF16, c.d, c.prefix_max, c.h_kv, ks)) !=
+           DA_OK ||
+       (st = encode_cache_map(&maps.v_prefix, c.V_prefix, DA_BF16, c.d, c.prefix_max, c.h_kv, ks)) !=
+           DA_OK))
+    return st;
+  p.dev_error = dev_error;
+  p.T = c.T, p.h_q = c.h_q, p.h_kv = c.h_kv, p.group = c.h_q / c.h_kv, p.n_max = c.n_max;
+  // (positions plus a window stay inside 32 bits)
+  p.window = c.window < (1 << 30) ? c.window : 1 << 30;
+  p.prefix = c.prefix < (1 << 30) ? c.prefix : 1 << 30;
+  if (p.window == 0) p.prefix = 0;  // every row up to the query's is seen
+  p.shared = shared, p.P = shared ? c.P : 0;
+  p.q_flip = c.scale < 0.f ? 1 : c.scale == 0.f ? 2 : 0;
+  p.scale_log2 = c.scale == 0.f ? 1.f : float(scale_log2);
+  p.lazy = float(8.0 / double(p.scale_log2));
+  p.single_read = plan.q_tiles == 1;
+  p.list = plan.list, p.q_tiles = plan.q_tiles, p.sms = sms;
+  p.max_items = int(plan.max_items), p.pitch = plan.pitch;
+  if (plan.list) {
+    char* ws = static_cast<char*>(workspace);
+    p.table = reinterpret_cast<int2*>(ws);
+    p.o_part = reinterpret_cast<float*>(ws + plan.table_bytes);
+    p.lse_part = p.o_part + plan.part_rows * c.d;
+  }
+#ifdef DA_TEST_HOOKS
+  p.withhold_cta = g_test_withhold_cta.load();
+#endif
+  for (int b0 = 0; b0 < c.B; b0 += plan.slice) {
+    p.B = c.B - b0 < plan.slice ? c.B - b0 : plan.slice;
+    p.b_offset = b0;
+    p.q = static_cast<const char*>(c.q) + b0 * c.q_strides[0] * 2;
+    p.out = static_cast<char*>(c.out) + b0 * c.out_strides[0] * (p.out_bf16 ? 2 : 4);
+    p.seq_lens = c.seq_lens + b0;
+    p.n_new = c.n_new ? c.n_new + b0 : nullptr;
+    p.prefix_tiles = shared ? (p.B * p.group + da::kAttendRows - 1) / da::kAttendRows : 0;
+    p.entries = p.list ? p.B * p.q_tiles + p.shared : 0;
+    const long long units = ((long long)p.B * p.q_tiles + p.prefix_tiles) * p.h_kv;
+    const int grid = int(p.list ? units + 2 * sms : units);
+    cudaError_t e = da::launch_attend(p, maps, c.d, grid, stream);
+    if (e != cudaSuccess) return fail_cuda(e, "attend launch");
+    g_launches.fetch_add(1);
+    if (p.list) {
+      e = da::launch_attend_combine(p, c.d, stream);
+      if (e != cudaSuccess) return fail_cuda(e, "attend combine launch");
+      g_launches.fetch_add(1);
+    }
+  }
+  return DA_OK;
+}
+}  // namespace
+
+size_t chunk_attn_workspace_bytes(int B, int T, int h_q, int h_kv, int d, int n_max, int dtype,
+                                  int* status) {
+  return attend_workspace(B, T, h_q, h_kv, d, n_max, dtype, -1, status);
+}
+
+int chunk_attn(const void* q, const long long* q_strides, int T, const int32_t* n_new, const void* K,
+               const void* V, const int32_t* seq_lens, int window, int prefix, void* out,
+               const long long* out_strides, int B, int h_q, int h_kv, int d, int n_max, float scale,
+               int dtype, void* workspace, size_t workspace_bytes, int32_t* dev_error,
+               cudaStream_t stream) {
+  const AttendCall c{q,    K,    V,   nullptr, nullptr, out,    q_strides, out_strides, seq_lens, n_new,
+                     B,    T,    h_q, h_kv,    d,       n_max,  window,    prefix,      -1,       0,
+                     dtype, scale};
+  return run_attend(c, workspace, workspace_bytes, dev_error, stream);
+}
+
+size_t decode_attn_shared_workspace_bytes(int B, int h_q, int h_kv, int d, int n_max,
+                                          int prefix_len, int dtype, int* status) {
+  if (prefix_len < 0) {
+    if (status) *status = DA_ERR_SHAPE;
+    return 0;
+  }
+  return attend_workspace(B, 1, h_q, h_kv, d, n_max, dtype, prefix_len, status);
+}
+
+int decode_attn_shared(const void* q, const void* K_prefix, const void* V_prefix, int prefix_len,
+                       int prefix_max, const void* K, const void* V, const int32_t* seq_lens,
+                       void* out, int B, int h_q, int h_kv, int d, int n_max, float scale, int dtype,
+                       void* workspace, size_t workspace_bytes, int32_t* dev_error,
+                       cudaStream_t stream) {
+  if (prefix_len < 0) return DA_ERR_SHAPE;
+  const long long strides[3] = {(long long)h_q * d, d, 0};  // q and out [B, h_q, d]
+  const AttendCall c{q, K, V,   K_prefix, V_prefix, out,   strides, strides, seq_lens, nullptr,
+                     B, 1, h_q, h_kv,     d,        n_max, 0,       0,       prefix_len, prefix_max,
+                     dtype, scale};
+  return run_attend(c, workspace, workspace_bytes, dev_error, stream);
 }
 
 int kv_quantize(const void* x, int x_dtype, void* codes, float* scales, long long rows, int d,

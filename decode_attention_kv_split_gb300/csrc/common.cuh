@@ -372,6 +372,65 @@ cudaError_t launch_combine(const SplitParams& p, int d, int heads_per_cta, int s
 cudaError_t launch_lse_merge(const float* o_parts, const float* lse_parts, int S, void* out,
                              int out_bf16, float* lse_out, long long heads, int d,
                              cudaStream_t stream);
+// kv_append_rope: x[0..2] = q, k, v; weight[0..1] and cache[0..1] = of q and k, K and V.
+struct RopeAppendArgs {
+  const void* x[3];
+  long long x_stride[3][3];      // elements: b, head, token
+  void* q_out;
+  long long out_stride[3];
+  void* cache[2];
+  const int32_t* pos;            // [B]
+  const int32_t* n_new;          // nullable
+  const int32_t* angle_pos;      // nullable
+  const float* cos;              // [n_angles, rot / 2]
+  const float* sin;
+  const void* weight[2];         // nullable
+  int32_t* dev_error;
+  int B, T, h_q, h_kv, d_k, d_v, n_max, rot, n_angles, interleaved, bf16, sms;
+  float eps, inv_d;
+  long long x_elems[3], out_elems;  // extents, for the checked build
+};
+cudaError_t launch_kv_append_rope(const RopeAppendArgs& a, cudaStream_t stream);
+
+// Attention of many query rows over one KV head's rows (attend.cu): the chunk
+// and the shared-prefix entry points.
+struct AttendParams {
+  const void* q;                 // bf16, element (b, h, t, :) at b * q_stride[0] + h * [1] + t * [2]
+  long long q_stride[3];
+  void* out;                     // float32 or bf16, strides alike
+  long long out_stride[3];
+  const int32_t* seq_lens;       // [B] rows of each sequence, the new tokens' among them
+  const int32_t* n_new;          // nullable: new tokens of each sequence (else T)
+  int32_t* dev_error;            // nullable
+  int B, T, h_q, h_kv, group, n_max;
+  int b_offset;                  // first sequence of this launch inside the tensor maps
+  int window, prefix;            // 0: unlimited; rows always seen
+  int shared, P;                 // shared prefix: on, its rows
+  int out_bf16;
+  int q_flip;                    // 1: q times -1 (negative scale), 2: q times 0 (scale 0)
+  float scale_log2;              // |scale| * log2 e, 1 for scale 0
+  float lazy;                    // 8 / scale_log2: a maximum may lag by 2^8
+  int single_read;               // each K and V row is read by one CTA: no use in keeping it in L2
+  // Units: (row tile of 256 query rows, KV head, sequence). list != 0: units are cut into items of
+  // about equal length, merged by the combine; else one item per unit.
+  int list, entries, q_tiles, prefix_tiles, sms, max_items, pitch;
+  float* o_part;                 // [max_items][pitch][d]
+  float* lse_part;               // [max_items][pitch], log2 domain
+  int2* table;                   // [entries] first item and items per unit
+  long long q_elems, out_elems;  // extents, for the checked build
+#ifdef DA_TEST_HOOKS
+  int withhold_cta;
+#endif
+};
+struct AttendMaps {
+  CUtensorMap k, v, k_prefix, v_prefix;
+};
+constexpr int kAttendEntries = 1024;  // entries of a list (shared memory of the schedule)
+constexpr int kAttendRows = 256;      // query rows of a unit
+cudaError_t launch_attend(const AttendParams& p, const AttendMaps& m, int d, int grid,
+                          cudaStream_t stream);
+cudaError_t launch_attend_combine(const AttendParams& p, int d, cudaStream_t stream);
+
 cudaError_t launch_kv_append(const void* k_new, const void* v_new, void* K, void* V,
                              const int32_t* pos, int B, int h_kv, int row_bytes_k,
                              int row_bytes_v, int n_max, const float* ks_new, const float* vs_new,

@@ -486,6 +486,98 @@ DA_API int kv_read_q8b(const void* K, const void* V, const float* k_scale, const
                        void* v_out, int out_dtype, int T, int B, int h_kv, int d, int n_max,
                        int dtype, int32_t* dev_error, cudaStream_t stream);
 
+/*
+ * From projections to the cache: the norm of each head of q and k, the rotation
+ * by position and the write into the cache, for a prompt, a chunk of one or a
+ * single token.  Token i of sequence b, i < m (m = n_new[b], or T where n_new is
+ * NULL), becomes row pos[b] + i.  For every head vector x of q and k, in float and
+ * rounded once:
+ *   y = x / sqrt(mean(x^2) + eps) * weight     (weight NULL: y = x)
+ *   (y_a, y_b) = (y_a c - y_b s, y_b c + y_a s) for the rot / 2 pairs (a, b) of its
+ *   first rot elements: (j, j + rot / 2), or (2j, 2j + 1) when interleaved;
+ *   c, s = cos, sin[(angle_pos ? angle_pos[b] : pos[b]) + i][j]
+ * q goes to q_out, k to K; v is copied to V bit for bit.
+ *   q [B, h_q, T, d_k], k_new [B, h_kv, T, d_k], v_new [B, h_kv, T, d_v],
+ *   q_out [B, h_q, T, d_k] : device, dtype (DA_FP32 or DA_BF16), element
+ *                  (b, h, i, j) at b * strides[0] + h * strides[1] +
+ *                  i * strides[2] + j (strides in elements, host arrays,
+ *                  multiples of 16 bytes, >= 0); 16-byte aligned.  Tokens at or
+ *                  past m are neither read nor written.  q_out may be q itself
+ *                  with the same strides; else no output may overlap an input.
+ *   K [B, h_kv, n_max, d_k], V [B, h_kv, n_max, d_v] : the caches, dtype
+ *   cos, sin     : device float32 [n_angles, rot / 2], 16-byte aligned
+ *   rot          : a multiple of 16, at most d_k
+ *   angle_pos    : nullable device int32 [B] (rows behind a shared prefix stand
+ *                  further on than their place in the cache)
+ *   q_weight, k_weight : nullable device [d_k], dtype, 16-byte aligned
+ *   A token whose cache row or angle row does not exist is not written anywhere;
+ *   an n_new outside [0, T] is clamped; each sets DA_DEVERR_POS.
+ *   d_k == d_v in {64, 128, 256}, or d_k = 192 and d_v = 128.
+ * Does not change lengths: the caller advances them.  T = 0 does nothing.
+ */
+DA_API int kv_append_rope(const void* q, const void* k_new, const void* v_new,
+                          const long long* q_strides, const long long* k_strides,
+                          const long long* v_strides, int T, const int32_t* n_new, void* q_out,
+                          const long long* out_strides, void* K, void* V, const int32_t* pos,
+                          const float* cos, const float* sin, int n_angles, int rot,
+                          int interleaved, const int32_t* angle_pos, const void* q_weight,
+                          const void* k_weight, float eps, int B, int h_q, int h_kv, int d_k,
+                          int d_v, int n_max, int dtype, int32_t* dev_error, cudaStream_t stream);
+
+/*
+ * Attention of a chunk: the last m rows of sequence b (m = n_new[b], or T where
+ * n_new is NULL) are its new tokens, already in the cache; token i stands at row
+ * p = seq_lens[b] - m + i and sees row l when
+ *   l <= p, and l > p - window or l < prefix        (window 0: every l <= p)
+ * with Steps I-III of decode_attn_ex over the rows it sees.  One token a sequence
+ * is a decode step; a chunk of a prompt or drafted tokens to be checked are more.
+ *   q, out    : device [B, h_q, T, d]; strides as in kv_append_rope.  q is bf16, out
+ *               float32, or bf16 when dtype (DA_BF16) carries DA_OUT_BF16.  Outputs
+ *               of tokens at or past m are left as they were.  out may not overlap
+ *               an input, nor itself.
+ *   K, V      : device bf16 [B, h_kv, n_max, d];  d = 64 or 128
+ *   seq_lens  : device int32 [B], the rows with the new tokens; outside [0, n_max]:
+ *               clamped.  An n_new outside [0, T] is clamped; of more new tokens
+ *               than rows the first see nothing and get 0.  Each sets
+ *               DA_DEVERR_SEQ_LEN.
+ *   Rows that no token of a sequence sees may hold anything, NaN too.  V rows that
+ *   some token sees must be finite: the tokens of a tile share its products, and an
+ *   infinity or NaN in one reaches also those that do not see it.
+ *   Weights are multiplied as bf16 for a bf16 out (each rounded by at most 2^-8 of
+ *   itself), as bf16 and its bf16 remainder for a float32 out (2^-16).
+ *   workspace : chunk_attn_workspace_bytes(...) bytes, 16-byte aligned (may be NULL
+ *               when that is 0); as decode_attn_ex's.
+ * One launch, and a second one where units of the work may be cut along the rows.
+ */
+DA_API size_t chunk_attn_workspace_bytes(int B, int T, int h_q, int h_kv, int d, int n_max,
+                                         int dtype, int* status);
+DA_API int chunk_attn(const void* q, const long long* q_strides, int T, const int32_t* n_new,
+                      const void* K, const void* V, const int32_t* seq_lens, int window, int prefix,
+                      void* out, const long long* out_strides, int B, int h_q, int h_kv, int d,
+                      int n_max, float scale, int dtype, void* workspace, size_t workspace_bytes,
+                      int32_t* dev_error, cudaStream_t stream);
+
+/*
+ * Decode attention of a batch that shares a prefix: every query sees the prefix_len
+ * rows of the prefix, then the seq_lens[b] rows of its own cache, in one softmax.
+ * The prefix is read once a KV head for the whole batch, not once a sequence.
+ *   q, out             : device [B, h_q, d] as decode_attn_ex, q bf16
+ *   K_prefix, V_prefix : device bf16 [h_kv, prefix_max, d], 0 <= prefix_len <= prefix_max
+ *   K, V               : device bf16 [B, h_kv, n_max, d];  d = 64 or 128
+ *   seq_lens           : device int32 [B]; may be 0 (the prefix alone; without rows
+ *                        anywhere out = 0).  Outside [0, n_max]: clamped,
+ *                        DA_DEVERR_SEQ_LEN.
+ *   V rows below the lengths must be finite; weights are rounded as in chunk_attn.
+ * Two launches (for each of several hundred sequences).
+ */
+DA_API size_t decode_attn_shared_workspace_bytes(int B, int h_q, int h_kv, int d, int n_max,
+                                                 int prefix_len, int dtype, int* status);
+DA_API int decode_attn_shared(const void* q, const void* K_prefix, const void* V_prefix,
+                              int prefix_len, int prefix_max, const void* K, const void* V,
+                              const int32_t* seq_lens, void* out, int B, int h_q, int h_kv, int d,
+                              int n_max, float scale, int dtype, void* workspace,
+                              size_t workspace_bytes, int32_t* dev_error, cudaStream_t stream);
+
 /* Static, human-readable name of a da_status. */
 DA_API const char* decode_attn_status_string(int status);
 
