@@ -1298,6 +1298,9 @@ int run_attend(const AttendCall& c, void* workspace, size_t workspace_bytes, int
   p.single_read = plan.q_tiles == 1;
   p.list = plan.list, p.q_tiles = plan.q_tiles, p.sms = sms;
   p.max_items = int(plan.max_items), p.pitch = plan.pitch;
+  const long long own = (long long)c.T * p.group;
+  p.unit_rows = int(own < da::kAttendRows ? own : da::kAttendRows);
+  p.by_group = da::FastDiv(uint32_t(p.group));
   if (plan.list) {
     char* ws = static_cast<char*>(workspace);
     p.table = reinterpret_cast<int2*>(ws);
@@ -1310,6 +1313,7 @@ int run_attend(const AttendCall& c, void* workspace, size_t workspace_bytes, int
   for (int b0 = 0; b0 < c.B; b0 += plan.slice) {
     p.B = c.B - b0 < plan.slice ? c.B - b0 : plan.slice;
     p.b_offset = b0;
+    p.by_batch = da::FastDiv(uint32_t(p.B));
     p.q = static_cast<const char*>(c.q) + b0 * c.q_strides[0] * 2;
     p.out = static_cast<char*>(c.out) + b0 * c.out_strides[0] * (p.out_bf16 ? 2 : 4);
     p.seq_lens = c.seq_lens + b0;

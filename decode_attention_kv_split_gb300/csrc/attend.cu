@@ -23,8 +23,8 @@
 // streams for the same rows on alternate tiles and merges them at the end.
 //
 // Roles (384 threads): warps 0-3 and 4-7 the softmax of streams 0 and 1, warp 8
-// the TMA producer, warp 9 the MMA issuer (10 and 11 fill their warpgroup, which
-// gives registers to the others).  TMEM: S 2 x 128 columns, O 2 x d.
+// the TMA producer, warp 9 the MMA issuer, warp 10 clears V rows that may hold
+// anything.  TMEM: S 2 x 128 columns, O 2 x d.
 #include <math.h>
 
 #include "common.cuh"
@@ -36,6 +36,7 @@ namespace {
 constexpr int kTile = 128;              // K and V rows of a tile, query rows of a stream
 constexpr int kAttendThreads = 384;
 constexpr int kScheduleThreads = 256;
+constexpr int kEdges = 4;               // most tiles of an item with rows to clear (see edge_tile)
 
 template <int D_>
 struct AttendCfg {
@@ -43,23 +44,27 @@ struct AttendCfg {
   static constexpr int kTileBytes = kTile * D * 2;  // Q of a stream, a K tile, a V tile
   static constexpr int kHalfBytes = kTile * 128;    // 64 columns of one
   static constexpr int kSlots = D == 128 ? 5 : 11;  // ring of K and V tiles
-  // q_full[2], kv_full[slots], kv_empty[slots], s_full[2], p_full[2], o_full[2], fin
-  static constexpr int kBars = 2 + 2 * kSlots + 2 + 2 + 2 + 1;
-  static constexpr size_t kSmemBytes = 1024 + size_t(2 + kSlots) * kTileBytes + kBars * 8 + 128;
+  // q_full[2], kv_full[slots], kv_empty[slots], s_full[2], p_full[2], o_full[2], edge[4], fin
+  static constexpr int kBars = 2 + 2 * kSlots + 2 + 2 + 2 + kEdges + 1;
+  static constexpr size_t kSmemBytes = 1024 + size_t(2 + kSlots) * kTileBytes + kBars * 8 + 256;
   static_assert(kSmemBytes <= 227 * 1024, "shared memory");
   // the schedule's scratch lies in the ring before the first load
   static_assert((kAttendEntries + 64) * 4 <= kTileBytes, "schedule scratch");
 };
 
-// The rows of a unit and the tiles of rows they see.  List tile k is tile k of
+// What one CTA does: some tiles of a unit.  List tile k of a unit is tile k of
 // the cache below `pt` (always-seen rows before the window) and tile
 // first + k - pt from there on.
-struct Unit {
-  int rows;       // query rows, 0: no unit
-  int row0;       // first of them among the sequence's (or the batch's) rows
-  int p0;         // position of the query row 0's token: its last visible row
-  int lo, hi;     // first windowed row and last row that some query sees
-  int pt, first, tiles;
+struct Item {
+  int kvh, b;        // b < 0: the prefix
+  int rows, row0;    // query rows, and the first among the sequence's (or the batch's)
+  int n;             // rows of the sequence (or the prefix)
+  int past;          // position of a sequence's token 0: token t sees rows up to past + t
+  int pt, first, tiles;  // of the unit
+  int begin, count;  // this item's list tiles
+  int upto[2];       // tiles of it that each stream takes (from the first on)
+  int clear_lo;      // rows of [prefix, clear_lo) and from n on are seen by no query of the sequence
+  int slot;          // partial, or -1: the unit's only item writes the output
 };
 
 __device__ __forceinline__ int seq_rows(const AttendParams& p, int b, bool& bad) {
@@ -73,139 +78,157 @@ __device__ __forceinline__ int seq_new(const AttendParams& p, int b, bool& bad) 
   return min(max(m, 0), p.T);
 }
 
-// Unit of row tile qt of a sequence of n rows, the last m of them new.
-__device__ __forceinline__ Unit seq_unit(const AttendParams& p, int n, int m, int qt) {
-  Unit u;
-  const long long rows = (long long)m * p.group - (long long)qt * kAttendRows;
-  u.rows = rows <= 0 ? 0 : int(rows < kAttendRows ? rows : kAttendRows);
-  u.row0 = qt * kAttendRows;
-  u.p0 = n - m + u.row0 / p.group;
-  u.hi = n - m + (u.row0 + u.rows - 1) / p.group;
-  u.lo = p.window ? max(0, u.p0 + 1 - p.window) : 0;
-  u.first = u.lo / kTile;
-  u.pt = p.window ? min(min((p.prefix + kTile - 1) / kTile, u.hi / kTile + 1), u.first) : 0;
-  u.tiles = u.rows == 0 || u.hi < 0 ? 0 : u.pt + u.hi / kTile - u.first + 1;
-  return u;
+// First cached row of list tile k.
+__device__ __forceinline__ int tile_row(const Item& w, int k) {
+  return (k < w.pt ? k : w.first + k - w.pt) * kTile;
 }
 
-__device__ __forceinline__ Unit prefix_unit(const AttendParams& p, int mt) {
-  Unit u;
-  const int rows = p.B * p.group - mt * kAttendRows;
-  u.rows = min(rows, kAttendRows);
-  u.row0 = mt * kAttendRows;
-  u.p0 = u.hi = p.P - 1;
-  u.lo = u.first = u.pt = 0;
-  u.tiles = (p.P + kTile - 1) / kTile;
-  return u;
+// Whether the V tile at row r0 holds rows that no query of the sequence sees: they
+// may hold anything, even NaN, and a weight of zero times NaN is NaN, so they are
+// cleared.  In the tiles of an item that is the end of the always-seen rows, the
+// window's first tile and the last tile.
+__device__ __forceinline__ bool edge_tile(const AttendParams& p, const Item& w, int r0) {
+  return r0 + kTile > w.n || (r0 < w.clear_lo && r0 + kTile > p.prefix);
+}
+
+// Unit of row tile qt of a sequence of n rows, the last m of them new.
+__device__ __forceinline__ void seq_unit(const AttendParams& p, int n, int m, int qt, Item& w) {
+  const long long rows = (long long)m * p.group - (long long)qt * kAttendRows;
+  w.rows = rows <= 0 ? 0 : int(rows < kAttendRows ? rows : kAttendRows);
+  w.row0 = qt * kAttendRows;
+  w.n = n;
+  w.past = n - m;
+  w.pt = w.first = w.tiles = 0;
+  if (w.rows == 0) return;
+  const int hi = w.past + p.by_group.div(w.row0 + w.rows - 1);
+  if (hi < 0) return;
+  if (p.window) {
+    w.first = max(0, w.past + p.by_group.div(w.row0) + 1 - p.window) / kTile;
+    w.pt = min(min((p.prefix + kTile - 1) / kTile, hi / kTile + 1), w.first);
+  }
+  w.tiles = w.pt + hi / kTile - w.first + 1;
+}
+
+// The rest of an item, tiles [begin, end) of its unit.
+__device__ __forceinline__ void cut_item(const AttendParams& p, int begin, int end, int slot,
+                                         Item& w) {
+  w.begin = begin;
+  w.count = end - begin;
+  w.slot = slot;
+  w.clear_lo = w.b >= 0 && p.window ? max(0, w.past + 1 - p.window) : 0;
+  w.upto[0] = w.upto[1] = w.count;
+  if (w.b >= 0 && w.rows > kTile) {  // stream 0 ends at its last query's row
+    const int hi = w.past + p.by_group.div(w.row0 + kTile - 1);
+    const int tiles = hi < 0 ? 0 : w.pt + hi / kTile - w.first + 1;
+    w.upto[0] = min(max(tiles - begin, 0), w.count);
+  }
 }
 
 // Entry e of the list: the prefix (with a shared one), then row tile by row tile
 // from the last (in a chunk the longest) down, every sequence of it.
 __device__ __forceinline__ void entry_of(const AttendParams& p, int e, int& b, int& qt) {
   e -= p.shared;
-  qt = p.q_tiles - 1 - e / p.B;
-  b = e % p.B;
+  const int up = p.by_batch.div(e);
+  qt = p.q_tiles - 1 - up;
+  b = e - up * p.B;
 }
 
-__device__ __forceinline__ int entry_tiles(const AttendParams& p, int e, bool& present) {
+// The unit of an entry; false: it has no part.
+__device__ __forceinline__ bool entry_unit(const AttendParams& p, int e, Item& w) {
   if (p.shared && e == 0) {
-    present = p.P > 0;
-    return (p.P + kTile - 1) / kTile;
+    w.b = -1;
+    w.n = p.P;
+    w.tiles = (p.P + kTile - 1) / kTile;
+    return p.P > 0;
   }
-  int b, qt;
-  entry_of(p, e, b, qt);
+  int qt;
+  entry_of(p, e, w.b, qt);
   bool bad;
-  const Unit u = seq_unit(p, seq_rows(p, b, bad), seq_new(p, b, bad), qt);
+  const int n = seq_rows(p, w.b, bad);
+  seq_unit(p, n, seq_new(p, w.b, bad), qt, w);
   // (behind a prefix a sequence without rows has no part)
-  present = u.rows > 0 && (u.tiles > 0 || !p.shared);
-  return u.tiles;
+  return w.rows > 0 && (w.tiles > 0 || !p.shared);
 }
 
 __device__ __forceinline__ int entry_units(const AttendParams& p, int e) {
   return p.h_kv * (p.shared && e == 0 ? p.prefix_tiles : 1);
 }
 
-// What one CTA does.
-struct Work {
-  int kvh, b;       // b < 0: the prefix
-  int begin, end;   // list tiles
-  int slot;         // partial, or -1: the unit's only item writes the output
-  int n;            // rows of the sequence (or the prefix)
-  Unit u;
-};
-
 // The list: every unit is cut into ceil(tiles / c) items of equal length, with one c
 // for the whole launch, the one that ends first by a simple model (rounds of the
 // grid times the tiles of an item and a constant for its start and end).  All
 // CTAs compute the same list from the lengths; CTA 0 leaves the table for the
-// combine.  Returns false for a CTA without an item.
-constexpr int kLengthChoices = 32;
-constexpr float kItemTiles = 3.f;  // an item's fixed cost in tiles
+// combine.  Returns false for a CTA without an item.  Ends with a barrier.
+constexpr int kScheduleWarps = kScheduleThreads / 32;
+constexpr int kLengthChoices = 2 * kScheduleWarps;
+constexpr float kItemTiles = 5.f;  // an item's fixed cost in tiles
 
-__device__ __forceinline__ bool list_item(const AttendParams& p, int* scratch, Work& w) {
+__device__ __forceinline__ bool list_item(const AttendParams& p, int* scratch, Item* out) {
   int* tiles = scratch;                       // [kAttendEntries], -1: absent
-  int* sums = scratch + kAttendEntries;       // [32]
-  int* found = sums + 32;                     // [4]
+  int* sums = scratch + kAttendEntries;       // [64]
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const bool mine = tid < kScheduleThreads;
-  long long total = 0;
+  float total = 0.f;
+  int tallest = 0;
   if (mine)
     for (int e = tid; e < p.entries; e += kScheduleThreads) {
-      bool present;
-      const int t = entry_tiles(p, e, present);
-      tiles[e] = present ? t : -1;
-      total += (long long)t * entry_units(p, e);
+      Item w;
+      const bool present = entry_unit(p, e, w);
+      tiles[e] = present ? w.tiles : -1;
+      if (present) {
+        total += float(w.tiles) * float(entry_units(p, e));
+        tallest = max(tallest, w.tiles);
+      }
     }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-  long long* totals = reinterpret_cast<long long*>(sums);
-  if (lane == 0 && mine) totals[warp] = total;
-  if (tid == 0) found[0] = -1;
+  for (int o = 16; o > 0; o >>= 1) {
+    total += __shfl_xor_sync(0xffffffffu, total, o);
+    tallest = max(tallest, __shfl_xor_sync(0xffffffffu, tallest, o));
+  }
+  if (lane == 0 && mine) {
+    sums[warp] = __float_as_int(total);
+    sums[kScheduleWarps + warp] = tallest;
+  }
+  if (tid == 0) out->count = -1;
   __syncthreads();
-  total = 0;
+  total = 0.f;
 #pragma unroll
-  for (int i = 0; i < kScheduleThreads / 32; ++i) total += totals[i];
-  // one length after the other by a warp: items and the longest of them
-  float best = 1e30f;
-  int best_c = 1;
-  const float share = float(total) / float(p.sms);
-  __syncthreads();
+  for (int i = 0; i < kScheduleWarps; ++i) {
+    total += __int_as_float(sums[i]);
+    tallest = max(tallest, sums[kScheduleWarps + i]);
+  }
+  // two lengths a warp: the items there would be
   if (mine) {
-    for (int k = warp; k < kLengthChoices; k += kScheduleThreads / 32) {
-      // half an even share up to 4 of them, in steps of 2^(1/8)
-      const int c = max(2, int(ceilf(share * exp2f(float(k - 8) * 0.125f))));
-      int items = 0, longest = 0;
+    const float share = total / float(p.sms);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      // from half an even share to 2.4 of them, in steps of 2^(3/20)
+      const int c = max(2, int(ceilf(share * exp2f(float(warp + k * kScheduleWarps) * 0.15f - 1.f))));
+      const float inv = 1.f / float(c);
+      int items = 0;
       for (int e = lane; e < p.entries; e += 32) {
         const int t = tiles[e];
-        if (t < 0) continue;
-        const int cut = max(1, (t + c - 1) / c);
-        items += cut * entry_units(p, e);
-        longest = max(longest, (t + cut - 1) / cut);
+        if (t >= 0) items += max(1, int(ceilf(float(t) * inv))) * entry_units(p, e);
       }
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        items += __shfl_xor_sync(0xffffffffu, items, o);
-        longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, o));
+      for (int o = 16; o > 0; o >>= 1) items += __shfl_xor_sync(0xffffffffu, items, o);
+      const float longest = float(min(c, tallest)) + kItemTiles;
+      const float mean = (total + kItemTiles * float(items)) / float(p.sms);
+      const float t = fmaxf(fminf(ceilf(float(items) / float(p.sms)) * longest, mean + longest), mean);
+      if (lane == 0) {
+        sums[2 * kScheduleWarps + warp + k * kScheduleWarps] = __float_as_int(t);
+        sums[2 * kScheduleWarps + kLengthChoices + warp + k * kScheduleWarps] = c;
       }
-      const float rounds = float((items + p.sms - 1) / p.sms);
-      const float mean = (float(total) + kItemTiles * float(items)) / float(p.sms);
-      const float t = fmaxf(fminf(rounds * (float(longest) + kItemTiles),
-                                  mean + float(longest) + kItemTiles), mean);
-      if (t < best) best = t, best_c = c;
-    }
-    if (lane == 0) {
-      sums[warp] = __float_as_int(best);
-      sums[8 + warp] = best_c;
     }
   }
   __syncthreads();
-  best = __int_as_float(sums[0]);
-  int c = sums[8];
+  float best = 1e30f;
+  int c = 2;
 #pragma unroll
-  for (int i = 1; i < kScheduleThreads / 32; ++i)
-    if (__int_as_float(sums[i]) < best || (__int_as_float(sums[i]) == best && sums[8 + i] > c))
-      best = __int_as_float(sums[i]), c = sums[8 + i];
-  __syncthreads();
+  for (int i = 0; i < kLengthChoices; ++i) {
+    const float t = __int_as_float(sums[2 * kScheduleWarps + i]);
+    if (t <= best) best = t, c = sums[2 * kScheduleWarps + kLengthChoices + i];
+  }
   // first item of every entry: four consecutive entries a thread
   constexpr int kPer = kAttendEntries / kScheduleThreads;
   int cut[kPer], own = 0;
@@ -234,48 +257,49 @@ __device__ __forceinline__ bool list_item(const AttendParams& p, int* scratch, W
       if (e >= p.entries) break;
       const int items = cut[i] * entry_units(p, e);
       const int x = int(blockIdx.x) - at;
-      if (x >= 0 && x < items) found[0] = e, found[1] = x, found[2] = cut[i];
       if (blockIdx.x == 0) p.table[e] = make_int2(at, cut[i]);
+      if (x >= 0 && x < items && int(blockIdx.x) < p.max_items) {  // this CTA's
+        Item w;
+        entry_unit(p, e, w);
+        const int unit = x / cut[i], s = x - unit * cut[i];
+        if (w.b < 0) {
+          w.kvh = unit / p.prefix_tiles;
+          w.row0 = (unit - w.kvh * p.prefix_tiles) * kAttendRows;
+          w.rows = min(p.B * p.group - w.row0, kAttendRows);
+          w.past = w.n - 1;
+          w.pt = w.first = 0;
+        } else {
+          w.kvh = unit;
+        }
+        cut_item(p, int((long long)w.tiles * s / cut[i]), int((long long)w.tiles * (s + 1) / cut[i]),
+                 cut[i] == 1 && !p.shared ? -1 : int(blockIdx.x), w);
+        *out = w;
+      }
       at += items;
     }
   }
+  fence_proxy_async_smem();  // the scratch is the ring's: before its first loads
   __syncthreads();
-  const int e = found[0], x = found[1], cuts = found[2];
-  if (e < 0 || int(blockIdx.x) >= p.max_items) return false;
-  bool bad;
-  if (p.shared && e == 0) {
-    const int unit = x / cuts;
-    w.b = -1;
-    w.kvh = unit / p.prefix_tiles;
-    w.n = p.P;
-    w.u = prefix_unit(p, unit % p.prefix_tiles);
-  } else {
-    int qt;
-    entry_of(p, e, w.b, qt);
-    w.kvh = x / cuts;
-    w.n = seq_rows(p, w.b, bad);
-    w.u = seq_unit(p, w.n, seq_new(p, w.b, bad), qt);
-  }
-  const int s = x % cuts;
-  w.begin = int((long long)w.u.tiles * s / cuts);
-  w.end = int((long long)w.u.tiles * (s + 1) / cuts);
-  w.slot = cuts == 1 && !p.shared ? -1 : int(blockIdx.x);
-  return true;
+  return out->count >= 0;
 }
 
-__device__ __forceinline__ bool direct_item(const AttendParams& p, Work& w) {
-  // the last row tiles, the longest of a chunk, first
-  const int per = p.B * p.h_kv;
-  const int qt = p.q_tiles - 1 - int(blockIdx.x) / per, rest = int(blockIdx.x) % per;
-  w.b = rest / p.h_kv;
-  w.kvh = rest % p.h_kv;
-  bool bad;
-  w.n = seq_rows(p, w.b, bad);
-  w.u = seq_unit(p, w.n, seq_new(p, w.b, bad), qt);
-  w.begin = 0;
-  w.end = w.u.tiles;
-  w.slot = -1;
-  return w.u.rows > 0;
+// Without a list: one item per unit, the last row tiles, the longest of a chunk, first.
+__device__ __forceinline__ bool unit_item(const AttendParams& p, Item* out) {
+  if (threadIdx.x == 0) {
+    const int per = p.B * p.h_kv;
+    const int up = int(blockIdx.x) / per, rest = int(blockIdx.x) - up * per;
+    Item w;
+    w.b = rest / p.h_kv;
+    w.kvh = rest - w.b * p.h_kv;
+    bool bad;
+    const int n = seq_rows(p, w.b, bad);
+    seq_unit(p, n, seq_new(p, w.b, bad), p.q_tiles - 1 - up, w);
+    cut_item(p, 0, w.tiles, -1, w);
+    if (w.rows == 0) w.count = -1;
+    *out = w;
+  }
+  __syncthreads();
+  return out->count >= 0;
 }
 
 // 32 consecutive 32-bit TMEM columns of this thread's lane.
@@ -317,49 +341,39 @@ __device__ __forceinline__ uint64_t l2_policy_evict_normal() {
   return p;
 }
 
-// The streams of a work item and what each sees.
-struct Streams {
-  bool alternate;      // one set of rows, tiles dealt to the streams in turn
-  int rows[2];
-  int lo[2], hi[2];    // first windowed row of the stream's first query, last row of its last
-  int lo_last[2], hi_first[2];  // the same of its last and its first query
-};
+__device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t n) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(n) : "memory");
+}
 
-__device__ __forceinline__ Streams streams_of(const AttendParams& p, const Work& w) {
-  Streams s;
-  s.alternate = w.u.rows <= kTile;
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int r0 = s.alternate ? 0 : i * kTile;
-    s.rows[i] = min(w.u.rows - r0, kTile);
-    if (w.b < 0) {
-      s.lo[i] = s.lo_last[i] = 0;
-      s.hi[i] = s.hi_first[i] = w.n - 1;
-    } else {
-      const int t0 = w.u.row0 / p.group;
-      const int p_first = w.u.p0 - t0 + (w.u.row0 + r0) / p.group;
-      const int p_last = w.u.p0 - t0 + (w.u.row0 + r0 + s.rows[i] - 1) / p.group;
-      s.hi_first[i] = p_first;
-      s.hi[i] = p_last;
-      s.lo[i] = p.window ? max(0, p_first + 1 - p.window) : 0;
-      s.lo_last[i] = p.window ? max(0, p_last + 1 - p.window) : 0;
-    }
+// Two floats at a time.
+__device__ __forceinline__ uint64_t pair_of(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void halves_of(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// A place of the ring: the producer and the MMA issuer pass through it in one order.
+template <int SLOTS>
+struct RingPlace {
+  int slot = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++slot == SLOTS) slot = 0, phase ^= 1u;
   }
-  return s;
-}
-
-// First cached row of list tile k.
-__device__ __forceinline__ int tile_row(const Unit& u, int k) {
-  return (k < u.pt ? k : u.first + k - u.pt) * kTile;
-}
-// Whether stream i takes list tile k.
-__device__ __forceinline__ bool takes(const AttendParams& p, const Work& w, const Streams& s, int i,
-                                      int k) {
-  if (k >= w.end) return false;
-  if (s.alternate) return ((k - w.begin) & 1) == i;
-  const int r = tile_row(w.u, k);
-  return r <= s.hi[i] && (r + kTile > s.lo[i] || r < p.prefix);
-}
+};
 
 template <class Cfg, bool WIDE_P>
 __global__ void __launch_bounds__(kAttendThreads, 1)
@@ -374,7 +388,8 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
   uint8_t* q_tile = smem;                            // [2]
   uint8_t* ring = smem + 2 * kTileBytes;             // [kSlots]
   uint64_t* bars = reinterpret_cast<uint64_t*>(ring + size_t(kSlots) * kTileBytes);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + Cfg::kBars);
+  Item* item = reinterpret_cast<Item*>(bars + Cfg::kBars);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(item + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const uint32_t q_full0 = smem_u32(bars);
@@ -383,12 +398,13 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
   const uint32_t s_full0 = empty0 + 8 * kSlots;
   const uint32_t p_full0 = s_full0 + 16;
   const uint32_t o_full0 = p_full0 + 16;
-  const uint32_t fin = o_full0 + 16;
+  const uint32_t edge0 = o_full0 + 16;
+  const uint32_t fin = edge0 + 8 * kEdges;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(q_full0 + 8 * i, 4);  // one arrival per softmax warp of the stream
+      mbar_init(q_full0 + 8 * i, 4);  // the softmax warps of the stream (see `arrivals`)
       mbar_init(s_full0 + 8 * i, 1);
       mbar_init(p_full0 + 8 * i, 4);
       mbar_init(o_full0 + 8 * i, 1);
@@ -397,6 +413,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
       mbar_init(full0 + 8 * i, 1);
       mbar_init(empty0 + 8 * i, 1);   // released by one tcgen05.commit
     }
+    for (int i = 0; i < kEdges; ++i) mbar_init(edge0 + 8 * i, 1);
     mbar_init(fin, 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -413,197 +430,214 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
       prefetch_tmap(&maps.v_prefix);
     }
   }
+  tc5::fence_before();
   allow_dependent_launch();
   wait_for_prerequisite_grid();
-  Work w;
-  const bool has = p.list ? list_item(p, reinterpret_cast<int*>(ring), w) : direct_item(p, w);
-  // lengths that were clamped are reported once each
+  const bool has = p.list ? list_item(p, reinterpret_cast<int*>(ring), item) : unit_item(p, item);
+  // lengths that were clamped are reported
   if (blockIdx.x == 0 && p.dev_error)
     for (int b = threadIdx.x; b < p.B; b += kAttendThreads) {
       bool bad_n, bad_m;
       const int n = seq_rows(p, b, bad_n), m = seq_new(p, b, bad_m);
       if (bad_n || bad_m || (m > n && !p.shared)) flag_error(p.dev_error, DA_DEVERR_SEQ_LEN);
     }
-  fence_proxy_async_smem();  // the schedule's scratch, before the ring's first loads
-  tc5::fence_before();
-  __syncthreads();
   tc5::fence_after();
   const uint32_t tmem = *tmem_slot;
   if (!has) {
     if (warp == 9) tc5::dealloc(tmem, kTmemCols);
     return;
   }
-  const Streams st = streams_of(p, w);
-  const int count = w.end - w.begin;             // tiles of this item
-  const int ahead = st.alternate ? 2 : 1;        // S tiles issued before the first P.V
-  // Loads follow their use: K of the first `ahead` tiles, then V_j and K_(j + ahead).
-  // Place of tile j's K and V in that order:
-  auto k_place = [&](int j) { return j + max(0, j - ahead + 1); };
-  auto v_place = [&](int j) { return j + min(count, ahead + j); };
+  const int count = item->count;
+  const bool alternate = item->rows <= kTile;    // one set of rows, tiles dealt to the streams in turn
+  const int ahead = alternate ? 2 : 1;           // tiles whose scores are issued before the first P.V
+  auto give_up = [&] {
+    if (!*abort_flag) {
+      *abort_flag = 1;
+      flag_error(p.dev_error, DA_DEVERR_TIMEOUT);
+    }
+  };
 
   // Registers: 168 a thread at launch for each of three warpgroups; 2 * 208 + 88 then.
   if (warp >= 8) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-  // ------------------------------------------------------------------ producer
-  if (warp == 8) {
-    if (lane == 0) {
-      const uint64_t policy = p.single_read || (w.b < 0 && p.prefix_tiles == 1)
-                                  ? l2_policy_evict_first()
-                                  : l2_policy_evict_normal();
-      const CUtensorMap* mk = w.b < 0 ? &maps.k_prefix : &maps.k;
-      const CUtensorMap* mv = w.b < 0 ? &maps.v_prefix : &maps.v;
-      const int z = w.b < 0 ? w.kvh : (p.b_offset + w.b) * p.h_kv + w.kvh;
-      const uint32_t ring0 = smem_u32(ring);
-      bool aborted = false;
-      int issued = 0;
-      auto load = [&](const CUtensorMap* map, int place, int j) {
-        const int slot = place % kSlots;
-        if (aborted) return;
-        if (place >= kSlots &&
-            !mbar_wait_bounded(empty0 + 8 * slot, ((place / kSlots) - 1) & 1, abort_flag)) {
-          *abort_flag = 1;
-          flag_error(p.dev_error, DA_DEVERR_TIMEOUT);
-          aborted = true;
-          return;
-        }
-#ifdef DA_TEST_HOOKS
-        if (int(blockIdx.x) == p.withhold_cta && map == mv && j == count - 1) return;
-#endif
-        const uint32_t bar = full0 + 8 * slot;
-        const uint32_t dst = ring0 + slot * kTileBytes;
-        const int y = tile_row(w.u, w.begin + j);
-        mbar_arrive_expect_tx(bar, kTileBytes);
-#pragma unroll
-        for (int c = 0; c < D; c += 64)
-          tma_load_3d(dst + (c / 64) * kHalfBytes, map, c, y, z, bar, policy);
-        issued = place + 1;
-      };
-      for (int j = 0; j < min(ahead, count); ++j) load(mk, k_place(j), j);
-      for (int j = 0; j < count; ++j) {
-        load(mv, v_place(j), j);
-        if (j + ahead < count) load(mk, k_place(j + ahead), j + ahead);
-      }
-      if (aborted) {  // copies in flight land before the CTA ends
-        volatile int never = 0;
-        for (int i = max(0, issued - kSlots); i < issued; ++i)
-          mbar_wait_bounded(full0 + 8 * (i % kSlots), (i / kSlots) & 1, &never);
-      }
-    }
-    return;
-  }
-
-  // ------------------------------------------------------------------ MMA issuer
-  if (warp == 9) {
-    bool ok = true;
-    auto wait = [&](uint32_t bar, uint32_t parity) {  // whole warp
-      if (lane == 0) ok = ok && mbar_wait_bounded(bar, parity, abort_flag);
-      const bool all = __shfl_sync(0xffffffffu, ok, 0);
-      if (!all && lane == 0 && !*abort_flag) {
-        *abort_flag = 1;
-        flag_error(p.dev_error, DA_DEVERR_TIMEOUT);
-      }
-      ok = all;
-      return all;
-    };
-    const uint32_t idesc_s = tc5::idesc_bf16(128, 128, 0, 0);
-    const uint32_t idesc_o = tc5::idesc_bf16(128, D, 0, 1);
-    bool any = false;
-    int seen_p[2] = {0, 0};   // tiles of each stream whose P.V was issued
-    auto scores = [&](int i, int j) {  // S_i = Q_i K_j^T
-      const int place = k_place(j);
-      if (!wait(full0 + 8 * (place % kSlots), (place / kSlots) & 1)) return;
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    // ---------------------------------------------------------------- producer
+    if (warp == 8) {
       if (lane == 0) {
-        tc5::fence_after();
-        const uint32_t ka = smem_u32(ring) + (place % kSlots) * kTileBytes;
-        const uint32_t qa = smem_u32(q_tile) + (st.alternate ? 0 : i * kTileBytes);
-#pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-          const uint32_t off = (ks >> 2) * kHalfBytes + (ks & 3) * 32;
-          tc5::mma(tmem + i * 128, tc5::sdesc(qa + off, 16, 1024), tc5::sdesc(ka + off, 16, 1024),
-                   idesc_s, ks > 0);
-        }
-        tc5::commit(s_full0 + 8 * i);
-      }
-      any = true;
-      __syncwarp();
-    };
-    if (count > 0) {
-      ok = wait(q_full0, 0);
-      if (ok && !st.alternate) ok = wait(q_full0 + 8, 0);
-    }
-    for (int j = 0; j < min(ahead, count) && ok; ++j) {
-      for (int i = 0; i < 2 && ok; ++i)
-        if (takes(p, w, st, i, w.begin + j)) scores(i, j);
-      if (ok && lane == 0) tc5::commit(empty0 + 8 * (k_place(j) % kSlots));
-    }
-    for (int j = 0; j < count && ok; ++j) {
-      const int place = v_place(j);
-      const uint32_t vslot = place % kSlots;
-      bool v_ready = false;
-      for (int i = 0; i < 2 && ok; ++i) {
-        if (takes(p, w, st, i, w.begin + j)) {
-          if (!v_ready) {
-            if (!wait(full0 + 8 * vslot, (place / kSlots) & 1)) break;
-            v_ready = true;
-            // rows that no query of the unit sees may hold anything, even NaN: cleared
-            const int r0 = tile_row(w.u, w.begin + j);
-            if (r0 + kTile - 1 > w.u.hi || (r0 < w.u.lo && r0 + kTile > p.prefix)) {
-              uint8_t* vt = ring + size_t(vslot) * kTileBytes;
-              for (int r = 0; r < kTile; ++r) {
-                const int row = r0 + r;
-                if ((row > w.u.hi || (row < w.u.lo && row >= p.prefix)) && lane < D / 8)
-                  *reinterpret_cast<uint4*>(vt + tc5::sw128(r, lane * 8, kTile)) =
-                      make_uint4(0, 0, 0, 0);
-              }
-              fence_proxy_async_smem();
-              __syncwarp();
-            }
+        const bool pre = item->b < 0;
+        const uint64_t policy = p.single_read || (pre && p.prefix_tiles == 1)
+                                    ? l2_policy_evict_first()
+                                    : l2_policy_evict_normal();
+        const CUtensorMap* mk = pre ? &maps.k_prefix : &maps.k;
+        const CUtensorMap* mv = pre ? &maps.v_prefix : &maps.v;
+        const int z = pre ? item->kvh : (p.b_offset + item->b) * p.h_kv + item->kvh;
+        const uint32_t ring0 = smem_u32(ring);
+        RingPlace<kSlots> at;
+        uint32_t issued = 0, parity = 0;  // per slot: loaded at all, phase of its newest load
+        int edges = 0;
+        bool ok = true;
+        auto load = [&](const CUtensorMap* map, int j) {
+          if (!ok) return;
+          if (!mbar_wait_bounded(empty0 + 8 * at.slot, at.phase ^ 1u, abort_flag)) {
+            give_up();
+            ok = false;
+            return;
           }
-          if (!wait(p_full0 + 8 * i, seen_p[i] & 1)) break;
-          if (lane == 0) {
-            tc5::fence_after();
-            const uint32_t va = smem_u32(ring) + vslot * kTileBytes;
-            const uint32_t o = tmem + 256 + i * D, pa = tmem + i * 128;
+#ifdef DA_TEST_HOOKS
+          if (int(blockIdx.x) == p.withhold_cta && map == mv && j == count - 1) return;
+#endif
+          const uint32_t dst = ring0 + at.slot * kTileBytes;
+          const int y = tile_row(*item, item->begin + j);
+          // a V tile with rows to clear goes to warp 10 first, which says when it is full
+          const bool edge = map == mv && edges < kEdges && edge_tile(p, *item, y);
+          const uint32_t bar = edge ? edge0 + 8 * edges++ : full0 + 8 * at.slot;
+          mbar_arrive_expect_tx(bar, kTileBytes);
 #pragma unroll
-            for (int ks = 0; ks < kTile / 16; ++ks)
-              mma_tmem_a(o, pa + ks * 8, tc5::sdesc(va + ks * 16 * 128, kHalfBytes, 1024), idesc_o,
-                         seen_p[i] > 0 || ks > 0);
-            if constexpr (WIDE_P) {
+          for (int c = 0; c < D; c += 64)
+            tma_load_3d(dst + (c / 64) * kHalfBytes, map, c, y, z, bar, policy);
+          issued = edge ? issued & ~(1u << at.slot) : issued | 1u << at.slot;
+          parity = (parity & ~(1u << at.slot)) | (at.phase << at.slot);
+          at.next();
+        };
+        // loads follow their use: K of the first `ahead` tiles, then V_j and K_(j + ahead)
+        for (int j = 0; j < min(ahead, count); ++j) load(mk, j);
+        for (int j = 0; j < count; ++j) {
+          load(mv, j);
+          if (j + ahead < count) load(mk, j + ahead);
+        }
+        if (!ok) {  // copies in flight land before the CTA ends
+          volatile int never = 0;
+          for (int i = 0; i < kSlots; ++i)
+            if (issued >> i & 1) mbar_wait_bounded(full0 + 8 * i, (parity >> i) & 1, &never);
+          for (int i = 0; i < edges; ++i) mbar_wait_bounded(edge0 + 8 * i, 0, &never);
+        }
+      }
+      return;
+    }
+    // ---------------------------------------------------------------- MMA issuer
+    if (warp == 9) {
+      if (lane == 0) {
+        const uint32_t idesc_s = tc5::idesc_bf16(128, 128, 0, 0);
+        const uint32_t idesc_o = tc5::idesc_bf16(128, D, 0, 1);
+        // descriptors of the operands' first bytes; their addresses count 16 bytes
+        const uint64_t k_major = tc5::sdesc(0, 16, 1024), mn_major = tc5::sdesc(0, kHalfBytes, 1024);
+        const uint32_t q_at = smem_u32(q_tile) >> 4, ring_at = smem_u32(ring) >> 4;
+        const int upto0 = item->upto[0], upto1 = item->upto[1];
+        bool ok = true, any = false;
+        uint32_t p_phase = 0;                     // a bit for each stream
+        uint32_t started = 0;                     // streams with a P.V issued
+        RingPlace<kSlots> at;
+        auto wait = [&](uint32_t bar, uint32_t parity) {
+          if (ok && !mbar_wait_bounded(bar, parity, abort_flag)) {
+            give_up();
+            ok = false;
+          }
+          return ok;
+        };
+        auto scores = [&](int i, int slot) {  // S_i = Q_i K^T
+          tc5::fence_after();
+          const uint64_t a = k_major + q_at + (alternate ? 0 : i * (kTileBytes >> 4));
+          const uint64_t b = k_major + ring_at + slot * (kTileBytes >> 4);
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks) {
+            const uint32_t off = ((ks >> 2) * kHalfBytes + (ks & 3) * 32) >> 4;
+            tc5::mma(tmem + i * 128, a + off, b + off, idesc_s, ks > 0);
+          }
+          tc5::commit(s_full0 + 8 * i);
+          any = true;
+        };
+        if (count > 0 && wait(q_full0, 0) && !alternate) wait(q_full0 + 8, 0);
+        for (int j = 0; j < min(ahead, count) && ok; ++j) {
+          if (!wait(full0 + 8 * at.slot, at.phase)) break;
+          if (alternate) {
+            scores(j, at.slot);
+          } else {
+            if (j < upto0) scores(0, at.slot);
+            if (j < upto1) scores(1, at.slot);
+          }
+          tc5::commit(empty0 + 8 * at.slot);
+          at.next();
+        }
+        for (int j = 0; j < count && ok; ++j) {
+          const RingPlace<kSlots> v = at;         // V_j
+          at.next();
+          const bool more = j + ahead < count;
+          if (!wait(full0 + 8 * v.slot, v.phase)) break;
+          bool k_here = false;
+          const int i_end = alternate ? (j & 1) + 1 : 2;
+          for (int i = alternate ? j & 1 : 0; i < i_end; ++i) {
+            const int mine = alternate ? count : i == 0 ? upto0 : upto1;
+            if (j < mine) {
+              if (!wait(p_full0 + 8 * i, (p_phase >> i) & 1)) break;
+              p_phase ^= 1u << i;
+              tc5::fence_after();
+              const uint64_t b = mn_major + ring_at + v.slot * (kTileBytes >> 4);
+              const uint32_t o = tmem + 256 + i * D, pa = tmem + i * 128;
+              const bool more_o = (started >> i) & 1;
 #pragma unroll
               for (int ks = 0; ks < kTile / 16; ++ks)
-                mma_tmem_a(o, pa + 64 + ks * 8, tc5::sdesc(va + ks * 16 * 128, kHalfBytes, 1024),
-                           idesc_o, 1);
+                mma_tmem_a(o, pa + ks * 8, b + ks * (16 * 128 >> 4), idesc_o, more_o || ks > 0);
+              if constexpr (WIDE_P) {
+#pragma unroll
+                for (int ks = 0; ks < kTile / 16; ++ks)
+                  mma_tmem_a(o, pa + 64 + ks * 8, b + ks * (16 * 128 >> 4), idesc_o, 1);
+              }
+              started |= 1u << i;
+            }
+            if (j + ahead < mine) {
+              if (!k_here && !wait(full0 + 8 * at.slot, at.phase)) break;
+              k_here = true;
+              scores(i, at.slot);
             }
           }
-          any = true;
-          ++seen_p[i];
-          __syncwarp();
+          if (!ok) break;
+          tc5::commit(empty0 + 8 * v.slot);
+          if (more) {
+            tc5::commit(empty0 + 8 * at.slot);
+            at.next();
+          }
         }
-        if (j + ahead < count && takes(p, w, st, i, w.begin + j + ahead)) scores(i, j + ahead);
+        if (ok && any) {
+          tc5::commit(o_full0);
+          tc5::commit(o_full0 + 8);
+        }
+        // every MMA has completed before TMEM is freed
+        if (any) tc5::commit(fin);
+        else mbar_arrive(fin);
+        volatile int never = 0;
+        mbar_wait_bounded(fin, 0, &never);
       }
-      if (ok && lane == 0) {
-        tc5::commit(empty0 + 8 * vslot);
-        if (j + ahead < count) tc5::commit(empty0 + 8 * (k_place(j + ahead) % kSlots));
+      __syncwarp();
+      named_bar_sync(2, 288);
+      tc5::fence_after();
+      tc5::dealloc(tmem, kTmemCols);
+      return;
+    }
+    // ---------------------------------------------------------------- clearing V
+    if (warp == 10) {
+      int edges = 0;
+      for (int j = 0; j < count && edges < kEdges; ++j) {
+        const int r0 = tile_row(*item, item->begin + j);
+        if (!edge_tile(p, *item, r0)) continue;
+        const bool got = mbar_wait_bounded(edge0 + 8 * edges++, 0, abort_flag);
+        if (!got) give_up();
+        if (!__all_sync(0xffffffffu, got)) break;
+        const int slot = (j + min(count, ahead + j)) % kSlots;  // V_j in the order of the loads
+        uint8_t* vt = ring + size_t(slot) * kTileBytes;
+        const int seen_end = item->n, clear_lo = item->clear_lo;
+        constexpr int kChunks = D / 8;  // 16-byte pieces of a row
+#pragma unroll 8
+        for (int x = lane; x < kTile * kChunks; x += 32) {
+          const int row = r0 + x / kChunks;
+          if (row >= seen_end || (row < clear_lo && row >= p.prefix))
+            *reinterpret_cast<uint4*>(vt + tc5::sw128(x / kChunks, (x % kChunks) * 8, kTile)) =
+                make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(full0 + 8 * slot);
       }
     }
-    if (lane == 0) {
-      if (ok && any) {
-        tc5::commit(o_full0);
-        tc5::commit(o_full0 + 8);
-      }
-      // every MMA has completed before TMEM is freed
-      if (any) tc5::commit(fin);
-      else mbar_arrive(fin);
-      volatile int never = 0;
-      mbar_wait_bounded(fin, 0, &never);
-    }
-    __syncwarp();
-    named_bar_sync(2, 288);
-    tc5::fence_after();
-    tc5::dealloc(tmem, kTmemCols);
     return;
-  }
-  return;
   }
 
   // ------------------------------------------------------------------ softmax
@@ -613,130 +647,148 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
   const int r = quarter * 32 + lane;                // row of the stream = TMEM lane
   const uint32_t lanes = uint32_t(quarter * 32) << 16;
   const uint32_t s_col = tmem + i * 128 + lanes, o_col = tmem + 256 + i * D + lanes;
-  const bool valid = r < st.rows[i];
+  const int rows = alternate ? item->rows : min(item->rows - i * kTile, kTile);
+  // Warps without a query row stay out (their rows of S, P and O are never
+  // looked at); the stream's first warp arrives for them.
+  const bool works = quarter * 32 < rows;
+  const uint32_t arrivals = quarter == 0 ? 4 - (rows - 1) / 32 : 1;
+  const bool valid = r < rows;
+  const int unit_row = (alternate ? 0 : i * kTile) + r;
   // this row's token, head and position
-  const int unit_row = (st.alternate ? 0 : i * kTile) + r;
   int hi = -1, lo = 0;
-  long long q_off = 0, out_off = 0;
-  if (valid) {
-    const int flat = w.u.row0 + unit_row;
-    const int t = flat / p.group, head = w.kvh * p.group + flat % p.group;
-    const int b = w.b < 0 ? t : w.b, tok = w.b < 0 ? 0 : t;
-    hi = w.b < 0 ? w.n - 1 : w.u.p0 - w.u.row0 / p.group + t;
-    lo = w.b < 0 || !p.window ? 0 : hi + 1 - p.window;
-    q_off = b * p.q_stride[0] + head * p.q_stride[1] + tok * p.q_stride[2];
-    out_off = b * p.out_stride[0] + head * p.out_stride[1] + tok * p.out_stride[2];
-  }
-  bool live = true;
-  if (count > 0 && !(st.alternate && i == 1)) {
-    // Q of the stream's rows, swizzled K-major; rows past the unit are zero
-    constexpr int kChunks = D / 8, kPer = 32 / kChunks;  // 16-byte pieces of a row; rows at a time
-    uint4 v[32 / kPer];
-    const uint4* q = static_cast<const uint4*>(p.q);
-#pragma unroll
-    for (int k = 0; k < 32 / kPer; ++k) {
-      const int row = k * kPer + lane / kChunks;
-      const long long off = __shfl_sync(0xffffffffu, q_off, row);
-      const bool in = quarter * 32 + row < st.rows[i] && DA_IN(p, off + D - 1, p.q_elems);
-      v[k] = in ? q[off / 8 + lane % kChunks] : make_uint4(0, 0, 0, 0);
-    }
-    const uint32_t flip = p.q_flip == 1 ? 0x80008000u : 0u, keep = p.q_flip == 2 ? 0u : ~0u;
-#pragma unroll
-    for (int k = 0; k < 32 / kPer; ++k) {
-      const int row = quarter * 32 + k * kPer + lane / kChunks;
-      *reinterpret_cast<uint4*>(q_tile + i * kTileBytes + tc5::sw128(row, (lane % kChunks) * 8, kTile)) =
-          make_uint4((v[k].x ^ flip) & keep, (v[k].y ^ flip) & keep, (v[k].z ^ flip) & keep,
-                     (v[k].w ^ flip) & keep);
-    }
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(q_full0 + 8 * i);
-  }
-
+  long long out_off = 0;
+  bool live = works;
   float m_run = -INFINITY, l_run = 0.f;
   int done = 0;  // tiles of this stream
-  auto give_up = [&] {
-    if (!*abort_flag) {
-      *abort_flag = 1;
-      flag_error(p.dev_error, DA_DEVERR_TIMEOUT);
+  if (works) {
+    const bool pre = item->b < 0;
+    long long q_off = 0;
+    if (valid) {
+      const int flat = item->row0 + unit_row;
+      const int t = p.by_group.div(flat), head = item->kvh * p.group + flat - t * p.group;
+      const int b = pre ? t : item->b, tok = pre ? 0 : t;
+      hi = item->past + tok;
+      lo = pre || !p.window ? 0 : hi + 1 - p.window;
+      q_off = b * p.q_stride[0] + head * p.q_stride[1] + tok * p.q_stride[2];
+      out_off = b * p.out_stride[0] + head * p.out_stride[1] + tok * p.out_stride[2];
     }
-  };
-  for (int j = 0; j < count; ++j) {
-    if (!takes(p, w, st, i, w.begin + j)) continue;
-    const bool got = mbar_wait_bounded(s_full0 + 8 * i, done & 1, abort_flag);
-    if (!got) give_up();
-    live = __all_sync(0xffffffffu, got);  // warp-uniform: the TMEM accesses below are .sync.aligned
-    if (!live) break;
-    tc5::fence_after();
-    uint32_t raw[128];
-    float* s = reinterpret_cast<float*>(raw);
+    if (!(alternate && i == 1)) {
+      // Q of the warp's rows, swizzled K-major
+      constexpr int kChunks = D / 8, kPer = 32 / kChunks;  // 16-byte pieces of a row; rows at a time
+      uint4 v[32 / kPer];
+      const uint4* q = static_cast<const uint4*>(p.q);
 #pragma unroll
-    for (int c = 0; c < 128; c += 32) tmem_ld32(s_col + c, raw + c);
-    tc5::wait_ld();
-    const int r0 = tile_row(w.u, w.begin + j);
-    if (r0 + kTile - 1 > st.hi_first[i] || (r0 < st.lo_last[i] && r0 + kTile > p.prefix)) {
-      const int hi_c = hi - r0, lo_c = lo - r0, pre_c = p.prefix - r0;
-#pragma unroll
-      for (int c = 0; c < 128; ++c) {
-        const bool seen = c <= hi_c && (c >= lo_c || c < pre_c);
-        s[c] = seen ? s[c] : -INFINITY;
+      for (int k = 0; k < 32 / kPer; ++k) {
+        const int row = k * kPer + lane / kChunks;
+        const long long off = __shfl_sync(0xffffffffu, q_off, row);
+        const bool in = quarter * 32 + row < rows && DA_IN(p, off + D - 1, p.q_elems);
+        v[k] = in ? q[off / 8 + lane % kChunks] : make_uint4(0, 0, 0, 0);
       }
+      const uint32_t flip = p.q_flip == 1 ? 0x80008000u : 0u, keep = p.q_flip == 2 ? 0u : ~0u;
+#pragma unroll
+      for (int k = 0; k < 32 / kPer; ++k) {
+        const int row = quarter * 32 + k * kPer + lane / kChunks;
+        *reinterpret_cast<uint4*>(q_tile + i * kTileBytes + tc5::sw128(row, (lane % kChunks) * 8, kTile)) =
+            make_uint4((v[k].x ^ flip) & keep, (v[k].y ^ flip) & keep, (v[k].z ^ flip) & keep,
+                       (v[k].w ^ flip) & keep);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_n(q_full0 + 8 * i, arrivals);
     }
-    float m4[4] = {s[0], s[1], s[2], s[3]};
+    // Tiles from here on need the mask: rows past the stream's first query, and of the
+    // window's start up to its last query's.
+    const int row_last = item->row0 + (alternate ? 0 : i * kTile) + rows - 1;
+    const int row_first = item->row0 + (alternate ? 0 : i * kTile);
+    const int hi_first = pre ? item->past : item->past + p.by_group.div(row_first);
+    const int lo_last =
+        pre || !p.window ? 0 : max(0, item->past + p.by_group.div(row_last) + 1 - p.window);
+
+    const int end = item->upto[i], step = alternate ? 2 : 1;
+    for (int j = alternate ? i : 0; j < end; j += step) {
+      const bool got = mbar_wait_bounded(s_full0 + 8 * i, done & 1, abort_flag);
+      if (!got) give_up();
+      live = __all_sync(0xffffffffu, got);  // warp-uniform: the TMEM accesses are .sync.aligned
+      if (!live) break;
+      tc5::fence_after();
+      uint32_t raw[128];
+      float* s = reinterpret_cast<float*>(raw);
 #pragma unroll
-    for (int c = 4; c < 128; ++c) m4[c & 3] = fmaxf(m4[c & 3], s[c]);
-    const float m_tile = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-    const bool over = m_tile > m_run + p.lazy || (m_run == -INFINITY && m_tile > -INFINITY);
-    if (__any_sync(0xffffffffu, over)) {
-      const float m_new = over ? m_tile : m_run;
-      const float alpha = over ? ex2((m_run - m_new) * p.scale_log2) : 1.f;  // 0 from -inf
-      m_run = m_new;
-      l_run *= alpha;
-      if (done > 0) {  // (S of this tile was issued behind the P.V of the last)
+      for (int c = 0; c < 128; c += 32) tmem_ld32(s_col + c, raw + c);
+      const int r0 = tile_row(*item, item->begin + j);
+      tc5::wait_ld();
+      if (r0 + kTile - 1 > hi_first || (r0 < lo_last && r0 + kTile > p.prefix)) {
+        const int hi_c = hi - r0, lo_c = lo - r0, pre_c = p.prefix - r0;
 #pragma unroll
-        for (int c = 0; c < D; c += 32) {
-          uint32_t o[32];
-          tmem_ld32(o_col + c, o);
-          tc5::wait_ld();
-#pragma unroll
-          for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
-          tmem_st32(o_col + c, o);
+        for (int c = 0; c < 128; ++c) {
+          const bool seen = c <= hi_c && (c >= lo_c || c < pre_c);
+          s[c] = seen ? s[c] : -INFINITY;
         }
       }
-    }
-    const float shift = m_run == -INFINITY ? 0.f : -m_run * p.scale_log2;
-    float l4[4] = {0.f, 0.f, 0.f, 0.f};
-    // exponentials in halves of 64 columns; P over the first columns of S, which
-    // every lane of the warp has loaded
+      float m4[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-    for (int h = 0; h < 128; h += 64) {
-      uint32_t hi_p[32];
+      for (int c = 4; c < 124; c += 8)
 #pragma unroll
-      for (int c = 0; c < 64; c += 2) {
-        const float a = ex2(fmaf(s[h + c], p.scale_log2, shift));
-        const float b = ex2(fmaf(s[h + c + 1], p.scale_log2, shift));
-        l4[c & 2] += a;
-        l4[(c & 2) + 1] += b;
-        hi_p[c / 2] = pack_bf16x2(a, b);
+        for (int k = 0; k < 4; ++k) m4[k] = fmaxf(fmaxf(m4[k], s[c + k]), s[c + 4 + k]);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) m4[k] = fmaxf(m4[k], s[124 + k]);
+      const float m_tile = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+      const bool over = m_tile > m_run + p.lazy || (m_run == -INFINITY && m_tile > -INFINITY);
+      if (__any_sync(0xffffffffu, over)) {
+        const float m_new = over ? m_tile : m_run;
+        const float alpha = over ? ex2((m_run - m_new) * p.scale_log2) : 1.f;  // 0 from -inf
+        m_run = m_new;
+        l_run *= alpha;
+        if (done > 0) {  // (S of this tile was issued behind the P.V of the last)
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            uint32_t o[32];
+            tmem_ld32(o_col + c, o);
+            tc5::wait_ld();
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+            tmem_st32(o_col + c, o);
+          }
+        }
+      }
+      const float shift = m_run == -INFINITY ? 0.f : -m_run * p.scale_log2;
+      const uint64_t scale2 = pair_of(p.scale_log2, p.scale_log2), shift2 = pair_of(shift, shift);
+      uint64_t l2[2] = {0, 0};
+      // exponentials in halves of 64 columns; P over the first columns of S, which
+      // every lane of the warp has loaded
+#pragma unroll
+      for (int h = 0; h < 128; h += 64) {
+        uint32_t hi_p[32];
+#pragma unroll
+        for (int c = 0; c < 64; c += 2) {
+          float a, b;
+          halves_of(fma2(pair_of(s[h + c], s[h + c + 1]), scale2, shift2), a, b);
+          a = ex2(a);
+          b = ex2(b);
+          l2[(c >> 1) & 1] = add2(l2[(c >> 1) & 1], pair_of(a, b));
+          hi_p[c / 2] = pack_bf16x2(a, b);
+          if constexpr (WIDE_P) {
+            s[h + c] = a - bf16_lo_to_f32(hi_p[c / 2]);
+            s[h + c + 1] = b - bf16_hi_to_f32(hi_p[c / 2]);
+          }
+        }
+        tmem_st32(s_col + h / 2, hi_p);
         if constexpr (WIDE_P) {
-          s[h + c] = a - bf16_lo_to_f32(hi_p[c / 2]);
-          s[h + c + 1] = b - bf16_hi_to_f32(hi_p[c / 2]);
+          uint32_t lo_p[32];
+#pragma unroll
+          for (int c = 0; c < 64; c += 2) lo_p[c / 2] = pack_bf16x2(s[h + c], s[h + c + 1]);
+          tmem_st32(s_col + 64 + h / 2, lo_p);
         }
       }
-      tmem_st32(s_col + h / 2, hi_p);
-      if constexpr (WIDE_P) {
-        uint32_t lo_p[32];
-#pragma unroll
-        for (int c = 0; c < 64; c += 2) lo_p[c / 2] = pack_bf16x2(s[h + c], s[h + c + 1]);
-        tmem_st32(s_col + 64 + h / 2, lo_p);
-      }
+      float la, lb;
+      halves_of(add2(l2[0], l2[1]), la, lb);
+      l_run += la + lb;
+      tc5::wait_st();
+      tc5::fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_n(p_full0 + 8 * i, arrivals);
+      ++done;
     }
-    l_run += (l4[0] + l4[1]) + (l4[2] + l4[3]);
-    tc5::wait_st();
-    tc5::fence_before();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(p_full0 + 8 * i);
-    ++done;
   }
 
   // ---- the unit's rows are final once both streams' MMAs are
@@ -749,53 +801,54 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
   }
   // (a CTA whose wait ran out writes nothing)
   float* other = reinterpret_cast<float*>(ring);  // alternate: O^T [D][128], m [128], l [128] of stream 1
-  if (st.alternate) {
+  const bool with_other = alternate && count > 1;
+  if (with_other) {
     if (i == 1 && live) {
-      if (done > 0) {
+#pragma unroll 2
+      for (int c = 0; c < D; c += 32) {
+        uint32_t o[32];
+        tmem_ld32(o_col + c, o);
+        tc5::wait_ld();
 #pragma unroll
-        for (int c = 0; c < D; c += 32) {
-          uint32_t o[32];
-          tmem_ld32(o_col + c, o);
-          tc5::wait_ld();
-#pragma unroll
-          for (int k = 0; k < 32; ++k) other[(c + k) * kTile + r] = __uint_as_float(o[k]);
-        }
+        for (int k = 0; k < 32; ++k) other[(c + k) * kTile + r] = __uint_as_float(o[k]);
       }
       other[D * kTile + r] = m_run;
       other[D * kTile + kTile + r] = l_run;
     }
     named_bar_sync(1, 256);
-    if (i == 1 || *abort_flag) live = false;
+    if (*abort_flag) live = false;
     live = __all_sync(0xffffffffu, live);
   }
-  float keep0 = 1.f, keep1 = 0.f;  // weights of the two streams' O
-  const bool with_other = st.alternate && count > 1;
-  if (live && with_other) {
-    const float m1 = other[D * kTile + r], l1 = other[D * kTile + kTile + r];
-    const float m = fmaxf(m_run, m1), m_use = m == -INFINITY ? 0.f : m;
-    keep0 = ex2((m_run - m_use) * p.scale_log2);
-    keep1 = ex2((m1 - m_use) * p.scale_log2);
-    l_run = l_run * keep0 + l1 * keep1;
-    m_run = m;
-  }
-  if (live) {
+  if (live && !(alternate && i == 1)) {
+    float keep0 = 1.f, keep1 = 0.f;  // weights of the two streams' O
+    if (with_other) {
+      const float m1 = other[D * kTile + r], l1 = other[D * kTile + kTile + r];
+      const float m = fmaxf(m_run, m1), m_use = m == -INFINITY ? 0.f : m;
+      keep0 = ex2((m_run - m_use) * p.scale_log2);
+      keep1 = ex2((m1 - m_use) * p.scale_log2);
+      l_run = l_run * keep0 + l1 * keep1;
+      m_run = m;
+    }
     const float inv = l_run > 0.f ? 1.f / l_run : (l_run == 0.f ? 0.f : l_run);
     keep0 *= inv;
     keep1 *= inv;
-    const bool part = w.slot >= 0;
-    if (part) out_off = ((long long)w.slot * p.pitch + unit_row) * D;
+    const bool part = item->slot >= 0;
+    const long long part_row = (long long)item->slot * p.pitch + unit_row;
+    if (part) out_off = part_row * D;
     const long long extent = part ? (long long)p.max_items * p.pitch * D : p.out_elems;
-    if (part && valid && DA_IN(p, (long long)w.slot * p.pitch + unit_row, (long long)p.max_items * p.pitch))
-      p.lse_part[(long long)w.slot * p.pitch + unit_row] =
+    if (part && valid && DA_IN(p, part_row, (long long)p.max_items * p.pitch))
+      p.lse_part[part_row] =
           l_run > 0.f ? m_run * p.scale_log2 + log2f(l_run) : (l_run == 0.f ? -INFINITY : l_run);
     const bool narrow = !part && p.out_bf16;
     uint8_t* stage = q_tile + i * kTileBytes + quarter * (kTileBytes / 4);  // 32 rows of 2 D bytes
     constexpr int kChunks = D / 8, kPer = 32 / kChunks;
+    const int mine = min(rows - quarter * 32, 32);  // rows of this warp
     // a row of 2 D bytes at a time (D bf16 or D / 2 floats) through shared memory,
     // so that whole rows are written
-    for (int c0 = 0; c0 < D; c0 += narrow ? D : D / 2) {
-      const int cols = narrow ? D : D / 2;
+    const int cols = narrow ? D : D / 2;
 #pragma unroll 1
+    for (int c0 = 0; c0 < D; c0 += cols) {
+#pragma unroll 2
       for (int c = 0; c < cols; c += 32) {
         uint32_t o[32];
         if (done > 0) {
@@ -828,11 +881,11 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
       }
       __syncwarp();
 #pragma unroll 4
-      for (int k = 0; k < 32; k += kPer) {
+      for (int k = 0; k < mine; k += kPer) {
         const int row = k + lane / kChunks, ch = lane % kChunks;
         const long long off = __shfl_sync(0xffffffffu, out_off, row);
         const uint4 v = *reinterpret_cast<const uint4*>(stage + row * 2 * D + ((ch ^ (row & 7)) << 4));
-        if (quarter * 32 + row < st.rows[i] && DA_IN(p, off + D - 1, extent)) {
+        if (row < mine && DA_IN(p, off + D - 1, extent)) {
           if (narrow)
             *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + off + ch * 8) = v;
           else
@@ -863,12 +916,12 @@ __global__ void __launch_bounds__(kAttendCombineWarps * 32)
   const int lane = threadIdx.x & 31;
   const long long warps = (long long)gridDim.x * kAttendCombineWarps;
   // rows as [entry][kv head][row of the unit]
-  const long long all = (long long)p.B * p.q_tiles * p.h_kv * p.pitch;
+  const long long all = (long long)p.B * p.q_tiles * p.h_kv * p.unit_rows;
   for (long long x = (long long)blockIdx.x * kAttendCombineWarps + (threadIdx.x >> 5); x < all;
        x += warps) {
-    const int ur = int(x % p.pitch);
-    const int kvh = int(x / p.pitch % p.h_kv);
-    const int e = int(x / p.pitch / p.h_kv) + p.shared;
+    const int ur = int(x % p.unit_rows);
+    const int kvh = int(x / p.unit_rows % p.h_kv);
+    const int e = int(x / p.unit_rows / p.h_kv) + p.shared;
     const int2 at = __ldcg(p.table + e);
     if (!p.shared && at.y <= 1) continue;
     int b, qt;
@@ -968,7 +1021,7 @@ cudaError_t launch_attend(const AttendParams& p, const AttendMaps& m, int d, int
 }
 
 cudaError_t launch_attend_combine(const AttendParams& p, int d, cudaStream_t stream) {
-  const long long rows = (long long)p.B * p.q_tiles * p.h_kv * p.pitch;
+  const long long rows = (long long)p.B * p.q_tiles * p.h_kv * p.unit_rows;
   const long long most = (rows + kAttendCombineWarps - 1) / kAttendCombineWarps;
   const int grid = int(most < 8LL * p.sms ? most : 8LL * p.sms);
   if (d == 128)

@@ -394,6 +394,21 @@ cudaError_t launch_kv_append_rope(const RopeAppendArgs& a, cudaStream_t stream);
 
 // Attention of many query rows over one KV head's rows (attend.cu): the chunk
 // and the shared-prefix entry points.
+//
+// Division of a non-negative int by a divisor known on the host: with l = ceil(log2 d),
+// n / d = (floor(n mul / 2^32) + n) >> l for mul = floor(2^32 (2^l - d) / d) + 1.
+struct FastDiv {
+  uint32_t mul = 0, shift = 0;
+  FastDiv() = default;
+  explicit FastDiv(uint32_t d) {
+    while ((1ull << shift) < d) ++shift;
+    mul = uint32_t(((1ull << 32) * ((1ull << shift) - d)) / d + 1);
+  }
+  __device__ __forceinline__ int div(int n) const {
+    return int((__umulhi(uint32_t(n), mul) + uint32_t(n)) >> shift);
+  }
+};
+
 struct AttendParams {
   const void* q;                 // bf16, element (b, h, t, :) at b * q_stride[0] + h * [1] + t * [2]
   long long q_stride[3];
@@ -413,7 +428,9 @@ struct AttendParams {
   int single_read;               // each K and V row is read by one CTA: no use in keeping it in L2
   // Units: (row tile of 256 query rows, KV head, sequence). list != 0: units are cut into items of
   // about equal length, merged by the combine; else one item per unit.
-  int list, entries, q_tiles, prefix_tiles, sms, max_items, pitch;
+  int list, entries, q_tiles, prefix_tiles, sms, max_items;
+  int pitch, unit_rows;          // most query rows of any unit, of a sequence's
+  FastDiv by_group, by_batch;
   float* o_part;                 // [max_items][pitch][d]
   float* lse_part;               // [max_items][pitch], log2 domain
   int2* table;                   // [entries] first item and items per unit
