@@ -1204,11 +1204,16 @@ int plan_attend(int B, int T, int h_q, int h_kv, int d, int n_max, int dtype, in
   const long long entries = (long long)a.slice * a.q_tiles + (P >= 0 ? 1 : 0);
   // Cut and merged behind a prefix (its units and a sequence's own are merged anyway), and in a
   // chunk when there are few units of more than a few tiles.
-  a.list = P >= 0 || (a.units < 4LL * sms && n_max > 2 * 128 && entries <= da::kAttendEntries);
+  const int most_tiles = (n_max + 127) / 128, prefix_most = P > 0 ? (P + 127) / 128 : 0;
+  a.list = P >= 0 || (a.units < 4LL * sms && most_tiles > 8 && entries <= da::kAttendEntries);
   a.entries = a.list ? int(entries) : 0;
   const long long tallest = P >= 0 ? a.slice * g : rows;
   a.pitch = int(tallest < da::kAttendRows ? tallest : da::kAttendRows);
-  a.max_items = a.list ? a.units + 2 * sms : a.units;
+  // An item of a list has two tiles at least where its unit was cut, and half an even share of
+  // the launch's: at most a cut for each pair of tiles, and 2 * sms in all.
+  const long long cuts = (long long)a.slice * a.q_tiles * h_kv * ((most_tiles + 1) / 2) +
+                         (long long)a.prefix_tiles * h_kv * ((prefix_most + 1) / 2);
+  a.max_items = !a.list ? a.units : cuts < a.units + 2 * sms ? cuts : a.units + 2 * sms;
   a.table_bytes = (size_t(a.entries) * 8 + 255) & ~size_t(255);
   a.part_rows = size_t(a.max_items) * a.pitch;
   *plan = a;
@@ -1292,8 +1297,8 @@ int run_attend(const AttendCall& c, void* workspace, size_t workspace_bytes, int
   p.prefix = c.prefix < (1 << 30) ? c.prefix : 1 << 30;
   if (p.window == 0) p.prefix = 0;  // every row up to the query's is seen
   p.shared = shared, p.P = shared ? c.P : 0;
-  p.q_flip = c.scale < 0.f ? 1 : c.scale == 0.f ? 2 : 0;
-  p.scale_log2 = c.scale == 0.f ? 1.f : float(scale_log2);
+  p.negate = c.scale < 0.f;
+  p.scale_log2 = scale_log2 < 1.2e-38 ? 1.2e-38f : float(scale_log2);
   p.lazy = float(8.0 / double(p.scale_log2));
   p.single_read = plan.q_tiles == 1;
   p.list = plan.list, p.q_tiles = plan.q_tiles, p.sms = sms;
@@ -1321,8 +1326,12 @@ int run_attend(const AttendCall& c, void* workspace, size_t workspace_bytes, int
     p.prefix_tiles = shared ? (p.B * p.group + da::kAttendRows - 1) / da::kAttendRows : 0;
     p.entries = p.list ? p.B * p.q_tiles + p.shared : 0;
     const long long units = ((long long)p.B * p.q_tiles + p.prefix_tiles) * p.h_kv;
-    const int grid = int(p.list ? units + 2 * sms : units);
-    cudaError_t e = da::launch_attend(p, maps, c.d, grid, stream);
+    // a CTA per SM; more where a list gives one more than it can note
+    long long grid = p.list ? plan.max_items : units;
+    if (grid > sms) grid = sms;
+    if (p.list && grid * da::kAttendOwn < plan.max_items)
+      grid = (plan.max_items + da::kAttendOwn - 1) / da::kAttendOwn;
+    cudaError_t e = da::launch_attend(p, maps, c.d, int(grid), stream);
     if (e != cudaSuccess) return fail_cuda(e, "attend launch");
     g_launches.fetch_add(1);
     if (p.list) {

@@ -22,9 +22,12 @@
 // A unit of at most 128 query rows (few tokens, one sequence's group) uses both
 // streams for the same rows on alternate tiles and merges them at the end.
 //
+// The kernel is persistent: a CTA per SM takes its items one after the other, so
+// that the loads and first scores of one run under the end of the last.
+//
 // Roles (384 threads): warps 0-3 and 4-7 the softmax of streams 0 and 1, warp 8
-// the TMA producer, warp 9 the MMA issuer, warp 10 clears V rows that may hold
-// anything.  TMEM: S 2 x 128 columns, O 2 x d.
+// the items and the TMA loads, warp 9 the MMAs, warp 10 clears V rows that may hold
+// anything (11 fills their warpgroup, which gives registers to the others).  TMEM: S 2 x 128 columns, O 2 x d.
 #include <math.h>
 
 #include "common.cuh"
@@ -36,7 +39,8 @@ namespace {
 constexpr int kTile = 128;              // K and V rows of a tile, query rows of a stream
 constexpr int kAttendThreads = 384;
 constexpr int kScheduleThreads = 256;
-constexpr int kEdges = 4;               // most tiles of an item with rows to clear (see edge_tile)
+constexpr int kEdges = 8;               // more than the V tiles that the ring can hold
+constexpr int kOwnItems = kAttendOwn;
 
 template <int D_>
 struct AttendCfg {
@@ -44,12 +48,15 @@ struct AttendCfg {
   static constexpr int kTileBytes = kTile * D * 2;  // Q of a stream, a K tile, a V tile
   static constexpr int kHalfBytes = kTile * 128;    // 64 columns of one
   static constexpr int kSlots = D == 128 ? 5 : 11;  // ring of K and V tiles
-  // q_full[2], kv_full[slots], kv_empty[slots], s_full[2], p_full[2], o_full[2], edge[4], fin
-  static constexpr int kBars = 2 + 2 * kSlots + 2 + 2 + 2 + kEdges + 1;
-  static constexpr size_t kSmemBytes = 1024 + size_t(2 + kSlots) * kTileBytes + kBars * 8 + 256;
+  // full[slots], empty[slots], out_done[slots], edge[kEdges], then for each stream q_full, s_full,
+  // p_full[2], o_full, o_empty; item_full[2], item_empty[2], meet[2], fin
+  static constexpr int kBars = 3 * kSlots + kEdges + 2 * 6 + 2 + 2 + 2 + 1;
+  static constexpr size_t kSmemBytes = size_t(2 + kSlots) * kTileBytes + kBars * 8 +
+                                       (kOwnItems + 2) * 60 + 16 + 4 * kTile * 4;
   static_assert(kSmemBytes <= 227 * 1024, "shared memory");
   // the schedule's scratch lies in the ring before the first load
   static_assert((kAttendEntries + 64) * 4 <= kTileBytes, "schedule scratch");
+  static_assert(kEdges > (kSlots + 1) / 2, "edge barriers");
 };
 
 // What one CTA does: some tiles of a unit.  List tile k of a unit is tile k of
@@ -66,6 +73,7 @@ struct Item {
   int clear_lo;      // rows of [prefix, clear_lo) and from n on are seen by no query of the sequence
   int slot;          // partial, or -1: the unit's only item writes the output
 };
+static_assert(sizeof(Item) <= 60, "shared memory of the items");
 
 __device__ __forceinline__ int seq_rows(const AttendParams& p, int b, bool& bad) {
   const int n = p.seq_lens[b];
@@ -158,12 +166,13 @@ __device__ __forceinline__ int entry_units(const AttendParams& p, int e) {
 // for the whole launch, the one that ends first by a simple model (rounds of the
 // grid times the tiles of an item and a constant for its start and end).  All
 // CTAs compute the same list from the lengths; CTA 0 leaves the table for the
-// combine.  Returns false for a CTA without an item.  Ends with a barrier.
+// combine.  CTA b takes items b, b + gridDim.x, ... of it, into `own`, and returns
+// how many they are.  Ends with a barrier.
 constexpr int kScheduleWarps = kScheduleThreads / 32;
 constexpr int kLengthChoices = 2 * kScheduleWarps;
 constexpr float kItemTiles = 5.f;  // an item's fixed cost in tiles
 
-__device__ __forceinline__ bool list_item(const AttendParams& p, int* scratch, Item* out) {
+__device__ __forceinline__ int list_items(const AttendParams& p, int* scratch, Item* own_items) {
   int* tiles = scratch;                       // [kAttendEntries], -1: absent
   int* sums = scratch + kAttendEntries;       // [64]
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -189,7 +198,6 @@ __device__ __forceinline__ bool list_item(const AttendParams& p, int* scratch, I
     sums[warp] = __float_as_int(total);
     sums[kScheduleWarps + warp] = tallest;
   }
-  if (tid == 0) out->count = -1;
   __syncthreads();
   total = 0.f;
 #pragma unroll
@@ -248,6 +256,10 @@ __device__ __forceinline__ bool list_item(const AttendParams& p, int* scratch, I
   }
   if (lane == 31 && mine) sums[warp] = upto;
   __syncthreads();
+  const int grid = int(gridDim.x), cta = int(blockIdx.x);
+  int all = 0;
+#pragma unroll
+  for (int i = 0; i < kScheduleWarps; ++i) all += sums[i];
   if (mine) {
     int at = upto - own;
     for (int i = 0; i < warp; ++i) at += sums[i];
@@ -256,9 +268,10 @@ __device__ __forceinline__ bool list_item(const AttendParams& p, int* scratch, I
       const int e = tid * kPer + i;
       if (e >= p.entries) break;
       const int items = cut[i] * entry_units(p, e);
-      const int x = int(blockIdx.x) - at;
-      if (blockIdx.x == 0) p.table[e] = make_int2(at, cut[i]);
-      if (x >= 0 && x < items && int(blockIdx.x) < p.max_items) {  // this CTA's
+      if (cta == 0) p.table[e] = make_int2(at, cut[i]);
+      int k = at > cta ? (at - cta + grid - 1) / grid : 0;
+      for (; cta + k * grid < at + items && k < kOwnItems; ++k) {  // this CTA's
+        const int x = cta + k * grid - at;
         Item w;
         entry_unit(p, e, w);
         const int unit = x / cut[i], s = x - unit * cut[i];
@@ -272,34 +285,29 @@ __device__ __forceinline__ bool list_item(const AttendParams& p, int* scratch, I
           w.kvh = unit;
         }
         cut_item(p, int((long long)w.tiles * s / cut[i]), int((long long)w.tiles * (s + 1) / cut[i]),
-                 cut[i] == 1 && !p.shared ? -1 : int(blockIdx.x), w);
-        *out = w;
+                 cut[i] == 1 && !p.shared ? -1 : cta + k * grid, w);
+        own_items[k] = w;
       }
       at += items;
     }
   }
   fence_proxy_async_smem();  // the scratch is the ring's: before its first loads
   __syncthreads();
-  return out->count >= 0;
+  return all > cta ? min((all - cta - 1) / grid + 1, kOwnItems) : 0;
 }
 
 // Without a list: one item per unit, the last row tiles, the longest of a chunk, first.
-__device__ __forceinline__ bool unit_item(const AttendParams& p, Item* out) {
-  if (threadIdx.x == 0) {
-    const int per = p.B * p.h_kv;
-    const int up = int(blockIdx.x) / per, rest = int(blockIdx.x) - up * per;
-    Item w;
-    w.b = rest / p.h_kv;
-    w.kvh = rest - w.b * p.h_kv;
-    bool bad;
-    const int n = seq_rows(p, w.b, bad);
-    seq_unit(p, n, seq_new(p, w.b, bad), p.q_tiles - 1 - up, w);
-    cut_item(p, 0, w.tiles, -1, w);
-    if (w.rows == 0) w.count = -1;
-    *out = w;
-  }
-  __syncthreads();
-  return out->count >= 0;
+// False: the unit has no rows.
+__device__ __forceinline__ bool unit_item(const AttendParams& p, int u, Item& w) {
+  const int per = p.B * p.h_kv;
+  const int up = u / per, rest = u - up * per;
+  w.b = rest / p.h_kv;
+  w.kvh = rest - w.b * p.h_kv;
+  bool bad;
+  const int n = seq_rows(p, w.b, bad);
+  seq_unit(p, n, seq_new(p, w.b, bad), p.q_tiles - 1 - up, w);
+  cut_item(p, 0, w.tiles, -1, w);
+  return w.rows > 0;
 }
 
 // 32 consecutive 32-bit TMEM columns of this thread's lane.
@@ -325,13 +333,45 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
       : "memory");
 }
 
-// D (TMEM) += A (TMEM: lane = row, two bf16 of K a column) . B (smem), fp32 accumulators.
-__device__ __forceinline__ void mma_tmem_a(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
-                                           uint32_t idesc, uint32_t accumulate) {
+// The MMA issuer runs as a whole warp, so that addresses and descriptors stay in
+// registers of the warp; one lane's instructions count.  (One thread in a branch took
+// 115 cycles for each MMA of 64: 1070 us for the prompts.)
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t e;
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+  return e;
+}
+// D (TMEM) = A (smem) . B (smem)^T [+ D], fp32 accumulators.
+__device__ __forceinline__ void mma_smem_a(uint32_t leader, uint32_t d_tmem, uint64_t adesc,
+                                           uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 e, %5, 0;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(leader)
+      : "memory");
+}
+// A in TMEM: lane = row, two bf16 of K a column.
+__device__ __forceinline__ void mma_tmem_a(uint32_t leader, uint32_t d_tmem, uint32_t a_tmem,
+                                           uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 e, %5, 0;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ void commit_one(uint32_t leader, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %1, 0;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+      "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ void arrive_one(uint32_t leader, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %1, 0;\n\t"
+      "@e mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(bar),
+      "r"(leader)
       : "memory");
 }
 
@@ -365,7 +405,8 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return r;
 }
 
-// A place of the ring: the producer and the MMA issuer pass through it in one order.
+// A place of the ring: K and V tiles in the order of their use, and behind each item
+// one through which the softmax warps write its output.
 template <int SLOTS>
 struct RingPlace {
   int slot = 0;
@@ -375,47 +416,677 @@ struct RingPlace {
   }
 };
 
+// What the roles of the kernel share.
+template <class Cfg>
+struct AttendShared {
+  uint8_t *q_tile, *ring;   // [2], [kSlots] tiles
+  Item* items;              // [2]: the items underway
+  Item* own;                // [kOwnItems]: a list's items of this CTA
+  float* pairs;             // [2][m, l][128]: the streams' sums of the same rows
+  volatile int* abort_flag;
+  uint32_t tmem;
+  uint32_t bars;
+  __device__ __forceinline__ uint32_t full(int s) const { return bars + 8 * s; }
+  __device__ __forceinline__ uint32_t empty(int s) const { return bars + 8 * (Cfg::kSlots + s); }
+  __device__ __forceinline__ uint32_t out_done(int s) const {
+    return bars + 8 * (2 * Cfg::kSlots + s);
+  }
+  __device__ __forceinline__ uint32_t edge(int e) const {
+    return bars + 8 * (3 * Cfg::kSlots + e % kEdges);
+  }
+  __device__ __forceinline__ uint32_t of(int i, int what) const {  // stream i's
+    return bars + 8 * (3 * Cfg::kSlots + kEdges + 6 * i + what);
+  }
+  __device__ __forceinline__ uint32_t q_full(int i) const { return of(i, 0); }
+  __device__ __forceinline__ uint32_t s_full(int i) const { return of(i, 1); }
+  __device__ __forceinline__ uint32_t p_full(int i, int h) const { return of(i, 2 + h); }
+  __device__ __forceinline__ uint32_t o_full(int i) const { return of(i, 4); }
+  __device__ __forceinline__ uint32_t o_empty(int i) const { return of(i, 5); }
+  __device__ __forceinline__ uint32_t rest(int what) const { return of(2, what); }
+  __device__ __forceinline__ uint32_t item_full(int k) const { return rest(k & 1); }
+  __device__ __forceinline__ uint32_t item_empty(int k) const { return rest(2 + (k & 1)); }
+  __device__ __forceinline__ uint32_t meet(int k) const { return rest(4 + k); }
+  __device__ __forceinline__ uint32_t fin() const { return rest(6); }
+
+  __device__ __forceinline__ void give_up(const AttendParams& p) const {
+    if (!*abort_flag) {
+      *abort_flag = 1;
+      flag_error(p.dev_error, DA_DEVERR_TIMEOUT);
+    }
+  }
+  // One thread's wait.
+  __device__ __forceinline__ bool wait(const AttendParams& p, uint32_t bar, uint32_t parity) const {
+    if (mbar_wait_bounded(bar, parity, abort_flag)) return true;
+    give_up(p);
+    return false;
+  }
+  // A warp's in which the control flow stays the warp's.
+  __device__ __forceinline__ bool wait_uniform(const AttendParams& p, uint32_t bar,
+                                               uint32_t parity) const {
+#pragma unroll 1
+    for (int n = 0; n < 256; ++n)
+      if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    return wait_warp(p, bar, parity);
+  }
+  // A warp's: every thread's, with one answer.
+  __device__ __forceinline__ bool wait_warp(const AttendParams& p, uint32_t bar,
+                                            uint32_t parity) const {
+    return __all_sync(0xffffffffu, wait(p, bar, parity));
+  }
+};
+constexpr int kItemReaders = 1 + 1 + 8;  // MMA issuer, the clearing warp, softmax warps
+
+// One set of rows, tiles dealt to the streams in turn.
+__device__ __forceinline__ bool alternates(const Item& w) { return w.rows <= kTile; }
+// Tiles whose scores are issued before a stream's first P.V.
+__device__ __forceinline__ int lookahead(const Item& w) { return alternates(w) ? 2 : 1; }
+
+// ---- the items and their loads: one thread
+template <class Cfg>
+__device__ __forceinline__ void attend_load(const AttendParams& p, const AttendMaps& maps,
+                                            const AttendShared<Cfg>& sh, int own_count) {
+  constexpr int kSlots = Cfg::kSlots;
+  RingPlace<kSlots> at;
+  uint32_t issued = 0, parity = 0;  // per slot: loaded on its full barrier, phase of that load
+  uint32_t outs = 0, out_parity = 0;  // per slot: held an output, phase of its out_done
+  int edges = 0;
+  bool ok = true;
+  auto free_place = [&] {
+    if (!sh.wait(p, sh.empty(at.slot), at.phase ^ 1u)) return false;
+    if (outs >> at.slot & 1) {
+      if (!sh.wait(p, sh.out_done(at.slot), out_parity >> at.slot & 1)) return false;
+      outs &= ~(1u << at.slot);
+      out_parity ^= 1u << at.slot;
+    }
+    return true;
+  };
+  int unit = int(blockIdx.x);
+  for (int k = 0; ok; ++k) {
+    if (k >= 2 && !sh.wait(p, sh.item_empty(k), ((k >> 1) - 1) & 1)) {
+      ok = false;
+      break;
+    }
+    Item& w = sh.items[k & 1];
+    if (p.list) {
+      if (k < own_count) w = sh.own[k];
+      else w.count = -1;
+    } else {
+      const int units = p.B * p.h_kv * p.q_tiles;
+      bool found = false;
+      for (; unit < units && !found; unit += int(gridDim.x)) found = unit_item(p, unit, w);
+      if (!found) w.count = -1;
+    }
+    mbar_arrive(sh.item_full(k));
+    if (w.count < 0) break;
+    const bool pre = w.b < 0;
+    const uint64_t policy = p.single_read || (pre && p.prefix_tiles == 1) ? l2_policy_evict_first()
+                                                                          : l2_policy_evict_normal();
+    const CUtensorMap* mk = pre ? &maps.k_prefix : &maps.k;
+    const CUtensorMap* mv = pre ? &maps.v_prefix : &maps.v;
+    const int z = pre ? w.kvh : (p.b_offset + w.b) * p.h_kv + w.kvh;
+    const int count = w.count, ahead = lookahead(w);
+    auto load = [&](const CUtensorMap* map, int j) {
+      if (!ok) return;
+      if (!(ok = free_place())) return;
+#ifdef DA_TEST_HOOKS
+      if (int(blockIdx.x) == p.withhold_cta && k == 0 && map == mv && j == count - 1) {
+        at.next();
+        return;
+      }
+#endif
+      const int y = tile_row(w, w.begin + j);
+      // a V tile with rows to clear goes to warp 10 first, which says when it is full
+      const bool edge = map == mv && edge_tile(p, w, y);
+      const uint32_t bar = edge ? sh.edge(edges++) : sh.full(at.slot);
+      mbar_arrive_expect_tx(bar, Cfg::kTileBytes);
+      const uint32_t dst = smem_u32(sh.ring) + at.slot * Cfg::kTileBytes;
+#pragma unroll
+      for (int c = 0; c < Cfg::D; c += 64)
+        tma_load_3d(dst + (c / 64) * Cfg::kHalfBytes, map, c, y, z, bar, policy);
+      issued = edge ? issued & ~(1u << at.slot) : issued | 1u << at.slot;
+      parity = (parity & ~(1u << at.slot)) | (at.phase << at.slot);
+      at.next();
+    };
+    // loads follow their use: K of the first tiles, then V_j and K_(j + ahead)
+    for (int j = 0; j < min(ahead, count); ++j) load(mk, j);
+    for (int j = 0; j < count; ++j) {
+      load(mv, j);
+      if (j + ahead < count) load(mk, j + ahead);
+    }
+    // a place for the output
+    if (ok && (ok = free_place())) {
+      issued &= ~(1u << at.slot);
+      outs |= 1u << at.slot;
+      mbar_arrive(sh.full(at.slot));
+      at.next();
+    }
+  }
+  if (!ok) {  // copies in flight land before the CTA ends
+    volatile int never = 0;
+    for (int i = 0; i < kSlots; ++i)
+      if (issued >> i & 1) mbar_wait_bounded(sh.full(i), (parity >> i) & 1, &never);
+    for (int e = max(0, edges - kEdges); e < edges; ++e)
+      mbar_wait_bounded(sh.edge(e), (e / kEdges) & 1, &never);
+  }
+}
+
+// ---- the MMAs: a warp, whose first lane issues them
+// Per tile and stream O += P V, then S = Q K^T of the stream's next tile: the new S
+// takes the place of the P that has just been read.  One lane issues both streams'
+// in turn, which keeps them apart: the softmax of one runs under the MMAs of the other.
+// (A warp for each let them fall into step: their exponentials then shared the
+// special-function units while the tensor cores waited, 20 % slower.)
+template <class Cfg, bool WIDE_P>
+__device__ __forceinline__ void attend_mma(const AttendParams& p, const AttendShared<Cfg>& sh) {
+  constexpr int D = Cfg::D, kTileBytes = Cfg::kTileBytes;
+  const uint32_t idesc_s = tc5::idesc_bf16(128, 128, 0, 0) | (p.negate ? 1u << 13 : 0u);  // -Q
+  const uint32_t idesc_o = tc5::idesc_bf16(128, D, 0, 1);
+  // descriptors of the operands' first bytes; their addresses count 16 bytes
+  const uint32_t ring_at = smem_u32(sh.ring) >> 4;
+  const uint64_t k_major = tc5::sdesc(0, 16, 1024) + ring_at;
+  const uint64_t mn_major = tc5::sdesc(0, Cfg::kHalfBytes, 1024) + ring_at;
+  const uint64_t q0 = tc5::sdesc(0, 16, 1024) + (smem_u32(sh.q_tile) >> 4);
+  const uint32_t tmem = __shfl_sync(0xffffffffu, sh.tmem, 0), leader = elect_one();
+  RingPlace<Cfg::kSlots> at;
+  bool ok = true, any = false;
+  uint32_t p_phase = 0;      // a bit for each stream: the parity of its p_full barriers
+  uint32_t pairs = 0;        // items of two sets of rows
+  for (int k = 0; ok; ++k) {
+    if (!(ok = sh.wait_uniform(p, sh.item_full(k), (k >> 1) & 1))) break;
+    const Item& w = sh.items[k & 1];
+    const int count = __shfl_sync(0xffffffffu, w.count, 0);
+    if (count < 0) break;
+    const bool alternate = __shfl_sync(0xffffffffu, w.rows, 0) <= kTile;
+    const int ahead = alternate ? 2 : 1;
+    const int upto0 = __shfl_sync(0xffffffffu, w.upto[0], 0);
+    const int upto1 = __shfl_sync(0xffffffffu, w.upto[1], 0);
+    if (!(ok = sh.wait_uniform(p, sh.q_full(0), k & 1))) break;
+    if (!alternate && !(ok = sh.wait_uniform(p, sh.q_full(1), pairs++ & 1))) break;
+    uint32_t started = 0;    // streams with a P.V in this item
+    auto scores = [&](int i, int slot) {
+      const uint64_t a = q0 + (alternate ? 0 : i * (kTileBytes >> 4));
+      const uint64_t b = k_major + slot * (kTileBytes >> 4);
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks) {
+        const uint32_t off = ((ks >> 2) * Cfg::kHalfBytes + (ks & 3) * 32) >> 4;
+        mma_smem_a(leader, tmem + i * 128, a + off, b + off, idesc_s, ks > 0);
+      }
+      commit_one(leader, sh.s_full(i));
+      any = true;
+    };
+    for (int j = 0; j < min(ahead, count); ++j) {
+      if (!(ok = sh.wait_uniform(p, sh.full(at.slot), at.phase))) break;
+      tc5::fence_after();
+      if (alternate) {
+        scores(j, at.slot);
+      } else {
+        if (j < upto0) scores(0, at.slot);
+        if (j < upto1) scores(1, at.slot);
+      }
+      commit_one(leader, sh.empty(at.slot));
+      at.next();
+    }
+    for (int j = 0; j < count && ok; ++j) {
+      const RingPlace<Cfg::kSlots> v = at;         // V_j, then K_(j + ahead)
+      if (!(ok = sh.wait_uniform(p, sh.full(v.slot), v.phase))) break;
+      at.next();
+      const bool more = j + ahead < count;
+      if (more && !(ok = sh.wait_uniform(p, sh.full(at.slot), at.phase))) break;
+      const uint64_t b = mn_major + v.slot * (kTileBytes >> 4);
+      const int i_end = alternate ? (j & 1) + 1 : 2;
+      for (int i = alternate ? j & 1 : 0; i < i_end; ++i) {
+        const int mine = alternate ? count : i == 0 ? upto0 : upto1;
+        if (j < mine) {
+          const uint32_t o = tmem + 256 + i * D, pa = tmem + i * 128;
+          const bool more_o = started >> i & 1;
+          // (O of the last item has been read)
+          if (!more_o && k > 0 && !(ok = sh.wait_uniform(p, sh.o_empty(i), (k - 1) & 1))) break;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {            // P comes in halves of 64 rows of V
+            if (!(ok = sh.wait_uniform(p, sh.p_full(i, h), p_phase >> i & 1))) break;
+            tc5::fence_after();
+#pragma unroll
+            for (int ks = 4 * h; ks < 4 * h + 4; ++ks)
+              mma_tmem_a(leader, o, pa + ks * 8, b + ks * (16 * 128 >> 4), idesc_o, more_o || ks > 0);
+            if constexpr (WIDE_P) {
+#pragma unroll
+              for (int ks = 4 * h; ks < 4 * h + 4; ++ks)
+                mma_tmem_a(leader, o, pa + 64 + ks * 8, b + ks * (16 * 128 >> 4), idesc_o, 1);
+            }
+          }
+          if (!ok) break;
+          p_phase ^= 1u << i;
+          started |= 1u << i;
+        }
+        if (j + ahead < mine) scores(i, at.slot);
+      }
+      if (!ok) break;
+      commit_one(leader, sh.empty(v.slot));
+      if (more) {
+        commit_one(leader, sh.empty(at.slot));
+        at.next();
+      }
+    }
+    for (int i = 0; i < 2 && ok; ++i) {
+      if (started >> i & 1) {
+        commit_one(leader, sh.o_full(i));
+      } else {
+        if (k > 0 && !(ok = sh.wait_uniform(p, sh.o_empty(i), (k - 1) & 1))) break;
+        arrive_one(leader, sh.o_full(i));
+      }
+    }
+    if (!ok) break;
+    arrive_one(leader, sh.item_empty(k));
+    // the output's place
+    if (!(ok = sh.wait_uniform(p, sh.full(at.slot), at.phase))) break;
+    arrive_one(leader, sh.empty(at.slot));
+    at.next();
+  }
+  // every MMA has completed before TMEM is freed
+  if (any) commit_one(leader, sh.fin());
+  else arrive_one(leader, sh.fin());
+  volatile int never = 0;
+  if (leader) mbar_wait_bounded(sh.fin(), 0, &never);
+  __syncwarp();
+}
+
+// ---- V rows to clear: a warp
+template <class Cfg>
+__device__ __forceinline__ void attend_clear(const AttendParams& p, const AttendShared<Cfg>& sh) {
+  constexpr int kChunks = Cfg::D / 8;  // 16-byte pieces of a row
+  const int lane = threadIdx.x & 31;
+  int edges = 0, place = 0;            // place of the item's first load in the ring
+  for (int k = 0;; ++k) {
+    if (!sh.wait_warp(p, sh.item_full(k), (k >> 1) & 1)) return;
+    const Item& w = sh.items[k & 1];
+    const int count = w.count;
+    if (count < 0) return;
+    const int ahead = lookahead(w), seen_end = w.n, clear_lo = w.clear_lo;
+    for (int j = 0; j < count; ++j) {
+      const int r0 = tile_row(w, w.begin + j);
+      if (!edge_tile(p, w, r0)) continue;
+      if (!sh.wait_warp(p, sh.edge(edges), (edges / kEdges) & 1)) return;
+      ++edges;
+      const int slot = (place + j + min(count, ahead + j)) % Cfg::kSlots;  // V_j's
+      uint8_t* vt = sh.ring + size_t(slot) * Cfg::kTileBytes;
+#pragma unroll 8
+      for (int x = lane; x < kTile * kChunks; x += 32) {
+        const int row = r0 + x / kChunks;
+        if (row >= seen_end || (row < clear_lo && row >= p.prefix))
+          *reinterpret_cast<uint4*>(vt + tc5::sw128(x / kChunks, (x % kChunks) * 8, kTile)) =
+              make_uint4(0, 0, 0, 0);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(sh.full(slot));
+    }
+    place = (place + 2 * count + 1) % Cfg::kSlots;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(sh.item_empty(k));
+  }
+}
+
+// Q of an item's rows of a softmax warp, swizzled K-major, for stream i (alternate: for
+// both): asynchronous copies, rows past the unit left as they are.  The MMAs that read
+// the buffer before have completed.
+template <class Cfg>
+__device__ __forceinline__ void start_q(const AttendParams& p, const AttendShared<Cfg>& sh,
+                                        const Item& w, int i, int quarter) {
+  constexpr int D = Cfg::D, kChunks = D / 8, kPer = 32 / kChunks;  // 16-byte pieces; rows at a time
+  const int lane = threadIdx.x & 31;
+  const bool alternate = alternates(w);
+  const int rows = (alternate ? w.rows : min(w.rows - i * kTile, kTile)) - quarter * 32;
+  if (rows <= 0 || (alternate && i == 1)) return;
+  long long q_off = 0;
+  if (lane < rows) {
+    const int flat = w.row0 + i * kTile + quarter * 32 + lane;
+    const int t = p.by_group.div(flat), head = w.kvh * p.group + flat - t * p.group;
+    q_off = (w.b < 0 ? t : w.b) * p.q_stride[0] + head * p.q_stride[1] +
+            (w.b < 0 ? 0 : t) * p.q_stride[2];
+  }
+  const char* q = static_cast<const char*>(p.q) + lane % kChunks * 16;
+  const uint32_t to = smem_u32(sh.q_tile) + i * Cfg::kTileBytes;
+#pragma unroll 4
+  for (int y = 0; y < 32; y += kPer) {
+    const int row = y + lane / kChunks;
+    const long long off = __shfl_sync(0xffffffffu, q_off, row);
+    if (row < rows && DA_IN(p, off + D - 1, p.q_elems))
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                       to + tc5::sw128(quarter * 32 + row, (lane % kChunks) * 8, kTile)),
+                   "l"(q + off * 2)
+                   : "memory");
+  }
+}
+// And its arrival for the MMAs.
+template <class Cfg>
+__device__ __forceinline__ void finish_q(const AttendShared<Cfg>& sh, const Item& w, int i,
+                                         int quarter) {
+  const bool alternate = alternates(w);
+  const int rows = (alternate ? w.rows : min(w.rows - i * kTile, kTile)) - quarter * 32;
+  if (rows <= 0 || (alternate && i == 1)) return;
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  fence_proxy_async_smem();
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) {
+    // the stream's first warp arrives for those without rows
+    const uint32_t arrivals = quarter == 0 ? 4 - (rows - 1) / 32 : 1;
+    mbar_arrive_n(sh.q_full(i), arrivals);
+  }
+}
+
+// ---- the softmax of stream i and the output: four warps
+template <class Cfg, bool WIDE_P>
+__device__ __forceinline__ void attend_softmax(const AttendParams& p, const AttendShared<Cfg>& sh) {
+  constexpr int D = Cfg::D;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int i = warp >> 2;                          // stream
+  const int quarter = warp & 3;
+  const int r = quarter * 32 + lane;                // row of the stream = TMEM lane
+  const uint32_t lanes = uint32_t(quarter * 32) << 16;
+  const uint32_t s_col = sh.tmem + i * 128 + lanes, o_col0 = sh.tmem + 256 + lanes;
+  const uint32_t o_col = o_col0 + i * D;
+  uint32_t tiles = 0;                               // of this stream: the parity of s_full
+  uint32_t met = 0;                                 // items of both streams on the same rows
+  if (!sh.wait_warp(p, sh.item_full(0), 0)) return;
+  if (sh.items[0].count >= 0) {
+    start_q<Cfg>(p, sh, sh.items[0], i, quarter);
+    finish_q<Cfg>(sh, sh.items[0], i, quarter);
+  }
+  uint32_t place = 0;                               // of the item's first load, not wrapped
+
+  for (int k = 0;; ++k) {
+    const Item& w = sh.items[k & 1];                // (its barrier was waited for with Q)
+    const int count = w.count;
+    if (count < 0) return;
+    const bool alternate = alternates(w), pre = w.b < 0;
+    const int first_row = w.row0 + (alternate ? 0 : i * kTile);
+    const int rows = alternate ? w.rows : min(w.rows - i * kTile, kTile);
+    // Warps without a query row stay out of the tiles (their rows of S, P and O are
+    // never looked at); the stream's first warp arrives for them.
+    const bool works = quarter * 32 < rows;
+    const uint32_t arrivals = quarter == 0 ? 4 - (rows - 1) / 32 : 1;
+    const bool valid = r < rows;
+    const int begin = w.begin, first = w.first, pt = w.pt;
+    // this row's position and where its output goes
+    int hi = -1, lo = 0;
+    long long out_off = 0;
+    if (valid) {
+      const int flat = first_row + r;
+      const int t = p.by_group.div(flat), head = w.kvh * p.group + flat - t * p.group;
+      hi = w.past + (pre ? 0 : t);
+      lo = pre || !p.window ? 0 : hi + 1 - p.window;
+      out_off = (pre ? t : w.b) * p.out_stride[0] + head * p.out_stride[1] +
+                (pre ? 0 : t) * p.out_stride[2];
+    }
+    float m_run = -INFINITY, l_run = 0.f;
+    const uint32_t tiles0 = tiles;
+    if (works) {
+      // Tiles from here on need the mask: rows past the stream's first query, and of the
+      // window's start up to its last query's.
+      const int hi_first = pre ? w.past : w.past + p.by_group.div(first_row);
+      const int lo_last =
+          pre || !p.window ? 0 : max(0, w.past + p.by_group.div(first_row + rows - 1) + 1 - p.window);
+      const int end = w.upto[i], step = alternate ? 2 : 1;
+      for (int j = alternate ? i : 0; j < end; j += step) {
+        // (warp-uniform: the TMEM accesses below are .sync.aligned)
+        if (!sh.wait_warp(p, sh.s_full(i), tiles & 1)) return;
+        tc5::fence_after();
+        const int r0 = (begin + j < pt ? begin + j : first + begin + j - pt) * kTile;
+        uint32_t raw[kTile];
+        float* s = reinterpret_cast<float*>(raw);
+#pragma unroll
+        for (int c = 0; c < kTile; c += 32) tmem_ld32(s_col + c, raw + c);
+        tc5::wait_ld();
+        if (r0 + kTile - 1 > hi_first || (r0 < lo_last && r0 + kTile > p.prefix)) {
+          const int hi_c = hi - r0, lo_c = lo - r0, pre_c = p.prefix - r0;
+#pragma unroll
+          for (int c = 0; c < kTile; ++c) {
+            const bool seen = c <= hi_c && (c >= lo_c || c < pre_c);
+            s[c] = seen ? s[c] : -INFINITY;
+          }
+        }
+        float m4[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+        for (int c = 4; c < 124; c += 8)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) m4[x] = fmaxf(fmaxf(m4[x], s[c + x]), s[c + 4 + x]);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) m4[x] = fmaxf(m4[x], s[124 + x]);
+        const float m_tile = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+        const bool over = m_tile > m_run + p.lazy || (m_run == -INFINITY && m_tile > -INFINITY);
+        if (__any_sync(0xffffffffu, over)) {
+          const float m_new = over ? m_tile : m_run;
+          const float alpha = over ? ex2((m_run - m_new) * p.scale_log2) : 1.f;  // 0 from -inf
+          m_run = m_new;
+          l_run *= alpha;
+          if (tiles != tiles0) {  // (S of this tile was issued behind the P.V of the last)
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+              uint32_t o[32];
+              tmem_ld32(o_col + c, o);
+              tc5::wait_ld();
+#pragma unroll
+              for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * alpha);
+              tmem_st32(o_col + c, o);
+            }
+          }
+        }
+        const float shift = m_run == -INFINITY ? 0.f : -m_run * p.scale_log2;
+        const uint64_t scale2 = pair_of(p.scale_log2, p.scale_log2), shift2 = pair_of(shift, shift);
+        uint64_t l2[2] = {0, 0};
+        // P over the first columns of S, which every lane of the warp has loaded.  Its first
+        // half goes to the MMAs while the second is computed: behind the third quarter, when
+        // its stores are done without a wait.
+        uint32_t hi_p[32], lo_p[WIDE_P ? 32 : 1];
+        auto quarter_of_p = [&](int c0) {
+#pragma unroll
+          for (int c = 0; c < 32; c += 2) {
+            float a, b;
+            halves_of(fma2(pair_of(s[c0 + c], s[c0 + c + 1]), scale2, shift2), a, b);
+            a = ex2(a);
+            b = ex2(b);
+            l2[(c >> 1) & 1] = add2(l2[(c >> 1) & 1], pair_of(a, b));
+            const int at = (c0 & 32) / 2 + c / 2;
+            hi_p[at] = pack_bf16x2(a, b);
+            if constexpr (WIDE_P)
+              lo_p[at] = pack_bf16x2(a - bf16_lo_to_f32(hi_p[at]), b - bf16_hi_to_f32(hi_p[at]));
+          }
+        };
+        auto store_half = [&](int h) {
+          tmem_st32(s_col + 32 * h, hi_p);
+          if constexpr (WIDE_P) tmem_st32(s_col + 64 + 32 * h, lo_p);
+        };
+        auto hand_over = [&](int h) {
+          tc5::wait_st();
+          tc5::fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_n(sh.p_full(i, h), arrivals);
+        };
+        quarter_of_p(0);
+        quarter_of_p(32);
+        store_half(0);
+        quarter_of_p(64);
+        hand_over(0);
+        quarter_of_p(96);
+        store_half(1);
+        hand_over(1);
+        float la, lb;
+        halves_of(add2(l2[0], l2[1]), la, lb);
+        l_run += la + lb;
+        ++tiles;
+      }
+    }
+    // (warps that stayed out count along)
+    const int own_tiles = alternate ? (count - i + 1) / 2 : w.upto[i];
+    tiles = tiles0 + own_tiles;
+    // Q of the next item, for its first scores to run under the end of this one
+    // (the stream's own score MMAs are complete; alternate: both streams' below; a warp that
+    // stayed out has not seen this item's Q arrive yet)
+    const bool early = works && !alternate;
+    if (!sh.wait_warp(p, sh.item_full(k + 1), ((k + 1) >> 1) & 1)) return;
+    const Item& next = sh.items[(k + 1) & 1];
+    if (early && next.count >= 0) start_q<Cfg>(p, sh, next, i, quarter);
+
+    place += 2 * count;
+    const int out_slot = int(place % Cfg::kSlots);
+    const uint32_t out_phase = (place / Cfg::kSlots) & 1;
+    ++place;
+    // ---- the rows' sums are final once the MMAs are
+    float* pairs = sh.pairs;
+    if (alternate) {
+      pairs[i * 2 * kTile + r] = m_run;
+      pairs[i * 2 * kTile + kTile + r] = l_run;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(sh.meet(0));
+      if (!sh.wait_warp(p, sh.meet(0), met & 1)) return;
+      if (!sh.wait_warp(p, sh.o_full(1 - i), k & 1)) return;
+    }
+    if (!sh.wait_warp(p, sh.o_full(i), k & 1)) return;
+    tc5::fence_after();
+    if (next.count >= 0) {
+      if (early) finish_q<Cfg>(sh, next, i, quarter);
+      else start_q<Cfg>(p, sh, next, i, quarter);
+    }
+    if (works) {
+      // Weights of the streams' O.  Alternate: of streams 0 and 1, and each stream's warps
+      // take a half of the columns.
+      float keep0 = 1.f, keep1 = 0.f;
+      if (alternate) {
+        const float m0 = pairs[r], m1 = pairs[2 * kTile + r];
+        m_run = fmaxf(m0, m1);
+        const float use = m_run == -INFINITY ? 0.f : m_run;
+        keep0 = ex2((m0 - use) * p.scale_log2);
+        keep1 = ex2((m1 - use) * p.scale_log2);
+        l_run = pairs[kTile + r] * keep0 + pairs[3 * kTile + r] * keep1;
+      }
+      const float inv = l_run > 0.f ? 1.f / l_run : (l_run == 0.f ? 0.f : l_run);
+      keep0 *= inv;
+      keep1 *= inv;
+      const bool part = w.slot >= 0, narrow = !part && p.out_bf16;
+      const long long part_row = (long long)w.slot * p.pitch + (alternate ? 0 : i * kTile) + r;
+      if (part) out_off = part_row * D;
+      const long long extent = part ? (long long)p.max_items * p.pitch * D : p.out_elems;
+      if (part && valid && !(alternate && i == 1) &&
+          DA_IN(p, part_row, (long long)p.max_items * p.pitch))
+        p.lse_part[part_row] =
+            l_run > 0.f ? m_run * p.scale_log2 + log2f(l_run) : (l_run == 0.f ? -INFINITY : l_run);
+      // Through the ring's place, D bytes of each of the warp's rows at a time, so that rows
+      // are written in runs of D bytes.
+      const bool there = own_tiles > 0 || (alternate && count > 0), both = alternate && count > 1;
+      const int c_begin = alternate ? i * (D / 2) : 0, c_end = alternate ? c_begin + D / 2 : D;
+      const int mine = min(rows - quarter * 32, 32);  // rows of this warp
+      const int cols = narrow ? D / 2 : D / 4;
+      char* base = static_cast<char*>(part ? static_cast<void*>(p.o_part) : p.out);
+      constexpr int kChunks = D / 16, kPer = 32 / kChunks;  // 16-byte pieces; rows at a time
+      if (!sh.wait_warp(p, sh.full(out_slot), out_phase)) return;
+      uint8_t* stage = sh.ring + out_slot * Cfg::kTileBytes + warp * (Cfg::kTileBytes / 8);
+#pragma unroll 1
+      for (int c = c_begin; c < c_end; c += cols) {
+#pragma unroll 2
+        for (int x = 0; x < cols; x += 16) {
+          float o[16];
+          if (there) {
+            tc5::ld16((alternate ? o_col0 : o_col) + c + x, o);
+            tc5::wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] *= keep0;
+            if (both) {
+              float o1[16];
+              tc5::ld16(o_col0 + D + c + x, o1);
+              tc5::wait_ld();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = fmaf(o1[e], keep1, o[e]);
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = 0.f;
+          }
+          auto put = [&](int chunk, uint32_t v0, uint32_t v1, uint32_t v2, uint32_t v3) {
+            *reinterpret_cast<uint4*>(stage + lane * D + ((chunk ^ (lane & (kChunks - 1))) << 4)) =
+                make_uint4(v0, v1, v2, v3);
+          };
+          if (narrow) {
+#pragma unroll
+            for (int e = 0; e < 16; e += 8)
+              put((x + e) / 8, pack_bf16x2(o[e], o[e + 1]), pack_bf16x2(o[e + 2], o[e + 3]),
+                  pack_bf16x2(o[e + 4], o[e + 5]), pack_bf16x2(o[e + 6], o[e + 7]));
+          } else {
+#pragma unroll
+            for (int e = 0; e < 16; e += 4)
+              put((x + e) / 4, __float_as_uint(o[e]), __float_as_uint(o[e + 1]),
+                  __float_as_uint(o[e + 2]), __float_as_uint(o[e + 3]));
+          }
+        }
+        __syncwarp();
+#pragma unroll 4
+        for (int y = 0; y < mine; y += kPer) {
+          const int row = y + lane / kChunks, ch = lane % kChunks;
+          const long long off = __shfl_sync(0xffffffffu, out_off, row & 31) + c;
+          const uint4 v =
+              *reinterpret_cast<const uint4*>(stage + row * D + ((ch ^ (row & (kChunks - 1))) << 4));
+          if (row < mine && DA_IN(p, off + cols - 1, extent))
+            *reinterpret_cast<uint4*>(base + off * (narrow ? 2 : 4) + ch * 16) = v;
+        }
+        __syncwarp();
+      }
+    }
+    if (!early && next.count >= 0) finish_q<Cfg>(sh, next, i, quarter);
+    fence_proxy_async_smem();  // the ring's next load there comes after these rows
+    tc5::fence_before();
+    __syncwarp();
+    if (lane == 0) {
+      if (alternate) {
+        mbar_arrive(sh.o_empty(0));
+        mbar_arrive(sh.o_empty(1));
+        mbar_arrive(sh.meet(1));
+      } else {
+        mbar_arrive_n(sh.o_empty(i), 2);
+      }
+      mbar_arrive(sh.out_done(out_slot));
+      mbar_arrive(sh.item_empty(k));
+    }
+    // both streams have read the shared sums
+    if (alternate && !sh.wait_warp(p, sh.meet(1), met++ & 1)) return;
+  }
+}
+
 template <class Cfg, bool WIDE_P>
 __global__ void __launch_bounds__(kAttendThreads, 1)
     attend_kernel(const __grid_constant__ AttendMaps maps, const AttendParams p) {
-  constexpr int D = Cfg::D;
-  constexpr int kSlots = Cfg::kSlots, kTileBytes = Cfg::kTileBytes, kHalfBytes = Cfg::kHalfBytes;
   constexpr uint32_t kTmemCols = 512;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  AttendShared<Cfg> sh;
+  sh.q_tile = smem;
+  sh.ring = smem + 2 * Cfg::kTileBytes;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sh.ring + size_t(Cfg::kSlots) * Cfg::kTileBytes);
+  sh.bars = smem_u32(bars);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + Cfg::kBars);
+  sh.abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  sh.pairs = reinterpret_cast<float*>(tmem_slot + 4);
+  sh.items = reinterpret_cast<Item*>(sh.pairs + 4 * kTile);
+  sh.own = sh.items + 2;
 
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~uintptr_t(1023));
-  uint8_t* q_tile = smem;                            // [2]
-  uint8_t* ring = smem + 2 * kTileBytes;             // [kSlots]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(ring + size_t(kSlots) * kTileBytes);
-  Item* item = reinterpret_cast<Item*>(bars + Cfg::kBars);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(item + 1);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-
-  const uint32_t q_full0 = smem_u32(bars);
-  const uint32_t full0 = q_full0 + 16;
-  const uint32_t empty0 = full0 + 8 * kSlots;
-  const uint32_t s_full0 = empty0 + 8 * kSlots;
-  const uint32_t p_full0 = s_full0 + 16;
-  const uint32_t o_full0 = p_full0 + 16;
-  const uint32_t edge0 = o_full0 + 16;
-  const uint32_t fin = edge0 + 8 * kEdges;
-
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
+    for (int s = 0; s < Cfg::kSlots; ++s) {
+      mbar_init(sh.full(s), 1);
+      mbar_init(sh.empty(s), 1);       // a tcgen05.commit
+      mbar_init(sh.out_done(s), 8);    // softmax warps
+    }
+    for (int e = 0; e < kEdges; ++e) mbar_init(sh.edge(e), 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(q_full0 + 8 * i, 4);  // the softmax warps of the stream (see `arrivals`)
-      mbar_init(s_full0 + 8 * i, 1);
-      mbar_init(p_full0 + 8 * i, 4);
-      mbar_init(o_full0 + 8 * i, 1);
+      mbar_init(sh.q_full(i), 4);      // softmax warps
+      mbar_init(sh.s_full(i), 1);
+      mbar_init(sh.p_full(i, 0), 4);
+      mbar_init(sh.p_full(i, 1), 4);
+      mbar_init(sh.o_full(i), 1);
+      mbar_init(sh.o_empty(i), 8);
+      mbar_init(sh.item_full(i), 1);
+      mbar_init(sh.item_empty(i), kItemReaders);
+      mbar_init(sh.meet(i), 8);
     }
-    for (int i = 0; i < kSlots; ++i) {
-      mbar_init(full0 + 8 * i, 1);
-      mbar_init(empty0 + 8 * i, 1);   // released by one tcgen05.commit
-    }
-    for (int i = 0; i < kEdges; ++i) mbar_init(edge0 + 8 * i, 1);
-    mbar_init(fin, 1);
-    *abort_flag = 0;
+    mbar_init(sh.fin(), 1);
+    *sh.abort_flag = 0;
     fence_mbar_init();
   }
   if (warp == 9) {
@@ -433,7 +1104,9 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
   tc5::fence_before();
   allow_dependent_launch();
   wait_for_prerequisite_grid();
-  const bool has = p.list ? list_item(p, reinterpret_cast<int*>(ring), item) : unit_item(p, item);
+  int own_count = 0;
+  if (p.list) own_count = list_items(p, reinterpret_cast<int*>(sh.ring), sh.own);
+  else __syncthreads();
   // lengths that were clamped are reported
   if (blockIdx.x == 0 && p.dev_error)
     for (int b = threadIdx.x; b < p.B; b += kAttendThreads) {
@@ -442,460 +1115,25 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
       if (bad_n || bad_m || (m > n && !p.shared)) flag_error(p.dev_error, DA_DEVERR_SEQ_LEN);
     }
   tc5::fence_after();
-  const uint32_t tmem = *tmem_slot;
-  if (!has) {
-    if (warp == 9) tc5::dealloc(tmem, kTmemCols);
-    return;
-  }
-  const int count = item->count;
-  const bool alternate = item->rows <= kTile;    // one set of rows, tiles dealt to the streams in turn
-  const int ahead = alternate ? 2 : 1;           // tiles whose scores are issued before the first P.V
-  auto give_up = [&] {
-    if (!*abort_flag) {
-      *abort_flag = 1;
-      flag_error(p.dev_error, DA_DEVERR_TIMEOUT);
-    }
-  };
+  sh.tmem = *tmem_slot;
 
   // Registers: 168 a thread at launch for each of three warpgroups; 2 * 208 + 88 then.
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-    // ---------------------------------------------------------------- producer
     if (warp == 8) {
-      if (lane == 0) {
-        const bool pre = item->b < 0;
-        const uint64_t policy = p.single_read || (pre && p.prefix_tiles == 1)
-                                    ? l2_policy_evict_first()
-                                    : l2_policy_evict_normal();
-        const CUtensorMap* mk = pre ? &maps.k_prefix : &maps.k;
-        const CUtensorMap* mv = pre ? &maps.v_prefix : &maps.v;
-        const int z = pre ? item->kvh : (p.b_offset + item->b) * p.h_kv + item->kvh;
-        const uint32_t ring0 = smem_u32(ring);
-        RingPlace<kSlots> at;
-        uint32_t issued = 0, parity = 0;  // per slot: loaded at all, phase of its newest load
-        int edges = 0;
-        bool ok = true;
-        auto load = [&](const CUtensorMap* map, int j) {
-          if (!ok) return;
-          if (!mbar_wait_bounded(empty0 + 8 * at.slot, at.phase ^ 1u, abort_flag)) {
-            give_up();
-            ok = false;
-            return;
-          }
-#ifdef DA_TEST_HOOKS
-          if (int(blockIdx.x) == p.withhold_cta && map == mv && j == count - 1) return;
-#endif
-          const uint32_t dst = ring0 + at.slot * kTileBytes;
-          const int y = tile_row(*item, item->begin + j);
-          // a V tile with rows to clear goes to warp 10 first, which says when it is full
-          const bool edge = map == mv && edges < kEdges && edge_tile(p, *item, y);
-          const uint32_t bar = edge ? edge0 + 8 * edges++ : full0 + 8 * at.slot;
-          mbar_arrive_expect_tx(bar, kTileBytes);
-#pragma unroll
-          for (int c = 0; c < D; c += 64)
-            tma_load_3d(dst + (c / 64) * kHalfBytes, map, c, y, z, bar, policy);
-          issued = edge ? issued & ~(1u << at.slot) : issued | 1u << at.slot;
-          parity = (parity & ~(1u << at.slot)) | (at.phase << at.slot);
-          at.next();
-        };
-        // loads follow their use: K of the first `ahead` tiles, then V_j and K_(j + ahead)
-        for (int j = 0; j < min(ahead, count); ++j) load(mk, j);
-        for (int j = 0; j < count; ++j) {
-          load(mv, j);
-          if (j + ahead < count) load(mk, j + ahead);
-        }
-        if (!ok) {  // copies in flight land before the CTA ends
-          volatile int never = 0;
-          for (int i = 0; i < kSlots; ++i)
-            if (issued >> i & 1) mbar_wait_bounded(full0 + 8 * i, (parity >> i) & 1, &never);
-          for (int i = 0; i < edges; ++i) mbar_wait_bounded(edge0 + 8 * i, 0, &never);
-        }
-      }
-      return;
-    }
-    // ---------------------------------------------------------------- MMA issuer
-    if (warp == 9) {
-      if (lane == 0) {
-        const uint32_t idesc_s = tc5::idesc_bf16(128, 128, 0, 0);
-        const uint32_t idesc_o = tc5::idesc_bf16(128, D, 0, 1);
-        // descriptors of the operands' first bytes; their addresses count 16 bytes
-        const uint64_t k_major = tc5::sdesc(0, 16, 1024), mn_major = tc5::sdesc(0, kHalfBytes, 1024);
-        const uint32_t q_at = smem_u32(q_tile) >> 4, ring_at = smem_u32(ring) >> 4;
-        const int upto0 = item->upto[0], upto1 = item->upto[1];
-        bool ok = true, any = false;
-        uint32_t p_phase = 0;                     // a bit for each stream
-        uint32_t started = 0;                     // streams with a P.V issued
-        RingPlace<kSlots> at;
-        auto wait = [&](uint32_t bar, uint32_t parity) {
-          if (ok && !mbar_wait_bounded(bar, parity, abort_flag)) {
-            give_up();
-            ok = false;
-          }
-          return ok;
-        };
-        auto scores = [&](int i, int slot) {  // S_i = Q_i K^T
-          tc5::fence_after();
-          const uint64_t a = k_major + q_at + (alternate ? 0 : i * (kTileBytes >> 4));
-          const uint64_t b = k_major + ring_at + slot * (kTileBytes >> 4);
-#pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks) {
-            const uint32_t off = ((ks >> 2) * kHalfBytes + (ks & 3) * 32) >> 4;
-            tc5::mma(tmem + i * 128, a + off, b + off, idesc_s, ks > 0);
-          }
-          tc5::commit(s_full0 + 8 * i);
-          any = true;
-        };
-        if (count > 0 && wait(q_full0, 0) && !alternate) wait(q_full0 + 8, 0);
-        for (int j = 0; j < min(ahead, count) && ok; ++j) {
-          if (!wait(full0 + 8 * at.slot, at.phase)) break;
-          if (alternate) {
-            scores(j, at.slot);
-          } else {
-            if (j < upto0) scores(0, at.slot);
-            if (j < upto1) scores(1, at.slot);
-          }
-          tc5::commit(empty0 + 8 * at.slot);
-          at.next();
-        }
-        for (int j = 0; j < count && ok; ++j) {
-          const RingPlace<kSlots> v = at;         // V_j
-          at.next();
-          const bool more = j + ahead < count;
-          if (!wait(full0 + 8 * v.slot, v.phase)) break;
-          bool k_here = false;
-          const int i_end = alternate ? (j & 1) + 1 : 2;
-          for (int i = alternate ? j & 1 : 0; i < i_end; ++i) {
-            const int mine = alternate ? count : i == 0 ? upto0 : upto1;
-            if (j < mine) {
-              if (!wait(p_full0 + 8 * i, (p_phase >> i) & 1)) break;
-              p_phase ^= 1u << i;
-              tc5::fence_after();
-              const uint64_t b = mn_major + ring_at + v.slot * (kTileBytes >> 4);
-              const uint32_t o = tmem + 256 + i * D, pa = tmem + i * 128;
-              const bool more_o = (started >> i) & 1;
-#pragma unroll
-              for (int ks = 0; ks < kTile / 16; ++ks)
-                mma_tmem_a(o, pa + ks * 8, b + ks * (16 * 128 >> 4), idesc_o, more_o || ks > 0);
-              if constexpr (WIDE_P) {
-#pragma unroll
-                for (int ks = 0; ks < kTile / 16; ++ks)
-                  mma_tmem_a(o, pa + 64 + ks * 8, b + ks * (16 * 128 >> 4), idesc_o, 1);
-              }
-              started |= 1u << i;
-            }
-            if (j + ahead < mine) {
-              if (!k_here && !wait(full0 + 8 * at.slot, at.phase)) break;
-              k_here = true;
-              scores(i, at.slot);
-            }
-          }
-          if (!ok) break;
-          tc5::commit(empty0 + 8 * v.slot);
-          if (more) {
-            tc5::commit(empty0 + 8 * at.slot);
-            at.next();
-          }
-        }
-        if (ok && any) {
-          tc5::commit(o_full0);
-          tc5::commit(o_full0 + 8);
-        }
-        // every MMA has completed before TMEM is freed
-        if (any) tc5::commit(fin);
-        else mbar_arrive(fin);
-        volatile int never = 0;
-        mbar_wait_bounded(fin, 0, &never);
-      }
-      __syncwarp();
+      if (lane == 0) attend_load<Cfg>(p, maps, sh, own_count);
+    } else if (warp == 9) {
+      attend_mma<Cfg, WIDE_P>(p, sh);
       named_bar_sync(2, 288);
       tc5::fence_after();
-      tc5::dealloc(tmem, kTmemCols);
-      return;
-    }
-    // ---------------------------------------------------------------- clearing V
-    if (warp == 10) {
-      int edges = 0;
-      for (int j = 0; j < count && edges < kEdges; ++j) {
-        const int r0 = tile_row(*item, item->begin + j);
-        if (!edge_tile(p, *item, r0)) continue;
-        const bool got = mbar_wait_bounded(edge0 + 8 * edges++, 0, abort_flag);
-        if (!got) give_up();
-        if (!__all_sync(0xffffffffu, got)) break;
-        const int slot = (j + min(count, ahead + j)) % kSlots;  // V_j in the order of the loads
-        uint8_t* vt = ring + size_t(slot) * kTileBytes;
-        const int seen_end = item->n, clear_lo = item->clear_lo;
-        constexpr int kChunks = D / 8;  // 16-byte pieces of a row
-#pragma unroll 8
-        for (int x = lane; x < kTile * kChunks; x += 32) {
-          const int row = r0 + x / kChunks;
-          if (row >= seen_end || (row < clear_lo && row >= p.prefix))
-            *reinterpret_cast<uint4*>(vt + tc5::sw128(x / kChunks, (x % kChunks) * 8, kTile)) =
-                make_uint4(0, 0, 0, 0);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(full0 + 8 * slot);
-      }
+      tc5::dealloc(sh.tmem, kTmemCols);
+    } else if (warp == 10) {
+      attend_clear<Cfg>(p, sh);
     }
     return;
   }
-
-  // ------------------------------------------------------------------ softmax
   asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-  const int i = warp >> 2;                          // stream
-  const int quarter = warp & 3;
-  const int r = quarter * 32 + lane;                // row of the stream = TMEM lane
-  const uint32_t lanes = uint32_t(quarter * 32) << 16;
-  const uint32_t s_col = tmem + i * 128 + lanes, o_col = tmem + 256 + i * D + lanes;
-  const int rows = alternate ? item->rows : min(item->rows - i * kTile, kTile);
-  // Warps without a query row stay out (their rows of S, P and O are never
-  // looked at); the stream's first warp arrives for them.
-  const bool works = quarter * 32 < rows;
-  const uint32_t arrivals = quarter == 0 ? 4 - (rows - 1) / 32 : 1;
-  const bool valid = r < rows;
-  const int unit_row = (alternate ? 0 : i * kTile) + r;
-  // this row's token, head and position
-  int hi = -1, lo = 0;
-  long long out_off = 0;
-  bool live = works;
-  float m_run = -INFINITY, l_run = 0.f;
-  int done = 0;  // tiles of this stream
-  if (works) {
-    const bool pre = item->b < 0;
-    long long q_off = 0;
-    if (valid) {
-      const int flat = item->row0 + unit_row;
-      const int t = p.by_group.div(flat), head = item->kvh * p.group + flat - t * p.group;
-      const int b = pre ? t : item->b, tok = pre ? 0 : t;
-      hi = item->past + tok;
-      lo = pre || !p.window ? 0 : hi + 1 - p.window;
-      q_off = b * p.q_stride[0] + head * p.q_stride[1] + tok * p.q_stride[2];
-      out_off = b * p.out_stride[0] + head * p.out_stride[1] + tok * p.out_stride[2];
-    }
-    if (!(alternate && i == 1)) {
-      // Q of the warp's rows, swizzled K-major
-      constexpr int kChunks = D / 8, kPer = 32 / kChunks;  // 16-byte pieces of a row; rows at a time
-      uint4 v[32 / kPer];
-      const uint4* q = static_cast<const uint4*>(p.q);
-#pragma unroll
-      for (int k = 0; k < 32 / kPer; ++k) {
-        const int row = k * kPer + lane / kChunks;
-        const long long off = __shfl_sync(0xffffffffu, q_off, row);
-        const bool in = quarter * 32 + row < rows && DA_IN(p, off + D - 1, p.q_elems);
-        v[k] = in ? q[off / 8 + lane % kChunks] : make_uint4(0, 0, 0, 0);
-      }
-      const uint32_t flip = p.q_flip == 1 ? 0x80008000u : 0u, keep = p.q_flip == 2 ? 0u : ~0u;
-#pragma unroll
-      for (int k = 0; k < 32 / kPer; ++k) {
-        const int row = quarter * 32 + k * kPer + lane / kChunks;
-        *reinterpret_cast<uint4*>(q_tile + i * kTileBytes + tc5::sw128(row, (lane % kChunks) * 8, kTile)) =
-            make_uint4((v[k].x ^ flip) & keep, (v[k].y ^ flip) & keep, (v[k].z ^ flip) & keep,
-                       (v[k].w ^ flip) & keep);
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_n(q_full0 + 8 * i, arrivals);
-    }
-    // Tiles from here on need the mask: rows past the stream's first query, and of the
-    // window's start up to its last query's.
-    const int row_last = item->row0 + (alternate ? 0 : i * kTile) + rows - 1;
-    const int row_first = item->row0 + (alternate ? 0 : i * kTile);
-    const int hi_first = pre ? item->past : item->past + p.by_group.div(row_first);
-    const int lo_last =
-        pre || !p.window ? 0 : max(0, item->past + p.by_group.div(row_last) + 1 - p.window);
-
-    const int end = item->upto[i], step = alternate ? 2 : 1;
-    for (int j = alternate ? i : 0; j < end; j += step) {
-      const bool got = mbar_wait_bounded(s_full0 + 8 * i, done & 1, abort_flag);
-      if (!got) give_up();
-      live = __all_sync(0xffffffffu, got);  // warp-uniform: the TMEM accesses are .sync.aligned
-      if (!live) break;
-      tc5::fence_after();
-      uint32_t raw[128];
-      float* s = reinterpret_cast<float*>(raw);
-#pragma unroll
-      for (int c = 0; c < 128; c += 32) tmem_ld32(s_col + c, raw + c);
-      const int r0 = tile_row(*item, item->begin + j);
-      tc5::wait_ld();
-      if (r0 + kTile - 1 > hi_first || (r0 < lo_last && r0 + kTile > p.prefix)) {
-        const int hi_c = hi - r0, lo_c = lo - r0, pre_c = p.prefix - r0;
-#pragma unroll
-        for (int c = 0; c < 128; ++c) {
-          const bool seen = c <= hi_c && (c >= lo_c || c < pre_c);
-          s[c] = seen ? s[c] : -INFINITY;
-        }
-      }
-      float m4[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-      for (int c = 4; c < 124; c += 8)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) m4[k] = fmaxf(fmaxf(m4[k], s[c + k]), s[c + 4 + k]);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) m4[k] = fmaxf(m4[k], s[124 + k]);
-      const float m_tile = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-      const bool over = m_tile > m_run + p.lazy || (m_run == -INFINITY && m_tile > -INFINITY);
-      if (__any_sync(0xffffffffu, over)) {
-        const float m_new = over ? m_tile : m_run;
-        const float alpha = over ? ex2((m_run - m_new) * p.scale_log2) : 1.f;  // 0 from -inf
-        m_run = m_new;
-        l_run *= alpha;
-        if (done > 0) {  // (S of this tile was issued behind the P.V of the last)
-#pragma unroll 1
-          for (int c = 0; c < D; c += 32) {
-            uint32_t o[32];
-            tmem_ld32(o_col + c, o);
-            tc5::wait_ld();
-#pragma unroll
-            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
-            tmem_st32(o_col + c, o);
-          }
-        }
-      }
-      const float shift = m_run == -INFINITY ? 0.f : -m_run * p.scale_log2;
-      const uint64_t scale2 = pair_of(p.scale_log2, p.scale_log2), shift2 = pair_of(shift, shift);
-      uint64_t l2[2] = {0, 0};
-      // exponentials in halves of 64 columns; P over the first columns of S, which
-      // every lane of the warp has loaded
-#pragma unroll
-      for (int h = 0; h < 128; h += 64) {
-        uint32_t hi_p[32];
-#pragma unroll
-        for (int c = 0; c < 64; c += 2) {
-          float a, b;
-          halves_of(fma2(pair_of(s[h + c], s[h + c + 1]), scale2, shift2), a, b);
-          a = ex2(a);
-          b = ex2(b);
-          l2[(c >> 1) & 1] = add2(l2[(c >> 1) & 1], pair_of(a, b));
-          hi_p[c / 2] = pack_bf16x2(a, b);
-          if constexpr (WIDE_P) {
-            s[h + c] = a - bf16_lo_to_f32(hi_p[c / 2]);
-            s[h + c + 1] = b - bf16_hi_to_f32(hi_p[c / 2]);
-          }
-        }
-        tmem_st32(s_col + h / 2, hi_p);
-        if constexpr (WIDE_P) {
-          uint32_t lo_p[32];
-#pragma unroll
-          for (int c = 0; c < 64; c += 2) lo_p[c / 2] = pack_bf16x2(s[h + c], s[h + c + 1]);
-          tmem_st32(s_col + 64 + h / 2, lo_p);
-        }
-      }
-      float la, lb;
-      halves_of(add2(l2[0], l2[1]), la, lb);
-      l_run += la + lb;
-      tc5::wait_st();
-      tc5::fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_n(p_full0 + 8 * i, arrivals);
-      ++done;
-    }
-  }
-
-  // ---- the unit's rows are final once both streams' MMAs are
-  if (live && count > 0) {
-    bool got = mbar_wait_bounded(o_full0, 0, abort_flag);
-    got = mbar_wait_bounded(o_full0 + 8, 0, abort_flag) && got;
-    if (!got) give_up();
-    live = __all_sync(0xffffffffu, got);
-    tc5::fence_after();
-  }
-  // (a CTA whose wait ran out writes nothing)
-  float* other = reinterpret_cast<float*>(ring);  // alternate: O^T [D][128], m [128], l [128] of stream 1
-  const bool with_other = alternate && count > 1;
-  if (with_other) {
-    if (i == 1 && live) {
-#pragma unroll 2
-      for (int c = 0; c < D; c += 32) {
-        uint32_t o[32];
-        tmem_ld32(o_col + c, o);
-        tc5::wait_ld();
-#pragma unroll
-        for (int k = 0; k < 32; ++k) other[(c + k) * kTile + r] = __uint_as_float(o[k]);
-      }
-      other[D * kTile + r] = m_run;
-      other[D * kTile + kTile + r] = l_run;
-    }
-    named_bar_sync(1, 256);
-    if (*abort_flag) live = false;
-    live = __all_sync(0xffffffffu, live);
-  }
-  if (live && !(alternate && i == 1)) {
-    float keep0 = 1.f, keep1 = 0.f;  // weights of the two streams' O
-    if (with_other) {
-      const float m1 = other[D * kTile + r], l1 = other[D * kTile + kTile + r];
-      const float m = fmaxf(m_run, m1), m_use = m == -INFINITY ? 0.f : m;
-      keep0 = ex2((m_run - m_use) * p.scale_log2);
-      keep1 = ex2((m1 - m_use) * p.scale_log2);
-      l_run = l_run * keep0 + l1 * keep1;
-      m_run = m;
-    }
-    const float inv = l_run > 0.f ? 1.f / l_run : (l_run == 0.f ? 0.f : l_run);
-    keep0 *= inv;
-    keep1 *= inv;
-    const bool part = item->slot >= 0;
-    const long long part_row = (long long)item->slot * p.pitch + unit_row;
-    if (part) out_off = part_row * D;
-    const long long extent = part ? (long long)p.max_items * p.pitch * D : p.out_elems;
-    if (part && valid && DA_IN(p, part_row, (long long)p.max_items * p.pitch))
-      p.lse_part[part_row] =
-          l_run > 0.f ? m_run * p.scale_log2 + log2f(l_run) : (l_run == 0.f ? -INFINITY : l_run);
-    const bool narrow = !part && p.out_bf16;
-    uint8_t* stage = q_tile + i * kTileBytes + quarter * (kTileBytes / 4);  // 32 rows of 2 D bytes
-    constexpr int kChunks = D / 8, kPer = 32 / kChunks;
-    const int mine = min(rows - quarter * 32, 32);  // rows of this warp
-    // a row of 2 D bytes at a time (D bf16 or D / 2 floats) through shared memory,
-    // so that whole rows are written
-    const int cols = narrow ? D : D / 2;
-#pragma unroll 1
-    for (int c0 = 0; c0 < D; c0 += cols) {
-#pragma unroll 2
-      for (int c = 0; c < cols; c += 32) {
-        uint32_t o[32];
-        if (done > 0) {
-          tmem_ld32(o_col + c0 + c, o);
-          tc5::wait_ld();
-        } else {
-#pragma unroll
-          for (int k = 0; k < 32; ++k) o[k] = 0;
-        }
-#pragma unroll
-        for (int k = 0; k < 32; ++k) {
-          float x = __uint_as_float(o[k]) * keep0;
-          if (with_other) x = fmaf(other[(c0 + c + k) * kTile + r], keep1, x);
-          o[k] = __float_as_uint(x);
-        }
-        if (narrow) {
-#pragma unroll
-          for (int k = 0; k < 32; k += 8) {
-            const float* f = reinterpret_cast<const float*>(o) + k;
-            *reinterpret_cast<uint4*>(stage + lane * 2 * D + ((((c + k) / 8) ^ (lane & 7)) << 4)) =
-                make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
-                           pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
-          }
-        } else {
-#pragma unroll
-          for (int k = 0; k < 32; k += 4)
-            *reinterpret_cast<uint4*>(stage + lane * 2 * D + ((((c + k) / 4) ^ (lane & 7)) << 4)) =
-                make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
-        }
-      }
-      __syncwarp();
-#pragma unroll 4
-      for (int k = 0; k < mine; k += kPer) {
-        const int row = k + lane / kChunks, ch = lane % kChunks;
-        const long long off = __shfl_sync(0xffffffffu, out_off, row);
-        const uint4 v = *reinterpret_cast<const uint4*>(stage + row * 2 * D + ((ch ^ (row & 7)) << 4));
-        if (row < mine && DA_IN(p, off + D - 1, extent)) {
-          if (narrow)
-            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + off + ch * 8) = v;
-          else
-            *reinterpret_cast<uint4*>((part ? p.o_part : static_cast<float*>(p.out)) + off + c0 +
-                                      ch * 4) = v;
-        }
-      }
-      __syncwarp();
-    }
-  }
+  attend_softmax<Cfg, WIDE_P>(p, sh);
   tc5::fence_before();
   named_bar_sync(2, 288);
 }

@@ -422,8 +422,9 @@ struct AttendParams {
   int window, prefix;            // 0: unlimited; rows always seen
   int shared, P;                 // shared prefix: on, its rows
   int out_bf16;
-  int q_flip;                    // 1: q times -1 (negative scale), 2: q times 0 (scale 0)
-  float scale_log2;              // |scale| * log2 e, 1 for scale 0
+  int negate;                    // q times -1 (negative scale)
+  float scale_log2;              // |scale| * log2 e; at least float's smallest normal number, so
+                                 // that a masked -inf stays one
   float lazy;                    // 8 / scale_log2: a maximum may lag by 2^8
   int single_read;               // each K and V row is read by one CTA: no use in keeping it in L2
   // Units: (row tile of 256 query rows, KV head, sequence). list != 0: units are cut into items of
@@ -444,6 +445,7 @@ struct AttendMaps {
 };
 constexpr int kAttendEntries = 1024;  // entries of a list (shared memory of the schedule)
 constexpr int kAttendRows = 256;      // query rows of a unit
+constexpr int kAttendOwn = 8;         // items of a CTA with a list, at most
 cudaError_t launch_attend(const AttendParams& p, const AttendMaps& m, int d, int grid,
                           cudaStream_t stream);
 cudaError_t launch_attend_combine(const AttendParams& p, int d, cudaStream_t stream);
