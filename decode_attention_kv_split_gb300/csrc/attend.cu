@@ -385,6 +385,11 @@ __device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t n) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(n) : "memory");
 }
 
+// Bits 0 .. n - 1, for any n.
+__device__ __forceinline__ uint32_t bits_below(int n) {
+  return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u;
+}
+
 // Two floats at a time.
 __device__ __forceinline__ uint64_t pair_of(float lo, float hi) {
   uint64_t r;
@@ -840,9 +845,12 @@ __device__ __forceinline__ void attend_softmax(const AttendParams& p, const Atte
         if (r0 + kTile - 1 > hi_first || (r0 < lo_last && r0 + kTile > p.prefix)) {
           const int hi_c = hi - r0, lo_c = lo - r0, pre_c = p.prefix - r0;
 #pragma unroll
-          for (int c = 0; c < kTile; ++c) {
-            const bool seen = c <= hi_c && (c >= lo_c || c < pre_c);
-            s[c] = seen ? s[c] : -INFINITY;
+          for (int c0 = 0; c0 < kTile; c0 += 32) {
+            // a bit for each column that the row sees
+            const uint32_t seen = bits_below(hi_c + 1 - c0) &
+                                  (~bits_below(lo_c - c0) | bits_below(pre_c - c0));
+#pragma unroll
+            for (int c = 0; c < 32; ++c) s[c0 + c] = seen >> c & 1 ? s[c0 + c] : -INFINITY;
           }
         }
         float m4[4] = {s[0], s[1], s[2], s[3]};
