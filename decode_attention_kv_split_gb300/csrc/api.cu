@@ -1167,11 +1167,11 @@ namespace {
 // The launches of chunk_attn and decode_attn_shared.
 struct AttendPlan {
   int slice;                 // sequences per launch
-  int q_tiles, prefix_tiles, entries, pitch, list;
-  long long units, max_items;
-  size_t table_bytes, part_rows;
+  int q_tiles, prefix_tiles, list, ctas, pitch, unit_rows;
+  long long units, part_rows, own_parts;
+  size_t table_bytes;
   size_t bytes(int d) const {
-    return list ? table_bytes + part_rows * (size_t(d) + 1) * 4 : 0;
+    return list ? table_bytes + size_t(part_rows) * (size_t(d) + 1) * 4 : 0;
   }
 };
 
@@ -1202,20 +1202,29 @@ int plan_attend(int B, int T, int h_q, int h_kv, int d, int n_max, int dtype, in
   a.units = ((long long)a.slice * a.q_tiles + a.prefix_tiles) * h_kv;
   if (a.units > 0x7fffffffLL - 2 * sms) return DA_ERR_SHAPE;
   const long long entries = (long long)a.slice * a.q_tiles + (P >= 0 ? 1 : 0);
-  // Cut and merged behind a prefix (its units and a sequence's own are merged anyway), and in a
-  // chunk when there are few units of more than a few tiles.
+  // Cut into equal pieces, one per CTA, and merged: behind a prefix (whose partials are merged with a
+  // sequence's own anyway), and a chunk's units of more than 8 tiles (below, one CTA a unit takes
+  // less time than the second launch: 300 rows, 9 us against 13).  Of very many units (32 a CTA)
+  // whole ones even out by themselves.
   const int most_tiles = (n_max + 127) / 128, prefix_most = P > 0 ? (P + 127) / 128 : 0;
-  a.list = P >= 0 || (a.units < 4LL * sms && most_tiles > 8 && entries <= da::kAttendEntries);
-  a.entries = a.list ? int(entries) : 0;
-  const long long tallest = P >= 0 ? a.slice * g : rows;
-  a.pitch = int(tallest < da::kAttendRows ? tallest : da::kAttendRows);
-  // An item of a list has two tiles at least where its unit was cut, and half an even share of
-  // the launch's: at most a cut for each pair of tiles, and 2 * sms in all.
-  const long long cuts = (long long)a.slice * a.q_tiles * h_kv * ((most_tiles + 1) / 2) +
-                         (long long)a.prefix_tiles * h_kv * ((prefix_most + 1) / 2);
-  a.max_items = !a.list ? a.units : cuts < a.units + 2 * sms ? cuts : a.units + 2 * sms;
-  a.table_bytes = (size_t(a.entries) * 8 + 255) & ~size_t(255);
-  a.part_rows = size_t(a.max_items) * a.pitch;
+  a.list = P >= 0 || (a.units < 32LL * sms && most_tiles > 8 && entries <= da::kAttendEntries);
+  a.pitch = int((P >= 0 ? a.slice * g : rows) < da::kAttendRows ? (P >= 0 ? a.slice * g : rows)
+                                                                 : da::kAttendRows);
+  a.unit_rows = int(rows < da::kAttendRows ? rows : da::kAttendRows);
+  // a CTA per SM, but no more than pairs of tiles
+  const long long pairs = (long long)a.slice * a.q_tiles * h_kv * ((most_tiles + 1) / 2) +
+                          (long long)a.prefix_tiles * h_kv * ((prefix_most + 1) / 2);
+  a.ctas = int(!a.list ? (a.units < sms ? a.units : sms) : (pairs < sms ? pairs : sms));
+  if (P >= 0) {
+    // a partial for each CTA of a unit; one number per unit and CTA, prefix units first
+    const long long pre_units = (long long)a.prefix_tiles * h_kv;
+    a.own_parts = (pre_units + a.ctas) * a.pitch;
+    a.part_rows = a.own_parts + (a.units - pre_units + a.ctas) * a.unit_rows;
+    if (a.part_rows > 0x7fffffffLL) return DA_ERR_SHAPE;
+  } else {
+    a.part_rows = 2LL * a.ctas * a.pitch;  // the first and the last unit of each CTA
+  }
+  a.table_bytes = ((size_t(a.ctas) * 16 + (P >= 0 ? size_t(a.units) * 8 : 0)) + 255) & ~size_t(255);
   *plan = a;
   return DA_OK;
 }
@@ -1301,14 +1310,14 @@ int run_attend(const AttendCall& c, void* workspace, size_t workspace_bytes, int
   p.scale_log2 = scale_log2 < 1.2e-38 ? 1.2e-38f : float(scale_log2);
   p.lazy = float(8.0 / double(p.scale_log2));
   p.single_read = plan.q_tiles == 1;
-  p.list = plan.list, p.q_tiles = plan.q_tiles, p.sms = sms;
-  p.max_items = int(plan.max_items), p.pitch = plan.pitch;
-  const long long own = (long long)c.T * p.group;
-  p.unit_rows = int(own < da::kAttendRows ? own : da::kAttendRows);
+  p.list = plan.list, p.q_tiles = plan.q_tiles, p.ctas = plan.ctas;
+  p.pitch = plan.pitch, p.unit_rows = plan.unit_rows, p.own_parts = int(plan.own_parts);
+  p.part_rows = plan.part_rows;
   p.by_group = da::FastDiv(uint32_t(p.group));
   if (plan.list) {
     char* ws = static_cast<char*>(workspace);
-    p.table = reinterpret_cast<int2*>(ws);
+    p.cta_start = reinterpret_cast<int4*>(ws);
+    p.unit_ctas = reinterpret_cast<int2*>(ws + size_t(plan.ctas) * 16);
     p.o_part = reinterpret_cast<float*>(ws + plan.table_bytes);
     p.lse_part = p.o_part + plan.part_rows * c.d;
   }
@@ -1325,16 +1334,10 @@ int run_attend(const AttendCall& c, void* workspace, size_t workspace_bytes, int
     p.n_new = c.n_new ? c.n_new + b0 : nullptr;
     p.prefix_tiles = shared ? (p.B * p.group + da::kAttendRows - 1) / da::kAttendRows : 0;
     p.entries = p.list ? p.B * p.q_tiles + p.shared : 0;
-    const long long units = ((long long)p.B * p.q_tiles + p.prefix_tiles) * p.h_kv;
-    // a CTA per SM; more where a list gives one more than it can note
-    long long grid = p.list ? plan.max_items : units;
-    if (grid > sms) grid = sms;
-    if (p.list && grid * da::kAttendOwn < plan.max_items)
-      grid = (plan.max_items + da::kAttendOwn - 1) / da::kAttendOwn;
-    cudaError_t e = da::launch_attend(p, maps, c.d, int(grid), stream);
+    cudaError_t e = da::launch_attend(p, maps, c.d, p.ctas, stream);
     if (e != cudaSuccess) return fail_cuda(e, "attend launch");
     g_launches.fetch_add(1);
-    if (p.list) {
+    if (p.list && (p.shared || p.ctas > 1)) {
       e = da::launch_attend_combine(p, c.d, stream);
       if (e != cudaSuccess) return fail_cuda(e, "attend combine launch");
       g_launches.fetch_add(1);

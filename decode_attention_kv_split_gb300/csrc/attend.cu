@@ -40,7 +40,6 @@ constexpr int kTile = 128;              // K and V rows of a tile, query rows of
 constexpr int kAttendThreads = 384;
 constexpr int kScheduleThreads = 256;
 constexpr int kEdges = 8;               // more than the V tiles that the ring can hold
-constexpr int kOwnItems = kAttendOwn;
 
 template <int D_>
 struct AttendCfg {
@@ -52,10 +51,8 @@ struct AttendCfg {
   // p_full[2], o_full, o_empty; item_full[2], item_empty[2], meet[2], fin
   static constexpr int kBars = 3 * kSlots + kEdges + 2 * 6 + 2 + 2 + 2 + 1;
   static constexpr size_t kSmemBytes = size_t(2 + kSlots) * kTileBytes + kBars * 8 +
-                                       (kOwnItems + 2) * 60 + 16 + 4 * kTile * 4;
+                                       2 * 60 + 64 + 4 * kTile * 4;
   static_assert(kSmemBytes <= 227 * 1024, "shared memory");
-  // the schedule's scratch lies in the ring before the first load
-  static_assert((kAttendEntries + 64) * 4 <= kTileBytes, "schedule scratch");
   static_assert(kEdges > (kSlots + 1) / 2, "edge barriers");
 };
 
@@ -71,7 +68,7 @@ struct Item {
   int begin, count;  // this item's list tiles
   int upto[2];       // tiles of it that each stream takes (from the first on)
   int clear_lo;      // rows of [prefix, clear_lo) and from n on are seen by no query of the sequence
-  int slot;          // partial, or -1: the unit's only item writes the output
+  int part;          // first row of its partial, or -1: the unit's only item writes the output
 };
 static_assert(sizeof(Item) <= 60, "shared memory of the items");
 
@@ -118,11 +115,11 @@ __device__ __forceinline__ void seq_unit(const AttendParams& p, int n, int m, in
 }
 
 // The rest of an item, tiles [begin, end) of its unit.
-__device__ __forceinline__ void cut_item(const AttendParams& p, int begin, int end, int slot,
+__device__ __forceinline__ void cut_item(const AttendParams& p, int begin, int end, int part,
                                          Item& w) {
   w.begin = begin;
   w.count = end - begin;
-  w.slot = slot;
+  w.part = part;
   w.clear_lo = w.b >= 0 && p.window ? max(0, w.past + 1 - p.window) : 0;
   w.upto[0] = w.upto[1] = w.count;
   if (w.b >= 0 && w.rows > kTile) {  // stream 0 ends at its last query's row
@@ -132,8 +129,18 @@ __device__ __forceinline__ void cut_item(const AttendParams& p, int begin, int e
   }
 }
 
-// Entry e of the list: the prefix (with a shared one), then row tile by row tile
-// from the last (in a chunk the longest) down, every sequence of it.
+// ---- The line: all units in a row, each as long as its work, cut into one equal
+// piece per CTA.  A unit takes kStart for the start and end of an item and
+// kPairTile or kTileCost a tile (two streams of rows, or one); a tile belongs to the
+// CTA whose piece it starts in.  A CTA so gets parts of a unit or two and whole ones
+// between them, and the CTAs end together whatever the lengths are (one item a unit,
+// dealt in turn, ended 30 % apart for ragged chunks, 65 % behind a shared prefix).
+// Entries of units of one length: the prefix (with a shared one), then row tile by
+// row tile from the last down, every sequence of it, its KV heads.
+constexpr int kStart = 12, kPairTile = 4, kTileCost = 3;  // about 0.35 us each
+constexpr int kLeastPiece = kStart + 2 * kPairTile;       // of a CTA
+constexpr int kScheduleWarps = kScheduleThreads / 32;
+
 __device__ __forceinline__ void entry_of(const AttendParams& p, int e, int& b, int& qt) {
   e -= p.shared;
   const int up = p.by_batch.div(e);
@@ -146,6 +153,9 @@ __device__ __forceinline__ bool entry_unit(const AttendParams& p, int e, Item& w
   if (p.shared && e == 0) {
     w.b = -1;
     w.n = p.P;
+    w.past = p.P - 1;
+    w.pt = w.first = 0;
+    w.rows = min(p.B * p.group, kAttendRows);
     w.tiles = (p.P + kTile - 1) / kTile;
     return p.P > 0;
   }
@@ -157,144 +167,149 @@ __device__ __forceinline__ bool entry_unit(const AttendParams& p, int e, Item& w
   // (behind a prefix a sequence without rows has no part)
   return w.rows > 0 && (w.tiles > 0 || !p.shared);
 }
-
 __device__ __forceinline__ int entry_units(const AttendParams& p, int e) {
   return p.h_kv * (p.shared && e == 0 ? p.prefix_tiles : 1);
 }
+__device__ __forceinline__ int tile_cost(const Item& w) {
+  return w.rows > kTile ? kPairTile : kTileCost;
+}
 
-// The list: every unit is cut into ceil(tiles / c) items of equal length, with one c
-// for the whole launch, the one that ends first by a simple model (rounds of the
-// grid times the tiles of an item and a constant for its start and end).  All
-// CTAs compute the same list from the lengths; CTA 0 leaves the table for the
-// combine.  CTA b takes items b, b + gridDim.x, ... of it, into `own`, and returns
-// how many they are.  Ends with a barrier.
-constexpr int kScheduleWarps = kScheduleThreads / 32;
-constexpr int kLengthChoices = 2 * kScheduleWarps;
-constexpr float kItemTiles = 5.f;  // an item's fixed cost in tiles
+// Where a CTA's piece starts: unit i of entry e, at position `pos` of the line; and
+// where the piece lies.
+struct LineStart {
+  long long pos, lo, hi;
+  int e, i;
+};
 
-__device__ __forceinline__ int list_items(const AttendParams& p, int* scratch, Item* own_items) {
-  int* tiles = scratch;                       // [kAttendEntries], -1: absent
-  int* sums = scratch + kAttendEntries;       // [64]
+// All CTAs compute the same line from the lengths.  Ends with a barrier.
+__device__ __forceinline__ void line_start(const AttendParams& p, long long* scratch,
+                                           LineStart* out) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const bool mine = tid < kScheduleThreads;
-  float total = 0.f;
-  int tallest = 0;
-  if (mine)
-    for (int e = tid; e < p.entries; e += kScheduleThreads) {
-      Item w;
-      const bool present = entry_unit(p, e, w);
-      tiles[e] = present ? w.tiles : -1;
-      if (present) {
-        total += float(w.tiles) * float(entry_units(p, e));
-        tallest = max(tallest, w.tiles);
-      }
-    }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    total += __shfl_xor_sync(0xffffffffu, total, o);
-    tallest = max(tallest, __shfl_xor_sync(0xffffffffu, tallest, o));
-  }
-  if (lane == 0 && mine) {
-    sums[warp] = __float_as_int(total);
-    sums[kScheduleWarps + warp] = tallest;
-  }
-  __syncthreads();
-  total = 0.f;
-#pragma unroll
-  for (int i = 0; i < kScheduleWarps; ++i) {
-    total += __int_as_float(sums[i]);
-    tallest = max(tallest, sums[kScheduleWarps + i]);
-  }
-  // two lengths a warp: the items there would be
-  if (mine) {
-    const float share = total / float(p.sms);
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      // from half an even share to 2.4 of them, in steps of 2^(3/20)
-      const int c = max(2, int(ceilf(share * exp2f(float(warp + k * kScheduleWarps) * 0.15f - 1.f))));
-      const float inv = 1.f / float(c);
-      int items = 0;
-      for (int e = lane; e < p.entries; e += 32) {
-        const int t = tiles[e];
-        if (t >= 0) items += max(1, int(ceilf(float(t) * inv))) * entry_units(p, e);
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) items += __shfl_xor_sync(0xffffffffu, items, o);
-      const float longest = float(min(c, tallest)) + kItemTiles;
-      const float mean = (total + kItemTiles * float(items)) / float(p.sms);
-      const float t = fmaxf(fminf(ceilf(float(items) / float(p.sms)) * longest, mean + longest), mean);
-      if (lane == 0) {
-        sums[2 * kScheduleWarps + warp + k * kScheduleWarps] = __float_as_int(t);
-        sums[2 * kScheduleWarps + kLengthChoices + warp + k * kScheduleWarps] = c;
-      }
-    }
-  }
-  __syncthreads();
-  float best = 1e30f;
-  int c = 2;
-#pragma unroll
-  for (int i = 0; i < kLengthChoices; ++i) {
-    const float t = __int_as_float(sums[2 * kScheduleWarps + i]);
-    if (t <= best) best = t, c = sums[2 * kScheduleWarps + kLengthChoices + i];
-  }
-  // first item of every entry: four consecutive entries a thread
   constexpr int kPer = kAttendEntries / kScheduleThreads;
-  int cut[kPer], own = 0;
+  const bool mine = tid < kScheduleThreads;
+  long long own = 0;
+  int unit_cost[kPer];  // 0: absent
   if (mine)
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int e = tid * kPer + i;
-      const int t = e < p.entries ? tiles[e] : -1;
-      cut[i] = t < 0 ? 0 : max(1, (t + c - 1) / c);
-      own += e < p.entries ? cut[i] * entry_units(p, e) : 0;
+    for (int x = 0; x < kPer; ++x) {
+      const int e = tid * kPer + x;
+      unit_cost[x] = 0;
+      Item w;
+      if (e < p.entries && entry_unit(p, e, w)) {
+        unit_cost[x] = kStart + w.tiles * tile_cost(w);
+        own += (long long)unit_cost[x] * entry_units(p, e);
+      }
     }
-  int upto = own;
+  long long upto = own;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, upto, o);
+    const long long v = __shfl_up_sync(0xffffffffu, upto, o);
     if (lane >= o) upto += v;
   }
-  if (lane == 31 && mine) sums[warp] = upto;
+  if (lane == 31 && mine) scratch[warp] = upto;
+  if (tid == 0) out->pos = out->lo = out->hi = 0;
   __syncthreads();
-  const int grid = int(gridDim.x), cta = int(blockIdx.x);
-  int all = 0;
-#pragma unroll
-  for (int i = 0; i < kScheduleWarps; ++i) all += sums[i];
   if (mine) {
-    int at = upto - own;
-    for (int i = 0; i < warp; ++i) at += sums[i];
+    long long total = 0, at = upto - own;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int e = tid * kPer + i;
-      if (e >= p.entries) break;
-      const int items = cut[i] * entry_units(p, e);
-      if (cta == 0) p.table[e] = make_int2(at, cut[i]);
-      int k = at > cta ? (at - cta + grid - 1) / grid : 0;
-      for (; cta + k * grid < at + items && k < kOwnItems; ++k) {  // this CTA's
-        const int x = cta + k * grid - at;
-        Item w;
-        entry_unit(p, e, w);
-        const int unit = x / cut[i], s = x - unit * cut[i];
-        if (w.b < 0) {
-          w.kvh = unit / p.prefix_tiles;
-          w.row0 = (unit - w.kvh * p.prefix_tiles) * kAttendRows;
-          w.rows = min(p.B * p.group - w.row0, kAttendRows);
-          w.past = w.n - 1;
-          w.pt = w.first = 0;
-        } else {
-          w.kvh = unit;
-        }
-        cut_item(p, int((long long)w.tiles * s / cut[i]), int((long long)w.tiles * (s + 1) / cut[i]),
-                 cut[i] == 1 && !p.shared ? -1 : cta + k * grid, w);
-        own_items[k] = w;
-      }
-      at += items;
+    for (int x = 0; x < kScheduleWarps; ++x) {
+      total += scratch[x];
+      if (x < warp) at += scratch[x];
     }
+    // CTAs that take part, and this one's piece
+    const long long most = total / kLeastPiece;
+    const int ctas = most < 1 ? 1 : most < int(gridDim.x) ? int(most) : int(gridDim.x);
+    const int c = blockIdx.x;
+    const long long lo = total * c / ctas, hi = total * (c + 1) / ctas;
+    if (tid == 0) p.cta_start[c] = make_int4(-1, 0, 0, 0);
+    if (c < ctas && total > 0)
+#pragma unroll
+      for (int x = 0; x < kPer; ++x) {
+        const int e = tid * kPer + x;
+        const long long len = e < p.entries ? (long long)unit_cost[x] * entry_units(p, e) : 0;
+        if (lo >= at && lo < at + len) {
+          out->lo = lo;
+          out->hi = hi;
+          out->e = e;
+          out->i = int((lo - at) / unit_cost[x]);
+          out->pos = at + (long long)out->i * unit_cost[x];
+        }
+        at += len;
+      }
   }
   fence_proxy_async_smem();  // the scratch is the ring's: before its first loads
   __syncthreads();
-  return all > cta ? min((all - cta - 1) / grid + 1, kOwnItems) : 0;
 }
+
+// The CTA's way along its piece.
+struct LineWalk {
+  long long pos, lo, hi;
+  int e, i;
+  bool fresh = true;   // entry e is not in `unit` yet
+  Item unit;
+  __device__ __forceinline__ explicit LineWalk(const LineStart& s)
+      : pos(s.pos), lo(s.lo), hi(s.hi), e(s.e), i(s.i) {}
+
+  // The next item; false: the piece ends.
+  __device__ __forceinline__ bool next(const AttendParams& p, Item& w) {
+    while (pos < hi) {
+      if (fresh) {
+        if (e >= p.entries) return false;
+        if (!entry_unit(p, e, unit)) {
+          ++e;
+          continue;
+        }
+        fresh = false;
+      }
+      if (i >= entry_units(p, e)) {
+        ++e;
+        i = 0;
+        fresh = true;
+        continue;
+      }
+      const int cost = tile_cost(unit), n = unit.tiles, u = i;
+      const long long first = pos + kStart;     // of the unit's tiles
+      const bool whole_start = first >= lo, whole_end = first + (long long)(n - 1) * cost < hi;
+      const int begin = whole_start ? 0 : int(min((long long)n, (lo - first + cost - 1) / cost));
+      const int end = whole_end ? n : int(max(0ll, (hi - first + cost - 1) / cost));
+      // (a unit without tiles, all of whose tokens see nothing, belongs where it ends)
+      const bool here = n > 0 ? end > begin : first - 1 >= lo && first - 1 < hi;
+      pos = first + (long long)n * cost;
+      ++i;
+      if (!here) continue;
+      w = unit;
+      const int cta = blockIdx.x;
+      int part = -1;
+      if (p.shared) {
+        int unit_index;
+        if (w.b < 0) {
+          unit_index = u;
+          w.kvh = u / p.prefix_tiles;
+          w.row0 = (u - w.kvh * p.prefix_tiles) * kAttendRows;
+          w.rows = min(p.B * p.group - w.row0, kAttendRows);
+          part = (u + cta) * p.pitch;
+        } else {
+          const int own = (e - 1) * p.h_kv + u;
+          unit_index = p.h_kv * p.prefix_tiles + own;
+          w.kvh = u;
+          part = p.own_parts + (own + cta) * p.unit_rows;
+        }
+        // the CTAs of a unit's first and last items, for the combine
+        int* at = reinterpret_cast<int*>(p.unit_ctas + unit_index);
+        if (begin == 0) at[0] = cta;
+        if (end == n) at[1] = cta;
+      } else {
+        w.kvh = u;
+        if (begin > 0 || end < n) part = (2 * cta + (begin == 0)) * p.pitch;
+        // a unit that goes on from the CTA before: its number, its entry and KV head
+        if (begin > 0) p.cta_start[cta] = make_int4(e * p.h_kv + u, e, u, 0);
+      }
+      cut_item(p, begin, end, part, w);
+      return true;
+    }
+    return false;
+  }
+};
 
 // Without a list: one item per unit, the last row tiles, the longest of a chunk, first.
 // False: the unit has no rows.
@@ -426,7 +441,7 @@ template <class Cfg>
 struct AttendShared {
   uint8_t *q_tile, *ring;   // [2], [kSlots] tiles
   Item* items;              // [2]: the items underway
-  Item* own;                // [kOwnItems]: a list's items of this CTA
+  LineStart* line;          // the CTA's piece
   float* pairs;             // [2][m, l][128]: the streams' sums of the same rows
   volatile int* abort_flag;
   uint32_t tmem;
@@ -489,7 +504,7 @@ __device__ __forceinline__ int lookahead(const Item& w) { return alternates(w) ?
 // ---- the items and their loads: one thread
 template <class Cfg>
 __device__ __forceinline__ void attend_load(const AttendParams& p, const AttendMaps& maps,
-                                            const AttendShared<Cfg>& sh, int own_count) {
+                                            const AttendShared<Cfg>& sh) {
   constexpr int kSlots = Cfg::kSlots;
   RingPlace<kSlots> at;
   uint32_t issued = 0, parity = 0;  // per slot: loaded on its full barrier, phase of that load
@@ -506,6 +521,7 @@ __device__ __forceinline__ void attend_load(const AttendParams& p, const AttendM
     return true;
   };
   int unit = int(blockIdx.x);
+  LineWalk walk(*sh.line);
   for (int k = 0; ok; ++k) {
     if (k >= 2 && !sh.wait(p, sh.item_empty(k), ((k >> 1) - 1) & 1)) {
       ok = false;
@@ -513,8 +529,7 @@ __device__ __forceinline__ void attend_load(const AttendParams& p, const AttendM
     }
     Item& w = sh.items[k & 1];
     if (p.list) {
-      if (k < own_count) w = sh.own[k];
-      else w.count = -1;
+      if (!walk.next(p, w)) w.count = -1;
     } else {
       const int units = p.B * p.h_kv * p.q_tiles;
       bool found = false;
@@ -970,12 +985,12 @@ __device__ __forceinline__ void attend_softmax(const AttendParams& p, const Atte
       const float inv = l_run > 0.f ? 1.f / l_run : (l_run == 0.f ? 0.f : l_run);
       keep0 *= inv;
       keep1 *= inv;
-      const bool part = w.slot >= 0, narrow = !part && p.out_bf16;
-      const long long part_row = (long long)w.slot * p.pitch + (alternate ? 0 : i * kTile) + r;
+      const bool part = w.part >= 0, narrow = !part && p.out_bf16;
+      const long long part_row = (long long)w.part + (alternate ? 0 : i * kTile) + r;
       if (part) out_off = part_row * D;
-      const long long extent = part ? (long long)p.max_items * p.pitch * D : p.out_elems;
+      const long long extent = part ? p.part_rows * D : p.out_elems;
       if (part && valid && !(alternate && i == 1) &&
-          DA_IN(p, part_row, (long long)p.max_items * p.pitch))
+          DA_IN(p, part_row, p.part_rows))
         p.lse_part[part_row] =
             l_run > 0.f ? m_run * p.scale_log2 + log2f(l_run) : (l_run == 0.f ? -INFINITY : l_run);
       // Through the ring's place, D bytes of each of the warp's rows at a time, so that rows
@@ -1070,9 +1085,9 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
   sh.bars = smem_u32(bars);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + Cfg::kBars);
   sh.abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  sh.pairs = reinterpret_cast<float*>(tmem_slot + 4);
-  sh.items = reinterpret_cast<Item*>(sh.pairs + 4 * kTile);
-  sh.own = sh.items + 2;
+  sh.pairs = reinterpret_cast<float*>(tmem_slot + 2);
+  sh.line = reinterpret_cast<LineStart*>(sh.pairs + 4 * kTile);
+  sh.items = reinterpret_cast<Item*>(sh.line + 1);
 
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -1112,8 +1127,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
   tc5::fence_before();
   allow_dependent_launch();
   wait_for_prerequisite_grid();
-  int own_count = 0;
-  if (p.list) own_count = list_items(p, reinterpret_cast<int*>(sh.ring), sh.own);
+  if (p.list) line_start(p, reinterpret_cast<long long*>(sh.ring), sh.line);
   else __syncthreads();
   // lengths that were clamped are reported
   if (blockIdx.x == 0 && p.dev_error)
@@ -1129,7 +1143,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == 8) {
-      if (lane == 0) attend_load<Cfg>(p, maps, sh, own_count);
+      if (lane == 0) attend_load<Cfg>(p, maps, sh);
     } else if (warp == 9) {
       attend_mma<Cfg, WIDE_P>(p, sh);
       named_bar_sync(2, 288);
@@ -1148,100 +1162,122 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
 
 // ---------------------------------------------------------------------------
 // Combine: a warp per query row merges the partials of its unit's items (and,
-// behind a shared prefix, of the prefix unit's) by their log-sum-exps.  Rows
-// whose unit had one item are skipped: it wrote them.
+// behind a shared prefix, of the prefix unit's) by their log-sum-exps.
 // ---------------------------------------------------------------------------
 constexpr int kAttendCombineWarps = 8;
 
+// Row `off` of the output from partials: rows first, first + step, ... (count0 of them),
+// then first1, ... (count1).
 template <int D>
-__global__ void __launch_bounds__(kAttendCombineWarps * 32)
-    attend_combine_kernel(const AttendParams p) {
+__device__ __forceinline__ void merge_row(const AttendParams& p, long long off, long long first0,
+                                          long long step0, int count0, long long first1,
+                                          long long step1, int count1) {
   constexpr int EPL = D / 32, NB = 8;  // columns a lane, partials in flight
-  allow_dependent_launch();
-  wait_for_prerequisite_grid();
-  const int lane = threadIdx.x & 31;
-  const long long warps = (long long)gridDim.x * kAttendCombineWarps;
-  // rows as [entry][kv head][row of the unit]
-  const long long all = (long long)p.B * p.q_tiles * p.h_kv * p.unit_rows;
-  for (long long x = (long long)blockIdx.x * kAttendCombineWarps + (threadIdx.x >> 5); x < all;
-       x += warps) {
-    const int ur = int(x % p.unit_rows);
-    const int kvh = int(x / p.unit_rows % p.h_kv);
-    const int e = int(x / p.unit_rows / p.h_kv) + p.shared;
-    const int2 at = __ldcg(p.table + e);
-    if (!p.shared && at.y <= 1) continue;
-    int b, qt;
-    entry_of(p, e, b, qt);
-    bool bad;
-    const long long flat = (long long)qt * kAttendRows + ur;
-    if (flat >= (long long)(p.shared ? 1 : seq_new(p, b, bad)) * p.group) continue;
-    const int t = int(flat / p.group), h = int(flat % p.group);
-    // the partials: `first` of the prefix, then those of the sequence
-    long long pre_row = 0, own_row = ((long long)at.x + (long long)kvh * at.y) * p.pitch + ur;
-    int pre = 0;
-    if (p.shared) {
-      const int2 pt = __ldcg(p.table);
-      const long long pr = (long long)b * p.group + flat;
-      const int mt = int(pr / kAttendRows);
-      pre = pt.y;
-      pre_row = ((long long)pt.x + ((long long)kvh * p.prefix_tiles + mt) * pt.y) * p.pitch +
-                pr % kAttendRows;
-    }
-    const int parts = pre + at.y;
-    float m = -INFINITY, sum = 0.f, acc[EPL];
+  const int lane = threadIdx.x & 31, parts = count0 + count1;
+  float m = -INFINITY, sum = 0.f, acc[EPL];
 #pragma unroll
-    for (int k = 0; k < EPL; ++k) acc[k] = 0.f;
-    for (int s0 = 0; s0 < parts; s0 += NB) {
-      float l[NB], v[NB][EPL];
+  for (int k = 0; k < EPL; ++k) acc[k] = 0.f;
+  for (int s0 = 0; s0 < parts; s0 += NB) {
+    float l[NB], v[NB][EPL];
 #pragma unroll
-      for (int u = 0; u < NB; ++u) {
-        const int s = s0 + u;
-        const long long row = s < pre ? pre_row + (long long)s * p.pitch
-                                      : own_row + (long long)(s - pre) * p.pitch;
-        const bool in = s < parts && DA_IN(p, row, (long long)p.max_items * p.pitch);
-        l[u] = in ? __ldcg(p.lse_part + row) : -INFINITY;
+    for (int u = 0; u < NB; ++u) {
+      const int s = s0 + u;
+      const long long row = s < count0 ? first0 + s * step0 : first1 + (s - count0) * step1;
+      const bool in = s < parts && DA_IN(p, row, p.part_rows);
+      l[u] = in ? __ldcg(p.lse_part + row) : -INFINITY;
 #pragma unroll
-        for (int k = 0; k < EPL; ++k) v[u][k] = 0.f;
-        if (in) {
-          if constexpr (EPL == 4) {
-            const float4 f = __ldcg(reinterpret_cast<const float4*>(p.o_part + row * D) + lane);
-            v[u][0] = f.x, v[u][1] = f.y, v[u][2] = f.z, v[u][3] = f.w;
-          } else {
-            const float2 f = __ldcg(reinterpret_cast<const float2*>(p.o_part + row * D) + lane);
-            v[u][0] = f.x, v[u][1] = f.y;
-          }
+      for (int k = 0; k < EPL; ++k) v[u][k] = 0.f;
+      if (in) {
+        if constexpr (EPL == 4) {
+          const float4 f = __ldcg(reinterpret_cast<const float4*>(p.o_part + row * D) + lane);
+          v[u][0] = f.x, v[u][1] = f.y, v[u][2] = f.z, v[u][3] = f.w;
+        } else {
+          const float2 f = __ldcg(reinterpret_cast<const float2*>(p.o_part + row * D) + lane);
+          v[u][0] = f.x, v[u][1] = f.y;
         }
       }
-      float mx = m;
-#pragma unroll
-      for (int u = 0; u < NB; ++u) mx = fmaxf(mx, l[u]);
-      const float use = mx == -INFINITY ? 0.f : mx;
-      const float scale = ex2(m - use);
-      sum *= scale;
-#pragma unroll
-      for (int k = 0; k < EPL; ++k) acc[k] *= scale;
-#pragma unroll
-      for (int u = 0; u < NB; ++u) {
-        const float f = ex2(l[u] - use);
-        sum += f;
-#pragma unroll
-        for (int k = 0; k < EPL; ++k) acc[k] = fmaf(f, v[u][k], acc[k]);
-      }
-      m = mx;
     }
-    const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
-    const long long off = b * p.out_stride[0] + (long long)(kvh * p.group + h) * p.out_stride[1] +
-                          t * p.out_stride[2] + lane * EPL;
-    if (!DA_IN(p, off + EPL - 1, p.out_elems)) continue;
-    if (p.out_bf16) {
-      uint32_t* y = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.out) + off);
+    float mx = m;
 #pragma unroll
-      for (int k = 0; k < EPL; k += 2) y[k / 2] = pack_bf16x2(acc[k] * inv, acc[k + 1] * inv);
-    } else {
+    for (int u = 0; u < NB; ++u) mx = fmaxf(mx, l[u]);
+    const float use = mx == -INFINITY ? 0.f : mx;
+    const float scale = ex2(m - use);
+    sum *= scale;
 #pragma unroll
-      for (int k = 0; k < EPL; ++k) static_cast<float*>(p.out)[off + k] = acc[k] * inv;
+    for (int k = 0; k < EPL; ++k) acc[k] *= scale;
+#pragma unroll
+    for (int u = 0; u < NB; ++u) {
+      const float f = ex2(l[u] - use);
+      sum += f;
+#pragma unroll
+      for (int k = 0; k < EPL; ++k) acc[k] = fmaf(f, v[u][k], acc[k]);
     }
+    m = mx;
   }
+  const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
+  off += lane * EPL;
+  if (!DA_IN(p, off + EPL - 1, p.out_elems)) return;
+  if (p.out_bf16) {
+    uint32_t* y = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.out) + off);
+#pragma unroll
+    for (int k = 0; k < EPL; k += 2) y[k / 2] = pack_bf16x2(acc[k] * inv, acc[k + 1] * inv);
+  } else {
+#pragma unroll
+    for (int k = 0; k < EPL; ++k) static_cast<float*>(p.out)[off + k] = acc[k] * inv;
+  }
+}
+
+// Behind a shared prefix: every row, of the CTAs noted for its units.
+template <int D>
+__global__ void __launch_bounds__(kAttendCombineWarps * 32)
+    attend_merge_kernel(const AttendParams p) {
+  allow_dependent_launch();
+  const int row = int(blockIdx.x) * kAttendCombineWarps + int(threadIdx.x >> 5);
+  if (row >= p.B * p.h_q) return;
+  const int b = row / p.h_q, head = row - b * p.h_q;
+  const int kvh = p.by_group.div(head), hh = head - kvh * p.group;
+  wait_for_prerequisite_grid();
+  bool bad;
+  const bool own = seq_rows(p, b, bad) > 0;
+  // the prefix unit's rows are those of all sequences, one after the other
+  const int flat = b * p.group + hh, mt = flat / kAttendRows;
+  const int pre_unit = kvh * p.prefix_tiles + mt;
+  const int qt = hh / kAttendRows;
+  const int own_unit = ((p.q_tiles - 1 - qt) * p.B + b) * p.h_kv + kvh;
+  int2 pre = make_int2(0, -1), mine = make_int2(0, -1);
+  if (p.P > 0) pre = __ldcg(p.unit_ctas + pre_unit);
+  if (own) mine = __ldcg(p.unit_ctas + p.h_kv * p.prefix_tiles + own_unit);
+  merge_row<D>(p, b * p.out_stride[0] + head * p.out_stride[1],
+               (long long)(pre_unit + pre.x) * p.pitch + flat % kAttendRows, p.pitch,
+               pre.y - pre.x + 1,
+               p.own_parts + (long long)(own_unit + mine.x) * p.unit_rows + hh % kAttendRows,
+               p.unit_rows, mine.y - mine.x + 1);
+}
+
+// A chunk: the rows of the units that were cut, each taken at its first cut.
+template <int D>
+__global__ void __launch_bounds__(kAttendCombineWarps * 32)
+    attend_join_kernel(const AttendParams p) {
+  allow_dependent_launch();
+  wait_for_prerequisite_grid();
+  const int c = blockIdx.y + 1;              // a CTA whose piece starts inside a unit
+  const int4 at = __ldcg(p.cta_start + c);
+  if (at.x < 0 || __ldcg(p.cta_start + c - 1).x == at.x) return;
+  const int r = int(blockIdx.x) * kAttendCombineWarps + int(threadIdx.x >> 5);
+  int b, qt;
+  entry_of(p, at.y, b, qt);
+  bool bad;
+  const long long flat = (long long)qt * kAttendRows + r;
+  if (r >= kAttendRows || flat >= (long long)seq_new(p, b, bad) * p.group) return;
+  int last = c;                              // the last CTA of the unit
+  while (last + 1 < p.ctas && __ldcg(p.cta_start + last + 1).x == at.x) ++last;
+  const int t = int(flat / p.group), h = int(flat % p.group);
+  // the first item ends its CTA's piece, the others start theirs
+  merge_row<D>(p,
+               b * p.out_stride[0] + (long long)(at.z * p.group + h) * p.out_stride[1] +
+                   t * p.out_stride[2],
+               (2LL * (c - 1) + 1) * p.pitch + r, 0, 1, 2LL * c * p.pitch + r, 2LL * p.pitch,
+               last - c + 1);
 }
 
 template <class Cfg, bool WIDE_P>
@@ -1267,12 +1303,15 @@ cudaError_t launch_attend(const AttendParams& p, const AttendMaps& m, int d, int
 }
 
 cudaError_t launch_attend_combine(const AttendParams& p, int d, cudaStream_t stream) {
-  const long long rows = (long long)p.B * p.q_tiles * p.h_kv * p.unit_rows;
-  const long long most = (rows + kAttendCombineWarps - 1) / kAttendCombineWarps;
-  const int grid = int(most < 8LL * p.sms ? most : 8LL * p.sms);
-  if (d == 128)
-    return launch_dependent(attend_combine_kernel<128>, grid, kAttendCombineWarps * 32, 0, stream, p);
-  return launch_dependent(attend_combine_kernel<64>, grid, kAttendCombineWarps * 32, 0, stream, p);
+  const int threads = kAttendCombineWarps * 32;
+  if (p.shared) {
+    const int grid = (p.B * p.h_q + kAttendCombineWarps - 1) / kAttendCombineWarps;
+    return d == 128 ? launch_dependent(attend_merge_kernel<128>, grid, threads, 0, stream, p)
+                    : launch_dependent(attend_merge_kernel<64>, grid, threads, 0, stream, p);
+  }
+  const dim3 grid((p.unit_rows + kAttendCombineWarps - 1) / kAttendCombineWarps, p.ctas - 1);
+  return d == 128 ? launch_dependent(attend_join_kernel<128>, grid, threads, 0, stream, p)
+                  : launch_dependent(attend_join_kernel<64>, grid, threads, 0, stream, p);
 }
 
 }  // namespace da

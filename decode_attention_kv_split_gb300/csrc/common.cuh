@@ -427,14 +427,17 @@ struct AttendParams {
                                  // that a masked -inf stays one
   float lazy;                    // 8 / scale_log2: a maximum may lag by 2^8
   int single_read;               // each K and V row is read by one CTA: no use in keeping it in L2
-  // Units: (row tile of 256 query rows, KV head, sequence). list != 0: units are cut into items of
-  // about equal length, merged by the combine; else one item per unit.
-  int list, entries, q_tiles, prefix_tiles, sms, max_items;
+  // Units: (row tile of 256 query rows, KV head, sequence).  list != 0: their work is cut into
+  // one equal piece per CTA and merged by a second kernel; else one item per unit.
+  int list, entries, q_tiles, prefix_tiles, ctas;
   int pitch, unit_rows;          // most query rows of any unit, of a sequence's
+  int own_parts;                 // shared prefix: first partial row of the sequences' units
+  int4* cta_start;               // [ctas] chunk: the unit that a CTA goes on with, or -1
+  int2* unit_ctas;               // [units] shared prefix: the CTAs of a unit's first and last items
+  float* o_part;                 // [part_rows][d]
+  float* lse_part;               // [part_rows], log2 domain
+  long long part_rows;
   FastDiv by_group, by_batch;
-  float* o_part;                 // [max_items][pitch][d]
-  float* lse_part;               // [max_items][pitch], log2 domain
-  int2* table;                   // [entries] first item and items per unit
   long long q_elems, out_elems;  // extents, for the checked build
 #ifdef DA_TEST_HOOKS
   int withhold_cta;
@@ -445,7 +448,6 @@ struct AttendMaps {
 };
 constexpr int kAttendEntries = 1024;  // entries of a list (shared memory of the schedule)
 constexpr int kAttendRows = 256;      // query rows of a unit
-constexpr int kAttendOwn = 8;         // items of a CTA with a list, at most
 cudaError_t launch_attend(const AttendParams& p, const AttendMaps& m, int d, int grid,
                           cudaStream_t stream);
 cudaError_t launch_attend_combine(const AttendParams& p, int d, cudaStream_t stream);
@@ -1742,10 +1744,10 @@ cudaError_t set_smem_limit_once(void (*kernel)(Params...), size_t smem,
 // anything it reads.
 // cluster > 1: in clusters of that many CTAs.
 template <class... Params, class... Args>
-cudaError_t launch_dependent_clusters(void (*kernel)(Params...), int grid, int cluster, int threads,
+cudaError_t launch_dependent_clusters(void (*kernel)(Params...), dim3 grid, int cluster, int threads,
                                       size_t smem, cudaStream_t stream, Args&&... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(grid));
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(unsigned(threads));
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
@@ -1761,7 +1763,7 @@ cudaError_t launch_dependent_clusters(void (*kernel)(Params...), int grid, int c
 }
 
 template <class... Params, class... Args>
-cudaError_t launch_dependent(void (*kernel)(Params...), int grid, int threads, size_t smem,
+cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, int threads, size_t smem,
                              cudaStream_t stream, Args&&... args) {
   return launch_dependent_clusters(kernel, grid, 1, threads, smem, stream,
                                    static_cast<Args&&>(args)...);
