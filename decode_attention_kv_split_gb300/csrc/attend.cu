@@ -51,7 +51,7 @@ struct AttendCfg {
   // p_full[2], o_full, o_empty; item_full[2], item_empty[2], meet[2], fin
   static constexpr int kBars = 3 * kSlots + kEdges + 2 * 6 + 2 + 2 + 2 + 1;
   static constexpr size_t kSmemBytes = size_t(2 + kSlots) * kTileBytes + kBars * 8 +
-                                       2 * 60 + 64 + 4 * kTile * 4;
+                                       3 * 64 + 64 + 4 * kTile * 4;
   static_assert(kSmemBytes <= 227 * 1024, "shared memory");
   static_assert(kEdges > (kSlots + 1) / 2, "edge barriers");
 };
@@ -68,9 +68,10 @@ struct Item {
   int begin, count;  // this item's list tiles
   int upto[2];       // tiles of it that each stream takes (from the first on)
   int clear_lo;      // rows of [prefix, clear_lo) and from n on are seen by no query of the sequence
+  int q_buf;         // alternate: the buffer of Q, which the next such item does not use
   int part;          // first row of its partial, or -1: the unit's only item writes the output
 };
-static_assert(sizeof(Item) <= 60, "shared memory of the items");
+static_assert(sizeof(Item) == 64, "shared memory of the items");
 
 __device__ __forceinline__ int seq_rows(const AttendParams& p, int b, bool& bad) {
   const int n = p.seq_lens[b];
@@ -179,6 +180,7 @@ __device__ __forceinline__ int tile_cost(const Item& w) {
 struct LineStart {
   long long pos, lo, hi;
   int e, i;
+  Item unit;  // of entry e
 };
 
 // All CTAs compute the same line from the lengths.  Ends with a barrier.
@@ -233,6 +235,7 @@ __device__ __forceinline__ void line_start(const AttendParams& p, long long* scr
           out->e = e;
           out->i = int((lo - at) / unit_cost[x]);
           out->pos = at + (long long)out->i * unit_cost[x];
+          entry_unit(p, e, out->unit);
         }
         at += len;
       }
@@ -245,10 +248,10 @@ __device__ __forceinline__ void line_start(const AttendParams& p, long long* scr
 struct LineWalk {
   long long pos, lo, hi;
   int e, i;
-  bool fresh = true;   // entry e is not in `unit` yet
+  bool fresh = false;  // entry e is not in `unit` yet
   Item unit;
   __device__ __forceinline__ explicit LineWalk(const LineStart& s)
-      : pos(s.pos), lo(s.lo), hi(s.hi), e(s.e), i(s.i) {}
+      : pos(s.pos), lo(s.lo), hi(s.hi), e(s.e), i(s.i), unit(s.unit) {}
 
   // The next item; false: the piece ends.
   __device__ __forceinline__ bool next(const AttendParams& p, Item& w) {
@@ -520,7 +523,7 @@ __device__ __forceinline__ void attend_load(const AttendParams& p, const AttendM
     }
     return true;
   };
-  int unit = int(blockIdx.x);
+  int unit = int(blockIdx.x), q_buf = 1;
   LineWalk walk(*sh.line);
   for (int k = 0; ok; ++k) {
     if (k >= 2 && !sh.wait(p, sh.item_empty(k), ((k >> 1) - 1) & 1)) {
@@ -536,6 +539,9 @@ __device__ __forceinline__ void attend_load(const AttendParams& p, const AttendM
       for (; unit < units && !found; unit += int(gridDim.x)) found = unit_item(p, unit, w);
       if (!found) w.count = -1;
     }
+    // behind an item of both buffers the first, whose stream 0 loads it early
+    q_buf = w.count >= 0 && alternates(w) ? q_buf ^ 1 : 1;
+    w.q_buf = q_buf;
     mbar_arrive(sh.item_full(k));
     if (w.count < 0) break;
     const bool pre = w.b < 0;
@@ -620,11 +626,12 @@ __device__ __forceinline__ void attend_mma(const AttendParams& p, const AttendSh
     const int ahead = alternate ? 2 : 1;
     const int upto0 = __shfl_sync(0xffffffffu, w.upto[0], 0);
     const int upto1 = __shfl_sync(0xffffffffu, w.upto[1], 0);
+    const int q_buf = __shfl_sync(0xffffffffu, w.q_buf, 0);
     if (!(ok = sh.wait_uniform(p, sh.q_full(0), k & 1))) break;
     if (!alternate && !(ok = sh.wait_uniform(p, sh.q_full(1), pairs++ & 1))) break;
     uint32_t started = 0;    // streams with a P.V in this item
     auto scores = [&](int i, int slot) {
-      const uint64_t a = q0 + (alternate ? 0 : i * (kTileBytes >> 4));
+      const uint64_t a = q0 + (alternate ? q_buf : i) * (kTileBytes >> 4);
       const uint64_t b = k_major + slot * (kTileBytes >> 4);
 #pragma unroll
       for (int ks = 0; ks < D / 16; ++ks) {
@@ -765,7 +772,7 @@ __device__ __forceinline__ void start_q(const AttendParams& p, const AttendShare
             (w.b < 0 ? 0 : t) * p.q_stride[2];
   }
   const char* q = static_cast<const char*>(p.q) + lane % kChunks * 16;
-  const uint32_t to = smem_u32(sh.q_tile) + i * Cfg::kTileBytes;
+  const uint32_t to = smem_u32(sh.q_tile) + (alternate ? w.q_buf : i) * Cfg::kTileBytes;
 #pragma unroll 4
   for (int y = 0; y < 32; y += kPer) {
     const int row = y + lane / kChunks;
@@ -943,11 +950,12 @@ __device__ __forceinline__ void attend_softmax(const AttendParams& p, const Atte
     const int own_tiles = alternate ? (count - i + 1) / 2 : w.upto[i];
     tiles = tiles0 + own_tiles;
     // Q of the next item, for its first scores to run under the end of this one
-    // (the stream's own score MMAs are complete; alternate: both streams' below; a warp that
-    // stayed out has not seen this item's Q arrive yet)
-    const bool early = works && !alternate;
     if (!sh.wait_warp(p, sh.item_full(k + 1), ((k + 1) >> 1) & 1)) return;
     const Item& next = sh.items[(k + 1) & 1];
+    // The stream's own score MMAs are complete, and of two items of one set of rows each has
+    // its buffer; else behind both streams' below.  (And a warp that stayed out has not seen
+    // this item's Q arrive yet.)
+    const bool early = works && own_tiles > 0 && (!alternate || alternates(next));
     if (early && next.count >= 0) start_q<Cfg>(p, sh, next, i, quarter);
 
     place += 2 * count;
@@ -993,33 +1001,62 @@ __device__ __forceinline__ void attend_softmax(const AttendParams& p, const Atte
           DA_IN(p, part_row, p.part_rows))
         p.lse_part[part_row] =
             l_run > 0.f ? m_run * p.scale_log2 + log2f(l_run) : (l_run == 0.f ? -INFINITY : l_run);
+      char* base = static_cast<char*>(part ? static_cast<void*>(p.o_part) : p.out);
+      if (alternate) {
+        // (few rows as a rule) each lane its row's half of the columns
+        const bool in = valid && DA_IN(p, out_off + D - 1, extent);
+        char* y = base + out_off * (narrow ? 2 : 4);
+#pragma unroll 1
+        for (int c = i * (D / 2); c < (i + 1) * (D / 2); c += 16) {
+          float f[16];
+          if (count > 0) {
+            tc5::ld16(o_col0 + c, f);
+            tc5::wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) f[e] *= keep0;
+            if (count > 1) {
+              float f1[16];
+              tc5::ld16(o_col0 + D + c, f1);
+              tc5::wait_ld();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) f[e] = fmaf(f1[e], keep1, f[e]);
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) f[e] = 0.f;
+          }
+          if (in && narrow) {
+#pragma unroll
+            for (int e = 0; e < 16; e += 8)
+              *reinterpret_cast<uint4*>(y + (c + e) * 2) =
+                  make_uint4(pack_bf16x2(f[e], f[e + 1]), pack_bf16x2(f[e + 2], f[e + 3]),
+                             pack_bf16x2(f[e + 4], f[e + 5]), pack_bf16x2(f[e + 6], f[e + 7]));
+          } else if (in) {
+#pragma unroll
+            for (int e = 0; e < 16; e += 4)
+              *reinterpret_cast<float4*>(y + (c + e) * 4) =
+                  make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
+          }
+          __syncwarp();
+        }
+      } else {
       // Through the ring's place, D bytes of each of the warp's rows at a time, so that rows
       // are written in runs of D bytes.
-      const bool there = own_tiles > 0 || (alternate && count > 0), both = alternate && count > 1;
-      const int c_begin = alternate ? i * (D / 2) : 0, c_end = alternate ? c_begin + D / 2 : D;
       const int mine = min(rows - quarter * 32, 32);  // rows of this warp
       const int cols = narrow ? D / 2 : D / 4;
-      char* base = static_cast<char*>(part ? static_cast<void*>(p.o_part) : p.out);
       constexpr int kChunks = D / 16, kPer = 32 / kChunks;  // 16-byte pieces; rows at a time
       if (!sh.wait_warp(p, sh.full(out_slot), out_phase)) return;
       uint8_t* stage = sh.ring + out_slot * Cfg::kTileBytes + warp * (Cfg::kTileBytes / 8);
 #pragma unroll 1
-      for (int c = c_begin; c < c_end; c += cols) {
+      for (int c = 0; c < D; c += cols) {
 #pragma unroll 2
         for (int x = 0; x < cols; x += 16) {
           float o[16];
-          if (there) {
-            tc5::ld16((alternate ? o_col0 : o_col) + c + x, o);
+          if (own_tiles > 0) {
+            tc5::ld16(o_col + c + x, o);
             tc5::wait_ld();
 #pragma unroll
             for (int e = 0; e < 16; ++e) o[e] *= keep0;
-            if (both) {
-              float o1[16];
-              tc5::ld16(o_col0 + D + c + x, o1);
-              tc5::wait_ld();
-#pragma unroll
-              for (int e = 0; e < 16; ++e) o[e] = fmaf(o1[e], keep1, o[e]);
-            }
           } else {
 #pragma unroll
             for (int e = 0; e < 16; ++e) o[e] = 0.f;
@@ -1051,6 +1088,7 @@ __device__ __forceinline__ void attend_softmax(const AttendParams& p, const Atte
             *reinterpret_cast<uint4*>(base + off * (narrow ? 2 : 4) + ch * 16) = v;
         }
         __syncwarp();
+      }
       }
     }
     if (!early && next.count >= 0) finish_q<Cfg>(sh, next, i, quarter);
