@@ -138,7 +138,7 @@ __device__ __forceinline__ void cut_item(const AttendParams& p, int begin, int e
 // dealt in turn, ended 30 % apart for ragged chunks, 65 % behind a shared prefix).
 // Entries of units of one length: the prefix (with a shared one), then row tile by
 // row tile from the last down, every sequence of it, its KV heads.
-constexpr int kStart = 12, kPairTile = 4, kTileCost = 3;  // about 0.35 us each
+constexpr int kStart = 14, kPairTile = 4, kTileCost = 3;  // about 0.3 us each
 constexpr int kLeastPiece = kStart + 2 * kPairTile;       // of a CTA
 constexpr int kScheduleWarps = kScheduleThreads / 32;
 
@@ -173,6 +173,11 @@ __device__ __forceinline__ int entry_units(const AttendParams& p, int e) {
 }
 __device__ __forceinline__ int tile_cost(const Item& w) {
   return w.rows > kTile ? kPairTile : kTileCost;
+}
+
+// Tiles of a unit that start before x, x > -kStart from its first.
+__device__ __forceinline__ int tiles_before(int x, int cost) {
+  return x <= 0 ? 0 : cost == kPairTile ? (x + kPairTile - 1) / kPairTile : (x + kTileCost - 1) / kTileCost;
 }
 
 // Where a CTA's piece starts: unit i of entry e, at position `pos` of the line; and
@@ -222,7 +227,10 @@ __device__ __forceinline__ void line_start(const AttendParams& p, long long* scr
     const long long most = total / kLeastPiece;
     const int ctas = most < 1 ? 1 : most < int(gridDim.x) ? int(most) : int(gridDim.x);
     const int c = blockIdx.x;
-    const long long lo = total * c / ctas, hi = total * (c + 1) / ctas;
+    // borders at total * c / ctas
+    const long long each = total <= 0xffffffffLL ? uint32_t(total) / uint32_t(ctas) : total / ctas;
+    const int over = int(total - each * ctas);
+    const long long lo = each * c + over * c / ctas, hi = each * (c + 1) + over * (c + 1) / ctas;
     if (tid == 0) p.cta_start[c] = make_int4(-1, 0, 0, 0);
     if (c < ctas && total > 0)
 #pragma unroll
@@ -233,7 +241,8 @@ __device__ __forceinline__ void line_start(const AttendParams& p, long long* scr
           out->lo = lo;
           out->hi = hi;
           out->e = e;
-          out->i = int((lo - at) / unit_cost[x]);
+          const long long in = lo - at;
+          out->i = in <= 0x7fffffffLL ? int(in) / unit_cost[x] : int(in / unit_cost[x]);
           out->pos = at + (long long)out->i * unit_cost[x];
           entry_unit(p, e, out->unit);
         }
@@ -273,8 +282,9 @@ struct LineWalk {
       const int cost = tile_cost(unit), n = unit.tiles, u = i;
       const long long first = pos + kStart;     // of the unit's tiles
       const bool whole_start = first >= lo, whole_end = first + (long long)(n - 1) * cost < hi;
-      const int begin = whole_start ? 0 : int(min((long long)n, (lo - first + cost - 1) / cost));
-      const int end = whole_end ? n : int(max(0ll, (hi - first + cost - 1) / cost));
+      // (a border inside the unit lies less than its length away)
+      const int begin = whole_start ? 0 : min(n, tiles_before(int(lo - first), cost));
+      const int end = whole_end ? n : max(0, tiles_before(int(hi - first), cost));
       // (a unit without tiles, all of whose tokens see nothing, belongs where it ends)
       const bool here = n > 0 ? end > begin : first - 1 >= lo && first - 1 < hi;
       pos = first + (long long)n * cost;
@@ -973,6 +983,8 @@ __device__ __forceinline__ void attend_softmax(const AttendParams& p, const Atte
       if (!sh.wait_warp(p, sh.o_full(1 - i), k & 1)) return;
     }
     if (!sh.wait_warp(p, sh.o_full(i), k & 1)) return;
+    // (whether it is used or not: else its out_done could be a phase ahead of the producer's wait)
+    if (!sh.wait_warp(p, sh.full(out_slot), out_phase)) return;
     tc5::fence_after();
     if (next.count >= 0) {
       if (early) finish_q<Cfg>(sh, next, i, quarter);
@@ -1045,7 +1057,6 @@ __device__ __forceinline__ void attend_softmax(const AttendParams& p, const Atte
       const int mine = min(rows - quarter * 32, 32);  // rows of this warp
       const int cols = narrow ? D / 2 : D / 4;
       constexpr int kChunks = D / 16, kPer = 32 / kChunks;  // 16-byte pieces; rows at a time
-      if (!sh.wait_warp(p, sh.full(out_slot), out_phase)) return;
       uint8_t* stage = sh.ring + out_slot * Cfg::kTileBytes + warp * (Cfg::kTileBytes / 8);
 #pragma unroll 1
       for (int c = 0; c < D; c += cols) {
@@ -1293,29 +1304,111 @@ __global__ void __launch_bounds__(kAttendCombineWarps * 32)
 }
 
 // A chunk: the rows of the units that were cut, each taken at its first cut.
+// Which cut that is, and the rows from r0 on; false: none.
+struct JoinUnit {
+  int b, qt, kvh, first, last, rows;   // CTAs of its first and last items
+};
+__device__ __forceinline__ bool join_unit(const AttendParams& p, int r0, int most, JoinUnit& u) {
+  const int c = blockIdx.y + 1;        // a CTA whose piece starts inside a unit
+  const int4 at = __ldcg(p.cta_start + c);
+  if (at.x < 0 || __ldcg(p.cta_start + c - 1).x == at.x) return false;
+  entry_of(p, at.y, u.b, u.qt);
+  u.kvh = at.z;
+  bool bad;
+  const long long left = (long long)seq_new(p, u.b, bad) * p.group - (long long)u.qt * kAttendRows - r0;
+  u.rows = int(min((long long)min(most, p.unit_rows - r0), left));
+  if (u.rows <= 0) return false;
+  u.first = c - 1;
+  u.last = c;
+  while (u.last + 1 < p.ctas && __ldcg(p.cta_start + u.last + 1).x == at.x) ++u.last;
+  return true;
+}
+// Where row r of the unit goes.
+__device__ __forceinline__ long long join_out(const AttendParams& p, const JoinUnit& u, int r) {
+  const int flat = u.qt * kAttendRows + r;
+  const int t = p.by_group.div(flat), h = flat - t * p.group;
+  return u.b * p.out_stride[0] + (long long)(u.kvh * p.group + h) * p.out_stride[1] +
+         t * p.out_stride[2];
+}
+
+// Few rows, cut into many items as a rule (few tokens behind a long context): a warp a row.
 template <int D>
 __global__ void __launch_bounds__(kAttendCombineWarps * 32)
-    attend_join_kernel(const AttendParams p) {
+    attend_join_few_kernel(const AttendParams p) {
   allow_dependent_launch();
   wait_for_prerequisite_grid();
-  const int c = blockIdx.y + 1;              // a CTA whose piece starts inside a unit
-  const int4 at = __ldcg(p.cta_start + c);
-  if (at.x < 0 || __ldcg(p.cta_start + c - 1).x == at.x) return;
   const int r = int(blockIdx.x) * kAttendCombineWarps + int(threadIdx.x >> 5);
-  int b, qt;
-  entry_of(p, at.y, b, qt);
-  bool bad;
-  const long long flat = (long long)qt * kAttendRows + r;
-  if (r >= kAttendRows || flat >= (long long)seq_new(p, b, bad) * p.group) return;
-  int last = c;                              // the last CTA of the unit
-  while (last + 1 < p.ctas && __ldcg(p.cta_start + last + 1).x == at.x) ++last;
-  const int t = int(flat / p.group), h = int(flat % p.group);
+  JoinUnit u;
+  if (!join_unit(p, r, 1, u)) return;
   // the first item ends its CTA's piece, the others start theirs
-  merge_row<D>(p,
-               b * p.out_stride[0] + (long long)(at.z * p.group + h) * p.out_stride[1] +
-                   t * p.out_stride[2],
-               (2LL * (c - 1) + 1) * p.pitch + r, 0, 1, 2LL * c * p.pitch + r, 2LL * p.pitch,
-               last - c + 1);
+  merge_row<D>(p, join_out(p, u, r), (2LL * u.first + 1) * p.pitch + r, 0, 1,
+               2LL * (u.first + 1) * p.pitch + r, 2LL * p.pitch, u.last - u.first);
+}
+
+// More rows, cut in two as a rule: a warp takes four at once and the partials one after the
+// other (a warp a row took 28 us of launching behind 150 CTAs; 8 tokens of 131072 rows, ten
+// items a unit, took 166 us this way and 159 the other).
+constexpr int kJoinRows = 4;
+
+template <int D>
+__global__ void __launch_bounds__(kAttendCombineWarps * 32, 4)
+    attend_join_kernel(const AttendParams p) {
+  constexpr int EPL = D / 32;                // columns a lane
+  allow_dependent_launch();
+  wait_for_prerequisite_grid();
+  const int lane = threadIdx.x & 31;
+  const int r0 = (int(blockIdx.x) * kAttendCombineWarps + int(threadIdx.x >> 5)) * kJoinRows;
+  JoinUnit u;
+  if (!join_unit(p, r0, kJoinRows, u)) return;
+  const int rows = u.rows;
+  float m[kJoinRows], sum[kJoinRows], acc[kJoinRows][EPL];
+#pragma unroll
+  for (int y = 0; y < kJoinRows; ++y) {
+    m[y] = -INFINITY;
+    sum[y] = 0.f;
+#pragma unroll
+    for (int k = 0; k < EPL; ++k) acc[y][k] = 0.f;
+  }
+  for (int s = u.first; s <= u.last; ++s) {
+    // the first item ends its CTA's piece, the others start theirs
+    const long long row = (2LL * s + (s == u.first)) * p.pitch + r0;
+    float l[kJoinRows], v[kJoinRows][EPL];
+#pragma unroll
+    for (int y = 0; y < kJoinRows; ++y) {
+      const bool in = y < rows && DA_IN(p, row + y, p.part_rows);
+      l[y] = in ? __ldcg(p.lse_part + row + y) : -INFINITY;
+#pragma unroll
+      for (int k = 0; k < EPL; k += 2) {
+        const float2 f = in ? __ldcg(reinterpret_cast<const float2*>(p.o_part + (row + y) * D + lane * EPL + k))
+                            : make_float2(0.f, 0.f);
+        v[y][k] = f.x, v[y][k + 1] = f.y;
+      }
+    }
+#pragma unroll
+    for (int y = 0; y < kJoinRows; ++y) {
+      const float top = fmaxf(m[y], l[y]), use = top == -INFINITY ? 0.f : top;
+      const float a = ex2(m[y] - use), f = ex2(l[y] - use);
+      sum[y] = sum[y] * a + f;
+#pragma unroll
+      for (int k = 0; k < EPL; ++k) acc[y][k] = acc[y][k] * a + f * v[y][k];
+      m[y] = top;
+    }
+  }
+#pragma unroll
+  for (int y = 0; y < kJoinRows; ++y) {
+    if (y >= rows) break;
+    const long long off = join_out(p, u, r0 + y) + lane * EPL;
+    const float inv = sum[y] > 0.f ? 1.f / sum[y] : (sum[y] == 0.f ? 0.f : sum[y]);
+    if (!DA_IN(p, off + EPL - 1, p.out_elems)) continue;
+    if (p.out_bf16) {
+      uint32_t* z = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.out) + off);
+#pragma unroll
+      for (int k = 0; k < EPL; k += 2) z[k / 2] = pack_bf16x2(acc[y][k] * inv, acc[y][k + 1] * inv);
+    } else {
+#pragma unroll
+      for (int k = 0; k < EPL; ++k) static_cast<float*>(p.out)[off + k] = acc[y][k] * inv;
+    }
+  }
 }
 
 template <class Cfg, bool WIDE_P>
@@ -1347,7 +1440,12 @@ cudaError_t launch_attend_combine(const AttendParams& p, int d, cudaStream_t str
     return d == 128 ? launch_dependent(attend_merge_kernel<128>, grid, threads, 0, stream, p)
                     : launch_dependent(attend_merge_kernel<64>, grid, threads, 0, stream, p);
   }
-  const dim3 grid((p.unit_rows + kAttendCombineWarps - 1) / kAttendCombineWarps, p.ctas - 1);
+  const bool few = p.unit_rows <= 64;
+  const int rows = kAttendCombineWarps * (few ? 1 : kJoinRows);
+  const dim3 grid((p.unit_rows + rows - 1) / rows, p.ctas - 1);
+  if (few)
+    return d == 128 ? launch_dependent(attend_join_few_kernel<128>, grid, threads, 0, stream, p)
+                    : launch_dependent(attend_join_few_kernel<64>, grid, threads, 0, stream, p);
   return d == 128 ? launch_dependent(attend_join_kernel<128>, grid, threads, 0, stream, p)
                   : launch_dependent(attend_join_kernel<64>, grid, threads, 0, stream, p);
 }

@@ -66,7 +66,7 @@ __device__ __forceinline__ float group_sum(float v, unsigned lanes) {
   return v;
 }
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 128;  // (256: prompts 153 us, not 134)
 
 template <typename T, int LPR, int HC>
 __global__ void __launch_bounds__(kRopeThreads) kv_append_rope_kernel(const RopeAppendArgs p) {
