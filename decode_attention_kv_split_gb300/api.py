@@ -925,17 +925,24 @@ def kv_read_q8b(K: torch.Tensor, V: torch.Tensor, k_scale: torch.Tensor, v_scale
 
 
 # ----------------------------------- from projections to the cache, chunks, shared prefixes
+_stride_cache: dict = {}
+
+
 def _row_strides(name: str, t: torch.Tensor, shape, dtype, device: int, write: bool = False):
     """The strides (b, head, token) of rows t, which has to be of ``shape`` [B, h, T, d]."""
     if t.shape != shape or t.dtype is not dtype or t.get_device() != device:
         raise ValueError(f"{name} must be a {dtype} tensor {list(shape)} on the cache's device")
+    key = (shape, t.stride(), write)
+    known = _stride_cache.get(key)
+    if known is not None:
+        return known
     sb, sh, st, sd = t.stride()
     if sd != 1:
         raise ValueError(f"{name} must be contiguous in its last dimension")
     B, h, T, d = shape
     # a dimension of one element has no step: its stride in the tensor may be anything
     steps = (sb if B > 1 else 0, sh if h > 1 else 0, st if T > 1 else 0)
-    if write and not t.is_contiguous():
+    if write:
         # rows that are written may not share an element: each step passes what the smaller ones reach
         reach = d
         for step, n in sorted(zip(steps, (B, h, T))):
@@ -943,7 +950,10 @@ def _row_strides(name: str, t: torch.Tensor, shape, dtype, device: int, write: b
                 if step < reach:
                     raise ValueError(f"{name} must not overlap itself")
                 reach = step * (n - 1) + reach
-    return _Strides(*steps)
+    if len(_stride_cache) > 4096:
+        _stride_cache.clear()
+    strides = _stride_cache[key] = _Strides(*steps)
+    return strides
 
 
 def _new_out(out, dtype, B: int, h: int, T: int, d: int, device, stream):
@@ -979,8 +989,9 @@ def kv_append_rope(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor, K:
         raise ValueError("expected q [B, h_q, T, d_k] and float32 or bfloat16 caches K [B, h_kv, n_max, d_k], "
                          "V [B, h_kv, n_max, d_v]")
     B, h_kv, n_max, d_k = K.shape
-    h_q, T, d_v = q.shape[1], q.shape[2], V.shape[3]
-    if V.shape != (B, h_kv, n_max, d_v) or device < 0 or V.get_device() != device \
+    _, h_q, T, _ = q.shape
+    d_v = V.shape[3]
+    if device < 0 or V.shape != (B, h_kv, n_max, d_v) or V.get_device() != device \
             or not (K.is_contiguous() and V.is_contiguous()):
         raise ValueError("K and V must be contiguous CUDA tensors of one batch, on one device")
     q_shape = (B, h_q, T, d_k)
@@ -989,21 +1000,23 @@ def kv_append_rope(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor, K:
                _row_strides("v_new", v_new, (B, h_kv, T, d_v), dtype, device))
     q_out = _new_out(q_out, dtype, B, h_q, T, d_k, K.device, stream)
     out_strides = _row_strides("q_out", q_out, q_shape, dtype, device, write=True)
-    angles = cos.shape
-    for t in (cos, sin):
-        if t.dim() != 2 or t.shape != angles or t.dtype is not torch.float32 \
-                or t.get_device() != device or not t.is_contiguous():
-            raise ValueError("cos and sin must be contiguous float32 tensors [n_angles, rot / 2] on "
-                             "the cache's device")
+    angles, f32 = cos.shape, torch.float32
+    if len(angles) != 2 or sin.shape != angles or cos.dtype is not f32 or sin.dtype is not f32 \
+            or cos.get_device() != device or sin.get_device() != device \
+            or not (cos.is_contiguous() and sin.is_contiguous()):
+        raise ValueError("cos and sin must be contiguous float32 tensors [n_angles, rot / 2] on the "
+                         "cache's device")
     for t in (q_weight, k_weight):
-        if t is not None and (t.shape != (d_k,) or t.dtype is not dtype or t.get_device() != device
+        if t is not None and (t.dtype is not dtype or t.shape != (d_k,) or t.get_device() != device
                               or not t.is_contiguous()):
             raise ValueError("q_weight and k_weight must be contiguous tensors [d_k] of the cache's "
                              "type and device")
     if _bad_seq_lens(pos, B, device):
         raise ValueError("pos must be a contiguous int32 tensor [B] on the cache's device")
-    _row_counts("n_new", n_new, B, device)
-    _row_counts("angle_pos", angle_pos, B, device)
+    if n_new is not None:
+        _row_counts("n_new", n_new, B, device)
+    if angle_pos is not None:
+        _row_counts("angle_pos", angle_pos, B, device)
     err = None if dev_error is None else _error_word(dev_error, device)
     prev = _enter(device)
     try:
@@ -1058,7 +1071,7 @@ def chunk_attn(q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, seq_lens: torc
     if q.dim() != 4 or K.dim() != 4 or V.shape != K.shape:
         raise ValueError("expected q [B, h_q, T, d], K and V [B, h_kv, n_max, d]")
     B, h_kv, n_max, d = K.shape
-    h_q, T = q.shape[1], q.shape[2]
+    _, h_q, T, _ = q.shape
     if K.dtype is not torch.bfloat16 or V.dtype is not torch.bfloat16 or device < 0 \
             or K.get_device() != device or V.get_device() != device \
             or not (K.is_contiguous() and V.is_contiguous()):
@@ -1073,7 +1086,8 @@ def chunk_attn(q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, seq_lens: torc
     out_strides = _row_strides("out", out, shape, dtype, device, write=True)
     if _bad_seq_lens(seq_lens, B, device):
         raise ValueError("seq_lens must be a contiguous int32 tensor [B] on the device of the others")
-    _row_counts("n_new", n_new, B, device)
+    if n_new is not None:
+        _row_counts("n_new", n_new, B, device)
     if not 0 <= window < 1 << 31 or not 0 <= prefix < 1 << 31:
         raise ValueError("window and prefix must be non-negative ints")
     err = None if dev_error is None else _error_word(dev_error, device)
@@ -1111,14 +1125,14 @@ def decode_attn_shared(q: torch.Tensor, K_prefix: torch.Tensor, V_prefix: torch.
     prefix is read once for the whole batch.  Returns ``out`` [B, h_q, d]."""
     device, out, dims, dt = _cache_args(q, K, V, seq_lens, out, out_dtype, stream)
     B, h_q, h_kv, d, d_v, n_max = dims
-    if K_prefix.dim() != 3 or K_prefix.shape[0] != h_kv or K_prefix.shape[2] != d or d_v != d \
-            or V_prefix.shape != K_prefix.shape or K_prefix.dtype is not K.dtype \
-            or V_prefix.dtype is not K.dtype or K_prefix.get_device() != device \
-            or V_prefix.get_device() != device \
+    shape, dtype = K_prefix.shape, K.dtype
+    if len(shape) != 3 or shape[0] != h_kv or shape[2] != d or d_v != d or V_prefix.shape != shape \
+            or K_prefix.dtype is not dtype or V_prefix.dtype is not dtype \
+            or K_prefix.get_device() != device or V_prefix.get_device() != device \
             or not (K_prefix.is_contiguous() and V_prefix.is_contiguous()):
         raise ValueError("K_prefix and V_prefix must be contiguous tensors [h_kv, prefix_max, d] of "
                          "the cache's type and device")
-    prefix_max = K_prefix.shape[1]
+    prefix_max = shape[1]
     if prefix_len is None:
         prefix_len = prefix_max
     err = None if dev_error is None else _error_word(dev_error, device)

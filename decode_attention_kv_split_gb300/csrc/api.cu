@@ -1121,7 +1121,7 @@ int kv_append_rope(const void* q, const void* k_new, const void* v_new, const lo
   if (!sizes) return DA_ERR_UNSUPPORTED;
   if (T == 0) return DA_OK;
   // lanes of the launch (one to four heads for every 4 to 32 of them) in 32 bits
-  if (T > (1 << 30) || (double)B * T * (h_q + 2.0 * h_kv) * 32.0 > 2147483647.0 * 256.0)
+  if (T > (1 << 30) || (double)B * T * (h_q + 2.0 * h_kv) * 32.0 > 2147483647.0 * 128.0)
     return DA_ERR_SHAPE;
   if (!q || !k_new || !v_new || !q_out) return DA_ERR_NULL;
   if (!aligned16(q) || !aligned16(k_new) || !aligned16(v_new) || !aligned16(q_out) ||
