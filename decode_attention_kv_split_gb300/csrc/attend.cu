@@ -1052,54 +1052,54 @@ __device__ __forceinline__ void attend_softmax(const AttendParams& p, const Atte
           __syncwarp();
         }
       } else {
-      // Through the ring's place, D bytes of each of the warp's rows at a time, so that rows
-      // are written in runs of D bytes.
-      const int mine = min(rows - quarter * 32, 32);  // rows of this warp
-      const int cols = narrow ? D / 2 : D / 4;
-      constexpr int kChunks = D / 16, kPer = 32 / kChunks;  // 16-byte pieces; rows at a time
-      uint8_t* stage = sh.ring + out_slot * Cfg::kTileBytes + warp * (Cfg::kTileBytes / 8);
+        // Through the ring's place, D bytes of each of the warp's rows at a time, so that rows
+        // are written in runs of D bytes.
+        const int mine = min(rows - quarter * 32, 32);  // rows of this warp
+        const int cols = narrow ? D / 2 : D / 4;
+        constexpr int kChunks = D / 16, kPer = 32 / kChunks;  // 16-byte pieces; rows at a time
+        uint8_t* stage = sh.ring + out_slot * Cfg::kTileBytes + warp * (Cfg::kTileBytes / 8);
 #pragma unroll 1
-      for (int c = 0; c < D; c += cols) {
+        for (int c = 0; c < D; c += cols) {
 #pragma unroll 2
-        for (int x = 0; x < cols; x += 16) {
-          float o[16];
-          if (own_tiles > 0) {
-            tc5::ld16(o_col + c + x, o);
-            tc5::wait_ld();
+          for (int x = 0; x < cols; x += 16) {
+            float o[16];
+            if (own_tiles > 0) {
+              tc5::ld16(o_col + c + x, o);
+              tc5::wait_ld();
 #pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] *= keep0;
-          } else {
+              for (int e = 0; e < 16; ++e) o[e] *= keep0;
+            } else {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = 0.f;
+              for (int e = 0; e < 16; ++e) o[e] = 0.f;
+            }
+            auto put = [&](int chunk, uint32_t v0, uint32_t v1, uint32_t v2, uint32_t v3) {
+              *reinterpret_cast<uint4*>(stage + lane * D + ((chunk ^ (lane & (kChunks - 1))) << 4)) =
+                  make_uint4(v0, v1, v2, v3);
+            };
+            if (narrow) {
+#pragma unroll
+              for (int e = 0; e < 16; e += 8)
+                put((x + e) / 8, pack_bf16x2(o[e], o[e + 1]), pack_bf16x2(o[e + 2], o[e + 3]),
+                    pack_bf16x2(o[e + 4], o[e + 5]), pack_bf16x2(o[e + 6], o[e + 7]));
+            } else {
+#pragma unroll
+              for (int e = 0; e < 16; e += 4)
+                put((x + e) / 4, __float_as_uint(o[e]), __float_as_uint(o[e + 1]),
+                    __float_as_uint(o[e + 2]), __float_as_uint(o[e + 3]));
+            }
           }
-          auto put = [&](int chunk, uint32_t v0, uint32_t v1, uint32_t v2, uint32_t v3) {
-            *reinterpret_cast<uint4*>(stage + lane * D + ((chunk ^ (lane & (kChunks - 1))) << 4)) =
-                make_uint4(v0, v1, v2, v3);
-          };
-          if (narrow) {
-#pragma unroll
-            for (int e = 0; e < 16; e += 8)
-              put((x + e) / 8, pack_bf16x2(o[e], o[e + 1]), pack_bf16x2(o[e + 2], o[e + 3]),
-                  pack_bf16x2(o[e + 4], o[e + 5]), pack_bf16x2(o[e + 6], o[e + 7]));
-          } else {
-#pragma unroll
-            for (int e = 0; e < 16; e += 4)
-              put((x + e) / 4, __float_as_uint(o[e]), __float_as_uint(o[e + 1]),
-                  __float_as_uint(o[e + 2]), __float_as_uint(o[e + 3]));
-          }
-        }
-        __syncwarp();
+          __syncwarp();
 #pragma unroll 4
-        for (int y = 0; y < mine; y += kPer) {
-          const int row = y + lane / kChunks, ch = lane % kChunks;
-          const long long off = __shfl_sync(0xffffffffu, out_off, row & 31) + c;
-          const uint4 v =
-              *reinterpret_cast<const uint4*>(stage + row * D + ((ch ^ (row & (kChunks - 1))) << 4));
-          if (row < mine && DA_IN(p, off + cols - 1, extent))
-            *reinterpret_cast<uint4*>(base + off * (narrow ? 2 : 4) + ch * 16) = v;
+          for (int y = 0; y < mine; y += kPer) {
+            const int row = y + lane / kChunks, ch = lane % kChunks;
+            const long long off = __shfl_sync(0xffffffffu, out_off, row & 31) + c;
+            const uint4 v =
+                *reinterpret_cast<const uint4*>(stage + row * D + ((ch ^ (row & (kChunks - 1))) << 4));
+            if (row < mine && DA_IN(p, off + cols - 1, extent))
+              *reinterpret_cast<uint4*>(base + off * (narrow ? 2 : 4) + ch * 16) = v;
+          }
+          __syncwarp();
         }
-        __syncwarp();
-      }
       }
     }
     if (!early && next.count >= 0) finish_q<Cfg>(sh, next, i, quarter);
