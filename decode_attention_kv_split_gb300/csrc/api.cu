@@ -1202,19 +1202,24 @@ int plan_attend(int B, int T, int h_q, int h_kv, int d, int n_max, int dtype, in
   a.units = ((long long)a.slice * a.q_tiles + a.prefix_tiles) * h_kv;
   if (a.units > 0x7fffffffLL - 2 * sms) return DA_ERR_SHAPE;
   const long long entries = (long long)a.slice * a.q_tiles + (P >= 0 ? 1 : 0);
-  // Cut into equal pieces, one per CTA, and merged: behind a prefix (whose partials are merged with a
-  // sequence's own anyway), and a chunk's units of more than 8 tiles (below, one CTA a unit takes
-  // less time than the second launch: 300 rows, 9 us against 13).  Of very many units (32 a CTA)
-  // whole ones even out by themselves.
+  // Cut into equal pieces, one per CTA, and merged: behind a prefix (whose partials are merged with
+  // a sequence's own anyway), and of a chunk where whole units, taken one by one by CTAs that are
+  // done, would end apart.  Cutting and merging costs 3 to 20 us, so not with up to 16 tiles of
+  // cache (5 tokens: 7.9 us whole and 10.6 cut behind 300 rows, 14.8 and 14.2 behind 2000; 64
+  // sequences of 16 tokens, one of 2048 rows: 28 and 35), nor where units are many beside the
+  // longest, n_max / T times a prompt's (prompts, 4 of 2048 tokens: 120 and 146, 2 of 8192: 732
+  // and 761; the other side, 4 x 2048 tokens behind up to 14336 rows: 1087 and 1047).
   const int most_tiles = (n_max + 127) / 128, prefix_most = P > 0 ? (P + 127) / 128 : 0;
-  a.list = P >= 0 || (a.units < 32LL * sms && most_tiles > 8 && entries <= da::kAttendEntries);
+  const bool whole = most_tiles <= 16 || a.units * T >= (long long)sms * n_max;
+  a.list = P >= 0 || (!whole && entries <= da::kAttendEntries);
   a.pitch = int((P >= 0 ? a.slice * g : rows) < da::kAttendRows ? (P >= 0 ? a.slice * g : rows)
                                                                  : da::kAttendRows);
   a.unit_rows = int(rows < da::kAttendRows ? rows : da::kAttendRows);
-  // a CTA per SM, but no more than pairs of tiles
+  // a CTA per SM, but no more than pairs of tiles; without cuts one a unit, most of which are
+  // taken over by CTAs that are done
   const long long pairs = (long long)a.slice * a.q_tiles * h_kv * ((most_tiles + 1) / 2) +
                           (long long)a.prefix_tiles * h_kv * ((prefix_most + 1) / 2);
-  a.ctas = int(!a.list ? (a.units < sms ? a.units : sms) : (pairs < sms ? pairs : sms));
+  a.ctas = int(!a.list ? a.units : pairs < sms ? pairs : sms);
   if (P >= 0) {
     // a partial for each CTA of a unit; one number per unit and CTA, prefix units first
     const long long pre_units = (long long)a.prefix_tiles * h_kv;
