@@ -1175,9 +1175,10 @@ struct AttendPlan {
   }
 };
 
-// Sizes and types of both; P < 0: no shared prefix.
+// Sizes and types of both; P < 0: no shared prefix.  seen: rows that a unit sees at most (a
+// workspace asked for without the window's is never too small: fewer rows, fewer cuts).
 int plan_attend(int B, int T, int h_q, int h_kv, int d, int n_max, int dtype, int P, int sms,
-                AttendPlan* plan) {
+                long long seen, AttendPlan* plan) {
   DtypeArg dt;
   if (!parse_dtype(dtype, &dt)) return DA_ERR_DTYPE;
   if (dt.kv != DA_FP32 && dt.kv != DA_BF16) return DA_ERR_DTYPE;
@@ -1204,13 +1205,13 @@ int plan_attend(int B, int T, int h_q, int h_kv, int d, int n_max, int dtype, in
   const long long entries = (long long)a.slice * a.q_tiles + (P >= 0 ? 1 : 0);
   // Cut into equal pieces, one per CTA, and merged: behind a prefix (whose partials are merged with
   // a sequence's own anyway), and of a chunk where whole units, taken one by one by CTAs that are
-  // done, would end apart.  Cutting and merging costs 3 to 20 us, so not with up to 16 tiles of
-  // cache (5 tokens: 7.9 us whole and 10.6 cut behind 300 rows, 14.8 and 14.2 behind 2000; 64
-  // sequences of 16 tokens, one of 2048 rows: 28 and 35), nor where units are many beside the
-  // longest, n_max / T times a prompt's (prompts, 4 of 2048 tokens: 120 and 146, 2 of 8192: 732
-  // and 761; the other side, 4 x 2048 tokens behind up to 14336 rows: 1087 and 1047).
+  // done, would end apart.  Cutting and merging costs 3 to 20 us, so not up to 16 tiles of rows
+  // (5 tokens: 7.9 us whole and 10.6 cut behind 300 rows, 14.8 and 14.2 behind 2000; 64 sequences
+  // of 16 tokens, one of 2048 rows: 28 and 35; 1024 tokens with a window of 1024: 22 and 39), nor
+  // where units are many beside the longest (prompts, 4 of 2048 tokens: 120 and 146, 2 of 8192:
+  // 732 and 761; the other side, 4 x 2048 tokens behind up to 14336 rows: 1087 and 1047).
   const int most_tiles = (n_max + 127) / 128, prefix_most = P > 0 ? (P + 127) / 128 : 0;
-  const bool whole = most_tiles <= 16 || a.units * T >= (long long)sms * n_max;
+  const bool whole = seen <= 16 * 128 || a.units * T >= sms * seen;
   a.list = P >= 0 || (!whole && entries <= da::kAttendEntries);
   a.pitch = int((P >= 0 ? a.slice * g : rows) < da::kAttendRows ? (P >= 0 ? a.slice * g : rows)
                                                                  : da::kAttendRows);
@@ -1239,9 +1240,9 @@ size_t attend_workspace(int B, int T, int h_q, int h_kv, int d, int n_max, int d
   int dev, sms;
   AttendPlan plan{};
   // sizes first, so that a wrong call is told without a GPU
-  int st = plan_attend(B, T, h_q, h_kv, d, n_max, dtype, P, 1, &plan);
+  int st = plan_attend(B, T, h_q, h_kv, d, n_max, dtype, P, 1, n_max, &plan);
   if (st == DA_OK) st = current_device(&dev, &sms);
-  if (st == DA_OK) st = plan_attend(B, T, h_q, h_kv, d, n_max, dtype, P, sms, &plan);
+  if (st == DA_OK) st = plan_attend(B, T, h_q, h_kv, d, n_max, dtype, P, sms, n_max, &plan);
   if (status) *status = st;
   return st == DA_OK ? plan.bytes(d) : 0;
 }
@@ -1261,7 +1262,7 @@ int run_attend(const AttendCall& c, void* workspace, size_t workspace_bytes, int
   if (!c.K || !c.V || !c.seq_lens || !c.q_strides || !c.out_strides) return DA_ERR_NULL;
   if (shared && (!c.K_prefix || !c.V_prefix)) return DA_ERR_NULL;
   AttendPlan plan{};
-  int st = plan_attend(c.B, c.T, c.h_q, c.h_kv, c.d, c.n_max, c.dtype, c.P, 1, &plan);
+  int st = plan_attend(c.B, c.T, c.h_q, c.h_kv, c.d, c.n_max, c.dtype, c.P, 1, c.n_max, &plan);
   if (st != DA_OK) return st;
   if (c.window < 0 || c.prefix < 0) return DA_ERR_SHAPE;
   const double scale_log2 = fabs(double(c.scale)) * 1.4426950408889634;
@@ -1289,7 +1290,10 @@ int run_attend(const AttendCall& c, void* workspace, size_t workspace_bytes, int
   }
   int dev, sms;
   if ((st = current_device(&dev, &sms)) != DA_OK) return st;
-  plan_attend(c.B, c.T, c.h_q, c.h_kv, c.d, c.n_max, c.dtype, c.P, sms, &plan);
+  // a window and its first rows, behind the first of a unit's tokens
+  const long long seen = c.window == 0 ? c.n_max : (long long)c.window + c.prefix + da::kAttendRows;
+  plan_attend(c.B, c.T, c.h_q, c.h_kv, c.d, c.n_max, c.dtype, c.P, sms,
+              seen < c.n_max ? seen : c.n_max, &plan);
   if (plan.list && (!workspace || workspace_bytes < plan.bytes(c.d))) return DA_ERR_WORKSPACE;
   if (plan.list && !aligned16(workspace)) return DA_ERR_ALIGN;
   da::AttendMaps maps;

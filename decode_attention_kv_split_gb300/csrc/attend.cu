@@ -1494,6 +1494,7 @@ cudaError_t launch_attend_combine(const AttendParams& p, int d, cudaStream_t str
     return d == 128 ? launch_dependent(attend_merge_kernel<128>, grid, threads, 0, stream, p)
                     : launch_dependent(attend_merge_kernel<64>, grid, threads, 0, stream, p);
   }
+  // (16 sequences of 16 tokens, 128 rows a unit, behind 8000 rows: 93 us, and 98 a warp a row)
   const bool few = p.unit_rows <= 64;
   const int rows = kAttendCombineWarps * (few ? 1 : kJoinRows);
   const dim3 grid((p.unit_rows + rows - 1) / rows, p.ctas - 1);

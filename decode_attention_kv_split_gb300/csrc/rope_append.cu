@@ -20,6 +20,8 @@ namespace da {
 // the norm's sum is the only exchange.  A group takes HC heads of one token and
 // one kind (q, k or v), so that their loads are in flight together and the
 // angles and weights are read once for all of them.
+// Measured: 16 prompts of 2048 tokens, 32 + 2 * 8 heads of 128 in bf16, 134 us = 6.0 TB/s
+// (0.88 of a copy's rate); one token 2.3 us, which is the launch.
 // ---------------------------------------------------------------------------
 template <typename T>
 struct RopeVec;
@@ -66,7 +68,8 @@ __device__ __forceinline__ float group_sum(float v, unsigned lanes) {
   return v;
 }
 
-constexpr int kRopeThreads = 128;  // (256: prompts 153 us, not 134)
+// 256 threads: prompts 153 us, not 134; 64: the chunks in float32 36 us, not 30.
+constexpr int kRopeThreads = 128;
 
 template <typename T, int LPR, int HC>
 __global__ void __launch_bounds__(kRopeThreads) kv_append_rope_kernel(const RopeAppendArgs p) {
@@ -226,6 +229,8 @@ static cudaError_t launch_rope_hc(const RopeAppendArgs& a, cudaStream_t stream) 
 template <typename T, int LPR>
 static cudaError_t launch_rope_lanes(const RopeAppendArgs& a, cudaStream_t stream) {
   const long long lanes = (long long)a.B * a.T * (a.h_q + 2LL * a.h_kv) * LPR;
+  // Four heads a group once the SMs have threads enough without (1024 tokens of 32 + 2 * 8 heads of
+  // 128 in float32: 7.2 us with four, 9.7 with one; 256 tokens 4.2 and 3.7, one token 2.8 and 2.1).
   if (lanes > a.sms * 2048LL) return launch_rope_hc<T, LPR, 4>(a, stream);
   return launch_rope_hc<T, LPR, 1>(a, stream);
 }

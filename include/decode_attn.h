@@ -568,7 +568,7 @@ DA_API int chunk_attn(const void* q, const long long* q_strides, int T, const in
  *                        anywhere out = 0).  Outside [0, n_max]: clamped,
  *                        DA_DEVERR_SEQ_LEN.
  *   V rows below the lengths must be finite; weights are rounded as in chunk_attn.
- * Two launches (for each of several hundred sequences).
+ * Two launches for each 1023 sequences (fewer with more than 256 query heads a KV head).
  */
 DA_API size_t decode_attn_shared_workspace_bytes(int B, int h_q, int h_kv, int d, int n_max,
                                                  int prefix_len, int dtype, int* status);

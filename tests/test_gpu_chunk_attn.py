@@ -213,3 +213,56 @@ def test_graph_streams_and_threads():
         g.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(o, want) for o in outs)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_units_cut_between(d):
+    """Units of one and two streams, cut wherever a piece ends, in a cache of 2500 rows."""
+    B, T = 12, 70
+    q, K, V = make(B, T, 20, 5, d, 2500, seed=15)
+    news = [(b * 29) % (T + 1) for b in range(B)]
+    lens = [min(2500, m + (b * 997) % 2450) for b, m in enumerate(news)]
+    run(q, K, V, lens, news, torch.bfloat16)
+    run(q, K, V, lens, news, torch.float32, window=900, prefix=3)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_units_taken_over(d):
+    """Several times as many units as SMs, whole, many of them without tokens."""
+    B, T = 20, 70
+    q, K, V = make(B, T, 24, 12, d, 900, seed=16)
+    news = [(b * 223) % (T + 1) if b % 3 else 0 for b in range(B)]
+    lens = [min(900, m + (b * 497) % 750) for b, m in enumerate(news)]
+    run(q, K, V, lens, news, torch.bfloat16)
+    run(q, K, V, [T] * B, [T] * B, torch.float32)
+    run(q, K, V, [900] + [1] * (B - 1), [T] + [1] * (B - 1), torch.bfloat16, window=300, prefix=2)
+    run(q, K, V, [0] * B, [0] * B, torch.bfloat16)
+    # lengths out of range are reported whoever takes the sequence's units
+    for b in (0, 7, B - 1):
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        api.chunk_attn(q, K, V, i32([901 if x == b else 700 for x in range(B)]), dev_error=err)
+        assert int(err) == api.DEVERR_SEQ_LEN
+
+
+def test_units_taken_over_at_once():
+    """Two streams and two graphs at a time, whole units: the same bits as alone."""
+    q, K, V = make(12, 500, 16, 8, 128, 1000, seed=17)
+    lens = i32([500 + (b * 101) % 501 for b in range(12)])
+    want = api.chunk_attn(q, K, V, lens, out_dtype=torch.bfloat16)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = [torch.zeros_like(want) for _ in streams]
+    graphs = []
+    for s, o in zip(streams, outs):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            for _ in range(3):
+                api.chunk_attn(q, K, V, lens, out=o)
+        graphs.append(g)
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(3):
+        for s, o, g in zip(streams, outs, graphs):
+            api.chunk_attn(q, K, V, lens, out=o, stream=s)
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in outs)
