@@ -1335,6 +1335,14 @@ __device__ __forceinline__ void merge_row(const AttendParams& p, long long off, 
   }
 }
 
+// The first and last CTA noted for a unit; (0, -1) where there are none.  A CTA whose wait ran
+// out notes nothing for the rest of its piece, whose words then hold what the workspace held: only
+// CTAs of the grid, in order, are followed.
+__device__ __forceinline__ int2 noted_ctas(const AttendParams& p, bool there, int unit) {
+  const int2 c = there ? __ldcg(p.unit_ctas + unit) : make_int2(0, -1);
+  return c.x >= 0 && c.x <= c.y && c.y < p.ctas ? c : make_int2(0, -1);
+}
+
 // Behind a shared prefix: every row, of the CTAs noted for its units.
 template <int D>
 __global__ void __launch_bounds__(kAttendCombineWarps * 32)
@@ -1352,9 +1360,8 @@ __global__ void __launch_bounds__(kAttendCombineWarps * 32)
   const int pre_unit = kvh * p.prefix_tiles + mt;
   const int qt = hh / kAttendRows;
   const int own_unit = ((p.q_tiles - 1 - qt) * p.B + b) * p.h_kv + kvh;
-  int2 pre = make_int2(0, -1), mine = make_int2(0, -1);
-  if (p.P > 0) pre = __ldcg(p.unit_ctas + pre_unit);
-  if (own) mine = __ldcg(p.unit_ctas + p.h_kv * p.prefix_tiles + own_unit);
+  const int2 pre = noted_ctas(p, p.P > 0, pre_unit);
+  const int2 mine = noted_ctas(p, own, p.h_kv * p.prefix_tiles + own_unit);
   merge_row<D>(p, b * p.out_stride[0] + head * p.out_stride[1],
                (long long)(pre_unit + pre.x) * p.pitch + flat % kAttendRows, p.pitch,
                pre.y - pre.x + 1,
