@@ -51,11 +51,13 @@ struct RopeVec<float> {
   }
 };
 
+// (Ordinary loads, here and of the weights: the grid before may still write them when this one
+// starts, which the read-only path must not see.)
 template <int N>
 __device__ __forceinline__ void load_floats(const float* p, float* x) {
 #pragma unroll
   for (int i = 0; i < N; i += 4) {
-    const float4 v = __ldg(reinterpret_cast<const float4*>(p + i));
+    const float4 v = *reinterpret_cast<const float4*>(p + i);
     x[i] = v.x, x[i + 1] = v.y, x[i + 2] = v.z, x[i + 3] = v.w;
   }
 }
@@ -172,8 +174,8 @@ __global__ void __launch_bounds__(kRopeThreads) kv_append_rope_kernel(const Rope
   const T* weight = static_cast<const T*>(p.weight[kind]);
   uint4 w_raw[2] = {};
   if (weight && on) {
-    w_raw[0] = __ldg(reinterpret_cast<const uint4*>(weight + pa * N));
-    w_raw[1] = __ldg(reinterpret_cast<const uint4*>(weight + pb * N));
+    w_raw[0] = *reinterpret_cast<const uint4*>(weight + pa * N);
+    w_raw[1] = *reinterpret_cast<const uint4*>(weight + pb * N);
   }
 #pragma unroll
   for (int u = 0; u < HC; ++u) {
