@@ -1006,6 +1006,8 @@ def kv_append_rope(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor, K:
             or not (cos.is_contiguous() and sin.is_contiguous()):
         raise ValueError("cos and sin must be contiguous float32 tensors [n_angles, rot / 2] on the "
                          "cache's device")
+    if angles[0] >= 1 << 31 or angles[1] >= 1 << 30:   # (the library would take 32 bits of them)
+        raise ValueError("cos and sin must have less than 2^31 rows, of at most d_k / 2 angles")
     for t in (q_weight, k_weight):
         if t is not None and (t.dtype is not dtype or t.shape != (d_k,) or t.get_device() != device
                               or not t.is_contiguous()):
@@ -1135,6 +1137,8 @@ def decode_attn_shared(q: torch.Tensor, K_prefix: torch.Tensor, V_prefix: torch.
     prefix_max = shape[1]
     if prefix_len is None:
         prefix_len = prefix_max
+    elif not -(1 << 31) <= prefix_len < 1 << 31:   # (the library would take 32 bits of it)
+        raise ValueError("prefix_len must be between 0 and prefix_max")
     err = None if dev_error is None else _error_word(dev_error, device)
     if scale is None:
         scale = 1.0 / math.sqrt(d)
