@@ -983,6 +983,77 @@ int check_stride(long long stride, int es) {
   return stride * es % 16 != 0 ? DA_ERR_ALIGN : DA_OK;
 }
 
+// Rows in memory: `run` bytes at `at` plus any index below n[i] times step[i] (bytes), all of
+// them within `reach` bytes.
+struct RowSet {
+  uintptr_t at;
+  long long run, step[3], reach;
+  int n[3];
+};
+constexpr long long kMostReach = 1LL << 60;  // no memory is that large
+RowSet one_span(const void* at, long long bytes) {
+  return RowSet{reinterpret_cast<uintptr_t>(at), bytes, {0, 0, 0}, bytes, {1, 1, 1}};
+}
+RowSet strided_rows(const void* at, const long long* strides, int B, int h, int T, int d, int es) {
+  RowSet r = one_span(at, (long long)d * es);
+  const int n[3] = {B, h, T};
+  for (int i = 0; i < 3; ++i) {
+    r.n[i] = n[i];
+    r.step[i] = strides[i] * es;
+    if (n[i] > 1 && r.step[i] > kMostReach / n[i]) r.reach = kMostReach;
+    if (r.reach < kMostReach) r.reach += (n[i] - 1) * r.step[i];
+  }
+  return r;
+}
+
+// Whether two of them share a byte.  Rows of one start a sum of steps away from rows of the
+// other, each step taken up to n - 1 times forward (its own) or back (the other's): the sums that
+// lie less than a run away are looked for from the largest step down.
+struct RowSteps {
+  long long step[6], lo[6], hi[6];      // times that each is taken
+  long long least[7], most[7];          // sums of what follows
+  int count = 0, budget = 1 << 14;
+  void add(long long s, long long l, long long h) {
+    int i = 0;
+    while (i < count && step[i] > s) ++i;
+    if (i < count && step[i] == s) {
+      lo[i] += l, hi[i] += h;
+      return;
+    }
+    for (int k = count++; k > i; --k) step[k] = step[k - 1], lo[k] = lo[k - 1], hi[k] = hi[k - 1];
+    step[i] = s, lo[i] = l, hi[i] = h;
+  }
+  static long long floor_div(long long a, long long b) { return a / b - (a % b < 0); }
+  // a sum from step i on in (above, below)?
+  bool reach(int i, long long above, long long below) {
+    if (most[i] <= above || least[i] >= below) return false;
+    if (i == count) return true;
+    if (--budget < 0) return false;     // (strides that nest in neither order: not told apart)
+    const long long from = floor_div(above - most[i + 1], step[i]) + 1;
+    const long long to = -(floor_div(least[i + 1] - below, step[i]) + 1);
+    for (long long x = from < lo[i] ? lo[i] : from; x <= to && x <= hi[i]; ++x)
+      if (reach(i + 1, above - x * step[i], below - x * step[i])) return true;
+    return false;
+  }
+};
+bool share_bytes(const RowSet& a, const RowSet& b) {
+  if (!a.at || !b.at) return false;
+  const long long delta = (long long)(a.at - b.at);
+  if (delta >= b.reach || -delta >= a.reach) return false;
+  if (a.reach >= kMostReach || b.reach >= kMostReach) return false;
+  RowSteps r;
+  for (int i = 0; i < 3; ++i) {
+    if (a.n[i] > 1 && a.step[i] > 0) r.add(a.step[i], 0, a.n[i] - 1);
+    if (b.n[i] > 1 && b.step[i] > 0) r.add(b.step[i], 1 - b.n[i], 0);
+  }
+  r.least[r.count] = r.most[r.count] = 0;
+  for (int i = r.count - 1; i >= 0; --i) {
+    r.least[i] = r.least[i + 1] + r.lo[i] * r.step[i];
+    r.most[i] = r.most[i + 1] + r.hi[i] * r.step[i];
+  }
+  return r.reach(0, -a.run - delta, b.run - delta);
+}
+
 // Sizes and types shared by the write into and the read from a block-scaled cache.
 int check_blocks(int B, int h_kv, int T, int d, int n_max, int block, int dtype, int io_dtype) {
   if (!is_q8(dtype) || (io_dtype != DA_FP32 && io_dtype != DA_BF16)) return DA_ERR_DTYPE;
@@ -1144,6 +1215,29 @@ int kv_append_rope(const void* q, const void* k_new, const void* v_new, const lo
     }
     (x < 3 ? a.x_elems[x] : a.out_elems) = last;
   }
+  // no output over an input or another output, but q_out on q itself
+  const int es = elem_size(dtype);
+  const long long cache_rows = (long long)B * h_kv * n_max, angle_bytes = (long long)n_angles * rot * 2;
+  const RowSet out[3] = {strided_rows(q_out, out_strides, B, h_q, T, d_k, es),
+                         one_span(K, cache_rows * d_k * es), one_span(V, cache_rows * d_v * es)};
+  const RowSet in[10] = {strided_rows(q, q_strides, B, h_q, T, d_k, es),
+                         strided_rows(k_new, k_strides, B, h_kv, T, d_k, es),
+                         strided_rows(v_new, v_strides, B, h_kv, T, d_v, es),
+                         one_span(pos, 4LL * B),
+                         one_span(n_new, 4LL * B),
+                         one_span(angle_pos, 4LL * B),
+                         one_span(cos, angle_bytes),
+                         one_span(sin, angle_bytes),
+                         one_span(q_weight, (long long)d_k * es),
+                         one_span(k_weight, (long long)d_k * es)};
+  bool in_place = q == q_out;
+  for (int i = 0; i < 3; ++i) in_place = in_place && (out[0].n[i] == 1 || q_strides[i] == out_strides[i]);
+  for (int y = 0; y < 3; ++y) {
+    for (int x = 0; x < 10; ++x)
+      if (!(x == 0 && y == 0 && in_place) && share_bytes(out[y], in[x])) return DA_ERR_SHAPE;
+    for (int x = 0; x < y; ++x)
+      if (share_bytes(out[y], out[x])) return DA_ERR_SHAPE;
+  }
   int dev, sms;
   const int st = current_device(&dev, &sms);
   if (st != DA_OK) return st;
@@ -1287,6 +1381,14 @@ int run_attend(const AttendCall& c, void* workspace, size_t workspace_bytes, int
     p.out_stride[i] = c.out_strides[i];
     p.q_elems += (shape[i] - 1) * c.q_strides[i];
     p.out_elems += (shape[i] - 1) * c.out_strides[i];
+  }
+  if (!shared) {  // out over no input
+    const RowSet out = strided_rows(c.out, c.out_strides, c.B, c.h_q, c.T, c.d, p.out_bf16 ? 2 : 4);
+    const long long cache_bytes = (long long)c.B * c.h_kv * c.n_max * c.d * 2;
+    if (share_bytes(out, strided_rows(c.q, c.q_strides, c.B, c.h_q, c.T, c.d, 2)) ||
+        share_bytes(out, one_span(c.K, cache_bytes)) || share_bytes(out, one_span(c.V, cache_bytes)) ||
+        share_bytes(out, one_span(c.seq_lens, 4LL * c.B)) || share_bytes(out, one_span(c.n_new, 4LL * c.B)))
+      return DA_ERR_SHAPE;
   }
   int dev, sms;
   if ((st = current_device(&dev, &sms)) != DA_OK) return st;

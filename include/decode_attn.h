@@ -503,7 +503,8 @@ DA_API int kv_read_q8b(const void* K, const void* V, const float* k_scale, const
  *                  i * strides[2] + j (strides in elements, host arrays,
  *                  multiples of 16 bytes, >= 0); 16-byte aligned.  Tokens at or
  *                  past m are neither read nor written.  q_out may be q itself
- *                  with the same strides; else no output may overlap an input.
+ *                  with the same strides; else no output may overlap an input or
+ *                  another output (refused: DA_ERR_SHAPE).
  *   K [B, h_kv, n_max, d_k], V [B, h_kv, n_max, d_v] : the caches, dtype
  *   cos, sin     : device float32 [n_angles, rot / 2], 16-byte aligned
  *   rot          : a multiple of 16, at most d_k
@@ -534,7 +535,7 @@ DA_API int kv_append_rope(const void* q, const void* k_new, const void* v_new,
  *   q, out    : device [B, h_q, T, d]; strides as in kv_append_rope.  q is bf16, out
  *               float32, or bf16 when dtype (DA_BF16) carries DA_OUT_BF16.  Outputs
  *               of tokens at or past m are left as they were.  out may not overlap
- *               an input, nor itself.
+ *               an input (refused: DA_ERR_SHAPE), nor itself.
  *   K, V      : device bf16 [B, h_kv, n_max, d];  d = 64 or 128
  *   seq_lens  : device int32 [B], the rows with the new tokens; outside [0, n_max]:
  *               clamped.  An n_new outside [0, T] is clamped; of more new tokens
