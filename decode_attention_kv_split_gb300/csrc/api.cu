@@ -1373,14 +1373,14 @@ int run_attend(const AttendCall& c, void* workspace, size_t workspace_bytes, int
   da::AttendParams p{};
   p.out_bf16 = (c.dtype & DA_OUT_BF16) != 0;
   const long long shape[3] = {c.B, c.h_q, c.T};
-  p.q_elems = p.out_elems = c.d;
+  long long q_elems = c.d, out_elems = c.d;
   for (int i = 0; i < 3; ++i) {
     if ((st = check_stride(c.q_strides[i], 2)) != DA_OK) return st;
     if ((st = check_stride(c.out_strides[i], p.out_bf16 ? 2 : 4)) != DA_OK) return st;
     p.q_stride[i] = c.q_strides[i];
     p.out_stride[i] = c.out_strides[i];
-    p.q_elems += (shape[i] - 1) * c.q_strides[i];
-    p.out_elems += (shape[i] - 1) * c.out_strides[i];
+    q_elems += (shape[i] - 1) * c.q_strides[i];
+    out_elems += (shape[i] - 1) * c.out_strides[i];
   }
   if (!shared) {  // out over no input
     const RowSet out = strided_rows(c.out, c.out_strides, c.B, c.h_q, c.T, c.d, p.out_bf16 ? 2 : 4);
@@ -1441,6 +1441,9 @@ int run_attend(const AttendCall& c, void* workspace, size_t workspace_bytes, int
     p.by_batch = da::FastDiv(uint32_t(p.B));
     p.q = static_cast<const char*>(c.q) + b0 * c.q_strides[0] * 2;
     p.out = static_cast<char*>(c.out) + b0 * c.out_strides[0] * (p.out_bf16 ? 2 : 4);
+    // (from the launch's first sequence on)
+    p.q_elems = q_elems - b0 * c.q_strides[0];
+    p.out_elems = out_elems - b0 * c.out_strides[0];
     p.seq_lens = c.seq_lens + b0;
     p.n_new = c.n_new ? c.n_new + b0 : nullptr;
     p.prefix_tiles = shared ? (p.B * p.group + da::kAttendRows - 1) / da::kAttendRows : 0;
