@@ -1394,8 +1394,9 @@ int run_attend(const AttendCall& c, void* workspace, size_t workspace_bytes, int
   if ((st = current_device(&dev, &sms)) != DA_OK) return st;
   // a window and its first rows, behind the first of a unit's tokens
   const long long seen = c.window == 0 ? c.n_max : (long long)c.window + c.prefix + da::kAttendRows;
-  plan_attend(c.B, c.T, c.h_q, c.h_kv, c.d, c.n_max, c.dtype, c.P, sms,
-              seen < c.n_max ? seen : c.n_max, &plan);
+  if ((st = plan_attend(c.B, c.T, c.h_q, c.h_kv, c.d, c.n_max, c.dtype, c.P, sms,
+                        seen < c.n_max ? seen : c.n_max, &plan)) != DA_OK)
+    return st;
   if (plan.list && (!workspace || workspace_bytes < plan.bytes(c.d))) return DA_ERR_WORKSPACE;
   if (plan.list && !aligned16(workspace)) return DA_ERR_ALIGN;
   da::AttendMaps maps;
