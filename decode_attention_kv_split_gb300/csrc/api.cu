@@ -1273,6 +1273,8 @@ struct AttendPlan {
 // workspace asked for without the window's is never too small: fewer rows, fewer cuts).
 int plan_attend(int B, int T, int h_q, int h_kv, int d, int n_max, int dtype, int P, int sms,
                 long long seen, AttendPlan* plan) {
+  if ((dtype & DA_BF16_WEIGHTS) && !(dtype & DA_OUT_BF16)) return DA_ERR_DTYPE;
+  dtype &= ~DA_BF16_WEIGHTS;
   DtypeArg dt;
   if (!parse_dtype(dtype, &dt)) return DA_ERR_DTYPE;
   if (dt.kv != DA_FP32 && dt.kv != DA_BF16) return DA_ERR_DTYPE;
@@ -1372,6 +1374,7 @@ int run_attend(const AttendCall& c, void* workspace, size_t workspace_bytes, int
     return DA_ERR_ALIGN;
   da::AttendParams p{};
   p.out_bf16 = (c.dtype & DA_OUT_BF16) != 0;
+  p.bf16_weights = (c.dtype & DA_BF16_WEIGHTS) != 0;
   const long long shape[3] = {c.B, c.h_q, c.T};
   long long q_elems = c.d, out_elems = c.d;
   for (int i = 0; i < 3; ++i) {

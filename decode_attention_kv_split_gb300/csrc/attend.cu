@@ -16,8 +16,8 @@
 // The MMAs of one stream run under the softmax of the other.  A running maximum
 // may lag behind by 2^8 before O is rescaled in TMEM; every exponent is taken
 // against the same maximum that scales O, so that changes nothing but rounding.
-// P is rounded to bf16 (2^-8 of each weight, as the output is); with a float32
-// output its bf16 remainder is multiplied as well (2^-16).
+// P is multiplied as a bf16 and its bf16 remainder (2^-16 of each weight, as the decode
+// kernels do); where the caller asks for it as one bf16 (2^-8), a third of the MMAs less.
 //
 // A unit of at most 128 query rows (few tokens, one sequence's group) uses both
 // streams for the same rows on alternate tiles and merges them at the end.
@@ -1493,10 +1493,10 @@ cudaError_t launch_attend_cfg(const AttendParams& p, const AttendMaps& m, int gr
 cudaError_t launch_attend(const AttendParams& p, const AttendMaps& m, int d, int grid,
                           cudaStream_t stream) {
   if (d == 128)
-    return p.out_bf16 ? launch_attend_cfg<AttendCfg<128>, false>(p, m, grid, stream)
-                      : launch_attend_cfg<AttendCfg<128>, true>(p, m, grid, stream);
-  return p.out_bf16 ? launch_attend_cfg<AttendCfg<64>, false>(p, m, grid, stream)
-                    : launch_attend_cfg<AttendCfg<64>, true>(p, m, grid, stream);
+    return p.bf16_weights ? launch_attend_cfg<AttendCfg<128>, false>(p, m, grid, stream)
+                          : launch_attend_cfg<AttendCfg<128>, true>(p, m, grid, stream);
+  return p.bf16_weights ? launch_attend_cfg<AttendCfg<64>, false>(p, m, grid, stream)
+                        : launch_attend_cfg<AttendCfg<64>, true>(p, m, grid, stream);
 }
 
 cudaError_t launch_attend_combine(const AttendParams& p, int d, cudaStream_t stream) {

@@ -422,6 +422,7 @@ struct AttendParams {
   int window, prefix;            // 0: unlimited; rows always seen
   int shared, P;                 // shared prefix: on, its rows
   int out_bf16;
+  int bf16_weights;              // weights as one bf16, without its remainder (host)
   int negate;                    // q times -1 (negative scale)
   float scale_log2;              // |scale| * log2 e; at least float's smallest normal number, so
                                  // that a masked -inf stays one

@@ -78,6 +78,14 @@ typedef enum {
  */
 #define DA_OUT_BF16 0x100
 
+/*
+ * Flag OR-ed into the dtype argument of chunk_attn, decode_attn_shared and their
+ * workspace queries, beside DA_OUT_BF16: the softmax's weights are multiplied with V as
+ * one bf16 each (rounded by at most 2^-8 of themselves) instead of a bf16 and its bf16
+ * remainder (2^-16).  A third less of the tensor work.
+ */
+#define DA_BF16_WEIGHTS 0x400
+
 /* Bits the kernels OR into the optional device error word. */
 #define DA_DEVERR_SEQ_LEN 1 /* some seq_lens[b] outside [0, n_max]: clamped into range */
 #define DA_DEVERR_POS 2     /* some kv_append pos[b] outside [0, n_max): that row not written */
@@ -544,8 +552,8 @@ DA_API int kv_append_rope(const void* q, const void* k_new, const void* v_new,
  *   Rows that no token of a sequence sees may hold anything, NaN too.  V rows that
  *   some token sees must be finite: the tokens of a tile share its products, and an
  *   infinity or NaN in one reaches also those that do not see it.
- *   Weights are multiplied as bf16 for a bf16 out (each rounded by at most 2^-8 of
- *   itself), as bf16 and its bf16 remainder for a float32 out (2^-16).
+ *   Weights are multiplied as a bf16 and its bf16 remainder (each rounded by at most
+ *   2^-16 of itself); as one bf16 (2^-8) where dtype carries DA_BF16_WEIGHTS.
  *   workspace : chunk_attn_workspace_bytes(...) bytes, 16-byte aligned (may be NULL
  *               when that is 0); as decode_attn_ex's.
  * One launch, and a second one where units of the work may be cut along the rows.
