@@ -1415,6 +1415,7 @@ int run_attend(const AttendCall& c, void* workspace, size_t workspace_bytes, int
            DA_OK))
     return st;
   p.dev_error = dev_error;
+  p.V = c.V;
   p.T = c.T, p.h_q = c.h_q, p.h_kv = c.h_kv, p.group = c.h_q / c.h_kv, p.n_max = c.n_max;
   // (positions plus a window stay inside 32 bits)
   p.window = c.window < (1 << 30) ? c.window : 1 << 30;

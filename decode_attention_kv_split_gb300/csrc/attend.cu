@@ -32,8 +32,8 @@
 // start (7 us to the first scores), 3 to 4 us an item beside its tiles, 5 to 8 us to merge.
 //
 // Roles (384 threads): warps 0-3 and 4-7 the softmax of streams 0 and 1, warp 8
-// the items and the TMA loads, warp 9 the MMAs, warp 10 clears V rows that may hold
-// anything (11 fills their warpgroup, which gives registers to the others).  TMEM: S 2 x 128 columns, O 2 x d.
+// the items and the TMA loads, warp 9 the MMAs, warp 10 looks through V rows that some
+// query does not see (11 fills their warpgroup, which gives registers to the others).  TMEM: S 2 x 128 columns, O 2 x d.
 #include <math.h>
 
 #include "common.cuh"
@@ -99,12 +99,27 @@ __device__ __forceinline__ int tile_row(const Item& w, int k) {
   return (k < w.pt ? k : w.first + k - w.pt) * kTile;
 }
 
-// Whether the V tile at row r0 holds rows that no query of the sequence sees: they
-// may hold anything, even NaN, and a weight of zero times NaN is NaN, so they are
-// cleared.  In the tiles of an item that is the end of the always-seen rows, the
-// window's first tile and the last tile.
-__device__ __forceinline__ bool edge_tile(const AttendParams& p, const Item& w, int r0) {
-  return r0 + kTile > w.n || (r0 < w.clear_lo && r0 + kTile > p.prefix);
+// Rows that some query of a unit does not see: those past `hi`, its first query's, and of
+// [prefix, lo) the window.
+struct PartSeen {
+  int hi, lo;
+};
+__device__ __forceinline__ PartSeen part_seen(const AttendParams& p, const Item& w) {
+  return {w.past + p.by_group.div(w.row0),
+          p.window ? max(0, w.past + p.by_group.div(w.row0 + w.rows - 1) + 1 - p.window) : 0};
+}
+
+// Whether the V tile at row r0 holds such rows.  A weight of zero times an infinity or NaN is
+// NaN, so a warp looks through them first: rows that no query of the sequence sees may hold
+// anything and are cleared; of the others (MANY: sequences of more than one token) what is not
+// finite is cleared too, and added behind the item to the outputs of the queries that see it.
+// In the tiles of an item that is the end of the always-seen rows, the window's first tiles and
+// the last ones.
+template <bool MANY>
+__device__ __forceinline__ bool edge_tile(const AttendParams& p, const Item& w, const PartSeen& part,
+                                          int r0) {
+  if (!MANY) return r0 + kTile > w.n || (r0 < w.clear_lo && r0 + kTile > p.prefix);
+  return r0 + kTile - 1 > part.hi || (r0 < part.lo && r0 + kTile > p.prefix);
 }
 
 // Unit of row tile qt of a sequence of n rows, the last m of them new.
@@ -551,7 +566,7 @@ __device__ __forceinline__ bool alternates(const Item& w) { return w.rows <= kTi
 __device__ __forceinline__ int lookahead(const Item& w) { return alternates(w) ? 2 : 1; }
 
 // ---- the items and their loads: one thread
-template <class Cfg>
+template <class Cfg, bool MANY>
 __device__ __forceinline__ void attend_load(const AttendParams& p, const AttendMaps& maps,
                                             const AttendShared<Cfg>& sh) {
   constexpr int kSlots = Cfg::kSlots;
@@ -616,6 +631,7 @@ __device__ __forceinline__ void attend_load(const AttendParams& p, const AttendM
     const CUtensorMap* mv = pre ? &maps.v_prefix : &maps.v;
     const int z = pre ? w.kvh : (p.b_offset + w.b) * p.h_kv + w.kvh;
     const int count = w.count, ahead = lookahead(w);
+    const PartSeen part = MANY ? part_seen(p, w) : PartSeen{};
     auto load = [&](const CUtensorMap* map, int j) {
       if (!ok) return;
       if (!(ok = free_place())) return;
@@ -626,8 +642,8 @@ __device__ __forceinline__ void attend_load(const AttendParams& p, const AttendM
       }
 #endif
       const int y = tile_row(w, w.begin + j);
-      // a V tile with rows to clear goes to warp 10 first, which says when it is full
-      const bool edge = map == mv && edge_tile(p, w, y);
+      // a V tile to look through goes to warp 10 first, which says when it is full
+      const bool edge = map == mv && edge_tile<MANY>(p, w, part, y);
       const uint32_t bar = edge ? sh.edge(edges++) : sh.full(at.slot);
       mbar_arrive_expect_tx(bar, Cfg::kTileBytes);
       const uint32_t dst = smem_u32(sh.ring) + at.slot * Cfg::kTileBytes;
@@ -785,8 +801,59 @@ __device__ __forceinline__ void attend_mma(const AttendParams& p, const AttendSh
   __syncwarp();
 }
 
-// ---- V rows to clear: a warp
+// A bit of 0x80008000 for each infinity or NaN of two bf16, among other bits.
+__device__ __forceinline__ uint32_t not_finite2(uint32_t w) { return (w & 0x7f807f80u) + 0x00800080u; }
+constexpr uint32_t kNotFinite2 = 0x80008000u;
+// All ones over each of them that is finite.
+__device__ __forceinline__ uint32_t finite_halves(uint32_t w) {
+  const uint32_t f = not_finite2(w);
+  return (f & 0x8000u ? 0u : 0xffffu) | (f & 0x80000000u ? 0u : 0xffff0000u);
+}
+
+// What was not finite in V, and was cleared, goes to the outputs of an item's queries that see it:
+// they become infinite or NaN in its column.  A lane a query; rare.
 template <class Cfg>
+__device__ __forceinline__ void add_values(const AttendParams& p, const Item& w, const PartSeen& part) {
+  constexpr int D = Cfg::D;
+  const long long v0 = ((long long)(p.b_offset + w.b) * p.h_kv + w.kvh) * p.n_max;
+  const uint16_t* V = static_cast<const uint16_t*>(p.V) + v0 * D;
+  const bool narrow = w.part < 0 && p.out_bf16;
+#pragma unroll 1
+  for (int r = threadIdx.x & 31; r < w.rows; r += 32) {
+    const int flat = w.row0 + r, t = p.by_group.div(flat), head = w.kvh * p.group + flat - t * p.group;
+    const int hi = w.past + t, lo = p.window ? hi + 1 - p.window : 0;
+    const long long off = w.part >= 0 ? ((long long)w.part + r) * D
+                                      : w.b * p.out_stride[0] + head * p.out_stride[1] + t * p.out_stride[2];
+    if (!DA_IN(p, off + D - 1, w.part >= 0 ? p.part_rows * D : p.out_elems)) continue;
+    char* y = static_cast<char*>(w.part >= 0 ? static_cast<void*>(p.o_part) : p.out) + off * (narrow ? 2 : 4);
+#pragma unroll 1
+    for (int j = 0; j < w.count; ++j) {
+      const int r0 = tile_row(w, w.begin + j), end = min(min(r0 + kTile, w.n), hi + 1);
+      if (!edge_tile<true>(p, w, part, r0)) continue;
+#pragma unroll 1
+      for (int l = r0; l < end; ++l) {
+        // (seen by this query, not by each of them)
+        if ((l < lo && l >= p.prefix) || (l <= part.hi && (l >= part.lo || r0 + kTile <= p.prefix))) continue;
+        if (!DA_IN(p, v0 + l, (long long)(p.b_offset + p.B) * p.h_kv * p.n_max)) continue;
+#pragma unroll 1
+        for (int c = 0; c < D; ++c) {
+          const uint32_t v = V[(long long)l * D + c];
+          if (!(not_finite2(v) & 0x8000u)) continue;
+          const float f = __uint_as_float(v << 16);
+          if (narrow) {
+            __nv_bfloat16* at = reinterpret_cast<__nv_bfloat16*>(y) + c;
+            *at = __float2bfloat16_rn(__bfloat162float(*at) + f);
+          } else {
+            reinterpret_cast<float*>(y)[c] += f;
+          }
+        }
+      }
+    }
+  }
+}
+
+// ---- V rows that some query does not see: a warp
+template <class Cfg, bool MANY>
 __device__ __forceinline__ void attend_clear(const AttendParams& p, const AttendShared<Cfg>& sh) {
   constexpr int kChunks = Cfg::D / 8;  // 16-byte pieces of a row
   const int lane = threadIdx.x & 31;
@@ -797,19 +864,46 @@ __device__ __forceinline__ void attend_clear(const AttendParams& p, const Attend
     const int count = w.count;
     if (count < 0) return;
     const int ahead = lookahead(w), seen_end = w.n, clear_lo = w.clear_lo;
+    const PartSeen part = MANY ? part_seen(p, w) : PartSeen{};
+    bool bad = false;                  // some of V was not finite
     for (int j = 0; j < count; ++j) {
       const int r0 = tile_row(w, w.begin + j);
-      if (!edge_tile(p, w, r0)) continue;
+      if (!edge_tile<MANY>(p, w, part, r0)) continue;
       if (!sh.wait_warp(p, sh.edge(edges), (edges / kEdges) & 1)) return;
       ++edges;
       const int slot = (place + j + min(count, ahead + j)) % Cfg::kSlots;  // V_j's
       uint8_t* vt = sh.ring + size_t(slot) * Cfg::kTileBytes;
+      auto piece = [&](int x) -> uint4& {
+        return *reinterpret_cast<uint4*>(vt + tc5::sw128(x / kChunks, (x % kChunks) * 8, kTile));
+      };
+      if (!MANY || r0 + kTile > seen_end || (r0 < clear_lo && r0 + kTile > p.prefix)) {
 #pragma unroll 8
-      for (int x = lane; x < kTile * kChunks; x += 32) {
-        const int row = r0 + x / kChunks;
-        if (row >= seen_end || (row < clear_lo && row >= p.prefix))
-          *reinterpret_cast<uint4*>(vt + tc5::sw128(x / kChunks, (x % kChunks) * 8, kTile)) =
-              make_uint4(0, 0, 0, 0);
+        for (int x = lane; x < kTile * kChunks; x += 32) {
+          const int row = r0 + x / kChunks;
+          if (row >= seen_end || (row < clear_lo && row >= p.prefix)) piece(x) = make_uint4(0, 0, 0, 0);
+        }
+      }
+      if constexpr (MANY) {  // rows that some queries do not see
+        __syncwarp();
+        auto look = [&](int from, int to) {
+          uint32_t found = 0;
+#pragma unroll 8
+          for (int x = from * kChunks + lane; x < to * kChunks; x += 32) {
+            const uint4 v = piece(x);
+            found |= not_finite2(v.x) | not_finite2(v.y) | not_finite2(v.z) | not_finite2(v.w);
+          }
+          if (!__any_sync(0xffffffffu, (found & kNotFinite2) != 0)) return;
+          bad = true;
+          for (int x = from * kChunks + lane; x < to * kChunks; x += 32) {
+            uint4 v = piece(x);
+            v.x &= finite_halves(v.x), v.y &= finite_halves(v.y);
+            v.z &= finite_halves(v.z), v.w &= finite_halves(v.w);
+            piece(x) = v;
+          }
+        };
+        const int end = min(seen_end - r0, kTile), past = min(max(part.hi + 1 - r0, 0), kTile);
+        look(past, end);
+        if (r0 + kTile > p.prefix) look(0, min(part.lo - r0, min(past, end)));
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -817,6 +911,18 @@ __device__ __forceinline__ void attend_clear(const AttendParams& p, const Attend
     }
     place = (place + 2 * count + 1) % Cfg::kSlots;
     __syncwarp();
+    if constexpr (MANY) {
+      if (bad) {
+        const Item mine = w;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sh.item_empty(k));
+        // (which completes when the item's outputs have been written, and not again before the next
+        // arrival here)
+        if (!sh.wait_warp(p, sh.item_empty(k), (k >> 1) & 1)) return;
+        add_values<Cfg>(p, mine, part);
+        continue;
+      }
+    }
     if (lane == 0) mbar_arrive(sh.item_empty(k));
   }
 }
@@ -1180,7 +1286,7 @@ __device__ __forceinline__ void attend_softmax(const AttendParams& p, const Atte
   }
 }
 
-template <class Cfg, bool WIDE_P>
+template <class Cfg, bool WIDE_P, bool MANY>
 __global__ void __launch_bounds__(kAttendThreads, 1)
     attend_kernel(const __grid_constant__ AttendMaps maps, const AttendParams p) {
   constexpr uint32_t kTmemCols = 512;
@@ -1251,14 +1357,14 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == 8) {
-      if (lane == 0) attend_load<Cfg>(p, maps, sh);
+      if (lane == 0) attend_load<Cfg, MANY>(p, maps, sh);
     } else if (warp == 9) {
       attend_mma<Cfg, WIDE_P>(p, sh);
       named_bar_sync(2, 288);
       tc5::fence_after();
       tc5::dealloc(sh.tmem, kTmemCols);
     } else if (warp == 10) {
-      attend_clear<Cfg>(p, sh);
+      attend_clear<Cfg, MANY>(p, sh);
     }
     return;
   }
@@ -1477,26 +1583,36 @@ __global__ void __launch_bounds__(kAttendCombineWarps * 32, 4)
   }
 }
 
-template <class Cfg, bool WIDE_P>
+template <class Cfg, bool WIDE_P, bool MANY>
 cudaError_t launch_attend_cfg(const AttendParams& p, const AttendMaps& m, int grid,
                               cudaStream_t stream) {
   static std::atomic<unsigned long long> smem_set{0};
   const cudaError_t e =
-      set_smem_limit_once(attend_kernel<Cfg, WIDE_P>, Cfg::kSmemBytes, smem_set);
+      set_smem_limit_once(attend_kernel<Cfg, WIDE_P, MANY>, Cfg::kSmemBytes, smem_set);
   if (e != cudaSuccess) return e;
-  return launch_dependent(attend_kernel<Cfg, WIDE_P>, grid, kAttendThreads, Cfg::kSmemBytes, stream,
-                          m, p);
+  return launch_dependent(attend_kernel<Cfg, WIDE_P, MANY>, grid, kAttendThreads, Cfg::kSmemBytes,
+                          stream, m, p);
+}
+
+// One token a sequence (and so behind a shared prefix) goes without the look through rows that
+// only some queries see: 36.5 us for 38.3 (16 sequences behind 8192 rows), 141 for 147 (64 behind
+// 32768).  Elsewhere that look costs 1 % (prompts 1020 -> 1029 us, ragged window 217 -> 220).
+template <class Cfg>
+cudaError_t launch_attend_d(const AttendParams& p, const AttendMaps& m, int grid,
+                            cudaStream_t stream) {
+  if (p.T > 1)
+    return p.bf16_weights ? launch_attend_cfg<Cfg, false, true>(p, m, grid, stream)
+                          : launch_attend_cfg<Cfg, true, true>(p, m, grid, stream);
+  return p.bf16_weights ? launch_attend_cfg<Cfg, false, false>(p, m, grid, stream)
+                        : launch_attend_cfg<Cfg, true, false>(p, m, grid, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_attend(const AttendParams& p, const AttendMaps& m, int d, int grid,
                           cudaStream_t stream) {
-  if (d == 128)
-    return p.bf16_weights ? launch_attend_cfg<AttendCfg<128>, false>(p, m, grid, stream)
-                          : launch_attend_cfg<AttendCfg<128>, true>(p, m, grid, stream);
-  return p.bf16_weights ? launch_attend_cfg<AttendCfg<64>, false>(p, m, grid, stream)
-                        : launch_attend_cfg<AttendCfg<64>, true>(p, m, grid, stream);
+  return d == 128 ? launch_attend_d<AttendCfg<128>>(p, m, grid, stream)
+                  : launch_attend_d<AttendCfg<64>>(p, m, grid, stream);
 }
 
 cudaError_t launch_attend_combine(const AttendParams& p, int d, cudaStream_t stream) {

@@ -414,6 +414,7 @@ struct AttendParams {
   long long q_stride[3];
   void* out;                     // float32 or bf16, strides alike
   long long out_stride[3];
+  const void* V;                 // the cache behind the tensor maps, for what is not finite in it
   const int32_t* seq_lens;       // [B] rows of each sequence, the new tokens' among them
   const int32_t* n_new;          // nullable: new tokens of each sequence (else T)
   int32_t* dev_error;            // nullable

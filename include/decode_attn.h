@@ -549,9 +549,9 @@ DA_API int kv_append_rope(const void* q, const void* k_new, const void* v_new,
  *               clamped.  An n_new outside [0, T] is clamped; of more new tokens
  *               than rows the first see nothing and get 0.  Each sets
  *               DA_DEVERR_SEQ_LEN.
- *   Rows that no token of a sequence sees may hold anything, NaN too.  V rows that
- *   some token sees must be finite: the tokens of a tile share its products, and an
- *   infinity or NaN in one reaches also those that do not see it.
+ *   Rows that a token does not see may hold anything, NaN too: nothing of them reaches
+ *   its output.  An infinity or NaN in a V row makes the outputs of the tokens that see
+ *   it infinite or NaN in its column.
  *   Weights are multiplied as a bf16 and its bf16 remainder (each rounded by at most
  *   2^-16 of itself); as one bf16 (2^-8) where dtype carries DA_BF16_WEIGHTS.
  *   workspace : chunk_attn_workspace_bytes(...) bytes, 16-byte aligned (may be NULL
@@ -576,7 +576,9 @@ DA_API int chunk_attn(const void* q, const long long* q_strides, int T, const in
  *   seq_lens           : device int32 [B]; may be 0 (the prefix alone; without rows
  *                        anywhere out = 0).  Outside [0, n_max]: clamped,
  *                        DA_DEVERR_SEQ_LEN.
- *   V rows below the lengths must be finite; weights are rounded as in chunk_attn.
+ *   Rows at or past the lengths may hold anything.  An infinity or NaN in a V row below
+ *   them makes the outputs that see it infinite or NaN in its column.  Weights are rounded
+ *   as in chunk_attn.
  * Two launches for each 1023 sequences (fewer with more than 256 query heads a KV head).
  */
 DA_API size_t decode_attn_shared_workspace_bytes(int B, int h_q, int h_kv, int d, int n_max,
