@@ -1136,8 +1136,8 @@ def decode_attn_shared(q: torch.Tensor, K_prefix: torch.Tensor, V_prefix: torch.
     """Decode attention of a batch that shares a prefix (calls ``decode_attn_shared``): each query q
     [B, h_q, d] sees the first prefix_len rows (all by default) of K_prefix, V_prefix [h_kv,
     prefix_max, d], then the seq_lens[b] rows of its own K, V [B, h_kv, n_max, d] (bf16).  The
-    prefix is read once for the whole batch.  ``bf16_weights``: as in ``chunk_attn``.  Returns
-    ``out`` [B, h_q, d]."""
+    prefix is read once for every 256 query rows (sequences times a group's heads) of a KV head.
+    ``bf16_weights``: as in ``chunk_attn``.  Returns ``out`` [B, h_q, d]."""
     device, out, dims, dt = _cache_args(q, K, V, seq_lens, out, out_dtype, stream)
     if bf16_weights:
         dt = _bf16_weights(dt)

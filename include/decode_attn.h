@@ -569,7 +569,8 @@ DA_API int chunk_attn(const void* q, const long long* q_strides, int T, const in
 /*
  * Decode attention of a batch that shares a prefix: every query sees the prefix_len
  * rows of the prefix, then the seq_lens[b] rows of its own cache, in one softmax.
- * The prefix is read once a KV head for the whole batch, not once a sequence.
+ * The prefix is read once for every 256 query rows of a KV head (sequences times the
+ * h_q / h_kv heads of a group), not once a sequence.
  *   q, out             : device [B, h_q, d] as decode_attn_ex, q bf16
  *   K_prefix, V_prefix : device bf16 [h_kv, prefix_max, d], 0 <= prefix_len <= prefix_max
  *   K, V               : device bf16 [B, h_kv, n_max, d];  d = 64 or 128
