@@ -1306,6 +1306,7 @@ int plan_attend(int B, int T, int h_q, int h_kv, int d, int n_max, int dtype, in
   // of 16 tokens, one of 2048 rows: 28 and 35; 1024 tokens with a window of 1024: 22 and 39), nor
   // where units are many beside the longest (prompts, 4 of 2048 tokens: 120 and 146, 2 of 8192:
   // 732 and 761; the other side, 4 x 2048 tokens behind up to 14336 rows: 1087 and 1047).
+  // Nor where a chunk has more entries (sequences times row tiles) than the schedule's list holds.
   const int most_tiles = (n_max + 127) / 128, prefix_most = P > 0 ? (P + 127) / 128 : 0;
   const bool whole = seen <= 16 * 128 || a.units * T >= sms * seen;
   a.list = P >= 0 || (!whole && entries <= da::kAttendEntries);

@@ -349,10 +349,11 @@ struct LineWalk {
   }
 };
 
-// Without a list: a CTA per unit, the last row tiles, the longest of a chunk, first; a CTA
-// that is done goes on with the next unit whose CTA has not been launched.  (Units dealt in
-// turn instead: one long prompt among 19 took 497 us, not 53, ragged ones 504, not 266.)
-// False: the unit has no rows.
+// Without a list: a CTA per unit, the last row tiles of all sequences first, which are the
+// longest where the sequences bring as many tokens; a CTA that is done goes on with the next unit
+// whose CTA has not been launched.  (Units dealt in turn instead: one long prompt among 19 took
+// 497 us, not 53, ragged ones 504, not 266.)  A sequence of few tokens has row tile 0 alone,
+// which comes last however long its context is.  False: the unit has no rows.
 __device__ __forceinline__ bool unit_item(const AttendParams& p, int u, Item& w) {
   const int per = p.B * p.h_kv;
   const int up = u / per, rest = u - up * per;

@@ -556,7 +556,11 @@ DA_API int kv_append_rope(const void* q, const void* k_new, const void* v_new,
  *   2^-16 of itself); as one bf16 (2^-8) where dtype carries DA_BF16_WEIGHTS.
  *   workspace : chunk_attn_workspace_bytes(...) bytes, 16-byte aligned (may be NULL
  *               when that is 0); as decode_attn_ex's.
- * One launch, and a second one where units of the work may be cut along the rows.
+ * One launch, and a second one where units of the work (256 query rows of a KV head) may
+ * be cut along the rows.  They are not in short caches, nor where units are many beside
+ * the longest, nor with more than 1024 of them a KV head, B * ceil(T * h_q / h_kv / 256):
+ * one SM then goes along a whole context, so a larger batch with a few contexts far longer
+ * than the others is faster as two calls.
  */
 DA_API size_t chunk_attn_workspace_bytes(int B, int T, int h_q, int h_kv, int d, int n_max,
                                          int dtype, int* status);
