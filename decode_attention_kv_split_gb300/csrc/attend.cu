@@ -812,45 +812,78 @@ __device__ __forceinline__ uint32_t finite_halves(uint32_t w) {
 }
 
 // What was not finite in V, and was cleared, goes to the outputs of an item's queries that see it:
-// they become infinite or NaN in its column.  A lane a query; rare.
+// they become infinite or NaN in its column.  A warp, each lane D / 32 columns, once up the rows and
+// the tokens: of each column the last row with an infinity of either sign and with a NaN is kept,
+// and a token sees one if it is not behind its window.  (2 of 8192 tokens, 32 heads on 8, without a
+// finite value in V: 2.5 ms, and 0.94 with finite ones; on 32: 4.7 and 0.98, 42 where each token
+// went through its rows by itself.)
 template <class Cfg>
 __device__ __forceinline__ void add_values(const AttendParams& p, const Item& w, const PartSeen& part) {
-  constexpr int D = Cfg::D;
+  constexpr int D = Cfg::D, EPL = D / 32, kNone = -0x7fffffff, kAlways = 0x7fffffff;
+  const int c0 = (threadIdx.x & 31) * EPL;
   const long long v0 = ((long long)(p.b_offset + w.b) * p.h_kv + w.kvh) * p.n_max;
-  const uint16_t* V = static_cast<const uint16_t*>(p.V) + v0 * D;
+  const uint16_t* V = static_cast<const uint16_t*>(p.V) + v0 * D + c0;
   const bool narrow = w.part < 0 && p.out_bf16;
+  const int last = p.by_group.div(w.row0 + w.rows - 1);
+  int t = p.by_group.div(w.row0), plus[EPL], minus[EPL], nan[EPL];
+#pragma unroll
+  for (int e = 0; e < EPL; ++e) plus[e] = minus[e] = nan[e] = kNone;
+  // the outputs of the tokens at rows below l
+  auto finish = [&](int l) {
 #pragma unroll 1
-  for (int r = threadIdx.x & 31; r < w.rows; r += 32) {
-    const int flat = w.row0 + r, t = p.by_group.div(flat), head = w.kvh * p.group + flat - t * p.group;
-    const int hi = w.past + t, lo = p.window ? hi + 1 - p.window : 0;
-    const long long off = w.part >= 0 ? ((long long)w.part + r) * D
-                                      : w.b * p.out_stride[0] + head * p.out_stride[1] + t * p.out_stride[2];
-    if (!DA_IN(p, off + D - 1, w.part >= 0 ? p.part_rows * D : p.out_elems)) continue;
-    char* y = static_cast<char*>(w.part >= 0 ? static_cast<void*>(p.o_part) : p.out) + off * (narrow ? 2 : 4);
+    for (; t <= last && w.past + t < l; ++t) {
+      const int lo = p.window ? w.past + t + 1 - p.window : 0;
+      float add[EPL];
+      bool any = false;
+#pragma unroll
+      for (int e = 0; e < EPL; ++e) {
+        add[e] = (plus[e] >= lo ? INFINITY : 0.f) + (minus[e] >= lo ? -INFINITY : 0.f);
+        if (nan[e] >= lo) add[e] = INFINITY - INFINITY;
+        any |= !(add[e] == 0.f);
+      }
+      if (!__any_sync(0xffffffffu, any)) continue;
+      const int end = min((t + 1) * p.group, w.row0 + w.rows);
 #pragma unroll 1
-    for (int j = 0; j < w.count; ++j) {
-      const int r0 = tile_row(w, w.begin + j), end = min(min(r0 + kTile, w.n), hi + 1);
-      if (!edge_tile<true>(p, w, part, r0)) continue;
-#pragma unroll 1
-      for (int l = r0; l < end; ++l) {
-        // (seen by this query, not by each of them)
-        if ((l < lo && l >= p.prefix) || (l <= part.hi && (l >= part.lo || r0 + kTile <= p.prefix))) continue;
-        if (!DA_IN(p, v0 + l, (long long)(p.b_offset + p.B) * p.h_kv * p.n_max)) continue;
-#pragma unroll 1
-        for (int c = 0; c < D; ++c) {
-          const uint32_t v = V[(long long)l * D + c];
-          if (!(not_finite2(v) & 0x8000u)) continue;
-          const float f = __uint_as_float(v << 16);
-          if (narrow) {
-            __nv_bfloat16* at = reinterpret_cast<__nv_bfloat16*>(y) + c;
-            *at = __float2bfloat16_rn(__bfloat162float(*at) + f);
-          } else {
-            reinterpret_cast<float*>(y)[c] += f;
-          }
+      for (int flat = max(t * p.group, w.row0); flat < end; ++flat) {
+        const long long off = w.part >= 0
+                                  ? ((long long)w.part + flat - w.row0) * D
+                                  : w.b * p.out_stride[0] + t * p.out_stride[2] +
+                                        (w.kvh * p.group + flat - t * p.group) * p.out_stride[1];
+        if (!DA_IN(p, off + D - 1, w.part >= 0 ? p.part_rows * D : p.out_elems)) continue;
+        float* y = (w.part >= 0 ? p.o_part : static_cast<float*>(p.out)) + off + c0;
+        __nv_bfloat16* z = static_cast<__nv_bfloat16*>(p.out) + off + c0;
+#pragma unroll
+        for (int e = 0; e < EPL; ++e) {
+          if (add[e] == 0.f) continue;
+          if (narrow) z[e] = __float2bfloat16_rn(__bfloat162float(z[e]) + add[e]);
+          else y[e] += add[e];
         }
       }
     }
+  };
+#pragma unroll 1
+  for (int j = 0; j < w.count; ++j) {
+    const int r0 = tile_row(w, w.begin + j), end = min(r0 + kTile, w.n);
+    if (!edge_tile<true>(p, w, part, r0)) continue;
+#pragma unroll 1
+    for (int l = r0; l < end; ++l) {
+      // (the rows that were looked through)
+      if (l <= part.hi && (l >= part.lo || r0 + kTile <= p.prefix)) continue;
+      if (!DA_IN(p, v0 + l, (long long)(p.b_offset + p.B) * p.h_kv * p.n_max)) continue;
+      finish(l);
+      const int seen = l < p.prefix ? kAlways : l;
+      const uint32_t* at = reinterpret_cast<const uint32_t*>(V + (long long)l * D);
+#pragma unroll
+      for (int e = 0; e < EPL; ++e) {
+        const uint32_t v = e & 1 ? at[e / 2] >> 16 : at[e / 2] & 0xffffu;
+        if (!(not_finite2(v) & 0x8000u)) continue;
+        if (v & 0x7fu) nan[e] = max(nan[e], seen);
+        else if (v & 0x8000u) minus[e] = max(minus[e], seen);
+        else plus[e] = max(plus[e], seen);
+      }
+    }
   }
+  finish(kAlways);
 }
 
 // ---- V rows that some query does not see: a warp

@@ -129,3 +129,45 @@ def test_in_the_checked_build(checked, monkeypatch, out_dtype, n_max, window, pr
         got.append(api.chunk_attn(q, K, V, lens, window=window, prefix=prefix, out_dtype=out_dtype, dev_error=err))
         assert int(err) == 0
     assert got[0].isnan().any() and torch.equal(got[0].contiguous().view(torch.uint8), got[1].contiguous().view(torch.uint8))
+
+
+@pytest.mark.parametrize("group", [1, 4])
+def test_nothing_finite(group):
+    """A sequence all of whose values are NaN: its outputs are, the other's are not, and no wait runs out."""
+    B, T, h_kv, d = 2, 2048, 4, 128
+    g = torch.Generator(device="cuda").manual_seed(11)
+    q, K, V = (torch.randn(s, generator=g, device="cuda").bfloat16() for s in ((B, h_kv * group, T, d), (B, h_kv, T, d),
+                                                                               (B, h_kv, T, d)))
+    for window in (0, 300):
+        want = api.chunk_attn(q, K, V, i32([T, T]), window=window)
+        Vx = V.clone()
+        Vx[1] = float("nan")
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        out = api.chunk_attn(q, K, Vx, i32([T, T]), window=window, dev_error=err)
+        assert int(err) == 0
+        assert torch.equal(out[0], want[0]) and out[1].isnan().all()
+
+
+@pytest.mark.parametrize("out_dtype", OUTS, ids=OID)
+@pytest.mark.parametrize("window,prefix", [(0, 0), (20, 0), (20, 35)])
+def test_signs(window, prefix, out_dtype):
+    """Of rows that not every token sees: an infinity where only one sign is seen, NaN where both are or one is NaN."""
+    T, d = 128, 64
+    g = torch.Generator(device="cuda").manual_seed(12)
+    q, K, V = (torch.randn(s, generator=g, device="cuda").bfloat16() for s in ((1, 2, T, d), (1, 1, T, d), (1, 1, T, d)))
+    inf = float("inf")
+    V[0, 0, 50, 3], V[0, 0, 60, 4], V[0, 0, 30, 5], V[0, 0, 45, 5], V[0, 0, 100, 6], V[0, 0, 33, 7] = inf, -inf, inf, -inf, \
+        float("nan"), -inf
+    out = torch.zeros((1, 2, T, d), dtype=out_dtype, device="cuda")
+    api.chunk_attn(q, K, V, i32([T]), window=window, prefix=prefix, out=out)
+    for p in range(T):
+        for c in range(8):
+            seen = V[0, 0, [l for l in range(p + 1) if not window or l > p - window or l < prefix], c]
+            bad = seen[~seen.isfinite()]
+            for got in out[0, :, p, c]:
+                if not bad.numel():
+                    assert got.isfinite()
+                elif bad.isnan().any() or bad.unique().numel() == 2:
+                    assert got.isnan()
+                else:
+                    assert got == bad[0]
