@@ -1302,10 +1302,10 @@ int plan_attend(int B, int T, int h_q, int h_kv, int d, int n_max, int dtype, in
   // Cut into equal pieces, one per CTA, and merged: behind a prefix (whose partials are merged with
   // a sequence's own anyway), and of a chunk where whole units, taken one by one by CTAs that are
   // done, would end apart.  Cutting and merging costs 3 to 20 us, so not up to 16 tiles of rows
-  // (5 tokens: 7.9 us whole and 10.6 cut behind 300 rows, 14.8 and 14.2 behind 2000; 64 sequences
-  // of 16 tokens, one of 2048 rows: 28 and 35; 1024 tokens with a window of 1024: 22 and 39), nor
-  // where units are many beside the longest (prompts, 4 of 2048 tokens: 120 and 146, 2 of 8192:
-  // 732 and 761; the other side, 4 x 2048 tokens behind up to 14336 rows: 1087 and 1047).
+  // (5 tokens of 8 heads: 9.5 us whole and 11.6 cut behind 300 rows, 18.7 and 16.7 behind 2000; 64
+  // sequences of 16 tokens, one of 2048 rows: 31 and 39; 1024 tokens with a window of 1024: 31 and
+  // 49), nor where units are many beside the longest (prompts, 4 of 2048 tokens: 162 and 222, 2 of
+  // 8192: 955 and 1040; the other side, 2 x 2048 tokens behind 6144 rows: 475 and 450).
   // Nor where a chunk has more entries (sequences times row tiles) than the schedule's list holds.
   const int most_tiles = (n_max + 127) / 128, prefix_most = P > 0 ? (P + 127) / 128 : 0;
   const bool whole = seen <= 16 * 128 || a.units * T >= sms * seen;

@@ -26,10 +26,12 @@
 // that the loads and first scores of one run under the end of the last.  The items are
 // equal pieces of all units, or whole units from the grid's CTAs that wait for launch.
 //
-// What bounds it.  Prompts (2 of 8192 tokens, 32 heads of 128): 719 us, 1.53 PFLOP/s or 0.79 of a
-// library product's rate; a tile of both streams takes 2750 cycles, its MMAs 2048.  Few tokens of
-// long contexts (2 of 131056 rows): HBM, 159 us, 6.75 TB/s.  Batches behind a shared prefix: the
-// start (7 us to the first scores), 3 to 4 us an item beside its tiles, 5 to 8 us to merge.
+// What bounds it.  Prompts (2 of 8192 tokens, 32 heads of 128): 980 to 1050 us, the MMAs at 1.57 to
+// 1.68 PFLOP/s with the remainder's counted, 0.81 to 0.87 of a library product's rate; with weights
+// of one bf16 727 to 744 us, 1.5 PFLOP/s.  Heads of 64 (731 us, 549): the exponentials, 16 a cycle
+// and SM.  Few tokens of long contexts (2 of 131056 rows): HBM, 168 to 174 us, 6.2 to 6.4 TB/s.
+// Batches behind a shared prefix: the start (7 us to the first scores), 3 to 4 us an item beside its
+// tiles, 5 to 8 us to merge.
 //
 // Roles (384 threads): warps 0-3 and 4-7 the softmax of streams 0 and 1, warp 8
 // the items and the TMA loads, warp 9 the MMAs, warp 10 looks through V rows that some
@@ -392,7 +394,7 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
 
 // The MMA issuer runs as a whole warp, so that addresses and descriptors stay in
 // registers of the warp; one lane's instructions count.  (One thread in a branch took
-// 115 cycles for each MMA of 64: 1070 us for the prompts.)
+// 115 cycles for each MMA of 64: prompts with weights of one bf16 1070 us, and 725 this way.)
 __device__ __forceinline__ uint32_t elect_one() {
   uint32_t e;
   asm volatile(
@@ -1553,7 +1555,7 @@ __global__ void __launch_bounds__(kAttendCombineWarps * 32)
 
 // More rows, cut in two as a rule: a warp takes four at once and the partials one after the
 // other (a warp a row took 28 us of launching behind 150 CTAs; 8 tokens of 131072 rows, ten
-// items a unit, took 166 us this way and 159 the other).
+// items a unit, took 7 us more this way than the other).
 constexpr int kJoinRows = 4;
 
 template <int D>
@@ -1656,7 +1658,7 @@ cudaError_t launch_attend_combine(const AttendParams& p, int d, cudaStream_t str
     return d == 128 ? launch_dependent(attend_merge_kernel<128>, grid, threads, 0, stream, p)
                     : launch_dependent(attend_merge_kernel<64>, grid, threads, 0, stream, p);
   }
-  // (16 sequences of 16 tokens, 128 rows a unit, behind 8000 rows: 93 us, and 98 a warp a row)
+  // (16 sequences of 16 tokens, 128 rows a unit, behind 8000 rows: 5 us less than a warp a row)
   const bool few = p.unit_rows <= 64;
   const int rows = kAttendCombineWarps * (few ? 1 : kJoinRows);
   const dim3 grid((p.unit_rows + rows - 1) / rows, p.ctas - 1);

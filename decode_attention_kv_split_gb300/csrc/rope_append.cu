@@ -20,8 +20,8 @@ namespace da {
 // the norm's sum is the only exchange.  A group takes HC heads of one token and
 // one kind (q, k or v), so that their loads are in flight together and the
 // angles and weights are read once for all of them.
-// Measured: 16 prompts of 2048 tokens, 32 + 2 * 8 heads of 128 in bf16, 134 us = 6.0 TB/s
-// (0.88 of a copy's rate); one token 2.3 us, which is the launch.
+// Measured: 16 prompts of 2048 tokens, 32 + 2 * 8 heads of 128 in bf16, 137 us = 5.9 TB/s
+// (0.87 of a copy's rate); one token 2.3 us, which is the launch.
 // ---------------------------------------------------------------------------
 template <typename T>
 struct RopeVec;
@@ -62,7 +62,7 @@ __device__ __forceinline__ void load_floats(const float* p, float* x) {
   }
 }
 
-// The mean of squares over a head's d elements and what follows from it.
+// The sum over the lanes of a head's vector.
 template <int LPR>
 __device__ __forceinline__ float group_sum(float v, unsigned lanes) {
 #pragma unroll
